@@ -316,6 +316,164 @@ size_t rmsnorm_bwd_call_workspace_bytes(const void *dy, const void *dresidual_ou
                                         rmsnorm_dtype_t dt, int fused);
 
 /* ------------------------------------------------------------------------
+ * Head rows: rotary positions, a paged cache and the attention that reads
+ * it: what a model does with the q, k and v heads after their per-head norm.
+ * The pages have no counterpart to these entry points.
+ *
+ * A head-row array is [T, heads, head_dim] with head_dim contiguous and any
+ * token and head strides (in elements), e.g. one part of a fused qkv
+ * projection. A call is a structure that the library reads before it
+ * returns; all pointers in it are device pointers except where noted.
+ * Streams, errors and the device follow the rules at the top of this file.
+ * --------------------------------------------------------------------- */
+
+#define ROPE_MAX_AXES 4
+#define HEAD_MAX_DIM 256
+
+typedef enum {
+    ROPE_HALF = 0,    /* frequency i turns the pair (i, i + rotary_dim / 2) */
+    ROPE_ADJACENT = 1 /* frequency i turns the pair (2 i, 2 i + 1)          */
+} rope_pairing_t;
+
+/* Head rows read from `in` and written to `out` (strides in elements). */
+typedef struct {
+    const void *in;
+    void *out;
+    int64_t in_token, in_head;
+    int64_t out_token, out_head;
+} rope_rows_t;
+
+/* The angles: token t's frequency i is turned by
+ * positions[axes[i]][t] * inv_freq[i], axes being a separate argument. */
+typedef struct {
+    const void *positions;  /* [n_axes, T], int32 or int64, |position| < 2^31 */
+    const float *inv_freq;  /* [rotary_dim / 2]                               */
+    int64_t axis_stride;    /* elements between two axes' positions           */
+    int32_t position_bytes; /* 4 or 8                                         */
+    int32_t n_axes;         /* 1 .. ROPE_MAX_AXES                             */
+    int32_t rotary_dim;     /* even, 2 .. head_dim; the rest passes unturned  */
+    int32_t pairing;        /* rope_pairing_t                                 */
+} rope_angles_t;
+
+typedef struct {
+    rope_rows_t q, k; /* k unused when k_heads is 0 */
+    rope_angles_t angles;
+    int64_t tokens;
+    int32_t q_heads, k_heads, head_dim;
+    int32_t dtype; /* RMSNORM_F32, RMSNORM_BF16 or RMSNORM_F16 */
+} rope_call_t;
+
+/*
+ * Rotary positions with one to four axes (e.g. time, height and width).
+ * With a = axes[i], c = cos(p_a f_i), s = sin(p_a f_i) and (x1, x2) the pair
+ * of frequency i:   y1 = x1 c - x2 s,   y2 = x2 c + x1 s.
+ * The angle's product and its reduction to one turn carry about 48 bits, so
+ * far positions lose nothing; cos, sin and the products are fp32, each
+ * output rounded once. axes: HOST pointer to rotary_dim / 2 bytes, the axis
+ * of each frequency, or NULL (all on axis 0).
+ * rope_bwd is the gradient: `in` holds the gradient of the outputs, `out`
+ * receives that of the inputs (the rotation by the negative angle).
+ * out may equal in (same strides); nothing else may overlap. head_dim is
+ * 1 .. HEAD_MAX_DIM. Rows, strides and inv_freq on 16-byte boundaries with
+ * rotary_dim and head_dim whole chunks run the vectorised kernel; anything
+ * else an element-wise one.
+ */
+rmsnorm_status_t rope_fwd(const rope_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream);
+rmsnorm_status_t rope_bwd(const rope_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream);
+
+/* A paged cache: keys and values [pages, page_size, heads, head_dim] with
+ * head_dim contiguous, strides in elements. */
+typedef struct {
+    void *k, *v;
+    int64_t pages;
+    int64_t k_page, k_slot, k_head;
+    int64_t v_page, v_slot, v_head;
+    int32_t page_size, heads;
+} paged_cache_t;
+
+typedef struct {
+    rope_rows_t q;      /* rotated queries to out; unused when q_heads is 0  */
+    rope_rows_t k, v;   /* out is unused: they go to the cache               */
+    rope_angles_t angles; /* positions NULL: nothing is rotated              */
+    paged_cache_t cache;
+    const int64_t *slots; /* [T]: page * page_size + place in the page       */
+    const void *wq, *wk;  /* [head_dim] per-head RMSNorm weights or NULL     */
+    int64_t tokens;
+    float eps, offset;
+    int32_t q_heads, head_dim;
+    int32_t dtype; /* as rope_call_t, or with RMSNORM_WEIGHT_F32: wq, wk fp32 */
+    int32_t reserved;
+} paged_append_call_t;
+
+/*
+ * Append keys and values to a paged cache, in one launch with what precedes
+ * it: k (and q) normalised per head where a weight is given,
+ * z = x rstd (offset + w) with rstd = 1 / sqrt(mean(x^2) + eps) over the
+ * head's head_dim values, then rotated as rope_fwd does, rounded once; v is
+ * copied. A token whose slot is negative or not below pages * page_size is
+ * not appended (a padded batch); its q is still written. No two tokens may
+ * have the same slot. cache.heads is the number of k and v heads.
+ */
+rmsnorm_status_t paged_kv_append(const paged_append_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream);
+
+typedef struct {
+    const void *q;        /* [T, q_heads, head_dim]                           */
+    void *out;            /* the same shape                                   */
+    float *lse;           /* [T, q_heads] contiguous, or NULL                 */
+    int64_t q_token, q_head, out_token, out_head;
+    paged_cache_t cache;
+    const int32_t *block_table; /* [batch, table_width]: each sequence's pages */
+    const int32_t *kv_lens;     /* [batch]: cached tokens, the new ones included */
+    const int32_t *cu_q;        /* [batch + 1]: first row of each sequence     */
+    int64_t table_stride;       /* elements between two rows of block_table    */
+    int64_t tokens;             /* T, rows of q and out                        */
+    void *workspace;            /* NULL: stream-ordered memory                 */
+    size_t workspace_bytes;
+    float scale;                /* > 0: scores are scale * q . k               */
+    int32_t batch, table_width, q_heads, head_dim;
+    int32_t max_q;              /* no sequence has more new tokens             */
+    int32_t max_kv;             /* no sequence is longer                       */
+    int32_t causal;
+    int32_t dtype;              /* RMSNORM_BF16 or RMSNORM_F16                 */
+} paged_attn_call_t;
+
+/*
+ * Attention of new tokens over a paged cache. Sequence b's new tokens are
+ * the rows cu_q[b] .. cu_q[b + 1] of q and the last n = cu_q[b+1] - cu_q[b]
+ * of its kv_lens[b] cached ones (append them first). Token i of them sees
+ * the keys j <= kv_lens[b] - n + i (all kv_lens[b] keys when causal is 0):
+ *
+ *   x_j = scale q . k_j,   lse = log sum_j exp(x_j),   o = sum_j exp(x_j - lse) v_j
+ *
+ * with query head h reading key head h / (q_heads / heads). A row that sees
+ * no key gets o = 0 and lse = -inf. Rows of q behind the last sequence are
+ * not written. Products of the storage type with fp32 sums; the softmax in
+ * fp32, its weights rounded to the storage type for the second product;
+ * o rounded once.
+ *
+ * What lies in the cache past a sequence's length never reaches its rows,
+ * infinities and NaN included. A key that later rows of the same sequence
+ * see is multiplied by a zero weight for the earlier rows, so its value has
+ * to be finite.
+ * Lengths are read on the device and held to the call's bounds: kv_lens to
+ * max_kv and table_width * page_size, rows to T; rows past max_q of a
+ * sequence are not written. A table entry that is no page reads as zeros.
+ *
+ * UNSUPPORTED: head_dim not a multiple of 8 or above 128, page_size not a
+ * multiple of 8, more than 128 query heads a key head, cache base or strides
+ * not on 16-byte boundaries.
+ * workspace: as for rmsnorm_bwd; paged_attn_workspace_bytes gives its size
+ * (0 where the work is not split over the keys). Each row's sum has a fixed
+ * order: the same call gives the same bits.
+ */
+rmsnorm_status_t paged_attn_fwd(const paged_attn_call_t *call, rmsnorm_stream_t stream);
+
+/* Workspace bytes of paged_attn_fwd for these sizes (tokens, batch, q_heads,
+ * cache.heads, head_dim, max_q, max_kv of the call) on the current device;
+ * 0 for invalid sizes, without a device, or where none is needed. */
+size_t paged_attn_workspace_bytes(const paged_attn_call_t *call);
+
+/* ------------------------------------------------------------------------
  * Plans: which kernel runs. Exposed for tests and benchmarks (the analogue
  * of the A/B toggles of Liger-Kernel PR #1388, "Behavior when the fast path
  * does not apply", and of the tuned-kernel registry of

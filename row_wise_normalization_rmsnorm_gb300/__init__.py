@@ -13,6 +13,15 @@ beside 16-bit activations) and launch on the current stream:
   rmsnorm_add_bwd(dy, dres, h, w, rstd)   -> dx (= dresidual), dw
   rmsnorm_bwd_workspace_bytes(M, N, dt)
 
+and, on [tokens, heads, head_dim] rows of any token and head strides:
+
+  rope_fwd(q, k, positions, inv_freq)     -> q, k rotated (1 to 4 axes)
+  rope_bwd(dq, dk, positions, inv_freq)   -> its gradient
+  paged_kv_append(k, v, k_cache, v_cache, slots, ...) -> keys (normalised and
+                                             rotated) and values into a paged cache
+  paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_q, ...)
+                                          -> out, lse
+
 The CUDA library is loaded on first use and must have been built
 (``python -m row_wise_normalization_rmsnorm_gb300.build``); there is no CPU
 fallback. ``inputs`` holds the seeded synthetic workloads.
@@ -44,4 +53,12 @@ from ._binding import (  # noqa: F401
     rmsnorm_fwd,
     rmsnorm_fwd_ex,
     rmsnorm_fwd_fp8,
+)
+from ._heads import (  # noqa: F401
+    paged_attn_fwd,
+    paged_attn_workspace_bytes,
+    paged_kv_append,
+    rope_axes,
+    rope_bwd,
+    rope_fwd,
 )

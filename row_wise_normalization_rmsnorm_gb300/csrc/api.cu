@@ -374,6 +374,15 @@ static cudaError_t device_sms(int *dev_out, int *sms_out) {
     return cudaSuccess;
 }
 
+// The current device's SM count and status word, for the entry points of
+// other translation units.
+int current_device(int *sms, int **status) {
+    int dev = 0;
+    cudaError_t e = device_sms(&dev, sms);
+    if (e == cudaSuccess && status) e = status_word(dev, status);
+    return (int)e;
+}
+
 // The kernels of a call's type pair. `peel`: the instantiation for rows at a
 // common offset, which exists for the default vectorised plans of the types
 // whose weight is the activations' type (NULL elsewhere).

@@ -1,0 +1,547 @@
+// rope.cu -- rope_fwd, rope_bwd and paged_kv_append: rotary positions on
+// head rows, and the same with a per-head RMSNorm before and a paged cache
+// behind.
+//
+// The mathematics: frequency i of token t turns one pair of a head's values
+// by the angle p f (position times frequency). The angle is reduced to a
+// fraction of a turn with error-free fp32 products (half_turns), since
+// fp32's p f has lost its fraction where p is large, and the device's fp64
+// rate is too low to spend on it; sincospif takes the fraction.
+//
+// What bounds it: memory. Every value is read once and written once, at a
+// few fp32 operations a value; the angles are shared by all heads of a
+// token. So a warp takes one token: a lane keeps the cos and sin of one
+// 16-byte chunk's frequencies in registers and walks the heads, a group of
+// lanes a head, with several heads' loads in flight. No shared memory and no
+// barrier; what a warp repeats (the angles, once a group of lanes) hides
+// behind the copies. With few tokens the heads are split over more warps.
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "head_rows.h"
+
+// the structures as the Python binding packs them
+static_assert(sizeof(rope_call_t) == 160, "rope_call_t");
+static_assert(sizeof(paged_append_call_t) == 320, "paged_append_call_t");
+
+namespace rmsn {
+
+struct HeadSeg {
+    const char *in;
+    char *out;
+    int64_t in_token, in_head;    // bytes
+    int64_t out_token, out_head;  // bytes; a cache segment: page, head
+    int64_t out_slot;             // bytes; cache segments only
+    int heads;
+};
+
+struct RopeParams {
+    HeadSeg seg[3];  // q, k, v
+    const void *positions;
+    const float *inv_freq;
+    const int64_t *slots;
+    const void *w[2];       // q's and k's norm weight, or NULL
+    int64_t axis_stride;    // positions, in elements
+    int64_t tokens, slots_end;
+    uint32_t axis[8];       // two bits a frequency
+    int naxes, pos64, half_dim, head_dim, adjacent;
+    int page_size;
+    int blocks, block_heads;  // head blocks a token, heads a block
+    int items, lanes_log2;    // vector kernel: chunk pairs a head, lanes a head
+    float sign;               // -1: the gradient's rotation
+    float eps, offset, inv_n;
+    int w32;
+};
+
+// ------------------------------------------------------------- angles --
+// The fraction of a turn that p f is, as sincospif's argument (half turns).
+// p = hi + lo with hi a multiple of 4096, both exact in fp32; each product
+// with f is kept as its rounding and its error, and each rounding is scaled
+// by 1 / (2 pi) in three fp32 parts (72 bits), its own rounding error kept as
+// well, before the whole turns are dropped: what remains is the rounding of
+// a fraction of a turn, a few 2^-25 of it, for |p| < 2^31 and f <= 1.
+__device__ __forceinline__ float part_turns(float p, float &rest) {
+    const float c1 = 0x1.45f306p-3f, c2 = 0x1.b9391p-28f, c3 = 0x1.529fc2p-54f;
+    const float t = __fmul_rn(p, c1);
+    rest += __fmaf_rn(p, c1, -t) + __fmaf_rn(p, c2, __fmul_rn(p, c3));
+    return t - rintf(t);
+}
+__device__ __forceinline__ float half_turns(int64_t pos, float f) {
+    const float c1 = 0x1.45f306p-3f;
+    const int p32 = (int)pos;
+    const float lo = (float)(p32 & 4095), hi = (float)(p32 - (p32 & 4095));
+    const float pl = __fmul_rn(lo, f);
+    float rest = __fmul_rn(__fmaf_rn(lo, f, -pl), c1);
+    float t = part_turns(pl, rest);
+    if (hi != 0.f) {
+        const float ph = __fmul_rn(hi, f);
+        rest += __fmul_rn(__fmaf_rn(hi, f, -ph), c1);
+        t += part_turns(ph, rest);
+    }
+    t += rest;
+    return 2.f * (t - rintf(t));
+}
+
+__device__ __forceinline__ int64_t position(const RopeParams &p, int axis, int64_t t) {
+    const int64_t i = (int64_t)axis * p.axis_stride + t;
+    return p.pos64 ? __ldg(reinterpret_cast<const long long *>(p.positions) + i)
+                   : (int64_t)__ldg(reinterpret_cast<const int *>(p.positions) + i);
+}
+
+__device__ __forceinline__ int axis_of(const RopeParams &p, int i) { return (p.axis[i >> 4] >> (2 * (i & 15))) & 3; }
+
+// cos and sin of the NF frequencies from i0 of token t.
+template <int NF>
+__device__ __forceinline__ void angles_of(const RopeParams &p, int64_t t, int i0, float *c, float *s) {
+    int64_t at[ROPE_MAX_AXES];
+    at[0] = position(p, 0, t);
+#pragma unroll
+    for (int a = 1; a < ROPE_MAX_AXES; ++a) at[a] = a < p.naxes ? position(p, a, t) : at[0];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+        int64_t pos = at[0];
+        if (p.naxes > 1) {
+            const int a = axis_of(p, i0 + i);
+            pos = a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
+        }
+        sincospif(half_turns(pos, __ldg(p.inv_freq + i0 + i)), s + i, c + i);
+        s[i] *= p.sign;
+    }
+}
+
+// Where token t's row of head h (counted within its segment) is written;
+// NULL: a token without a slot.
+template <bool APPEND>
+__device__ __forceinline__ char *row_out(const RopeParams &p, const HeadSeg &g, bool cache, int64_t t, int h,
+                                         int64_t page, int place) {
+    if (APPEND && cache) {
+        if (page < 0) return nullptr;
+        return g.out + page * g.out_token + place * g.out_slot + h * g.out_head;
+    }
+    return g.out + t * g.out_token + h * g.out_head;
+}
+
+// The page and the place in it of token t's slot; page -1: none.
+__device__ __forceinline__ void find_slot(const RopeParams &p, int64_t t, int64_t &page, int &place) {
+    const int64_t slot = __ldg(reinterpret_cast<const long long *>(p.slots) + t);
+    page = -1;
+    place = 0;
+    if (slot < 0 || slot >= p.slots_end) return;
+    if (slot <= 0x7fffffffLL) {
+        const uint32_t q = (uint32_t)slot / (uint32_t)p.page_size;
+        page = q;
+        place = (int)((uint32_t)slot - q * (uint32_t)p.page_size);
+    } else {
+        page = slot / p.page_size;
+        place = (int)(slot - page * p.page_size);
+    }
+}
+
+// Norm weight values of the chunk at element e.
+template <typename T>
+__device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w, int e, float2 (&f)[Elem<T>::NP]) {
+    if (std::is_same<T, float>::value || !p.w32) {
+        load_w_chunk<T, T>(w, e / Elem<T>::E, f);
+    } else if constexpr (!std::is_same<T, float>::value) {
+        load_w_chunk<T, float>(w, e / Elem<T>::E, f);
+    }
+#pragma unroll
+    for (int q = 0; q < Elem<T>::NP; ++q) f[q] = make_float2(p.offset + f[q].x, p.offset + f[q].y);
+}
+
+// ------------------------------------------------------ vectorised rows --
+// A lane's two chunks of a head: the two halves of E pairs (half pairing),
+// two neighbouring chunks of E pairs (adjacent pairing), or two chunks of
+// the values that pass unturned.
+constexpr int kRopeThreads = 128;
+constexpr int kRopeUnroll = 4;
+
+template <typename T, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads) rope_vector(const __grid_constant__ RopeParams p) {
+    constexpr int E = Elem<T>::E, NP = Elem<T>::NP, U = kRopeUnroll;
+    using PR = Pair<true>;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (unit >= p.tokens * p.blocks) return;
+    const int64_t t = unit / p.blocks;
+    const int h0 = (int)(unit - t * p.blocks) * p.block_heads;
+    const int hq = p.seg[0].heads, hqk = hq + p.seg[1].heads;
+    const int htot = hqk + (APPEND ? p.seg[2].heads : 0);
+    const int h1 = min(h0 + p.block_heads, htot);
+    const int item = lane & ((1 << p.lanes_log2) - 1), grp = lane >> p.lanes_log2;
+    const int step = 32 >> p.lanes_log2;
+    const int rot_items = p.half_dim / E;
+    const bool turns = item < rot_items;
+
+    int e0, e1;
+    if (turns) {
+        e0 = p.adjacent ? item * 2 * E : item * E;
+        e1 = p.adjacent ? e0 + E : e0 + p.half_dim;
+    } else {
+        e0 = 2 * p.half_dim + (item - rot_items) * 2 * E;
+        e1 = e0 + E;
+    }
+    const bool has0 = e0 < p.head_dim, has1 = e1 < p.head_dim;
+
+    uint4 x0[U], x1[U];
+    auto load = [&](int hb) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = hb + u * step + grp;
+            x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
+            if (h < h1) {
+                const int sg = h < hq ? 0 : (h < hqk ? 1 : 2);
+                const HeadSeg &g = p.seg[sg];
+                const char *row = g.in + t * g.in_token + (h - (sg == 0 ? 0 : sg == 1 ? hq : hqk)) * g.in_head;
+                if (has0) x0[u] = ld_stream(reinterpret_cast<const uint4 *>(row + e0 * (int)sizeof(T)));
+                if (has1) x1[u] = ld_stream(reinterpret_cast<const uint4 *>(row + e1 * (int)sizeof(T)));
+            }
+        }
+    };
+    load(h0);
+
+    int64_t page = 0;
+    int place = 0;
+    if (APPEND) find_slot(p, t, page, place);
+    float c[E], s[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        c[i] = 1.f;
+        s[i] = 0.f;
+    }
+    if (turns && h0 < hqk) angles_of<E>(p, t, item * E, c, s);
+
+    for (int hb = h0;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = hb + u * step + grp;
+            const int sg = h < hq ? 0 : (h < hqk ? 1 : 2);
+            const bool live = h < h1;
+            float2 a[NP], b[NP];
+            unpack<T>(x0[u], a);
+            unpack<T>(x1[u], b);
+            if (APPEND) {
+                const void *w = sg < 2 ? p.w[sg] : nullptr;
+                // (p.w is the same for the whole grid, so the shuffles are uniform)
+                if (p.w[0] || p.w[1]) {
+                    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) acc = PR::fma(a[q], a[q], PR::fma(b[q], b[q], acc));
+                    float ss = acc.x + acc.y;
+                    for (int o = (1 << p.lanes_log2) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    if (w) {
+                        const float r = rsqrtf(__fmaf_rn(ss, p.inv_n, p.eps));
+                        const float2 r2 = make_float2(r, r);
+                        float2 f[NP];
+                        if (has0) {
+                            norm_factors<T>(p, w, e0, f);
+#pragma unroll
+                            for (int q = 0; q < NP; ++q) a[q] = PR::mul(PR::mul(a[q], r2), f[q]);
+                        }
+                        if (has1) {
+                            norm_factors<T>(p, w, e1, f);
+#pragma unroll
+                            for (int q = 0; q < NP; ++q) b[q] = PR::mul(PR::mul(b[q], r2), f[q]);
+                        }
+                    }
+                }
+            }
+            if (!live) continue;
+            if (turns && sg < 2) {
+                if (!p.adjacent) {
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        const float2 cc = make_float2(c[2 * q], c[2 * q + 1]), sn = make_float2(s[2 * q], s[2 * q + 1]);
+                        const float2 ns = make_float2(-sn.x, -sn.y);
+                        const float2 y0 = PR::fma(b[q], ns, PR::mul(a[q], cc));
+                        b[q] = PR::fma(a[q], sn, PR::mul(b[q], cc));
+                        a[q] = y0;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        const float ca = c[q], sa = s[q], cb = c[NP + q], sb = s[NP + q];
+                        a[q] = make_float2(__fmaf_rn(-a[q].y, sa, a[q].x * ca), __fmaf_rn(a[q].x, sa, a[q].y * ca));
+                        b[q] = make_float2(__fmaf_rn(-b[q].y, sb, b[q].x * cb), __fmaf_rn(b[q].x, sb, b[q].y * cb));
+                    }
+                }
+            }
+            const HeadSeg &g = p.seg[sg];
+            char *row = row_out<APPEND>(p, g, sg > 0, t, h - (sg == 0 ? 0 : sg == 1 ? hq : hqk), page, place);
+            if (row) {
+                // values that pass as they are keep their bits (a NaN's payload too)
+                const bool raw = sg == 2 || (!turns && !(APPEND && p.w[sg]));
+                if (has0) *reinterpret_cast<uint4 *>(row + e0 * (int)sizeof(T)) = raw ? x0[u] : pack<T>(a);
+                if (has1) *reinterpret_cast<uint4 *>(row + e1 * (int)sizeof(T)) = raw ? x1[u] : pack<T>(b);
+            }
+        }
+        hb += U * step;
+        if (hb >= h1) break;
+        load(hb);
+    }
+}
+
+// --------------------------------------------------------- element-wise --
+// Any head size, stride and alignment: a warp takes up to eight heads of a
+// token, a lane one pair at a time; a head's sum of squares is taken in a
+// pass of its own.
+constexpr int kElemHeads = 8;
+
+template <typename T, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads) rope_elements(const __grid_constant__ RopeParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (unit >= p.tokens * p.blocks) return;
+    const int64_t t = unit / p.blocks;
+    const int h0 = (int)(unit - t * p.blocks) * p.block_heads;
+    const int hq = p.seg[0].heads, hqk = hq + p.seg[1].heads;
+    const int htot = hqk + (APPEND ? p.seg[2].heads : 0);
+    const int n = min(p.block_heads, htot - h0);
+    int64_t page = 0;
+    int place = 0;
+    if (APPEND) find_slot(p, t, page, place);
+
+    const T *in[kElemHeads];
+    T *out[kElemHeads];
+    float rstd[kElemHeads];
+#pragma unroll
+    for (int u = 0; u < kElemHeads; ++u) {
+        in[u] = nullptr;
+        out[u] = nullptr;
+        rstd[u] = 1.f;
+        if (u >= n) continue;
+        const int h = h0 + u, sg = h < hq ? 0 : (h < hqk ? 1 : 2);
+        const HeadSeg &g = p.seg[sg];
+        const int hh = h - (sg == 0 ? 0 : sg == 1 ? hq : hqk);
+        in[u] = reinterpret_cast<const T *>(g.in + t * g.in_token + hh * g.in_head);
+        out[u] = reinterpret_cast<T *>(row_out<APPEND>(p, g, sg > 0, t, hh, page, place));
+        if (APPEND && sg < 2 && p.w[sg]) {
+            float ss = 0.f;
+            for (int i = lane; i < p.head_dim; i += 32) {
+                const float v = load_elem(in[u], i);
+                ss = __fmaf_rn(v, v, ss);
+            }
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            rstd[u] = rsqrtf(__fmaf_rn(ss, p.inv_n, p.eps));
+        }
+    }
+    // value i of head u, normalised
+    auto value = [&](int u, int sg, int i) {
+        float v = load_elem(in[u], i);
+        if (APPEND && sg < 2 && p.w[sg]) {
+            const float w = std::is_same<T, float>::value || p.w32
+                                ? load_w(reinterpret_cast<const float *>(p.w[sg]), i)
+                                : load_w(reinterpret_cast<const T *>(p.w[sg]), i);
+            v = v * rstd[u] * (p.offset + w);
+        }
+        return v;
+    };
+    for (int i = lane; i < p.half_dim; i += 32) {
+        const int e0 = p.adjacent ? 2 * i : i, e1 = p.adjacent ? 2 * i + 1 : i + p.half_dim;
+        float c = 1.f, s = 0.f;
+        if (h0 < hqk) angles_of<1>(p, t, i, &c, &s);
+#pragma unroll
+        for (int u = 0; u < kElemHeads; ++u) {
+            if (u >= n || !out[u]) continue;
+            const int h = h0 + u, sg = h < hq ? 0 : (h < hqk ? 1 : 2);
+            const float a = value(u, sg, e0), b = value(u, sg, e1);
+            store_elem(out[u], e0, sg == 2 ? a : __fmaf_rn(-b, s, a * c));
+            store_elem(out[u], e1, sg == 2 ? b : __fmaf_rn(a, s, b * c));
+        }
+    }
+    for (int i = 2 * p.half_dim + lane; i < p.head_dim; i += 32) {
+#pragma unroll
+        for (int u = 0; u < kElemHeads; ++u) {
+            if (u >= n || !out[u]) continue;
+            const int h = h0 + u, sg = h < hq ? 0 : (h < hqk ? 1 : 2);
+            store_elem(out[u], i, value(u, sg, i));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host --
+
+static int elem_bytes(int dt) { return (dt & 0xff) == RMSNORM_F32 ? 4 : 2; }
+
+static bool on16(int64_t a) { return a % 16 == 0; }
+
+template <typename T, bool APPEND>
+static int launch_rope(bool vec, const RopeParams &p, unsigned grid, cudaStream_t stream) {
+    LaunchCfg lc(grid, kRopeThreads, 0, stream);
+    return vec ? (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, APPEND>, p)
+               : (int)cudaLaunchKernelEx(&lc.cfg, rope_elements<T, APPEND>, p);
+}
+
+template <bool APPEND>
+static int launch_rope_dt(int base, bool vec, const RopeParams &p, unsigned grid, cudaStream_t s) {
+    switch (base) {
+    case RMSNORM_F32: return launch_rope<float, APPEND>(vec, p, grid, s);
+    case RMSNORM_BF16: return launch_rope<__nv_bfloat16, APPEND>(vec, p, grid, s);
+    default: return launch_rope<__half, APPEND>(vec, p, grid, s);
+    }
+}
+
+// The angles' part of the parameters; false: an invalid argument.
+static bool take_angles(const rope_angles_t &a, const uint8_t *axes, int head_dim, RopeParams &p) {
+    if (!a.inv_freq || !on(a.inv_freq, 4)) return false;
+    if (a.position_bytes != 4 && a.position_bytes != 8) return false;
+    if (!on(a.positions, (uintptr_t)a.position_bytes)) return false;
+    if (a.n_axes < 1 || a.n_axes > ROPE_MAX_AXES) return false;
+    if (a.rotary_dim < 2 || a.rotary_dim % 2 != 0 || a.rotary_dim > head_dim) return false;
+    if (a.pairing != ROPE_HALF && a.pairing != ROPE_ADJACENT) return false;
+    p.positions = a.positions;
+    p.inv_freq = a.inv_freq;
+    p.axis_stride = a.n_axes > 1 ? a.axis_stride : 0;
+    p.pos64 = a.position_bytes == 8;
+    p.naxes = a.n_axes;
+    p.half_dim = a.rotary_dim / 2;
+    p.adjacent = a.pairing == ROPE_ADJACENT;
+    for (int i = 0; axes && i < p.half_dim; ++i) {
+        if (axes[i] >= a.n_axes) return false;
+        p.axis[i >> 4] |= (uint32_t)axes[i] << (2 * (i & 15));
+    }
+    return true;
+}
+
+static HeadSeg segment(const rope_rows_t &r, int heads, int64_t tokens, int es) {
+    HeadSeg g;
+    std::memset(&g, 0, sizeof g);
+    g.in = static_cast<const char *>(r.in);
+    g.out = static_cast<char *>(r.out);
+    g.in_token = stride_of(r.in_token, tokens) * es;
+    g.in_head = stride_of(r.in_head, heads) * es;
+    g.out_token = stride_of(r.out_token, tokens) * es;
+    g.out_head = stride_of(r.out_head, heads) * es;
+    g.heads = heads;
+    return g;
+}
+
+static bool seg_on(const HeadSeg &g, uintptr_t a) { return g.heads == 0 || (on(g.in, a) && on(g.out, a)); }
+static bool seg_vec(const HeadSeg &g) {
+    return g.heads == 0 || (on(g.in, 16) && on(g.out, 16) && on16(g.in_token) && on16(g.in_head) &&
+                            on16(g.out_token) && on16(g.out_head) && on16(g.out_slot));
+}
+
+// Geometry and launch, the segments and the rest of `p` being set.
+template <bool APPEND>
+static rmsnorm_status_t run_rope(RopeParams &p, int base, cudaStream_t stream) {
+    const int es = elem_bytes(base), E = 16 / es;
+    int sms = 0;
+    int e = current_device(&sms, nullptr);
+    if (e != 0) return head_cuda_fail(e);
+    bool vec = p.half_dim % E == 0 && p.head_dim % E == 0 && on(p.inv_freq, 16);
+    for (const HeadSeg &g : p.seg) vec = vec && seg_vec(g);
+    for (const void *w : p.w) vec = vec && on(w, 16);
+    const int heads = p.seg[0].heads + p.seg[1].heads + p.seg[2].heads;
+    if (vec) {
+        p.items = p.half_dim / E + ((p.head_dim - 2 * p.half_dim) / E + 1) / 2;
+        while ((1 << p.lanes_log2) < p.items) ++p.lanes_log2;  // at most 32: head_dim <= 256
+        // One warp takes all heads of a token, so that their angles are
+        // computed once, as long as that leaves eight warps an SM; with
+        // fewer tokens the heads are halved until it does, down to one
+        // round of the warp's lanes.
+        const int round = 32 >> p.lanes_log2;
+        p.block_heads = (heads + round - 1) / round * round;
+        while (p.block_heads > round &&
+               p.tokens * ((heads + p.block_heads - 1) / p.block_heads) < (int64_t)8 * sms)
+            p.block_heads = (p.block_heads / round + 1) / 2 * round;
+    } else {
+        p.block_heads = kElemHeads;
+        while (p.block_heads > 1 && p.tokens * ((heads + p.block_heads - 1) / p.block_heads) < (int64_t)8 * sms)
+            p.block_heads /= 2;
+    }
+    p.blocks = (heads + p.block_heads - 1) / p.block_heads;
+    const int64_t warps = p.tokens * p.blocks;
+    const int64_t grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    if (grid > 0x7fffffffLL) return RMSNORM_ERR_UNSUPPORTED;
+    e = launch_rope_dt<APPEND>(base, vec, p, (unsigned)grid, stream);
+    return e == 0 ? RMSNORM_SUCCESS : head_cuda_fail(e);
+}
+
+static rmsnorm_status_t rope_impl(const rope_call_t *c, const uint8_t *axes, float sign, cudaStream_t stream) {
+    if (!c) return RMSNORM_ERR_INVALID_ARG;
+    if (c->dtype != RMSNORM_F32 && c->dtype != RMSNORM_BF16 && c->dtype != RMSNORM_F16) return RMSNORM_ERR_INVALID_ARG;
+    if (c->head_dim < 1 || c->head_dim > HEAD_MAX_DIM || c->tokens < 0 || c->tokens > 0x7fffffffLL ||
+        c->q_heads < 1 || c->k_heads < 0 || c->q_heads > 65535 || c->k_heads > 65535)
+        return RMSNORM_ERR_INVALID_ARG;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    if (!take_angles(c->angles, axes, c->head_dim, p)) return RMSNORM_ERR_INVALID_ARG;
+    if (c->tokens == 0) return RMSNORM_SUCCESS;
+    const int es = elem_bytes(c->dtype);
+    if (!c->angles.positions || !c->q.in || !c->q.out || (c->k_heads && (!c->k.in || !c->k.out)))
+        return RMSNORM_ERR_INVALID_ARG;
+    p.seg[0] = segment(c->q, c->q_heads, c->tokens, es);
+    p.seg[1] = segment(c->k, c->k_heads, c->tokens, es);
+    if (!seg_on(p.seg[0], es) || !seg_on(p.seg[1], es)) return RMSNORM_ERR_INVALID_ARG;
+    p.tokens = c->tokens;
+    p.head_dim = c->head_dim;
+    p.sign = sign;
+    return run_rope<false>(p, c->dtype, stream);
+}
+
+}  // namespace rmsn
+
+using namespace rmsn;
+
+extern "C" rmsnorm_status_t rope_fwd(const rope_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream) {
+    return rope_impl(call, axes, 1.f, (cudaStream_t)stream);
+}
+
+extern "C" rmsnorm_status_t rope_bwd(const rope_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream) {
+    return rope_impl(call, axes, -1.f, (cudaStream_t)stream);
+}
+
+extern "C" rmsnorm_status_t paged_kv_append(const paged_append_call_t *c, const uint8_t *axes,
+                                            rmsnorm_stream_t stream) {
+    if (!c) return RMSNORM_ERR_INVALID_ARG;
+    const int base = c->dtype & ~RMSNORM_WEIGHT_F32;
+    if (base != RMSNORM_F32 && base != RMSNORM_BF16 && base != RMSNORM_F16) return RMSNORM_ERR_INVALID_ARG;
+    const paged_cache_t &pc = c->cache;
+    if (c->head_dim < 1 || c->head_dim > HEAD_MAX_DIM || c->tokens < 0 || c->tokens > 0x7fffffffLL ||
+        c->q_heads < 0 || c->q_heads > 65535 || pc.heads < 1 || pc.heads > 65535)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (pc.page_size < 1 || pc.pages < 0 || pc.pages > (int64_t)1 << 40) return RMSNORM_ERR_INVALID_ARG;
+    if (!std::isfinite(c->eps) || !std::isfinite(c->offset) || c->eps < 0.f) return RMSNORM_ERR_INVALID_ARG;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    if (c->angles.positions && !take_angles(c->angles, axes, c->head_dim, p)) return RMSNORM_ERR_INVALID_ARG;
+    if (c->tokens == 0) return RMSNORM_SUCCESS;
+    const int es = elem_bytes(base);
+    if (!c->k.in || !c->v.in || !c->slots || !on(c->slots, 8) || !pc.k || !pc.v ||
+        (c->q_heads && (!c->q.in || !c->q.out)))
+        return RMSNORM_ERR_INVALID_ARG;
+    const uintptr_t wes = (c->dtype & RMSNORM_WEIGHT_F32) ? 4 : (uintptr_t)es;
+    if (!on(c->wq, wes) || !on(c->wk, wes)) return RMSNORM_ERR_INVALID_ARG;
+    p.seg[0] = segment(c->q, c->q_heads, c->tokens, es);
+    auto cached = [&](const rope_rows_t &r, void *cache, int64_t page, int64_t slot, int64_t head) {
+        HeadSeg g = segment(r, pc.heads, c->tokens, es);
+        g.out = static_cast<char *>(cache);
+        g.out_token = stride_of(page, pc.pages) * es;
+        g.out_slot = stride_of(slot, pc.page_size) * es;
+        g.out_head = stride_of(head, pc.heads) * es;
+        return g;
+    };
+    p.seg[1] = cached(c->k, pc.k, pc.k_page, pc.k_slot, pc.k_head);
+    p.seg[2] = cached(c->v, pc.v, pc.v_page, pc.v_slot, pc.v_head);
+    for (const HeadSeg &g : p.seg)
+        if (!seg_on(g, es)) return RMSNORM_ERR_INVALID_ARG;
+    p.slots = c->slots;
+    p.slots_end = pc.pages * pc.page_size;
+    p.page_size = pc.page_size;
+    p.w[0] = c->q_heads ? c->wq : nullptr;
+    p.w[1] = c->wk;
+    p.w32 = (c->dtype & RMSNORM_WEIGHT_F32) ? 1 : 0;
+    p.tokens = c->tokens;
+    p.head_dim = c->head_dim;
+    p.sign = 1.f;
+    p.eps = c->eps;
+    p.offset = c->offset;
+    p.inv_n = 1.f / (float)c->head_dim;
+    return run_rope<true>(p, base, (cudaStream_t)stream);
+}
