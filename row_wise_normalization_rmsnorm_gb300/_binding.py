@@ -89,12 +89,13 @@ SIGNATURES = {
     "rmsnorm_fwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i, _f, _f, _vp, _i, _PPlan]),
     "rmsnorm_bwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i, _f, _f, _vp,
                             _i, _i, _i, _i, _vp, _PPlan]),
-    # calls on head rows: a packed structure (_heads.py), the axes' bytes, the stream
-    "rope_fwd": (_i, [ctypes.c_char_p, ctypes.c_char_p, _vp]),
-    "rope_bwd": (_i, [ctypes.c_char_p, ctypes.c_char_p, _vp]),
-    "paged_kv_append": (_i, [ctypes.c_char_p, ctypes.c_char_p, _vp]),
-    "paged_attn_fwd": (_i, [ctypes.c_char_p, _vp]),
-    "paged_attn_workspace_bytes": (_sz, [ctypes.c_char_p]),
+    # calls on head rows: a structure, the axes' bytes, the stream (the Python
+    # functions go through _heads_ext, see _heads.py)
+    "rope_fwd": (_i, [_vp, ctypes.c_char_p, _vp]),
+    "rope_bwd": (_i, [_vp, ctypes.c_char_p, _vp]),
+    "paged_kv_append": (_i, [_vp, ctypes.c_char_p, _vp]),
+    "paged_attn_fwd": (_i, [_vp, _vp]),
+    "paged_attn_workspace_bytes": (_sz, [_vp]),
     "rmsnorm_status_string": (ctypes.c_char_p, [_i]),
     "rmsnorm_last_cuda_error": (_i, []),
     "rmsnorm_self_check": (_i, []),

@@ -1,4 +1,5 @@
-"""Build librmsnorm_gb300.so in-tree with nvcc for sm_103a.
+"""Build librmsnorm_gb300.so in-tree with nvcc for sm_103a, and the native
+Python module _heads_ext.so beside it with the host compiler.
 
 The translation units compile in parallel (one nvcc per file) into
 ``_build/`` and link into ``librmsnorm_gb300.so`` next to this file. The
@@ -12,10 +13,12 @@ Usage:  python -m row_wise_normalization_rmsnorm_gb300.build [--force]
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +26,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librmsnorm_gb300.so")
 HEADER = os.path.join(ROOT, "include", "rmsnorm.h")
+EXT = os.path.join(HERE, "_heads_ext.so")
+EXT_SOURCE = os.path.join(CSRC, "heads_ext.cpp")
 
 SOURCES = ["api.cu", "fwd_bf16.cu", "fwd_f32.cu", "fwd_f16.cu", "fwd_bf16w32.cu", "fwd_f16w32.cu",
            "fwd8_bf16.cu", "fwd8_f16.cu", "fwd8_f32.cu", "fwd8_bf16w32.cu", "fwd8_f16w32.cu", "ln_bf16.cu", "ln_f16.cu", "ln_f32.cu", "ln_bf16w32.cu", "ln_f16w32.cu",
@@ -47,6 +52,48 @@ def _mtime(p):
     return os.path.getmtime(p) if os.path.exists(p) else 0.0
 
 
+def _cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+
+
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")  # found, not imported
+    if spec is None or not spec.origin:
+        raise RuntimeError("PyTorch is required to build the Python module")
+    return os.path.dirname(spec.origin)
+
+
+def _ext_stale(force: bool) -> bool:
+    deps = [EXT_SOURCE, HEADER, os.path.abspath(__file__)]
+    return force or not os.path.exists(EXT) or max(_mtime(p) for p in deps) > _mtime(EXT)
+
+
+def _compile_ext() -> str:
+    t = _torch_dir()
+    obj = os.path.join(BUILD, "heads_ext.o")
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(_cuda_home(), "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(a for d in inc for a in ("-isystem", d)),
+           "-c", EXT_SOURCE, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for heads_ext.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj: str) -> None:
+    """The module finds the library beside itself; PyTorch's libraries are in
+    the process that imports it."""
+    t = os.path.join(_torch_dir(), "lib")
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + t,
+           "-Wl,-rpath," + t, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of heads_ext failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def _stale(force: bool) -> bool:
     if force or not os.path.exists(LIB):
         return True
@@ -65,21 +112,29 @@ def _compile(src: str, extra: list[str]) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile (if any source changed) and return the library path."""
-    if not _stale(force):
+    lib_stale, ext_stale = _stale(force), _ext_stale(force)
+    if not lib_stale and not ext_stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext_obj = ex.submit(_compile_ext) if ext_stale else None
+        if lib_stale:
+            _link(list(ex.map(lambda s: _compile(s, extra), SOURCES)))
+        if ext_obj:
+            _link_ext(ext_obj.result())
+    return LIB
+
+
+def _link(objs: list[str]) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -38,8 +38,6 @@
 #include "head_rows.h"
 #include "tcgen05.cuh"
 
-static_assert(sizeof(paged_attn_call_t) == 232, "paged_attn_call_t");
-
 namespace rmsn {
 
 constexpr int kKeyTile = 128;
@@ -73,7 +71,10 @@ struct AttnShape {
     static constexpr int kStages = NQ == 2 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 3 : 6);
     static constexpr int kBars = NQ * kQBytes + kStages * kStage;
     static constexpr int kSmem = kBars + 256;
-    static constexpr int kThreads = NQ * 128 + 64;
+    // NQ == 2: the copy and issue warps fill up a warpgroup of their own, so
+    // that registers can move to the softmax warps: 168 a thread at launch,
+    // then 2 x 128 x 208 + 128 x 88 = 384 x 168
+    static constexpr int kThreads = NQ == 2 ? 384 : 192;
     static constexpr int kRows = NQ * kQRows;  // packed rows a CTA takes
     // tensor memory: s (and p) of each tile, then o of each tile
     static constexpr uint32_t kO = NQ * kKeyTile;
@@ -88,6 +89,12 @@ struct AttnShape {
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
@@ -106,10 +113,10 @@ struct Waiter {
     volatile int *gave_up;  // shared memory
     int *status;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait_cta(bar, parity)) return true;
         const uint64_t began = now_ns();
         for (uint32_t i = 0; i < kAttnWait; ++i) {
-            if (mbar_try_wait(bar, parity)) return true;
+            if (mbar_try_wait_cta(bar, parity)) return true;
             if ((i & 15u) == 15u && (*gave_up || now_ns() - began > kAttnWaitNs)) break;
         }
         *gave_up = 1;
@@ -119,7 +126,7 @@ struct Waiter {
 };
 
 template <typename T, int DP, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
+__global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
     paged_attn(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap) {
     using S = AttnShape<DP, NQ>;
@@ -166,11 +173,11 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
     }
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
     uint64_t *full = bars, *empty = bars + NST;
-    uint64_t *s_ready = empty + NST, *p_ready = s_ready + NQ, *o_done = p_ready + NQ;
+    uint64_t *s_ready = empty + NST, *p_half = s_ready + NQ, *p_ready = p_half + NQ, *o_done = p_ready + NQ;
     uint64_t *q_ready = o_done + NQ, *v_fixed = q_ready + 1, *drained = v_fixed + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     volatile int *gave_up = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * S::kStages + 3 * NQ + 3) * 8 + 8 <= 256, "barriers");
+    static_assert((2 * S::kStages + 4 * NQ + 3) * 8 + 8 <= 256, "barriers");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -180,7 +187,8 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
         for (int t = 0; t < NQ; ++t) {
             const int live = min(max(rows - t * 128, 0), 128);
             mbar_init(s_ready + t, 1);
-            mbar_init(p_ready + t, live > 0 ? (live + 31) / 32 : 1);  // its warps with rows
+            mbar_init(p_half + t, live > 0 ? (live + 31) / 32 : 1);  // its warps with rows
+            mbar_init(p_ready + t, live > 0 ? (live + 31) / 32 : 1);
             mbar_init(o_done + t, 1);
         }
         mbar_init(q_ready, NQ * 4);
@@ -201,6 +209,8 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t stage0 = sbase + NQ * S::kQBytes;
 
+    if (warp >= kProducer) {
+    if constexpr (NQ == 2) fewer_registers<88>();
     if (warp == kProducer) {
         // ---------------------------------------------------- K and V copies
         // A tile is 128 / box_rows boxes by 64 columns; lane l copies piece
@@ -265,58 +275,80 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
         }
     } else if (warp == kIssuer) {
         // ------------------------------------------- the matrix instructions
-        if (lane == 0) {
-            const int ksteps = (p.head_dim + 15) / 16;
-            const uint32_t qk_word = mma_word(std::is_same<T, __nv_bfloat16>::value, 128, kKeyTile, 0);
-            const uint32_t pv_word = mma_word(std::is_same<T, __nv_bfloat16>::value, 128, (uint32_t)ksteps * 16, 1);
-            auto qk = [&](int t, int st) {
-                const uint32_t qa = sbase + t * S::kQBytes, ka = stage0 + st * S::kStage;
-                for (int i = 0; i < ksteps; ++i) {
-                    const uint32_t h = i >> 2, o = (i & 3) * 32;
-                    mma_ss(tmem + t * kKeyTile, smem_operand(qa + h * (S::kQRows * 128) + o, 16, 1024),
-                           smem_operand(ka + h * (kKeyTile * 128) + o, 16, 1024), qk_word, i > 0);
+        // The whole warp walks the tiles (operands stay uniform), one lane issues.
+        const bool issues = elect_one();
+        const int ksteps = (p.head_dim + 15) / 16;
+        const uint32_t qk_word = mma_word(std::is_same<T, __nv_bfloat16>::value, 128, kKeyTile, 0);
+        const uint32_t pv_word = mma_word(std::is_same<T, __nv_bfloat16>::value, 128, (uint32_t)ksteps * 16, 1);
+        const uint64_t q_op = smem_operand(sbase, 16, 1024);
+        const uint64_t k_op = smem_operand(stage0, 16, 1024);
+        const uint64_t v_op = smem_operand(stage0, kKeyTile * 128, 1024);
+        // (an operand's address field counts 16 bytes)
+        auto qk = [&](int t, int st) {
+            if (issues) {
+                const uint64_t a = q_op + (uint64_t)(t * S::kQBytes / 16), b = k_op + (uint64_t)(st * (S::kStage / 16));
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const int h = i >> 2, o = (i & 3) * 2;
+                    if (i < ksteps)
+                        mma_ss(tmem + t * kKeyTile, a + (uint64_t)(h * (S::kQRows * 8) + o), b + (uint64_t)(h * (kKeyTile * 8) + o),
+                               qk_word, i > 0);
                 }
                 mma_commit(s_ready + t);
-            };
-            auto pv = [&](int t, int st, bool add) {
-                const uint32_t va = stage0 + st * S::kStage;
+            }
+            __syncwarp();
+        };
+        // half the keys' product
+        auto pv = [&](int t, int st, int half, bool add) {
+            if (issues) {
+                const uint64_t b = v_op + (uint64_t)(st * (S::kStage / 16) + half * (kKeyTile / 32) * 128);
+                const uint32_t a = tmem + t * kKeyTile + half * (kKeyTile / 4);
 #pragma unroll
-                for (int i = 0; i < kKeyTile / 16; ++i)
-                    mma_ts(tmem + S::kO + t * DP, tmem + t * kKeyTile + i * 8,
-                           smem_operand(va + i * 2048, kKeyTile * 128, 1024), pv_word, add || i > 0);
-                mma_commit(o_done + t);
-            };
-            // stage and phase of the ring's n-th tile (K_0, V_0, K_1, V_1, ...)
-            auto arrived = [&](int n) { return wait(full + n % NST, (uint32_t)((n / NST) & 1)); };
-            bool ok = wait(q_ready, 0) && (ntiles == 0 || arrived(0));
-            if (ok && ntiles > 0) {
-                tc_after_sync();
-                for (int t = 0; t < act; ++t) qk(t, 0);
-                mma_commit(empty + 0);
+                for (int i = 0; i < kKeyTile / 32; ++i)
+                    mma_ts(tmem + S::kO + t * DP, a + i * 8, b + (uint64_t)(i * 128), pv_word, add || i > 0);
+                if (half) mma_commit(o_done + t);
             }
-            for (int j = 0; j < ntiles && ok; ++j) {
-                const bool more = j + 1 < ntiles;
-                ok = arrived(2 * j + 1) && (more || !fix || wait(v_fixed, 0));
-                for (int t = 0; t < act && ok; ++t) {
-                    ok = wait(p_ready + t, (uint32_t)(j & 1));
-                    if (!ok) break;
-                    tc_after_sync();
-                    pv(t, (2 * j + 1) % NST, j > 0);
-                    if (t == act - 1) mma_commit(empty + (2 * j + 1) % NST);
-                    if (more) {
-                        if (t == 0) ok = arrived(2 * j + 2);
-                        if (ok) qk(t, (2 * j + 2) % NST);
-                    }
-                }
-                if (more && ok) mma_commit(empty + (2 * j + 2) % NST);
-            }
-            if (*gave_up) {  // nor may a matrix instruction be
-                mma_commit(drained);
-                Waiter{&still, p.status}(drained, 0);
-            }
+            __syncwarp();
+        };
+        auto free_stage = [&](int n) {
+            if (issues) mma_commit(empty + n % NST);
+            __syncwarp();
+        };
+        // stage and phase of the ring's n-th tile (K_0, V_0, K_1, V_1, ...)
+        auto arrived = [&](int n) { return warp_wait(full + n % NST, (uint32_t)((n / NST) & 1)); };
+        bool ok = warp_wait(q_ready, 0) && (ntiles == 0 || arrived(0));
+        if (ok && ntiles > 0) {
+            tc_after_sync();
+            for (int t = 0; t < act; ++t) qk(t, 0);
+            free_stage(0);
         }
+        for (int j = 0; j < ntiles && ok; ++j) {
+            const bool more = j + 1 < ntiles;
+            ok = arrived(2 * j + 1) && (more || !fix || warp_wait(v_fixed, 0));
+            for (int t = 0; t < act && ok; ++t) {
+                if (!(ok = warp_wait(p_half + t, (uint32_t)(j & 1)))) break;
+                tc_after_sync();
+                pv(t, (2 * j + 1) % NST, 0, j > 0);
+                if (!(ok = warp_wait(p_ready + t, (uint32_t)(j & 1)))) break;
+                tc_after_sync();
+                pv(t, (2 * j + 1) % NST, 1, true);
+                if (t == act - 1) free_stage(2 * j + 1);
+                if (more) {
+                    if (t == 0) ok = arrived(2 * j + 2);
+                    if (ok) qk(t, (2 * j + 2) % NST);
+                }
+            }
+            if (more && ok) free_stage(2 * j + 2);
+        }
+        if (*gave_up) {  // nor may a matrix instruction be
+            __syncwarp();
+            if (issues) mma_commit(drained);
+            Waiter{&still, p.status}(drained, 0);
+        }
+    }
     } else {
         // --------------------------------------------------------- softmax
+        if constexpr (NQ == 2) more_registers<208>();
         const int t = warp >> 2, r = threadIdx.x & 127;  // tile, row in it
         // q, 16 bytes a step, to the swizzled rows (zeros past the rows and head_dim)
         {
@@ -376,14 +408,16 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
                         for (int i = 0; i < 32; ++i)
                             if (32 * q + i >= n) s[q][i] = 0xff800000u;  // -infinity
                 }
-                float mx[4];
+                float mx[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mx[q] = __uint_as_float(s[q][0]);
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t *v = &s[q >> 1][16 * (q & 1)];
+                    mx[q] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                    for (int i = 2; i < 16; i += 2)
+                        mx[q] = max3(mx[q], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                 }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
                 const bool grown = mt > m && (m == -INFINITY || (mt - m) * c > kRescale);
                 if (__any_sync(0xffffffffu, grown)) {
                     const float mn = grown ? mt : m;
@@ -413,22 +447,35 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 2 ? 1 : 2)
                 const float mc = m == -INFINITY ? 0.f : -m * c;
                 const float2 c2 = make_float2(c, c), m2 = make_float2(mc, mc);
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    uint32_t w[32];
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int qq = q + (i >> 4), e = 2 * (i & 15);
-                        float2 x = PR::fma(make_float2(__uint_as_float(s[qq][e]), __uint_as_float(s[qq][e + 1])), c2, m2);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = PR::fma(make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, m2);
                         x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                        l2 = PR::add(l2, x);
                         w[i] = pack_pair<T>(x);
+                        s[q][2 * i] = __float_as_uint(x.x);
+                        s[q][2 * i + 1] = __float_as_uint(x.y);
                     }
-                    tmem_st32(ts + 16 * q, w);
+                    tmem_st16(ts + 16 * q, w);
+                    if (q & 1) {
+                        // half of p is there: its product can start
+                        tmem_wait_st();
+                        tc_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive((q == 1 ? p_half : p_ready) + t);
+                    }
                 }
-                tmem_wait_st();
-                tc_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + t);
+                // the sum, off the path that the products wait for
+                float2 a2[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a2[q] = make_float2(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2)
+                        a2[q] = PR::add(a2[q], make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
+                }
+                l2 = PR::add(l2, PR::add(PR::add(a2[0], a2[1]), PR::add(a2[2], a2[3])));
             }
             // ------------------------------------------------------ results
             if (ok && ntiles > 0) {

@@ -21,10 +21,6 @@
 #include "common.cuh"
 #include "head_rows.h"
 
-// the structures as the Python binding packs them
-static_assert(sizeof(rope_call_t) == 160, "rope_call_t");
-static_assert(sizeof(paged_append_call_t) == 320, "paged_append_call_t");
-
 namespace rmsn {
 
 struct HeadSeg {

@@ -84,6 +84,20 @@ __host__ __device__ constexpr uint32_t mma_word(bool bf16, uint32_t m, uint32_t 
            ((m >> 4) << 24);
 }
 
+// True for one lane of the (converged) warp. The matrix instructions take
+// their operands from uniform registers; under this predicate the compiler
+// keeps them there, while under `lane == 0` each one cost 125 cycles to
+// issue, twice what it takes to execute.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
 // D (tensor memory) = A B (+ D). One thread issues; A in shared memory ...
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add) {
     asm volatile(
@@ -109,8 +123,30 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
                  : "memory");
 }
 
+// Registers of the calling warpgroup (all four warps call it), from the
+// pool that the block was launched with.
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// True once the phase with the given parity has completed; acquire within
+// the CTA (the cluster-wide form costs a hundred cycles more a call).
+__device__ __forceinline__ bool mbar_try_wait_cta(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 // Generic-proxy writes to shared memory ordered before the async proxy's
 // reads (matrix instructions, copies).
