@@ -367,8 +367,8 @@ typedef struct {
  * Rotary positions with one to four axes (e.g. time, height and width).
  * With a = axes[i], c = cos(p_a f_i), s = sin(p_a f_i) and (x1, x2) the pair
  * of frequency i:   y1 = x1 c - x2 s,   y2 = x2 c + x1 s.
- * The angle's product and its reduction to one turn carry about 48 bits, so
- * far positions lose nothing; cos, sin and the products are fp32, each
+ * The angle's product is reduced to one turn in 64-bit fixed point, so far
+ * positions lose nothing (for |inv_freq| < 2); cos, sin and the products are fp32, each
  * output rounded once. axes: HOST pointer to rotary_dim / 2 bytes, the axis
  * of each frequency, or NULL (all on axis 0).
  * rope_bwd is the gradient: `in` holds the gradient of the outputs, `out`

@@ -733,6 +733,14 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     const bool empty = pc.pages == 0 || c.table_width == 0 || c.max_kv == 0;
     if (!empty && (!pc.k || !pc.v || !c.block_table)) return RMSNORM_ERR_INVALID_ARG;
 
+    // what a tiled copy takes: 16-byte boundaries everywhere
+    auto legal = [&](const void *base, int64_t page, int64_t slot, int64_t head) {
+        auto ok = [](int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 38); };
+        return on(base, 16) && ok(page, pc.pages) && ok(slot, pc.page_size) && ok(head, pc.heads);
+    };
+    if (!empty && (!legal(pc.k, pc.k_page, pc.k_slot, pc.k_head) || !legal(pc.v, pc.v_page, pc.v_slot, pc.v_head)))
+        return RMSNORM_ERR_UNSUPPORTED;
+
     int sms = 0, *status = nullptr;
     int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
@@ -747,12 +755,6 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     std::memset(&vm, 0, sizeof vm);
     p.box_rows = gcd_of(pc.page_size, kKeyTile);
     if (!empty) {
-        auto legal = [&](const void *base, int64_t page, int64_t slot, int64_t head) {
-            auto ok = [](int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 38); };
-            return on(base, 16) && ok(page, pc.pages) && ok(slot, pc.page_size) && ok(head, pc.heads);
-        };
-        if (!legal(pc.k, pc.k_page, pc.k_slot, pc.k_head) || !legal(pc.v, pc.v_page, pc.v_slot, pc.v_head))
-            return RMSNORM_ERR_UNSUPPORTED;
         if (!cache_map(&km, c.dtype, pc.k, c.head_dim, pc, pc.k_page, pc.k_slot, pc.k_head, p.box_rows) ||
             !cache_map(&vm, c.dtype, pc.v, c.head_dim, pc, pc.v_page, pc.v_slot, pc.v_head, p.box_rows))
             return RMSNORM_ERR_UNSUPPORTED;

@@ -4,9 +4,9 @@
 //
 // The mathematics: frequency i of token t turns one pair of a head's values
 // by the angle p f (position times frequency). The angle is reduced to a
-// fraction of a turn with error-free fp32 products (half_turns), since
-// fp32's p f has lost its fraction where p is large, and the device's fp64
-// rate is too low to spend on it; sincospif takes the fraction.
+// fraction of a turn in 64-bit integers (half_turns), since fp32's p f has
+// lost its fraction where p is large, and the device's fp64 rate is too low
+// to spend on it; sincospif takes the fraction.
 //
 // What bounds it: memory. Every value is read once and written once, at a
 // few fp32 operations a value; the angles are shared by all heads of a
@@ -51,32 +51,27 @@ struct RopeParams {
 };
 
 // ------------------------------------------------------------- angles --
-// The fraction of a turn that p f is, as sincospif's argument (half turns).
-// p = hi + lo with hi a multiple of 4096, both exact in fp32; each product
-// with f is kept as its rounding and its error, and each rounding is scaled
-// by 1 / (2 pi) in three fp32 parts (72 bits), its own rounding error kept as
-// well, before the whole turns are dropped: what remains is the rounding of
-// a fraction of a turn, a few 2^-25 of it, for |p| < 2^31 and f <= 1.
-__device__ __forceinline__ float part_turns(float p, float &rest) {
-    const float c1 = 0x1.45f306p-3f, c2 = 0x1.b9391p-28f, c3 = 0x1.529fc2p-54f;
-    const float t = __fmul_rn(p, c1);
-    rest += __fmaf_rn(p, c1, -t) + __fmaf_rn(p, c2, __fmul_rn(p, c3));
-    return t - rintf(t);
+// The angle p f is wanted modulo a turn, and fp32's p f has lost that where p
+// is large. So the frequency is taken as a 64-bit fixed-point fraction of a
+// turn, g = f / (2 pi) 2^64 (turn_step), and p g in wrapping integer
+// arithmetic is the angle modulo a turn at once, exact but for g's last bit
+// times p: below 2^-32 of a turn for |p| < 2^31 and |f| < 2. Its top 32 bits
+// in fp32 (2^-26 of a turn) are sincospif's argument.
+__device__ __forceinline__ int64_t turn_step(float f) {
+    constexpr uint64_t kPerTurn = 0xa2f9836e4e44152aull;  // 2^66 / (2 pi)
+    const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;
+    const int ex = (int)(bits >> 23);
+    // |f| = m 2^(ex - 150), m of 24 bits (a denormal's step is below one unit)
+    const uint64_t m = (bits & 0x7fffffu) | 0x800000u;
+    const uint64_t top = __umul64hi(m << 40, kPerTurn);  // m kPerTurn / 2^24
+    const int shift = ex - 128;                          // g = top 2^(ex - 150 - 2 + 24)
+    const uint64_t g = shift <= -64 ? 0 : (shift < 0 ? top >> -shift : (shift < 64 ? top << shift : 0));
+    return f < 0.f ? -(int64_t)g : (int64_t)g;
 }
-__device__ __forceinline__ float half_turns(int64_t pos, float f) {
-    const float c1 = 0x1.45f306p-3f;
-    const int p32 = (int)pos;
-    const float lo = (float)(p32 & 4095), hi = (float)(p32 - (p32 & 4095));
-    const float pl = __fmul_rn(lo, f);
-    float rest = __fmul_rn(__fmaf_rn(lo, f, -pl), c1);
-    float t = part_turns(pl, rest);
-    if (hi != 0.f) {
-        const float ph = __fmul_rn(hi, f);
-        rest += __fmul_rn(__fmaf_rn(hi, f, -ph), c1);
-        t += part_turns(ph, rest);
-    }
-    t += rest;
-    return 2.f * (t - rintf(t));
+// In half turns, [-1, 1).
+__device__ __forceinline__ float half_turns(int64_t pos, int64_t step) {
+    const uint64_t a = (uint64_t)pos * (uint64_t)step;
+    return (float)(int32_t)(uint32_t)(a >> 32) * 0x1p-31f;
 }
 
 __device__ __forceinline__ int64_t position(const RopeParams &p, int axis, int64_t t) {
@@ -101,7 +96,8 @@ __device__ __forceinline__ void angles_of(const RopeParams &p, int64_t t, int i0
             const int a = axis_of(p, i0 + i);
             pos = a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
         }
-        sincospif(half_turns(pos, __ldg(p.inv_freq + i0 + i)), s + i, c + i);
+        const float f = __ldg(p.inv_freq + i0 + i);
+        sincospif(isfinite(f) ? half_turns(pos, turn_step(f)) : NAN, s + i, c + i);
         s[i] *= p.sign;
     }
 }
