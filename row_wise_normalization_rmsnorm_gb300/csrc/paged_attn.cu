@@ -59,7 +59,8 @@ struct AttnParams {
     float c;  // scale * log2(e)
     int batch, width, heads, kv_heads, group, head_dim, pages, page_size, box_rows;
     int max_q, max_kv, causal, q_tiles, splits, chunk;  // chunk: keys a split takes
-    int q_vec, out_vec;
+    int tile_toks;                                      // tokens a row tile takes
+    int q_tma, q_vec, out_vec;
 };
 
 template <int DP, int NQ>
@@ -75,7 +76,6 @@ struct AttnShape {
     // that registers can move to the softmax warps: 168 a thread at launch,
     // then 2 x 128 x 208 + 128 x 88 = 384 x 168
     static constexpr int kThreads = NQ == 2 ? 384 : 192;
-    static constexpr int kRows = NQ * kQRows;  // packed rows a CTA takes
     // tensor memory: s (and p) of each tile, then o of each tile
     static constexpr uint32_t kO = NQ * kKeyTile;
     static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;
@@ -127,8 +127,8 @@ struct Waiter {
 
 template <typename T, int DP, int NQ>
 __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
-    paged_attn(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-               const __grid_constant__ CUtensorMap vmap) {
+    paged_attn(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
+               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using S = AttnShape<DP, NQ>;
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int NST = S::kStages;
@@ -152,18 +152,18 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
     const int nq = min(max(__ldg(p.cu_q + b + 1), q0), T_) - q0;  // the sequence's new tokens
     const int nq_out = min(nq, p.max_q);                           // those that are written
     const int kv = max(0, min(min(__ldg(p.kv_lens + b), p.max_kv), (int)min((int64_t)p.width * p.page_size, (int64_t)0x7fffffff)));
-    const int row0 = qt * S::kRows;
-    const int rows = min(nq_out * p.group - row0, S::kRows);
-    if (rows <= 0) return;
+    const int tt = p.tile_toks, tok0 = qt * NQ * tt;
+    const int toks = min(nq_out - tok0, NQ * tt);  // the CTA's tokens, tt a tile
+    if (toks <= 0) return;
     // keys that the CTA's last row sees, and this split's part of them
-    const int last_tok = (row0 + rows - 1) / p.group;
+    const int last_tok = tok0 + toks - 1;
     const int64_t lim = p.causal ? min((int64_t)kv, max((int64_t)0, (int64_t)kv - nq + last_tok + 1)) : kv;
     const int64_t kbeg64 = (int64_t)split * p.chunk;
     const int64_t kend64 = p.splits > 1 ? min(lim, kbeg64 + p.chunk) : lim;
     if (p.splits > 1 && kend64 <= kbeg64) return;
     const int kbeg = (int)kbeg64, kend = (int)kend64;
     const int ntiles = (kend - kbeg + kKeyTile - 1) / kKeyTile;
-    const int act = NQ == 2 ? (rows > 128 ? 2 : 1) : 1;  // tiles with rows
+    const int act = toks > tt ? 2 : 1;  // tiles with rows
     const int last_valid = kv - (kbeg + (ntiles - 1) * kKeyTile);  // cached keys of the last tile
     const bool fix = ntiles > 0 && last_valid < kKeyTile && last_valid % p.box_rows != 0;
 
@@ -185,13 +185,13 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             mbar_init(empty + i, 1);
         }
         for (int t = 0; t < NQ; ++t) {
-            const int live = min(max(rows - t * 128, 0), 128);
+            const int live = min(max(toks - t * tt, 0), tt) * p.group;  // rows of the tile
             mbar_init(s_ready + t, 1);
             mbar_init(p_half + t, live > 0 ? (live + 31) / 32 : 1);  // its warps with rows
             mbar_init(p_ready + t, live > 0 ? (live + 31) / 32 : 1);
             mbar_init(o_done + t, 1);
         }
-        mbar_init(q_ready, NQ * 4);
+        mbar_init(q_ready, p.q_tma ? 1 : NQ * 4);
         mbar_init(v_fixed, 1);
         mbar_init(drained, 1);
         *gave_up = 0;
@@ -232,6 +232,14 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         };
         int page, place, next_page, next_place;
         find(0, page, place);
+        if (p.q_tma && lane == 0) {
+            // q's rows: tt tokens of `group` heads are one box, row after row
+            mbar_arrive_expect_tx(q_ready, (uint32_t)(act * S::kHalves * tt * p.group * 128));
+            for (int t = 0; t < act; ++t)
+                for (int h = 0; h < S::kHalves; ++h)
+                    tile_g2s(sbase + t * S::kQBytes + h * (S::kQRows * 128), &qmap, h * 64, 0, kvh, q0 + tok0 + t * tt, q_ready);
+        }
+        __syncwarp();
         int issued = 0;
         bool ok = true;
         for (int j = 0; j < ntiles && ok; ++j) {
@@ -271,6 +279,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         }
         if (*gave_up) {  // no copy may be in flight when the CTA ends
             const Waiter last{&still, p.status};
+            if (p.q_tma) last(q_ready, 0);
             for (int i = max(0, issued - NST); i < issued; ++i) last(full + i % NST, (uint32_t)((i / NST) & 1));
         }
     } else if (warp == kIssuer) {
@@ -321,10 +330,11 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             tc_after_sync();
             for (int t = 0; t < act; ++t) qk(t, 0);
             free_stage(0);
+            ok = arrived(1);
         }
         for (int j = 0; j < ntiles && ok; ++j) {
             const bool more = j + 1 < ntiles;
-            ok = arrived(2 * j + 1) && (more || !fix || warp_wait(v_fixed, 0));
+            if (!more && fix) ok = warp_wait(v_fixed, 0);
             for (int t = 0; t < act && ok; ++t) {
                 if (!(ok = warp_wait(p_half + t, (uint32_t)(j & 1)))) break;
                 tc_after_sync();
@@ -336,6 +346,8 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
                 if (more) {
                     if (t == 0) ok = arrived(2 * j + 2);
                     if (ok) qk(t, (2 * j + 2) % NST);
+                    // (here, where the products just issued cover the wait)
+                    if (ok && t == 0) ok = arrived(2 * j + 3);
                 }
             }
             if (more && ok) free_stage(2 * j + 2);
@@ -350,38 +362,47 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         // --------------------------------------------------------- softmax
         if constexpr (NQ == 2) more_registers<208>();
         const int t = warp >> 2, r = threadIdx.x & 127;  // tile, row in it
-        // q, 16 bytes a step, to the swizzled rows (zeros past the rows and head_dim)
-        {
-            const int chunks = S::kHalves * 8, total = S::kQRows * chunks;
-            const int hd_chunks = p.head_dim / 8;
-            for (int i = r; i < total; i += 128) {
-                const int rr = i / chunks, c = i % chunks;
-                const int row = t * 128 + rr;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row < rows && c < hd_chunks) {
-                    const int tok = (row0 + row) / p.group, g = row0 + row - tok * p.group;
-                    const char *src = p.q + (int64_t)(q0 + tok) * p.q_token + (int64_t)(kvh * p.group + g) * p.q_head + c * 16;
-                    if (p.q_vec) {
-                        v = __ldg(reinterpret_cast<const uint4 *>(src));
-                    } else {
-                        const uint16_t *s16 = reinterpret_cast<const uint16_t *>(src);
-                        uint32_t w[4];
+        if (!p.q_tma) {
+            // q that a tiled copy does not take (bases or strides off 16-byte
+            // boundaries): eight chunks in flight a thread, to the swizzled rows,
+            // zeros past the rows and head_dim
+            constexpr int kChunks = S::kHalves * 8, kBatch = 8;
+            const int rows = min(max(toks - t * tt, 0), tt) * p.group, hd_chunks = p.head_dim / 8;
+            for (int i0 = r; i0 < S::kQRows * kChunks; i0 += 128 * kBatch) {
+                uint4 v[kBatch];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = (uint32_t)s16[2 * k] | ((uint32_t)s16[2 * k + 1] << 16);
-                        v = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + u * 128, rr = i / kChunks, c = i % kChunks;
+                    v[u] = make_uint4(0, 0, 0, 0);
+                    if (rr < rows && c < hd_chunks) {
+                        const int tok = rr / p.group, g = rr - tok * p.group;
+                        const char *src = p.q + (int64_t)(q0 + tok0 + t * tt + tok) * p.q_token +
+                                          (int64_t)(kvh * p.group + g) * p.q_head + c * 16;
+                        if (p.q_vec) {
+                            v[u] = __ldg(reinterpret_cast<const uint4 *>(src));
+                        } else {
+                            const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
+                            v[u] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                              e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                        }
                     }
                 }
-                sts128(smem + t * S::kQBytes + (c >> 3) * (S::kQRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), v);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + u * 128, rr = i / kChunks, c = i % kChunks;
+                    if (rr < S::kQRows)
+                        sts128(smem + t * S::kQBytes + (c >> 3) * (S::kQRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), v[u]);
+                }
             }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
 
-        const int row = t * 128 + r;
-        if (t * 128 + (warp & 3) * 32 < rows) {  // the warp has rows
-            const bool live = row < rows;
-            const int tok = (row0 + row) / p.group, g = row0 + row - tok * p.group;
+        const int rows = min(max(toks - t * tt, 0), tt) * p.group;
+        if ((warp & 3) * 32 < rows) {  // the warp has rows
+            const bool live = r < rows;
+            const int tok = tok0 + t * tt + r / p.group, g = r % p.group;
             // keys this row sees, counted from the split's first; a row past the
             // end masks nothing (its result goes nowhere)
             const int64_t seen = p.causal ? max((int64_t)0, min((int64_t)kv, (int64_t)kv - nq + tok + 1)) : kv;
@@ -631,26 +652,35 @@ static EncodeTiled encoder() {
 
 static int gcd_of(int a, int b) { return b == 0 ? a : gcd_of(b, a % b); }
 
-// The cache as a 4-D array (head_dim, place in the page, head, page), copied
-// in boxes of 64 values by `rows` places, swizzled by 128 bytes.
-static bool cache_map(CUtensorMap *map, int dtype, void *base, int d, const paged_cache_t &c, int64_t page,
-                      int64_t slot, int64_t head, int rows) {
+struct Three {
+    int64_t v[3];
+};
+
+// A 4-D array (head_dim and three more dimensions, strides in elements of 2
+// bytes) copied in boxes of 64 values by `box1` by 1 by `box3`, swizzled by
+// 128 bytes. The cache: (head_dim, place in the page, head, page); q:
+// (head_dim, head in the group, key head, token).
+static bool tile_map(CUtensorMap *map, int dtype, const void *base, int d, Three n, Three stride, int box1, int box3) {
     EncodeTiled enc = encoder();
     if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n.v[0], (cuuint64_t)n.v[1], (cuuint64_t)n.v[2]};
+    cuuint64_t strides[3];
     // a dimension of one entry has no stride: any legal value serves
-    const int64_t row = d * 2;
-    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)(c.page_size > 1 ? slot * 2 : row), (cuuint64_t)(c.heads > 1 ? head * 2 : row),
-                                   (cuuint64_t)(c.pages > 1 ? page * 2 : row)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return enc(map, dtype == RMSNORM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
-               dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    for (int i = 0; i < 3; ++i) strides[i] = (cuuint64_t)(n.v[i] > 1 ? stride.v[i] : d) * 2;
+    const cuuint32_t box[4] = {64, (cuuint32_t)box1, 1, (cuuint32_t)box3}, ones[4] = {1, 1, 1, 1};
+    return enc(map, dtype == RMSNORM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+               const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// Strides (in elements of 2 bytes) and base that a tiled copy takes: 16-byte
+// boundaries everywhere.
+static bool tile_stride(int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 38); }
 
 // How a call is cut: the geometry, the row tiles and the splits over keys.
 struct AttnCut {
-    int nq, q_tiles, splits, chunk;
+    int nq, tile_toks, q_tiles, splits, chunk;
     size_t workspace;
 };
 
@@ -661,8 +691,10 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
     // few rows: the cache's bytes bound the call, and 64 rows a CTA let two
     // CTAs share an SM
     k.nq = rows <= 64 ? 1 : 2;
-    const int64_t per = k.nq == 1 ? 64 : 256;
-    k.q_tiles = (int)((rows + per - 1) / per);
+    // a row tile takes whole tokens: the tiled copy of q then is one box
+    k.tile_toks = (int)((k.nq == 1 ? 64 : 128) / group);
+    const int64_t per = (int64_t)k.nq * k.tile_toks;
+    k.q_tiles = (int)(((int64_t)c.max_q + per - 1) / per);
     const int64_t ctas = (int64_t)c.batch * c.cache.heads * k.q_tiles;
     const int64_t slots = (int64_t)sms * (k.nq == 1 ? 2 : 1);
     const int64_t tiles = ((int64_t)c.max_kv + kKeyTile - 1) / kKeyTile;
@@ -699,22 +731,20 @@ static rmsnorm_status_t attn_sizes(const paged_attn_call_t &c) {
 }
 
 template <typename T, int DP, int NQ>
-static int launch_attn(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, unsigned grid,
-                       cudaStream_t stream) {
+static int launch_attn(const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t stream) {
     using S = AttnShape<DP, NQ>;
     auto *kernel = paged_attn<T, DP, NQ>;
     const int e = allow_staged_smem(reinterpret_cast<const void *>(kernel));
     if (e != 0) return e;
     LaunchCfg lc(grid, S::kThreads, S::kSmem, stream);
-    return (int)cudaLaunchKernelEx(&lc.cfg, kernel, p, km, vm);
+    return (int)cudaLaunchKernelEx(&lc.cfg, kernel, p, maps[0], maps[1], maps[2]);
 }
 
 template <typename T>
-static int launch_attn_t(int nq, const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, unsigned grid,
-                         cudaStream_t s) {
+static int launch_attn_t(int nq, const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t s) {
     if (p.head_dim > 64)
-        return nq == 2 ? launch_attn<T, 128, 2>(p, km, vm, grid, s) : launch_attn<T, 128, 1>(p, km, vm, grid, s);
-    return nq == 2 ? launch_attn<T, 64, 2>(p, km, vm, grid, s) : launch_attn<T, 64, 1>(p, km, vm, grid, s);
+        return nq == 2 ? launch_attn<T, 128, 2>(p, maps, grid, s) : launch_attn<T, 128, 1>(p, maps, grid, s);
+    return nq == 2 ? launch_attn<T, 64, 2>(p, maps, grid, s) : launch_attn<T, 64, 1>(p, maps, grid, s);
 }
 
 static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t stream) {
@@ -733,10 +763,8 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     const bool empty = pc.pages == 0 || c.table_width == 0 || c.max_kv == 0;
     if (!empty && (!pc.k || !pc.v || !c.block_table)) return RMSNORM_ERR_INVALID_ARG;
 
-    // what a tiled copy takes: 16-byte boundaries everywhere
     auto legal = [&](const void *base, int64_t page, int64_t slot, int64_t head) {
-        auto ok = [](int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 38); };
-        return on(base, 16) && ok(page, pc.pages) && ok(slot, pc.page_size) && ok(head, pc.heads);
+        return on(base, 16) && tile_stride(page, pc.pages) && tile_stride(slot, pc.page_size) && tile_stride(head, pc.heads);
     };
     if (!empty && (!legal(pc.k, pc.k_page, pc.k_slot, pc.k_head) || !legal(pc.v, pc.v_page, pc.v_slot, pc.v_head)))
         return RMSNORM_ERR_UNSUPPORTED;
@@ -750,13 +778,13 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
 
     AttnParams p;
     std::memset(&p, 0, sizeof p);
-    CUtensorMap km, vm;
-    std::memset(&km, 0, sizeof km);
-    std::memset(&vm, 0, sizeof vm);
+    CUtensorMap maps[3];  // q, k, v
+    std::memset(maps, 0, sizeof maps);
     p.box_rows = gcd_of(pc.page_size, kKeyTile);
     if (!empty) {
-        if (!cache_map(&km, c.dtype, pc.k, c.head_dim, pc, pc.k_page, pc.k_slot, pc.k_head, p.box_rows) ||
-            !cache_map(&vm, c.dtype, pc.v, c.head_dim, pc, pc.v_page, pc.v_slot, pc.v_head, p.box_rows))
+        const int b = p.box_rows;
+        if (!tile_map(&maps[1], c.dtype, pc.k, c.head_dim, {pc.page_size, pc.heads, pc.pages}, {pc.k_slot, pc.k_head, pc.k_page}, b, 1) ||
+            !tile_map(&maps[2], c.dtype, pc.v, c.head_dim, {pc.page_size, pc.heads, pc.pages}, {pc.v_slot, pc.v_head, pc.v_page}, b, 1))
             return RMSNORM_ERR_UNSUPPORTED;
     }
 
@@ -802,6 +830,11 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     p.q_tiles = cut.q_tiles;
     p.splits = cut.splits;
     p.chunk = cut.chunk;
+    p.tile_toks = cut.tile_toks;
+    // (a group's heads share a box: their stride counts even for one key head)
+    if (!empty && on(c.q, 16) && tile_stride(c.q_head, c.q_heads) && tile_stride(c.q_token, c.tokens))
+        p.q_tma = tile_map(&maps[0], c.dtype, c.q, c.head_dim, {p.group, pc.heads, c.tokens},
+                           {c.q_head, c.q_head * p.group, c.q_token}, p.group, p.tile_toks);
     p.q_vec = on(c.q, 16) && p.q_token % 16 == 0 && p.q_head % 16 == 0;
     p.out_vec = on(c.out, 16) && p.out_token % 16 == 0 && p.out_head % 16 == 0;
 
@@ -811,8 +844,8 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     if (grid > 0x7fffffffLL || join > 0x7fffffffLL) {
         st = RMSNORM_ERR_UNSUPPORTED;
     } else {
-        le = c.dtype == RMSNORM_BF16 ? launch_attn_t<__nv_bfloat16>(cut.nq, p, km, vm, (unsigned)grid, stream)
-                                     : launch_attn_t<__half>(cut.nq, p, km, vm, (unsigned)grid, stream);
+        le = c.dtype == RMSNORM_BF16 ? launch_attn_t<__nv_bfloat16>(cut.nq, p, maps, (unsigned)grid, stream)
+                                     : launch_attn_t<__half>(cut.nq, p, maps, (unsigned)grid, stream);
         if (le == 0 && cut.splits > 1) {
             LaunchCfg lc((unsigned)join, 128, 0, stream);
             le = c.dtype == RMSNORM_BF16 ? (int)cudaLaunchKernelEx(&lc.cfg, paged_attn_join<__nv_bfloat16>, p)
