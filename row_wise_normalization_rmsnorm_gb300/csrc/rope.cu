@@ -12,9 +12,9 @@
 // few fp32 operations a value; the angles are shared by all heads of a
 // token. So a warp takes one token: a lane keeps the cos and sin of one
 // 16-byte chunk's frequencies in registers and walks the heads, a group of
-// lanes a head, with several heads' loads in flight. No shared memory and no
-// barrier; what a warp repeats (the angles, once a group of lanes) hides
-// behind the copies. With few tokens the heads are split over more warps.
+// lanes a head, with several heads' loads in flight. The warp computes each
+// angle once (two a lane for 64 frequencies) and hands them round in shared
+// memory. With few tokens the heads are split over more warps.
 #include <cmath>
 #include <cstring>
 
@@ -147,22 +147,21 @@ __device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w,
 // two neighbouring chunks of E pairs (adjacent pairing), or two chunks of
 // the values that pass unturned.
 constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeUnroll = 4;  // heads a lane has in flight
 
-template <typename T, bool APPEND>
+template <typename T, bool APPEND, bool NORM, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads) rope_vector(const __grid_constant__ RopeParams p) {
     constexpr int E = Elem<T>::E, NP = Elem<T>::NP, U = kRopeUnroll;
     using PR = Pair<true>;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    __shared__ float2 turn[kRopeWarps][HEAD_MAX_DIM / 2];  // (cos, sin) of the warp's token
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp;
     pdl_wait();
     pdl_trigger();
     if (unit >= p.tokens * p.blocks) return;
     const int64_t t = unit / p.blocks;
-    const int h0 = (int)(unit - t * p.blocks) * p.block_heads;
-    const int hq = p.seg[0].heads, hqk = hq + p.seg[1].heads;
-    const int htot = hqk + (APPEND ? p.seg[2].heads : 0);
-    const int h1 = min(h0 + p.block_heads, htot);
+    const int h0 = (int)(unit - t * p.blocks) * p.block_heads, h1 = h0 + p.block_heads;
     const int item = lane & ((1 << p.lanes_log2) - 1), grp = lane >> p.lanes_log2;
     const int step = 32 >> p.lanes_log2;
     const int rot_items = p.half_dim / E;
@@ -170,109 +169,160 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vector(const __grid_constan
 
     int e0, e1;
     if (turns) {
-        e0 = p.adjacent ? item * 2 * E : item * E;
-        e1 = p.adjacent ? e0 + E : e0 + p.half_dim;
+        e0 = ADJ ? item * 2 * E : item * E;
+        e1 = ADJ ? e0 + E : e0 + p.half_dim;
     } else {
         e0 = 2 * p.half_dim + (item - rot_items) * 2 * E;
         e1 = e0 + E;
     }
     const bool has0 = e0 < p.head_dim, has1 = e1 < p.head_dim;
-
-    uint4 x0[U], x1[U];
-    auto load = [&](int hb) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = hb + u * step + grp;
-            x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
-            if (h < h1) {
-                const int sg = h < hq ? 0 : (h < hqk ? 1 : 2);
-                const HeadSeg &g = p.seg[sg];
-                const char *row = g.in + t * g.in_token + (h - (sg == 0 ? 0 : sg == 1 ? hq : hqk)) * g.in_head;
-                if (has0) x0[u] = ld_stream(reinterpret_cast<const uint4 *>(row + e0 * (int)sizeof(T)));
-                if (has1) x1[u] = ld_stream(reinterpret_cast<const uint4 *>(row + e1 * (int)sizeof(T)));
-            }
-        }
-    };
-    load(h0);
+    const int b0 = e0 * (int)sizeof(T), b1 = e1 * (int)sizeof(T);
 
     int64_t page = 0;
     int place = 0;
     if (APPEND) find_slot(p, t, page, place);
-    float c[E], s[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-    }
-    if (turns && h0 < hqk) angles_of<E>(p, t, item * E, c, s);
 
-    for (int hb = h0;;) {
+    // The segments' heads in this block, one segment after the other.
+    int first = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = hb + u * step + grp;
-            const int sg = h < hq ? 0 : (h < hqk ? 1 : 2);
-            const bool live = h < h1;
-            float2 a[NP], b[NP];
-            unpack<T>(x0[u], a);
-            unpack<T>(x1[u], b);
-            if (APPEND) {
-                const void *w = sg < 2 ? p.w[sg] : nullptr;
-                // (p.w is the same for the whole grid, so the shuffles are uniform)
-                if (p.w[0] || p.w[1]) {
+    for (int sg = 0; sg < (APPEND ? 3 : 2); ++sg) {
+        const HeadSeg &g = p.seg[sg];
+        const int hb = max(h0 - first, 0), he = min(h1 - first, g.heads);
+        first += g.heads;
+        const bool cached = APPEND && sg > 0;
+        const char *in = g.in + t * g.in_token;
+        char *out = cached ? g.out + page * g.out_token + place * g.out_slot : g.out + t * g.out_token;
+        const bool kept = !cached || page >= 0;
+        uint4 x0[U], x1[U];
+        auto load = [&](int h) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int hh = h + u * step;
+                x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
+                if (hh < he) {
+                    const char *row = in + hh * g.in_head;
+                    if (has0) x0[u] = ld_stream(reinterpret_cast<const uint4 *>(row + b0));
+                    if (has1) x1[u] = ld_stream(reinterpret_cast<const uint4 *>(row + b1));
+                }
+            }
+        };
+        if (sg == 0) load(hb + grp);  // in flight while the angles are computed
+        if (sg == 0 && h0 < p.seg[0].heads + p.seg[1].heads) {
+            for (int i = lane; i < p.half_dim; i += 32) {
+                float c, s;
+                angles_of<1>(p, t, i, &c, &s);
+                turn[warp][i] = make_float2(c, s);
+            }
+            __syncwarp();
+        }
+        if (hb >= he) continue;
+        if (sg > 0) load(hb + grp);
+
+        if (APPEND && sg == 2) {  // v: copied
+            for (int h = hb + grp;;) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int hh = h + u * step;
+                    if (hh < he && kept) {
+                        char *row = out + hh * g.out_head;
+                        if (has0) *reinterpret_cast<uint4 *>(row + b0) = x0[u];
+                        if (has1) *reinterpret_cast<uint4 *>(row + b1) = x1[u];
+                    }
+                }
+                h += U * step;
+                if (h - grp >= he) break;
+                load(h);
+            }
+            continue;
+        }
+
+        // The turn's factors of this lane's pairs, the norm's weight folded
+        // into them: y1 = x1 ca - x2 sb, y2 = x2 cb + x1 sa (times rstd).
+        const void *w = NORM ? p.w[sg & 1] : nullptr;
+        float2 ca[NP], sb[NP], cb[NP], sa[NP];
+        {
+            float2 fa[NP], fb[NP];
+#pragma unroll
+            for (int q = 0; q < NP; ++q) fa[q] = fb[q] = make_float2(1.f, 1.f);
+            if (NORM && w) {
+                if (has0) norm_factors<T>(p, w, e0, fa);
+                if (has1) norm_factors<T>(p, w, e1, fb);
+            }
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                ca[q] = fa[q];
+                cb[q] = fb[q];
+                sa[q] = sb[q] = make_float2(0.f, 0.f);
+            }
+            if (turns) {
+                const float4 *cs = reinterpret_cast<const float4 *>(&turn[warp][item * E]);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    const float4 v = cs[q];  // frequencies 2q and 2q + 1 of the lane's E
+                    const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w);
+                    if (!ADJ) {
+                        ca[q] = PR::mul(fa[q], c);
+                        sb[q] = PR::mul(fb[q], make_float2(-s.x, -s.y));
+                        cb[q] = PR::mul(fb[q], c);
+                        sa[q] = PR::mul(fa[q], s);
+                    } else {
+                        // pairs (2i, 2i + 1): frequency i's two values are one pair
+                        // of registers; .x keeps the first's factors, .y the second's
+                        float2 *cc = q < NP / 2 ? ca : cb, *ss = q < NP / 2 ? sa : sb;
+                        const float2 *ff = q < NP / 2 ? fa : fb;
+                        const int k = 2 * (q % (NP / 2 > 0 ? NP / 2 : 1));
+                        cc[k] = PR::mul(ff[k], make_float2(c.x, c.x));
+                        ss[k] = PR::mul(make_float2(ff[k].y, ff[k].x), make_float2(-s.x, s.x));
+                        cc[k + 1] = PR::mul(ff[k + 1], make_float2(c.y, c.y));
+                        ss[k + 1] = PR::mul(make_float2(ff[k + 1].y, ff[k + 1].x), make_float2(-s.y, s.y));
+                    }
+                }
+            }
+        }
+        const bool raw = !turns && !(NORM && w);
+        for (int h = hb + grp;;) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int hh = h + u * step;
+                float2 a[NP], b[NP];
+                unpack<T>(x0[u], a);
+                unpack<T>(x1[u], b);
+                float2 r2 = make_float2(1.f, 1.f);
+                if (NORM && w) {  // (the same for the whole grid: the shuffles are uniform)
                     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int q = 0; q < NP; ++q) acc = PR::fma(a[q], a[q], PR::fma(b[q], b[q], acc));
                     float ss = acc.x + acc.y;
                     for (int o = (1 << p.lanes_log2) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    if (w) {
-                        const float r = rsqrtf(__fmaf_rn(ss, p.inv_n, p.eps));
-                        const float2 r2 = make_float2(r, r);
-                        float2 f[NP];
-                        if (has0) {
-                            norm_factors<T>(p, w, e0, f);
-#pragma unroll
-                            for (int q = 0; q < NP; ++q) a[q] = PR::mul(PR::mul(a[q], r2), f[q]);
-                        }
-                        if (has1) {
-                            norm_factors<T>(p, w, e1, f);
-#pragma unroll
-                            for (int q = 0; q < NP; ++q) b[q] = PR::mul(PR::mul(b[q], r2), f[q]);
-                        }
-                    }
+                    const float r = rsqrtf(__fmaf_rn(ss, p.inv_n, p.eps));
+                    r2 = make_float2(r, r);
                 }
-            }
-            if (!live) continue;
-            if (turns && sg < 2) {
-                if (!p.adjacent) {
+                if (hh >= he || !kept) continue;
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        const float2 cc = make_float2(c[2 * q], c[2 * q + 1]), sn = make_float2(s[2 * q], s[2 * q + 1]);
-                        const float2 ns = make_float2(-sn.x, -sn.y);
-                        const float2 y0 = PR::fma(b[q], ns, PR::mul(a[q], cc));
-                        b[q] = PR::fma(a[q], sn, PR::mul(b[q], cc));
-                        a[q] = y0;
+                for (int q = 0; q < NP; ++q) {
+                    float2 y0, y1;
+                    if (!turns) {
+                        y0 = PR::mul(a[q], ca[q]);
+                        y1 = PR::mul(b[q], cb[q]);
+                    } else if (!ADJ) {
+                        y0 = PR::fma(b[q], sb[q], PR::mul(a[q], ca[q]));
+                        y1 = PR::fma(a[q], sa[q], PR::mul(b[q], cb[q]));
+                    } else {
+                        y0 = PR::fma(make_float2(a[q].y, a[q].x), sa[q], PR::mul(a[q], ca[q]));
+                        y1 = PR::fma(make_float2(b[q].y, b[q].x), sb[q], PR::mul(b[q], cb[q]));
                     }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        const float ca = c[q], sa = s[q], cb = c[NP + q], sb = s[NP + q];
-                        a[q] = make_float2(__fmaf_rn(-a[q].y, sa, a[q].x * ca), __fmaf_rn(a[q].x, sa, a[q].y * ca));
-                        b[q] = make_float2(__fmaf_rn(-b[q].y, sb, b[q].x * cb), __fmaf_rn(b[q].x, sb, b[q].y * cb));
-                    }
+                    a[q] = NORM ? PR::mul(y0, r2) : y0;
+                    b[q] = NORM ? PR::mul(y1, r2) : y1;
                 }
+                char *row = out + hh * g.out_head;
+                // (values that pass as they are keep their bits, a NaN's payload too)
+                if (has0) *reinterpret_cast<uint4 *>(row + b0) = raw ? x0[u] : pack<T>(a);
+                if (has1) *reinterpret_cast<uint4 *>(row + b1) = raw ? x1[u] : pack<T>(b);
             }
-            const HeadSeg &g = p.seg[sg];
-            char *row = row_out<APPEND>(p, g, sg > 0, t, h - (sg == 0 ? 0 : sg == 1 ? hq : hqk), page, place);
-            if (row) {
-                // values that pass as they are keep their bits (a NaN's payload too)
-                const bool raw = sg == 2 || (!turns && !(APPEND && p.w[sg]));
-                if (has0) *reinterpret_cast<uint4 *>(row + e0 * (int)sizeof(T)) = raw ? x0[u] : pack<T>(a);
-                if (has1) *reinterpret_cast<uint4 *>(row + e1 * (int)sizeof(T)) = raw ? x1[u] : pack<T>(b);
-            }
+            h += U * step;
+            if (h - grp >= he) break;
+            load(h);
         }
-        hb += U * step;
-        if (hb >= h1) break;
-        load(hb);
     }
 }
 
@@ -365,8 +415,14 @@ static bool on16(int64_t a) { return a % 16 == 0; }
 template <typename T, bool APPEND>
 static int launch_rope(bool vec, const RopeParams &p, unsigned grid, cudaStream_t stream) {
     LaunchCfg lc(grid, kRopeThreads, 0, stream);
-    return vec ? (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, APPEND>, p)
-               : (int)cudaLaunchKernelEx(&lc.cfg, rope_elements<T, APPEND>, p);
+    if (!vec) return (int)cudaLaunchKernelEx(&lc.cfg, rope_elements<T, APPEND>, p);
+    if constexpr (APPEND) {
+        if (p.w[0] || p.w[1])
+            return p.adjacent ? (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, true, true, true>, p)
+                              : (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, true, true, false>, p);
+    }
+    return p.adjacent ? (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, APPEND, false, true>, p)
+                      : (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, APPEND, false, false>, p);
 }
 
 template <bool APPEND>
