@@ -148,10 +148,18 @@ __device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w,
 // the values that pass unturned.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeUnroll = 4;  // heads a lane has in flight
+// Heads a lane has in flight, and CTAs an SM that the registers are held to:
+// 3 and 5 measured best together (bf16 16384 tokens of 40 heads by 128:
+// 58.5 us against 59.3 with 4 and 4, 65.7 with 2 and 5, 60.0 with 2 and 7;
+// the append of 8192 tokens of 48 heads with its norm 39.9 us against 42.1,
+// 42.7 and 42.5).
+constexpr int kRopeUnroll = 3;
+constexpr int kRopeCtas = 5;
 
-template <typename T, bool APPEND, bool NORM, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_vector(const __grid_constant__ RopeParams p) {
+// FULL: every lane has two chunks of every head (head_dim = 2 E lanes a head,
+// e.g. 64, 128 or 256 values of 16 bits), so nothing is tested a chunk.
+template <typename T, bool APPEND, bool NORM, bool ADJ, bool FULL>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_vector(const __grid_constant__ RopeParams p) {
     constexpr int E = Elem<T>::E, NP = Elem<T>::NP, U = kRopeUnroll;
     using PR = Pair<true>;
     __shared__ float2 turn[kRopeWarps][HEAD_MAX_DIM / 2];  // (cos, sin) of the warp's token
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vector(const __grid_constan
         e0 = 2 * p.half_dim + (item - rot_items) * 2 * E;
         e1 = e0 + E;
     }
-    const bool has0 = e0 < p.head_dim, has1 = e1 < p.head_dim;
+    const bool has0 = FULL || e0 < p.head_dim, has1 = FULL || e1 < p.head_dim;
     const int b0 = e0 * (int)sizeof(T), b1 = e1 * (int)sizeof(T);
 
     int64_t page = 0;
@@ -198,7 +206,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vector(const __grid_constan
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int hh = h + u * step;
-                x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
+                if (!FULL) x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
                 if (hh < he) {
                     const char *row = in + hh * g.in_head;
                     if (has0) x0[u] = ld_stream(reinterpret_cast<const uint4 *>(row + b0));
@@ -412,17 +420,24 @@ static int elem_bytes(int dt) { return (dt & 0xff) == RMSNORM_F32 ? 4 : 2; }
 
 static bool on16(int64_t a) { return a % 16 == 0; }
 
+template <typename T, bool APPEND, bool NORM>
+static int launch_vector(const RopeParams &p, const cudaLaunchConfig_t *cfg) {
+    const bool full = p.head_dim * (int)sizeof(T) == 32 << p.lanes_log2;
+    if (p.adjacent)
+        return full ? (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, true, true>, p)
+                    : (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, true, false>, p);
+    return full ? (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, false, true>, p)
+                : (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, false, false>, p);
+}
+
 template <typename T, bool APPEND>
 static int launch_rope(bool vec, const RopeParams &p, unsigned grid, cudaStream_t stream) {
     LaunchCfg lc(grid, kRopeThreads, 0, stream);
     if (!vec) return (int)cudaLaunchKernelEx(&lc.cfg, rope_elements<T, APPEND>, p);
     if constexpr (APPEND) {
-        if (p.w[0] || p.w[1])
-            return p.adjacent ? (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, true, true, true>, p)
-                              : (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, true, true, false>, p);
+        if (p.w[0] || p.w[1]) return launch_vector<T, true, true>(p, &lc.cfg);
     }
-    return p.adjacent ? (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, APPEND, false, true>, p)
-                      : (int)cudaLaunchKernelEx(&lc.cfg, rope_vector<T, APPEND, false, false>, p);
+    return launch_vector<T, APPEND, false>(p, &lc.cfg);
 }
 
 template <bool APPEND>
