@@ -43,6 +43,7 @@ namespace rmsn {
 constexpr int kKeyTile = 128;
 constexpr uint32_t kAttnWait = 1u << 22;         // polls of one barrier ...
 constexpr uint64_t kAttnWaitNs = 2000000000ull;  // ... and time, before a kernel gives up
+constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
 constexpr float kRescale = 8.f;           // log2 of how far a row's reference maximum may lag
 
 struct AttnParams {
@@ -71,7 +72,7 @@ struct AttnShape {
     static constexpr int kStage = kKeyTile * DP * 2;
     static constexpr int kStages = NQ == 2 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 3 : 6);
     static constexpr int kBars = NQ * kQBytes + kStages * kStage;
-    static constexpr int kSmem = kBars + 256;
+    static constexpr int kSmem = kBars + 512;  // barriers, the work items
     // NQ == 2: the copy and issue warps fill up a warpgroup of their own, so
     // that registers can move to the softmax warps: 168 a thread at launch,
     // then 2 x 128 x 208 + 128 x 88 = 384 x 168
@@ -125,6 +126,101 @@ struct Waiter {
     }
 };
 
+// One piece of work: a row tile pair (or tile) of a sequence and key head, and
+// its keys. Made by the copying warp, read by the others from shared memory.
+struct Item {
+    int q0, nq, kv;      // the sequence: first row, new tokens, cached tokens
+    int tok0, toks;      // its tokens taken here
+    int kbeg, kend;      // keys taken here
+    int kvh, split, b;
+    int ntiles;          // key tiles; -1: no more work
+    int fix;             // the last tile's values past the sequence's end to become zeros
+};
+
+// Work item `id`: (sequence, key head) fastest, then the split, then the row
+// tile, the last rows (most keys) first. False: it has nothing to do.
+template <int NQ>
+__device__ __forceinline__ bool decode_item(const AttnParams &p, int id, Item &w) {
+    w.kvh = id % p.kv_heads;
+    id /= p.kv_heads;
+    const int b = id % p.batch;
+    id /= p.batch;
+    w.b = b;
+    w.split = id % p.splits;
+    const int qt = p.q_tiles - 1 - id / p.splits;
+    const int T_ = (int)p.tokens;
+    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_lens + b);
+    w.q0 = min(max(c0, 0), T_);
+    w.nq = min(max(c1, w.q0), T_) - w.q0;
+    w.kv = max(0, min(min(len, p.max_kv), (int)min((int64_t)p.width * p.page_size, (int64_t)0x7fffffff)));
+    w.tok0 = qt * NQ * p.tile_toks;
+    w.toks = min(min(w.nq, p.max_q) - w.tok0, NQ * p.tile_toks);
+    if (w.toks <= 0) return false;
+    // keys that the last row sees, and this split's part of them
+    const int64_t lim = p.causal ? min((int64_t)w.kv, max((int64_t)0, (int64_t)w.kv - w.nq + w.tok0 + w.toks)) : w.kv;
+    const int64_t kbeg = (int64_t)w.split * p.chunk;
+    const int64_t kend = p.splits > 1 ? min(lim, kbeg + p.chunk) : lim;
+    if (p.splits > 1 && kend <= kbeg) return false;
+    w.kbeg = (int)kbeg;
+    w.kend = (int)kend;
+    w.ntiles = (w.kend - w.kbeg + kKeyTile - 1) / kKeyTile;
+    const int last_valid = w.kv - (w.kbeg + (w.ntiles - 1) * kKeyTile);
+    w.fix = w.ntiles > 0 && last_valid < kKeyTile && last_valid % p.box_rows != 0;
+    return true;
+}
+
+// A 4 by 4 transposition within groups of four lanes: lane i's c[k] becomes
+// lane k's c[i].
+__device__ __forceinline__ void swap_lanes(uint32_t &a, uint32_t &b, bool upper, int o) {
+    const uint32_t give = upper ? a : b;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, o);
+    a = upper ? got : a;
+    b = upper ? b : got;
+}
+__device__ __forceinline__ void transpose4(uint4 (&c)[4], int lane) {
+    const bool u1 = lane & 1, u2 = lane & 2;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+        swap_lanes(c[k].x, c[k + 1].x, u1, 1);
+        swap_lanes(c[k].y, c[k + 1].y, u1, 1);
+        swap_lanes(c[k].z, c[k + 1].z, u1, 1);
+        swap_lanes(c[k].w, c[k + 1].w, u1, 1);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        swap_lanes(c[k].x, c[k + 2].x, u2, 2);
+        swap_lanes(c[k].y, c[k + 2].y, u2, 2);
+        swap_lanes(c[k].z, c[k + 2].z, u2, 2);
+        swap_lanes(c[k].w, c[k + 2].w, u2, 2);
+    }
+}
+
+// 32 columns of a tile's scores; columns from n on are masked.
+__device__ __forceinline__ void load_scores(uint32_t from, int n, bool masks, uint32_t (&s)[32]) {
+    __syncwarp();
+    tmem_ld32(from, s);
+    tmem_wait_ld();
+    if (masks) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i >= n) s[i] = 0xff800000u;  // -infinity
+    }
+}
+
+// 16 bytes to rows off 16-byte boundaries (out of line: rarely taken).
+__device__ __noinline__ void store_halves(uint16_t *to, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        to[2 * i] = (uint16_t)w[i];
+        to[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    }
+}
+
+// Persistent: a CTA takes its own block's item, then those of blocks that have
+// not started (the hardware's order, so the load balances itself), and the
+// roles run from one item into the next: while the softmax warps write an
+// item's rows, the next one's keys arrive and its first product is done.
 template <typename T, int DP, int NQ>
 __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
     paged_attn(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
@@ -135,49 +231,18 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
     constexpr int kProducer = NQ * 4, kIssuer = NQ * 4 + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    pdl_wait();
-    pdl_trigger();
-
-    // ---- which rows and keys: (b, key head) fastest, then the split, then
-    // the row tile, last rows (most keys) first
-    int id = blockIdx.x;
-    const int kvh = id % p.kv_heads;
-    id /= p.kv_heads;
-    const int b = id % p.batch;
-    id /= p.batch;
-    const int split = id % p.splits;
-    const int qt = p.q_tiles - 1 - id / p.splits;
-    const int T_ = (int)p.tokens;
-    const int q0 = min(max(__ldg(p.cu_q + b), 0), T_);
-    const int nq = min(max(__ldg(p.cu_q + b + 1), q0), T_) - q0;  // the sequence's new tokens
-    const int nq_out = min(nq, p.max_q);                           // those that are written
-    const int kv = max(0, min(min(__ldg(p.kv_lens + b), p.max_kv), (int)min((int64_t)p.width * p.page_size, (int64_t)0x7fffffff)));
-    const int tt = p.tile_toks, tok0 = qt * NQ * tt;
-    const int toks = min(nq_out - tok0, NQ * tt);  // the CTA's tokens, tt a tile
-    if (toks <= 0) return;
-    // keys that the CTA's last row sees, and this split's part of them
-    const int last_tok = tok0 + toks - 1;
-    const int64_t lim = p.causal ? min((int64_t)kv, max((int64_t)0, (int64_t)kv - nq + last_tok + 1)) : kv;
-    const int64_t kbeg64 = (int64_t)split * p.chunk;
-    const int64_t kend64 = p.splits > 1 ? min(lim, kbeg64 + p.chunk) : lim;
-    if (p.splits > 1 && kend64 <= kbeg64) return;
-    const int kbeg = (int)kbeg64, kend = (int)kend64;
-    const int ntiles = (kend - kbeg + kKeyTile - 1) / kKeyTile;
-    const int act = toks > tt ? 2 : 1;  // tiles with rows
-    const int last_valid = kv - (kbeg + (ntiles - 1) * kKeyTile);  // cached keys of the last tile
-    const bool fix = ntiles > 0 && last_valid < kKeyTile && last_valid % p.box_rows != 0;
-
-    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle goes by the address
-        if (threadIdx.x == 0) *p.status = 1;
-        return;
-    }
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
     uint64_t *full = bars, *empty = bars + NST;
     uint64_t *s_ready = empty + NST, *p_half = s_ready + NQ, *p_ready = p_half + NQ, *o_done = p_ready + NQ;
-    uint64_t *q_ready = o_done + NQ, *v_fixed = q_ready + 1, *drained = v_fixed + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+    uint64_t *q_ready = o_done + NQ, *q_free = q_ready + 1, *v_fixed = q_free + 1, *drained = v_fixed + 1;
+    uint64_t *item_full = drained + 1, *item_empty = item_full + 2, *answered = item_empty + 2;
+    static_assert(2 * S::kStages + 4 * NQ + 9 <= 36, "barriers");
+    uint8_t *after = smem + S::kBars + 36 * 8;
+    void *answer = after;  // 16 bytes, 16-byte aligned
+    Item *items = reinterpret_cast<Item *>(after + 16);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(items + 2);
     volatile int *gave_up = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * S::kStages + 4 * NQ + 3) * 8 + 8 <= 256, "barriers");
+    static_assert(36 * 8 + 16 + 2 * sizeof(Item) + 8 <= S::kSmem - S::kBars, "shared memory");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -185,19 +250,38 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             mbar_init(empty + i, 1);
         }
         for (int t = 0; t < NQ; ++t) {
-            const int live = min(max(toks - t * tt, 0), tt) * p.group;  // rows of the tile
             mbar_init(s_ready + t, 1);
-            mbar_init(p_half + t, live > 0 ? (live + 31) / 32 : 1);  // its warps with rows
-            mbar_init(p_ready + t, live > 0 ? (live + 31) / 32 : 1);
+            mbar_init(p_half + t, 4);  // the tile's warps
+            mbar_init(p_ready + t, 4);
             mbar_init(o_done + t, 1);
         }
         mbar_init(q_ready, p.q_tma ? 1 : NQ * 4);
+        mbar_init(q_free, 1);
         mbar_init(v_fixed, 1);
         mbar_init(drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(item_full + i, 1);
+            mbar_init(item_empty + i, NQ * 4 + 1);
+        }
+        mbar_init(answered, 1);
         *gave_up = 0;
         mbar_init_fence();
     }
+    if (warp == kProducer && lane == 0) {
+        prefetch_map(&qmap);
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
+    pdl_wait();
+    pdl_trigger();
+    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle goes by the address
+        if (threadIdx.x == 0) *p.status = 1;
+        return;
+    }
     if (warp == kIssuer) tmem_alloc(tmem_slot, S::kCols);
+    Item w0;
+    bool has_w0 = false;
+    if (warp == kProducer) has_w0 = decode_item<NQ>(p, blockIdx.x, w0);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -208,79 +292,177 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
     volatile int still = 0;  // the last waits, after giving up, have a limit of their own
     const uint32_t sbase = smem_u32(smem);
     const uint32_t stage0 = sbase + NQ * S::kQBytes;
+    const int tt = p.tile_toks;
+
+    // The n-th item of this CTA, as the producer left it; false: given up.
+    auto take = [&](int n, Item &w) {
+        if (!warp_wait(item_full + (n & 1), (uint32_t)((n >> 1) & 1))) return false;
+        w = items[n & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + (n & 1));
+        return true;
+    };
 
     if (warp >= kProducer) {
     if constexpr (NQ == 2) fewer_registers<88>();
     if (warp == kProducer) {
-        // ---------------------------------------------------- K and V copies
+        // ------------------------------------------ the work, and its copies
         // A tile is 128 / box_rows boxes by 64 columns; lane l copies piece
         // l % boxes of half l / boxes.
         const int boxes = kKeyTile / p.box_rows;
         const int piece = lane % boxes, half = lane / boxes;
         const bool copies = half < S::kHalves;
         const uint32_t off = (uint32_t)(half * kKeyTile * 128 + piece * p.box_rows * 128);
-        auto find = [&](int tile, int &page, int &place) {
-            const int key = kbeg + tile * kKeyTile + piece * p.box_rows;
-            page = p.pages;  // outside the cache: zeros
-            place = 0;
-            if (copies && tile < ntiles && key < kv) {
+        Item w = w0, next;
+        // (the table's entry is checked where it is used, a tile later: until
+        // then its load is under way)
+        int page, place, next_page, next_place;
+        auto find = [&](const Item &i, int tile, int &pg, int &pl) {
+            const int key = i.kbeg + tile * kKeyTile + piece * p.box_rows;
+            pg = -1;
+            pl = 0;
+            if (copies && tile < i.ntiles && key < i.kv) {
                 const int col = key / p.page_size;
-                const int id = __ldg(p.table + b * p.table_stride + col);
-                if (id >= 0 && id < p.pages) page = id;
-                place = key - col * p.page_size;
+                pg = __ldg(p.table + i.b * p.table_stride + col);
+                pl = key - col * p.page_size;
             }
         };
-        int page, place, next_page, next_place;
-        find(0, page, place);
-        if (p.q_tma && lane == 0) {
-            // q's rows: tt tokens of `group` heads are one box, row after row
-            mbar_arrive_expect_tx(q_ready, (uint32_t)(act * S::kHalves * tt * p.group * 128));
-            for (int t = 0; t < act; ++t)
-                for (int h = 0; h < S::kHalves; ++h)
-                    tile_g2s(sbase + t * S::kQBytes + h * (S::kQRows * 128), &qmap, h * 64, 0, kvh, q0 + tok0 + t * tt, q_ready);
-        }
-        __syncwarp();
-        int issued = 0;
+        int asked = 0;
         bool ok = true;
-        for (int j = 0; j < ntiles && ok; ++j) {
-            find(j + 1, next_page, next_place);
-#pragma unroll
-            for (int kvsel = 0; kvsel < 2; ++kvsel) {
-                const int st = issued % NST;
-                if (issued >= NST && !warp_wait(empty + st, (uint32_t)((issued / NST - 1) & 1))) {
+        auto ask = [&]() {
+            if (lane == 0) {
+                // (the answer before, read by this warp, precedes the next in its place)
+                fence_async_smem();
+                mbar_arrive_expect_tx(answered, 16);
+                next_block_ask(answer, answered);
+            }
+            __syncwarp();
+            ++asked;
+        };
+        // The next item with work (asked for), its first tile looked up; ntiles
+        // -1: none.
+        auto find_next = [&](Item &i, int &pg, int &pl) {
+            for (;; ask()) {
+                if (!warp_wait(answered, (uint32_t)((asked - 1) & 1))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
+                const int id = next_block_answer(answer);
                 __syncwarp();
-                if (copies)
-                    tile_g2s(stage0 + st * S::kStage + off, kvsel ? &vmap : &kmap, half * 64, place, kvh, page, full + st);
-                ++issued;
+                if (id < 0) break;
+                if (decode_item<NQ>(p, id, i)) {
+                    find(i, 0, pg, pl);
+                    return;
+                }
             }
+            i.ntiles = -1;
+        };
+        int issued = 0;  // tiles, over all items
+        auto copy_tile = [&](const CUtensorMap *map, int kvh, int pg, int pl) {
+            const int st = issued % NST;
+            if (issued >= NST && !warp_wait(empty + st, (uint32_t)((issued / NST - 1) & 1))) {
+                ok = false;
+                return;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
+            __syncwarp();
+            // what is no page lies outside the cache: zeros
+            if ((uint32_t)pg >= (uint32_t)p.pages) {
+                pg = p.pages;
+                pl = 0;
+            }
+            if (copies) tile_g2s(stage0 + st * S::kStage + off, map, half * 64, pl, kvh, pg, full + st);
+            ++issued;
+        };
+        // Values past the sequence's end in its last page would meet a zero
+        // weight, and 0 * NaN is NaN: they become zeros once the tile is there.
+        int fix_tile = -1, fix_from = 0;
+        auto fix_values = [&]() {
+            const int st = fix_tile % NST;
+            if (!warp_wait(full + st, (uint32_t)((fix_tile / NST) & 1))) {
+                ok = false;
+                return;
+            }
+            const int end = (fix_from / p.box_rows + 1) * p.box_rows;  // later boxes are zeros
+            const int chunks = (end - fix_from) * 8;
+            for (int i = lane; i < chunks * S::kHalves; i += 32) {
+                const int h = i / chunks, c = i - h * chunks;
+                sts128(smem + NQ * S::kQBytes + st * S::kStage + h * kKeyTile * 128 + fix_from * 128 + c * 16,
+                       make_uint4(0, 0, 0, 0));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_fixed);
+            fix_tile = -1;
+        };
+
+        if (has_w0) {
+            find(w, 0, page, place);
+        } else {
+            ask();
+            find_next(w, page, place);
+        }
+        int n = 0, q_loads = 0;
+        for (; ok; ++n) {
+            if (n >= 2 && !warp_wait(item_empty + (n & 1), (uint32_t)(((n >> 1) - 1) & 1))) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                items[n & 1] = w;
+                mbar_arrive(item_full + (n & 1));
+            }
+            __syncwarp();
+            if (w.ntiles < 0) break;
+            // Asked for when the item's last tiles are being copied: late, so that
+            // the blocks left go to whoever is done first, and early enough for
+            // the answer (a microsecond) to be there in time.
+            const int ask_at = max(w.ntiles - kAskAhead, 0);
+            if (w.ntiles == 0) ask();
+            for (int j = 0; j < w.ntiles && ok; ++j) {
+                int pg, pl;
+                copy_tile(&kmap, w.kvh, page, place);
+                find(w, j + 1, pg, pl);
+                if (j == 0) {
+                    // (this tile's place in the ring did not wait for the values mended here)
+                    if (ok && fix_tile >= 0) fix_values();
+                    if (ok && p.q_tma) {
+                        // q's rows: tt tokens of `group` heads are one box, row after row
+                        if (q_loads > 0 && !warp_wait(q_free, (uint32_t)((q_loads - 1) & 1))) ok = false;
+                        if (ok && lane == 0) {
+                            const int act = w.toks > tt ? 2 : 1;
+                            mbar_arrive_expect_tx(q_ready, (uint32_t)(act * S::kHalves * tt * p.group * 128));
+                            for (int t = 0; t < act; ++t)
+                                for (int h = 0; h < S::kHalves; ++h)
+                                    tile_g2s(sbase + t * S::kQBytes + h * (S::kQRows * 128), &qmap, h * 64, 0, w.kvh,
+                                             w.q0 + w.tok0 + t * tt, q_ready);
+                        }
+                        __syncwarp();
+                        if (ok) ++q_loads;
+                    }
+                }
+                if (ok) copy_tile(&vmap, w.kvh, page, place);
+                page = pg;
+                place = pl;
+                if (ok && j == ask_at) ask();
+            }
+            if (!ok) break;
+            if (w.fix) {
+                fix_tile = issued - 1;
+                fix_from = w.kv - (w.kbeg + (w.ntiles - 1) * kKeyTile);
+            }
+            find_next(next, next_page, next_place);
+            // (nothing follows to put the mending off to)
+            if (ok && next.ntiles <= 0 && fix_tile >= 0) fix_values();
+            w = next;
             page = next_page;
             place = next_place;
         }
-        if (fix && ok) {
-            // Values past the sequence's end in its last page would meet a
-            // zero weight, and 0 * NaN is NaN: they become zeros.
-            const int st = (issued - 1) % NST;
-            if (warp_wait(full + st, (uint32_t)(((issued - 1) / NST) & 1))) {
-                const int end = (last_valid / p.box_rows + 1) * p.box_rows;  // later boxes are zeros
-                const int chunks = (end - last_valid) * 8;
-                for (int i = lane; i < chunks * S::kHalves; i += 32) {
-                    const int h = i / chunks, c = i - h * chunks;
-                    sts128(smem + NQ * S::kQBytes + st * S::kStage + h * kKeyTile * 128 + last_valid * 128 + c * 16,
-                           make_uint4(0, 0, 0, 0));
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_fixed);
-            }
-        }
         if (*gave_up) {  // no copy may be in flight when the CTA ends
             const Waiter last{&still, p.status};
-            if (p.q_tma) last(q_ready, 0);
+            if (q_loads > 0) last(q_ready, (uint32_t)((q_loads - 1) & 1));
             for (int i = max(0, issued - NST); i < issued; ++i) last(full + i % NST, (uint32_t)((i / NST) & 1));
+            if (asked > 0) last(answered, (uint32_t)((asked - 1) & 1));
         }
     } else if (warp == kIssuer) {
         // ------------------------------------------- the matrix instructions
@@ -319,38 +501,55 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             }
             __syncwarp();
         };
-        auto free_stage = [&](int n) {
-            if (issues) mma_commit(empty + n % NST);
+        auto done_with = [&](uint64_t *bar) {
+            if (issues) mma_commit(bar);
             __syncwarp();
         };
-        // stage and phase of the ring's n-th tile (K_0, V_0, K_1, V_1, ...)
+        // stage and phase of the ring's n-th tile (K_0, V_0, K_1, V_1, ... over all items)
         auto arrived = [&](int n) { return warp_wait(full + n % NST, (uint32_t)((n / NST) & 1)); };
-        bool ok = warp_wait(q_ready, 0) && (ntiles == 0 || arrived(0));
-        if (ok && ntiles > 0) {
+        int base = 0, q_loads = 0, fixes = 0, steps[2] = {0, 0};
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            Item w;
+            if (!(ok = take(n, w)) || w.ntiles < 0) break;
+            if (w.ntiles == 0) continue;
+            const int act = w.toks > tt ? 2 : 1;
+            ok = arrived(base) && warp_wait(q_ready, (uint32_t)(q_loads & 1));
+            if (!ok) break;
+            ++q_loads;
             tc_after_sync();
-            for (int t = 0; t < act; ++t) qk(t, 0);
-            free_stage(0);
-            ok = arrived(1);
-        }
-        for (int j = 0; j < ntiles && ok; ++j) {
-            const bool more = j + 1 < ntiles;
-            if (!more && fix) ok = warp_wait(v_fixed, 0);
-            for (int t = 0; t < act && ok; ++t) {
-                if (!(ok = warp_wait(p_half + t, (uint32_t)(j & 1)))) break;
-                tc_after_sync();
-                pv(t, (2 * j + 1) % NST, 0, j > 0);
-                if (!(ok = warp_wait(p_ready + t, (uint32_t)(j & 1)))) break;
-                tc_after_sync();
-                pv(t, (2 * j + 1) % NST, 1, true);
-                if (t == act - 1) free_stage(2 * j + 1);
-                if (more) {
-                    if (t == 0) ok = arrived(2 * j + 2);
-                    if (ok) qk(t, (2 * j + 2) % NST);
-                    // (here, where the products just issued cover the wait)
-                    if (ok && t == 0) ok = arrived(2 * j + 3);
+            // (what the softmax still had to read of s, the products issued before have waited for)
+            for (int t = 0; t < act; ++t) qk(t, base % NST);
+            done_with(empty + base % NST);
+            if (w.ntiles == 1) done_with(q_free);
+            ok = arrived(base + 1);
+            for (int j = 0; j < w.ntiles && ok; ++j) {
+                const bool more = j + 1 < w.ntiles;
+                const int kn = base + 2 * j + 2, vn = base + 2 * j + 1;
+                if (!more && w.fix) ok = warp_wait(v_fixed, (uint32_t)(fixes++ & 1));
+                for (int t = 0; t < act && ok; ++t) {
+                    const uint32_t ph = (uint32_t)(steps[t] & 1);
+                    ++steps[t];
+                    if (!(ok = warp_wait(p_half + t, ph))) break;
+                    tc_after_sync();
+                    pv(t, vn % NST, 0, j > 0);
+                    if (!(ok = warp_wait(p_ready + t, ph))) break;
+                    tc_after_sync();
+                    pv(t, vn % NST, 1, true);
+                    if (t == act - 1) done_with(empty + vn % NST);
+                    if (more) {
+                        if (t == 0) ok = arrived(kn);
+                        if (ok) qk(t, kn % NST);
+                        // (here, where the products just issued cover the wait)
+                        if (ok && t == 0) ok = arrived(kn + 1);
+                    }
+                }
+                if (more && ok) {
+                    done_with(empty + kn % NST);
+                    if (j + 2 == w.ntiles) done_with(q_free);
                 }
             }
-            if (more && ok) free_stage(2 * j + 2);
+            base += 2 * w.ntiles;
         }
         if (*gave_up) {  // nor may a matrix instruction be
             __syncwarp();
@@ -362,95 +561,135 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         // --------------------------------------------------------- softmax
         if constexpr (NQ == 2) more_registers<208>();
         const int t = warp >> 2, r = threadIdx.x & 127;  // tile, row in it
-        if (!p.q_tma) {
-            // q that a tiled copy does not take (bases or strides off 16-byte
-            // boundaries): eight chunks in flight a thread, to the swizzled rows,
-            // zeros past the rows and head_dim
-            constexpr int kChunks = S::kHalves * 8, kBatch = 8;
-            const int rows = min(max(toks - t * tt, 0), tt) * p.group, hd_chunks = p.head_dim / 8;
-            for (int i0 = r; i0 < S::kQRows * kChunks; i0 += 128 * kBatch) {
-                uint4 v[kBatch];
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + t * kKeyTile, to = tmem + lanes + S::kO + t * DP;
+        const int row_tok = r / p.group, row_head = r % p.group;
+        const float c = p.c;
+        using PR = Pair<true>;
+        int steps = 0;  // key tiles, over all items
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            Item w;
+            if (!(ok = take(n, w)) || w.ntiles < 0) break;
+            const int rows = min(max(w.toks - t * tt, 0), tt) * p.group;
+            if (w.ntiles > 0 && !p.q_tma) {
+                // q that a tiled copy does not take (bases or strides off 16-byte
+                // boundaries): eight chunks in flight a thread, to the swizzled rows,
+                // zeros past the rows and head_dim. (The item before's last product
+                // with q was done before its last softmax.)
+                constexpr int kChunks = S::kHalves * 8, kBatch = 8;
+                const int hd_chunks = p.head_dim / 8;
+                for (int i0 = r; i0 < S::kQRows * kChunks; i0 += 128 * kBatch) {
+                    uint4 v[kBatch];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = i0 + u * 128, rr = i / kChunks, c = i % kChunks;
-                    v[u] = make_uint4(0, 0, 0, 0);
-                    if (rr < rows && c < hd_chunks) {
-                        const int tok = rr / p.group, g = rr - tok * p.group;
-                        const char *src = p.q + (int64_t)(q0 + tok0 + t * tt + tok) * p.q_token +
-                                          (int64_t)(kvh * p.group + g) * p.q_head + c * 16;
-                        if (p.q_vec) {
-                            v[u] = __ldg(reinterpret_cast<const uint4 *>(src));
-                        } else {
-                            const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
-                            v[u] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                              e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int i = i0 + u * 128, rr = i / kChunks, ch = i % kChunks;
+                        v[u] = make_uint4(0, 0, 0, 0);
+                        if (rr < rows && ch < hd_chunks) {
+                            const int tok = rr / p.group, g = rr - tok * p.group;
+                            const char *src = p.q + (int64_t)(w.q0 + w.tok0 + t * tt + tok) * p.q_token +
+                                              (int64_t)(w.kvh * p.group + g) * p.q_head + ch * 16;
+                            if (p.q_vec) {
+                                v[u] = __ldg(reinterpret_cast<const uint4 *>(src));
+                            } else {
+                                const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
+                                v[u] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                                  e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                            }
                         }
                     }
-                }
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = i0 + u * 128, rr = i / kChunks, c = i % kChunks;
-                    if (rr < S::kQRows)
-                        sts128(smem + t * S::kQBytes + (c >> 3) * (S::kQRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), v[u]);
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int i = i0 + u * 128, rr = i / kChunks, ch = i % kChunks;
+                        if (rr < S::kQRows)
+                            sts128(smem + t * S::kQBytes + (ch >> 3) * (S::kQRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                                   v[u]);
+                    }
                 }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
-        }
-
-        const int rows = min(max(toks - t * tt, 0), tt) * p.group;
-        if ((warp & 3) * 32 < rows) {  // the warp has rows
+            if (rows == 0) continue;  // (the tile's products are not issued either)
+            if ((warp & 3) * 32 >= rows) {
+                // a warp without rows only keeps the tile's count of arrivals
+                for (int j = 0; j < w.ntiles; ++j, ++steps) {
+                    if (!(ok = warp_wait(s_ready + t, (uint32_t)(steps & 1)))) break;
+                    if (lane == 0) {
+                        mbar_arrive(p_half + t);
+                        mbar_arrive(p_ready + t);
+                    }
+                }
+                continue;
+            }
             const bool live = r < rows;
-            const int tok = tok0 + t * tt + r / p.group, g = r % p.group;
-            // keys this row sees, counted from the split's first; a row past the
+            const int tok = w.tok0 + t * tt + row_tok;
+            // keys this row sees, counted from the item's first; a row past the
             // end masks nothing (its result goes nowhere)
-            const int64_t seen = p.causal ? max((int64_t)0, min((int64_t)kv, (int64_t)kv - nq + tok + 1)) : kv;
-            const int vis = live ? (int)(min(seen, (int64_t)kend) - kbeg) : 0x7fffffff;
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t ts = tmem + lanes + t * kKeyTile, to = tmem + lanes + S::kO + t * DP;
-            const float c = p.c;
+            const int64_t seen = p.causal ? max((int64_t)0, min((int64_t)w.kv, (int64_t)w.kv - w.nq + tok + 1)) : w.kv;
+            const int vis = live ? (int)(min(seen, (int64_t)w.kend) - w.kbeg) : 0x7fffffff;
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
-            using PR = Pair<true>;
-            bool ok = true;
-            for (int j = 0; j < ntiles; ++j) {
-                if (!(ok = warp_wait(s_ready + t, (uint32_t)(j & 1)))) break;
+            for (int j = 0; j < w.ntiles; ++j, ++steps) {
+                if (!(ok = warp_wait(s_ready + t, (uint32_t)(steps & 1)))) break;
                 tc_after_sync();
-                uint32_t s[4][32];
+                const int nk = vis - j * kKeyTile;  // keys of this tile the row sees
+                const bool masks = __any_sync(0xffffffffu, nk < kKeyTile);
+                // NQ == 2 holds the tile's scores in registers; NQ == 1, with fewer
+                // of them and time to spare, reads them twice, 32 columns at a time.
+                constexpr bool kHold = NQ == 2;
+                uint32_t s[kHold ? 4 : 1][32];
+                float mt;
+                if constexpr (kHold) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
-                tmem_wait_ld();
-                const int n = vis - j * kKeyTile;  // keys of this tile the row sees
-                if (__any_sync(0xffffffffu, n < kKeyTile)) {
+                    for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+                    tmem_wait_ld();
+                    if (masks) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * q + i >= n) s[q][i] = 0xff800000u;  // -infinity
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * q + i >= nk) s[q][i] = 0xff800000u;  // -infinity
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t *v = &s[q >> 1][16 * (q & 1)];
+                        mx[q] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+#pragma unroll
+                        for (int i = 2; i < 16; i += 2)
+                            mx[q] = max3(mx[q], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                    }
+                    mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                } else {
+                    mt = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        load_scores(ts + 32 * q, nk - 32 * q, masks, s[0]);
+                        float mx[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            mx[k] = fmaxf(__uint_as_float(s[0][8 * k]), __uint_as_float(s[0][8 * k + 1]));
+#pragma unroll
+                            for (int i = 2; i < 8; i += 2)
+                                mx[k] = max3(mx[k], __uint_as_float(s[0][8 * k + i]), __uint_as_float(s[0][8 * k + i + 1]));
+                        }
+                        mt = fmaxf(max3(mt, mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    }
                 }
-                float mx[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t *v = &s[q >> 1][16 * (q & 1)];
-                    mx[q] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
-#pragma unroll
-                    for (int i = 2; i < 16; i += 2)
-                        mx[q] = max3(mx[q], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                }
-                const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
                 const bool grown = mt > m && (m == -INFINITY || (mt - m) * c > kRescale);
                 if (__any_sync(0xffffffffu, grown)) {
                     const float mn = grown ? mt : m;
                     const float f = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
                     if (j > 0) {
                         // the previous product is in o before it is rescaled
-                        if (!(ok = warp_wait(o_done + t, (uint32_t)((j - 1) & 1)))) break;
+                        if (!(ok = warp_wait(o_done + t, (uint32_t)((steps - 1) & 1)))) break;
                         tc_after_sync();
                         const float2 f2 = make_float2(f, f);
-#pragma unroll
+#pragma unroll 1
                         for (int d = 0; d < DP; d += 16) {
                             uint32_t o[16];
+                            __syncwarp();
                             tmem_ld16(to + d, o);
                             tmem_wait_ld();
 #pragma unroll
@@ -467,91 +706,143 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
                 }
                 const float mc = m == -INFINITY ? 0.f : -m * c;
                 const float2 c2 = make_float2(c, c), m2 = make_float2(mc, mc);
+                if constexpr (kHold) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[16];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 x = PR::fma(make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, m2);
-                        x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                        w[i] = pack_pair<T>(x);
-                        s[q][2 * i] = __float_as_uint(x.x);
-                        s[q][2 * i + 1] = __float_as_uint(x.y);
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = PR::fma(make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, m2);
+                            x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                            pk[i] = pack_pair<T>(x);
+                            s[q][2 * i] = __float_as_uint(x.x);
+                            s[q][2 * i + 1] = __float_as_uint(x.y);
+                        }
+                        tmem_st16(ts + 16 * q, pk);
+                        if (q & 1) {
+                            // half of p is there: its product can start
+                            tmem_wait_st();
+                            tc_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive((q == 1 ? p_half : p_ready) + t);
+                        }
                     }
-                    tmem_st16(ts + 16 * q, w);
-                    if (q & 1) {
-                        // half of p is there: its product can start
-                        tmem_wait_st();
-                        tc_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive((q == 1 ? p_half : p_ready) + t);
+                    // the sum, off the path that the products wait for
+                    float2 a2[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        a2[q] = make_float2(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+                        for (int i = 2; i < 32; i += 2)
+                            a2[q] = PR::add(a2[q], make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
+                    }
+                    l2 = PR::add(l2, PR::add(PR::add(a2[0], a2[1]), PR::add(a2[2], a2[3])));
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        load_scores(ts + 32 * q, nk - 32 * q, masks, s[0]);
+                        uint32_t pk[16];
+                        float2 a2 = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = PR::fma(make_float2(__uint_as_float(s[0][2 * i]), __uint_as_float(s[0][2 * i + 1])), c2, m2);
+                            x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                            pk[i] = pack_pair<T>(x);
+                            a2 = PR::add(a2, x);
+                        }
+                        l2 = PR::add(l2, a2);
+                        // (columns 16 q .. of p lie before the scores still to be read)
+                        tmem_st16(ts + 16 * q, pk);
+                        if (q & 1) {
+                            tmem_wait_st();
+                            tc_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive((q == 1 ? p_half : p_ready) + t);
+                        }
                     }
                 }
-                // the sum, off the path that the products wait for
-                float2 a2[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    a2[q] = make_float2(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
-#pragma unroll
-                    for (int i = 2; i < 32; i += 2)
-                        a2[q] = PR::add(a2[q], make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
-                }
-                l2 = PR::add(l2, PR::add(PR::add(a2[0], a2[1]), PR::add(a2[2], a2[3])));
             }
             // ------------------------------------------------------ results
-            if (ok && ntiles > 0) {
-                ok = warp_wait(o_done + t, (uint32_t)((ntiles - 1) & 1));
+            if (ok && w.ntiles > 0) {
+                ok = warp_wait(o_done + t, (uint32_t)((steps - 1) & 1));
                 tc_after_sync();
             }
-            if (ok) {
-                const float l = l2.x + l2.y;
-                const bool none = m == -INFINITY && !(l != l);  // no key seen
-                const float inv = none ? 0.f : 1.f / l;
-                const float lse2 = none ? -INFINITY : m * c + log2f(l);
-                const int64_t token = q0 + tok;
-                const int head = kvh * p.group + g;
-                const int64_t orow = token * p.heads + head;
-                if (live && p.splits > 1) p.part_lse[(int64_t)split * p.tokens * p.heads + orow] = lse2;
-                if (live && p.splits == 1 && p.lse) p.lse[orow] = lse2 * 0.693147180559945309f;
-                float *po = p.splits > 1 ? p.part_o + ((int64_t)split * p.tokens * p.heads + orow) * p.head_dim : nullptr;
-                char *out = p.out + token * p.out_token + (int64_t)head * p.out_head;
+            if (!ok) break;
+            const float l = l2.x + l2.y;
+            const bool none = m == -INFINITY && !(l != l);  // no key seen
+            const float inv = none ? 0.f : 1.f / l;
+            const float lse2 = none ? -INFINITY : m * c + log2f(l);
+            const int head = w.kvh * p.group + row_head;
+            const int64_t token = w.q0 + tok, orow = token * p.heads + head, plane = p.tokens * p.heads;
+            const bool parts = p.splits > 1;
+            if (live) {
+                if (parts)
+                    p.part_lse[(int64_t)w.split * plane + orow] = lse2;
+                else if (p.lse)
+                    p.lse[orow] = lse2 * 0.693147180559945309f;
+            }
+            // A row is a lane's, and 16 bytes of each of 32 rows a store would
+            // occupy the store path for 32 cycles: four lanes exchange their
+            // chunks and write 64 bytes of each of eight rows instead.
+            char *dst = parts ? reinterpret_cast<char *>(p.part_o + ((int64_t)w.split * plane + orow) * p.head_dim)
+                              : p.out + token * p.out_token + (int64_t)head * p.out_head;
+            char *rows4[4];
 #pragma unroll
-                for (int d = 0; d < DP; d += 32) {
-                    if (d >= p.head_dim) break;
-                    uint32_t o[32];
-                    if (ntiles > 0) {
-                        __syncwarp();
-                        tmem_ld32(to + d, o);
-                        tmem_wait_ld();
-                    }
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(live ? dst : nullptr), (lane & 28) + k);
+                rows4[k] = reinterpret_cast<char *>(a);
+            }
+            // (rolled loops: unrolled, the code's fetches took longer than the work)
+            const int cols = p.head_dim;
+#pragma unroll 1
+            for (int d = 0; d < cols; d += 32) {
+                uint32_t o[32];
+                if (w.ntiles > 0) {
+                    __syncwarp();
+                    tmem_ld32(to + d, o);
+                    tmem_wait_ld();
+                }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+                for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+                uint4 ck[4];
+                if (parts) {  // fp32: two blocks of 16 values
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        if (!live || d + i >= p.head_dim) continue;
-                        if (p.splits > 1) {
-                            reinterpret_cast<uint4 *>(po + d + i)[0] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                            reinterpret_cast<uint4 *>(po + d + i)[1] = make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
-                            continue;
+                    for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = 16 * hh + 4 * k;
+                            ck[k] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
-                        uint32_t w[4];
+                        transpose4(ck, lane);
+                        const int at = d + 16 * hh + (lane & 3) * 4;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            w[k] = pack_pair<T>(make_float2(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1])));
-                        char *dst = out + (d + i) * 2;
-                        if (p.out_vec) {
-                            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-                            uint16_t *d16 = reinterpret_cast<uint16_t *>(dst);
+                            if (rows4[k] && at < cols) *reinterpret_cast<uint4 *>(rows4[k] + at * 4) = ck[k];
+                    }
+                } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                d16[2 * k] = (uint16_t)w[k];
-                                d16[2 * k + 1] = (uint16_t)(w[k] >> 16);
-                            }
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            pk[e] = pack_pair<T>(make_float2(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1])));
+                        ck[k] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    transpose4(ck, lane);
+                    const int at = d + (lane & 3) * 8;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (!rows4[k] || at >= cols) continue;
+                        if (p.out_vec)
+                            *reinterpret_cast<uint4 *>(rows4[k] + at * 2) = ck[k];
+                        else
+                            store_halves(reinterpret_cast<uint16_t *>(rows4[k]) + at, ck[k]);
                     }
                 }
             }
+            // (o is read before the next item's first product, which waits for
+            // this warp's next p)
+            tc_before_sync();
         }
     }
     __syncwarp();

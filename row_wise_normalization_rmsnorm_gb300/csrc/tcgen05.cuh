@@ -152,6 +152,35 @@ __device__ __forceinline__ bool mbar_try_wait_cta(uint64_t *bar, uint32_t parity
 // reads (matrix instructions, copies).
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Work from the blocks of this grid that have not started: asks for one to be
+// cancelled in this block's favour. 16 bytes arrive at `answer` (16-byte
+// aligned) and are counted on `bar`. Not asked again after a refusal.
+__device__ __forceinline__ void next_block_ask(void *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The cancelled block's index, or -1: none was left.
+__device__ __forceinline__ int next_block_answer(const void *answer) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Tiled copy of a box of a 4-D array into this CTA's shared memory, counted
 // in bytes on `bar`; what lies outside the array arrives as zeros. c0's byte
 // offset is a multiple of 16.
