@@ -41,8 +41,7 @@
 namespace rmsn {
 
 constexpr int kKeyTile = 128;
-constexpr uint32_t kAttnWait = 1u << 22;         // polls of one barrier ...
-constexpr uint64_t kAttnWaitNs = 2000000000ull;  // ... and time, before a kernel gives up
+constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kernel gives up
 constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
 constexpr float kRescale = 8.f;           // log2 of how far a row's reference maximum may lag
 
@@ -103,26 +102,31 @@ template <typename T> __device__ __forceinline__ uint32_t pack_pair(float2 v);
 template <> __device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float2 v) { return f2_to_bf16x2(v); }
 template <> __device__ __forceinline__ uint32_t pack_pair<__half>(float2 v) { return f2_to_f16x2(v); }
 
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
+// A CTA's waits: bounded, and given up by all roles once one of them
+// did. Kept short, since there are two dozen of them and the code's way into
+// the instruction cache is what a small call spends its time on.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status) {
+#pragma unroll 1
+    for (uint32_t i = 0; !mbar_try_wait_cta(bar, parity);) {
+        if ((++i & 15u) == 0 && (i >= kAttnWait || *gave_up)) {
+            *gave_up = 1;
+            *status = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
-// A CTA's waits: bounded, and given up by all roles once one of them did.
-struct Waiter {
-    volatile int *gave_up;  // shared memory
-    int *status;
-    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait_cta(bar, parity)) return true;
-        const uint64_t began = now_ns();
-        for (uint32_t i = 0; i < kAttnWait; ++i) {
-            if (mbar_try_wait_cta(bar, parity)) return true;
-            if ((i & 15u) == 15u && (*gave_up || now_ns() - began > kAttnWaitNs)) break;
-        }
-        *gave_up = 1;
-        *status = 1;
-        return false;
+// A place in the ring of K and V tiles (K_0, V_0, K_1, ... over all items) and
+// the parity of its turn.
+template <int NST> struct Ring {
+    int st = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ Ring next() const {
+        Ring r;
+        r.st = st + 1 == NST ? 0 : st + 1;
+        r.turn = st + 1 == NST ? turn ^ 1u : turn;
+        return r;
     }
 };
 
@@ -194,6 +198,8 @@ __device__ __forceinline__ void transpose4(uint4 (&c)[4], int lane) {
         swap_lanes(c[k].w, c[k + 2].w, u2, 2);
     }
 }
+
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // 32 columns of a tile's scores; columns from n on are masked.
 __device__ __forceinline__ void load_scores(uint32_t from, int n, bool masks, uint32_t (&s)[32]) {
@@ -279,16 +285,24 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         return;
     }
     if (warp == kIssuer) tmem_alloc(tmem_slot, S::kCols);
-    Item w0;
-    bool has_w0 = false;
-    if (warp == kProducer) has_w0 = decode_item<NQ>(p, blockIdx.x, w0);
+    if (warp == kProducer) {  // the first item's lengths, on their way while the CTA meets
+        const int b = (int)blockIdx.x / p.kv_heads % p.batch;
+        prefetch_l1(p.cu_q + b);
+        prefetch_l1(p.cu_q + b + 1);
+        prefetch_l1(p.kv_lens + b);
+    }
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const Waiter wait{gave_up, p.status};
-    // for a whole warp: all of it goes on or none
-    auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    // By a whole warp: all of it goes on or none. The first poll is apart and its
+    // branch uniform: as part of the loop, whose lanes may leave one by one, a
+    // wait for what is already there cost the inner loop 20% (prompt of 4864
+    // tokens over 32768: 1631 -> 1331 us). Every lane polls, and so acquires.
+    auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_cta(bar, parity))) return true;
+        return __all_sync(0xffffffffu, wait_on(bar, parity, gave_up, p.status)) != 0;
+    };
     volatile int still = 0;  // the last waits, after giving up, have a limit of their own
     const uint32_t sbase = smem_u32(smem);
     const uint32_t stage0 = sbase + NQ * S::kQBytes;
@@ -313,10 +327,10 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         const int piece = lane % boxes, half = lane / boxes;
         const bool copies = half < S::kHalves;
         const uint32_t off = (uint32_t)(half * kKeyTile * 128 + piece * p.box_rows * 128);
-        Item w = w0, next;
+        Item w;
         // (the table's entry is checked where it is used, a tile later: until
         // then its load is under way)
-        int page, place, next_page, next_place;
+        int page, place;
         auto find = [&](const Item &i, int tile, int &pg, int &pl) {
             const int key = i.kbeg + tile * kKeyTile + piece * p.box_rows;
             pg = -1;
@@ -339,16 +353,20 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             __syncwarp();
             ++asked;
         };
-        // The next item with work (asked for), its first tile looked up; ntiles
-        // -1: none.
+        // The next item with work (this block's own, then those asked for), its
+        // first tile looked up; ntiles -1: none.
         auto find_next = [&](Item &i, int &pg, int &pl) {
+#pragma unroll 1
             for (;; ask()) {
-                if (!warp_wait(answered, (uint32_t)((asked - 1) & 1))) {
-                    ok = false;
-                    break;
+                int id = blockIdx.x;
+                if (asked > 0) {
+                    if (!warp_wait(answered, (uint32_t)((asked - 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    id = next_block_answer(answer);
+                    __syncwarp();
                 }
-                const int id = next_block_answer(answer);
-                __syncwarp();
                 if (id < 0) break;
                 if (decode_item<NQ>(p, id, i)) {
                     find(i, 0, pg, pl);
@@ -357,10 +375,10 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             }
             i.ntiles = -1;
         };
-        int issued = 0;  // tiles, over all items
+        Ring<NST> at;  // the next tile's place
         auto copy_tile = [&](const CUtensorMap *map, int kvh, int pg, int pl) {
-            const int st = issued % NST;
-            if (issued >= NST && !warp_wait(empty + st, (uint32_t)((issued / NST - 1) & 1))) {
+            const int st = at.st;
+            if (!warp_wait(empty + st, at.turn ^ 1u)) {
                 ok = false;
                 return;
             }
@@ -372,19 +390,21 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
                 pl = 0;
             }
             if (copies) tile_g2s(stage0 + st * S::kStage + off, map, half * 64, pl, kvh, pg, full + st);
-            ++issued;
+            at = at.next();
         };
         // Values past the sequence's end in its last page would meet a zero
         // weight, and 0 * NaN is NaN: they become zeros once the tile is there.
-        int fix_tile = -1, fix_from = 0;
+        Ring<NST> fix_at;
+        int fix_from = -1;
         auto fix_values = [&]() {
-            const int st = fix_tile % NST;
-            if (!warp_wait(full + st, (uint32_t)((fix_tile / NST) & 1))) {
+            const int st = fix_at.st;
+            if (!warp_wait(full + st, fix_at.turn)) {
                 ok = false;
                 return;
             }
             const int end = (fix_from / p.box_rows + 1) * p.box_rows;  // later boxes are zeros
             const int chunks = (end - fix_from) * 8;
+#pragma unroll 1
             for (int i = lane; i < chunks * S::kHalves; i += 32) {
                 const int h = i / chunks, c = i - h * chunks;
                 sts128(smem + NQ * S::kQBytes + st * S::kStage + h * kKeyTile * 128 + fix_from * 128 + c * 16,
@@ -393,46 +413,47 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_fixed);
-            fix_tile = -1;
+            fix_from = -1;
         };
 
-        if (has_w0) {
-            find(w, 0, page, place);
-        } else {
-            ask();
-            find_next(w, page, place);
-        }
         int n = 0, q_loads = 0;
-        for (; ok; ++n) {
-            if (n >= 2 && !warp_wait(item_empty + (n & 1), (uint32_t)(((n >> 1) - 1) & 1))) {
-                ok = false;
-                break;
-            }
+#pragma unroll 1
+        for (;; ++n) {
+            find_next(w, page, place);
+            if (!ok) break;
+            // (an item that copies nothing leaves nothing to put the mending off to)
+            if (w.ntiles <= 0 && fix_from >= 0) fix_values();
+            if (!ok || (n >= 2 && !warp_wait(item_empty + (n & 1), (uint32_t)(((n >> 1) - 1) & 1)))) break;
             if (lane == 0) {
                 items[n & 1] = w;
                 mbar_arrive(item_full + (n & 1));
             }
             __syncwarp();
             if (w.ntiles < 0) break;
-            // Asked for when the item's last tiles are being copied: late, so that
-            // the blocks left go to whoever is done first, and early enough for
-            // the answer (a microsecond) to be there in time.
-            const int ask_at = max(w.ntiles - kAskAhead, 0);
+            // The next is asked for when the item's last tiles are being copied:
+            // late, so that the blocks left go to whoever is done first, and early
+            // enough for the answer (a microsecond) to be there in time.
+            const int ask_at = max(2 * (w.ntiles - kAskAhead), 1);
             if (w.ntiles == 0) ask();
-            for (int j = 0; j < w.ntiles && ok; ++j) {
-                int pg, pl;
-                copy_tile(&kmap, w.kvh, page, place);
-                find(w, j + 1, pg, pl);
-                if (j == 0) {
-                    // (this tile's place in the ring did not wait for the values mended here)
-                    if (ok && fix_tile >= 0) fix_values();
+            int next_page, next_place;
+            Ring<NST> last_at;
+#pragma unroll 1
+            for (int i = 0; i < 2 * w.ntiles; ++i) {  // K_0, V_0, K_1, ...
+                last_at = at;
+                copy_tile(i & 1 ? &vmap : &kmap, w.kvh, page, place);
+                if (!ok) break;
+                if (i == 0) {
+                    // (K_0's place in the ring did not wait for the values mended here)
+                    if (fix_from >= 0) fix_values();
                     if (ok && p.q_tma) {
                         // q's rows: tt tokens of `group` heads are one box, row after row
                         if (q_loads > 0 && !warp_wait(q_free, (uint32_t)((q_loads - 1) & 1))) ok = false;
                         if (ok && lane == 0) {
                             const int act = w.toks > tt ? 2 : 1;
                             mbar_arrive_expect_tx(q_ready, (uint32_t)(act * S::kHalves * tt * p.group * 128));
+#pragma unroll 1
                             for (int t = 0; t < act; ++t)
+#pragma unroll 1
                                 for (int h = 0; h < S::kHalves; ++h)
                                     tile_g2s(sbase + t * S::kQBytes + h * (S::kQRows * 128), &qmap, h * 64, 0, w.kvh,
                                              w.q0 + w.tok0 + t * tt, q_ready);
@@ -440,29 +461,28 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
                         __syncwarp();
                         if (ok) ++q_loads;
                     }
+                    if (!ok) break;
                 }
-                if (ok) copy_tile(&vmap, w.kvh, page, place);
-                page = pg;
-                place = pl;
-                if (ok && j == ask_at) ask();
+                if (i & 1) {
+                    page = next_page;
+                    place = next_place;
+                } else {
+                    find(w, (i >> 1) + 1, next_page, next_place);
+                }
+                if (i == ask_at) ask();
             }
             if (!ok) break;
             if (w.fix) {
-                fix_tile = issued - 1;
                 fix_from = w.kv - (w.kbeg + (w.ntiles - 1) * kKeyTile);
+                fix_at = last_at;
             }
-            find_next(next, next_page, next_place);
-            // (nothing follows to put the mending off to)
-            if (ok && next.ntiles <= 0 && fix_tile >= 0) fix_values();
-            w = next;
-            page = next_page;
-            place = next_place;
         }
         if (*gave_up) {  // no copy may be in flight when the CTA ends
-            const Waiter last{&still, p.status};
-            if (q_loads > 0) last(q_ready, (uint32_t)((q_loads - 1) & 1));
-            for (int i = max(0, issued - NST); i < issued; ++i) last(full + i % NST, (uint32_t)((i / NST) & 1));
-            if (asked > 0) last(answered, (uint32_t)((asked - 1) & 1));
+            if (q_loads > 0) wait_on(q_ready, (uint32_t)((q_loads - 1) & 1), &still, p.status);
+            // (the last turn of each place: a place not copied to yet has turn 1 behind it)
+#pragma unroll 1
+            for (int i = 0; i < NST; ++i, at = at.next()) wait_on(full + at.st, at.turn ^ 1u, &still, p.status);
+            if (asked > 0) wait_on(answered, (uint32_t)((asked - 1) & 1), &still, p.status);
         }
     } else if (warp == kIssuer) {
         // ------------------------------------------- the matrix instructions
@@ -505,56 +525,67 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             if (issues) mma_commit(bar);
             __syncwarp();
         };
-        // stage and phase of the ring's n-th tile (K_0, V_0, K_1, V_1, ... over all items)
-        auto arrived = [&](int n) { return warp_wait(full + n % NST, (uint32_t)((n / NST) & 1)); };
-        int base = 0, q_loads = 0, fixes = 0, steps[2] = {0, 0};
+        auto arrived = [&](const Ring<NST> &r) { return warp_wait(full + r.st, r.turn); };
+        Ring<NST> kr;  // the next key tile's place
+        uint32_t q_turn = 0, fix_turn = 0, turn[2] = {0, 0};
         bool ok = true;
+#pragma unroll 1
         for (int n = 0; ok; ++n) {
             Item w;
             if (!(ok = take(n, w)) || w.ntiles < 0) break;
             if (w.ntiles == 0) continue;
             const int act = w.toks > tt ? 2 : 1;
-            ok = arrived(base) && warp_wait(q_ready, (uint32_t)(q_loads & 1));
+            ok = arrived(kr) && warp_wait(q_ready, q_turn);
             if (!ok) break;
-            ++q_loads;
+            q_turn ^= 1u;
             tc_after_sync();
             // (what the softmax still had to read of s, the products issued before have waited for)
-            for (int t = 0; t < act; ++t) qk(t, base % NST);
-            done_with(empty + base % NST);
+#pragma unroll
+            for (int t = 0; t < NQ; ++t)
+                if (t < act) qk(t, kr.st);
+            done_with(empty + kr.st);
             if (w.ntiles == 1) done_with(q_free);
-            ok = arrived(base + 1);
+            Ring<NST> vr = kr.next();
+            kr = vr.next();
+            ok = arrived(vr);
+#pragma unroll 1
             for (int j = 0; j < w.ntiles && ok; ++j) {
                 const bool more = j + 1 < w.ntiles;
-                const int kn = base + 2 * j + 2, vn = base + 2 * j + 1;
-                if (!more && w.fix) ok = warp_wait(v_fixed, (uint32_t)(fixes++ & 1));
-                for (int t = 0; t < act && ok; ++t) {
-                    const uint32_t ph = (uint32_t)(steps[t] & 1);
-                    ++steps[t];
-                    if (!(ok = warp_wait(p_half + t, ph))) break;
+                if (!more && w.fix) {
+                    ok = warp_wait(v_fixed, fix_turn);
+                    fix_turn ^= 1u;
+                }
+                const Ring<NST> vn = kr.next();  // the next values' place
+#pragma unroll
+                for (int t = 0; t < NQ; ++t) {
+                    if (t >= act || !ok) break;
+                    if (!(ok = warp_wait(p_half + t, turn[t]))) break;
                     tc_after_sync();
-                    pv(t, vn % NST, 0, j > 0);
-                    if (!(ok = warp_wait(p_ready + t, ph))) break;
+                    pv(t, vr.st, 0, j > 0);
+                    if (!(ok = warp_wait(p_ready + t, turn[t]))) break;
+                    turn[t] ^= 1u;
                     tc_after_sync();
-                    pv(t, vn % NST, 1, true);
-                    if (t == act - 1) done_with(empty + vn % NST);
+                    pv(t, vr.st, 1, true);
+                    if (t == act - 1) done_with(empty + vr.st);
                     if (more) {
-                        if (t == 0) ok = arrived(kn);
-                        if (ok) qk(t, kn % NST);
+                        if (t == 0) ok = arrived(kr);
+                        if (ok) qk(t, kr.st);
                         // (here, where the products just issued cover the wait)
-                        if (ok && t == 0) ok = arrived(kn + 1);
+                        if (ok && t == 0) ok = arrived(vn);
                     }
                 }
                 if (more && ok) {
-                    done_with(empty + kn % NST);
+                    done_with(empty + kr.st);
                     if (j + 2 == w.ntiles) done_with(q_free);
+                    vr = vn;
+                    kr = vn.next();
                 }
             }
-            base += 2 * w.ntiles;
         }
         if (*gave_up) {  // nor may a matrix instruction be
             __syncwarp();
             if (issues) mma_commit(drained);
-            Waiter{&still, p.status}(drained, 0);
+            wait_on(drained, 0, &still, p.status);
         }
     }
     } else {
@@ -568,6 +599,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         using PR = Pair<true>;
         int steps = 0;  // key tiles, over all items
         bool ok = true;
+#pragma unroll 1
         for (int n = 0; ok; ++n) {
             Item w;
             if (!(ok = take(n, w)) || w.ntiles < 0) break;
@@ -579,6 +611,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
                 // with q was done before its last softmax.)
                 constexpr int kChunks = S::kHalves * 8, kBatch = 8;
                 const int hd_chunks = p.head_dim / 8;
+#pragma unroll 1
                 for (int i0 = r; i0 < S::kQRows * kChunks; i0 += 128 * kBatch) {
                     uint4 v[kBatch];
 #pragma unroll
@@ -613,6 +646,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             if (rows == 0) continue;  // (the tile's products are not issued either)
             if ((warp & 3) * 32 >= rows) {
                 // a warp without rows only keeps the tile's count of arrivals
+#pragma unroll 1
                 for (int j = 0; j < w.ntiles; ++j, ++steps) {
                     if (!(ok = warp_wait(s_ready + t, (uint32_t)(steps & 1)))) break;
                     if (lane == 0) {
@@ -630,6 +664,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             const int vis = live ? (int)(min(seen, (int64_t)w.kend) - w.kbeg) : 0x7fffffff;
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll 1
             for (int j = 0; j < w.ntiles; ++j, ++steps) {
                 if (!(ok = warp_wait(s_ready + t, (uint32_t)(steps & 1)))) break;
                 tc_after_sync();

@@ -136,7 +136,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // True once the phase with the given parity has completed; acquire within
-// the CTA (the cluster-wide form costs a hundred cycles more a call).
+// the CTA (the cluster-wide form costs a hundred cycles more a call, and the
+// form that names a suspension time 5% of the attention's inner loop).
 __device__ __forceinline__ bool mbar_try_wait_cta(uint64_t *bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
