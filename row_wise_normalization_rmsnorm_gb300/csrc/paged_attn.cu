@@ -42,6 +42,7 @@ namespace rmsn {
 
 constexpr int kKeyTile = 128;
 constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kernel gives up
+constexpr int kDecodeChunk = 16;           // key tiles of a decoding item, where there are several a CTA
 constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
 constexpr float kRescale = 8.f;           // log2 of how far a row's reference maximum may lag
 
@@ -60,6 +61,9 @@ struct AttnParams {
     int batch, width, heads, kv_heads, group, head_dim, pages, page_size, box_rows;
     int max_q, max_kv, causal, q_tiles, splits, chunk;  // chunk: keys a split takes
     int tile_toks;                                      // tokens a row tile takes
+    int nq;                                             // row tiles a CTA takes
+    int copiers;                                        // warps that copy K and V: 1 or 3
+    int by_seq;                                         // items in the order of the sequences' lengths
     int q_tma, q_vec, out_vec;
 };
 
@@ -72,10 +76,10 @@ struct AttnShape {
     static constexpr int kStages = NQ == 2 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 3 : 6);
     static constexpr int kBars = NQ * kQBytes + kStages * kStage;
     static constexpr int kSmem = kBars + 512;  // barriers, the work items
-    // NQ == 2: the copy and issue warps fill up a warpgroup of their own, so
-    // that registers can move to the softmax warps: 168 a thread at launch,
-    // then 2 x 128 x 208 + 128 x 88 = 384 x 168
-    static constexpr int kThreads = NQ == 2 ? 384 : 192;
+    // A fourth warpgroup's worth of warps copies (three) and issues matrix
+    // instructions (one). NQ == 2 moves registers from it to the softmax warps:
+    // 168 a thread at launch, then 2 x 128 x 208 + 128 x 88 = 384 x 168.
+    static constexpr int kThreads = NQ * 128 + 128;
     // tensor memory: s (and p) of each tile, then o of each tile
     static constexpr uint32_t kO = NQ * kKeyTile;
     static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;
@@ -137,36 +141,78 @@ struct Item {
     int tok0, toks;      // its tokens taken here
     int kbeg, kend;      // keys taken here
     int kvh, split, b;
+    int parts;           // the rows' keys are split: partial results
     int ntiles;          // key tiles; -1: no more work
     int fix;             // the last tile's values past the sequence's end to become zeros
 };
 
-// Work item `id`: (sequence, key head) fastest, then the split, then the row
-// tile, the last rows (most keys) first. False: it has nothing to do.
-template <int NQ>
-__device__ __forceinline__ bool decode_item(const AttnParams &p, int id, Item &w) {
+__device__ __forceinline__ int kv_length(const AttnParams &p, int len) {
+    return max(0, min(min(len, p.max_kv), (int)min((int64_t)p.width * p.page_size, (int64_t)0x7fffffff)));
+}
+
+// Keys that the last row of a row tile sees: tokens up to `end` of the nq new
+// ones of a sequence of kv.
+__device__ __forceinline__ int keys_seen(const AttnParams &p, int kv, int nq, int end) {
+    return p.causal ? (int)min((int64_t)kv, max((int64_t)0, (int64_t)kv - nq + end)) : kv;
+}
+
+// Work item `id`, for a whole warp; false: it has nothing to do. The long ones
+// come first, since the last to start decide when the call ends: (sequence,
+// key head) fastest, then the split, then the row tile from the last rows
+// (most keys) on; or, where the keys before the new tokens are most of them,
+// by_seq (at most 32 sequences): the sequences from the longest on, in each
+// the row tiles, splits and key heads.
+__device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per, Item &w) {
+    const int lane = threadIdx.x & 31;
+    const int T_ = (int)p.tokens;
     w.kvh = id % p.kv_heads;
     id /= p.kv_heads;
-    const int b = id % p.batch;
-    id /= p.batch;
+    int b, qt;
+    if (p.by_seq) {
+        int n = 0, parts = 1, kv = -1;
+        if (lane < p.batch) {
+            const int c0 = min(max(__ldg(p.cu_q + lane), 0), T_), c1 = min(max(__ldg(p.cu_q + lane + 1), c0), T_);
+            kv = kv_length(p, __ldg(p.kv_lens + lane));
+            n = (min(c1 - c0, p.max_q) + per - 1) / per;
+            if (p.splits > 1) parts = max((kv + p.chunk - 1) / p.chunk, 1);
+        }
+        int before = 0;
+        for (int o = 0; o < p.batch; ++o) {
+            const int k = __shfl_sync(0xffffffffu, kv, o), m = __shfl_sync(0xffffffffu, n * parts, o);
+            if (k > kv || (k == kv && o < lane)) before += m;
+        }
+        const uint32_t mine = __ballot_sync(0xffffffffu, id >= before && id < before + n * parts);
+        if (mine == 0) return false;
+        b = __ffs((int)mine) - 1;
+        id -= __shfl_sync(0xffffffffu, before, b);
+        parts = __shfl_sync(0xffffffffu, parts, b);
+        qt = __shfl_sync(0xffffffffu, n, b) - 1 - id / parts;
+        w.split = id % parts;
+    } else {
+        b = id % p.batch;
+        id /= p.batch;
+        w.split = id % p.splits;
+        qt = p.q_tiles - 1 - id / p.splits;
+    }
     w.b = b;
-    w.split = id % p.splits;
-    const int qt = p.q_tiles - 1 - id / p.splits;
-    const int T_ = (int)p.tokens;
-    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_lens + b);
+    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
+    w.kv = kv_length(p, __ldg(p.kv_lens + b));
     w.q0 = min(max(c0, 0), T_);
     w.nq = min(max(c1, w.q0), T_) - w.q0;
-    w.kv = max(0, min(min(len, p.max_kv), (int)min((int64_t)p.width * p.page_size, (int64_t)0x7fffffff)));
-    w.tok0 = qt * NQ * p.tile_toks;
-    w.toks = min(min(w.nq, p.max_q) - w.tok0, NQ * p.tile_toks);
+    w.tok0 = qt * per;
+    w.toks = min(min(w.nq, p.max_q) - w.tok0, per);
     if (w.toks <= 0) return false;
-    // keys that the last row sees, and this split's part of them
-    const int64_t lim = p.causal ? min((int64_t)w.kv, max((int64_t)0, (int64_t)w.kv - w.nq + w.tok0 + w.toks)) : w.kv;
-    const int64_t kbeg = (int64_t)w.split * p.chunk;
-    const int64_t kend = p.splits > 1 ? min(lim, kbeg + p.chunk) : lim;
-    if (p.splits > 1 && kend <= kbeg) return false;
-    w.kbeg = (int)kbeg;
-    w.kend = (int)kend;
+    const int lim = keys_seen(p, w.kv, w.nq, w.tok0 + w.toks);
+    w.kbeg = 0;
+    w.kend = lim;
+    w.parts = 0;
+    if (p.splits > 1) {
+        const int64_t kbeg = (int64_t)w.split * p.chunk;
+        if (kbeg >= lim) return false;  // (rows without keys are the join's)
+        w.kbeg = (int)kbeg;
+        w.kend = (int)min((int64_t)lim, kbeg + p.chunk);
+        w.parts = lim > p.chunk;
+    }
     w.ntiles = (w.kend - w.kbeg + kKeyTile - 1) / kKeyTile;
     const int last_valid = w.kv - (w.kbeg + (w.ntiles - 1) * kKeyTile);
     w.fix = w.ntiles > 0 && last_valid < kKeyTile && last_valid % p.box_rows != 0;
@@ -228,7 +274,7 @@ __device__ __noinline__ void store_halves(uint16_t *to, uint4 v) {
 // roles run from one item into the next: while the softmax warps write an
 // item's rows, the next one's keys arrive and its first product is done.
 template <typename T, int DP, int NQ>
-__global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
+__global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     paged_attn(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using S = AttnShape<DP, NQ>;
@@ -267,7 +313,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
         mbar_init(drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(item_full + i, 1);
-            mbar_init(item_empty + i, NQ * 4 + 1);
+            mbar_init(item_empty + i, NQ * 4 + p.copiers);  // all warps but the one that makes the items
         }
         mbar_init(answered, 1);
         *gave_up = 0;
@@ -286,7 +332,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
     }
     if (warp == kIssuer) tmem_alloc(tmem_slot, S::kCols);
     if (warp == kProducer) {  // the first item's lengths, on their way while the CTA meets
-        const int b = (int)blockIdx.x / p.kv_heads % p.batch;
+        const int b = p.by_seq ? min(lane, p.batch - 1) : (int)blockIdx.x / p.kv_heads % p.batch;
         prefetch_l1(p.cu_q + b);
         prefetch_l1(p.cu_q + b + 1);
         prefetch_l1(p.kv_lens + b);
@@ -319,28 +365,52 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
 
     if (warp >= kProducer) {
     if constexpr (NQ == 2) fewer_registers<88>();
+    // Copies of K and V. A tile is 128 / box_rows boxes by 64 columns. Issuing
+    // them takes a warp 85 cycles each (the operands of each lane go through
+    // uniform registers): with pages of 8, 5400 cycles a K and V tile where the
+    // products take 2100. With small boxes three warps share them; with large
+    // ones the other two only cost (2 x 8192 tokens, D 128: pages of 8 1178 ->
+    // 707 us and of 16 775 -> 674, but of 64 649 -> 677).
+    const int copier = warp == kProducer ? 0 : warp - kIssuer;  // 0, 1, 2
+    const int boxes = kKeyTile / p.box_rows;
+    const int item_box = copier + p.copiers * lane;
+    const int piece = item_box % boxes, half = item_box / boxes;
+    const bool copies = half < S::kHalves;
+    const uint32_t off = (uint32_t)(half * kKeyTile * 128 + piece * p.box_rows * 128);
+    // (the table's entry is checked where it is used, a tile later: until then
+    // its load is under way)
+    auto find = [&](const Item &i, int tile, int &pg, int &pl) {
+        const int key = i.kbeg + tile * kKeyTile + piece * p.box_rows;
+        pg = -1;
+        pl = 0;
+        if (copies && tile < i.ntiles && key < i.kv) {
+            const int col = key / p.page_size;
+            pg = __ldg(p.table + i.b * p.table_stride + col);
+            pl = key - col * p.page_size;
+        }
+    };
+    Ring<NST> at;  // the next tile's place
+    // This warp's boxes of the next tile, once its place is free.
+    auto copy_tile = [&](const CUtensorMap *map, int kvh, int pg, int pl) {
+        const int st = at.st;
+        if (!warp_wait(empty + st, at.turn ^ 1u)) return false;
+        if (copier == 0) {  // (boxes counted before this only wait for it)
+            if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
+            __syncwarp();
+        }
+        // what is no page lies outside the cache: zeros
+        if ((uint32_t)pg >= (uint32_t)p.pages) {
+            pg = p.pages;
+            pl = 0;
+        }
+        if (copies) tile_g2s(stage0 + st * S::kStage + off, map, half * 64, pl, kvh, pg, full + st);
+        at = at.next();
+        return true;
+    };
     if (warp == kProducer) {
         // ------------------------------------------ the work, and its copies
-        // A tile is 128 / box_rows boxes by 64 columns; lane l copies piece
-        // l % boxes of half l / boxes.
-        const int boxes = kKeyTile / p.box_rows;
-        const int piece = lane % boxes, half = lane / boxes;
-        const bool copies = half < S::kHalves;
-        const uint32_t off = (uint32_t)(half * kKeyTile * 128 + piece * p.box_rows * 128);
         Item w;
-        // (the table's entry is checked where it is used, a tile later: until
-        // then its load is under way)
         int page, place;
-        auto find = [&](const Item &i, int tile, int &pg, int &pl) {
-            const int key = i.kbeg + tile * kKeyTile + piece * p.box_rows;
-            pg = -1;
-            pl = 0;
-            if (copies && tile < i.ntiles && key < i.kv) {
-                const int col = key / p.page_size;
-                pg = __ldg(p.table + i.b * p.table_stride + col);
-                pl = key - col * p.page_size;
-            }
-        };
         int asked = 0;
         bool ok = true;
         auto ask = [&]() {
@@ -368,29 +438,12 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
                     __syncwarp();
                 }
                 if (id < 0) break;
-                if (decode_item<NQ>(p, id, i)) {
+                if (decode_item(p, id, NQ * tt, i)) {
                     find(i, 0, pg, pl);
                     return;
                 }
             }
             i.ntiles = -1;
-        };
-        Ring<NST> at;  // the next tile's place
-        auto copy_tile = [&](const CUtensorMap *map, int kvh, int pg, int pl) {
-            const int st = at.st;
-            if (!warp_wait(empty + st, at.turn ^ 1u)) {
-                ok = false;
-                return;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
-            __syncwarp();
-            // what is no page lies outside the cache: zeros
-            if ((uint32_t)pg >= (uint32_t)p.pages) {
-                pg = p.pages;
-                pl = 0;
-            }
-            if (copies) tile_g2s(stage0 + st * S::kStage + off, map, half * 64, pl, kvh, pg, full + st);
-            at = at.next();
         };
         // Values past the sequence's end in its last page would meet a zero
         // weight, and 0 * NaN is NaN: they become zeros once the tile is there.
@@ -440,8 +493,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
 #pragma unroll 1
             for (int i = 0; i < 2 * w.ntiles; ++i) {  // K_0, V_0, K_1, ...
                 last_at = at;
-                copy_tile(i & 1 ? &vmap : &kmap, w.kvh, page, place);
-                if (!ok) break;
+                if (!(ok = copy_tile(i & 1 ? &vmap : &kmap, w.kvh, page, place))) break;
                 if (i == 0) {
                     // (K_0's place in the ring did not wait for the values mended here)
                     if (fix_from >= 0) fix_values();
@@ -484,7 +536,34 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             for (int i = 0; i < NST; ++i, at = at.next()) wait_on(full + at.st, at.turn ^ 1u, &still, p.status);
             if (asked > 0) wait_on(answered, (uint32_t)((asked - 1) & 1), &still, p.status);
         }
-    } else if (warp == kIssuer) {
+    } else if (warp != kIssuer) {
+        // ---------------------------------------------- the copies' other warps
+#pragma unroll 1
+        for (int n = 0; copier < p.copiers; ++n) {
+            Item w;
+            if (!take(n, w) || w.ntiles < 0) break;
+            int page, place, next_page, next_place;
+            find(w, 0, page, place);
+            bool ok = true;
+#pragma unroll 1
+            for (int i = 0; i < 2 * w.ntiles; ++i) {
+                if (!(ok = copy_tile(i & 1 ? &vmap : &kmap, w.kvh, page, place))) break;
+                if (i & 1) {
+                    page = next_page;
+                    place = next_place;
+                } else {
+                    find(w, (i >> 1) + 1, next_page, next_place);
+                }
+            }
+            if (!ok) break;
+        }
+        if (copier < p.copiers && *gave_up) {  // the newest place's turn ends when all its copies are there
+            Ring<NST> last;
+            last.st = at.st == 0 ? NST - 1 : at.st - 1;
+            last.turn = at.st == 0 ? at.turn ^ 1u : at.turn;
+            wait_on(full + last.st, last.turn, &still, p.status);
+        }
+    } else {
         // ------------------------------------------- the matrix instructions
         // The whole warp walks the tiles (operands stay uniform), one lane issues.
         const bool issues = elect_one();
@@ -809,7 +888,7 @@ __global__ void __launch_bounds__(NQ == 2 ? 384 : 192, NQ == 2 ? 1 : 2)
             const float lse2 = none ? -INFINITY : m * c + log2f(l);
             const int head = w.kvh * p.group + row_head;
             const int64_t token = w.q0 + tok, orow = token * p.heads + head, plane = p.tokens * p.heads;
-            const bool parts = p.splits > 1;
+            const bool parts = w.parts;
             if (live) {
                 if (parts)
                     p.part_lse[(int64_t)w.split * plane + orow] = lse2;
@@ -908,8 +987,12 @@ __global__ void __launch_bounds__(128) paged_attn_join(const __grid_constant__ A
     const int q0 = min(max(__ldg(p.cu_q + b), 0), T_);
     const int nq = min(max(__ldg(p.cu_q + b + 1), q0), T_) - q0;
     if (tok >= nq) return;
-    const int kv = max(0, min(min(__ldg(p.kv_lens + b), p.max_kv), (int)min((int64_t)p.width * p.page_size, (int64_t)0x7fffffff)));
-    const int64_t seen = p.causal ? max((int64_t)0, min((int64_t)kv, (int64_t)kv - nq + tok + 1)) : kv;
+    const int kv = kv_length(p, __ldg(p.kv_lens + b));
+    // a row tile whose keys one split held has written its rows itself
+    const int per = p.nq * p.tile_toks, tile_end = min((tok / per + 1) * per, min(nq, p.max_q));
+    const int lim = keys_seen(p, kv, nq, tile_end);
+    if (lim > 0 && lim <= p.chunk) return;
+    const int64_t seen = keys_seen(p, kv, nq, tok + 1);
     const int n = (int)((seen + p.chunk - 1) / p.chunk);  // splits that hold keys of this row
     const int64_t token = q0 + tok, orow = token * p.heads + head, plane = p.tokens * p.heads;
     float top = -INFINITY;
@@ -1035,6 +1118,13 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
             k.splits = (int)((tiles + per_split - 1) / per_split);
             k.chunk = (int)(per_split * kKeyTile);
         }
+    } else if (k.nq == 1 && ctas < 4 * slots && tiles >= 2 * kDecodeChunk) {
+        // A few items a CTA: shorter ones let the CTAs end together (64
+        // sequences of 964 to 8192 keys: 219 -> 187 us; of 8192 each: 300 -> 304).
+        // Rows by the hundred lose more with their partial results (chunks of
+        // 512 over 8192: 124 -> 147 us in two).
+        k.splits = (int)((tiles + kDecodeChunk - 1) / kDecodeChunk);
+        k.chunk = kDecodeChunk * kKeyTile;
     }
     k.workspace = 0;
     if (k.splits > 1) {
@@ -1157,10 +1247,14 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     p.splits = cut.splits;
     p.chunk = cut.chunk;
     p.tile_toks = cut.tile_toks;
+    p.nq = cut.nq;
+    p.by_seq = c.batch > 1 && c.batch <= 32 && cc.max_kv / 2 >= c.max_q;
     // (a group's heads share a box: their stride counts even for one key head)
     if (!empty && on(c.q, 16) && tile_stride(c.q_head, c.q_heads) && tile_stride(c.q_token, c.tokens))
         p.q_tma = tile_map(&maps[0], c.dtype, c.q, c.head_dim, {p.group, pc.heads, c.tokens},
                            {c.q_head, c.q_head * p.group, c.q_token}, p.group, p.tile_toks);
+    const int pieces = kKeyTile / p.box_rows * (c.head_dim > 64 ? 2 : 1);
+    p.copiers = pieces > (cut.nq == 1 ? 16 : 8) ? 3 : 1;
     p.q_vec = on(c.q, 16) && p.q_token % 16 == 0 && p.q_head % 16 == 0;
     p.out_vec = on(c.out, 16) && p.out_token % 16 == 0 && p.out_head % 16 == 0;
 
