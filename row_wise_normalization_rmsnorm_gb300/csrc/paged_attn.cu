@@ -42,6 +42,7 @@ namespace rmsn {
 
 constexpr int kKeyTile = 128;
 constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kernel gives up
+constexpr int kJoinTiles = 4;              // key tiles that the join's kernel takes as long as
 constexpr int kDecodeChunk = 16;           // key tiles of a decoding item, where there are several a CTA
 constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
 constexpr float kRescale = 8.f;           // log2 of how far a row's reference maximum may lag
@@ -162,13 +163,23 @@ __device__ __forceinline__ int keys_seen(const AttnParams &p, int kv, int nq, in
 // (most keys) on; or, where the keys before the new tokens are most of them,
 // by_seq (at most 32 sequences): the sequences from the longest on, in each
 // the row tiles, splits and key heads.
+template <bool CL>
 __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per, Item &w) {
     const int lane = threadIdx.x & 31;
     const int T_ = (int)p.tokens;
+    int rank = 0;
+    if (CL) {  // (the split fastest: a cluster's CTAs)
+        rank = id % p.splits;
+        id /= p.splits;
+    }
     w.kvh = id % p.kv_heads;
     id /= p.kv_heads;
     int b, qt;
-    if (p.by_seq) {
+    if (CL) {
+        b = id;
+        qt = 0;
+        w.split = rank;
+    } else if (p.by_seq) {
         int n = 0, parts = 1, kv = -1;
         if (lane < p.batch) {
             const int c0 = min(max(__ldg(p.cu_q + lane), 0), T_), c1 = min(max(__ldg(p.cu_q + lane + 1), c0), T_);
@@ -201,14 +212,16 @@ __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per
     w.nq = min(max(c1, w.q0), T_) - w.q0;
     w.tok0 = qt * per;
     w.toks = min(min(w.nq, p.max_q) - w.tok0, per);
-    if (w.toks <= 0) return false;
+    w.parts = 0;
+    w.ntiles = 0;
+    w.fix = 0;
+    if (w.toks <= 0) return CL;
     const int lim = keys_seen(p, w.kv, w.nq, w.tok0 + w.toks);
     w.kbeg = 0;
     w.kend = lim;
-    w.parts = 0;
     if (p.splits > 1) {
         const int64_t kbeg = (int64_t)w.split * p.chunk;
-        if (kbeg >= lim) return false;  // (rows without keys are the join's)
+        if (kbeg >= lim) return CL;  // (rows without keys are the join's)
         w.kbeg = (int)kbeg;
         w.kend = (int)min((int64_t)lim, kbeg + p.chunk);
         w.parts = lim > p.chunk;
@@ -269,11 +282,87 @@ __device__ __noinline__ void store_halves(uint16_t *to, uint4 v) {
     }
 }
 
+// 4 and 16 bytes of another CTA of the cluster, at the address of a variable
+// of this one.
+__device__ __forceinline__ float ld_cluster(const float *local, uint32_t cta) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(cta));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(const void *local, uint32_t cta) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(cta));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M) over the cluster's CTAs, in
+// their order; four values a thread, the rows' chunks dealt to the CTAs.
+template <typename T, int DP>
+__device__ __forceinline__ void join_cluster(const AttnParams &p, const Item &w, const uint8_t *rows, const float *lse) {
+    constexpr int kMost = 8;  // CTAs of a cluster
+    const int chunks = p.head_dim / 4, total = w.toks * p.group * chunks;
+    const int rank = (int)cluster_ctarank(), splits = p.splits;
+    for (int i = rank * (int)blockDim.x + (int)threadIdx.x; i < total; i += splits * (int)blockDim.x) {
+        const int r = i / chunks, c = i - r * chunks;
+        float l[kMost], top = -INFINITY, sum = 0.f;
+        float4 v[kMost];
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) {
+            if (s >= splits) break;
+            l[s] = ld_cluster(lse + r, (uint32_t)s);
+            v[s] = ld_cluster4(rows + r * (DP * 4) + ((c + r) % (DP / 4)) * 16, (uint32_t)s);
+        }
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) {
+            if (s >= splits) break;
+            top = l[s] != l[s] || top != top ? NAN : fmaxf(top, l[s]);
+        }
+        const bool none = top == -INFINITY;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) {
+            if (s >= splits) break;
+            const float e = exp2_approx(l[s] - (none ? 0.f : top));
+            sum += e;
+            a.x = __fmaf_rn(e, v[s].x, a.x);
+            a.y = __fmaf_rn(e, v[s].y, a.y);
+            a.z = __fmaf_rn(e, v[s].z, a.z);
+            a.w = __fmaf_rn(e, v[s].w, a.w);
+        }
+        const float inv = none ? 0.f : __fdividef(1.f, sum);
+        const int64_t token = w.q0 + w.tok0 + r / p.group;
+        const int head = w.kvh * p.group + r % p.group;
+        if (c == 0 && p.lse)
+            p.lse[token * p.heads + head] = none ? -INFINITY : (top + __log2f(sum)) * 0.693147180559945309f;
+        char *dst = p.out + token * p.out_token + (int64_t)head * p.out_head + c * 8;
+        const uint32_t w0 = pack_pair<T>(make_float2(a.x * inv, a.y * inv)), w1 = pack_pair<T>(make_float2(a.z * inv, a.w * inv));
+        if (p.out_vec) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
+        } else {
+            uint16_t *e = reinterpret_cast<uint16_t *>(dst);
+            e[0] = (uint16_t)w0;
+            e[1] = (uint16_t)(w0 >> 16);
+            e[2] = (uint16_t)w1;
+            e[3] = (uint16_t)(w1 >> 16);
+        }
+    }
+}
+
 // Persistent: a CTA takes its own block's item, then those of blocks that have
 // not started (the hardware's order, so the load balances itself), and the
 // roles run from one item into the next: while the softmax warps write an
 // item's rows, the next one's keys arrive and its first product is done.
-template <typename T, int DP, int NQ>
+// CL (NQ == 1): the splits of a sequence and key head are a cluster. Each CTA
+// leaves its rows in its shared memory, and the cluster joins them there: no
+// workspace and no second kernel. No CTA takes a second item.
+template <typename T, int DP, int NQ, bool CL>
 __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     paged_attn(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -332,7 +421,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     }
     if (warp == kIssuer) tmem_alloc(tmem_slot, S::kCols);
     if (warp == kProducer) {  // the first item's lengths, on their way while the CTA meets
-        const int b = p.by_seq ? min(lane, p.batch - 1) : (int)blockIdx.x / p.kv_heads % p.batch;
+        const int b = CL         ? (int)blockIdx.x / p.splits / p.kv_heads
+                      : p.by_seq ? min(lane, p.batch - 1)
+                                 : (int)blockIdx.x / p.kv_heads % p.batch;
         prefetch_l1(p.cu_q + b);
         prefetch_l1(p.cu_q + b + 1);
         prefetch_l1(p.kv_lens + b);
@@ -353,6 +444,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t stage0 = sbase + NQ * S::kQBytes;
     const int tt = p.tile_toks;
+    // CL: the rows' partial results, over the ring's stages
+    uint8_t *join_at = smem + NQ * S::kQBytes;
+    float *join_lse = reinterpret_cast<float *>(join_at + S::kQRows * DP * 4);
+    static_assert(!CL || S::kQRows * (DP * 4 + 4) <= S::kStages * S::kStage, "join");
 
     // The n-th item of this CTA, as the producer left it; false: given up.
     auto take = [&](int n, Item &w) {
@@ -425,10 +520,12 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         };
         // The next item with work (this block's own, then those asked for), its
         // first tile looked up; ntiles -1: none.
+        int n = 0;  // items
         auto find_next = [&](Item &i, int &pg, int &pl) {
 #pragma unroll 1
             for (;; ask()) {
                 int id = blockIdx.x;
+                if (CL && n > 0) id = -1;
                 if (asked > 0) {
                     if (!warp_wait(answered, (uint32_t)((asked - 1) & 1))) {
                         ok = false;
@@ -438,7 +535,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                     __syncwarp();
                 }
                 if (id < 0) break;
-                if (decode_item(p, id, NQ * tt, i)) {
+                if (decode_item<CL>(p, id, NQ * tt, i)) {
                     find(i, 0, pg, pl);
                     return;
                 }
@@ -469,7 +566,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
             fix_from = -1;
         };
 
-        int n = 0, q_loads = 0;
+        int q_loads = 0;
 #pragma unroll 1
         for (;; ++n) {
             find_next(w, page, place);
@@ -487,7 +584,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
             // late, so that the blocks left go to whoever is done first, and early
             // enough for the answer (a microsecond) to be there in time.
             const int ask_at = max(2 * (w.ntiles - kAskAhead), 1);
-            if (w.ntiles == 0) ask();
+            if (!CL && w.ntiles == 0) ask();
             int next_page, next_place;
             Ring<NST> last_at;
 #pragma unroll 1
@@ -521,7 +618,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 } else {
                     find(w, (i >> 1) + 1, next_page, next_place);
                 }
-                if (i == ask_at) ask();
+                if (!CL && i == ask_at) ask();
             }
             if (!ok) break;
             if (w.fix) {
@@ -884,8 +981,33 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
             if (!ok) break;
             const float l = l2.x + l2.y;
             const bool none = m == -INFINITY && !(l != l);  // no key seen
-            const float inv = none ? 0.f : 1.f / l;
-            const float lse2 = none ? -INFINITY : m * c + log2f(l);
+            const float inv = none ? 0.f : __fdividef(1.f, l);
+            const float lse2 = none ? -INFINITY : m * c + __log2f(l);
+            if constexpr (CL) {
+                // to this CTA's shared memory, whose K and V are done with: a
+                // row's 16-byte chunks turned by the row, so that the lanes' stores
+                // spread over the banks
+                if (live) join_lse[r] = lse2;
+#pragma unroll 1
+                for (int d = 0; d < p.head_dim; d += 32) {
+                    uint32_t o[32];
+                    if (w.ntiles > 0) {
+                        __syncwarp();
+                        tmem_ld32(to + d, o);
+                        tmem_wait_ld();
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (!none)
+                            v = make_uint4(__float_as_uint(__uint_as_float(o[i]) * inv), __float_as_uint(__uint_as_float(o[i + 1]) * inv),
+                                           __float_as_uint(__uint_as_float(o[i + 2]) * inv), __float_as_uint(__uint_as_float(o[i + 3]) * inv));
+                        sts128(join_at + r * (DP * 4) + (((d + i) / 4 + r) % (DP / 4)) * 16, v);
+                    }
+                }
+                continue;
+            }
             const int head = w.kvh * p.group + row_head;
             const int64_t token = w.q0 + tok, orow = token * p.heads + head, plane = p.tokens * p.heads;
             const bool parts = w.parts;
@@ -966,6 +1088,13 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     if (warp == kIssuer) {
         __syncwarp();
         tmem_dealloc(tmem, S::kCols);
+    }
+    if constexpr (CL) {
+        __syncwarp();
+        cluster_sync();
+        join_cluster<T, DP>(p, items[0], join_at, join_lse);
+        __syncwarp();
+        cluster_sync();  // no CTA ends while another reads its rows
     }
 }
 
@@ -1090,6 +1219,7 @@ static bool tile_stride(int64_t s, int64_t n) { return n <= 1 || (s > 0 && s % 8
 // How a call is cut: the geometry, the row tiles and the splits over keys.
 struct AttnCut {
     int nq, tile_toks, q_tiles, splits, chunk;
+    bool cluster;  // the splits of a row are a cluster
     size_t workspace;
 };
 
@@ -1109,14 +1239,22 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
     const int64_t tiles = ((int64_t)c.max_kv + kKeyTile - 1) / kKeyTile;
     k.splits = 1;
     k.chunk = 0;
+    k.cluster = false;
     if (ctas < slots && tiles > 1) {
         int64_t want = slots / ctas;
         const int64_t least = 2;  // key tiles a split is worth
         if (want > tiles / least) want = tiles / least;
         if (want > 1) {
-            const int64_t per_split = (tiles + want - 1) / want;
+            int64_t per_split = (tiles + want - 1) / want;
+            // A cluster (at most eight CTAs everywhere) joins its splits itself;
+            // otherwise a second kernel does, which takes as long as a few key
+            // tiles.
+            const int64_t per_eight = (tiles + 7) / 8;
+            k.cluster = k.nq == 1 && per_eight - per_split <= kJoinTiles;
+            if (k.cluster && per_split < per_eight) per_split = per_eight;
             k.splits = (int)((tiles + per_split - 1) / per_split);
             k.chunk = (int)(per_split * kKeyTile);
+            if (k.splits < 2) k.cluster = false;
         }
     } else if (k.nq == 1 && ctas < 4 * slots && tiles >= 2 * kDecodeChunk) {
         // A few items a CTA: shorter ones let the CTAs end together (64
@@ -1127,7 +1265,7 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
         k.chunk = kDecodeChunk * kKeyTile;
     }
     k.workspace = 0;
-    if (k.splits > 1) {
+    if (k.splits > 1 && !k.cluster) {
         const size_t r = (size_t)c.tokens * c.q_heads * k.splits;
         k.workspace = ((r * c.head_dim * 4 + 255) / 256 + (r * 4 + 255) / 256) * 256;
     }
@@ -1146,21 +1284,25 @@ static rmsnorm_status_t attn_sizes(const paged_attn_call_t &c) {
     return RMSNORM_SUCCESS;
 }
 
-template <typename T, int DP, int NQ>
+template <typename T, int DP, int NQ, bool CL>
 static int launch_attn(const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t stream) {
     using S = AttnShape<DP, NQ>;
-    auto *kernel = paged_attn<T, DP, NQ>;
+    auto *kernel = paged_attn<T, DP, NQ, CL>;
     const int e = allow_staged_smem(reinterpret_cast<const void *>(kernel));
     if (e != 0) return e;
-    LaunchCfg lc(grid, S::kThreads, S::kSmem, stream);
+    LaunchCfg lc(grid, S::kThreads, S::kSmem, stream, CL ? (unsigned)p.splits : 0);
     return (int)cudaLaunchKernelEx(&lc.cfg, kernel, p, maps[0], maps[1], maps[2]);
 }
 
+template <typename T, int DP>
+static int launch_attn_d(const AttnCut &k, const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t s) {
+    if (k.nq == 2) return launch_attn<T, DP, 2, false>(p, maps, grid, s);
+    return k.cluster ? launch_attn<T, DP, 1, true>(p, maps, grid, s) : launch_attn<T, DP, 1, false>(p, maps, grid, s);
+}
+
 template <typename T>
-static int launch_attn_t(int nq, const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t s) {
-    if (p.head_dim > 64)
-        return nq == 2 ? launch_attn<T, 128, 2>(p, maps, grid, s) : launch_attn<T, 128, 1>(p, maps, grid, s);
-    return nq == 2 ? launch_attn<T, 64, 2>(p, maps, grid, s) : launch_attn<T, 64, 1>(p, maps, grid, s);
+static int launch_attn_t(const AttnCut &k, const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t s) {
+    return p.head_dim > 64 ? launch_attn_d<T, 128>(k, p, maps, grid, s) : launch_attn_d<T, 64>(k, p, maps, grid, s);
 }
 
 static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t stream) {
@@ -1248,7 +1390,7 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     p.chunk = cut.chunk;
     p.tile_toks = cut.tile_toks;
     p.nq = cut.nq;
-    p.by_seq = c.batch > 1 && c.batch <= 32 && cc.max_kv / 2 >= c.max_q;
+    p.by_seq = !cut.cluster && c.batch > 1 && c.batch <= 32 && cc.max_kv / 2 >= c.max_q;
     // (a group's heads share a box: their stride counts even for one key head)
     if (!empty && on(c.q, 16) && tile_stride(c.q_head, c.q_heads) && tile_stride(c.q_token, c.tokens))
         p.q_tma = tile_map(&maps[0], c.dtype, c.q, c.head_dim, {p.group, pc.heads, c.tokens},
@@ -1264,9 +1406,9 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     if (grid > 0x7fffffffLL || join > 0x7fffffffLL) {
         st = RMSNORM_ERR_UNSUPPORTED;
     } else {
-        le = c.dtype == RMSNORM_BF16 ? launch_attn_t<__nv_bfloat16>(cut.nq, p, maps, (unsigned)grid, stream)
-                                     : launch_attn_t<__half>(cut.nq, p, maps, (unsigned)grid, stream);
-        if (le == 0 && cut.splits > 1) {
+        le = c.dtype == RMSNORM_BF16 ? launch_attn_t<__nv_bfloat16>(cut, p, maps, (unsigned)grid, stream)
+                                     : launch_attn_t<__half>(cut, p, maps, (unsigned)grid, stream);
+        if (le == 0 && cut.splits > 1 && !cut.cluster) {
             LaunchCfg lc((unsigned)join, 128, 0, stream);
             le = c.dtype == RMSNORM_BF16 ? (int)cudaLaunchKernelEx(&lc.cfg, paged_attn_join<__nv_bfloat16>, p)
                                          : (int)cudaLaunchKernelEx(&lc.cfg, paged_attn_join<__half>, p);
