@@ -42,6 +42,7 @@ namespace rmsn {
 
 constexpr int kKeyTile = 128;
 constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kernel gives up
+constexpr int kClusterMost = 16;           // CTAs of a cluster (over 8: by opt-in)
 constexpr int kJoinTiles = 4;              // key tiles that the join's kernel takes as long as
 constexpr int kDecodeChunk = 16;           // key tiles of a decoding item, where there are several a CTA
 constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
@@ -306,28 +307,27 @@ __device__ __forceinline__ float4 ld_cluster4(const void *local, uint32_t cta) {
 // their order; four values a thread, the rows' chunks dealt to the CTAs.
 template <typename T, int DP>
 __device__ __forceinline__ void join_cluster(const AttnParams &p, const Item &w, const uint8_t *rows, const float *lse) {
-    constexpr int kMost = 8;  // CTAs of a cluster
     const int chunks = p.head_dim / 4, total = w.toks * p.group * chunks;
     const int rank = (int)cluster_ctarank(), splits = p.splits;
     for (int i = rank * (int)blockDim.x + (int)threadIdx.x; i < total; i += splits * (int)blockDim.x) {
         const int r = i / chunks, c = i - r * chunks;
-        float l[kMost], top = -INFINITY, sum = 0.f;
-        float4 v[kMost];
+        float l[kClusterMost], top = -INFINITY, sum = 0.f;
+        float4 v[kClusterMost];
 #pragma unroll
-        for (int s = 0; s < kMost; ++s) {
+        for (int s = 0; s < kClusterMost; ++s) {
             if (s >= splits) break;
             l[s] = ld_cluster(lse + r, (uint32_t)s);
             v[s] = ld_cluster4(rows + r * (DP * 4) + ((c + r) % (DP / 4)) * 16, (uint32_t)s);
         }
 #pragma unroll
-        for (int s = 0; s < kMost; ++s) {
+        for (int s = 0; s < kClusterMost; ++s) {
             if (s >= splits) break;
             top = l[s] != l[s] || top != top ? NAN : fmaxf(top, l[s]);
         }
         const bool none = top == -INFINITY;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int s = 0; s < kMost; ++s) {
+        for (int s = 0; s < kClusterMost; ++s) {
             if (s >= splits) break;
             const float e = exp2_approx(l[s] - (none ? 0.f : top));
             sum += e;
@@ -1246,12 +1246,15 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
         if (want > tiles / least) want = tiles / least;
         if (want > 1) {
             int64_t per_split = (tiles + want - 1) / want;
-            // A cluster (at most eight CTAs everywhere) joins its splits itself;
-            // otherwise a second kernel does, which takes as long as a few key
-            // tiles.
-            const int64_t per_eight = (tiles + 7) / 8;
-            k.cluster = k.nq == 1 && per_eight - per_split <= kJoinTiles;
-            if (k.cluster && per_split < per_eight) per_split = per_eight;
+            // A cluster joins its splits itself; otherwise a second kernel does,
+            // which takes as long as a few key tiles. A cluster lies in one of
+            // eight parts of the device, two CTAs an SM; its size is such that
+            // they all fit at once.
+            int64_t size = kClusterMost;
+            while (size > 1 && 8 * (sms / 4 / size) < ctas) --size;
+            const int64_t per_cluster = (tiles + size - 1) / size;
+            k.cluster = k.nq == 1 && size > 1 && per_cluster - per_split <= kJoinTiles;
+            if (k.cluster && per_split < per_cluster) per_split = per_cluster;
             k.splits = (int)((tiles + per_split - 1) / per_split);
             k.chunk = (int)(per_split * kKeyTile);
             if (k.splits < 2) k.cluster = false;
@@ -1290,6 +1293,13 @@ static int launch_attn(const AttnParams &p, const CUtensorMap (&maps)[3], unsign
     auto *kernel = paged_attn<T, DP, NQ, CL>;
     const int e = allow_staged_smem(reinterpret_cast<const void *>(kernel));
     if (e != 0) return e;
+    if (CL && p.splits > 8) {
+        const cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (ce != cudaSuccess) {
+            (void)cudaGetLastError();
+            return (int)ce;
+        }
+    }
     LaunchCfg lc(grid, S::kThreads, S::kSmem, stream, CL ? (unsigned)p.splits : 0);
     return (int)cudaLaunchKernelEx(&lc.cfg, kernel, p, maps[0], maps[1], maps[2]);
 }
