@@ -405,6 +405,28 @@ def test_attention(rn, dt, nq, lens, hq, hk, D, page, causal):
     check_attention(rn, q, kc, vc, table, ln, nq, causal)
 
 
+@pytest.mark.parametrize("nq,lens,hq,hk,D,page", [
+    ([1], [20011], 4, 1, 128, 16),                               # more splits than a cluster has: joined by a kernel
+    ([2, 1], [9000, 16500], 2, 1, 64, 32),
+    ([1] * 40, [5000 - 97 * i for i in range(40)], 16, 8, 64, 16),   # several items a CTA, 40 sequences
+    ([1, 3, 0, 2] * 5, [4200, 17, 900, 5001] * 5, 32, 16, 64, 8),    # in the order of their lengths, one without tokens
+    ([300, 0, 70, 129, 1], [2100, 40, 3333, 1000, 1], 8, 4, 128, 8),  # the same with row tiles, small pages
+    ([1500, 700], [1500, 700], 32, 16, 64, 24),                  # several row tiles a CTA, pages that end inside a tile
+    ([700], [900], 10, 10, 96, 16),
+    ([33, 5], [4000, 2500], 5, 5, 128, 64),                      # row tiles whose keys are split
+])
+def test_attention_many_items(rn, nq, lens, hq, hk, D, page):
+    """Every way of cutting the work: clusters, splits joined by a kernel, items
+    handed from CTA to CTA, row tiles that one split holds beside ones that are
+    split."""
+    g = gen(sum(nq) + D)
+    kc, vc, table, ln = paged(g, lens, page, hk, D, torch.bfloat16, fill=float("nan"))
+    q = normal(g, sum(nq), hq, D, dt=torch.bfloat16)
+    a, _ = check_attention(rn, q, kc, vc, table, ln, nq)
+    b = rn.paged_attn_fwd(q, kc, vc, table, ln, starts(nq), max_q=max(nq), max_kv=max(lens))[0]
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("nq,lens,page", [([1, 1], [77, 1030], 16), ([1], [3], 256), ([200, 9], [205, 130], 48),
                                           ([1], [0], 8)])
