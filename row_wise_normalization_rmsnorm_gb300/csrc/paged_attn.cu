@@ -974,11 +974,13 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 }
             }
             // ------------------------------------------------------ results
-            if (ok && w.ntiles > 0) {
-                ok = warp_wait(o_done + t, (uint32_t)((steps - 1) & 1));
-                tc_after_sync();
-            }
             if (!ok) break;
+            auto o_ready = [&]() {
+                if (w.ntiles == 0) return true;
+                if (!warp_wait(o_done + t, (uint32_t)((steps - 1) & 1))) return false;
+                tc_after_sync();
+                return true;
+            };
             const float l = l2.x + l2.y;
             const bool none = m == -INFINITY && !(l != l);  // no key seen
             const float inv = none ? 0.f : __fdividef(1.f, l);
@@ -988,6 +990,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 // row's 16-byte chunks turned by the row, so that the lanes' stores
                 // spread over the banks
                 if (live) join_lse[r] = lse2;
+                if (!(ok = o_ready())) break;
 #pragma unroll 1
                 for (int d = 0; d < p.head_dim; d += 32) {
                     uint32_t o[32];
@@ -1028,18 +1031,21 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(live ? dst : nullptr), (lane & 28) + k);
                 rows4[k] = reinterpret_cast<char *>(a);
             }
-            // (rolled loops: unrolled, the code's fetches took longer than the work)
             const int cols = p.head_dim;
-#pragma unroll 1
-            for (int d = 0; d < cols; d += 32) {
-                uint32_t o[32];
-                if (w.ntiles > 0) {
-                    __syncwarp();
-                    tmem_ld32(to + d, o);
-                    tmem_wait_ld();
-                }
+            const bool any_none = __any_sync(0xffffffffu, none);
+            const float2 inv2 = make_float2(inv, inv);
+            // 32 columns in registers: scaled, and to the rows
+            auto put = [&](uint32_t (&o)[32], int d) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 v = PR::mul(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), inv2);
+                    o[i] = __float_as_uint(v.x);
+                    o[i + 1] = __float_as_uint(v.y);
+                }
+                if (any_none) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = none ? 0u : o[i];
+                }
                 uint4 ck[4];
                 if (parts) {  // fp32: two blocks of 16 values
 #pragma unroll
@@ -1075,6 +1081,18 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                             store_halves(reinterpret_cast<uint16_t *>(rows4[k]) + at, ck[k]);
                     }
                 }
+            };
+            if (!(ok = o_ready())) break;
+            // (rolled: unrolled further, the code's fetches took longer than the work)
+#pragma unroll 1
+            for (int d = 0; d < cols; d += 64) {
+                uint32_t oa[32], ob[32];
+                __syncwarp();
+                tmem_ld32(to + d, oa);
+                tmem_ld32(to + d + 32, ob);
+                tmem_wait_ld();
+                put(oa, d);
+                put(ob, d + 32);
             }
             // (o is read before the next item's first product, which waits for
             // this warp's next p)
