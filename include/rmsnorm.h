@@ -449,7 +449,7 @@ typedef struct {
  * no key gets o = 0 and lse = -inf. Rows of q behind the last sequence are
  * not written. Products of the storage type with fp32 sums; the softmax in
  * fp32, its weights rounded to the storage type for the second product;
- * o rounded once.
+ * o rounded once. out may equal q (the same strides); nothing else overlaps.
  *
  * What lies in the cache past a sequence's length never reaches its rows,
  * infinities and NaN included. A key that later rows of the same sequence
@@ -461,10 +461,13 @@ typedef struct {
  *
  * UNSUPPORTED: head_dim not a multiple of 8 or above 128, page_size not a
  * multiple of 8, more than 128 query heads a key head, cache base or strides
- * not on 16-byte boundaries.
+ * not on 16-byte boundaries, fp32. q, out and lse take any strides and
+ * alignment (q on 16-byte boundaries is copied faster).
  * workspace: as for rmsnorm_bwd; paged_attn_workspace_bytes gives its size
- * (0 where the work is not split over the keys). Each row's sum has a fixed
- * order: the same call gives the same bits.
+ * (0 where none is used). How the work is cut depends on the call's sizes and
+ * the device alone, and each row's sum has a fixed order: the same call gives
+ * the same bits. Captured into a graph, a call reads the lengths, the table and
+ * the cache anew at each replay.
  */
 rmsnorm_status_t paged_attn_fwd(const paged_attn_call_t *call, rmsnorm_stream_t stream);
 

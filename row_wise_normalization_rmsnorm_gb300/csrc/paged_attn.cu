@@ -14,19 +14,30 @@
 // token * group + head in group), so a decoding step reads each key once
 // for all of them.
 //
-// Two geometries (NQ tiles of 128 rows a CTA):
-//  NQ = 2, prompts and chunks: 256 rows a CTA and one CTA an SM. Bound by
-//    the matrix instructions; while the softmax of one tile runs, the other
-//    tile's two products do.
-//  NQ = 1, few rows (decoding): at most 64 rows, two CTAs an SM, the keys
-//    split over CTAs where there are too few of them. Bound by the cache's
-//    bytes; the two CTAs cover each other's latencies.
+// Geometries (NQ row tiles a CTA):
+//  NQ = 2, prompts and chunks: two tiles of 128 rows, one CTA an SM. While the
+//    softmax of one tile runs, the other tile's two products do. Bound by the
+//    matrix instructions and, over seconds, the power limit: 4864 tokens of 32
+//    heads over 32768 keys, D 128, run at 1.82 PFLOP/s (a library product of
+//    8192^3: 1.89 in a burst, 1.72 sustained), prompts of 2 x 8192 at 1.54 to
+//    1.69. A key tile's shared-memory traffic (q and k read by the first
+//    product, v by the second, k and v written) fills the same time.
+//  NQ = 1, at most 64 rows (decoding): two CTAs an SM, which cover each other's
+//    latencies. Bound by the cache's bytes: 64 sequences of 964 to 8192 keys
+//    at 6.2 TB/s, of 8192 each at 7.0.
 //
-// Roles: four warps a tile for the softmax (a thread owns a row: no
-// shuffles), one warp copying K and V tiles (one TMA box a page, or part of
-// a page), one thread issuing matrix instructions. S and p share tensor
-// memory (p, as the 16-bit A operand of the second product, overwrites s);
-// o accumulates in tensor memory.
+// Few items leave SMs idle, so the keys of a row are split: over the CTAs of a
+// cluster that joins them in shared memory (NQ = 1, up to 16), or over items
+// whose partial results a second kernel joins. One sequence of 4095 keys, 8 key
+// heads: 54 us unsplit, 15.4 with the join's kernel, 11.7 as clusters. What
+// remains of a small call is latency: the lengths, the table, the first tile,
+// two dependent products and the launch, about 10 us together.
+//
+// Roles: four warps a tile for the softmax (a thread owns a row: no shuffles),
+// one to three warps copying K and V tiles (one box a page, or part of a page),
+// one warp issuing matrix instructions. s and p share tensor memory (p, as the
+// 16-bit A operand of the second product, overwrites s); o accumulates in
+// tensor memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1302,6 +1313,7 @@ static rmsnorm_status_t attn_sizes(const paged_attn_call_t &c) {
         return RMSNORM_ERR_INVALID_ARG;
     if (c.head_dim % 8 != 0 || c.head_dim > 128 || c.q_heads / c.cache.heads > 128) return RMSNORM_ERR_UNSUPPORTED;
     if ((int64_t)c.max_q * (c.q_heads / c.cache.heads) > 0x3fffffffLL) return RMSNORM_ERR_UNSUPPORTED;
+    if (c.max_kv > 0x7fffffff - 2 * kKeyTile) return RMSNORM_ERR_UNSUPPORTED;  // a tile's keys are counted in 32 bits
     return RMSNORM_SUCCESS;
 }
 
@@ -1336,7 +1348,8 @@ static int launch_attn_t(const AttnCut &k, const AttnParams &p, const CUtensorMa
 static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t stream) {
     rmsnorm_status_t st = attn_sizes(c);
     if (st != RMSNORM_SUCCESS) return st;
-    if (!std::isfinite(c.scale) || c.scale <= 0.f) return RMSNORM_ERR_INVALID_ARG;
+    const float log2_scale = c.scale * 1.44269504088896340736f;
+    if (!std::isfinite(log2_scale) || !(log2_scale > 0.f)) return RMSNORM_ERR_INVALID_ARG;
     const paged_cache_t &pc = c.cache;
     if (pc.page_size < 1 || pc.pages < 0 || pc.pages > 0x7ffffffeLL) return RMSNORM_ERR_INVALID_ARG;
     if (pc.page_size % 8 != 0) return RMSNORM_ERR_UNSUPPORTED;
@@ -1401,7 +1414,7 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     p.table_stride = stride_of(c.table_stride, c.batch);
     p.tokens = c.tokens;
     p.status = status;
-    p.c = c.scale * 1.44269504088896340736f;
+    p.c = log2_scale;
     p.batch = c.batch;
     p.width = empty ? 0 : c.table_width;
     p.heads = c.q_heads;
@@ -1431,12 +1444,13 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     const int64_t grid = (int64_t)c.batch * pc.heads * cut.q_tiles * cut.splits;
     const int64_t join = ((int64_t)c.batch * c.max_q * c.q_heads + 3) / 4;
     int le = 0;
-    if (grid > 0x7fffffffLL || join > 0x7fffffffLL) {
+    const bool joins = cut.splits > 1 && !cut.cluster;
+    if (grid > 0x7fffffffLL || (joins && join > 0x7fffffffLL)) {
         st = RMSNORM_ERR_UNSUPPORTED;
     } else {
         le = c.dtype == RMSNORM_BF16 ? launch_attn_t<__nv_bfloat16>(cut, p, maps, (unsigned)grid, stream)
                                      : launch_attn_t<__half>(cut, p, maps, (unsigned)grid, stream);
-        if (le == 0 && cut.splits > 1 && !cut.cluster) {
+        if (le == 0 && joins) {
             LaunchCfg lc((unsigned)join, 128, 0, stream);
             le = c.dtype == RMSNORM_BF16 ? (int)cudaLaunchKernelEx(&lc.cfg, paged_attn_join<__nv_bfloat16>, p)
                                          : (int)cudaLaunchKernelEx(&lc.cfg, paged_attn_join<__half>, p);

@@ -595,6 +595,74 @@ def test_attention_same_bits_stream_workspace_and_graph(rn, nq, lens):
     assert torch.equal(captured, rn.paged_attn_fwd(q, kc, vc, table, ln, cu, **kw)[0])
 
 
+@pytest.mark.parametrize("nq,lens", [([1, 2], [3000, 77]), ([150, 64], [900, 64]), ([60], [3000])])
+def test_attention_in_place(rn, nq, lens):
+    """out may be q."""
+    g = gen(21)
+    kc, vc, table, ln = paged(g, lens, 16, 2, 128, torch.bfloat16)
+    q = normal(g, sum(nq), 8, 128, dt=torch.bfloat16)
+    kw = dict(max_q=max(nq), max_kv=max(lens))
+    a = rn.paged_attn_fwd(q, kc, vc, table, ln, starts(nq), **kw)[0]
+    rn.paged_attn_fwd(q, kc, vc, table, ln, starts(nq), out=q, **kw)
+    assert torch.equal(q, a)
+
+
+def test_calls_on_two_streams_at_once(rn):
+    """Attention with a join's workspace and appends on two streams, many times
+    over, each with its own results."""
+    g = gen(22)
+    sides = []
+    for i in range(2):
+        lens = [20011 + 999 * i]
+        kc, vc, table, ln = paged(g, lens, 16, 1, 64, torch.bfloat16)
+        q = normal(g, 1, 4, 64, dt=torch.bfloat16)
+        sides.append((torch.cuda.Stream(), q, kc, vc, table, ln, max(lens), []))
+    want = [rn.paged_attn_fwd(q, kc, vc, t, ln, starts([1]), max_q=1, max_kv=m)[0]
+            for _, q, kc, vc, t, ln, m, _ in sides]
+    cu = starts([1])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, q, kc, vc, t, ln, m, got in sides:
+            with torch.cuda.stream(s):
+                got.append(rn.paged_attn_fwd(q, kc, vc, t, ln, cu, max_q=1, max_kv=m)[0])
+    torch.cuda.synchronize()
+    for w, side in zip(want, sides):
+        assert all(torch.equal(w, x) for x in side[-1])
+
+
+def test_append_and_rope_in_a_graph(rn):
+    g = gen(23)
+    T, H, D = 33, 4, 64
+    q, k, v = (normal(g, T, H, D, dt=torch.float16) for _ in range(3))
+    kc, vc = (torch.zeros(8, 8, H, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    slots, pos, f = torch.arange(T, device="cuda"), torch.arange(T, device="cuda").int(), freqs(32)
+
+    def run():
+        r, _ = rn.rope_fwd(q, None, pos, f)
+        b, _ = rn.rope_bwd(r, None, pos, f)
+        a = rn.paged_kv_append(k, v, kc, vc, slots, pos, f, q=q)
+        return r, b, a
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r, b, a = run()
+    q.copy_(normal(g, T, H, D, dt=torch.float16))
+    k.copy_(normal(g, T, H, D, dt=torch.float16))
+    pos.add_(1000)
+    slots.copy_(torch.arange(T, device="cuda").flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r, a)
+    want = [x.clone() for x in (r, kc, vc)]
+    run()
+    torch.cuda.synchronize()
+    assert torch.equal(rn.rope_fwd(q, None, pos, f)[0], want[0])
+    assert torch.equal(kc, want[1]) and torch.equal(vc, want[2])
+    near(b, q.double(), 8 * half_step(torch.float16) * (q.double().abs() + q.double().abs().roll(D // 2, -1)))
+
+
 def test_attention_refusals(rn):
     g = gen(19)
     kc, vc, table, ln = paged(g, [20], 16, 2, 64, torch.bfloat16)

@@ -150,7 +150,7 @@ def attn_call(**kw):
     ({"q_heads": 0}, INVALID), ({"q_heads": 258}, UNSUPPORTED), ({"cache__heads": 0}, INVALID), ({"batch": -1}, INVALID),
     ({"tokens": -1}, INVALID), ({"max_q": -1}, INVALID), ({"max_kv": -1}, INVALID), ({"table_width": -1}, INVALID),
     ({"scale": 0.0}, INVALID), ({"scale": -1.0}, INVALID), ({"scale": float("nan")}, INVALID),
-    ({"scale": float("inf")}, INVALID), ({"cache__page_size": 0}, INVALID), ({"cache__page_size": 12}, UNSUPPORTED),
+    ({"scale": float("inf")}, INVALID), ({"scale": 3e38}, INVALID), ({"max_kv": 2 ** 31 - 1}, UNSUPPORTED), ({"cache__page_size": 0}, INVALID), ({"cache__page_size": 12}, UNSUPPORTED),
     ({"cache__pages": -1}, INVALID), ({"q": None}, INVALID), ({"out": None}, INVALID), ({"q": A + 1}, INVALID),
     ({"lse": A + 2}, INVALID), ({"kv_lens": None}, INVALID), ({"cu_q": None}, INVALID), ({"block_table": None}, INVALID),
     ({"kv_lens": A + 2}, INVALID), ({"cache__k": None}, INVALID), ({"cache__k": A + 2}, UNSUPPORTED),
