@@ -87,7 +87,7 @@ def _link_ext(obj: str) -> None:
     t = os.path.join(_torch_dir(), "lib")
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + t,
-           "-Wl,-rpath," + t, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-Wl,-rpath," + t, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of heads_ext failed:\n{r.stdout}\n{r.stderr}")
