@@ -10,11 +10,15 @@
 //
 // What bounds it: memory. Every value is read once and written once, at a
 // few fp32 operations a value; the angles are shared by all heads of a
-// token. So a warp takes one token: a lane keeps the cos and sin of one
-// 16-byte chunk's frequencies in registers and walks the heads, a group of
-// lanes a head, with several heads' loads in flight. The warp computes each
-// angle once (two a lane for 64 frequencies) and hands them round in shared
-// memory. With few tokens the heads are split over more warps.
+// token. So a warp takes one token and walks its heads, a group of lanes a
+// head, the next heads' chunks on their way into shared memory by asynchronous
+// copies (each lane reads back what it asked for: no barrier). The warp
+// computes each angle once (two a lane for 64 frequencies) and hands them round
+// in shared memory. With few tokens the heads are split over more warps.
+// Measured (of 6770 GB/s, the copy rate): 16384 tokens of 40 heads by 128, bf16,
+// 53.6 us, 93%; the append of 8192 tokens of 48 heads with their norm 37.4 us,
+// 80%; the gradient of 4096 tokens 19 us, 65%: one wave of warps, whose latency
+// is what is left there.
 #include <cmath>
 #include <cstring>
 
@@ -148,21 +152,33 @@ __device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w,
 // the values that pass unturned.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
-// Heads a lane has in flight, and CTAs an SM that the registers are held to:
-// 3 and 5 measured best together (bf16 16384 tokens of 40 heads by 128:
-// 58.5 us against 59.3 with 4 and 4, 65.7 with 2 and 5, 60.0 with 2 and 7;
-// the append of 8192 tokens of 48 heads with its norm 39.9 us against 42.1,
-// 42.7 and 42.5).
-constexpr int kRopeUnroll = 3;
-constexpr int kRopeCtas = 5;
+// Heads of a batch, batches under way, and the CTAs an SM that the registers
+// are held to, without and with the norm. Measured together (bf16, 16384 tokens
+// of 40 heads by 128, and the append of 8192 tokens of 48 with its norm): 53.6
+// and 37.4 us; one batch of three heads in registers instead 58.5 and 40.3; four
+// batches 55.7 and 38.9; six CTAs for the norm too spill, 43.4.
+constexpr int kRopeUnroll = 2;
+constexpr int kRopeDepth = 3;
+constexpr int kRopeCtas[2] = {6, 5};
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the thread's newest N groups of copies have landed.
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // FULL: every lane has two chunks of every head (head_dim = 2 E lanes a head,
 // e.g. 64, 128 or 256 values of 16 bits), so nothing is tested a chunk.
 template <typename T, bool APPEND, bool NORM, bool ADJ, bool FULL>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_vector(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(const __grid_constant__ RopeParams p) {
     constexpr int E = Elem<T>::E, NP = Elem<T>::NP, U = kRopeUnroll;
     using PR = Pair<true>;
     __shared__ float2 turn[kRopeWarps][HEAD_MAX_DIM / 2];  // (cos, sin) of the warp's token
+    constexpr int kDepth = kRopeDepth;
+    __shared__ __align__(16) uint4 places[kRopeWarps][kRopeDepth * kRopeUnroll * 64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp;
     pdl_wait();
@@ -186,60 +202,88 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_vector(const __g
     const bool has0 = FULL || e0 < p.head_dim, has1 = FULL || e1 < p.head_dim;
     const int b0 = e0 * (int)sizeof(T), b1 = e1 * (int)sizeof(T);
 
+    // The heads of this block, segment by segment, in batches of U a group of
+    // lanes. A lane's chunks of the next kDepth batches are on their way into
+    // its own places in shared memory (copies that hold no registers), across
+    // the segments' ends.
+    constexpr int kSegs = APPEND ? 3 : 2;
+    int hb[kSegs], he[kSegs];
+    {
+        int first = 0;
+#pragma unroll
+        for (int sg = 0; sg < kSegs; ++sg) {
+            hb[sg] = max(h0 - first, 0);
+            he[sg] = min(h1 - first, p.seg[sg].heads);
+            first += p.seg[sg].heads;
+        }
+    }
+    uint4 *mine = places[warp] + lane;  // [kDepth][U][2], 32 apart
+    int nsg = 0, nh = hb[0], slot = 0;  // the next batch to ask for; the next place
+    auto ask = [&](int at) {
+#pragma unroll
+        for (int sg = 0; sg < kSegs; ++sg) {
+            if (nsg != sg) continue;
+            if (nh >= he[sg]) {  // (an empty segment too)
+                ++nsg;
+                if (sg + 1 < kSegs) nh = hb[sg + 1];
+                continue;
+            }
+            const HeadSeg &g = p.seg[sg];
+            const char *in = g.in + t * g.in_token;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = nh + u * step + grp;
+                if (h < he[sg]) {
+                    const char *row = in + h * g.in_head;
+                    uint4 *to = mine + (at * U + u) * 64;
+                    if (has0) cp_async16(to, row + b0);
+                    if (has1) cp_async16(to + 32, row + b1);
+                }
+            }
+            nh += U * step;
+            break;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) ask(k);
+
     int64_t page = 0;
     int place = 0;
     if (APPEND) find_slot(p, t, page, place);
+    if (h0 < p.seg[0].heads + p.seg[1].heads) {
+        for (int i = lane; i < p.half_dim; i += 32) {
+            float c, s;
+            angles_of<1>(p, t, i, &c, &s);
+            turn[warp][i] = make_float2(c, s);
+        }
+        __syncwarp();
+    }
 
-    // The segments' heads in this block, one segment after the other.
-    int first = 0;
 #pragma unroll
-    for (int sg = 0; sg < (APPEND ? 3 : 2); ++sg) {
+    for (int sg = 0; sg < kSegs; ++sg) {
+        if (hb[sg] >= he[sg]) continue;
         const HeadSeg &g = p.seg[sg];
-        const int hb = max(h0 - first, 0), he = min(h1 - first, g.heads);
-        first += g.heads;
         const bool cached = APPEND && sg > 0;
-        const char *in = g.in + t * g.in_token;
         char *out = cached ? g.out + page * g.out_token + place * g.out_slot : g.out + t * g.out_token;
         const bool kept = !cached || page >= 0;
-        uint4 x0[U], x1[U];
-        auto load = [&](int h) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hh = h + u * step;
-                if (!FULL) x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
-                if (hh < he) {
-                    const char *row = in + hh * g.in_head;
-                    if (has0) x0[u] = ld_stream(reinterpret_cast<const uint4 *>(row + b0));
-                    if (has1) x1[u] = ld_stream(reinterpret_cast<const uint4 *>(row + b1));
-                }
-            }
-        };
-        if (sg == 0) load(hb + grp);  // in flight while the angles are computed
-        if (sg == 0 && h0 < p.seg[0].heads + p.seg[1].heads) {
-            for (int i = lane; i < p.half_dim; i += 32) {
-                float c, s;
-                angles_of<1>(p, t, i, &c, &s);
-                turn[warp][i] = make_float2(c, s);
-            }
-            __syncwarp();
-        }
-        if (hb >= he) continue;
-        if (sg > 0) load(hb + grp);
 
         if (APPEND && sg == 2) {  // v: copied
-            for (int h = hb + grp;;) {
+#pragma unroll 1
+            for (int h = hb[sg]; h < he[sg]; h += U * step) {
+                cp_async_wait<kDepth - 1>();
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int hh = h + u * step;
-                    if (hh < he && kept) {
+                    const int hh = h + u * step + grp;
+                    if (hh < he[sg] && kept) {
+                        const uint4 *from = mine + (slot * U + u) * 64;
                         char *row = out + hh * g.out_head;
-                        if (has0) *reinterpret_cast<uint4 *>(row + b0) = x0[u];
-                        if (has1) *reinterpret_cast<uint4 *>(row + b1) = x1[u];
+                        if (has0) *reinterpret_cast<uint4 *>(row + b0) = lds128(from);
+                        if (has1) *reinterpret_cast<uint4 *>(row + b1) = lds128(from + 32);
                     }
                 }
-                h += U * step;
-                if (h - grp >= he) break;
-                load(h);
+                ask(slot);
+                slot = slot + 1 == kDepth ? 0 : slot + 1;
             }
             continue;
         }
@@ -288,10 +332,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_vector(const __g
             }
         }
         const bool raw = !turns && !(NORM && w);
-        for (int h = hb + grp;;) {
+#pragma unroll 1
+        for (int h = hb[sg]; h < he[sg]; h += U * step) {
+            cp_async_wait<kDepth - 1>();
+            uint4 x0[U], x1[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int hh = h + u * step;
+                const uint4 *from = mine + (slot * U + u) * 64;
+                x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
+                if (FULL || has0) x0[u] = lds128(from);
+                if (FULL || has1) x1[u] = lds128(from + 32);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int hh = h + u * step + grp;
                 float2 a[NP], b[NP];
                 unpack<T>(x0[u], a);
                 unpack<T>(x1[u], b);
@@ -305,7 +359,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_vector(const __g
                     const float r = rsqrtf(__fmaf_rn(ss, p.inv_n, p.eps));
                     r2 = make_float2(r, r);
                 }
-                if (hh >= he || !kept) continue;
+                if (hh >= he[sg] || !kept) continue;
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
                     float2 y0, y1;
@@ -327,9 +381,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_vector(const __g
                 if (has0) *reinterpret_cast<uint4 *>(row + b0) = raw ? x0[u] : pack<T>(a);
                 if (has1) *reinterpret_cast<uint4 *>(row + b1) = raw ? x1[u] : pack<T>(b);
             }
-            h += U * step;
-            if (h - grp >= he) break;
-            load(h);
+            // (the values read above have been used, so their places are free)
+            ask(slot);
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
         }
     }
 }
