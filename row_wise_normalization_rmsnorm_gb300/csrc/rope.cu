@@ -134,22 +134,76 @@ __device__ __forceinline__ void find_slot(const RopeParams &p, int64_t t, int64_
     }
 }
 
-// Norm weight values of the chunk at element e.
-template <typename T>
-__device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w, int e, float2 (&f)[Elem<T>::NP]) {
-    if (std::is_same<T, float>::value || !p.w32) {
-        load_w_chunk<T, T>(w, e / Elem<T>::E, f);
-    } else if constexpr (!std::is_same<T, float>::value) {
-        load_w_chunk<T, float>(w, e / Elem<T>::E, f);
-    }
+// ------------------------------------------------------------- chunks --
+// A lane's unit of a row: V values in 16 bytes, or in 8 where rows are not
+// whole 16-byte chunks (a half of 36 values of 16 bits).
+template <typename T, int V> struct Chunk {
+    static constexpr int W = V * (int)sizeof(T) / 4;  // words
+    uint32_t w[W];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int q = 0; q < Elem<T>::NP; ++q) f[q] = make_float2(p.offset + f[q].x, p.offset + f[q].y);
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void from_shared(const void *p) {
+        if constexpr (W == 4) {
+            const uint4 v = lds128(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(smem_u32(p)));
+        }
+    }
+    __device__ __forceinline__ void to_global(void *p) const {
+        if constexpr (W == 4)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+    __device__ __forceinline__ void unpack(float2 (&f)[V / 2]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (std::is_same<T, float>::value)
+                f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            else if constexpr (std::is_same<T, __half>::value)
+                f[i] = f16x2_to_f2(w[i]);
+            else
+                f[i] = bf16x2_to_f2(w[i]);
+        }
+    }
+    __device__ __forceinline__ void pack(const float2 (&f)[V / 2]) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (std::is_same<T, float>::value) {
+                w[2 * i] = __float_as_uint(f[i].x);
+                w[2 * i + 1] = __float_as_uint(f[i].y);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                w[i] = f2_to_f16x2(f[i]);
+            } else {
+                w[i] = f2_to_bf16x2(f[i]);
+            }
+        }
+    }
+};
+
+// offset + weight of the V values from element e (once a token and segment).
+template <typename T, int V>
+__device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w, int e, float2 (&f)[V / 2]) {
+#pragma unroll
+    for (int q = 0; q < V / 2; ++q) {
+        if (std::is_same<T, float>::value || p.w32) {
+            const float2 v = __ldg(reinterpret_cast<const float2 *>(static_cast<const float *>(w) + e) + q);
+            f[q] = make_float2(p.offset + v.x, p.offset + v.y);
+        } else if constexpr (!std::is_same<T, float>::value) {
+            const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const T *>(w) + e) + q);
+            const float2 v = std::is_same<T, __half>::value ? f16x2_to_f2(u) : bf16x2_to_f2(u);
+            f[q] = make_float2(p.offset + v.x, p.offset + v.y);
+        }
+    }
 }
 
 // ------------------------------------------------------ vectorised rows --
-// A lane's two chunks of a head: the two halves of E pairs (half pairing),
-// two neighbouring chunks of E pairs (adjacent pairing), or two chunks of
-// the values that pass unturned.
+// A lane's two chunks of a head: the two halves of V pairs (half pairing),
+// two neighbouring chunks of V / 2 pairs each (adjacent pairing), or two
+// chunks of the values that pass unturned.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 // Heads of a batch, batches under way, and the CTAs an SM that the registers
@@ -161,8 +215,11 @@ constexpr int kRopeUnroll = 2;
 constexpr int kRopeDepth = 3;
 constexpr int kRopeCtas[2] = {6, 5};
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+template <int BYTES> __device__ __forceinline__ void cp_async_chunk(void *dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the thread's newest N groups of copies have landed.
@@ -170,15 +227,15 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// FULL: every lane has two chunks of every head (head_dim = 2 E lanes a head,
+// FULL: every lane has two chunks of every head (head_dim = 2 V lanes a head,
 // e.g. 64, 128 or 256 values of 16 bits), so nothing is tested a chunk.
-template <typename T, bool APPEND, bool NORM, bool ADJ, bool FULL>
+template <typename T, int V, bool APPEND, bool NORM, bool ADJ, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(const __grid_constant__ RopeParams p) {
-    constexpr int E = Elem<T>::E, NP = Elem<T>::NP, U = kRopeUnroll;
+    constexpr int NP = V / 2, U = kRopeUnroll, CB = V * (int)sizeof(T);
     using PR = Pair<true>;
     __shared__ float2 turn[kRopeWarps][HEAD_MAX_DIM / 2];  // (cos, sin) of the warp's token
     constexpr int kDepth = kRopeDepth;
-    __shared__ __align__(16) uint4 places[kRopeWarps][kRopeDepth * kRopeUnroll * 64];
+    __shared__ __align__(16) uint8_t places[kRopeWarps][kRopeDepth * kRopeUnroll * 64 * CB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp;
     pdl_wait();
@@ -188,16 +245,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
     const int h0 = (int)(unit - t * p.blocks) * p.block_heads, h1 = h0 + p.block_heads;
     const int item = lane & ((1 << p.lanes_log2) - 1), grp = lane >> p.lanes_log2;
     const int step = 32 >> p.lanes_log2;
-    const int rot_items = p.half_dim / E;
+    const int rot_items = p.half_dim / V;
     const bool turns = item < rot_items;
 
     int e0, e1;
     if (turns) {
-        e0 = ADJ ? item * 2 * E : item * E;
-        e1 = ADJ ? e0 + E : e0 + p.half_dim;
+        e0 = ADJ ? item * 2 * V : item * V;
+        e1 = ADJ ? e0 + V : e0 + p.half_dim;
     } else {
-        e0 = 2 * p.half_dim + (item - rot_items) * 2 * E;
-        e1 = e0 + E;
+        e0 = 2 * p.half_dim + (item - rot_items) * 2 * V;
+        e1 = e0 + V;
     }
     const bool has0 = FULL || e0 < p.head_dim, has1 = FULL || e1 < p.head_dim;
     const int b0 = e0 * (int)sizeof(T), b1 = e1 * (int)sizeof(T);
@@ -217,7 +274,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
             first += p.seg[sg].heads;
         }
     }
-    uint4 *mine = places[warp] + lane;  // [kDepth][U][2], 32 apart
+    uint8_t *mine = places[warp] + lane * CB;  // [kDepth][U][2], 32 chunks apart
     int nsg = 0, nh = hb[0], slot = 0;  // the next batch to ask for; the next place
     auto ask = [&](int at) {
 #pragma unroll
@@ -235,9 +292,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
                 const int h = nh + u * step + grp;
                 if (h < he[sg]) {
                     const char *row = in + h * g.in_head;
-                    uint4 *to = mine + (at * U + u) * 64;
-                    if (has0) cp_async16(to, row + b0);
-                    if (has1) cp_async16(to + 32, row + b1);
+                    uint8_t *to = mine + (at * U + u) * 64 * CB;
+                    if (has0) cp_async_chunk<CB>(to, row + b0);
+                    if (has1) cp_async_chunk<CB>(to + 32 * CB, row + b1);
                 }
             }
             nh += U * step;
@@ -276,10 +333,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
                 for (int u = 0; u < U; ++u) {
                     const int hh = h + u * step + grp;
                     if (hh < he[sg] && kept) {
-                        const uint4 *from = mine + (slot * U + u) * 64;
+                        const uint8_t *from = mine + (slot * U + u) * 64 * CB;
                         char *row = out + hh * g.out_head;
-                        if (has0) *reinterpret_cast<uint4 *>(row + b0) = lds128(from);
-                        if (has1) *reinterpret_cast<uint4 *>(row + b1) = lds128(from + 32);
+                        Chunk<T, V> c;
+                        if (has0) {
+                            c.from_shared(from);
+                            c.to_global(row + b0);
+                        }
+                        if (has1) {
+                            c.from_shared(from + 32 * CB);
+                            c.to_global(row + b1);
+                        }
                     }
                 }
                 ask(slot);
@@ -297,8 +361,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
 #pragma unroll
             for (int q = 0; q < NP; ++q) fa[q] = fb[q] = make_float2(1.f, 1.f);
             if (NORM && w) {
-                if (has0) norm_factors<T>(p, w, e0, fa);
-                if (has1) norm_factors<T>(p, w, e1, fb);
+                if (has0) norm_factors<T, V>(p, w, e0, fa);
+                if (has1) norm_factors<T, V>(p, w, e1, fb);
             }
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
@@ -307,26 +371,34 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
                 sa[q] = sb[q] = make_float2(0.f, 0.f);
             }
             if (turns) {
-                const float4 *cs = reinterpret_cast<const float4 *>(&turn[warp][item * E]);
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
-                    const float4 v = cs[q];  // frequencies 2q and 2q + 1 of the lane's E
-                    const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w);
+                    // two frequencies of the lane's V
+                    const float4 v = reinterpret_cast<const float4 *>(&turn[warp][item * V])[q];
                     if (!ADJ) {
+                        const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w);
                         ca[q] = PR::mul(fa[q], c);
                         sb[q] = PR::mul(fb[q], make_float2(-s.x, -s.y));
                         cb[q] = PR::mul(fb[q], c);
                         sa[q] = PR::mul(fa[q], s);
                     } else {
-                        // pairs (2i, 2i + 1): frequency i's two values are one pair
-                        // of registers; .x keeps the first's factors, .y the second's
-                        float2 *cc = q < NP / 2 ? ca : cb, *ss = q < NP / 2 ? sa : sb;
-                        const float2 *ff = q < NP / 2 ? fa : fb;
-                        const int k = 2 * (q % (NP / 2 > 0 ? NP / 2 : 1));
-                        cc[k] = PR::mul(ff[k], make_float2(c.x, c.x));
-                        ss[k] = PR::mul(make_float2(ff[k].y, ff[k].x), make_float2(-s.x, s.x));
-                        cc[k + 1] = PR::mul(ff[k + 1], make_float2(c.y, c.y));
-                        ss[k + 1] = PR::mul(make_float2(ff[k + 1].y, ff[k + 1].x), make_float2(-s.y, s.y));
+                        // frequency i's pair (2i, 2i + 1) is one pair of registers, of
+                        // the first chunk or the second; .x keeps the first value's
+                        // factors, .y the second's
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int fi = 2 * q + h, at = fi % NP;
+                            const float c = h ? v.z : v.x, s = h ? v.w : v.y;
+                            const float2 ff = fi < NP ? fa[at] : fb[at];
+                            const float2 cc = PR::mul(ff, make_float2(c, c)), ss = PR::mul(make_float2(ff.y, ff.x), make_float2(-s, s));
+                            if (fi < NP) {
+                                ca[at] = cc;
+                                sa[at] = ss;
+                            } else {
+                                cb[at] = cc;
+                                sb[at] = ss;
+                            }
+                        }
                     }
                 }
             }
@@ -335,20 +407,23 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
 #pragma unroll 1
         for (int h = hb[sg]; h < he[sg]; h += U * step) {
             cp_async_wait<kDepth - 1>();
-            uint4 x0[U], x1[U];
+            Chunk<T, V> x0[U], x1[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint4 *from = mine + (slot * U + u) * 64;
-                x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
-                if (FULL || has0) x0[u] = lds128(from);
-                if (FULL || has1) x1[u] = lds128(from + 32);
+                const uint8_t *from = mine + (slot * U + u) * 64 * CB;
+                if (!FULL) {
+                    x0[u].clear();
+                    x1[u].clear();
+                }
+                if (has0) x0[u].from_shared(from);
+                if (has1) x1[u].from_shared(from + 32 * CB);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int hh = h + u * step + grp;
                 float2 a[NP], b[NP];
-                unpack<T>(x0[u], a);
-                unpack<T>(x1[u], b);
+                x0[u].unpack(a);
+                x1[u].unpack(b);
                 float2 r2 = make_float2(1.f, 1.f);
                 if (NORM && w) {  // (the same for the whole grid: the shuffles are uniform)
                     float2 acc = make_float2(0.f, 0.f);
@@ -378,8 +453,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(con
                 }
                 char *row = out + hh * g.out_head;
                 // (values that pass as they are keep their bits, a NaN's payload too)
-                if (has0) *reinterpret_cast<uint4 *>(row + b0) = raw ? x0[u] : pack<T>(a);
-                if (has1) *reinterpret_cast<uint4 *>(row + b1) = raw ? x1[u] : pack<T>(b);
+                if (!raw) {
+                    x0[u].pack(a);
+                    x1[u].pack(b);
+                }
+                if (has0) x0[u].to_global(row + b0);
+                if (has1) x1[u].to_global(row + b1);
             }
             // (the values read above have been used, so their places are free)
             ask(slot);
@@ -472,30 +551,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements(const __grid_const
 
 static int elem_bytes(int dt) { return (dt & 0xff) == RMSNORM_F32 ? 4 : 2; }
 
-static bool on16(int64_t a) { return a % 16 == 0; }
-
-template <typename T, bool APPEND, bool NORM>
+template <typename T, int V, bool APPEND, bool NORM>
 static int launch_vector(const RopeParams &p, const cudaLaunchConfig_t *cfg) {
-    const bool full = p.head_dim * (int)sizeof(T) == 32 << p.lanes_log2;
-    if (p.adjacent)
-        return full ? (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, true, true>, p)
-                    : (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, true, false>, p);
-    return full ? (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, false, true>, p)
-                : (int)cudaLaunchKernelEx(cfg, rope_vector<T, APPEND, NORM, false, false>, p);
+    if constexpr (V * sizeof(T) == 16) {
+        if (p.head_dim == 2 * V << p.lanes_log2)
+            return p.adjacent ? (int)cudaLaunchKernelEx(cfg, rope_vector<T, V, APPEND, NORM, true, true>, p)
+                              : (int)cudaLaunchKernelEx(cfg, rope_vector<T, V, APPEND, NORM, false, true>, p);
+    }
+    return p.adjacent ? (int)cudaLaunchKernelEx(cfg, rope_vector<T, V, APPEND, NORM, true, false>, p)
+                      : (int)cudaLaunchKernelEx(cfg, rope_vector<T, V, APPEND, NORM, false, false>, p);
 }
 
+// vec: bytes of a chunk, 16 or 8; 0: element-wise.
 template <typename T, bool APPEND>
-static int launch_rope(bool vec, const RopeParams &p, unsigned grid, cudaStream_t stream) {
+static int launch_rope(int vec, const RopeParams &p, unsigned grid, cudaStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T);
     LaunchCfg lc(grid, kRopeThreads, 0, stream);
-    if (!vec) return (int)cudaLaunchKernelEx(&lc.cfg, rope_elements<T, APPEND>, p);
+    if (vec == 0) return (int)cudaLaunchKernelEx(&lc.cfg, rope_elements<T, APPEND>, p);
     if constexpr (APPEND) {
-        if (p.w[0] || p.w[1]) return launch_vector<T, true, true>(p, &lc.cfg);
+        if (p.w[0] || p.w[1])
+            return vec == 16 ? launch_vector<T, V, true, true>(p, &lc.cfg) : launch_vector<T, V / 2, true, true>(p, &lc.cfg);
     }
-    return launch_vector<T, APPEND, false>(p, &lc.cfg);
+    return vec == 16 ? launch_vector<T, V, APPEND, false>(p, &lc.cfg) : launch_vector<T, V / 2, APPEND, false>(p, &lc.cfg);
 }
 
 template <bool APPEND>
-static int launch_rope_dt(int base, bool vec, const RopeParams &p, unsigned grid, cudaStream_t s) {
+static int launch_rope_dt(int base, int vec, const RopeParams &p, unsigned grid, cudaStream_t s) {
     switch (base) {
     case RMSNORM_F32: return launch_rope<float, APPEND>(vec, p, grid, s);
     case RMSNORM_BF16: return launch_rope<__nv_bfloat16, APPEND>(vec, p, grid, s);
@@ -539,25 +620,33 @@ static HeadSeg segment(const rope_rows_t &r, int heads, int64_t tokens, int es) 
 }
 
 static bool seg_on(const HeadSeg &g, uintptr_t a) { return g.heads == 0 || (on(g.in, a) && on(g.out, a)); }
-static bool seg_vec(const HeadSeg &g) {
-    return g.heads == 0 || (on(g.in, 16) && on(g.out, 16) && on16(g.in_token) && on16(g.in_head) &&
-                            on16(g.out_token) && on16(g.out_head) && on16(g.out_slot));
+static bool seg_vec(const HeadSeg &g, int vec) {
+    return g.heads == 0 || (on(g.in, vec) && on(g.out, vec) && g.in_token % vec == 0 && g.in_head % vec == 0 &&
+                            g.out_token % vec == 0 && g.out_head % vec == 0 && g.out_slot % vec == 0);
 }
 
 // Geometry and launch, the segments and the rest of `p` being set.
 template <bool APPEND>
 static rmsnorm_status_t run_rope(RopeParams &p, int base, cudaStream_t stream) {
-    const int es = elem_bytes(base), E = 16 / es;
+    const int es = elem_bytes(base);
     int sms = 0;
     int e = current_device(&sms, nullptr);
     if (e != 0) return head_cuda_fail(e);
-    bool vec = p.half_dim % E == 0 && p.head_dim % E == 0 && on(p.inv_freq, 16);
-    for (const HeadSeg &g : p.seg) vec = vec && seg_vec(g);
-    for (const void *w : p.w) vec = vec && on(w, 16);
+    // the widest chunks that every array, stride and the two halves are made of
+    // and that a warp's lanes hold a head in
+    int vec = 16;
+    for (; vec >= 8; vec /= 2) {
+        const int V = vec / es;
+        bool ok = p.half_dim % V == 0 && p.head_dim % V == 0;
+        for (const HeadSeg &g : p.seg) ok = ok && seg_vec(g, vec);
+        for (const void *w : p.w) ok = ok && on(w, p.w32 || es == 4 ? 8 : 4);
+        p.items = p.half_dim / V + ((p.head_dim - 2 * p.half_dim) / V + 1) / 2;
+        if (ok && p.items <= 32) break;
+    }
+    if (vec < 8) vec = 0;
     const int heads = p.seg[0].heads + p.seg[1].heads + p.seg[2].heads;
     if (vec) {
-        p.items = p.half_dim / E + ((p.head_dim - 2 * p.half_dim) / E + 1) / 2;
-        while ((1 << p.lanes_log2) < p.items) ++p.lanes_log2;  // at most 32: head_dim <= 256
+        while ((1 << p.lanes_log2) < p.items) ++p.lanes_log2;
         // One warp takes all heads of a token, so that their angles are
         // computed once, as long as that leaves eight warps an SM; with
         // fewer tokens the heads are halved until it does, down to one
