@@ -59,6 +59,36 @@ constexpr int kDecodeChunk = 16;           // key tiles of a decoding item, wher
 constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
 constexpr float kRescale = 8.f;           // log2 of how far a row's reference maximum may lag
 
+// Division by a number that the host knows, for 0 <= n < 2^31: with l = ceil
+// log2 d and m = floor(2^(31 + l) / d) + 1, n m / 2^(31 + l) is off by less
+// than 1 / d. (The instruction sequence for a division by a variable is a
+// dependent chain of some 150 cycles, and a small call had ten of them on its
+// way to the first copy.)
+struct Divisor {
+    int d;
+    uint32_t mul;
+    int shift;
+    static Divisor of(int d) {
+        Divisor r{d, 0, 0};
+        int l = 0;
+        while (((int64_t)1 << l) < d) ++l;
+        if (d > 1) {
+            r.mul = (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)d + 1);
+            r.shift = l - 1;
+        }
+        return r;
+    }
+    __device__ __forceinline__ int quotient(int n) const {
+        return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+    }
+    // the remainder; n becomes the quotient
+    __device__ __forceinline__ int split(int &n) const {
+        const int q = quotient(n), r = n - q * d;
+        n = q;
+        return r;
+    }
+};
+
 struct AttnParams {
     const char *q;
     char *out;
@@ -78,6 +108,8 @@ struct AttnParams {
     int copiers;                                        // warps that copy K and V: 1 or 3
     int by_seq;                                         // items in the order of the sequences' lengths
     int q_tma, q_vec, out_vec;
+    int box_log2;  // box_rows = 2^box_log2
+    Divisor by_heads, by_batch, by_splits, by_page, by_group;
 };
 
 template <int DP, int NQ>
@@ -181,11 +213,9 @@ __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per
     const int T_ = (int)p.tokens;
     int rank = 0;
     if (CL) {  // (the split fastest: a cluster's CTAs)
-        rank = id % p.splits;
-        id /= p.splits;
+        rank = p.by_splits.split(id);
     }
-    w.kvh = id % p.kv_heads;
-    id /= p.kv_heads;
+    w.kvh = p.by_heads.split(id);
     int b, qt;
     if (CL) {
         b = id;
@@ -212,10 +242,9 @@ __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per
         qt = __shfl_sync(0xffffffffu, n, b) - 1 - id / parts;
         w.split = id % parts;
     } else {
-        b = id % p.batch;
-        id /= p.batch;
-        w.split = id % p.splits;
-        qt = p.q_tiles - 1 - id / p.splits;
+        b = p.by_batch.split(id);
+        w.split = p.by_splits.split(id);
+        qt = p.q_tiles - 1 - id;
     }
     w.b = b;
     const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
@@ -240,7 +269,7 @@ __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per
     }
     w.ntiles = (w.kend - w.kbeg + kKeyTile - 1) / kKeyTile;
     const int last_valid = w.kv - (w.kbeg + (w.ntiles - 1) * kKeyTile);
-    w.fix = w.ntiles > 0 && last_valid < kKeyTile && last_valid % p.box_rows != 0;
+    w.fix = w.ntiles > 0 && last_valid < kKeyTile && (last_valid & (p.box_rows - 1)) != 0;
     return true;
 }
 
@@ -348,8 +377,9 @@ __device__ __forceinline__ void join_cluster(const AttnParams &p, const Item &w,
             a.w = __fmaf_rn(e, v[s].w, a.w);
         }
         const float inv = none ? 0.f : __fdividef(1.f, sum);
-        const int64_t token = w.q0 + w.tok0 + r / p.group;
-        const int head = w.kvh * p.group + r % p.group;
+        const int tok = p.by_group.quotient(r);
+        const int64_t token = w.q0 + w.tok0 + tok;
+        const int head = w.kvh * p.group + r - tok * p.group;
         if (c == 0 && p.lse)
             p.lse[token * p.heads + head] = none ? -INFINITY : (top + __log2f(sum)) * 0.693147180559945309f;
         char *dst = p.out + token * p.out_token + (int64_t)head * p.out_head + c * 8;
@@ -432,9 +462,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     }
     if (warp == kIssuer) tmem_alloc(tmem_slot, S::kCols);
     if (warp == kProducer) {  // the first item's lengths, on their way while the CTA meets
-        const int b = CL         ? (int)blockIdx.x / p.splits / p.kv_heads
-                      : p.by_seq ? min(lane, p.batch - 1)
-                                 : (int)blockIdx.x / p.kv_heads % p.batch;
+        int b = blockIdx.x;
+        if (CL) b = p.by_splits.quotient(b);
+        b = p.by_heads.quotient(b);
+        b = p.by_seq ? min(lane, p.batch - 1) : p.by_batch.split(b);
         prefetch_l1(p.cu_q + b);
         prefetch_l1(p.cu_q + b + 1);
         prefetch_l1(p.kv_lens + b);
@@ -478,19 +509,19 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     // ones the other two only cost (2 x 8192 tokens, D 128: pages of 8 1178 ->
     // 707 us and of 16 775 -> 674, but of 64 649 -> 677).
     const int copier = warp == kProducer ? 0 : warp - kIssuer;  // 0, 1, 2
-    const int boxes = kKeyTile / p.box_rows;
+    const int boxes_log2 = 7 - p.box_log2;  // of a key tile's 128 rows
     const int item_box = copier + p.copiers * lane;
-    const int piece = item_box % boxes, half = item_box / boxes;
+    const int piece = item_box & ((1 << boxes_log2) - 1), half = item_box >> boxes_log2;
     const bool copies = half < S::kHalves;
-    const uint32_t off = (uint32_t)(half * kKeyTile * 128 + piece * p.box_rows * 128);
+    const uint32_t off = (uint32_t)(half * kKeyTile * 128 + (piece << p.box_log2) * 128);
     // (the table's entry is checked where it is used, a tile later: until then
     // its load is under way)
     auto find = [&](const Item &i, int tile, int &pg, int &pl) {
-        const int key = i.kbeg + tile * kKeyTile + piece * p.box_rows;
+        const int key = i.kbeg + tile * kKeyTile + (piece << p.box_log2);
         pg = -1;
         pl = 0;
         if (copies && tile < i.ntiles && key < i.kv) {
-            const int col = key / p.page_size;
+            const int col = p.by_page.quotient(key);
             pg = __ldg(p.table + i.b * p.table_stride + col);
             pl = key - col * p.page_size;
         }
@@ -563,7 +594,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 ok = false;
                 return;
             }
-            const int end = (fix_from / p.box_rows + 1) * p.box_rows;  // later boxes are zeros
+            const int end = ((fix_from >> p.box_log2) + 1) << p.box_log2;  // later boxes are zeros
             const int chunks = (end - fix_from) * 8;
 #pragma unroll 1
             for (int i = lane; i < chunks * S::kHalves; i += 32) {
@@ -781,7 +812,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         const int t = warp >> 2, r = threadIdx.x & 127;  // tile, row in it
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * kKeyTile, to = tmem + lanes + S::kO + t * DP;
-        const int row_tok = r / p.group, row_head = r % p.group;
+        const int row_tok = p.by_group.quotient(r), row_head = r - row_tok * p.group;
         const float c = p.c;
         using PR = Pair<true>;
         int steps = 0;  // key tiles, over all items
@@ -806,7 +837,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                         const int i = i0 + u * 128, rr = i / kChunks, ch = i % kChunks;
                         v[u] = make_uint4(0, 0, 0, 0);
                         if (rr < rows && ch < hd_chunks) {
-                            const int tok = rr / p.group, g = rr - tok * p.group;
+                            const int tok = p.by_group.quotient(rr), g = rr - tok * p.group;
                             const char *src = p.q + (int64_t)(w.q0 + w.tok0 + t * tt + tok) * p.q_token +
                                               (int64_t)(w.kvh * p.group + g) * p.q_head + ch * 16;
                             if (p.q_vec) {
@@ -1423,6 +1454,12 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     p.head_dim = c.head_dim;
     p.pages = (int)pc.pages;
     p.page_size = pc.page_size;
+    while ((1 << p.box_log2) < p.box_rows) ++p.box_log2;
+    p.by_heads = Divisor::of(pc.heads);
+    p.by_batch = Divisor::of(c.batch);
+    p.by_splits = Divisor::of(cut.splits);
+    p.by_page = Divisor::of(pc.page_size);
+    p.by_group = Divisor::of(c.q_heads / pc.heads);
     p.max_q = c.max_q;
     p.max_kv = cc.max_kv;
     p.causal = c.causal != 0;
