@@ -41,6 +41,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -1300,30 +1301,29 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
     k.splits = 1;
     k.chunk = 0;
     k.cluster = false;
-    if (ctas < slots && tiles > 1) {
-        int64_t want = slots / ctas;
-        const int64_t least = 2;  // key tiles a split is worth
-        if (want > tiles / least) want = tiles / least;
-        if (want > 1) {
-            int64_t per_split = (tiles + want - 1) / want;
-            // A cluster joins its splits itself; otherwise a second kernel does,
-            // which takes as long as a few key tiles. A cluster lies in one of
-            // eight parts of the device, two CTAs an SM; its size is such that
-            // they all fit at once.
-            int64_t size = kClusterMost;
-            while (size > 1 && 8 * (sms / 4 / size) < ctas) --size;
-            const int64_t per_cluster = (tiles + size - 1) / size;
-            k.cluster = k.nq == 1 && size > 1 && per_cluster - per_split <= kJoinTiles;
-            if (k.cluster && per_split < per_cluster) per_split = per_cluster;
-            k.splits = (int)((tiles + per_split - 1) / per_split);
-            k.chunk = (int)(per_split * kKeyTile);
-            if (k.splits < 2) k.cluster = false;
-        }
+    // CTAs for each row tile, a split being worth two key tiles at least
+    const int64_t want = ctas < slots ? std::min(slots / ctas, tiles / 2) : 1;
+    if (want > 1) {
+        int64_t per_split = (tiles + want - 1) / want;
+        // A cluster joins its splits itself; otherwise a second kernel does,
+        // which takes as long as a few key tiles. A cluster lies in one of
+        // eight parts of the device, two CTAs an SM; its size is such that
+        // they all fit at once.
+        int64_t size = kClusterMost;
+        while (size > 1 && 8 * (sms / 4 / size) < ctas) --size;
+        const int64_t per_cluster = (tiles + size - 1) / size;
+        k.cluster = k.nq == 1 && size > 1 && per_cluster - per_split <= kJoinTiles;
+        if (k.cluster && per_split < per_cluster) per_split = per_cluster;
+        k.splits = (int)((tiles + per_split - 1) / per_split);
+        k.chunk = (int)(per_split * kKeyTile);
+        if (k.splits < 2) k.cluster = false;
     } else if (k.nq == 1 && ctas < 4 * slots && tiles >= 2 * kDecodeChunk) {
-        // A few items a CTA: shorter ones let the CTAs end together (64
-        // sequences of 964 to 8192 keys: 219 -> 187 us; of 8192 each: 300 -> 304).
-        // Rows by the hundred lose more with their partial results (chunks of
-        // 512 over 8192: 124 -> 147 us in two).
+        // Up to a few items a CTA: shorter ones let the CTAs end together where
+        // the lengths differ (lengths of 964 to 8192 keys, 8 key heads: 24
+        // sequences 119 -> 87 us, 32: 122 -> 105, 64: 219 -> 195; 8192 each:
+        // 129 -> 132, 161 -> 176, 300 -> 304). Rows by the hundred lose more
+        // with their partial results (chunks of 512 over 8192: 124 -> 147 us in
+        // two).
         k.splits = (int)((tiles + kDecodeChunk - 1) / kDecodeChunk);
         k.chunk = kDecodeChunk * kKeyTile;
     }
