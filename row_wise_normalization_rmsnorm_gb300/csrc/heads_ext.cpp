@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -211,6 +212,15 @@ rmsnorm_stream_t stream_of(PyObject *stream, const at::Tensor &like) {
     return static_cast<rmsnorm_stream_t>(p);
 }
 
+// Results made here for a call on a stream that the caller named: their memory
+// is not given out again before that stream is done with it.
+void used_on(PyObject *stream, rmsnorm_stream_t s, PyObject *result, PyObject *given) {
+    if (stream == Py_None || !result || given != Py_None || !THPVariable_Check(result)) return;
+    const at::Tensor &t = THPVariable_Unpack(result);
+    c10::cuda::CUDACachingAllocator::recordStream(
+        t.storage().data_ptr(), c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), t.device().index()));
+}
+
 // The tensors' device made current for the call, where it is not.
 struct OnDevice {
     std::optional<c10::cuda::CUDAGuard> guard;
@@ -293,6 +303,8 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         st = grad ? rope_bwd(&c, axes, s) : rope_fwd(&c, axes, s);
         Py_END_ALLOW_THREADS
         check(st, grad ? "rope_bwd" : "rope_fwd");
+        used_on(a[9], s, qo.o, a[7]);
+        used_on(a[9], s, ko.o, a[8]);
         PyObject *k_result = ko.o ? ko.take() : Py_NewRef(Py_None);
         PyObject *r = PyTuple_New(2);
         if (!r) {
@@ -366,6 +378,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         st = paged_kv_append(&c, axes, s);
         Py_END_ALLOW_THREADS
         check(st, "paged_kv_append");
+        used_on(a[15], s, qo.o, a[10]);
         return has_q ? qo.take() : Py_NewRef(Py_None);
     });
 }
@@ -451,6 +464,8 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         st = paged_attn_fwd(&c, s);
         Py_END_ALLOW_THREADS
         check(st, "paged_attn_fwd");
+        used_on(a[13], s, out.o, a[10]);
+        used_on(a[13], s, lse.o, a[11] == Py_True ? Py_None : a[11]);
         PyObject *result = PyTuple_New(2);
         if (!result) throw AlreadySet{};
         PyTuple_SET_ITEM(result, 0, out.take());

@@ -225,8 +225,8 @@ __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per
     } else if (p.by_seq) {
         int n = 0, parts = 1, kv = -1;
         if (lane < p.batch) {
-            const int c0 = min(max(__ldg(p.cu_q + lane), 0), T_), c1 = min(max(__ldg(p.cu_q + lane + 1), c0), T_);
-            kv = kv_length(p, __ldg(p.kv_lens + lane));
+            const int c0 = min(max(p.cu_q[lane], 0), T_), c1 = min(max(p.cu_q[lane + 1], c0), T_);
+            kv = kv_length(p, p.kv_lens[lane]);
             n = (min(c1 - c0, p.max_q) + per - 1) / per;
             if (p.splits > 1) parts = max((kv + p.chunk - 1) / p.chunk, 1);
         }
@@ -248,8 +248,8 @@ __device__ __forceinline__ bool decode_item(const AttnParams &p, int id, int per
         qt = p.q_tiles - 1 - id;
     }
     w.b = b;
-    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
-    w.kv = kv_length(p, __ldg(p.kv_lens + b));
+    const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1];
+    w.kv = kv_length(p, p.kv_lens[b]);
     w.q0 = min(max(c0, 0), T_);
     w.nq = min(max(c1, w.q0), T_) - w.q0;
     w.tok0 = qt * per;
@@ -455,6 +455,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         prefetch_map(&kmap);
         prefetch_map(&vmap);
     }
+    // (What the kernel before wrote is read with plain loads and copies only: the
+    // non-coherent path wants data that nothing writes while the kernel runs.)
     pdl_wait();
     pdl_trigger();
     if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle goes by the address
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         pl = 0;
         if (copies && tile < i.ntiles && key < i.kv) {
             const int col = p.by_page.quotient(key);
-            pg = __ldg(p.table + i.b * p.table_stride + col);
+            pg = p.table[i.b * p.table_stride + col];
             pl = key - col * p.page_size;
         }
     };
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                             const char *src = p.q + (int64_t)(w.q0 + w.tok0 + t * tt + tok) * p.q_token +
                                               (int64_t)(w.kvh * p.group + g) * p.q_head + ch * 16;
                             if (p.q_vec) {
-                                v[u] = __ldg(reinterpret_cast<const uint4 *>(src));
+                                v[u] = *reinterpret_cast<const uint4 *>(src);
                             } else {
                                 const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
                                 v[u] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
@@ -1174,10 +1176,10 @@ __global__ void __launch_bounds__(128) paged_attn_join(const __grid_constant__ A
     const int64_t rest = unit - b * per_seq;
     const int tok = (int)(rest / p.heads), head = (int)(rest - (int64_t)tok * p.heads);
     const int T_ = (int)p.tokens;
-    const int q0 = min(max(__ldg(p.cu_q + b), 0), T_);
-    const int nq = min(max(__ldg(p.cu_q + b + 1), q0), T_) - q0;
+    const int q0 = min(max(p.cu_q[b], 0), T_);
+    const int nq = min(max(p.cu_q[b + 1], q0), T_) - q0;
     if (tok >= nq) return;
-    const int kv = kv_length(p, __ldg(p.kv_lens + b));
+    const int kv = kv_length(p, p.kv_lens[b]);
     // a row tile whose keys one split held has written its rows itself
     const int per = p.nq * p.tile_toks, tile_end = min((tok / per + 1) * per, min(nq, p.max_q));
     const int lim = keys_seen(p, kv, nq, tile_end);

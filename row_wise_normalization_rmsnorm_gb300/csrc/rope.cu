@@ -54,6 +54,10 @@ struct RopeParams {
     int w32;
 };
 
+// (Plain loads throughout: the kernel may have been launched while the one
+// before it was still writing what is read here after pdl_wait, which the
+// non-coherent path does not provide for.)
+
 // ------------------------------------------------------------- angles --
 // The angle p f is wanted modulo a turn, and fp32's p f has lost that where p
 // is large. So the frequency is taken as a 64-bit fixed-point fraction of a
@@ -80,8 +84,8 @@ __device__ __forceinline__ float half_turns(int64_t pos, int64_t step) {
 
 __device__ __forceinline__ int64_t position(const RopeParams &p, int axis, int64_t t) {
     const int64_t i = (int64_t)axis * p.axis_stride + t;
-    return p.pos64 ? __ldg(reinterpret_cast<const long long *>(p.positions) + i)
-                   : (int64_t)__ldg(reinterpret_cast<const int *>(p.positions) + i);
+    return p.pos64 ? static_cast<const int64_t *>(p.positions)[i]
+                   : (int64_t) static_cast<const int32_t *>(p.positions)[i];
 }
 
 __device__ __forceinline__ int axis_of(const RopeParams &p, int i) { return (p.axis[i >> 4] >> (2 * (i & 15))) & 3; }
@@ -100,7 +104,7 @@ __device__ __forceinline__ void angles_of(const RopeParams &p, int64_t t, int i0
             const int a = axis_of(p, i0 + i);
             pos = a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
         }
-        const float f = __ldg(p.inv_freq + i0 + i);
+        const float f = p.inv_freq[i0 + i];
         sincospif(isfinite(f) ? half_turns(pos, turn_step(f)) : NAN, s + i, c + i);
         s[i] *= p.sign;
     }
@@ -120,7 +124,7 @@ __device__ __forceinline__ char *row_out(const RopeParams &p, const HeadSeg &g, 
 
 // The page and the place in it of token t's slot; page -1: none.
 __device__ __forceinline__ void find_slot(const RopeParams &p, int64_t t, int64_t &page, int &place) {
-    const int64_t slot = __ldg(reinterpret_cast<const long long *>(p.slots) + t);
+    const int64_t slot = p.slots[t];
     page = -1;
     place = 0;
     if (slot < 0 || slot >= p.slots_end) return;
@@ -190,10 +194,10 @@ __device__ __forceinline__ void norm_factors(const RopeParams &p, const void *w,
 #pragma unroll
     for (int q = 0; q < V / 2; ++q) {
         if (std::is_same<T, float>::value || p.w32) {
-            const float2 v = __ldg(reinterpret_cast<const float2 *>(static_cast<const float *>(w) + e) + q);
+            const float2 v = reinterpret_cast<const float2 *>(static_cast<const float *>(w) + e)[q];
             f[q] = make_float2(p.offset + v.x, p.offset + v.y);
         } else if constexpr (!std::is_same<T, float>::value) {
-            const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const T *>(w) + e) + q);
+            const uint32_t u = reinterpret_cast<const uint32_t *>(static_cast<const T *>(w) + e)[q];
             const float2 v = std::is_same<T, __half>::value ? f16x2_to_f2(u) : bf16x2_to_f2(u);
             f[q] = make_float2(p.offset + v.x, p.offset + v.y);
         }
@@ -518,8 +522,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements(const __grid_const
         float v = load_elem(in[u], i);
         if (APPEND && sg < 2 && p.w[sg]) {
             const float w = std::is_same<T, float>::value || p.w32
-                                ? load_w(reinterpret_cast<const float *>(p.w[sg]), i)
-                                : load_w(reinterpret_cast<const T *>(p.w[sg]), i);
+                                ? load_elem(reinterpret_cast<const float *>(p.w[sg]), i)
+                                : load_elem(reinterpret_cast<const T *>(p.w[sg]), i);
             v = v * rstd[u] * (p.offset + w);
         }
         return v;

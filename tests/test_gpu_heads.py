@@ -630,6 +630,30 @@ def test_calls_on_two_streams_at_once(rn):
         assert all(torch.equal(w, x) for x in side[-1])
 
 
+def test_results_made_for_a_named_stream(rn):
+    """With stream= and no result given, the call makes them and their memory
+    is not handed out again while that stream still writes it."""
+    g = gen(24)
+    T, H, D = 4000, 8, 128
+    q = normal(g, T, H, D, dt=torch.bfloat16)
+    pos, f = torch.arange(T, device="cuda"), freqs(64)
+    want = rn.rope_fwd(q, q, pos, f)
+    kc, vc, table, ln = paged(g, [300], 16, 8, D, torch.bfloat16)
+    kw = dict(max_q=200, max_kv=300, lse=True)
+    o, l = rn.paged_attn_fwd(q[:200], kc, vc, table, ln, starts([200]), **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        a = rn.rope_fwd(q, q, pos, f, stream=handle)
+        b = rn.paged_attn_fwd(q[:200], kc, vc, table, ln, starts([200]), stream=handle, **kw)
+        rn.rope_fwd(q, q, pos, f, stream=handle)          # dropped at once
+        other = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1])
+        assert torch.equal(b[0], o) and torch.equal(b[1], l) and not bool(other.any())
+
+
 def test_append_and_rope_in_a_graph(rn):
     g = gen(23)
     T, H, D = 33, 4, 64
