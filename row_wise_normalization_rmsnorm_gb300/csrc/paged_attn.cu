@@ -1034,8 +1034,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 // to this CTA's shared memory, whose K and V are done with: a
                 // row's 16-byte chunks turned by the row, so that the lanes' stores
                 // spread over the banks
-                if (live) join_lse[r] = lse2;
                 if (!(ok = o_ready())) break;
+                if (live) join_lse[r] = lse2;
 #pragma unroll 1
                 for (int d = 0; d < p.head_dim; d += 32) {
                     uint32_t o[32];

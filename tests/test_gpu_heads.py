@@ -427,6 +427,21 @@ def test_attention_many_items(rn, nq, lens, hq, hk, D, page):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("fill", [None, float("nan")])
+@pytest.mark.parametrize("hq,hk,D,page", [(128, 8, 112, 256), (24, 8, 128, 256), (16, 8, 64, 128), (32, 8, 128, 16)])
+def test_attention_last_piece_of_one_or_four_tiles(rn, fill, hq, hk, D, page):
+    """Keys cut over a cluster, the last piece one tile (or four) whose values
+    end inside a page: the rows' statistics take shared memory that the tile's
+    values are still read from until its last product is done."""
+    lens = [729, 636, 974, 667, 518, 965, 706, 297, 0, 1133, 839, 20, 996, 93, 1085, 0, 295]
+    nq = [1, 1, 1, 1, 1, 0] + [1] * 11
+    for seed in range(4):
+        g = gen(seed + D)
+        kc, vc, table, ln = paged(g, lens, page, hk, D, torch.float16, fill=fill)
+        q = normal(g, sum(nq), hq, D, dt=torch.float16)
+        check_attention(rn, q, kc, vc, table, ln, nq, causal=False)
+
+
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("nq,lens,page", [([1, 1], [77, 1030], 16), ([1], [3], 256), ([200, 9], [205, 130], 48),
                                           ([1], [0], 8)])
