@@ -417,9 +417,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
     uint64_t *full = bars, *empty = bars + NST;
     uint64_t *s_ready = empty + NST, *p_half = s_ready + NQ, *p_ready = p_half + NQ, *o_done = p_ready + NQ;
-    uint64_t *q_ready = o_done + NQ, *q_free = q_ready + 1, *v_fixed = q_free + 1, *drained = v_fixed + 1;
+    uint64_t *q_ready = o_done + NQ, *q_free = q_ready + 1, *v_fixed = q_free + 1, *drained = v_fixed + 2;
     uint64_t *item_full = drained + 1, *item_empty = item_full + 2, *answered = item_empty + 2;
-    static_assert(2 * S::kStages + 4 * NQ + 9 <= 36, "barriers");
+    static_assert(2 * S::kStages + 4 * NQ + 10 <= 36, "barriers");
     uint8_t *after = smem + S::kBars + 36 * 8;
     void *answer = after;  // 16 bytes, 16-byte aligned
     Item *items = reinterpret_cast<Item *>(after + 16);
@@ -440,9 +440,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         }
         mbar_init(q_ready, p.q_tma ? 1 : NQ * 4);
         mbar_init(q_free, 1);
-        mbar_init(v_fixed, 1);
         mbar_init(drained, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(v_fixed + i, 1);
             mbar_init(item_full + i, 1);
             mbar_init(item_empty + i, NQ * 4 + p.copiers);  // all warps but the one that makes the items
         }
@@ -589,8 +589,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         };
         // Values past the sequence's end in its last page would meet a zero
         // weight, and 0 * NaN is NaN: they become zeros once the tile is there.
+        // (Two barriers in turn: with the items' two places this warp may mend the
+        // next item's values before the products of this one's, and no further.)
         Ring<NST> fix_at;
-        int fix_from = -1;
+        int fix_from = -1, fixes = 0;
         auto fix_values = [&]() {
             const int st = fix_at.st;
             if (!warp_wait(full + st, fix_at.turn)) {
@@ -607,7 +609,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(v_fixed);
+            if (lane == 0) mbar_arrive(v_fixed + (fixes & 1));
+            ++fixes;
             fix_from = -1;
         };
 
@@ -748,7 +751,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         };
         auto arrived = [&](const Ring<NST> &r) { return warp_wait(full + r.st, r.turn); };
         Ring<NST> kr;  // the next key tile's place
-        uint32_t q_turn = 0, fix_turn = 0, turn[2] = {0, 0};
+        uint32_t q_turn = 0, turn[2] = {0, 0};
+        int fixes = 0;
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; ok; ++n) {
@@ -773,8 +777,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
             for (int j = 0; j < w.ntiles && ok; ++j) {
                 const bool more = j + 1 < w.ntiles;
                 if (!more && w.fix) {
-                    ok = warp_wait(v_fixed, fix_turn);
-                    fix_turn ^= 1u;
+                    ok = warp_wait(v_fixed + (fixes & 1), (uint32_t)((fixes >> 1) & 1));
+                    ++fixes;
                 }
                 const Ring<NST> vn = kr.next();  // the next values' place
 #pragma unroll

@@ -442,6 +442,19 @@ def test_attention_last_piece_of_one_or_four_tiles(rn, fill, hq, hk, D, page):
         check_attention(rn, q, kc, vc, table, ln, nq, causal=False)
 
 
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 56), (24, 8)])
+def test_attention_short_items_that_end_inside_a_page(rn, off, D, page):
+    """Four items a CTA and one key tile each: the copies run two items ahead of
+    the products, and so does the mending of the values past the end."""
+    lens = [1 + (37 * i) % 127 for i in range(80)]
+    nq = [128] * 80
+    g = gen(D + off)
+    kc, vc, table, ln = paged(g, lens, page, 8, D, torch.bfloat16, fill=float("nan"))
+    q = offset_view(normal(g, sum(nq), 16, D, dt=torch.bfloat16), off)
+    check_attention(rn, q, kc, vc, table, ln, nq, causal=False)
+
+
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("nq,lens,page", [([1, 1], [77, 1030], 16), ([1], [3], 256), ([200, 9], [205, 130], 48),
                                           ([1], [0], 8)])
