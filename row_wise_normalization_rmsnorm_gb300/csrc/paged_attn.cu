@@ -823,6 +823,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         const float c = p.c;
         using PR = Pair<true>;
         int steps = 0;  // key tiles, over all items
+        uint32_t q_turn = 0;
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; ok; ++n) {
@@ -867,6 +868,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_ready);
+                // all of q is there before any warp goes on: one without rows would
+                // arrive for its next item while this one's turn still counts
+                if (!(ok = warp_wait(q_ready, q_turn))) break;
+                q_turn ^= 1u;
             }
             if (rows == 0) continue;  // (the tile's products are not issued either)
             if ((warp & 3) * 32 >= rows) {

@@ -455,6 +455,19 @@ def test_attention_short_items_that_end_inside_a_page(rn, off, D, page):
     check_attention(rn, q, kc, vc, table, ln, nq, causal=False)
 
 
+@pytest.mark.parametrize("hk,group,D", [(3, 128, 104), (3, 16, 16), (6, 5, 128)])
+def test_attention_items_with_an_empty_row_tile_and_unaligned_q(rn, hk, group, D):
+    """Several items a CTA, the second row tile of most empty, q by plain loads:
+    a tile without rows does not get ahead of the other's q."""
+    per = 2 * (128 // group)
+    nq = [(1, per // 2, per + 1, 0, per)[i % 5] for i in range(120)]
+    lens = [16 * (1 + (7 * i) % 40) for i in range(120)]
+    g = gen(D)
+    kc, vc, table, ln = paged(g, lens, 16, hk, D, torch.bfloat16)
+    q = offset_view(normal(g, sum(nq), hk * group, D, dt=torch.bfloat16), 1)
+    check_attention(rn, q, kc, vc, table, ln, nq, causal=False)
+
+
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("nq,lens,page", [([1, 1], [77, 1030], 16), ([1], [3], 256), ([200, 9], [205, 130], 48),
                                           ([1], [0], 8)])
