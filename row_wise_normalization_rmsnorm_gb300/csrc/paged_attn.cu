@@ -619,9 +619,11 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 2 ? 1 : 2)
         for (;; ++n) {
             find_next(w, page, place);
             if (!ok) break;
-            // (an item that copies nothing leaves nothing to put the mending off to)
+            if (n >= 2 && !warp_wait(item_empty + (n & 1), (uint32_t)(((n >> 1) - 1) & 1))) break;
+            // (an item that copies nothing leaves nothing to put the mending off to;
+            // behind the wait, which keeps it within the two barriers)
             if (w.ntiles <= 0 && fix_from >= 0) fix_values();
-            if (!ok || (n >= 2 && !warp_wait(item_empty + (n & 1), (uint32_t)(((n >> 1) - 1) & 1)))) break;
+            if (!ok) break;
             if (lane == 0) {
                 items[n & 1] = w;
                 mbar_arrive(item_full + (n & 1));
