@@ -4,6 +4,12 @@ points on head rows of include/rmsnorm.h).
 The arguments are checked and marshalled by the module ``_heads_ext``
 (csrc/heads_ext.cpp): for a few tokens the host's share is most of a call.
 There is no CPU fallback.
+
+``stream`` names the stream to launch on (an object or a handle; None: the
+device's current one). The call waits for nothing there, so what it reads has
+to be ready in that stream's order. Results that it makes for a named stream
+lie in that stream's memory, and the current stream may read them once it has
+waited for the named one.
 """
 from __future__ import annotations
 

@@ -81,21 +81,56 @@ void beside(const at::Tensor &t, const char *name, at::ScalarType a, at::ScalarT
 
 void *ptr(const at::Tensor &t) { return t.data_ptr(); }
 
+// The stream that a call launches on: the device's current one (None), a
+// handle, or an object with one.
+struct LaunchStream {
+    rmsnorm_stream_t handle;
+    std::optional<c10::cuda::CUDAStream> named;  // where the caller named one
+    LaunchStream(PyObject *stream, const at::Tensor &like) {
+        const c10::DeviceIndex device = like.device().index();
+        if (stream == Py_None) {
+            handle = reinterpret_cast<rmsnorm_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
+            return;
+        }
+        PyObject *h = PyLong_Check(stream) ? Py_NewRef(stream) : PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) throw AlreadySet{};
+        void *p = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!p && PyErr_Occurred()) throw AlreadySet{};
+        if (p == static_cast<void *>(cudaStreamLegacy)) p = nullptr;  // the same stream; PyTorch knows it as 0
+        handle = static_cast<rmsnorm_stream_t>(p);
+        named = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), device);
+    }
+};
+
 // A contiguous tensor on `like`'s device, from PyTorch's allocator (its CUDA
-// entry itself: the dispatched at::empty takes 0.9 us a tensor longer).
-at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, const at::Tensor &like) {
-    return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
+// entry itself: the dispatched at::empty takes 0.9 us a tensor longer). For a
+// named stream the memory is that stream's own: the current stream's may still
+// be in use by what was queued there before its last owner dropped it, and the
+// named stream waits for none of that. Its first reader is likely to be the
+// current stream, so the memory is not given out again, once dropped, before
+// that one is done with it either.
+at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, const at::Tensor &like, const LaunchStream &s) {
+    if (!s.named) return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
+    const c10::cuda::CUDAStream reader = c10::cuda::getCurrentCUDAStream(like.device().index());
+    at::Tensor t;
+    {
+        c10::cuda::CUDAStreamGuard on(*s.named);
+        t = at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
+    }
+    if (t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), reader);
+    return t;
 }
 
 // Rows x (given as `in`) written to `out`, a tensor made here when None. The
 // result is a new reference.
-PyObject *rows_to(const at::Tensor &in, PyObject *out, const char *name, rope_rows_t &r) {
+PyObject *rows_to(const at::Tensor &in, PyObject *out, const char *name, const LaunchStream &s, rope_rows_t &r) {
     std::string out_name = std::string(name) + "_out";
     at::Tensor made;
     const at::Tensor *o = &made;
     PyObject *result;
     if (out == Py_None) {
-        made = new_tensor(in.sizes(), in.scalar_type(), in);
+        made = new_tensor(in.sizes(), in.scalar_type(), in, s);
         result = THPVariable_Wrap(made);
         if (!result) throw AlreadySet{};
     } else {
@@ -199,28 +234,6 @@ float float_arg(PyObject *o, const char *name) {
     return (float)v;
 }
 
-// The stream to launch on: the device's current one, a handle, or an object
-// with one.
-rmsnorm_stream_t stream_of(PyObject *stream, const at::Tensor &like) {
-    if (stream == Py_None)
-        return reinterpret_cast<rmsnorm_stream_t>(c10::cuda::getCurrentCUDAStream(like.device().index()).stream());
-    PyObject *h = PyLong_Check(stream) ? Py_NewRef(stream) : PyObject_GetAttrString(stream, "cuda_stream");
-    if (!h) throw AlreadySet{};
-    void *p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw AlreadySet{};
-    return static_cast<rmsnorm_stream_t>(p);
-}
-
-// Results made here for a call on a stream that the caller named: their memory
-// is not given out again before that stream is done with it.
-void used_on(PyObject *stream, rmsnorm_stream_t s, PyObject *result, PyObject *given) {
-    if (stream == Py_None || !result || given != Py_None || !THPVariable_Check(result)) return;
-    const at::Tensor &t = THPVariable_Unpack(result);
-    c10::cuda::CUDACachingAllocator::recordStream(
-        t.storage().data_ptr(), c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), t.device().index()));
-}
-
 // The tensors' device made current for the call, where it is not.
 struct OnDevice {
     std::optional<c10::cuda::CUDAGuard> guard;
@@ -291,20 +304,18 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             value_error(std::string(kn) + "_out needs " + kn);
         }
         const uint8_t *axes = angles_of(a[3], a[4], a[5], a[6], q, c.angles);
-        qo.o = rows_to(q, a[7], qn, c.q);
-        if (a[2] != Py_None) ko.o = rows_to(tensor(a[2], kn), a[8], kn, c.k);
+        const LaunchStream s(a[9], q);
+        qo.o = rows_to(q, a[7], qn, s, c.q);
+        if (a[2] != Py_None) ko.o = rows_to(tensor(a[2], kn), a[8], kn, s, c.k);
         c.tokens = q.size(0);
         c.q_heads = size32(q.size(1), qn);
         c.head_dim = size32(q.size(2), qn);
         OnDevice on(q);
-        const rmsnorm_stream_t s = stream_of(a[9], q);
         rmsnorm_status_t st;
         Py_BEGIN_ALLOW_THREADS
-        st = grad ? rope_bwd(&c, axes, s) : rope_fwd(&c, axes, s);
+        st = grad ? rope_bwd(&c, axes, s.handle) : rope_fwd(&c, axes, s.handle);
         Py_END_ALLOW_THREADS
         check(st, grad ? "rope_bwd" : "rope_fwd");
-        used_on(a[9], s, qo.o, a[7]);
-        used_on(a[9], s, ko.o, a[8]);
         PyObject *k_result = ko.o ? ko.take() : Py_NewRef(Py_None);
         PyObject *r = PyTuple_New(2);
         if (!r) {
@@ -365,20 +376,19 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         c.eps = float_arg(a[13], "eps");
         c.offset = float_arg(a[14], "offset");
         Ref qo;
-        if (has_q) qo.o = rows_to(tensor(a[9], "q"), a[10], "q", c.q);
+        const LaunchStream s(a[15], k);
+        if (has_q) qo.o = rows_to(tensor(a[9], "q"), a[10], "q", s, c.q);
         c.k = rope_rows_t{ptr(k), nullptr, k.stride(0), k.stride(1), 0, 0};
         c.v = rope_rows_t{ptr(v), nullptr, v.stride(0), v.stride(1), 0, 0};
         c.slots = static_cast<const int64_t *>(ptr(slots));
         c.tokens = tokens;
         c.head_dim = size32(dim, "k");
         OnDevice on(k);
-        const rmsnorm_stream_t s = stream_of(a[15], k);
         rmsnorm_status_t st;
         Py_BEGIN_ALLOW_THREADS
-        st = paged_kv_append(&c, axes, s);
+        st = paged_kv_append(&c, axes, s.handle);
         Py_END_ALLOW_THREADS
         check(st, "paged_kv_append");
-        used_on(a[15], s, qo.o, a[10]);
         return has_q ? qo.take() : Py_NewRef(Py_None);
     });
 }
@@ -410,9 +420,10 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         c.causal = causal;
         rope_rows_t r;
         Ref out, lse;
-        out.o = rows_to(q, a[10], "q", r);
+        const LaunchStream s(a[13], q);
+        out.o = rows_to(q, a[10], "q", s, r);
         if (a[11] == Py_True) {
-            const at::Tensor t = new_tensor({tokens, heads}, at::kFloat, q);
+            const at::Tensor t = new_tensor({tokens, heads}, at::kFloat, q, s);
             c.lse = static_cast<float *>(ptr(t));
             lse.o = THPVariable_Wrap(t);
             if (!lse.o) throw AlreadySet{};
@@ -448,24 +459,21 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 value_error("workspace must be a contiguous CUDA tensor on the input's device");
             c.workspace = ptr(w);
             c.workspace_bytes = (size_t)w.numel() * w.element_size();
-        } else if (a[13] == Py_None) {
+        } else if (!s.named) {
             // torch's allocator, on the current stream; for another stream the
             // library takes stream-ordered memory there
             const size_t bytes = paged_attn_workspace_bytes(&c);
             if (bytes > 0) {
-                made = new_tensor({(int64_t)bytes}, at::kByte, q);
+                made = new_tensor({(int64_t)bytes}, at::kByte, q, s);
                 c.workspace = ptr(made);
                 c.workspace_bytes = bytes;
             }
         }
-        const rmsnorm_stream_t s = stream_of(a[13], q);
         rmsnorm_status_t st;
         Py_BEGIN_ALLOW_THREADS
-        st = paged_attn_fwd(&c, s);
+        st = paged_attn_fwd(&c, s.handle);
         Py_END_ALLOW_THREADS
         check(st, "paged_attn_fwd");
-        used_on(a[13], s, out.o, a[10]);
-        used_on(a[13], s, lse.o, a[11] == Py_True ? Py_None : a[11]);
         PyObject *result = PyTuple_New(2);
         if (!result) throw AlreadySet{};
         PyTuple_SET_ITEM(result, 0, out.take());

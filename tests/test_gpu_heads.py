@@ -695,6 +695,63 @@ def test_results_made_for_a_named_stream(rn):
         assert torch.equal(b[0], o) and torch.equal(b[1], l) and not bool(other.any())
 
 
+@pytest.mark.parametrize("op", ["rope", "append", "attn", "lse"])
+def test_results_for_a_named_stream_are_not_memory_in_use_on_the_current_one(rn, op):
+    """The current stream still has a late read and a late write of a block
+    queued that has been dropped. What a call on another stream makes, which
+    waits for none of that, must lie elsewhere."""
+    g = gen(25)
+    T, H, D = 2048, 8, 128
+    q, k = (normal(g, T, H, D, dt=torch.bfloat16) for _ in range(2))
+    pos, f = torch.arange(T, device="cuda"), freqs(64)
+    kc, vc, table, ln = paged(g, [T], 16, H, D, torch.bfloat16)
+    cu, slots = starts([T]), torch.arange(T, device="cuda")
+    lse = torch.empty(T, H, device="cuda")
+    out = torch.empty_like(q)
+
+    def call(**kw):
+        if op == "rope":
+            return rn.rope_fwd(q, None, pos, f, **kw)[0]
+        if op == "append":
+            return rn.paged_kv_append(k, k, kc, vc, slots, pos, f, q=q, **kw)
+        if op == "attn":
+            return rn.paged_attn_fwd(q, kc, vc, table, ln, cu, max_q=T, max_kv=T, lse=lse, **kw)[0]
+        return rn.paged_attn_fwd(q, kc, vc, table, ln, cu, max_q=T, max_kv=T, lse=True, out=out, **kw)[1]
+
+    want = call()
+    kept = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        block = torch.full_like(want, 3.0)  # of the result's size: the next one of this pool
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        kept.copy_(block)
+        block.fill_(5.0)
+        del block
+        got = call(stream=handle)
+        torch.cuda.synchronize()
+        assert bool((kept == 3.0).all()) and torch.equal(got, want)
+        del got
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])
+def test_results_on_the_default_streams_by_handle(rn, handle):
+    """CUDA's handles of the legacy default stream (0 and 1) and of the
+    thread's own default one (2)."""
+    g = gen(26)
+    q, pos, f = normal(g, 9, 4, 64), torch.arange(9, device="cuda"), freqs(32)
+    want = rn.rope_fwd(q, None, pos, f)[0]
+    torch.cuda.synchronize()
+    got = rn.rope_fwd(q, None, pos, f, stream=handle)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del got
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
 def test_append_and_rope_in_a_graph(rn):
     g = gen(23)
     T, H, D = 33, 4, 64
