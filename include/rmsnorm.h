@@ -432,7 +432,8 @@ typedef struct {
     float scale;                /* > 0: scores are scale * q . k               */
     int32_t batch, table_width, q_heads, head_dim;
     int32_t max_q;              /* no sequence has more new tokens             */
-    int32_t max_kv;             /* no sequence is longer                       */
+    int32_t max_kv;             /* no sequence is longer; the work is cut by it,
+                                   so a bound far above the lengths costs time */
     int32_t causal;
     int32_t dtype;              /* RMSNORM_BF16 or RMSNORM_F16                 */
 } paged_attn_call_t;

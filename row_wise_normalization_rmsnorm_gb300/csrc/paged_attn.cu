@@ -57,6 +57,7 @@ constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kerne
 constexpr int kClusterMost = 16;           // CTAs of a cluster (over 8: by opt-in)
 constexpr int kJoinTiles = 4;              // key tiles that the join's kernel takes as long as
 constexpr int kDecodeChunk = 16;           // key tiles of a decoding item, where there are several a CTA
+constexpr int kDecodeItems = 32;           // and at most that many items a CTA
 constexpr int kAskAhead = 2;              // key tiles before an item's end to ask for the next one at
 constexpr float kRescale = 8.f;           // log2 of how far a row's reference maximum may lag
 
@@ -1337,8 +1338,16 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
         // 129 -> 132, 161 -> 176, 300 -> 304). Rows by the hundred lose more
         // with their partial results (chunks of 512 over 8192: 124 -> 147 us in
         // two).
-        k.splits = (int)((tiles + kDecodeChunk - 1) / kDecodeChunk);
-        k.chunk = kDecodeChunk * kKeyTile;
+        // max_kv is a bound that the lengths may be far below (one captured call
+        // for every length): the number of items is held, and with it the
+        // workspace and the empty items, each of which a CTA asks for and drops.
+        // Beyond 32 a CTA the items get longer instead. (64 sequences of 964 to
+        // 8192 keys, 193 us: called with max_kv 2^17 219 us, as without the limit;
+        // with 2^20 225 us and 20 MB, against 532 us and 541 MB.)
+        const int64_t most = kDecodeItems * slots / ctas;
+        const int64_t per_split = std::max((int64_t)kDecodeChunk, (tiles + most - 1) / most);
+        k.splits = (int)((tiles + per_split - 1) / per_split);
+        k.chunk = (int)(per_split * kKeyTile);
     }
     k.workspace = 0;
     if (k.splits > 1 && !k.cluster) {

@@ -427,6 +427,40 @@ def test_attention_many_items(rn, nq, lens, hq, hk, D, page):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("nq,lens,hq,hk,max_kv", [
+    ([1] * 40, [5000 - 97 * i for i in range(40)], 16, 8, 2 ** 20),     # more than one CTA a place, lengths far below
+    ([1] * 24, [4200, 17, 900, 5001] * 6, 16, 8, 2 ** 18),              # the same in the order of their lengths
+    ([2] * 70, [1, 2100, 350, 0, 4097] * 14, 16, 16, 2 ** 22),
+    ([1], [4095], 8, 2, 2 ** 21), ([90, 200], [500, 3000], 4, 2, 2 ** 21),
+])
+def test_attention_with_a_bound_far_above_the_lengths(rn, nq, lens, hq, hk, max_kv):
+    """max_kv is the largest length of all replays of a captured call: results
+    and the memory taken do not go by it."""
+    g = gen(27)
+    D, page = 64, 16
+    kc, vc, table, ln = paged(g, lens, page, hk, D, torch.bfloat16, fill=float("nan"))
+    wide = torch.full((len(lens), max_kv // page), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = normal(g, sum(nq), hq, D, dt=torch.bfloat16)
+    out, lse = rn.paged_attn_fwd(q, kc, vc, wide, ln, starts(nq), max_q=max(nq), max_kv=max_kv, lse=True)
+    o, l, bo, bl = attended(q, kc, vc, table, lens, nq, True, 1 / math.sqrt(D))
+    near(out, o, bo)
+    some = torch.isfinite(l)
+    assert bool((lse[~some] == -math.inf).all())
+    near(lse[some], l[some], bl[some])
+
+
+def test_attention_workspace_is_bounded_in_max_kv(rn):
+    """Partial results of at most 32 items for each CTA that the device holds
+    (two of 64 rows an SM), whatever the bound on the lengths."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    D = 128
+    most = 32 * (2 * sms) * 64 * (D + 1) * 4 + 512
+    for batch, hq, hk, max_q in ((128, 64, 8, 1), (128, 64, 8, 4), (40, 16, 8, 8), (24, 32, 8, 1), (1, 8, 1, 8), (7, 8, 8, 64)):
+        for max_kv in (4096, 8192, 2 ** 15, 2 ** 20, 2 ** 30):
+            assert rn.paged_attn_workspace_bytes(batch * max_q, batch, hq, hk, D, max_q, max_kv) <= most
+
+
 @pytest.mark.parametrize("fill", [None, float("nan")])
 @pytest.mark.parametrize("hq,hk,D,page", [(128, 8, 112, 256), (24, 8, 128, 256), (16, 8, 64, 128), (32, 8, 128, 16)])
 def test_attention_last_piece_of_one_or_four_tiles(rn, fill, hq, hk, D, page):
