@@ -477,6 +477,24 @@ rmsnorm_status_t paged_attn_fwd(const paged_attn_call_t *call, rmsnorm_stream_t 
  * 0 for invalid sizes, without a device, or where none is needed. */
 size_t paged_attn_workspace_bytes(const paged_attn_call_t *call);
 
+/* How paged_attn_fwd cuts a call. */
+typedef struct {
+    int32_t row_tiles;   /* row tiles a CTA takes: 1 (64 rows) or 2 (128 rows each) */
+    int32_t tile_tokens; /* tokens of a row tile                                    */
+    int32_t q_tiles;     /* CTAs over max_q new tokens                              */
+    int32_t splits;      /* pieces that max_kv keys are cut into                    */
+    int32_t chunk;       /* keys of a piece (0: one piece)                          */
+    int32_t clustered;   /* the pieces of a row are the CTAs of a cluster           */
+    int64_t workspace_bytes;
+} paged_attn_plan_t;
+
+/* The cut for the call's sizes (as for paged_attn_workspace_bytes; tokens,
+ * batch and max_q positive), launching nothing. num_sms > 0: for a device of
+ * that many SMs of which clusters[s] (HOST pointer, s = 0 .. 16) clusters of s
+ * CTAs, two an SM, are held at once: no device is needed. 0: the current one. */
+rmsnorm_status_t paged_attn_plan_query(const paged_attn_call_t *call, int32_t num_sms, const int32_t *clusters,
+                                       paged_attn_plan_t *plan);
+
 /* ------------------------------------------------------------------------
  * Plans: which kernel runs. Exposed for tests and benchmarks (the analogue
  * of the A/B toggles of Liger-Kernel PR #1388, "Behavior when the fast path

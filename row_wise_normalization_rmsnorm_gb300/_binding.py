@@ -96,6 +96,7 @@ SIGNATURES = {
     "paged_kv_append": (_i, [_vp, ctypes.c_char_p, _vp]),
     "paged_attn_fwd": (_i, [_vp, _vp]),
     "paged_attn_workspace_bytes": (_sz, [_vp]),
+    "paged_attn_plan_query": (_i, [_vp, _i, _vp, _vp]),
     "rmsnorm_status_string": (ctypes.c_char_p, [_i]),
     "rmsnorm_last_cuda_error": (_i, []),
     "rmsnorm_self_check": (_i, []),

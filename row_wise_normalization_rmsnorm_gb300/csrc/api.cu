@@ -374,12 +374,13 @@ static cudaError_t device_sms(int *dev_out, int *sms_out) {
     return cudaSuccess;
 }
 
-// The current device's SM count and status word, for the entry points of
-// other translation units.
-int current_device(int *sms, int **status) {
+// The current device's SM count, status word and index, for the entry points
+// of other translation units.
+int current_device(int *sms, int **status, int *dev_out) {
     int dev = 0;
     cudaError_t e = device_sms(&dev, sms);
     if (e == cudaSuccess && status) e = status_word(dev, status);
+    if (e == cudaSuccess && dev_out) *dev_out = dev;
     return (int)e;
 }
 

@@ -10,7 +10,8 @@
 namespace rmsn {
 
 void set_last_cuda_error(int e);                // api.cu
-int current_device(int *sms, int **status);     // api.cu: cudaError_t
+// api.cu: cudaError_t; status and dev may be NULL
+int current_device(int *sms, int **status, int *dev = nullptr);
 int allow_staged_smem(const void *k);           // api.cu: cudaError_t
 
 inline rmsnorm_status_t head_cuda_fail(int e) {

@@ -1298,7 +1298,8 @@ struct AttnCut {
     size_t workspace;
 };
 
-static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
+// held[s]: clusters of s CTAs that the device holds at once.
+static AttnCut attn_cut(const paged_attn_call_t &c, int sms, const int32_t *held) {
     AttnCut k;
     const int64_t group = c.q_heads / c.cache.heads;
     const int64_t rows = (int64_t)c.max_q * group;
@@ -1320,11 +1321,13 @@ static AttnCut attn_cut(const paged_attn_call_t &c, int sms) {
     if (want > 1) {
         int64_t per_split = (tiles + want - 1) / want;
         // A cluster joins its splits itself; otherwise a second kernel does,
-        // which takes as long as a few key tiles. A cluster lies in one of
-        // eight parts of the device, two CTAs an SM; its size is such that
-        // they all fit at once.
+        // which takes as long as a few key tiles. A cluster lies in one part of
+        // the device (which has parts of unequal sizes: 14 clusters of 16, not 16);
+        // its size is such that they all fit at once (two sequences of 8192
+        // keys, 8 key heads: 16 clusters of 16, two of them late, 27.4 us; of 13,
+        // 17.5; five sequences: 40 clusters of 7, of which 38 fit, 50.7, of 6 32.2).
         int64_t size = kClusterMost;
-        while (size > 1 && 8 * (sms / 4 / size) < ctas) --size;
+        while (size > 1 && held[size] < ctas) --size;
         const int64_t per_cluster = (tiles + size - 1) / size;
         k.cluster = k.nq == 1 && size > 1 && per_cluster - per_split <= kJoinTiles;
         if (k.cluster && per_split < per_cluster) per_split = per_cluster;
@@ -1387,6 +1390,45 @@ static int launch_attn(const AttnParams &p, const CUtensorMap (&maps)[3], unsign
     return (int)cudaLaunchKernelEx(&lc.cfg, kernel, p, maps[0], maps[1], maps[2]);
 }
 
+// attn_cut's `held` for the current device, asked once per device and head
+// size: [kClusterMost + 1] counts; 0 where the device has no room or no answer,
+// and the join's kernel serves. The runtime takes any kernel with tensor memory
+// for one CTA an SM (7 clusters of 16 on a GB300, where 14 run at once, as CTAs
+// that noted their start and end showed), so it is asked about one without:
+// never launched, with the threads, shared memory and bound on registers of
+// paged_attn<T, DP, 1, true>, whose 256 columns are half an SM's.
+__global__ void __launch_bounds__(256, 2) attn_cluster_room() {}
+
+template <int DP> static const int32_t *clusters_held(int dev, int sms) {
+    using S = AttnShape<DP, 1>;
+    static_assert(S::kThreads == 256 && S::kCols <= 256, "two CTAs an SM");
+    static std::mutex mu;
+    static int32_t held[64][kClusterMost + 1];
+    static bool asked[64];
+    std::lock_guard<std::mutex> lk(mu);
+    if (!asked[dev]) {
+        auto *kernel = attn_cluster_room;
+        bool ok = allow_staged_smem(reinterpret_cast<const void *>(kernel)) == 0;
+        const bool wide = ok && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+        for (int size = 2; ok && size <= (wide ? kClusterMost : 8); ++size) {
+            LaunchCfg lc((unsigned)(size * sms), S::kThreads, S::kSmem, nullptr, (unsigned)size, false);
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &lc.cfg) == cudaSuccess) held[dev][size] = n;
+        }
+        (void)cudaGetLastError();
+        asked[dev] = true;
+    }
+    return held[dev];
+}
+
+// The cut of a call on the current device; a cudaError_t.
+static int cut_here(const paged_attn_call_t &c, AttnCut &cut, int **status) {
+    int dev = 0, sms = 0;
+    const int e = current_device(&sms, status, &dev);
+    if (e == 0) cut = attn_cut(c, sms, c.head_dim > 64 ? clusters_held<128>(dev, sms) : clusters_held<64>(dev, sms));
+    return e;
+}
+
 template <typename T, int DP>
 static int launch_attn_d(const AttnCut &k, const AttnParams &p, const CUtensorMap (&maps)[3], unsigned grid, cudaStream_t s) {
     if (k.nq == 2) return launch_attn<T, DP, 2, false>(p, maps, grid, s);
@@ -1421,12 +1463,12 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     if (!empty && (!legal(pc.k, pc.k_page, pc.k_slot, pc.k_head) || !legal(pc.v, pc.v_page, pc.v_slot, pc.v_head)))
         return RMSNORM_ERR_UNSUPPORTED;
 
-    int sms = 0, *status = nullptr;
-    int e = current_device(&sms, &status);
-    if (e != 0) return head_cuda_fail(e);
     paged_attn_call_t cc = c;
     if (empty) cc.max_kv = 0;
-    const AttnCut cut = attn_cut(cc, sms);
+    AttnCut cut;
+    int *status = nullptr;
+    const int e = cut_here(cc, cut, &status);
+    if (e != 0) return head_cuda_fail(e);
 
     AttnParams p;
     std::memset(&p, 0, sizeof p);
@@ -1535,7 +1577,24 @@ extern "C" rmsnorm_status_t paged_attn_fwd(const paged_attn_call_t *call, rmsnor
 extern "C" size_t paged_attn_workspace_bytes(const paged_attn_call_t *call) {
     if (!call || attn_sizes(*call) != RMSNORM_SUCCESS) return 0;
     if (call->tokens == 0 || call->batch == 0 || call->max_q == 0) return 0;
-    int sms = 0;
-    if (current_device(&sms, nullptr) != 0) return 0;
-    return attn_cut(*call, sms).workspace;
+    AttnCut cut;
+    return cut_here(*call, cut, nullptr) == 0 ? cut.workspace : 0;
+}
+
+extern "C" rmsnorm_status_t paged_attn_plan_query(const paged_attn_call_t *call, int32_t num_sms, const int32_t *clusters,
+                                                  paged_attn_plan_t *plan) {
+    if (!call || !plan || (num_sms > 0 && !clusters)) return RMSNORM_ERR_INVALID_ARG;
+    const rmsnorm_status_t st = attn_sizes(*call);
+    if (st != RMSNORM_SUCCESS) return st;
+    if (call->tokens == 0 || call->batch == 0 || call->max_q == 0) return RMSNORM_ERR_INVALID_ARG;
+    AttnCut cut;
+    if (num_sms > 0) {
+        cut = attn_cut(*call, num_sms, clusters);
+    } else {
+        const int e = cut_here(*call, cut, nullptr);
+        if (e != 0) return head_cuda_fail(e);
+    }
+    *plan = paged_attn_plan_t{cut.nq, cut.tile_toks, cut.q_tiles, cut.splits, cut.chunk, cut.cluster ? 1 : 0,
+                              (int64_t)cut.workspace};
+    return RMSNORM_SUCCESS;
 }

@@ -450,6 +450,17 @@ def test_attention_with_a_bound_far_above_the_lengths(rn, nq, lens, hq, hk, max_
     near(lse[some], l[some], bl[some])
 
 
+@pytest.mark.parametrize("batch,hk", [(1, 13), (7, 2), (15, 1), (4, 4), (19, 1), (1, 23), (5, 6), (6, 8)])
+@pytest.mark.parametrize("kv", [2100, 9000])
+def test_attention_as_many_clusters_as_the_device_holds(rn, batch, hk, kv):
+    """Numbers of clusters around those that run at once."""
+    g = gen(batch * hk + kv)
+    lens = [kv - 97 * i for i in range(batch)]
+    kc, vc, table, ln = paged(g, lens, 16, hk, 128, torch.bfloat16, fill=float("nan"))
+    q = normal(g, batch, 2 * hk, 128, dt=torch.bfloat16)
+    check_attention(rn, q, kc, vc, table, ln, [1] * batch)
+
+
 def test_attention_workspace_is_bounded_in_max_kv(rn):
     """Partial results of at most 32 items for each CTA that the device holds
     (two of 64 rows an SM), whatever the bound on the lengths."""

@@ -169,6 +169,62 @@ def test_attention_of_nothing_is_done(rn):
     assert rn.lib().paged_attn_workspace_bytes(ctypes.byref(attn_call(head_dim=68))) == 0
 
 
+class AttnPlan(ctypes.Structure):
+    _fields_ = [("row_tiles", _i), ("tile_tokens", _i), ("q_tiles", _i), ("splits", _i), ("chunk", _i),
+                ("clustered", _i), ("workspace_bytes", _q)]
+
+
+# clusters of 0 .. 16 CTAs that a device holds at once: as a GB300 of 152 SMs
+# answers, a device without room for any, and one of whole parts
+GB300 = [0, 304, 152, 97, 74, 58, 46, 38, 36, 30, 28, 23, 23, 19, 14, 14, 14]
+NONE = [0] * 17
+WHOLE = [0, 304] + [8 * (38 // s) for s in range(2, 17)]
+
+
+def attn_plan(rn, clusters, batch, heads, kv_heads, max_q, max_kv, sms=152):
+    p = AttnPlan()
+    c = attn_call(tokens=batch * max_q, batch=batch, q_heads=heads, cache__heads=kv_heads, max_q=max_q, max_kv=max_kv)
+    held = (_i * 17)(*clusters)
+    assert rn.lib().paged_attn_plan_query(ctypes.byref(c), sms, held, ctypes.byref(p)) == 0
+    return p
+
+
+@pytest.mark.parametrize("held", [GB300, NONE, WHOLE])
+@pytest.mark.parametrize("batch,kv_heads", [(1, 1), (1, 8), (2, 8), (15, 1), (16, 1), (5, 3), (3, 16), (6, 8), (7, 8), (19, 8)])
+def test_attention_clusters_are_as_many_as_the_device_holds(rn, held, batch, kv_heads):
+    """A row's keys are cut over a cluster only where all of the call's
+    clusters run at once; else a second kernel joins the pieces."""
+    for max_kv in (500, 4095, 8192, 20000, 32768, 65536, 2 ** 20):
+        p = attn_plan(rn, held, batch, 4 * kv_heads, kv_heads, 1, max_kv)
+        assert p.row_tiles == 1 and (p.splits - 1) * p.chunk < max_kv
+        assert p.splits == 1 or p.splits * p.chunk >= max_kv
+        if p.clustered:
+            assert 2 <= p.splits <= 16 and held[p.splits] >= batch * kv_heads and p.workspace_bytes == 0
+        else:
+            assert (p.workspace_bytes > 0) == (p.splits > 1)
+    if held == GB300 and batch * kv_heads == 16:
+        # 14 clusters of 16 are held, and of 13 enough
+        assert attn_plan(rn, held, batch, 4 * kv_heads, kv_heads, 1, 128 * 128).splits <= 13
+
+
+def test_attention_items_are_bounded_in_max_kv(rn):
+    for batch, heads, kv_heads, max_q in ((128, 64, 8, 1), (128, 64, 8, 4), (40, 16, 8, 8), (64, 32, 8, 1), (90, 7, 7, 9)):
+        for max_kv in (4096, 8192, 2 ** 15, 2 ** 20, 2 ** 30):
+            p = attn_plan(rn, GB300, batch, heads, kv_heads, max_q, max_kv)
+            assert p.splits == 1 or p.splits * batch * kv_heads * p.q_tiles <= 32 * 304
+
+
+def test_attention_plan_refuses(rn):
+    p, held = AttnPlan(), (_i * 17)(*GB300)
+    ask = rn.lib().paged_attn_plan_query
+    assert ask(None, 152, held, ctypes.byref(p)) == INVALID
+    assert ask(ctypes.byref(attn_call()), 152, held, None) == INVALID
+    assert ask(ctypes.byref(attn_call()), 152, None, ctypes.byref(p)) == INVALID
+    assert ask(ctypes.byref(attn_call(head_dim=68)), 152, held, ctypes.byref(p)) == UNSUPPORTED
+    for kw in ({"tokens": 0}, {"batch": 0}, {"max_q": 0}):
+        assert ask(ctypes.byref(attn_call(**kw)), 152, held, ctypes.byref(p)) == INVALID
+
+
 def test_library_exports_the_head_row_calls(rn):
     from row_wise_normalization_rmsnorm_gb300._binding import SIGNATURES
     for name in ("rope_fwd", "rope_bwd", "paged_kv_append", "paged_attn_fwd", "paged_attn_workspace_bytes"):
