@@ -237,7 +237,7 @@ template <typename T, int V, bool APPEND, bool NORM, bool ADJ, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas[NORM]) rope_vector(const __grid_constant__ RopeParams p) {
     constexpr int NP = V / 2, U = kRopeUnroll, CB = V * (int)sizeof(T);
     using PR = Pair<true>;
-    __shared__ float2 turn[kRopeWarps][HEAD_MAX_DIM / 2];  // (cos, sin) of the warp's token
+    __shared__ __align__(16) float2 turn[kRopeWarps][HEAD_MAX_DIM / 2];  // (cos, sin) of the warp's token
     constexpr int kDepth = kRopeDepth;
     __shared__ __align__(16) uint8_t places[kRopeWarps][kRopeDepth * kRopeUnroll * 64 * CB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
