@@ -536,9 +536,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements(const __grid_const
         for (int u = 0; u < kElemHeads; ++u) {
             if (u >= n || !out[u]) continue;
             const int h = h0 + u, sg = h < hq ? 0 : (h < hqk ? 1 : 2);
+            if (sg == 2) {  // v: copied
+                out[u][e0] = in[u][e0];
+                out[u][e1] = in[u][e1];
+                continue;
+            }
             const float a = value(u, sg, e0), b = value(u, sg, e1);
-            store_elem(out[u], e0, sg == 2 ? a : __fmaf_rn(-b, s, a * c));
-            store_elem(out[u], e1, sg == 2 ? b : __fmaf_rn(a, s, b * c));
+            store_elem(out[u], e0, __fmaf_rn(-b, s, a * c));
+            store_elem(out[u], e1, __fmaf_rn(a, s, b * c));
         }
     }
     for (int i = 2 * p.half_dim + lane; i < p.head_dim; i += 32) {
@@ -546,7 +551,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements(const __grid_const
         for (int u = 0; u < kElemHeads; ++u) {
             if (u >= n || !out[u]) continue;
             const int h = h0 + u, sg = h < hq ? 0 : (h < hqk ? 1 : 2);
-            store_elem(out[u], i, value(u, sg, i));
+            // (what passes as it is keeps its bits, a NaN's payload too)
+            if (APPEND && sg < 2 && p.w[sg])
+                store_elem(out[u], i, value(u, sg, i));
+            else
+                out[u][i] = in[u][i];
         }
     }
 }

@@ -267,6 +267,42 @@ def test_append_into_one_tensor_of_keys_and_values(rn):
     assert torch.equal(odd[0], plain[0]) and torch.equal(odd[1], plain[1])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("off,D,R", [(0, 64, 32), (1, 64, 32), (0, 50, 22), (0, 33, 10), (1, 33, 0)])
+def test_what_passes_unturned_keeps_its_bits(rn, dt, off, D, R):
+    """v, and q and k values that are neither normalised nor turned, are every
+    bit pattern of their type, NaN payloads and signs among them, in the
+    vectorised and the element-wise kernel."""
+    t = TYPES[dt]
+    word = torch.int32 if dt == "f32" else torch.int16
+    g = gen(28)
+    T, H, page = 65, 3, 8
+    pages = -(-T // page) + 1
+
+    def bits(*shape):
+        info = torch.iinfo(word)
+        x = torch.randint(info.min, info.max + 1, shape, generator=g, device="cuda", dtype=torch.int64).to(word)
+        return offset_view(x, off).view(t)
+
+    q, k, v = bits(T, H, D), bits(T, H, D), bits(T, H, D)
+    assert bool(torch.isnan(v).any())
+    kc, vc = (torch.zeros(pages, page, H, D, dtype=t, device="cuda") for _ in range(2))
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:T]
+    pos, f = positions(g, 1, T, torch.int32), freqs(max(R // 2, 1))
+    rope = dict(positions=pos, inv_freq=f) if R else {}
+    got = rn.paged_kv_append(k, v, kc, vc, slots, q=q, **rope)
+
+    def same(a, b):
+        return torch.equal(a.contiguous().view(word), b.contiguous().view(word))
+
+    assert same(vc.view(-1, H, D)[slots], v)
+    assert same(kc.view(-1, H, D)[slots][..., R:], k[..., R:]) and same(got[..., R:], q[..., R:])
+    if R:
+        for fn in (rn.rope_fwd, rn.rope_bwd):
+            for x, y in zip((q, k), fn(q, k, pos, f)):
+                assert same(y[..., R:], x[..., R:])
+
+
 def test_append_far_into_a_large_cache(rn):
     """Offsets past 2^32 bytes and 2^31 elements."""
     T, H, D, page = 3, 8, 128, 64
