@@ -135,6 +135,26 @@ def test_rope_far_and_negative_positions(rn, dt, ptype):
     near(y, ref, half_step(t) * ref.abs() + 16 * U * mag)
 
 
+@pytest.mark.parametrize("pairing", ["half", "adjacent"])
+def test_rope_angles_keep_the_bits_that_fp32_holds(rn, pairing):
+    """Pairs (1, 0) come back as (cos, sin). In units of u, for values up to 1:
+    sincospi 1 (an ulp below 1), the sum with the angle's lower bits 1/2, the
+    integer product's 2^-32 of a turn below 0.03. An angle held in one fp32
+    fraction of a turn adds up to pi / 2."""
+    g = gen(29)
+    T, H, D = 8192, 1, 256
+    pos = torch.randint(-2 ** 24, 2 ** 24, (T,), generator=g, device="cuda", dtype=torch.int64)
+    f = freqs(128)
+    x = torch.zeros(T, H, D, device="cuda")
+    first = torch.arange(128, device="cuda") * (1 if pairing == "half" else 2)
+    second = first + (128 if pairing == "half" else 1)
+    x[..., first] = 1.0
+    y = rn.rope_fwd(x, None, pos, f, pairing=pairing)[0].double()
+    ang = pos.double()[:, None, None] * f.double()  # exact: 25 and 24 bits
+    near(y[..., first], ang.cos(), torch.full_like(ang, 1.6 * U))
+    near(y[..., second], ang.sin(), torch.full_like(ang, 1.6 * U))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_rope_layouts_give_the_same_bits(rn, dt):
     """In place, strided, off a 16-byte boundary and transposed layouts, int64
