@@ -322,7 +322,8 @@ size_t rmsnorm_bwd_call_workspace_bytes(const void *dy, const void *dresidual_ou
  *
  * A head-row array is [T, heads, head_dim] with head_dim contiguous and any
  * token and head strides (in elements), e.g. one part of a fused qkv
- * projection. A call is a structure that the library reads before it
+ * projection. What is written (rows, a cache) has no stride of 0 where its
+ * dimension has several entries (INVALID_ARG). A call is a structure that the library reads before it
  * returns; all pointers in it are device pointers except where noted.
  * Streams, errors and the device follow the rules at the top of this file.
  * --------------------------------------------------------------------- */

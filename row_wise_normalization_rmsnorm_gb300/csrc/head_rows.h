@@ -24,4 +24,8 @@ inline bool on(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 // A stride counts only where its dimension has more than one entry.
 inline int64_t stride_of(int64_t stride, int64_t entries) { return entries > 1 ? stride : 0; }
 
+// False where a written dimension's entries would share their place: the rows
+// would overwrite one another in no order.
+inline bool apart(int64_t stride, int64_t entries) { return entries <= 1 || stride != 0; }
+
 }  // namespace rmsn

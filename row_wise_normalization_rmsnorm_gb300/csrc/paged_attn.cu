@@ -1451,7 +1451,8 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     if (c.workspace && !on(c.workspace, 16)) return RMSNORM_ERR_WORKSPACE;
     if (c.tokens == 0 || c.batch == 0 || c.max_q == 0) return RMSNORM_SUCCESS;
     if (!c.q || !c.out || !on(c.q, 2) || !on(c.out, 2) || !on(c.lse, 4) || !c.kv_lens || !c.cu_q ||
-        !on(c.block_table, 4) || !on(c.kv_lens, 4) || !on(c.cu_q, 4))
+        !on(c.block_table, 4) || !on(c.kv_lens, 4) || !on(c.cu_q, 4) || !apart(c.out_token, c.tokens) ||
+        !apart(c.out_head, c.q_heads))
         return RMSNORM_ERR_INVALID_ARG;
     // without a page every sequence is empty; the kernel then reads no table
     const bool empty = pc.pages == 0 || c.table_width == 0 || c.max_kv == 0;

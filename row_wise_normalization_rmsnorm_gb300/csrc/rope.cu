@@ -640,6 +640,9 @@ static HeadSeg segment(const rope_rows_t &r, int heads, int64_t tokens, int es) 
     return g;
 }
 
+static bool rows_apart(const rope_rows_t &r, int heads, int64_t tokens) {
+    return heads == 0 || (apart(r.out_token, tokens) && apart(r.out_head, heads));
+}
 static bool seg_on(const HeadSeg &g, uintptr_t a) { return g.heads == 0 || (on(g.in, a) && on(g.out, a)); }
 static bool seg_vec(const HeadSeg &g, int vec) {
     return g.heads == 0 || (on(g.in, vec) && on(g.out, vec) && g.in_token % vec == 0 && g.in_head % vec == 0 &&
@@ -703,6 +706,7 @@ static rmsnorm_status_t rope_impl(const rope_call_t *c, const uint8_t *axes, flo
     const int es = elem_bytes(c->dtype);
     if (!c->angles.positions || !c->q.in || !c->q.out || (c->k_heads && (!c->k.in || !c->k.out)))
         return RMSNORM_ERR_INVALID_ARG;
+    if (!rows_apart(c->q, c->q_heads, c->tokens) || !rows_apart(c->k, c->k_heads, c->tokens)) return RMSNORM_ERR_INVALID_ARG;
     p.seg[0] = segment(c->q, c->q_heads, c->tokens, es);
     p.seg[1] = segment(c->k, c->k_heads, c->tokens, es);
     if (!seg_on(p.seg[0], es) || !seg_on(p.seg[1], es)) return RMSNORM_ERR_INVALID_ARG;
@@ -742,6 +746,10 @@ extern "C" rmsnorm_status_t paged_kv_append(const paged_append_call_t *c, const 
     const int es = elem_bytes(base);
     if (!c->k.in || !c->v.in || !c->slots || !on(c->slots, 8) || !pc.k || !pc.v ||
         (c->q_heads && (!c->q.in || !c->q.out)))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (!rows_apart(c->q, c->q_heads, c->tokens) || !apart(pc.k_page, pc.pages) || !apart(pc.k_slot, pc.page_size) ||
+        !apart(pc.k_head, pc.heads) || !apart(pc.v_page, pc.pages) || !apart(pc.v_slot, pc.page_size) ||
+        !apart(pc.v_head, pc.heads))
         return RMSNORM_ERR_INVALID_ARG;
     const uintptr_t wes = (c->dtype & RMSNORM_WEIGHT_F32) ? 4 : (uintptr_t)es;
     if (!on(c->wq, wes) || !on(c->wk, wes)) return RMSNORM_ERR_INVALID_ARG;

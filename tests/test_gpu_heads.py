@@ -886,6 +886,30 @@ def test_append_and_rope_in_a_graph(rn):
     near(b, q.double(), 8 * half_step(torch.float16) * (q.double().abs() + q.double().abs().roll(D // 2, -1)))
 
 
+def test_results_that_overlap_themselves_are_refused(rn):
+    """An expanded tensor as a result or a cache; as an input it is fine, and
+    so is a stride of 0 over a single entry."""
+    g = gen(30)
+    t = torch.bfloat16
+    kc, vc, table, ln = paged(g, [20], 16, 2, 64, t)
+    q, k = normal(g, 4, 4, 64, dt=t), normal(g, 4, 2, 64, dt=t)
+    p, f, s = torch.arange(4, device="cuda"), freqs(32), torch.arange(4, device="cuda")
+    cu, kw = starts([4]), dict(max_q=4, max_kv=20)
+    for out in (q[:1].expand(4, 4, 64), q[:, :1].expand(4, 4, 64)):
+        for call in (lambda: rn.rope_fwd(q, None, p, f, q_out=out), lambda: rn.rope_bwd(q, None, p, f, dq_out=out),
+                     lambda: rn.paged_kv_append(k, k, kc, vc, s, q=q, q_out=out),
+                     lambda: rn.paged_attn_fwd(q, kc, vc, table, ln, cu, out=out, **kw)):
+            with pytest.raises(rn.RMSNormError, match="INVALID"):
+                call()
+    for c in (kc[:1].expand_as(kc), kc[:, :1].expand_as(kc), kc[:, :, :1].expand_as(kc)):
+        for pair in ((c, vc), (kc, c)):
+            with pytest.raises(rn.RMSNormError, match="INVALID"):
+                rn.paged_kv_append(k, k, *pair, s)
+    assert torch.equal(rn.rope_fwd(q[:1].expand(4, 4, 64), None, p, f)[0], rn.rope_fwd(q[[0] * 4], None, p, f)[0])
+    one = torch.empty(1, 1, 64, dtype=t, device="cuda").as_strided((1, 1, 64), (0, 0, 1))
+    assert torch.equal(rn.rope_fwd(q[:1, :1], None, p[:1], f, q_out=one)[0], rn.rope_fwd(q[:1, :1], None, p[:1], f)[0])
+
+
 def test_attention_refusals(rn):
     g = gen(19)
     kc, vc, table, ln = paged(g, [20], 16, 2, 64, torch.bfloat16)

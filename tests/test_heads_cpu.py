@@ -122,6 +122,25 @@ def test_append_refuses(rn, bad):
     assert rn.lib().paged_kv_append(ctypes.byref(append_call(**bad)), None, None) == INVALID
 
 
+@pytest.mark.parametrize("bad", [{"q__out_token": 0}, {"q__out_head": 0}, {"k__out_token": 0}, {"k__out_head": 0}])
+def test_rope_refuses_rows_that_overwrite_one_another(rn, bad):
+    assert rn.lib().rope_fwd(ctypes.byref(rope_call(**bad)), None, None) == INVALID
+    assert rn.lib().rope_bwd(ctypes.byref(rope_call(**bad)), None, None) == INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    {"q__out_token": 0}, {"q__out_head": 0}, {"cache__k_page": 0}, {"cache__k_slot": 0}, {"cache__k_head": 0},
+    {"cache__v_page": 0}, {"cache__v_slot": 0}, {"cache__v_head": 0},
+])
+def test_append_refuses_places_that_overwrite_one_another(rn, bad):
+    assert rn.lib().paged_kv_append(ctypes.byref(append_call(**bad)), None, None) == INVALID
+
+
+@pytest.mark.parametrize("bad", [{"out_token": 0}, {"out_head": 0}])
+def test_attention_refuses_rows_that_overwrite_one_another(rn, bad):
+    assert rn.lib().paged_attn_fwd(ctypes.byref(attn_call(**bad)), None) == INVALID
+
+
 def test_append_of_no_tokens_is_done(rn):
     assert rn.lib().paged_kv_append(ctypes.byref(append_call(tokens=0, slots=None)), None, None) == 0
     assert rn.lib().paged_kv_append(None, None, None) == INVALID
