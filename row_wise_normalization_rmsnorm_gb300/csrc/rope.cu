@@ -737,7 +737,7 @@ extern "C" rmsnorm_status_t paged_kv_append(const paged_append_call_t *c, const 
     if (c->head_dim < 1 || c->head_dim > HEAD_MAX_DIM || c->tokens < 0 || c->tokens > 0x7fffffffLL ||
         c->q_heads < 0 || c->q_heads > 65535 || pc.heads < 1 || pc.heads > 65535)
         return RMSNORM_ERR_INVALID_ARG;
-    if (pc.page_size < 1 || pc.pages < 0 || pc.pages > (int64_t)1 << 40) return RMSNORM_ERR_INVALID_ARG;
+    if (pc.page_size < 1 || pc.pages < 0 || pc.pages > INT64_MAX / pc.page_size) return RMSNORM_ERR_INVALID_ARG;
     if (!std::isfinite(c->eps) || !std::isfinite(c->offset) || c->eps < 0.f) return RMSNORM_ERR_INVALID_ARG;
     RopeParams p;
     std::memset(&p, 0, sizeof p);

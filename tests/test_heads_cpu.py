@@ -131,6 +131,7 @@ def test_rope_refuses_rows_that_overwrite_one_another(rn, bad):
 @pytest.mark.parametrize("bad", [
     {"q__out_token": 0}, {"q__out_head": 0}, {"cache__k_page": 0}, {"cache__k_slot": 0}, {"cache__k_head": 0},
     {"cache__v_page": 0}, {"cache__v_slot": 0}, {"cache__v_head": 0},
+    {"cache__pages": 2 ** 40, "cache__page_size": 2 ** 30},   # places that 64 bits do not count
 ])
 def test_append_refuses_places_that_overwrite_one_another(rn, bad):
     assert rn.lib().paged_kv_append(ctypes.byref(append_call(**bad)), None, None) == INVALID
