@@ -28,6 +28,7 @@ LIB = os.path.join(HERE, "librmsnorm_gb300.so")
 HEADER = os.path.join(ROOT, "include", "rmsnorm.h")
 EXT = os.path.join(HERE, "_heads_ext.so")
 EXT_SOURCE = os.path.join(CSRC, "heads_ext.cpp")
+EXT_STAMP = os.path.join(BUILD, "heads_ext.stamp")  # the Python and PyTorch that EXT was built against
 
 SOURCES = ["api.cu", "fwd_bf16.cu", "fwd_f32.cu", "fwd_f16.cu", "fwd_bf16w32.cu", "fwd_f16w32.cu",
            "fwd8_bf16.cu", "fwd8_f16.cu", "fwd8_f32.cu", "fwd8_bf16w32.cu", "fwd8_f16w32.cu", "ln_bf16.cu", "ln_f16.cu", "ln_f32.cu", "ln_bf16w32.cu", "ln_f16w32.cu",
@@ -63,16 +64,52 @@ def _torch_dir() -> str:
     return os.path.dirname(spec.origin)
 
 
+def _python_include() -> str:
+    return sysconfig.get_paths()["include"]
+
+
+def _ext_missing() -> str | None:
+    """What the Python module's build lacks here (None: nothing). The C
+    library needs none of it."""
+    try:
+        torch = _torch_dir()
+    except RuntimeError as e:
+        return str(e)
+    if not os.path.exists(os.path.join(torch, "include", "ATen", "core", "Tensor.h")):
+        return "PyTorch's headers are missing"
+    if not os.path.exists(os.path.join(_python_include(), "Python.h")):
+        return "Python.h is missing"
+    return None if shutil.which("g++") else "g++ is missing"
+
+
+def _ext_for() -> str:
+    """The Python and PyTorch that a module built now is for ("": none)."""
+    try:
+        torch = _torch_dir()
+    except RuntimeError:
+        return ""
+    return "\n".join([str(sysconfig.get_config_var("SOABI")), torch, _text(os.path.join(torch, "version.py"))])
+
+
+def _text(p: str) -> str:
+    try:
+        with open(p, encoding="utf-8") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _ext_stale(force: bool) -> bool:
     deps = [EXT_SOURCE, HEADER, os.path.abspath(__file__)]
-    return force or not os.path.exists(EXT) or max(_mtime(p) for p in deps) > _mtime(EXT)
+    return (force or not os.path.exists(EXT) or max(_mtime(p) for p in deps) > _mtime(EXT)
+            or _text(EXT_STAMP) != _ext_for())
 
 
 def _compile_ext() -> str:
     t = _torch_dir()
     obj = os.path.join(BUILD, "heads_ext.o")
     inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
-           os.path.join(_cuda_home(), "include"), sysconfig.get_paths()["include"]]
+           os.path.join(_cuda_home(), "include"), _python_include()]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(a for d in inc for a in ("-isystem", d)),
            "-c", EXT_SOURCE, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -92,6 +129,8 @@ def _link_ext(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of heads_ext failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
+    with open(EXT_STAMP, "w", encoding="utf-8") as f:
+        f.write(_ext_for())
 
 
 def _stale(force: bool) -> bool:
@@ -111,8 +150,18 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile (if any source changed) and return the library path."""
+    """Compile (if any source changed) and return the library path.
+
+    The C library needs nvcc alone. Where the Python module cannot be built,
+    the library still is, and the calls on head rows say that their module is
+    not built."""
     lib_stale, ext_stale = _stale(force), _ext_stale(force)
+    missing = _ext_missing() if ext_stale else None
+    if missing:
+        print(f"_heads_ext is not built: {missing}", file=sys.stderr)
+        if os.path.exists(EXT):  # of an older source, Python or PyTorch
+            os.remove(EXT)
+        ext_stale = False
     if not lib_stale and not ext_stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
