@@ -403,7 +403,6 @@ typedef struct {
     float eps, offset;
     int32_t q_heads, head_dim;
     int32_t dtype; /* as rope_call_t, or with RMSNORM_WEIGHT_F32: wq, wk fp32 */
-    int32_t reserved;
 } paged_append_call_t;
 
 /*

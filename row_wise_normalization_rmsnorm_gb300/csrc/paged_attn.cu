@@ -103,7 +103,7 @@ struct AttnParams {
     int64_t tokens;
     int *status;
     float c;  // scale * log2(e)
-    int batch, width, heads, kv_heads, group, head_dim, pages, page_size, box_rows;
+    int batch, width, heads, group, head_dim, pages, page_size, box_rows;
     int max_q, max_kv, causal, q_tiles, splits, chunk;  // chunk: keys a split takes
     int tile_toks;                                      // tokens a row tile takes
     int nq;                                             // row tiles a CTA takes
@@ -1514,7 +1514,6 @@ static rmsnorm_status_t attn_impl(const paged_attn_call_t &c, cudaStream_t strea
     p.batch = c.batch;
     p.width = empty ? 0 : c.table_width;
     p.heads = c.q_heads;
-    p.kv_heads = pc.heads;
     p.group = c.q_heads / pc.heads;
     p.head_dim = c.head_dim;
     p.pages = (int)pc.pages;
