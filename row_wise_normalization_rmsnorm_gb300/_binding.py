@@ -7,6 +7,7 @@ CPU fallback: if the library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -136,6 +137,40 @@ def _stream_handle(stream, device) -> int:
     return stream.cuda_stream
 
 
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """The named stream (an object or a handle) as PyTorch's."""
+    handle = _stream_handle(stream, device)
+    if handle in (0, 1):  # CUDA's two handles of the legacy default stream
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _results_of_stream(call):
+    """``call`` with its results, where ``stream`` is named, in that stream's
+    memory: the current stream's may still be in use by what was queued there
+    before its last owner dropped it, and the named stream waits for none of
+    that. The current stream is their likely reader, so they are not given out
+    again, once dropped, before it is done with them either."""
+    rows = call.__code__.co_varnames[0]
+
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        device = getattr(args[0] if args else kw.get(rows), "device", None)
+        if device is None or device.type != "cuda":
+            return call(*args, **kw)  # (refused there)
+        reader = torch.cuda.current_stream(device)
+        with torch.cuda.stream(_torch_stream(stream, device)):
+            out = call(*args, **kw)
+        given = {id(t) for t in kw.values()}
+        for t in out.values() if isinstance(out, dict) else out:
+            if isinstance(t, torch.Tensor) and id(t) not in given:
+                t.record_stream(reader)
+        return out
+    return on_stream
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     try:
         return TORCH_DTYPE[t.dtype]
@@ -228,6 +263,7 @@ def _ws(workspace):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+@_results_of_stream
 def rmsnorm_fwd(x, w, *, eps: float = 1e-6, offset: float = 0.0, y=None, rstd=None, out_dtype=None, stream=None):
     """y, rstd = RMSNorm(x) over the last dimension (llama mode); w None is
     non-affine RMSNorm (y = x * rstd). For float32 x, y may be bfloat16 or
@@ -246,6 +282,7 @@ def rmsnorm_fwd(x, w, *, eps: float = 1e-6, offset: float = 0.0, y=None, rstd=No
     return y, rstd
 
 
+@_results_of_stream
 def rmsnorm_add_fwd(x, residual, w, *, eps: float = 1e-6, offset: float = 0.0, y=None, residual_out=None,
                     rstd=None, out_dtype=None, stream=None):
     """h = x + residual (rounded), y = RMSNorm(h); returns y, h, rstd. For
@@ -271,6 +308,7 @@ def rmsnorm_add_fwd(x, residual, w, *, eps: float = 1e-6, offset: float = 0.0, y
 FP8_SCALING = {"tensor": 0, "row": 1}
 
 
+@_results_of_stream
 def rmsnorm_fwd_fp8(x, w, *, scaling="row", scale=None, residual=None, eps: float = 1e-6, offset: float = 0.0,
                     y=None, residual_out=None, rstd=None, scale_inv=None, amax=False, force_plan=-1,
                     stream=None):
@@ -321,6 +359,7 @@ def rmsnorm_fwd_fp8(x, w, *, scaling="row", scale=None, residual=None, eps: floa
             "plan": p.as_dict()}
 
 
+@_results_of_stream
 def rmsnorm_bwd(dy, x, w, rstd, *, eps: float = 1e-6, offset: float = 0.0, dx=None, dw=None, workspace=None,
                 stream=None):
     """dx, dw of RMSNorm given the forward's rstd; w None is non-affine (dw None)."""
@@ -344,6 +383,7 @@ def rmsnorm_bwd(dy, x, w, rstd, *, eps: float = 1e-6, offset: float = 0.0, dx=No
     return dx, dw
 
 
+@_results_of_stream
 def rmsnorm_add_bwd(dy, dresidual_out, h, w, rstd, *, eps: float = 1e-6, offset: float = 0.0, dx=None, dw=None,
                     workspace=None, stream=None):
     """dx (= dresidual) and dw of the fused residual-add RMSNorm; h is the forward's residual_out."""
@@ -386,6 +426,7 @@ def plan_query(op: int, M: int, N: int, dtype: int, *, aligned: bool = True, num
     return p.as_dict()
 
 
+@_results_of_stream
 def rmsnorm_fwd_ex(x, w, *, residual=None, eps=1e-6, offset=0.0, y=None, residual_out=None, rstd=None,
                    force_plan=-1, out_dtype=None, stream=None):
     """Forward with a forced plan; returns (y, residual_out or None, rstd, plan dict)."""
@@ -402,6 +443,7 @@ def rmsnorm_fwd_ex(x, w, *, residual=None, eps=1e-6, offset=0.0, y=None, residua
     return y, residual_out, rstd, p.as_dict()
 
 
+@_results_of_stream
 def rmsnorm_bwd_ex(dy, x, w, rstd, *, dresidual_out=None, fused=False, eps=1e-6, offset=0.0, dx=None, dw=None,
                    workspace=None, force_plan=-1, force_ctas=0, force_packed=-1, event_after_main=None,
                    stream=None):
@@ -422,6 +464,7 @@ def rmsnorm_bwd_ex(dy, x, w, rstd, *, dresidual_out=None, fused=False, eps=1e-6,
 
 # ------------------------------------------------------------- LayerNorm --
 
+@_results_of_stream
 def layernorm_fwd(x, gamma, beta, *, residual=None, eps: float = 1e-5, offset: float = 0.0, y=None,
                   residual_out=None, mean=None, rstd=None, force_plan=-1, stream=None):
     """LayerNorm over the last dimension: y = (h - mean) rstd (offset + gamma) + beta,
@@ -451,6 +494,7 @@ def layernorm_fwd(x, gamma, beta, *, residual=None, eps: float = 1e-5, offset: f
     return {"y": y, "residual_out": residual_out, "mean": mean, "rstd": rstd, "plan": p.as_dict()}
 
 
+@_results_of_stream
 def layernorm_bwd(dy, x, gamma, mean, rstd, *, dresidual_out=None, want_dgamma=True, want_dbeta=True,
                   eps: float = 1e-5, offset: float = 0.0, dx=None, dgamma=None, dbeta=None, workspace=None,
                   force_plan=-1, force_ctas=0, stream=None):
