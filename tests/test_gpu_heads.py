@@ -772,6 +772,42 @@ def test_calls_on_two_streams_at_once(rn):
         assert all(torch.equal(w, x) for x in side[-1])
 
 
+def test_appends_and_rotations_on_two_streams_at_once(rn):
+    """Each stream appends to its own cache and rotates in place, many times
+    over, beside the other."""
+    g = gen(31)
+    T, H, D, page, pages = 4096, 8, 128, 16, 300
+    pos, f, w = torch.arange(T, device="cuda"), freqs(64), normal(g, D)
+    sides = []
+    for _ in range(2):
+        q, k, v = (normal(g, T, H, D, dt=torch.bfloat16) for _ in range(3))
+        slots = torch.randperm(pages * page, generator=g, device="cuda")[:T]
+        caches = [torch.zeros(pages, page, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        sides.append((torch.cuda.Stream(), q, k, v, slots, caches, q.clone()))
+
+    def step(q, k, v, slots, caches, x):
+        a = rn.paged_kv_append(k, v, *caches, slots, pos, f, q=q, wq=w, wk=w)
+        rn.rope_fwd(x, None, pos, f, q_out=x)
+        rn.rope_bwd(x, None, pos, f, dq_out=x)
+        return a, x.clone()
+
+    want = []
+    for _, q, k, v, slots, caches, x in sides:
+        first = step(q, k, v, slots, caches, x.clone())
+        want.append([*first, *(c.clone() for c in caches)])
+        for c in caches:
+            c.zero_()
+    torch.cuda.synchronize()
+    got = [None, None]
+    for i in range(20):
+        for n, (s, q, k, v, slots, caches, x) in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[n] = step(q, k, v, slots, caches, x) if i == 0 else (step(q, k, v, slots, caches, x)[0], got[n][1])
+    torch.cuda.synchronize()
+    for side, w4, g2 in zip(sides, want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w4, [*g2, *side[5]]))
+
+
 def test_results_made_for_a_named_stream(rn):
     """With stream= and no result given, the call makes them and their memory
     is not handed out again while that stream still writes it."""
