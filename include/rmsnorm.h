@@ -375,9 +375,9 @@ typedef struct {
  * rope_bwd is the gradient: `in` holds the gradient of the outputs, `out`
  * receives that of the inputs (the rotation by the negative angle).
  * out may equal in (same strides); nothing else may overlap. head_dim is
- * 1 .. HEAD_MAX_DIM. Rows, strides and inv_freq on 16-byte boundaries with
- * rotary_dim and head_dim whole chunks run the vectorised kernel; anything
- * else an element-wise one.
+ * 1 .. HEAD_MAX_DIM. Rows and strides on 16-byte (or all on 8-byte)
+ * boundaries, with head_dim and half of rotary_dim whole chunks of that size,
+ * run the vectorised kernel; anything else an element-wise one.
  */
 rmsnorm_status_t rope_fwd(const rope_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream);
 rmsnorm_status_t rope_bwd(const rope_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream);
@@ -413,6 +413,9 @@ typedef struct {
  * copied. A token whose slot is negative or not below pages * page_size is
  * not appended (a padded batch); its q is still written. No two tokens may
  * have the same slot. cache.heads is the number of k and v heads.
+ * (paged_attn_fwd reads fewer caches than can be filled here: bf16 or fp16,
+ * head_dim a multiple of 8 up to 128, pages of a multiple of 8 places, bases
+ * and strides on 16-byte boundaries.)
  */
 rmsnorm_status_t paged_kv_append(const paged_append_call_t *call, const uint8_t *axes, rmsnorm_stream_t stream);
 
@@ -431,7 +434,7 @@ typedef struct {
     size_t workspace_bytes;
     float scale;                /* > 0: scores are scale * q . k               */
     int32_t batch, table_width, q_heads, head_dim;
-    int32_t max_q;              /* no sequence has more new tokens             */
+    int32_t max_q;              /* no sequence has more new tokens (as max_kv) */
     int32_t max_kv;             /* no sequence is longer; the work is cut by it,
                                    so a bound far above the lengths costs time */
     int32_t causal;
@@ -448,9 +451,9 @@ typedef struct {
  *
  * with query head h reading key head h / (q_heads / heads). A row that sees
  * no key gets o = 0 and lse = -inf. Rows of q behind the last sequence are
- * not written. Products of the storage type with fp32 sums; the softmax in
- * fp32, its weights rounded to the storage type for the second product;
- * o rounded once. out may equal q (the same strides); nothing else overlaps.
+ * not written. Products of the storage type with fp32 sums; the softmax and
+ * its sum in fp32, the weights rounded to the storage type for the second
+ * product; o rounded once. out may equal q (the same strides); nothing else overlaps.
  *
  * What lies in the cache past a sequence's length never reaches its rows,
  * infinities and NaN included. A key that later rows of the same sequence

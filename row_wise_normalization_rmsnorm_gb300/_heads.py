@@ -75,7 +75,9 @@ def paged_kv_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None
     the token is left out). k is first normalised per head where ``wk`` is
     given and rotated where ``positions`` are (as rope_fwd); q (optional) is
     normalised by ``wq`` and rotated in the same launch and returned (None
-    without q). Two tokens of a call must not share a slot."""
+    without q). Two tokens of a call must not share a slot. What paged_attn_fwd
+    reads is narrower: bf16 or fp16, D a multiple of 8 up to 128, page_size a
+    multiple of 8."""
     return (_ext or _load()).append(k, v, k_cache, v_cache, slots, positions, inv_freq, axes, pairing, q, q_out, wq, wk,
                                     eps, offset, stream)
 
@@ -90,9 +92,9 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_q, *, max_q: in
     [batch, width] names each sequence's pages, kv_lens int32 [batch] its
     length with the new tokens (already appended). Causal: a new token sees
     the keys up to itself. max_q and max_kv bound the sequences' new tokens
-    and lengths. scale defaults to 1 / sqrt(D). lse: True, or an fp32 tensor
-    [T, heads], for the log of each row's sum of exponentials (None: not
-    written). Rows behind the last sequence are left as they were.
+    and lengths (bounds far above them cost time: the work is cut by them).
+    scale defaults to 1 / sqrt(D). lse: True, or an fp32 tensor [T, heads], for
+    the log of each row's sum of exponentials (None: not written). Rows behind the last sequence are left as they were.
     workspace: a tensor of at least paged_attn_workspace_bytes() bytes."""
     return (_ext or _load()).attn(q, k_cache, v_cache, block_table, kv_lens, cu_q, max_q, max_kv, scale, causal, out, lse,
                                   workspace, stream)

@@ -38,6 +38,12 @@
 // one warp issuing matrix instructions. s and p share tensor memory (p, as the
 // 16-bit A operand of the second product, overwrites s); o accumulates in
 // tensor memory.
+//
+// Rounding: the matrix instruction takes two operands of one 16-bit type, so p
+// is rounded to v's (half a step a weight, of either sign); l sums the unrounded
+// p in fp32. Against 64 bits the results are then off by 0.0023 (rms, of the
+// result, bf16; fp16 0.00026), where rounding the result alone gives 0.0017
+// (0.0002). p in two parts would be half as many products again.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -16,9 +16,10 @@
 // computes each angle once (two a lane for 64 frequencies) and hands them round
 // in shared memory. With few tokens the heads are split over more warps.
 // Measured (of 6770 GB/s, the copy rate): 16384 tokens of 40 heads by 128, bf16,
-// 53.6 us, 93%; the append of 8192 tokens of 48 heads with their norm 37.4 us,
-// 80%; the gradient of 4096 tokens 19 us, 65%: one wave of warps, whose latency
-// is what is left there.
+// 52.9 us, 94%; the append of 8192 tokens of 48 heads with their norm 39.2 us,
+// 76%; the gradient of 4096 tokens, fp16, 18.4 us, 68%. The last two are few
+// rounds of CTAs (2048 on 760 places, 1024 on 912): the gradient's second round
+// has 112 CTAs and takes as long as one of 912.
 #include <cmath>
 #include <cstring>
 
@@ -56,7 +57,8 @@ struct RopeParams {
 
 // (Plain loads throughout: the kernel may have been launched while the one
 // before it was still writing what is read here after pdl_wait, which the
-// non-coherent path does not provide for.)
+// non-coherent path does not provide for. With them the append of 8192 tokens
+// takes 39.3 us instead of 37.6, the rotation of 16384 52.9 instead of 53.8.)
 
 // ------------------------------------------------------------- angles --
 // The angle p f is wanted modulo a turn, and fp32's p f has lost that where p
@@ -220,9 +222,11 @@ constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 // Heads of a batch, batches under way, and the CTAs an SM that the registers
 // are held to, without and with the norm. Measured together (bf16, 16384 tokens
-// of 40 heads by 128, and the append of 8192 tokens of 48 with its norm): 53.6
-// and 37.4 us; one batch of three heads in registers instead 58.5 and 40.3; four
-// batches 55.7 and 38.9; six CTAs for the norm too spill, 43.4.
+// of 40 heads by 128, and the append of 8192 tokens of 48 with its norm; before
+// the loads became plain ones): 53.6 and 37.4 us; one batch of three heads in
+// registers instead 58.5 and 40.3; four batches 55.7 and 38.9; six CTAs for the
+// norm too spill, 43.4. (Few tokens lost: the gradient of 4096 15.3 -> 16.6 us,
+// calls one after the other.)
 constexpr int kRopeUnroll = 2;
 constexpr int kRopeDepth = 3;
 constexpr int kRopeCtas[2] = {6, 5};
