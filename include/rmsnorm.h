@@ -323,7 +323,8 @@ size_t rmsnorm_bwd_call_workspace_bytes(const void *dy, const void *dresidual_ou
  * A head-row array is [T, heads, head_dim] with head_dim contiguous and any
  * token and head strides (in elements), e.g. one part of a fused qkv
  * projection. What is written (rows, a cache) has no stride of 0 where its
- * dimension has several entries (INVALID_ARG). A call is a structure that the library reads before it
+ * dimension has several entries (INVALID_ARG).
+ * A call is a structure that the library reads before it
  * returns; all pointers in it are device pointers except where noted.
  * Streams, errors and the device follow the rules at the top of this file.
  * --------------------------------------------------------------------- */
@@ -434,9 +435,9 @@ typedef struct {
     size_t workspace_bytes;
     float scale;                /* > 0: scores are scale * q . k               */
     int32_t batch, table_width, q_heads, head_dim;
-    int32_t max_q;              /* no sequence has more new tokens (as max_kv) */
-    int32_t max_kv;             /* no sequence is longer; the work is cut by it,
-                                   so a bound far above the lengths costs time */
+    int32_t max_q;              /* no sequence has more new tokens             */
+    int32_t max_kv;             /* no sequence is longer; the work is cut by
+                                   both, so loose bounds cost time             */
     int32_t causal;
     int32_t dtype;              /* RMSNORM_BF16 or RMSNORM_F16                 */
 } paged_attn_call_t;

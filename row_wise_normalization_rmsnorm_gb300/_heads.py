@@ -94,7 +94,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_q, *, max_q: in
     the keys up to itself. max_q and max_kv bound the sequences' new tokens
     and lengths (bounds far above them cost time: the work is cut by them).
     scale defaults to 1 / sqrt(D). lse: True, or an fp32 tensor [T, heads], for
-    the log of each row's sum of exponentials (None: not written). Rows behind the last sequence are left as they were.
+    the log of each row's sum of exponentials (None: not written). Rows behind
+    the last sequence are left as they were.
     workspace: a tensor of at least paged_attn_workspace_bytes() bytes."""
     return (_ext or _load()).attn(q, k_cache, v_cache, block_table, kv_lens, cu_q, max_q, max_kv, scale, causal, out, lse,
                                   workspace, stream)

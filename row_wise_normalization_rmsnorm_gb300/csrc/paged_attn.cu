@@ -59,7 +59,7 @@
 namespace rmsn {
 
 constexpr int kKeyTile = 128;
-constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kernel gives up
+constexpr uint32_t kAttnWait = 1u << 22;  // polls of one barrier before a kernel gives up: 6 s (a failed one takes 1.4 us)
 constexpr int kClusterMost = 16;           // CTAs of a cluster (over 8: by opt-in)
 constexpr int kJoinTiles = 4;              // key tiles that the join's kernel takes as long as
 constexpr int kDecodeChunk = 16;           // key tiles of a decoding item, where there are several a CTA
