@@ -177,10 +177,8 @@ def _kept(x):
     step = exp - 7 + (frac >= 255 / 256).int()  # 127.5 steps would round to 128
     most = 9 if x.dtype == torch.float16 else 121  # 64 steps of more are no finite value of the type
     step = torch.where(top > 0, step, -127).clamp(-127, most)
-    one = torch.ones((), dtype=torch.float32, device=x.device)
-    up, half = torch.ldexp(one, (-step) // 2), torch.ldexp(one, -step - (-step) // 2)  # 2^-step in two factors
-    codes = torch.round(v * up * half).clamp(-127, 127)
-    return (codes / up / half).flatten(-2)[..., :n]
+    scale = torch.exp2(step.double()).float()
+    return (torch.round(v / scale).clamp(-127, 127) * scale).flatten(-2)[..., :n]
 
 
 def _norm_forward(h, w, offset=0.0):
