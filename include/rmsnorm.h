@@ -500,6 +500,138 @@ rmsnorm_status_t paged_attn_plan_query(const paged_attn_call_t *call, int32_t nu
                                        paged_attn_plan_t *plan);
 
 /* ------------------------------------------------------------------------
+ * Rows of a training step beside the norms above: what their rows are kept
+ * as for the backward pass, the group norm of convolutional models, and the
+ * embedding rows that enter the first norm. The pages have no counterpart to
+ * these entry points. Pointers, streams, errors, dtype codes and workspaces
+ * follow the rules at the top of this file (a 16-bit type with
+ * RMSNORM_WEIGHT_F32: weights and their gradients in fp32). Row arrays on
+ * 16-byte boundaries whose rows are whole 16-byte chunks run the vectorised
+ * kernels, anything else kernels that take any length and alignment.
+ * --------------------------------------------------------------------- */
+
+#define CKPT8_BLOCK 32 /* values that share a scale */
+
+/*
+ * Rows in 8 bits (activation checkpoints). codes [M, N] are signed bytes,
+ * scales [M, ceil(N / 32)] one byte b for each 32 neighbours of a row (the
+ * last block may be shorter). The value of a code c is c 2^(b - 127). b is
+ * the smallest for which the block's largest magnitude rounds to at most 127
+ * (not below 0, and at most 127 + 121, fp16: 127 + 9, whose 64 steps are
+ * still finite: there the largest code is 127); c is value / 2^(b - 127),
+ * rounded to nearest even. So a value is off by at most half a step, 2^-7 of
+ * the largest magnitude of its block (1 / 127.5 at most). A block that holds an
+ * infinity or a NaN has b = 255 and all of it stands for NaN.
+ * ckpt8_pack keeps x, ckpt8_unpack restores it (exact in all three types:
+ * a code has 7 bits; where fp16 has fewer, near 0, rounded to it). No
+ * buffers may overlap. dt without RMSNORM_WEIGHT_F32. N <= RMSNORM_MAX_N; M
+ * may pass 2^31.
+ */
+rmsnorm_status_t ckpt8_pack(const void *x, void *codes, uint8_t *scales, int64_t M, int64_t N,
+                            rmsnorm_dtype_t dt, rmsnorm_stream_t stream);
+rmsnorm_status_t ckpt8_unpack(const void *codes, const uint8_t *scales, void *x, int64_t M, int64_t N,
+                              rmsnorm_dtype_t dt, rmsnorm_stream_t stream);
+
+/*
+ * rmsnorm_fwd (residual and residual_out NULL) or rmsnorm_add_fwd, with the
+ * row that was normalised (x, or residual_out) kept in 8 bits as by
+ * ckpt8_pack, in the same pass. y may equal x, residual_out may equal
+ * residual.
+ */
+rmsnorm_status_t rmsnorm_fwd_ckpt8(const void *x, const void *residual, const void *w, void *y,
+                                   void *residual_out, float *rstd, void *codes, uint8_t *scales,
+                                   int64_t M, int64_t N, rmsnorm_dtype_t dt, float eps, float offset,
+                                   rmsnorm_stream_t stream);
+
+/*
+ * rmsnorm_bwd (dresidual_out NULL) or rmsnorm_add_bwd from kept rows:
+ * xhat = value(code) rstd with the forward's rstd (of the rows before they
+ * were kept), every other step as there; dw's sums have a fixed order. w and
+ * dw NULL: non-affine. dx may equal dy or dresidual_out.
+ */
+rmsnorm_status_t rmsnorm_bwd_ckpt8(const void *dy, const void *dresidual_out, const void *codes,
+                                   const uint8_t *scales, const void *w, const float *rstd, void *dx, void *dw,
+                                   void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                                   rmsnorm_dtype_t dt, float offset, rmsnorm_stream_t stream);
+size_t rmsnorm_bwd_ckpt8_workspace_bytes(int64_t M, int64_t N, rmsnorm_dtype_t dt);
+
+typedef enum {
+    ROWS_ACT_NONE = 0,
+    ROWS_ACT_SILU = 1, /* z / (1 + exp(-z))              */
+    ROWS_ACT_GELU = 2  /* z (1 + erf(z / sqrt(2))) / 2   */
+} rmsnorm_act_t;
+
+#define ROWS_MAX_GROUPS 4096
+
+/*
+ * Group norm with an activation, channels last: x [B, S, C] contiguous, S
+ * the places of a sample (height x width), G groups of C / G neighbouring
+ * channels. With n = S C / G and a group's mean and (biased) variance over
+ * its n values of a sample,
+ *
+ *   rstd = 1 / sqrt(var + eps),  xhat = (x - mean) rstd,  y = act(xhat gamma + beta)
+ *
+ * mean, rstd [B, G] fp32; gamma, beta [C] or NULL (1 and 0). The variance is
+ * summed about the pieces' own means and joined, so a mean far from 0 costs
+ * no digits. fp32 throughout, y rounded once. y may equal x.
+ * codes, scales: NULL, or x kept in 8 bits as by ckpt8_pack of [B S, C].
+ * S == 0 sets mean and rstd to 0. INVALID_ARG also: C % G != 0, C >
+ * RMSNORM_MAX_N, an unknown act. UNSUPPORTED: G > ROWS_MAX_GROUPS.
+ */
+rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, const void *beta, void *y, float *mean,
+                               float *rstd, void *codes, uint8_t *scales, void *workspace,
+                               size_t workspace_bytes, int64_t B, int64_t S, int64_t C, int64_t G,
+                               rmsnorm_act_t act, rmsnorm_dtype_t dt, float eps, rmsnorm_stream_t stream);
+
+/*
+ * Its gradient. x, or in its place (x NULL) the codes and scales it was kept
+ * as. With u = dy act'(xhat gamma + beta):
+ *
+ *   dgamma_c = sum u xhat,  dbeta_c = sum u   over all places of all samples
+ *   dx = rstd (u gamma - mean_n(u gamma) - xhat mean_n(u gamma xhat))
+ *
+ * dgamma, dbeta [C] or NULL (not wanted; dgamma needs gamma); their sums
+ * have a fixed order. dx may equal dy or x.
+ */
+rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const void *codes, const uint8_t *scales,
+                               const void *gamma, const void *beta, const float *mean, const float *rstd,
+                               void *dx, void *dgamma, void *dbeta, void *workspace, size_t workspace_bytes,
+                               int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_act_t act,
+                               rmsnorm_dtype_t dt, rmsnorm_stream_t stream);
+
+/* Workspace bytes of groupnorm_fwd (backward 0) or groupnorm_bwd on the
+ * current device; 0 for invalid sizes or without a device. */
+size_t groupnorm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward);
+
+/*
+ * Embedding rows: h_t = R(scale table[id_t]), table [rows, N], ids [T] int32
+ * or int64 (id_bytes 4 or 8). A token whose id is negative or not below
+ * `rows` (padding) gets a row of zeros.
+ * rmsnorm_embed_fwd also normalises h as rmsnorm_add_fwd does its sum: y and
+ * rstd of the rounded h, in the same pass (dt may carry RMSNORM_WEIGHT_F32; w
+ * NULL: non-affine). No buffers may overlap.
+ */
+rmsnorm_status_t embed_fwd(const void *ids, const void *table, void *h, int64_t T, int64_t N, int64_t rows,
+                           int id_bytes, rmsnorm_dtype_t dt, float scale, rmsnorm_stream_t stream);
+rmsnorm_status_t rmsnorm_embed_fwd(const void *ids, const void *table, const void *w, void *y, void *h, float *rstd,
+                                   int64_t T, int64_t N, int64_t rows, int id_bytes, rmsnorm_dtype_t dt, float scale,
+                                   float eps, float offset, rmsnorm_stream_t stream);
+
+/*
+ * The table's gradient: dtable_v = scale sum_{t: id_t = v} dh_t, summed in
+ * fp32 in an order that depends on the ids alone and rounded once; tokens
+ * whose id is outside the table add nothing. accumulate 0: every row of
+ * dtable [rows, N] is written (zeros where no token is); else the sums are
+ * added to what is there, and rows without a token are not touched. dtable is
+ * in dh's type, or fp32 where dt carries RMSNORM_WEIGHT_F32. rows < 2^31 - 1.
+ * No buffers may overlap.
+ */
+rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dtable, void *workspace, size_t workspace_bytes,
+                           int64_t T, int64_t N, int64_t rows, int id_bytes, rmsnorm_dtype_t dt, float scale,
+                           int accumulate, rmsnorm_stream_t stream);
+size_t embed_bwd_workspace_bytes(int64_t T, int64_t N, int64_t rows);
+
+/* ------------------------------------------------------------------------
  * Plans: which kernel runs. Exposed for tests and benchmarks (the analogue
  * of the A/B toggles of Liger-Kernel PR #1388, "Behavior when the fast path
  * does not apply", and of the tuned-kernel registry of

@@ -22,6 +22,18 @@ and, on [tokens, heads, head_dim] rows of any token and head strides:
   paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_q, ...)
                                           -> out, lse
 
+on rows of a training step:
+
+  rmsnorm_fwd_ckpt8(x, w, ...)            -> y, rstd and the normalised rows in
+                                             8 bits (dict: codes, scales)
+  rmsnorm_bwd_ckpt8(dy, codes, scales, w, rstd) -> dx, dw
+  ckpt8_pack(x), ckpt8_unpack(codes, scales, dtype)
+  groupnorm_fwd(x, gamma, beta, groups, act=...), groupnorm_bwd(...) -> dicts,
+                                             and their _ckpt8 forms
+  embed_fwd(ids, table), rmsnorm_embed_fwd(ids, table, w) -> embedding rows
+                                             (and their norm: y, h, rstd)
+  embed_bwd(dh, ids, rows)                -> the table's gradient
+
 The CUDA library is loaded on first use and must have been built
 (``python -m row_wise_normalization_rmsnorm_gb300.build``); there is no CPU
 fallback. ``inputs`` holds the seeded synthetic workloads.
@@ -61,4 +73,20 @@ from ._heads import (  # noqa: F401
     rope_axes,
     rope_bwd,
     rope_fwd,
+)
+from ._rows import (  # noqa: F401
+    ckpt8_pack,
+    ckpt8_unpack,
+    embed_bwd,
+    embed_bwd_workspace_bytes,
+    embed_fwd,
+    groupnorm_bwd,
+    groupnorm_bwd_ckpt8,
+    groupnorm_fwd,
+    groupnorm_fwd_ckpt8,
+    groupnorm_workspace_bytes,
+    rmsnorm_bwd_ckpt8,
+    rmsnorm_bwd_ckpt8_workspace_bytes,
+    rmsnorm_embed_fwd,
+    rmsnorm_fwd_ckpt8,
 )

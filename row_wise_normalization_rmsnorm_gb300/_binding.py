@@ -98,6 +98,20 @@ SIGNATURES = {
     "paged_attn_fwd": (_i, [_vp, _vp]),
     "paged_attn_workspace_bytes": (_sz, [_vp]),
     "paged_attn_plan_query": (_i, [_vp, _i, _vp, _vp]),
+    # rows of a training step (the Python functions go through _heads_ext, see
+    # _rows.py)
+    "ckpt8_pack": (_i, [_vp, _vp, _vp, _i64, _i64, _i, _vp]),
+    "ckpt8_unpack": (_i, [_vp, _vp, _vp, _i64, _i64, _i, _vp]),
+    "rmsnorm_fwd_ckpt8": (_i, [_vp] * 8 + [_i64, _i64, _i, _f, _f, _vp]),
+    "rmsnorm_bwd_ckpt8": (_i, [_vp] * 9 + [_sz, _i64, _i64, _i, _f, _vp]),
+    "rmsnorm_bwd_ckpt8_workspace_bytes": (_sz, [_i64, _i64, _i]),
+    "groupnorm_fwd": (_i, [_vp] * 9 + [_sz, _i64, _i64, _i64, _i64, _i, _i, _f, _vp]),
+    "groupnorm_bwd": (_i, [_vp] * 12 + [_sz, _i64, _i64, _i64, _i64, _i, _i, _vp]),
+    "groupnorm_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i, _i]),
+    "embed_fwd": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _f, _vp]),
+    "rmsnorm_embed_fwd": (_i, [_vp] * 6 + [_i64, _i64, _i64, _i, _i, _f, _f, _f, _vp]),
+    "embed_bwd": (_i, [_vp] * 4 + [_sz, _i64, _i64, _i64, _i, _i, _f, _i, _vp]),
+    "embed_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "rmsnorm_status_string": (ctypes.c_char_p, [_i]),
     "rmsnorm_last_cuda_error": (_i, []),
     "rmsnorm_self_check": (_i, []),

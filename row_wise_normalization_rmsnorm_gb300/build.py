@@ -27,15 +27,19 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librmsnorm_gb300.so")
 HEADER = os.path.join(ROOT, "include", "rmsnorm.h")
 EXT = os.path.join(HERE, "_heads_ext.so")
-EXT_SOURCE = os.path.join(CSRC, "heads_ext.cpp")
+EXT_SOURCES = [os.path.join(CSRC, f) for f in ("heads_ext.cpp", "rows_ext.cpp")]
+EXT_HEADERS = [os.path.join(CSRC, "ext_args.h")]
 EXT_STAMP = os.path.join(BUILD, "heads_ext.stamp")  # the Python and PyTorch that EXT was built against
 
 SOURCES = ["api.cu", "fwd_bf16.cu", "fwd_f32.cu", "fwd_f16.cu", "fwd_bf16w32.cu", "fwd_f16w32.cu",
            "fwd8_bf16.cu", "fwd8_f16.cu", "fwd8_f32.cu", "fwd8_bf16w32.cu", "fwd8_f16w32.cu", "ln_bf16.cu", "ln_f16.cu", "ln_f32.cu", "ln_bf16w32.cu", "ln_f16w32.cu",
            "bwd_bf16.cu", "bwd_f32.cu", "bwd_f16.cu", "bwd_bf16w32.cu", "bwd_f16w32.cu",
            "fwd_peel_f32.cu", "fwd_peel_bf16.cu", "fwd_peel_f16.cu", "bwd_peel_f32.cu", "bwd_peel_bf16.cu",
-           "bwd_peel_f16.cu", "noalloc.cu", "rope.cu", "paged_attn.cu"]
-HEADERS = ["common.cuh", "plans.h", "fwd_kernels.cuh", "bwd_kernels.cuh", "head_rows.h", "tcgen05.cuh"]
+           "bwd_peel_f16.cu", "noalloc.cu", "rope.cu", "paged_attn.cu",
+           "groupnorm.cu", "groupnorm_f32.cu", "groupnorm_bf16.cu", "groupnorm_f16.cu",
+           "ckpt8.cu", "rows_f32.cu", "rows_bf16.cu", "rows_f16.cu", "embed.cu"]
+HEADERS = ["common.cuh", "plans.h", "fwd_kernels.cuh", "bwd_kernels.cuh", "head_rows.h", "tcgen05.cuh",
+           "rows8.cuh", "groupnorm_kernels.cuh", "rows_kernels.cuh", "embed.cuh", "train_rows.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -100,30 +104,30 @@ def _text(p: str) -> str:
 
 
 def _ext_stale(force: bool) -> bool:
-    deps = [EXT_SOURCE, HEADER, os.path.abspath(__file__)]
+    deps = EXT_SOURCES + EXT_HEADERS + [HEADER, os.path.abspath(__file__)]
     return (force or not os.path.exists(EXT) or max(_mtime(p) for p in deps) > _mtime(EXT)
             or _text(EXT_STAMP) != _ext_for())
 
 
-def _compile_ext() -> str:
+def _compile_ext(source: str) -> str:
     t = _torch_dir()
-    obj = os.path.join(BUILD, "heads_ext.o")
+    obj = os.path.join(BUILD, os.path.splitext(os.path.basename(source))[0] + ".o")
     inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            os.path.join(_cuda_home(), "include"), _python_include()]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(a for d in inc for a in ("-isystem", d)),
-           "-c", EXT_SOURCE, "-o", obj]
+           "-c", source, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for heads_ext.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for {os.path.basename(source)}:\n{r.stdout}\n{r.stderr}")
     return obj
 
 
-def _link_ext(obj: str) -> None:
+def _link_ext(objs: list[str]) -> None:
     """The module finds the library beside itself; PyTorch's libraries are in
     the process that imports it."""
     t = os.path.join(_torch_dir(), "lib")
     tmp = EXT + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + t,
+    cmd = ["g++", "-shared", "-o", tmp, *objs, "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + t,
            "-Wl,-rpath," + t, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -168,12 +172,12 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     extra = list(extra or [])
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext_obj = ex.submit(_compile_ext) if ext_stale else None
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(EXT_SOURCES)) as ex:
+        ext_objs = [ex.submit(_compile_ext, s) for s in EXT_SOURCES] if ext_stale else []
         if lib_stale:
             _link(list(ex.map(lambda s: _compile(s, extra), SOURCES)))
-        if ext_obj:
-            _link_ext(ext_obj.result())
+        if ext_objs:
+            _link_ext([o.result() for o in ext_objs])
     return LIB
 
 

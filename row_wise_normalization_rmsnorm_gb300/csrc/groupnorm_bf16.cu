@@ -1,0 +1,6 @@
+// groupnorm_bf16.cu -- group norm kernels for bf16.
+#include "groupnorm_kernels.cuh"
+
+namespace rmsn {
+const void *gn_kernel_bf16(int which, bool wide, int act, bool kept) { return gn_kernel_t<__nv_bfloat16>(which, wide, act, kept); }
+}  // namespace rmsn

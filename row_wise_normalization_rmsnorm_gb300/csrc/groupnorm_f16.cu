@@ -1,0 +1,6 @@
+// groupnorm_f16.cu -- group norm kernels for f16.
+#include "groupnorm_kernels.cuh"
+
+namespace rmsn {
+const void *gn_kernel_f16(int which, bool wide, int act, bool kept) { return gn_kernel_t<__half>(which, wide, act, kept); }
+}  // namespace rmsn

@@ -1,0 +1,6 @@
+// groupnorm_f32.cu -- group norm kernels for f32.
+#include "groupnorm_kernels.cuh"
+
+namespace rmsn {
+const void *gn_kernel_f32(int which, bool wide, int act, bool kept) { return gn_kernel_t<float>(which, wide, act, kept); }
+}  // namespace rmsn
