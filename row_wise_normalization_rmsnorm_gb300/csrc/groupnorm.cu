@@ -1,10 +1,10 @@
 // groupnorm.cu -- entry points of group norm (declared in include/rmsnorm.h):
 // argument checks, the cut of the work, the workspace and the launches.
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 
-#include <cmath>
-
-#include "groupnorm_kernels.cuh"
+#include "groupnorm_held.cuh"
 #include "head_rows.h"
 #include "plans.h"
 #include "train_rows.h"
@@ -29,6 +29,71 @@ struct GnPlan {
     int threads, rows, chunks, batch;  // batch: samples a launch
     size_t parts, sums, means, bytes;  // workspace offsets
 };
+
+static const void *gn_held(int base, bool backward, bool wide, int act, bool kept) {
+    return base == RMSNORM_BF16 ? gn_held_bf16(backward, wide, act, kept)
+           : base == RMSNORM_F16 ? gn_held_f16(backward, wide, act, kept)
+                                 : gn_held_f32(backward, wide, act, kept);
+}
+
+// The cut of the one-launch kernels: a cluster of `ctas` CTAs a unit of K
+// groups of a sample. `ctas` is 0 where no cut fits.
+struct GnHeld {
+    int ctas, K, W, rows;
+    uint32_t slab[2], scales;
+    size_t smem;
+};
+
+constexpr size_t kHeldSmem = 112 * 1024;  // of a CTA: two an SM
+
+// What a cut needs; false: it does not fit.
+static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
+    const int es = bytes_of(c.dt), E = c.wide ? 16 / es : 1, cg = (int)(c.C / c.G);
+    const int64_t W = (int64_t)K * cg, rows = (c.S + ctas - 1) / ctas;
+    const bool span = K < c.G;
+    // a span is whole chunks, of 64 bytes a row at least; kept in whole blocks of 32
+    if (W > 4096 || K > 256 || (span && (!c.wide || W % E != 0 || W * es < 64))) return false;
+    if (keep && W % kBlock8 != 0) return false;
+    const int xb = c.kept ? 1 : es;
+    auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
+    const int64_t x = up(rows * W * xb + 16), d = c.backward ? up(rows * W * es + 16) : 0;
+    const int64_t sc = c.kept ? up(rows * (W / kBlock8 + 2)) : 0;
+    const int64_t fixed = kHeldThreads * E * 8 + W * 8 + (int64_t)ctas * K * 8 + K * 16;
+    if (x + d + sc + fixed > (int64_t)kHeldSmem) return false;
+    h = GnHeld{ctas, K, (int)W, (int)rows, {(uint32_t)x, (uint32_t)d}, (uint32_t)sc, (size_t)(x + d + sc + fixed)};
+    return true;
+}
+
+// The cheapest cut by estimate: rounds of the CTAs that an SM holds at once
+// (two), at 3 us each, and the bytes at the rate of memory, those of a span
+// that begins or ends inside a 32-byte sector counted with the whole sector.
+static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
+    GnHeld best{0, 0, 0, 0, {0, 0}, 0, 0};
+    double least = 0;
+    const int es = bytes_of(c.dt);
+    for (int K = 1; K <= c.G; ++K) {
+        if (c.G % K != 0) continue;
+        for (int n = 1; n <= kHeldCtas; n *= 2) {
+            GnHeld h;
+            if ((n > 1 && (c.S + n - 1) / n * (n - 1) >= c.S) || !held_cut(c, K, n, keep, h)) continue;
+            const double row = (double)h.W * es, sectors = K == c.G || (h.W * es) % 32 == 0 ? row : row + 32;
+            const double bytes = (double)c.B * c.S * c.C * es * (c.backward ? 3 : 2) * (sectors / row) * (row < 128 && K < c.G ? 1.25 : 1.0);
+            // clusters of 16 leave SMs without a CTA where a GPU's groups of SMs are no multiple of 8
+            const double ctas = (double)c.B * (c.G / K) * n, places = 2.0 * sms * (n == 16 ? 0.73 : n == 8 ? 0.94 : 1.0);
+            const double rounds = std::ceil(ctas / places);
+            const double share = ctas < sms ? sms / ctas : 1.0;  // SMs without a CTA
+            const double cost = 3.0 * rounds + (n > 1 ? 0.5 : 0.0) + bytes * share / 6.7e6;
+            if (best.ctas == 0 || cost < least) {
+                best = h;
+                least = cost;
+            }
+        }
+    }
+    return best;
+}
+
+// Workspace of the one-launch gradient: a CTA's channel sums.
+static size_t held_bytes(const GnCall &c, const GnHeld &h) { return ((size_t)c.B * h.ctas * 2 * c.C * 4 + 255) / 256 * 256; }
 
 static int gn_threads(bool backward) { return backward ? 256 : 512; }
 
@@ -68,6 +133,34 @@ static bool gn_sizes(int64_t B, int64_t S, int64_t C, int64_t G, int act, int dt
     if (B > 0x7fffffffLL || S > 0x7fffffffLL) return false;
     if (B > 0 && S > INT64_MAX / 8 / C / B) return false;
     return act >= kActNone && act <= kActGelu;
+}
+
+static rmsnorm_status_t gn_run_held(const GnParams &g, const GnCall &c, const GnHeld &h, void *dgamma, void *dbeta, int sms,
+                                    int *status, cudaStream_t s) {
+    const int base = base_of(c.dt);
+    HeldParams p;
+    std::memset(&p, 0, sizeof p);
+    p.g = g;
+    p.g.rows = h.rows;
+    if (c.backward && !dgamma && !dbeta) p.g.parts = nullptr;
+    p.ctas = h.ctas, p.W = h.W, p.K = h.K, p.spans = c.G / h.K;
+    p.slab[0] = h.slab[0], p.slab[1] = h.slab[1], p.scales = h.scales;
+    p.magic = g.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + g.cg - 1) / g.cg);
+    p.status = status;
+    const void *k = gn_held(base, c.backward, c.wide, c.act, c.backward ? c.kept : g.codes != nullptr);
+    if (h.ctas > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return head_cuda_fail((int)e);
+    }
+    void *args[] = {&p};
+    const int64_t grid = c.B * p.spans * h.ctas;
+    int e = launch(k, (unsigned)grid, 1, kHeldThreads, h.smem, args, s, (unsigned)h.ctas);
+    if (e == 0 && c.backward && (dgamma || dbeta)) {
+        const bool f32 = base == RMSNORM_F32 || g.w32;
+        auto *fin = f32 ? launch_dw_finalize_f32 : base == RMSNORM_BF16 ? launch_dw_finalize_bf16 : launch_dw_finalize_f16;
+        e = fin(g.parts, (int)(c.B * h.ctas), (int)(2 * c.C), dgamma, dbeta, (int)c.C, 0, s, false, sms);
+    }
+    return e == 0 ? RMSNORM_SUCCESS : head_cuda_fail(e);
 }
 
 static rmsnorm_status_t gn_run(GnParams &p, const GnCall &c, const GnPlan &plan, void *dgamma, void *dbeta, int sms,
@@ -111,8 +204,14 @@ static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, b
     size_t most = 0;
     for (int wide = 0; wide < 2; ++wide) {
         if (wide && C % (((dt & ~RMSNORM_WEIGHT_F32) == RMSNORM_F32) ? 4 : 8) != 0) continue;
-        const GnPlan p = gn_plan(GnCall{B, S, C, (int)G, 0, dt, backward, false, wide != 0}, sms);
-        if (p.bytes > most) most = p.bytes;
+        for (int kept = 0; kept < (backward ? 2 : 1); ++kept) {
+            const GnCall c{B, S, C, (int)G, 0, dt, backward, kept != 0, wide != 0};
+            const GnHeld h = held_plan(c, sms, false);
+            if (h.ctas)
+                most = backward ? std::max(most, held_bytes(c, h)) : most;
+            else
+                most = std::max(most, gn_plan(c, sms).bytes);
+        }
     }
     return most;
 }
@@ -135,8 +234,8 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     cudaStream_t s = (cudaStream_t)stream;
     if (S == 0) return zeros({{mean, (size_t)(B * G) * 4}, {rstd, (size_t)(B * G) * 4}}, s);
     if (!x || !y || !on(x, es) || !on(y, es)) return RMSNORM_ERR_INVALID_ARG;
-    int sms = 0;
-    int e = current_device(&sms, nullptr);
+    int sms = 0, *status = nullptr;
+    const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
     GnCall c{B, S, C, (int)G, act, dt, false, false, C % (16 / es) == 0 && on(x, 16) && on(y, 16)};
     const GnPlan plan = gn_plan(c, sms);
@@ -152,6 +251,8 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
         const rmsnorm_status_t st = ckpt8_pack(x, codes, scales, B * S, C, (rmsnorm_dtype_t)base, stream);
         if (st != RMSNORM_SUCCESS) return st;
     }
+    const GnHeld h = held_plan(c, sms, fused);
+    if (h.ctas) return gn_run_held(p, c, h, nullptr, nullptr, sms, status, s);
     return with_workspace(workspace, workspace_bytes, plan.bytes, s, [&](char *w) {
         p.parts = reinterpret_cast<float *>(w + plan.parts);
         return gn_run(p, c, plan, nullptr, nullptr, sms, s);
@@ -173,8 +274,8 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     if (G > ROWS_MAX_GROUPS) return RMSNORM_ERR_UNSUPPORTED;
     if (!dy || !dx || !mean || !rstd || (x == nullptr) == (codes == nullptr)) return RMSNORM_ERR_INVALID_ARG;
     if (!on(dy, es) || !on(dx, es) || !on(x, es) || !on(mean, 4) || !on(rstd, 4)) return RMSNORM_ERR_INVALID_ARG;
-    int sms = 0;
-    int e = current_device(&sms, nullptr);
+    int sms = 0, *status = nullptr;
+    const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
     GnCall c{B, S, C, (int)G, act, dt, true, codes != nullptr,
              C % (16 / es) == 0 && on(dy, 16) && on(dx, 16) && on(x, 16) && on(codes, 8)};
@@ -185,8 +286,10 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     p.gamma = gamma, p.beta = beta, p.out = dx, p.mean = const_cast<float *>(mean), p.rstd = const_cast<float *>(rstd);
     p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G), p.rows = plan.rows, p.chunks = plan.chunks;
     p.act = act, p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32;
-    return with_workspace(workspace, workspace_bytes, plan.bytes, s, [&](char *w) {
+    const GnHeld h = held_plan(c, sms, false);
+    return with_workspace(workspace, workspace_bytes, h.ctas ? held_bytes(c, h) : plan.bytes, s, [&](char *w) {
         p.parts = reinterpret_cast<float *>(w + plan.parts);
+        if (h.ctas) return gn_run_held(p, c, h, dgamma, dbeta, sms, status, s);
         p.sums = reinterpret_cast<float *>(w + plan.sums);
         p.means = reinterpret_cast<float2 *>(w + plan.means);
         return gn_run(p, c, plan, dgamma, dbeta, sms, s);

@@ -1,6 +1,7 @@
 // groupnorm_bf16.cu -- group norm kernels for bf16.
-#include "groupnorm_kernels.cuh"
+#include "groupnorm_held.cuh"
 
 namespace rmsn {
 const void *gn_kernel_bf16(int which, bool wide, int act, bool kept) { return gn_kernel_t<__nv_bfloat16>(which, wide, act, kept); }
+const void *gn_held_bf16(bool backward, bool wide, int act, bool kept) { return gn_held_t<__nv_bfloat16>(backward, wide, act, kept); }
 }  // namespace rmsn

@@ -1,0 +1,539 @@
+// groupnorm_held.cuh -- group norm in one launch that reads its rows once: a
+// cluster of CTAs holds what it normalises in shared memory.
+//
+// A cluster takes whole groups of one sample (all channels, or a span of them
+// that begins on a 16-byte boundary) and each of its CTAs an equal share of
+// the places, which comes into shared memory by asynchronous copies,
+// kHeldStages pieces one behind the other: the sums begin with the first.
+// Chunks are copied by the thread that later reads them, so no thread waits
+// for another's; rows of any length and alignment are copied in bulk (a bulk
+// copy a row of a span instead: 64 x 64 x 320 31 us against TBD). The CTAs'
+// group sums meet in distributed shared memory, and the second pass reads
+// shared memory.
+// Bytes: x in, y out (forward), x and dy in, dx out: once each.
+#pragma once
+
+#include "groupnorm_kernels.cuh"
+
+namespace rmsn {
+
+constexpr int kHeldThreads = 256;
+constexpr int kHeldStages = 4;
+constexpr int kHeldCtas = 16;                 // of a cluster at most
+constexpr uint32_t kHeldWaitLimit = 1u << 20;  // polls of a piece's copies
+
+struct HeldParams {
+    GnParams g;      // rows: places a CTA takes
+    int ctas;        // of a cluster
+    int W, K, spans;  // channels and groups a cluster takes, clusters a sample
+    uint32_t slab[2];  // bytes a CTA's share of x (or its codes) and of dy has in shared memory
+    uint32_t scales;   // and of scale bytes
+    uint32_t magic;    // ceil(2^32 / cg): c / cg = (c magic) >> 32 for c < 2^16
+    int *status;
+};
+
+// A CTA's share of rows in shared memory. Chunks (E > 1): one behind the
+// other, W / E a row. Single values: the 16-byte blocks that hold the share
+// (rows of all channels are contiguous, from any address).
+struct Slab {
+    const char *src;
+    uint8_t *dst;
+    uint32_t off, row, piece, bytes;  // offset of the first row, bytes of a row, of a piece, of all
+    __device__ __forceinline__ Slab(const void *base, int es, int64_t first_row, int C, int rows, uint8_t *to) {
+        src = static_cast<const char *>(base) + first_row * C * es;
+        dst = to;
+        row = (uint32_t)C * es;
+        const Cover c = cover16(src, (uint32_t)rows * row);
+        src = c.src;
+        off = c.off;
+        bytes = rows > 0 ? c.bytes : 0u;
+        piece = ((bytes + kHeldStages - 1) / kHeldStages + 15u) & ~15u;
+    }
+    __device__ __forceinline__ uint32_t piece_bytes(int i) const {
+        const uint32_t at = (uint32_t)i * piece;
+        return at < bytes ? min(piece, bytes - at) : 0u;
+    }
+    // rows that are there once pieces 0 .. i are
+    __device__ __forceinline__ int ready(int i, int rows) const {
+        const uint32_t end = (uint32_t)(i + 1) * piece;
+        return end >= bytes ? rows : end > off ? min(rows, (int)((end - off) / row)) : 0;
+    }
+    __device__ __forceinline__ void fetch(int i, uint64_t *bar) const {
+        const uint32_t at = (uint32_t)i * piece, n = piece_bytes(i);
+        if (n > 0) bulk_g2s(dst + at, src + at, n, bar);
+    }
+};
+
+template <int BYTES> __device__ __forceinline__ void copy_chunk(uint8_t *to, const void *from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the latest `n` groups of this thread's copies have landed.
+__device__ __forceinline__ void copies_wait(int n) {
+    switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+static_assert(kHeldStages == 4, "copies_wait");
+
+// This thread's rows of a chunk column: lane, lane + lanes, ..., n of them;
+// those of piece i end before the end_of(n, i)-th.
+__device__ __forceinline__ int rows_of_lane(int rows, int lane, int lanes) { return lane < rows ? (rows - lane + lanes - 1) / lanes : 0; }
+__device__ __forceinline__ int end_of(int n, int i) { return (n * (i + 1) + kHeldStages - 1) / kHeldStages; }
+
+// E values from shared memory.
+template <typename T, int E> __device__ __forceinline__ void held_values(const uint8_t *p, float (&v)[E]) {
+    if constexpr (E == Elem<T>::E) {
+        Vals<T, E> c;
+        c.w = lds128(p);
+        c.get(v);
+    } else {
+        Vals<T, E> c;
+        c.w = *reinterpret_cast<const typename Vals<T, E>::W *>(p);
+        c.get(v);
+    }
+}
+template <int E> __device__ __forceinline__ void held_codes(const uint8_t *p, uint32_t b, float (&v)[E]) {
+    Kept<E> k;
+    k.w = *reinterpret_cast<const typename Kept<E>::W *>(p);
+    k.b = b;
+    k.get(v);
+}
+
+// c / cg (magic 0: cg is 1)
+__device__ __forceinline__ int group_of(int c, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)c, magic) : c; }
+
+struct HeldPlace {
+    int rank, b, c0, g0, rows;
+    int64_t first;  // first row of the matrix
+    __device__ __forceinline__ HeldPlace(const HeldParams &p) {
+        const int unit = (int)blockIdx.x / p.ctas;
+        rank = (int)blockIdx.x - unit * p.ctas;
+        b = unit / p.spans;
+        const int s = unit - b * p.spans;
+        c0 = s * p.W;
+        g0 = s * p.K;
+        const int64_t r0 = (int64_t)rank * p.g.rows;
+        rows = (int)max((int64_t)0, min((int64_t)p.g.rows, p.g.S - r0));
+        first = (int64_t)b * p.g.S + r0;
+    }
+    static __device__ __forceinline__ int rows_of(const HeldParams &p, int r) {
+        return (int)max((int64_t)0, min((int64_t)p.g.rows, p.g.S - (int64_t)r * p.g.rows));
+    }
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <typename T, int E, int ACT, bool KEEP>
+__global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams p) {
+    extern __shared__ __align__(128) uint8_t held[];
+    __shared__ __align__(8) uint64_t bar[kHeldStages];
+    __shared__ bool failed;
+    const GnParams &g = p.g;
+    float *lane_mean = reinterpret_cast<float *>(held + p.slab[0]), *lane_m2 = lane_mean + kHeldThreads * E;
+    float *ch_mean = lane_m2 + kHeldThreads * E, *ch_m2 = ch_mean + p.W;
+    float2 *exch = reinterpret_cast<float2 *>(ch_m2 + p.W);
+    float2 *stat = exch + p.ctas * p.K;
+    const HeldPlace at(p);
+    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+    const Slab xs(g.x, sizeof(T), at.first, g.C, at.rows, held);
+    if constexpr (E == 1) {
+        if (threadIdx.x == 0) {
+            failed = false;
+            for (int i = 0; i < kHeldStages; ++i) mbar_init(&bar[i], 1);
+            mbar_init_fence();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncthreads();
+    }
+    cluster_arrive();  // by the exchange every CTA of the cluster has begun
+    pdl_wait();
+    pdl_trigger();
+    const int CW = p.W / E;
+    const Cut cut(CW);
+    const uint8_t *rows = held + (E == 1 ? xs.off : 0u);
+    const uint32_t pitch = (uint32_t)p.W * sizeof(T);
+    if constexpr (E == 1) {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < kHeldStages; ++i) {
+                mbar_arrive_expect_tx(&bar[i], xs.piece_bytes(i));
+                xs.fetch(i, &bar[i]);
+            }
+    }
+    for (int t0 = 0; t0 < CW; t0 += cut.cols) {
+        const int cc = t0 + cut.col;
+        const bool in = cut.in && cc < CW;
+        float K[E], s1[E], s2[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) K[i] = s1[i] = s2[i] = 0.f;
+        const int n = in ? rows_of_lane(at.rows, cut.lane, cut.lanes) : 0;
+        if constexpr (E > 1) {
+            const T *x = static_cast<const T *>(g.x) + (at.first + cut.lane) * g.C + at.c0 + cc * E;
+            uint8_t *to = held + (uint32_t)cut.lane * pitch + cc * 16;
+            int k = 0;
+            for (int i = 0; i < kHeldStages; ++i) {
+                for (const int end = end_of(n, i); k < end; ++k)
+                    copy_chunk<16>(to + (uint32_t)(k * cut.lanes) * pitch, x + (int64_t)k * cut.lanes * g.C);
+                copies_commit();
+            }
+        }
+        int r = cut.lane;
+        for (int i = 0; i < kHeldStages; ++i) {
+            int end;
+            if constexpr (E > 1) {
+                copies_wait(kHeldStages - 1 - i);
+                end = cut.lane + end_of(n, i) * cut.lanes;
+            } else {
+                if (!mbar_wait(&bar[i], 0, kHeldWaitLimit)) failed = true;
+                end = in ? xs.ready(i, at.rows) : 0;
+            }
+            if (r == cut.lane && r < end) {
+                held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), K);
+                r += cut.lanes;
+            }
+#pragma unroll 4
+            for (; r < end; r += cut.lanes) {
+                float v[E];
+                held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), v);
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const float d = v[k] - K[k];
+                    s1[k] += d;
+                    s2[k] = fmaf(d, d, s2[k]);
+                }
+            }
+        }
+        const float inv = n > 0 ? 1.f / (float)n : 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float m = s1[i] * inv;
+            lane_mean[threadIdx.x * E + i] = K[i] + m;
+            lane_m2[threadIdx.x * E + i] = fmaxf(s2[i] - s1[i] * m, 0.f);
+        }
+        __syncthreads();
+        // a channel's lanes (each with n or n - 1 rows), about their common mean
+        const int width = cut.cols * E, used = min(cut.lanes, at.rows);
+        const float all = 1.f / (float)max(at.rows, 1);
+        for (int c = threadIdx.x; c < width && t0 * E + c < p.W; c += kHeldThreads) {
+            const float ref = lane_mean[c];
+            float s = 0.f, m2 = 0.f;
+            for (int l = 1; l < used; ++l) s += (float)((at.rows - l + cut.lanes - 1) / cut.lanes) * (lane_mean[l * width + c] - ref);
+            const float m = ref + s * all;
+            for (int l = 0; l < used; ++l) {
+                const float d = lane_mean[l * width + c] - m;
+                m2 += fmaf((float)((at.rows - l + cut.lanes - 1) / cut.lanes) * d, d, lane_m2[l * width + c]);
+            }
+            ch_mean[t0 * E + c] = m;
+            ch_m2[t0 * E + c] = m2;
+        }
+        __syncthreads();
+    }
+    // a group's channels (all of at.rows places), a warp a group; then to every CTA of the cluster
+    cluster_wait();
+    for (int k = warp; k < p.K; k += kHeldThreads / 32) {
+        const float *cm = ch_mean + k * g.cg, *c2 = ch_m2 + k * g.cg;
+        const float ref = cm[0];
+        float s = 0.f, m2 = 0.f;
+        for (int c = wl; c < g.cg; c += 32) s += cm[c] - ref;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float m = ref + s / (float)g.cg;
+        for (int c = wl; c < g.cg; c += 32) {
+            const float d = cm[c] - m;
+            m2 += fmaf((float)at.rows * d, d, c2[c]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+        if (wl < p.ctas) st_cluster2(&exch[at.rank * p.K + k], (uint32_t)wl, make_float2(m, m2));
+    }
+    cluster_sync();
+    for (int k = threadIdx.x; k < p.K; k += kHeldThreads) {
+        const float n = (float)g.S * (float)g.cg, ref = exch[k].x;
+        float s = 0.f, m2 = 0.f;
+        for (int r = 1; r < p.ctas; ++r) {
+            const float cnt = (float)HeldPlace::rows_of(p, r);
+            if (cnt > 0.f) s += cnt * (exch[r * p.K + k].x - ref);
+        }
+        const float m = ref + s / (float)g.S;
+        for (int r = 0; r < p.ctas; ++r) {
+            const float cnt = (float)HeldPlace::rows_of(p, r) * (float)g.cg;
+            if (cnt > 0.f) {
+                const float2 e = exch[r * p.K + k];
+                const float d = e.x - m;
+                m2 += fmaf(cnt * d, d, e.y);
+            }
+        }
+        const float rs = 1.f / sqrtf(m2 / n + g.eps);
+        stat[k] = make_float2(m, rs);
+        if (at.rank == 0) {
+            g.mean[(int64_t)at.b * g.G + at.g0 + k] = m;
+            g.rstd[(int64_t)at.b * g.G + at.g0 + k] = rs;
+        }
+    }
+    __syncthreads();
+    T *y = static_cast<T *>(g.out) + at.first * g.C + at.c0;
+    for (int t0 = 0; t0 < CW; t0 += cut.cols) {
+        const int cc = t0 + cut.col;
+        if (!cut.in || cc >= CW) continue;
+        float mean[E], f[E], beta[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int c = cc * E + i;
+            const float2 s = stat[group_of(c, p.magic)];
+            mean[i] = s.x;
+            f[i] = s.y * param<T>(g.gamma, g.w32, at.c0 + c, 1.f);
+            beta[i] = param<T>(g.beta, g.w32, at.c0 + c, 0.f);
+        }
+#pragma unroll 2
+        for (int r = cut.lane; r < at.rows; r += cut.lanes) {
+            float v[E], z[E];
+            held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), v);
+#pragma unroll
+            for (int i = 0; i < E; ++i) z[i] = fmaf(v[i] - mean[i], f[i], beta[i]);
+            act_of<T, ACT>(z);
+            Vals<T, E> o;
+            o.set(z);
+            o.store(y + (int64_t)r * g.C + cc * E);
+            if constexpr (KEEP) {
+                const int64_t row = at.first + r;
+                const int c = at.c0 + cc * E;
+                keep_chunk<T, E>(v, true, g.codes + row * g.C + c, g.scales + row * (g.C / kBlock8) + c / kBlock8);
+            }
+        }
+    }
+    if (E == 1 && failed && threadIdx.x == 0) {
+        for (int i = 0; i < kHeldStages; ++i) mbar_wait(&bar[i], 0, kHeldWaitLimit);
+        if (p.status) *p.status = 1;
+    }
+}
+
+template <typename T, int E, int ACT, bool KEPT>
+__global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams p) {
+    extern __shared__ __align__(128) uint8_t held[];
+    __shared__ __align__(8) uint64_t bar[kHeldStages];
+    __shared__ bool failed;
+    const GnParams &g = p.g;
+    uint8_t *sc = held + p.slab[0] + p.slab[1];  // scale bytes [rows, nsc]
+    float *lane_a = reinterpret_cast<float *>(sc + p.scales), *lane_s = lane_a + kHeldThreads * E;
+    float *ch_a = lane_s + kHeldThreads * E, *ch_s = ch_a + p.W;
+    float2 *exch = reinterpret_cast<float2 *>(ch_s + p.W);
+    float2 *means = exch + p.ctas * p.K, *stat = means + p.K;
+    const HeldPlace at(p);
+    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+    constexpr int XE = KEPT ? 1 : (int)sizeof(T);  // bytes of a value of x
+    const Slab xs(KEPT ? (const void *)g.codes_in : g.x, XE, at.first, g.C, at.rows, held);
+    const Slab ds(g.dy, sizeof(T), at.first, g.C, at.rows, held + p.slab[0]);
+    if constexpr (E == 1) {
+        if (threadIdx.x == 0) {
+            failed = false;
+            for (int i = 0; i < kHeldStages; ++i) mbar_init(&bar[i], 1);
+            mbar_init_fence();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncthreads();
+    }
+    cluster_arrive();
+    pdl_wait();
+    pdl_trigger();
+    const int CW = p.W / E;
+    const Cut cut(CW);
+    const uint8_t *xrows = held + (E == 1 ? xs.off : 0u), *drows = held + p.slab[0] + (E == 1 ? ds.off : 0u);
+    const uint32_t xpitch = (uint32_t)p.W * XE, dpitch = (uint32_t)p.W * sizeof(T);
+    auto copy_column = [&](int cc, int n) {  // a chunk column's rows of this lane
+        const int64_t first = (at.first + cut.lane) * g.C + at.c0 + cc * E;
+        const char *x = (KEPT ? (const char *)g.codes_in : static_cast<const char *>(g.x)) + first * XE;
+        const T *d = static_cast<const T *>(g.dy) + first;
+        uint8_t *xto = held + (uint32_t)cut.lane * xpitch + cc * (E * XE), *dto = held + p.slab[0] + (uint32_t)cut.lane * dpitch + cc * 16;
+        const int64_t step = (int64_t)cut.lanes * g.C;
+        int k = 0;
+        for (int i = 0; i < kHeldStages; ++i) {
+            for (const int end = end_of(n, i); k < end; ++k) {
+                copy_chunk<E * XE>(xto + (uint32_t)(k * cut.lanes) * xpitch, x + k * step * XE);
+                copy_chunk<16>(dto + (uint32_t)(k * cut.lanes) * dpitch, d + k * step);
+            }
+            copies_commit();
+        }
+    };
+    if constexpr (E == 1) {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < kHeldStages; ++i) {
+                mbar_arrive_expect_tx(&bar[i], xs.piece_bytes(i) + ds.piece_bytes(i));
+                xs.fetch(i, &bar[i]);
+                ds.fetch(i, &bar[i]);
+            }
+    } else {
+        copy_column(cut.col, cut.in ? rows_of_lane(at.rows, cut.lane, cut.lanes) : 0);
+    }
+    const int sc0 = at.c0 / kBlock8, nsc = KEPT ? (at.c0 + p.W - 1) / kBlock8 - sc0 + 1 : 0;
+    if constexpr (KEPT) {
+        const int all = (g.C + kBlock8 - 1) / kBlock8;
+        for (int i = threadIdx.x; i < at.rows * nsc; i += kHeldThreads) {
+            const int r = i / nsc;
+            sc[i] = g.scales_in[(at.first + r) * all + sc0 + (i - r * nsc)];
+        }
+    }
+    for (int k = threadIdx.x; k < p.K; k += kHeldThreads) {
+        const int64_t i = (int64_t)at.b * g.G + at.g0 + k;
+        stat[k] = make_float2(g.mean[i], g.rstd[i]);
+    }
+    __syncthreads();
+    // xhat, u and z's slope of a chunk: what both passes form anew
+    auto chunk = [&](int r, int cc, const float (&mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E],
+                     float (&xhat)[E], float (&u)[E]) {
+        float z[E];
+        if constexpr (KEPT)
+            held_codes<E>(xrows + (size_t)r * xpitch + cc * E, sc[r * nsc + (at.c0 + cc * E) / kBlock8 - sc0], xhat);
+        else
+            held_values<T, E>(xrows + (size_t)r * xpitch + cc * (E * XE), xhat);
+        held_values<T, E>(drows + (size_t)r * dpitch + cc * (E * sizeof(T)), u);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            xhat[i] = (xhat[i] - mean[i]) * rstd[i];
+            z[i] = fmaf(xhat[i], gamma[i], beta[i]);
+        }
+        act_slope<T, ACT>(z);
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] *= z[i];
+    };
+    auto constants = [&](int cc, float (&mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int c = cc * E + i;
+            const float2 s = stat[group_of(c, p.magic)];
+            mean[i] = s.x;
+            rstd[i] = s.y;
+            gamma[i] = param<T>(g.gamma, g.w32, at.c0 + c, 1.f);
+            beta[i] = param<T>(g.beta, g.w32, at.c0 + c, 0.f);
+        }
+    };
+    float *out = g.parts + ((int64_t)at.b * p.ctas + at.rank) * 2 * g.C;
+    for (int t0 = 0; t0 < CW; t0 += cut.cols) {
+        const int cc = t0 + cut.col;
+        const bool in = cut.in && cc < CW;
+        float a[E], s[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) a[i] = s[i] = 0.f;
+        float mean[E], rstd[E], gamma[E], beta[E];
+        const int n = in ? rows_of_lane(at.rows, cut.lane, cut.lanes) : 0;
+        if constexpr (E > 1) {
+            if (t0 > 0) copy_column(cc, n);
+        }
+        if (in) constants(cc, mean, rstd, gamma, beta);
+        int r = cut.lane;
+        for (int i = 0; i < kHeldStages; ++i) {
+            int end;
+            if constexpr (E > 1) {
+                copies_wait(kHeldStages - 1 - i);
+                end = cut.lane + end_of(n, i) * cut.lanes;
+            } else {
+                if (!mbar_wait(&bar[i], 0, kHeldWaitLimit)) failed = true;
+                end = in ? min(xs.ready(i, at.rows), ds.ready(i, at.rows)) : 0;
+            }
+#pragma unroll 2
+            for (; r < end; r += cut.lanes) {
+                float xhat[E], u[E];
+                chunk(r, cc, mean, rstd, gamma, beta, xhat, u);
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    a[k] = fmaf(u[k], xhat[k], a[k]);
+                    s[k] += u[k];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            lane_a[threadIdx.x * E + i] = a[i];
+            lane_s[threadIdx.x * E + i] = s[i];
+        }
+        __syncthreads();
+        const int width = cut.cols * E;
+        for (int c = threadIdx.x; c < width && t0 * E + c < p.W; c += kHeldThreads) {
+            float ta = lane_a[c], ts = lane_s[c];
+            for (int l = 1; l < cut.lanes; ++l) {
+                ta += lane_a[l * width + c];
+                ts += lane_s[l * width + c];
+            }
+            const int ch = t0 * E + c;
+            if (g.parts) {
+                out[at.c0 + ch] = ta;
+                out[g.C + at.c0 + ch] = ts;
+            }
+            const float ga = param<T>(g.gamma, g.w32, at.c0 + ch, 1.f);
+            ch_a[ch] = ta * ga;
+            ch_s[ch] = ts * ga;
+        }
+        __syncthreads();
+    }
+    cluster_wait();
+    for (int k = warp; k < p.K; k += kHeldThreads / 32) {
+        float2 m = make_float2(0.f, 0.f);
+        for (int c = wl; c < g.cg; c += 32) m = add2(m, make_float2(ch_s[k * g.cg + c], ch_a[k * g.cg + c]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
+        if (wl < p.ctas) st_cluster2(&exch[at.rank * p.K + k], (uint32_t)wl, m);
+    }
+    cluster_sync();
+    for (int k = threadIdx.x; k < p.K; k += kHeldThreads) {
+        const float n = (float)g.S * (float)g.cg;
+        float2 m = exch[k];
+        for (int r = 1; r < p.ctas; ++r) m = add2(m, exch[r * p.K + k]);
+        means[k] = make_float2(m.x / n, m.y / n);
+    }
+    __syncthreads();
+    T *dx = static_cast<T *>(g.out) + at.first * g.C + at.c0;
+    for (int t0 = 0; t0 < CW; t0 += cut.cols) {
+        const int cc = t0 + cut.col;
+        if (!cut.in || cc >= CW) continue;
+        float mean[E], rstd[E], gamma[E], beta[E];
+        constants(cc, mean, rstd, gamma, beta);
+        float2 m[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) m[i] = means[group_of(cc * E + i, p.magic)];
+#pragma unroll 1
+        for (int r = cut.lane; r < at.rows; r += cut.lanes) {
+            float xhat[E], u[E];
+            chunk(r, cc, mean, rstd, gamma, beta, xhat, u);
+#pragma unroll
+            for (int i = 0; i < E; ++i) u[i] = rstd[i] * (fmaf(u[i], gamma[i], -m[i].x) - xhat[i] * m[i].y);
+            Vals<T, E> o;
+            o.set(u);
+            o.store(dx + (int64_t)r * g.C + cc * E);
+        }
+    }
+    if (E == 1 && failed && threadIdx.x == 0) {
+        for (int i = 0; i < kHeldStages; ++i) mbar_wait(&bar[i], 0, kHeldWaitLimit);
+        if (p.status) *p.status = 1;
+    }
+}
+
+// (keeping x in the same pass: whole 16-byte chunks only)
+template <typename T, int E, int ACT> static const void *held_fwd() {
+    if constexpr (E > 1)
+        return (const void *)gn_fwd_held<T, E, ACT, true>;
+    else
+        return nullptr;
+}
+template <typename T, int E> static const void *gn_held_e(bool backward, int act, bool kept) {
+#define HELD(A)                                                                                        \
+    (backward ? (kept ? (const void *)gn_bwd_held<T, E, A, true> : (const void *)gn_bwd_held<T, E, A, false>) \
+     : kept   ? held_fwd<T, E, A>()                                                                    \
+              : (const void *)gn_fwd_held<T, E, A, false>)
+    return act == kActSilu ? HELD(kActSilu) : act == kActGelu ? HELD(kActGelu) : HELD(kActNone);
+#undef HELD
+}
+template <typename T> static const void *gn_held_t(bool backward, bool wide, int act, bool kept) {
+    return wide ? gn_held_e<T, Elem<T>::E>(backward, act, kept) : gn_held_e<T, 1>(backward, act, kept);
+}
+
+const void *gn_held_f32(bool backward, bool wide, int act, bool kept);
+const void *gn_held_bf16(bool backward, bool wide, int act, bool kept);
+const void *gn_held_f16(bool backward, bool wide, int act, bool kept);
+
+}  // namespace rmsn

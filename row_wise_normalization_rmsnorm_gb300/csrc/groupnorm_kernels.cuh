@@ -119,33 +119,70 @@ template <typename T> __device__ __forceinline__ float param(const void *w, int 
 }
 
 // ------------------------------------------------------------- activations --
-// The exponential and the division are the fast ones where the result is
-// rounded to 16 bits (their error, 2^-21 near z = 1, is far below that
-// rounding), the accurate ones for fp32.
-template <typename T> __device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (std::is_same<T, float>::value)
-        return 1.f / (1.f + expf(-z));
-    else
-        return __fdividef(1.f, 1.f + __expf(-z));
-}
-template <typename T, int ACT> __device__ __forceinline__ float act_of(float z) {
-    if constexpr (ACT == kActSilu) {
-        // z times the sigmoid: below -88 the fast division gives 0 for what is under 2^-120
-        return z * sigmoid<T>(z);
-    } else if constexpr (ACT == kActGelu) {
-        return 0.5f * z * (1.f + erff(z * 0.70710678f));
+// The sigmoids of two values. For 16-bit rows one reciprocal serves both
+// (1 / a = b / (a b)): the special-function unit, 16 results a clock and SM,
+// bounds these kernels next to memory, and so it gives 1.5 results a value
+// instead of 2. z is held at -43, where the sigmoid is 2^-62 and a b still
+// finite. fp32 rows take the accurate exponential.
+template <typename T> __device__ __forceinline__ float2 sigmoid2(float2 z) {
+    if constexpr (std::is_same<T, float>::value) {
+        return make_float2(__fdividef(1.f, 1.f + expf(-z.x)), __fdividef(1.f, 1.f + expf(-z.y)));
     } else {
-        return z;
+        const float a = 1.f + __expf(-fmaxf(z.x, -43.f)), b = 1.f + __expf(-fmaxf(z.y, -43.f));
+        const float r = __fdividef(1.f, a * b);
+        return make_float2(r * b, r * a);
     }
 }
-template <typename T, int ACT> __device__ __forceinline__ float act_slope(float z) {
+template <typename T> __device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (std::is_same<T, float>::value)
+        return __fdividef(1.f, 1.f + expf(-z));
+    else
+        return __fdividef(1.f, 1.f + __expf(-fmaxf(z, -43.f)));
+}
+// (fmaxf drops a NaN: z, which every result is multiplied by, brings it back.)
+
+__device__ __forceinline__ float gelu_of(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); }
+__device__ __forceinline__ float gelu_slope(float z) {
+    return 0.5f * (1.f + erff(z * 0.70710678f)) + z * __expf(-0.5f * z * z) * 0.39894228f;
+}
+
+// act(z) and act'(z) of E values, in place.
+template <typename T, int ACT, int E> __device__ __forceinline__ void act_of(float (&z)[E]) {
     if constexpr (ACT == kActSilu) {
-        const float p = sigmoid<T>(z);
-        return p * (1.f + z * (1.f - p));
+        if constexpr (E > 1) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const float2 p = sigmoid2<T>(make_float2(z[i], z[i + 1]));
+                z[i] *= p.x, z[i + 1] *= p.y;
+            }
+        } else {
+            z[0] *= sigmoid<T>(z[0]);
+        }
     } else if constexpr (ACT == kActGelu) {
-        return 0.5f * (1.f + erff(z * 0.70710678f)) + z * __expf(-0.5f * z * z) * 0.39894228f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) z[i] = gelu_of(z[i]);
+    }
+}
+template <typename T, int ACT, int E> __device__ __forceinline__ void act_slope(float (&z)[E]) {
+    if constexpr (ACT == kActSilu) {
+        float p[E];
+        if constexpr (E > 1) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const float2 q = sigmoid2<T>(make_float2(z[i], z[i + 1]));
+                p[i] = q.x, p[i + 1] = q.y;
+            }
+        } else {
+            p[0] = sigmoid<T>(z[0]);
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) z[i] = p[i] * fmaf(z[i], 1.f - p[i], 1.f);
+    } else if constexpr (ACT == kActGelu) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) z[i] = gelu_slope(z[i]);
     } else {
-        return 1.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) z[i] = 1.f;
     }
 }
 
@@ -336,7 +373,8 @@ __global__ void __launch_bounds__(512) gn_apply(const GnParams p) {
                     float v[E], z[E];
                     c[q].get(v);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) z[i] = act_of<T, ACT>(fmaf(v[i] - mean[i], f[i], beta[i]));
+                    for (int i = 0; i < E; ++i) z[i] = fmaf(v[i] - mean[i], f[i], beta[i]);
+                    act_of<T, ACT>(z);
                     Vals<T, E> o;
                     o.set(z);
                     o.store(y + (int64_t)rr * p.C + cc * E);
@@ -408,14 +446,19 @@ __global__ void __launch_bounds__(256) gn_bwd_sums(const GnParams p) {
 #pragma unroll
                 for (int q = 0; q < kGnBatch; ++q)
                     if (r + q * cut.lanes < rows) {
-                        float v[E], g[E];
+                        float v[E], g[E], z[E];
                         x[q].c.get(v);
                         d[q].get(g);
 #pragma unroll
                         for (int i = 0; i < E; ++i) {
-                            const float xhat = (v[i] - mean[i]) * rstd[i];
-                            const float u = g[i] * act_slope<T, ACT>(fmaf(xhat, gamma[i], beta[i]));
-                            a[i] = fmaf(u, xhat, a[i]);
+                            v[i] = (v[i] - mean[i]) * rstd[i];
+                            z[i] = fmaf(v[i], gamma[i], beta[i]);
+                        }
+                        act_slope<T, ACT>(z);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            const float u = g[i] * z[i];
+                            a[i] = fmaf(u, v[i], a[i]);
                             s[i] += u;
                         }
                     }
@@ -526,15 +569,17 @@ __global__ void __launch_bounds__(256) gn_bwd_apply(const GnParams p) {
             for (int q = 0; q < kGnBatch; ++q) {
                 const int rr = r + q * cut.lanes;
                 if (rr < rows) {
-                    float v[E], g[E];
+                    float v[E], g[E], z[E];
                     x[q].c.get(v);
                     d[q].get(g);
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
-                        const float xhat = (v[i] - mean[i]) * rstd[i];
-                        const float u = g[i] * act_slope<T, ACT>(fmaf(xhat, gamma[i], beta[i]));
-                        g[i] = rstd[i] * (fmaf(u, gamma[i], -m1[i]) - xhat * m2[i]);
+                        v[i] = (v[i] - mean[i]) * rstd[i];
+                        z[i] = fmaf(v[i], gamma[i], beta[i]);
                     }
+                    act_slope<T, ACT>(z);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) g[i] = rstd[i] * (fmaf(g[i] * z[i], gamma[i], -m1[i]) - v[i] * m2[i]);
                     Vals<T, E> o;
                     o.set(g);
                     o.store(dx + (int64_t)rr * p.C + cc * E);
