@@ -11,23 +11,16 @@
 
 namespace rmsn {
 
-static const void *gn_kernel(int which, int base, bool wide, int act, bool kept) {
-    return base == RMSNORM_BF16 ? gn_kernel_bf16(which, wide, act, kept)
-           : base == RMSNORM_F16 ? gn_kernel_f16(which, wide, act, kept)
-                                 : gn_kernel_f32(which, wide, act, kept);
+static const void *gn_flow(int base, bool backward, bool wide, int act, bool kept) {
+    return base == RMSNORM_BF16 ? gn_flow_bf16(backward, wide, act, kept)
+           : base == RMSNORM_F16 ? gn_flow_f16(backward, wide, act, kept)
+                                 : gn_flow_f32(backward, wide, act, kept);
 }
 
 struct GnCall {
     int64_t B, S, C;
     int G, act, dt;
     bool backward, kept, wide;
-};
-
-// How a call is cut. A CTA has at most `threads` threads, as rows x channel
-// chunks; a sample is `chunks` runs of `rows` rows.
-struct GnPlan {
-    int threads, rows, chunks, batch;  // batch: samples a launch
-    size_t parts, sums, means, bytes;  // workspace offsets
 };
 
 static const void *gn_held(int base, bool backward, bool wide, int act, bool kept) {
@@ -95,35 +88,50 @@ static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
 // Workspace of the one-launch gradient: a CTA's channel sums.
 static size_t held_bytes(const GnCall &c, const GnHeld &h) { return ((size_t)c.B * h.ctas * 2 * c.C * 4 + 255) / 256 * 256; }
 
-static int gn_threads(bool backward) { return backward ? 256 : 512; }
+// The cut of the flow: pieces of `rows` places of a sample.
+struct GnFlow {
+    int rows, pieces, lag, grid, folds;
+    size_t smem;
+    size_t state, part, stat, parts, folded, bytes;  // workspace offsets (state_bytes of zeros first)
+    size_t state_bytes;
+};
 
-static GnPlan gn_plan(const GnCall &c, int sms) {
-    GnPlan p;
-    const int es = (c.dt & ~RMSNORM_WEIGHT_F32) == RMSNORM_F32 ? 4 : 2, E = c.wide ? 16 / es : 1;
-    const int64_t CC = c.C / E;
-    p.threads = gn_threads(c.backward);
-    const int64_t cols = CC < p.threads ? CC : p.threads, lanes = p.threads / cols;
-    // samples whose rows the L2 holds between the two passes over them
-    const int64_t sample = c.S * c.C * es * (c.backward ? 2 : 1);
-    int64_t batch = sample > 0 ? (int64_t)(48 << 20) / sample : c.B;
-    p.batch = (int)(batch < 1 ? 1 : batch > c.B ? c.B : batch > 65535 ? 65535 : batch);
-    // about four CTAs' worth of threads an SM; whole batches of rows a lane, 64 at most
-    // (a lane's sums stay short) unless the chunks of a sample became more than 512
-    const int64_t ctas = (int64_t)sms * (2048 / p.threads);
-    int64_t per = (c.S * p.batch + ctas - 1) / ctas;
-    int64_t k = (per + lanes - 1) / lanes;
-    k = k > kGnBatch ? (k + kGnBatch - 1) / kGnBatch * kGnBatch : k;
-    if (k > 64) k = 64;
-    if (k < 1) k = 1;
-    while ((c.S + k * lanes - 1) / (k * lanes) > 512) k *= 2;
-    p.rows = (int)(k * lanes);
-    p.chunks = (int)((c.S + p.rows - 1) / p.rows);
-    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    p.parts = 0;
-    p.sums = up((size_t)c.B * p.chunks * 2 * (c.backward ? c.C : c.G) * sizeof(float));
-    p.means = p.sums + (c.backward ? up((size_t)c.B * 2 * c.C * sizeof(float)) : 0);
-    p.bytes = p.means + (c.backward ? up((size_t)c.B * c.G * sizeof(float2)) : 0);
-    return p;
+static GnFlow flow_plan(const GnCall &c, int sms) {
+    GnFlow f;
+    const int es = bytes_of(c.dt), E = c.wide ? 16 / es : 1;
+    const int64_t CC = c.C / E, cols = CC < kFlowThreads ? CC : kFlowThreads, lanes = kFlowThreads / cols;
+    f.grid = 2 * sms;
+    // about four pieces a CTA, of 16 KB at least and 64 KB at most, whole turns of the lanes
+    const int64_t row = c.C * es;
+    int64_t rows = (c.S * c.B + 4 * f.grid - 1) / (4 * f.grid);
+    rows = std::min<int64_t>(std::max<int64_t>(rows, (16 << 10) / row), std::max<int64_t>(1, (64 << 10) / row));
+    rows = std::max<int64_t>(1, (rows + lanes - 1) / lanes) * lanes;
+    while ((c.S + rows - 1) / rows > 65535) rows *= 2;
+    f.rows = (int)std::min<int64_t>(rows, c.S);
+    f.pieces = (int)((c.S + f.rows - 1) / f.rows);
+    f.lag = f.grid;
+    f.grid = (int)std::min<int64_t>(f.grid, c.B * f.pieces);
+    if (c.B * f.pieces <= f.lag) f.lag = 0;  // one turn of the CTAs: nothing to put between
+    f.smem = 2 * sizeof(float) * kFlowThreads * E + (size_t)c.G * sizeof(float2);
+    size_t at = 0;
+    auto take = [&at](size_t n) {
+        const size_t a = at;
+        at += (n + 255) / 256 * 256;
+        return a;
+    };
+    f.state_bytes = (size_t)(2 + 2 * c.B) * 4;
+    f.state = take(f.state_bytes);
+    f.part = take((size_t)c.B * f.pieces * c.G * sizeof(float2));
+    f.stat = take((size_t)c.B * c.G * sizeof(float2));
+    f.parts = f.folded = at;
+    f.folds = 0;
+    if (c.backward) {
+        f.parts = take((size_t)c.B * f.pieces * 2 * c.C * 4);
+        if (c.B * f.pieces > 512) f.folds = 64;  // (the finalizer sums 32 groups of rows, one after the other)
+        f.folded = take((size_t)f.folds * 2 * c.C * 4);
+    }
+    f.bytes = at;
+    return f;
 }
 
 static bool gn_sizes(int64_t B, int64_t S, int64_t C, int64_t G, int act, int dt) {
@@ -133,6 +141,12 @@ static bool gn_sizes(int64_t B, int64_t S, int64_t C, int64_t G, int act, int dt
     if (B > 0x7fffffffLL || S > 0x7fffffffLL) return false;
     if (B > 0 && S > INT64_MAX / 8 / C / B) return false;
     return act >= kActNone && act <= kActGelu;
+}
+
+// dgamma and dbeta from rows of both ([n, 2 C]).
+static int gn_finalize(int base, int w32, const float *rows, int n, int64_t C, void *dgamma, void *dbeta, int sms, cudaStream_t s) {
+    auto *fin = base == RMSNORM_F32 || w32 ? launch_dw_finalize_f32 : base == RMSNORM_BF16 ? launch_dw_finalize_bf16 : launch_dw_finalize_f16;
+    return fin(rows, n, (int)(2 * C), dgamma, dbeta, (int)C, 0, s, false, sms);
 }
 
 static rmsnorm_status_t gn_run_held(const GnParams &g, const GnCall &c, const GnHeld &h, void *dgamma, void *dbeta, int sms,
@@ -145,7 +159,6 @@ static rmsnorm_status_t gn_run_held(const GnParams &g, const GnCall &c, const Gn
     if (c.backward && !dgamma && !dbeta) p.g.parts = nullptr;
     p.ctas = h.ctas, p.W = h.W, p.K = h.K, p.spans = c.G / h.K;
     p.slab[0] = h.slab[0], p.slab[1] = h.slab[1], p.scales = h.scales;
-    p.magic = g.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + g.cg - 1) / g.cg);
     p.status = status;
     const void *k = gn_held(base, c.backward, c.wide, c.act, c.backward ? c.kept : g.codes != nullptr);
     if (h.ctas > 8) {
@@ -155,45 +168,41 @@ static rmsnorm_status_t gn_run_held(const GnParams &g, const GnCall &c, const Gn
     void *args[] = {&p};
     const int64_t grid = c.B * p.spans * h.ctas;
     int e = launch(k, (unsigned)grid, 1, kHeldThreads, h.smem, args, s, (unsigned)h.ctas);
-    if (e == 0 && c.backward && (dgamma || dbeta)) {
-        const bool f32 = base == RMSNORM_F32 || g.w32;
-        auto *fin = f32 ? launch_dw_finalize_f32 : base == RMSNORM_BF16 ? launch_dw_finalize_bf16 : launch_dw_finalize_f16;
-        e = fin(g.parts, (int)(c.B * h.ctas), (int)(2 * c.C), dgamma, dbeta, (int)c.C, 0, s, false, sms);
-    }
+    if (e == 0 && c.backward && (dgamma || dbeta)) e = gn_finalize(base, g.w32, g.parts, (int)(c.B * h.ctas), c.C, dgamma, dbeta, sms, s);
     return e == 0 ? RMSNORM_SUCCESS : head_cuda_fail(e);
 }
 
-static rmsnorm_status_t gn_run(GnParams &p, const GnCall &c, const GnPlan &plan, void *dgamma, void *dbeta, int sms,
-                               cudaStream_t s) {
-    const int base = c.dt & ~RMSNORM_WEIGHT_F32;
-    const int E = c.wide ? (base == RMSNORM_F32 ? 4 : 8) : 1;
-    const size_t stat = (size_t)p.G * sizeof(float2);
+static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const GnFlow &f, char *w, void *dgamma, void *dbeta,
+                                    int sms, int *status, cudaStream_t s) {
+    const int base = base_of(c.dt);
+    FlowParams p;
+    std::memset(&p, 0, sizeof p);
+    p.g = g;
+    p.g.rows = f.rows;
+    const bool sums = c.backward && (dgamma || dbeta);
+    p.g.parts = sums ? reinterpret_cast<float *>(w + f.parts) : nullptr;
+    p.pieces = f.pieces, p.lag = f.lag;
+    p.tickets = 2 * (c.B * f.pieces + f.pieces + f.lag);
+    p.state = reinterpret_cast<uint32_t *>(w + f.state);
+    p.part = reinterpret_cast<float2 *>(w + f.part), p.stat = reinterpret_cast<float2 *>(w + f.stat);
+    p.status = status;
+    int e = (int)cudaMemsetAsync(p.state, 0, f.state_bytes, s);
     void *args[] = {&p};
-    int e = 0;
-    const bool keep = !c.backward && p.codes;
-    for (int64_t b0 = 0; b0 < c.B && e == 0; b0 += plan.batch) {
-        p.b0 = (int)b0;
-        const unsigned nb = (unsigned)(c.B - b0 < plan.batch ? c.B - b0 : plan.batch);
-        if (!c.backward) {
-            e = launch(gn_kernel(kGnStats, base, c.wide, 0, false), plan.chunks, nb, plan.threads,
-                       2 * sizeof(float) * plan.threads * E + stat, args, s);
-            if (e == 0) e = launch(gn_kernel(kGnApply, base, c.wide, c.act, keep), plan.chunks, nb, plan.threads, stat, args, s);
-        } else {
-            e = launch(gn_kernel(kGnBwdSums, base, c.wide, c.act, c.kept), plan.chunks, nb, plan.threads,
-                       2 * sizeof(float) * plan.threads * E, args, s);
-            int gpc = 1;
-            while ((p.G + gpc - 1) / gpc > 4 * sms) gpc *= 2;
-            void *rargs[] = {&p, &gpc};
-            if (e == 0)
-                e = launch(gn_kernel(kGnBwdReduce, base, c.wide, 0, false), (unsigned)((p.G + gpc - 1) / gpc), nb,
-                           kGnReduceThreads, 0, rargs, s);
-            if (e == 0) e = launch(gn_kernel(kGnBwdApply, base, c.wide, c.act, c.kept), plan.chunks, nb, plan.threads, 0, args, s);
+    if (e == 0)
+        e = launch(gn_flow(base, c.backward, c.wide, c.act, c.backward ? c.kept : g.codes != nullptr), (unsigned)f.grid, 1, kFlowThreads,
+                   f.smem, args, s);
+    if (e == 0 && sums) {
+        const float *in = p.g.parts;
+        int64_t n = c.B * f.pieces;
+        if (f.folds) {
+            float *out = reinterpret_cast<float *>(w + f.folded);
+            int width = (int)(2 * c.C);
+            void *fargs[] = {&in, &out, &n, &width};
+            e = launch((const void *)gn_fold, (unsigned)((width + 255) / 256), (unsigned)f.folds, 256, 0, fargs, s);
+            in = out;
+            n = f.folds;
         }
-    }
-    if (e == 0 && c.backward && (dgamma || dbeta)) {
-        const bool f32 = base == RMSNORM_F32 || p.w32;
-        auto *fin = f32 ? launch_dw_finalize_f32 : base == RMSNORM_BF16 ? launch_dw_finalize_bf16 : launch_dw_finalize_f16;
-        e = fin(p.sums, (int)c.B, (int)(2 * c.C), dgamma, dbeta, (int)c.C, 0, s, false, sms);
+        if (e == 0) e = gn_finalize(base, g.w32, in, (int)n, c.C, dgamma, dbeta, sms, s);
     }
     return e == 0 ? RMSNORM_SUCCESS : head_cuda_fail(e);
 }
@@ -210,7 +219,7 @@ static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, b
             if (h.ctas)
                 most = backward ? std::max(most, held_bytes(c, h)) : most;
             else
-                most = std::max(most, gn_plan(c, sms).bytes);
+                most = std::max(most, flow_plan(c, sms).bytes);
         }
     }
     return most;
@@ -238,12 +247,12 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
     GnCall c{B, S, C, (int)G, act, dt, false, false, C % (16 / es) == 0 && on(x, 16) && on(y, 16)};
-    const GnPlan plan = gn_plan(c, sms);
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.gamma = gamma, p.beta = beta, p.out = y, p.mean = mean, p.rstd = rstd;
-    p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G), p.rows = plan.rows, p.chunks = plan.chunks;
-    p.act = act, p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32, p.eps = eps;
+    p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G);
+    p.magic = p.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + p.cg - 1) / p.cg);
+    p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32, p.eps = eps;
     // the codes in the same pass where rows are whole blocks of chunks
     const bool fused = codes && c.wide && C % kBlock8 == 0 && on(codes, 8);
     if (fused) p.codes = static_cast<uint8_t *>(codes), p.scales = scales;
@@ -253,10 +262,9 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     }
     const GnHeld h = held_plan(c, sms, fused);
     if (h.ctas) return gn_run_held(p, c, h, nullptr, nullptr, sms, status, s);
-    return with_workspace(workspace, workspace_bytes, plan.bytes, s, [&](char *w) {
-        p.parts = reinterpret_cast<float *>(w + plan.parts);
-        return gn_run(p, c, plan, nullptr, nullptr, sms, s);
-    });
+    const GnFlow f = flow_plan(c, sms);
+    return with_workspace(workspace, workspace_bytes, f.bytes, s,
+                          [&](char *w) { return gn_run_flow(p, c, f, w, nullptr, nullptr, sms, status, s); });
 }
 
 extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const void *codes, const uint8_t *scales,
@@ -279,21 +287,22 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     if (e != 0) return head_cuda_fail(e);
     GnCall c{B, S, C, (int)G, act, dt, true, codes != nullptr,
              C % (16 / es) == 0 && on(dy, 16) && on(dx, 16) && on(x, 16) && on(codes, 8)};
-    const GnPlan plan = gn_plan(c, sms);
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.dy = dy, p.codes_in = static_cast<const uint8_t *>(codes), p.scales_in = scales;
     p.gamma = gamma, p.beta = beta, p.out = dx, p.mean = const_cast<float *>(mean), p.rstd = const_cast<float *>(rstd);
-    p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G), p.rows = plan.rows, p.chunks = plan.chunks;
-    p.act = act, p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32;
+    p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G);
+    p.magic = p.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + p.cg - 1) / p.cg);
+    p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32;
     const GnHeld h = held_plan(c, sms, false);
-    return with_workspace(workspace, workspace_bytes, h.ctas ? held_bytes(c, h) : plan.bytes, s, [&](char *w) {
-        p.parts = reinterpret_cast<float *>(w + plan.parts);
-        if (h.ctas) return gn_run_held(p, c, h, dgamma, dbeta, sms, status, s);
-        p.sums = reinterpret_cast<float *>(w + plan.sums);
-        p.means = reinterpret_cast<float2 *>(w + plan.means);
-        return gn_run(p, c, plan, dgamma, dbeta, sms, s);
-    });
+    if (h.ctas)
+        return with_workspace(workspace, workspace_bytes, held_bytes(c, h), s, [&](char *w) {
+            p.parts = reinterpret_cast<float *>(w);
+            return gn_run_held(p, c, h, dgamma, dbeta, sms, status, s);
+        });
+    const GnFlow f = flow_plan(c, sms);
+    return with_workspace(workspace, workspace_bytes, f.bytes, s,
+                          [&](char *w) { return gn_run_flow(p, c, f, w, dgamma, dbeta, sms, status, s); });
 }
 
 extern "C" size_t groupnorm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward) {

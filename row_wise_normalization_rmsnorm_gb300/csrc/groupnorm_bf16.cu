@@ -2,6 +2,6 @@
 #include "groupnorm_held.cuh"
 
 namespace rmsn {
-const void *gn_kernel_bf16(int which, bool wide, int act, bool kept) { return gn_kernel_t<__nv_bfloat16>(which, wide, act, kept); }
+const void *gn_flow_bf16(bool backward, bool wide, int act, bool kept) { return gn_flow_t<__nv_bfloat16>(backward, wide, act, kept); }
 const void *gn_held_bf16(bool backward, bool wide, int act, bool kept) { return gn_held_t<__nv_bfloat16>(backward, wide, act, kept); }
 }  // namespace rmsn

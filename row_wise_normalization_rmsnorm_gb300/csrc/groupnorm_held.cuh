@@ -28,7 +28,6 @@ struct HeldParams {
     int W, K, spans;  // channels and groups a cluster takes, clusters a sample
     uint32_t slab[2];  // bytes a CTA's share of x (or its codes) and of dy has in shared memory
     uint32_t scales;   // and of scale bytes
-    uint32_t magic;    // ceil(2^32 / cg): c / cg = (c magic) >> 32 for c < 2^16
     int *status;
 };
 
@@ -105,9 +104,6 @@ template <int E> __device__ __forceinline__ void held_codes(const uint8_t *p, ui
     k.b = b;
     k.get(v);
 }
-
-// c / cg (magic 0: cg is 1)
-__device__ __forceinline__ int group_of(int c, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)c, magic) : c; }
 
 struct HeldPlace {
     int rank, b, c0, g0, rows;
@@ -196,42 +192,24 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
             }
             if (r == cut.lane && r < end) {
                 held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), K);
+#pragma unroll
+                for (int k = 0; k < E; ++k) K[k] = -K[k];
                 r += cut.lanes;
             }
 #pragma unroll 4
             for (; r < end; r += cut.lanes) {
                 float v[E];
                 held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), v);
-#pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    const float d = v[k] - K[k];
-                    s1[k] += d;
-                    s2[k] = fmaf(d, d, s2[k]);
-                }
+                gn_deviate(v, K, s1, s2);
             }
         }
-        const float inv = n > 0 ? 1.f / (float)n : 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float m = s1[i] * inv;
-            lane_mean[threadIdx.x * E + i] = K[i] + m;
-            lane_m2[threadIdx.x * E + i] = fmaxf(s2[i] - s1[i] * m, 0.f);
-        }
+        lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
         __syncthreads();
-        // a channel's lanes (each with n or n - 1 rows), about their common mean
-        const int width = cut.cols * E, used = min(cut.lanes, at.rows);
-        const float all = 1.f / (float)max(at.rows, 1);
-        for (int c = threadIdx.x; c < width && t0 * E + c < p.W; c += kHeldThreads) {
-            const float ref = lane_mean[c];
-            float s = 0.f, m2 = 0.f;
-            for (int l = 1; l < used; ++l) s += (float)((at.rows - l + cut.lanes - 1) / cut.lanes) * (lane_mean[l * width + c] - ref);
-            const float m = ref + s * all;
-            for (int l = 0; l < used; ++l) {
-                const float d = lane_mean[l * width + c] - m;
-                m2 += fmaf((float)((at.rows - l + cut.lanes - 1) / cut.lanes) * d, d, lane_m2[l * width + c]);
-            }
-            ch_mean[t0 * E + c] = m;
-            ch_m2[t0 * E + c] = m2;
+        join_lanes(lane_mean, lane_m2, cut.cols * E, cut.lanes, at.rows);
+        __syncthreads();
+        for (int c = threadIdx.x; c < cut.cols * E && t0 * E + c < p.W; c += kHeldThreads) {
+            ch_mean[t0 * E + c] = lane_mean[c];
+            ch_m2[t0 * E + c] = lane_m2[c];
         }
         __syncthreads();
     }
@@ -271,7 +249,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
             }
         }
         const float rs = 1.f / sqrtf(m2 / n + g.eps);
-        stat[k] = make_float2(m, rs);
+        stat[k] = make_float2(-m, rs);
         if (at.rank == 0) {
             g.mean[(int64_t)at.b * g.G + at.g0 + k] = m;
             g.rstd[(int64_t)at.b * g.G + at.g0 + k] = rs;
@@ -282,22 +260,16 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
     for (int t0 = 0; t0 < CW; t0 += cut.cols) {
         const int cc = t0 + cut.col;
         if (!cut.in || cc >= CW) continue;
-        float mean[E], f[E], beta[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = cc * E + i;
-            const float2 s = stat[group_of(c, p.magic)];
-            mean[i] = s.x;
-            f[i] = s.y * param<T>(g.gamma, g.w32, at.c0 + c, 1.f);
-            beta[i] = param<T>(g.beta, g.w32, at.c0 + c, 0.f);
-        }
+        float minus_mean[E], f[E], beta[E], gamma[E];
+        groups_v(stat, cc * E, g.cg, g.magic, minus_mean, f);
+        params_v<T>(g.gamma, g.w32, at.c0 + cc * E, 1.f, gamma);
+        params_v<T>(g.beta, g.w32, at.c0 + cc * E, 0.f, beta);
+        mul_v(f, gamma, f);
 #pragma unroll 2
         for (int r = cut.lane; r < at.rows; r += cut.lanes) {
             float v[E], z[E];
             held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) z[i] = fmaf(v[i] - mean[i], f[i], beta[i]);
-            act_of<T, ACT>(z);
+            gn_value<T, ACT>(v, minus_mean, f, beta, z);
             Vals<T, E> o;
             o.set(z);
             o.store(y + (int64_t)r * g.C + cc * E);
@@ -381,37 +353,23 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
     }
     for (int k = threadIdx.x; k < p.K; k += kHeldThreads) {
         const int64_t i = (int64_t)at.b * g.G + at.g0 + k;
-        stat[k] = make_float2(g.mean[i], g.rstd[i]);
+        stat[k] = make_float2(-g.mean[i], g.rstd[i]);
     }
     __syncthreads();
-    // xhat, u and z's slope of a chunk: what both passes form anew
-    auto chunk = [&](int r, int cc, const float (&mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E],
+    // xhat and u of a chunk: what both passes form anew
+    auto chunk = [&](int r, int cc, const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E],
                      float (&xhat)[E], float (&u)[E]) {
-        float z[E];
         if constexpr (KEPT)
             held_codes<E>(xrows + (size_t)r * xpitch + cc * E, sc[r * nsc + (at.c0 + cc * E) / kBlock8 - sc0], xhat);
         else
             held_values<T, E>(xrows + (size_t)r * xpitch + cc * (E * XE), xhat);
         held_values<T, E>(drows + (size_t)r * dpitch + cc * (E * sizeof(T)), u);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            xhat[i] = (xhat[i] - mean[i]) * rstd[i];
-            z[i] = fmaf(xhat[i], gamma[i], beta[i]);
-        }
-        act_slope<T, ACT>(z);
-#pragma unroll
-        for (int i = 0; i < E; ++i) u[i] *= z[i];
+        gn_slope<T, ACT>(xhat, u, minus_mean, rstd, gamma, beta);
     };
-    auto constants = [&](int cc, float (&mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = cc * E + i;
-            const float2 s = stat[group_of(c, p.magic)];
-            mean[i] = s.x;
-            rstd[i] = s.y;
-            gamma[i] = param<T>(g.gamma, g.w32, at.c0 + c, 1.f);
-            beta[i] = param<T>(g.beta, g.w32, at.c0 + c, 0.f);
-        }
+    auto constants = [&](int cc, float (&minus_mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
+        groups_v(stat, cc * E, g.cg, g.magic, minus_mean, rstd);
+        params_v<T>(g.gamma, g.w32, at.c0 + cc * E, 1.f, gamma);
+        params_v<T>(g.beta, g.w32, at.c0 + cc * E, 0.f, beta);
     };
     float *out = g.parts + ((int64_t)at.b * p.ctas + at.rank) * 2 * g.C;
     for (int t0 = 0; t0 < CW; t0 += cut.cols) {
@@ -440,11 +398,8 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
             for (; r < end; r += cut.lanes) {
                 float xhat[E], u[E];
                 chunk(r, cc, mean, rstd, gamma, beta, xhat, u);
-#pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    a[k] = fmaf(u[k], xhat[k], a[k]);
-                    s[k] += u[k];
-                }
+                fma_v(u, xhat, a, a);
+                add_v(s, u, s);
             }
         }
 #pragma unroll
@@ -484,7 +439,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
         const float n = (float)g.S * (float)g.cg;
         float2 m = exch[k];
         for (int r = 1; r < p.ctas; ++r) m = add2(m, exch[r * p.K + k]);
-        means[k] = make_float2(m.x / n, m.y / n);
+        means[k] = make_float2(-m.x / n, -m.y / n);
     }
     __syncthreads();
     T *dx = static_cast<T *>(g.out) + at.first * g.C + at.c0;
@@ -493,15 +448,13 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
         if (!cut.in || cc >= CW) continue;
         float mean[E], rstd[E], gamma[E], beta[E];
         constants(cc, mean, rstd, gamma, beta);
-        float2 m[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) m[i] = means[group_of(cc * E + i, p.magic)];
+        float m1[E], m2[E];
+        groups_v(means, cc * E, g.cg, g.magic, m1, m2);
 #pragma unroll 1
         for (int r = cut.lane; r < at.rows; r += cut.lanes) {
             float xhat[E], u[E];
             chunk(r, cc, mean, rstd, gamma, beta, xhat, u);
-#pragma unroll
-            for (int i = 0; i < E; ++i) u[i] = rstd[i] * (fmaf(u[i], gamma[i], -m[i].x) - xhat[i] * m[i].y);
+            gn_dx(xhat, u, rstd, gamma, m1, m2);
             Vals<T, E> o;
             o.set(u);
             o.store(dx + (int64_t)r * g.C + cc * E);
@@ -531,9 +484,5 @@ template <typename T, int E> static const void *gn_held_e(bool backward, int act
 template <typename T> static const void *gn_held_t(bool backward, bool wide, int act, bool kept) {
     return wide ? gn_held_e<T, Elem<T>::E>(backward, act, kept) : gn_held_e<T, 1>(backward, act, kept);
 }
-
-const void *gn_held_f32(bool backward, bool wide, int act, bool kept);
-const void *gn_held_bf16(bool backward, bool wide, int act, bool kept);
-const void *gn_held_f16(bool backward, bool wide, int act, bool kept);
 
 }  // namespace rmsn

@@ -29,14 +29,12 @@ struct GnParams {
     void *out;                 // y or dx
     float *mean, *rstd;        // [B, G]
     uint8_t *codes, *scales;   // x kept in 8 bits (forward) or NULL
-    float *parts;              // a chunk's sums: [B, chunks, G, 2] (forward), [B, chunks, 2, C] (backward)
-    float *sums;               // backward: [B, 2, C], a sample's sums of u xhat and of u
-    float2 *means;             // backward: [B, G], the group means of u gamma and of u gamma xhat
+    float *parts;              // backward: [pieces, 2, C], a piece's channel sums of u xhat and of u (NULL: not wanted)
     int64_t S;
     int B, C, G, cg;           // cg = C / G
-    int b0;                    // first sample of the launch
-    int rows, chunks;          // rows a CTA takes, CTAs a sample
-    int act, w32;
+    int rows;                  // places a CTA takes
+    int w32;
+    uint32_t magic;            // ceil(2^32 / cg), 0 where cg is 1
     float eps;
 };
 
@@ -118,72 +116,185 @@ template <typename T> __device__ __forceinline__ float param(const void *w, int 
     return w32 ? static_cast<const float *>(w)[c] : widen<T>(static_cast<const T *>(w)[c]);
 }
 
+// ---------------------------------------------------------- chunk arithmetic --
+// E values at once, in pairs where there are two (f32x2 instructions: these
+// kernels are as near to their instruction rate as to memory's).
+template <int E> __device__ __forceinline__ void fma_v(const float (&a)[E], const float (&b)[E], const float (&c)[E], float (&d)[E]) {
+    if constexpr (E == 1) {
+        d[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float2 r = Pair<true>::fma(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+            d[i] = r.x, d[i + 1] = r.y;
+        }
+    }
+}
+template <int E> __device__ __forceinline__ void mul_v(const float (&a)[E], const float (&b)[E], float (&d)[E]) {
+    if constexpr (E == 1) {
+        d[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float2 r = Pair<true>::mul(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+            d[i] = r.x, d[i + 1] = r.y;
+        }
+    }
+}
+template <int E> __device__ __forceinline__ void add_v(const float (&a)[E], const float (&b)[E], float (&d)[E]) {
+    if constexpr (E == 1) {
+        d[0] = a[0] + b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float2 r = Pair<true>::add(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+            d[i] = r.x, d[i + 1] = r.y;
+        }
+    }
+}
+template <int E> __device__ __forceinline__ void fill_v(float v, float (&d)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) d[i] = v;
+}
+
 // ------------------------------------------------------------- activations --
-// The sigmoids of two values. For 16-bit rows one reciprocal serves both
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The sigmoids of E values. For 16-bit rows one reciprocal serves two
 // (1 / a = b / (a b)): the special-function unit, 16 results a clock and SM,
 // bounds these kernels next to memory, and so it gives 1.5 results a value
 // instead of 2. z is held at -43, where the sigmoid is 2^-62 and a b still
-// finite. fp32 rows take the accurate exponential.
-template <typename T> __device__ __forceinline__ float2 sigmoid2(float2 z) {
+// finite. (fmaxf drops a NaN; z, which every result is multiplied by, brings
+// it back.) fp32 rows take the accurate exponential.
+template <typename T, int E> __device__ __forceinline__ void sigmoid_v(const float (&z)[E], float (&p)[E]) {
     if constexpr (std::is_same<T, float>::value) {
-        return make_float2(__fdividef(1.f, 1.f + expf(-z.x)), __fdividef(1.f, 1.f + expf(-z.y)));
+#pragma unroll
+        for (int i = 0; i < E; ++i) p[i] = rcp_fast(1.f + expf(-z[i]));
+    } else if constexpr (E == 1) {
+        p[0] = rcp_fast(1.f + exp2_fast(-1.4426950f * fmaxf(z[0], -43.f)));
     } else {
-        const float a = 1.f + __expf(-fmaxf(z.x, -43.f)), b = 1.f + __expf(-fmaxf(z.y, -43.f));
-        const float r = __fdividef(1.f, a * b);
-        return make_float2(r * b, r * a);
+#pragma unroll
+        for (int i = 0; i < E; ++i) p[i] = fmaxf(z[i], -43.f);
+        float k[E], one[E];
+        fill_v(-1.4426950f, k);
+        fill_v(1.f, one);
+        mul_v(p, k, p);
+#pragma unroll
+        for (int i = 0; i < E; ++i) p[i] = exp2_fast(p[i]);
+        add_v(p, one, p);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float r = rcp_fast(p[i] * p[i + 1]);
+            const float2 q = Pair<true>::mul(make_float2(r, r), make_float2(p[i + 1], p[i]));
+            p[i] = q.x, p[i + 1] = q.y;
+        }
     }
 }
-template <typename T> __device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (std::is_same<T, float>::value)
-        return __fdividef(1.f, 1.f + expf(-z));
-    else
-        return __fdividef(1.f, 1.f + __expf(-fmaxf(z, -43.f)));
-}
-// (fmaxf drops a NaN: z, which every result is multiplied by, brings it back.)
-
 __device__ __forceinline__ float gelu_of(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); }
 __device__ __forceinline__ float gelu_slope(float z) {
     return 0.5f * (1.f + erff(z * 0.70710678f)) + z * __expf(-0.5f * z * z) * 0.39894228f;
 }
 
-// act(z) and act'(z) of E values, in place.
+// act(z), act'(z) in place.
 template <typename T, int ACT, int E> __device__ __forceinline__ void act_of(float (&z)[E]) {
     if constexpr (ACT == kActSilu) {
-        if constexpr (E > 1) {
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const float2 p = sigmoid2<T>(make_float2(z[i], z[i + 1]));
-                z[i] *= p.x, z[i + 1] *= p.y;
-            }
-        } else {
-            z[0] *= sigmoid<T>(z[0]);
-        }
+        float p[E];
+        sigmoid_v<T>(z, p);
+        mul_v(z, p, z);
     } else if constexpr (ACT == kActGelu) {
 #pragma unroll
         for (int i = 0; i < E; ++i) z[i] = gelu_of(z[i]);
     }
 }
 template <typename T, int ACT, int E> __device__ __forceinline__ void act_slope(float (&z)[E]) {
-    if constexpr (ACT == kActSilu) {
-        float p[E];
-        if constexpr (E > 1) {
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const float2 q = sigmoid2<T>(make_float2(z[i], z[i + 1]));
-                p[i] = q.x, p[i + 1] = q.y;
-            }
-        } else {
-            p[0] = sigmoid<T>(z[0]);
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) z[i] = p[i] * fmaf(z[i], 1.f - p[i], 1.f);
+    if constexpr (ACT == kActSilu) {  // p (1 + z (1 - p))
+        float p[E], one[E], minus[E], q[E];
+        sigmoid_v<T>(z, p);
+        fill_v(1.f, one);
+        fill_v(-1.f, minus);
+        fma_v(p, minus, one, q);
+        fma_v(z, q, one, q);
+        mul_v(p, q, z);
     } else if constexpr (ACT == kActGelu) {
 #pragma unroll
         for (int i = 0; i < E; ++i) z[i] = gelu_slope(z[i]);
     } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) z[i] = 1.f;
+        fill_v(1.f, z);
     }
+}
+
+// gamma and beta of E channels from c0 (NULL: 1 and 0).
+template <typename T, int E> __device__ __forceinline__ void params_v(const void *w, int w32, int c0, float none, float (&v)[E]) {
+    if (!w) {
+        fill_v(none, v);
+    } else if (w32) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = static_cast<const float *>(w)[c0 + i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = widen<T>(static_cast<const T *>(w)[c0 + i]);
+    }
+}
+// A group's pair of values for each of E channels from c0 (of the groups at
+// `of`): one look where the chunk lies in a group.
+template <int E> __device__ __forceinline__ void groups_v(const float2 *of, int c0, int cg, uint32_t magic, float (&x)[E], float (&y)[E]) {
+    // c / cg for c < 2^16 (magic = ceil(2^32 / cg), 0 where cg is 1)
+    auto group = [&](int c) { return magic ? (int)__umulhi((uint32_t)c, magic) : c; };
+    if (cg % E == 0) {
+        const float2 s = of[group(c0)];
+        fill_v(s.x, x);
+        fill_v(s.y, y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float2 s = of[group(c0 + i)];
+            x[i] = s.x;
+            y[i] = s.y;
+        }
+    }
+}
+
+// y = act((v - mean) f + beta), f = rstd gamma; v and the result in z.
+template <typename T, int ACT, int E>
+__device__ __forceinline__ void gn_value(const float (&v)[E], const float (&minus_mean)[E], const float (&f)[E], const float (&beta)[E], float (&z)[E]) {
+    add_v(v, minus_mean, z);
+    fma_v(z, f, beta, z);
+    act_of<T, ACT>(z);
+}
+// v becomes xhat and g (dy) u = dy act'(xhat gamma + beta).
+template <typename T, int ACT, int E>
+__device__ __forceinline__ void gn_slope(float (&v)[E], float (&g)[E], const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E]) {
+    float z[E];
+    add_v(v, minus_mean, v);
+    mul_v(v, rstd, v);
+    if constexpr (ACT != kActNone) {
+        fma_v(v, gamma, beta, z);
+        act_slope<T, ACT>(z);
+        mul_v(g, z, g);
+    }
+}
+// dx from xhat and u, in u: rstd (u gamma - m1 - xhat m2), m1 and m2 given negated.
+template <int E>
+__device__ __forceinline__ void gn_dx(const float (&xhat)[E], float (&u)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&minus_m1)[E], const float (&minus_m2)[E]) {
+    fma_v(u, gamma, minus_m1, u);
+    fma_v(xhat, minus_m2, u, u);
+    mul_v(u, rstd, u);
+}
+// Sums of deviations from K and of their squares.
+template <int E> __device__ __forceinline__ void gn_deviate(const float (&v)[E], const float (&minus_K)[E], float (&s1)[E], float (&s2)[E]) {
+    float d[E];
+    add_v(v, minus_K, d);
+    add_v(s1, d, s1);
+    fma_v(d, d, s2, s2);
 }
 
 // ------------------------------------------------------------ the CTA's cut --
@@ -202,194 +313,6 @@ struct Cut {
     }
 };
 
-constexpr int kGnBatch = 4;  // rows of a thread under way at once
-
-// ----------------------------------------------------------------- forward --
-// A chunk of rows' statistics, (mean, sum of squared deviations) for each
-// group. A thread sums (x - K) and (x - K)^2 a channel, K its first value, so
-// a mean far from zero costs no digits: the error of its sum of squares is at
-// most rows 2^-24 of it, whatever K is, and the pieces are then joined about
-// their own means.
-template <typename T, int E>
-__global__ void __launch_bounds__(512) gn_stats(const GnParams p) {
-    extern __shared__ float sm[];
-    float *sm_mean = sm, *sm_m2 = sm + blockDim.x * E;
-    float2 *acc = reinterpret_cast<float2 *>(sm + 2 * blockDim.x * E);  // [G], (mean, M2) over the tiles so far
-    pdl_wait();
-    pdl_trigger();
-    const int b = p.b0 + blockIdx.y;
-    const int64_t r0 = (int64_t)blockIdx.x * p.rows;
-    const int rows = (int)min((int64_t)p.rows, p.S - r0);
-    const int CC = p.C / E;
-    const Cut cut(CC);
-    const T *x = static_cast<const T *>(p.x) + ((int64_t)b * p.S + r0) * p.C;
-    for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-        const int cc = t0 + cut.col;
-        const int n = cut.in && cc < CC && cut.lane < rows ? (rows - cut.lane + cut.lanes - 1) / cut.lanes : 0;
-        float K[E], s1[E], s2[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) K[i] = s1[i] = s2[i] = 0.f;
-        const T *px = x + (int64_t)cut.lane * p.C + (int64_t)cc * E;
-        const int64_t step = (int64_t)cut.lanes * p.C;
-        for (int k = 0; k < n; k += kGnBatch) {
-            Vals<T, E> c[kGnBatch];
-#pragma unroll
-            for (int q = 0; q < kGnBatch; ++q)
-                if (k + q < n) c[q].load(px + (k + q) * step);
-#pragma unroll
-            for (int q = 0; q < kGnBatch; ++q)
-                if (k + q < n) {
-                    float v[E];
-                    c[q].get(v);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        if (k + q == 0) K[i] = v[i];
-                        const float d = v[i] - K[i];
-                        s1[i] += d;
-                        s2[i] = fmaf(d, d, s2[i]);
-                    }
-                }
-        }
-        const float inv = n > 0 ? 1.f / (float)n : 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float m = s1[i] * inv;
-            sm_mean[threadIdx.x * E + i] = K[i] + m;
-            sm_m2[threadIdx.x * E + i] = fmaxf(s2[i] - s1[i] * m, 0.f);
-        }
-        __syncthreads();
-        // a warp a group: the lanes' and channels' pieces of this tile, then joined with the tiles before
-        const int c0 = t0 * E, c1 = min((t0 + cut.cols) * E, p.C);
-        const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-        const int width = cut.cols * E;
-        for (int g = c0 / p.cg + warp; g * p.cg < c1; g += blockDim.x >> 5) {
-            const int lo = max(g * p.cg, c0), w = min((g + 1) * p.cg, c1) - lo;
-            const int used = min(cut.lanes, rows);  // lanes with rows
-            const float *mean0 = sm_mean + (lo - c0), *m20 = sm_m2 + (lo - c0);
-            const float ref = mean0[0];
-            float s = 0.f;
-            for (int i = wl; i < used * w; i += 32) {
-                const int l = i / w, c = i - l * w;
-                s += (float)((rows - l + cut.lanes - 1) / cut.lanes) * (mean0[l * width + c] - ref);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float cnt = (float)rows * (float)w;
-            float m = ref + s / cnt, m2 = 0.f;
-            for (int i = wl; i < used * w; i += 32) {
-                const int l = i / w, c = i - l * w;
-                const float d = mean0[l * width + c] - m;
-                m2 += fmaf((float)((rows - l + cut.lanes - 1) / cut.lanes) * d, d, m20[l * width + c]);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-            if (wl == 0) {
-                if (lo > g * p.cg) {  // the group's first channels were in earlier tiles
-                    const float2 a = acc[g];
-                    const float na = (float)rows * (float)(lo - g * p.cg), all = na + cnt, d = m - a.x;
-                    m = a.x + d * (cnt / all);
-                    m2 = a.y + m2 + d * d * (na * (cnt / all));
-                }
-                if (lo + w < (g + 1) * p.cg)
-                    acc[g] = make_float2(m, m2);
-                else
-                    reinterpret_cast<float2 *>(p.parts)[((int64_t)b * p.chunks + blockIdx.x) * p.G + g] = make_float2(m, m2);
-            }
-        }
-        __syncthreads();
-    }
-}
-
-// A sample's statistics from its chunks', into shared memory (every CTA of
-// the sample joins them anew, in one order: all have the same bits).
-__device__ __forceinline__ void gn_join(const GnParams &p, int b, float2 *stat, bool write) {
-    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-    for (int g = warp; g < p.G; g += blockDim.x >> 5) {
-        const float2 *part = reinterpret_cast<const float2 *>(p.parts) + (int64_t)b * p.chunks * p.G + g;
-        const float ref = part[0].x;
-        const float n = (float)p.S * (float)p.cg;
-        auto count = [&](int i) { return (float)min((int64_t)p.rows, p.S - (int64_t)i * p.rows) * (float)p.cg; };
-        float s = 0.f;
-        for (int i = wl; i < p.chunks; i += 32) s += count(i) * (part[(int64_t)i * p.G].x - ref);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float m = ref + s / n;
-        float m2 = 0.f;
-        for (int i = wl; i < p.chunks; i += 32) {
-            const float2 a = part[(int64_t)i * p.G];
-            const float d = a.x - m;
-            m2 += fmaf(count(i) * d, d, a.y);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-        if (wl == 0) {
-            const float r = 1.f / sqrtf(m2 / n + p.eps);
-            stat[g] = make_float2(m, r);
-            if (write) {
-                p.mean[(int64_t)b * p.G + g] = m;
-                p.rstd[(int64_t)b * p.G + g] = r;
-            }
-        }
-    }
-}
-
-template <typename T, int E, int ACT, bool KEEP>
-__global__ void __launch_bounds__(512) gn_apply(const GnParams p) {
-    extern __shared__ float sm[];
-    float2 *stat = reinterpret_cast<float2 *>(sm);
-    pdl_wait();
-    pdl_trigger();
-    const int b = p.b0 + blockIdx.y;
-    const int64_t r0 = (int64_t)blockIdx.x * p.rows;
-    const int rows = (int)min((int64_t)p.rows, p.S - r0);
-    const int CC = p.C / E;
-    const Cut cut(CC);
-    gn_join(p, b, stat, blockIdx.x == 0);
-    __syncthreads();
-    const int64_t at = ((int64_t)b * p.S + r0) * p.C;
-    const T *x = static_cast<const T *>(p.x) + at;
-    T *y = static_cast<T *>(p.out) + at;
-    for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-        const int cc = t0 + cut.col;
-        if (!cut.in || cc >= CC) continue;
-        float mean[E], f[E], beta[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = cc * E + i;
-            const float2 s = stat[c / p.cg];
-            mean[i] = s.x;
-            f[i] = s.y * param<T>(p.gamma, p.w32, c, 1.f);
-            beta[i] = param<T>(p.beta, p.w32, c, 0.f);
-        }
-        for (int r = cut.lane; r < rows; r += kGnBatch * cut.lanes) {
-            Vals<T, E> c[kGnBatch];
-#pragma unroll
-            for (int q = 0; q < kGnBatch; ++q)
-                if (r + q * cut.lanes < rows) c[q].load_last(x + (int64_t)(r + q * cut.lanes) * p.C + cc * E);
-#pragma unroll
-            for (int q = 0; q < kGnBatch; ++q) {
-                const int rr = r + q * cut.lanes;
-                if (rr < rows) {
-                    float v[E], z[E];
-                    c[q].get(v);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) z[i] = fmaf(v[i] - mean[i], f[i], beta[i]);
-                    act_of<T, ACT>(z);
-                    Vals<T, E> o;
-                    o.set(z);
-                    o.store(y + (int64_t)rr * p.C + cc * E);
-                    if constexpr (KEEP) {
-                        const int64_t row = (int64_t)b * p.S + r0 + rr;
-                        keep_chunk<T, E>(v, true, p.codes + row * p.C + cc * E, p.scales + row * (p.C / kBlock8) + cc * E / kBlock8);
-                    }
-                }
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------- backward --
-
 // x of E channels, from its rows or from what they are kept as.
 template <typename T, int E, bool KEPT> struct XLoad {
     typename std::conditional<KEPT, Kept<E>, Vals<T, E>>::type c;
@@ -401,239 +324,487 @@ template <typename T, int E, bool KEPT> struct XLoad {
     }
 };
 
-// A chunk of rows' sums of u xhat and of u for each channel.
-template <typename T, int E, int ACT, bool KEPT>
-__global__ void __launch_bounds__(256) gn_bwd_sums(const GnParams p) {
+// ----------------------------------------------------------------- the flow --
+// Samples that no cluster holds: one launch of persistent CTAs that take
+// pieces (rows of a sample) by ticket, first to sum them and, `lag` pieces
+// behind the sample's last sum, to normalise them. By then the piece's sample
+// is summed and its rows still lie in the L2, so memory reads them once, and
+// reads and writes overlap all the way. A piece waits only for pieces with
+// earlier tickets, which running CTAs have taken and which wait for none:
+// the launch makes progress however few of its CTAs run at once.
+//
+// A piece's group statistics, (mean, sum of squared deviations) or the two
+// sums of the gradient, go to memory; the CTA that brings a sample's last
+// ones joins them, in the pieces' order.
+
+struct FlowParams {
+    GnParams g;
+    int pieces, lag;     // of a sample; S and A tickets of a piece lie pieces + lag pairs apart
+    int64_t tickets;
+    uint32_t *state;     // [0], [1]: the next ticket (64 bits); then [B] pieces summed, [B] samples joined. Zeros at the start
+    float2 *part;        // [B, pieces, G]
+    float2 *stat;        // [B, G]: (-mean, rstd), or the negated means of u gamma and of u gamma xhat
+    int *status;
+};
+
+constexpr int kFlowThreads = 256;
+constexpr uint32_t kFlowWaitLimit = 1u << 22;  // polls of 100 ns for a sample's statistics
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+struct FlowShared {
+    unsigned long long ticket;
+    uint32_t before;
+};
+
+// The CTA's next ticket.
+__device__ __forceinline__ int64_t next_ticket(const FlowParams &p, FlowShared &s) {
+    __syncthreads();  // everybody is done with the last one
+    if (threadIdx.x == 0) s.ticket = atomicAdd(reinterpret_cast<unsigned long long *>(p.state), 1ull);
+    __syncthreads();
+    return (int64_t)s.ticket;
+}
+
+// Joins a sample's pieces where this CTA's was the last: `join(g, sub, subs)`
+// by `subs` neighbouring lanes a group.
+template <class Join> __device__ __forceinline__ void sum_given(const FlowParams &p, FlowShared &s, int b, Join &&join) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s.before = atomicAdd(p.state + 2 + b, 1u);
+    __syncthreads();
+    if (s.before != (uint32_t)p.pieces - 1) return;
+    __threadfence();
+    constexpr int subs = 8;
+    for (int g = threadIdx.x / subs; g < (p.g.G + kFlowThreads / subs - 1) / (kFlowThreads / subs) * (kFlowThreads / subs); g += kFlowThreads / subs)
+        join(g, (int)threadIdx.x % subs, subs);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) st_release(p.state + 2 + p.g.B + b, 1u);
+}
+__device__ __forceinline__ void wait_joined(const FlowParams &p, int b) {
+    if (threadIdx.x == 0) {
+        uint32_t k = 0;
+        while (ld_acquire(p.state + 2 + p.g.B + b) == 0 && ++k < kFlowWaitLimit) __nanosleep(100);
+        if (k >= kFlowWaitLimit && p.status) *p.status = 1;
+    }
+    __syncthreads();
+}
+template <int subs> __device__ __forceinline__ float sub_sum(float v) {
+#pragma unroll
+    for (int o = subs / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A thread's sums of (x - K) and (x - K)^2 a channel as mean and sum of
+// squared deviations. K is its first value, so a mean far from zero costs no
+// digits: the error of its sum of squares is at most n 2^-24 of it.
+template <int E> __device__ __forceinline__ void lane_stats(int n, const float (&minus_K)[E], const float (&s1)[E], const float (&s2)[E], float *mean, float *m2) {
+    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float m = s1[i] * inv;
+        mean[i] = m - minus_K[i];
+        m2[i] = fmaxf(s2[i] - s1[i] * m, 0.f);
+    }
+}
+// The lanes' statistics of each of `width` channels ([lanes, width]) joined
+// about their common mean, in place of lane 0's; `rows` in all.
+__device__ __forceinline__ void join_lanes(float *mean, float *m2, int width, int lanes, int rows) {
+    const int used = min(lanes, rows);
+    const float all = 1.f / (float)max(rows, 1);
+    for (int c = threadIdx.x; c < width; c += blockDim.x) {
+        const float ref = mean[c];
+        float s = 0.f, q = 0.f;
+#pragma unroll 4
+        for (int l = 1; l < used; ++l) s += (float)((rows - l + lanes - 1) / lanes) * (mean[l * width + c] - ref);
+        const float m = ref + s * all;
+#pragma unroll 4
+        for (int l = 0; l < used; ++l) {
+            const float d = mean[l * width + c] - m;
+            q += fmaf((float)((rows - l + lanes - 1) / lanes) * d, d, m2[l * width + c]);
+        }
+        mean[c] = m;
+        m2[c] = q;
+    }
+}
+
+template <typename T, int E, int ACT, bool KEEP>
+__global__ void __launch_bounds__(kFlowThreads, 2) gn_fwd_flow(const FlowParams p) {
     extern __shared__ float sm[];
-    float *sa = sm, *sb = sm + blockDim.x * E;
+    __shared__ FlowShared fs;
+    float *lane_mean = sm, *lane_m2 = sm + kFlowThreads * E;
+    float2 *acc = reinterpret_cast<float2 *>(sm + 2 * kFlowThreads * E);  // [G]: groups over several tiles; then the statistics
+    const GnParams &g = p.g;
     pdl_wait();
     pdl_trigger();
-    const int b = p.b0 + blockIdx.y;
-    const int64_t r0 = (int64_t)blockIdx.x * p.rows;
-    const int rows = (int)min((int64_t)p.rows, p.S - r0);
-    const int64_t first = (int64_t)b * p.S + r0;
-    const int CC = p.C / E;
+    const int CC = g.C / E;
     const Cut cut(CC);
-    const T *dy = static_cast<const T *>(p.dy) + first * p.C;
-    float *out = p.parts + ((int64_t)b * p.chunks + blockIdx.x) * 2 * p.C;
-    for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-        const int cc = t0 + cut.col;
-        const bool in = cut.in && cc < CC;
-        float a[E], s[E];
+    const int64_t all = (int64_t)g.B * p.pieces;
+    for (;;) {
+        const int64_t ticket = next_ticket(p, fs);
+        if (ticket >= p.tickets) return;
+        const bool normalise = ticket & 1;
+        const int64_t item = (ticket >> 1) - (normalise ? p.pieces + p.lag : 0);
+        if (item < 0 || item >= all) continue;
+        const int b = (int)(item / p.pieces), piece = (int)(item - (int64_t)b * p.pieces);
+        const int64_t r0 = (int64_t)piece * g.rows, first = (int64_t)b * g.S + r0;
+        const int rows = (int)min((int64_t)g.rows, g.S - r0);
+        const T *x = static_cast<const T *>(g.x) + first * g.C;
+        const int64_t step = (int64_t)cut.lanes * g.C;
+        if (!normalise) {
+            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+                const int cc = t0 + cut.col;
+                const int n = cut.in && cc < CC && cut.lane < rows ? (rows - cut.lane + cut.lanes - 1) / cut.lanes : 0;
+                float K[E], s1[E], s2[E];
+                fill_v(0.f, K);
+                fill_v(0.f, s1);
+                fill_v(0.f, s2);
+                const T *px = x + (int64_t)cut.lane * g.C + cc * E;
+                if (n > 0) {
+                    Vals<T, E> c;
+                    c.load(px);
+                    c.get(K);
 #pragma unroll
-        for (int i = 0; i < E; ++i) a[i] = s[i] = 0.f;
-        if (in) {
-            float mean[E], rstd[E], gamma[E], beta[E];
+                    for (int i = 0; i < E; ++i) K[i] = -K[i];
+                }
+                constexpr int BATCH = 8;
+                int k = 1;
+                for (; k + BATCH <= n; k += BATCH) {
+                    Vals<T, E> c[BATCH];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = cc * E + i;
-                mean[i] = p.mean[(int64_t)b * p.G + c / p.cg];
-                rstd[i] = p.rstd[(int64_t)b * p.G + c / p.cg];
-                gamma[i] = param<T>(p.gamma, p.w32, c, 1.f);
-                beta[i] = param<T>(p.beta, p.w32, c, 0.f);
+                    for (int q = 0; q < BATCH; ++q) c[q].load(px + (k + q) * step);
+#pragma unroll
+                    for (int q = 0; q < BATCH; ++q) {
+                        float v[E];
+                        c[q].get(v);
+                        gn_deviate(v, K, s1, s2);
+                    }
+                }
+#pragma unroll 4
+                for (; k < n; ++k) {
+                    Vals<T, E> c;
+                    c.load(px + k * step);
+                    float v[E];
+                    c.get(v);
+                    gn_deviate(v, K, s1, s2);
+                }
+                lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
+                __syncthreads();
+                join_lanes(lane_mean, lane_m2, cut.cols * E, cut.lanes, rows);
+                __syncthreads();
+                // a warp a group: this tile's channels, joined with the tiles before
+                const int c0 = t0 * E, c1 = min((t0 + cut.cols) * E, g.C);
+                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+                for (int k2 = c0 / g.cg + warp; k2 * g.cg < c1; k2 += kFlowThreads / 32) {
+                    const int lo = max(k2 * g.cg, c0), w = min((k2 + 1) * g.cg, c1) - lo;
+                    const float *cm = lane_mean + (lo - c0), *cq = lane_m2 + (lo - c0);
+                    const float ref = cm[0];
+                    float s = 0.f, m2 = 0.f;
+                    for (int c = wl; c < w; c += 32) s += cm[c] - ref;
+                    s = sub_sum<32>(s);
+                    float m = ref + s / (float)w;
+                    for (int c = wl; c < w; c += 32) {
+                        const float d = cm[c] - m;
+                        m2 += fmaf((float)rows * d, d, cq[c]);
+                    }
+                    m2 = sub_sum<32>(m2);
+                    if (wl == 0) {
+                        const float cnt = (float)rows * (float)w;
+                        if (lo > k2 * g.cg) {
+                            const float2 a = acc[k2];
+                            const float na = (float)rows * (float)(lo - k2 * g.cg), d = m - a.x, share = cnt / (na + cnt);
+                            m = a.x + d * share;
+                            m2 = a.y + m2 + d * d * (na * share);
+                        }
+                        if (lo + w < (k2 + 1) * g.cg)
+                            acc[k2] = make_float2(m, m2);
+                        else
+                            p.part[item * g.G + k2] = make_float2(m, m2);
+                    }
+                }
+                __syncthreads();
             }
-            for (int r = cut.lane; r < rows; r += kGnBatch * cut.lanes) {
-                XLoad<T, E, KEPT> x[kGnBatch];
-                Vals<T, E> d[kGnBatch];
+            sum_given(p, fs, b, [&](int k, int sub, int subs) {
+                const bool in = k < g.G;
+                const float2 *part = p.part + (int64_t)b * p.pieces * g.G + k;
+                const float n = (float)g.S * (float)g.cg;
+                auto count = [&](int i) { return (float)min((int64_t)g.rows, g.S - (int64_t)i * g.rows) * (float)g.cg; };
+                const float ref = in ? __ldcg(part).x : 0.f;
+                float s = 0.f, m2 = 0.f;
+                if (in) {
+#pragma unroll 8
+                    for (int i = sub; i < p.pieces; i += subs) s += count(i) * (__ldcg(part + (int64_t)i * g.G).x - ref);
+                }
+                const float m = ref + sub_sum<8>(s) / n;
+                if (in) {
+#pragma unroll 8
+                    for (int i = sub; i < p.pieces; i += subs) {
+                        const float2 a = __ldcg(part + (int64_t)i * g.G);
+                        const float d = a.x - m;
+                        m2 += fmaf(count(i) * d, d, a.y);
+                    }
+                }
+                m2 = sub_sum<8>(m2);
+                if (in && sub == 0) {
+                    const float r = 1.f / sqrtf(m2 / n + g.eps);
+                    p.stat[(int64_t)b * g.G + k] = make_float2(-m, r);
+                    g.mean[(int64_t)b * g.G + k] = m;
+                    g.rstd[(int64_t)b * g.G + k] = r;
+                }
+            });
+            continue;
+        }
+        wait_joined(p, b);
+        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)b * g.G + k);
+        __syncthreads();
+        T *y = static_cast<T *>(g.out) + first * g.C;
+        for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+            const int cc = t0 + cut.col;
+            if (!cut.in || cc >= CC) continue;
+            float minus_mean[E], f[E], gamma[E], beta[E];
+            groups_v(acc, cc * E, g.cg, g.magic, minus_mean, f);
+            params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
+            params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
+            mul_v(f, gamma, f);
+            constexpr int BATCH = 4;
+            for (int r = cut.lane; r < rows; r += BATCH * cut.lanes) {
+                Vals<T, E> c[BATCH];
 #pragma unroll
-                for (int q = 0; q < kGnBatch; ++q) {
+                for (int q = 0; q < BATCH; ++q)
+                    if (r + q * cut.lanes < rows) c[q].load_last(x + (int64_t)(r + q * cut.lanes) * g.C + cc * E);
+#pragma unroll
+                for (int q = 0; q < BATCH; ++q) {
                     const int rr = r + q * cut.lanes;
                     if (rr < rows) {
-                        x[q].load(p, first + rr, cc * E);
-                        d[q].load(dy + (int64_t)rr * p.C + cc * E);
+                        float v[E], z[E];
+                        c[q].get(v);
+                        gn_value<T, ACT>(v, minus_mean, f, beta, z);
+                        Vals<T, E> o;
+                        o.set(z);
+                        o.store(y + (int64_t)rr * g.C + cc * E);
+                        if constexpr (KEEP)
+                            keep_chunk<T, E>(v, true, g.codes + (first + rr) * g.C + cc * E,
+                                             g.scales + (first + rr) * (g.C / kBlock8) + cc * E / kBlock8);
                     }
                 }
-#pragma unroll
-                for (int q = 0; q < kGnBatch; ++q)
-                    if (r + q * cut.lanes < rows) {
-                        float v[E], g[E], z[E];
-                        x[q].c.get(v);
-                        d[q].get(g);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            v[i] = (v[i] - mean[i]) * rstd[i];
-                            z[i] = fmaf(v[i], gamma[i], beta[i]);
-                        }
-                        act_slope<T, ACT>(z);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            const float u = g[i] * z[i];
-                            a[i] = fmaf(u, v[i], a[i]);
-                            s[i] += u;
-                        }
-                    }
             }
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            sa[threadIdx.x * E + i] = a[i];
-            sb[threadIdx.x * E + i] = s[i];
-        }
-        __syncthreads();
-        const int width = cut.cols * E;
-        for (int c = threadIdx.x; c < width; c += blockDim.x)
-            if (t0 * E + c < p.C) {
-                float ta = sa[c], ts = sb[c];
-                for (int l = 1; l < cut.lanes; ++l) {
-                    ta += sa[l * width + c];
-                    ts += sb[l * width + c];
-                }
-                out[t0 * E + c] = ta;
-                out[p.C + t0 * E + c] = ts;
-            }
-        __syncthreads();
-    }
-}
-
-// A sample's sums over its chunks, in order, and its groups' means: a CTA
-// takes groups [blockIdx.x gpc, ...) of sample b0 + blockIdx.y.
-constexpr int kGnReduceThreads = 256;
-template <typename T>
-__global__ void __launch_bounds__(kGnReduceThreads) gn_bwd_reduce(const GnParams p, int groups_a_cta) {
-    __shared__ float2 red[kGnReduceThreads / 32];
-    pdl_wait();
-    pdl_trigger();
-    const int b = p.b0 + blockIdx.y;
-    const float *part = p.parts + (int64_t)b * p.chunks * 2 * p.C;
-    float *sums = p.sums + (int64_t)b * 2 * p.C;
-    const float n = (float)p.S * (float)p.cg;
-    const int g1 = min((blockIdx.x + 1) * groups_a_cta, (unsigned)p.G);
-    for (int g = blockIdx.x * groups_a_cta; g < g1; ++g) {
-        float2 m = make_float2(0.f, 0.f);
-        for (int c = g * p.cg + threadIdx.x; c < (g + 1) * p.cg; c += blockDim.x) {
-            float a = 0.f, s = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < p.chunks; ++k) {
-                a += part[(int64_t)k * 2 * p.C + c];
-                s += part[(int64_t)k * 2 * p.C + p.C + c];
-            }
-            sums[c] = a;
-            sums[p.C + c] = s;
-            const float gamma = param<T>(p.gamma, p.w32, c, 1.f);
-            m.x = fmaf(s, gamma, m.x);
-            m.y = fmaf(a, gamma, m.y);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float2 t = red[0];
-            for (int i = 1; i < (int)blockDim.x / 32; ++i) t = add2(t, red[i]);
-            p.means[(int64_t)b * p.G + g] = make_float2(t.x / n, t.y / n);
-        }
-        __syncthreads();
     }
 }
 
 template <typename T, int E, int ACT, bool KEPT>
-__global__ void __launch_bounds__(256) gn_bwd_apply(const GnParams p) {
+__global__ void __launch_bounds__(kFlowThreads, 2) gn_bwd_flow(const FlowParams p) {
+    extern __shared__ float sm[];
+    __shared__ FlowShared fs;
+    float *lane_a = sm, *lane_s = sm + kFlowThreads * E;
+    float2 *acc = reinterpret_cast<float2 *>(sm + 2 * kFlowThreads * E);  // [G]
+    const GnParams &g = p.g;
     pdl_wait();
     pdl_trigger();
-    const int b = p.b0 + blockIdx.y;
-    const int64_t r0 = (int64_t)blockIdx.x * p.rows;
-    const int rows = (int)min((int64_t)p.rows, p.S - r0);
-    const int64_t first = (int64_t)b * p.S + r0;
-    const int CC = p.C / E;
+    const int CC = g.C / E;
     const Cut cut(CC);
-    const T *dy = static_cast<const T *>(p.dy) + first * p.C;
-    T *dx = static_cast<T *>(p.out) + first * p.C;
-    for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-        const int cc = t0 + cut.col;
-        if (!cut.in || cc >= CC) continue;
-        float mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
+    const int64_t all = (int64_t)g.B * p.pieces;
+    constexpr int BATCH = 4;
+    for (;;) {
+        const int64_t ticket = next_ticket(p, fs);
+        if (ticket >= p.tickets) return;
+        const bool normalise = ticket & 1;
+        const int64_t item = (ticket >> 1) - (normalise ? p.pieces + p.lag : 0);
+        if (item < 0 || item >= all) continue;
+        const int b = (int)(item / p.pieces), piece = (int)(item - (int64_t)b * p.pieces);
+        const int64_t r0 = (int64_t)piece * g.rows, first = (int64_t)b * g.S + r0;
+        const int rows = (int)min((int64_t)g.rows, g.S - r0);
+        const T *dy = static_cast<const T *>(g.dy) + first * g.C;
+        auto constants = [&](int cc, float (&minus_mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
+            const int64_t at = (int64_t)b * g.G;
+            auto group = [&](int c) { return g.magic ? (int)__umulhi((uint32_t)c, g.magic) : c; };
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = cc * E + i;
-            const int64_t g = (int64_t)b * p.G + c / p.cg;
-            mean[i] = p.mean[g];
-            rstd[i] = p.rstd[g];
-            gamma[i] = param<T>(p.gamma, p.w32, c, 1.f);
-            beta[i] = param<T>(p.beta, p.w32, c, 0.f);
-            const float2 m = p.means[g];
-            m1[i] = m.x;
-            m2[i] = m.y;
-        }
-        for (int r = cut.lane; r < rows; r += kGnBatch * cut.lanes) {
-            XLoad<T, E, KEPT> x[kGnBatch];
-            Vals<T, E> d[kGnBatch];
-#pragma unroll
-            for (int q = 0; q < kGnBatch; ++q) {
-                const int rr = r + q * cut.lanes;
-                if (rr < rows) {
-                    x[q].load(p, first + rr, cc * E);
-                    d[q].load_last(dy + (int64_t)rr * p.C + cc * E);
-                }
+            for (int i = 0; i < E; ++i) {
+                const int k = group(cc * E + i);
+                minus_mean[i] = -g.mean[at + k];
+                rstd[i] = g.rstd[at + k];
             }
+            params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
+            params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
+        };
+        if (!normalise) {
+            float *out = g.parts ? g.parts + item * 2 * g.C : nullptr;
+            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+                const int cc = t0 + cut.col;
+                float a[E], s[E];
+                fill_v(0.f, a);
+                fill_v(0.f, s);
+                if (cut.in && cc < CC) {
+                    float minus_mean[E], rstd[E], gamma[E], beta[E];
+                    constants(cc, minus_mean, rstd, gamma, beta);
+                    for (int r = cut.lane; r < rows; r += BATCH * cut.lanes) {
+                        XLoad<T, E, KEPT> x[BATCH];
+                        Vals<T, E> d[BATCH];
 #pragma unroll
-            for (int q = 0; q < kGnBatch; ++q) {
-                const int rr = r + q * cut.lanes;
-                if (rr < rows) {
-                    float v[E], g[E], z[E];
-                    x[q].c.get(v);
-                    d[q].get(g);
+                        for (int q = 0; q < BATCH; ++q) {
+                            const int rr = r + q * cut.lanes;
+                            if (rr < rows) {
+                                x[q].load(g, first + rr, cc * E);
+                                d[q].load(dy + (int64_t)rr * g.C + cc * E);
+                            }
+                        }
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        v[i] = (v[i] - mean[i]) * rstd[i];
-                        z[i] = fmaf(v[i], gamma[i], beta[i]);
+                        for (int q = 0; q < BATCH; ++q)
+                            if (r + q * cut.lanes < rows) {
+                                float v[E], u[E];
+                                x[q].c.get(v);
+                                d[q].get(u);
+                                gn_slope<T, ACT>(v, u, minus_mean, rstd, gamma, beta);
+                                fma_v(u, v, a, a);
+                                add_v(s, u, s);
+                            }
                     }
-                    act_slope<T, ACT>(z);
+                }
 #pragma unroll
-                    for (int i = 0; i < E; ++i) g[i] = rstd[i] * (fmaf(g[i] * z[i], gamma[i], -m1[i]) - v[i] * m2[i]);
-                    Vals<T, E> o;
-                    o.set(g);
-                    o.store(dx + (int64_t)rr * p.C + cc * E);
+                for (int i = 0; i < E; ++i) {
+                    lane_a[threadIdx.x * E + i] = a[i];
+                    lane_s[threadIdx.x * E + i] = s[i];
+                }
+                __syncthreads();
+                const int width = cut.cols * E, c0 = t0 * E, c1 = min(c0 + width, g.C);
+                for (int c = threadIdx.x; c < c1 - c0; c += kFlowThreads) {
+                    float ta = lane_a[c], ts = lane_s[c];
+#pragma unroll 4
+                    for (int l = 1; l < cut.lanes; ++l) {
+                        ta += lane_a[l * width + c];
+                        ts += lane_s[l * width + c];
+                    }
+                    if (out) {
+                        out[c0 + c] = ta;
+                        out[g.C + c0 + c] = ts;
+                    }
+                    const float ga = param<T>(g.gamma, g.w32, c0 + c, 1.f);
+                    lane_a[c] = ta * ga;
+                    lane_s[c] = ts * ga;
+                }
+                __syncthreads();
+                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+                for (int k = c0 / g.cg + warp; k * g.cg < c1; k += kFlowThreads / 32) {
+                    const int lo = max(k * g.cg, c0), hi = min((k + 1) * g.cg, c1);
+                    float2 m = make_float2(0.f, 0.f);
+                    for (int c = lo + wl; c < hi; c += 32) m = add2(m, make_float2(lane_s[c - c0], lane_a[c - c0]));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
+                    if (wl == 0) {
+                        if (lo > k * g.cg) m = add2(acc[k], m);
+                        if (hi < (k + 1) * g.cg)
+                            acc[k] = m;
+                        else
+                            p.part[item * g.G + k] = m;
+                    }
+                }
+                __syncthreads();
+            }
+            sum_given(p, fs, b, [&](int k, int sub, int subs) {
+                const bool in = k < g.G;
+                const float2 *part = p.part + (int64_t)b * p.pieces * g.G + k;
+                float2 m = make_float2(0.f, 0.f);
+                if (in) {
+#pragma unroll 8
+                    for (int i = sub; i < p.pieces; i += subs) m = add2(m, __ldcg(part + (int64_t)i * g.G));
+                }
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
+                const float n = (float)g.S * (float)g.cg;
+                if (in && sub == 0) p.stat[(int64_t)b * g.G + k] = make_float2(-m.x / n, -m.y / n);
+            });
+            continue;
+        }
+        wait_joined(p, b);
+        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)b * g.G + k);
+        __syncthreads();
+        T *dx = static_cast<T *>(g.out) + first * g.C;
+        for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+            const int cc = t0 + cut.col;
+            if (!cut.in || cc >= CC) continue;
+            float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
+            constants(cc, minus_mean, rstd, gamma, beta);
+            groups_v(acc, cc * E, g.cg, g.magic, m1, m2);
+            constexpr int HALF = 2;
+            for (int r = cut.lane; r < rows; r += HALF * cut.lanes) {
+                XLoad<T, E, KEPT> x[HALF];
+                Vals<T, E> d[HALF];
+#pragma unroll
+                for (int q = 0; q < HALF; ++q) {
+                    const int rr = r + q * cut.lanes;
+                    if (rr < rows) {
+                        x[q].load(g, first + rr, cc * E);
+                        d[q].load_last(dy + (int64_t)rr * g.C + cc * E);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < HALF; ++q) {
+                    const int rr = r + q * cut.lanes;
+                    if (rr < rows) {
+                        float v[E], u[E];
+                        x[q].c.get(v);
+                        d[q].get(u);
+                        gn_slope<T, ACT>(v, u, minus_mean, rstd, gamma, beta);
+                        gn_dx(v, u, rstd, gamma, m1, m2);
+                        Vals<T, E> o;
+                        o.set(u);
+                        o.store(dx + (int64_t)rr * g.C + cc * E);
+                    }
                 }
             }
         }
     }
 }
 
-// ---------------------------------------------------------------- launches --
+// Many rows of sums folded into gridDim.y: row i of the result is the sum of
+// rows [i n / gridDim.y, (i + 1) n / gridDim.y), in order.
+static __global__ void __launch_bounds__(256) gn_fold(const float *in, float *out, int64_t n, int width) {
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    const int64_t i0 = n * blockIdx.y / gridDim.y, i1 = n * (blockIdx.y + 1) / gridDim.y;
+    if (c >= width) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int64_t i = i0; i < i1; ++i) s += in[i * width + c];
+    out[(int64_t)blockIdx.y * width + c] = s;
+}
 
-// Which of the compiled widths a call takes: 16-byte chunks, or one value.
-enum { kGnStats = 0, kGnApply, kGnBwdSums, kGnBwdReduce, kGnBwdApply };
+// ---------------------------------------------------------------- kernels --
 
-template <typename T, int E>
-static const void *gn_kernel_e(int which, int act, bool kept) {
-    switch (which) {
-    case kGnStats: return (const void *)gn_stats<T, E>;
-    case kGnApply:
-        if constexpr (E > 1) {
-            if (kept)
-                return act == kActSilu   ? (const void *)gn_apply<T, E, kActSilu, true>
-                       : act == kActGelu ? (const void *)gn_apply<T, E, kActGelu, true>
-                                         : (const void *)gn_apply<T, E, kActNone, true>;
-        }
-        return act == kActSilu   ? (const void *)gn_apply<T, E, kActSilu, false>
-               : act == kActGelu ? (const void *)gn_apply<T, E, kActGelu, false>
-                                 : (const void *)gn_apply<T, E, kActNone, false>;
-    case kGnBwdSums:
-        if (kept)
-            return act == kActSilu   ? (const void *)gn_bwd_sums<T, E, kActSilu, true>
-                   : act == kActGelu ? (const void *)gn_bwd_sums<T, E, kActGelu, true>
-                                     : (const void *)gn_bwd_sums<T, E, kActNone, true>;
-        return act == kActSilu   ? (const void *)gn_bwd_sums<T, E, kActSilu, false>
-               : act == kActGelu ? (const void *)gn_bwd_sums<T, E, kActGelu, false>
-                                 : (const void *)gn_bwd_sums<T, E, kActNone, false>;
-    case kGnBwdReduce: return (const void *)gn_bwd_reduce<T>;
-    default:
-        if (kept)
-            return act == kActSilu   ? (const void *)gn_bwd_apply<T, E, kActSilu, true>
-                   : act == kActGelu ? (const void *)gn_bwd_apply<T, E, kActGelu, true>
-                                     : (const void *)gn_bwd_apply<T, E, kActNone, true>;
-        return act == kActSilu   ? (const void *)gn_bwd_apply<T, E, kActSilu, false>
-               : act == kActGelu ? (const void *)gn_bwd_apply<T, E, kActGelu, false>
-                                 : (const void *)gn_bwd_apply<T, E, kActNone, false>;
+// (keeping x in the same pass: whole 16-byte chunks only)
+template <typename T, int E, int ACT> static const void *gn_flow_fwd(bool kept) {
+    if constexpr (E > 1) {
+        if (kept) return (const void *)gn_fwd_flow<T, E, ACT, true>;
     }
+    return (const void *)gn_fwd_flow<T, E, ACT, false>;
+}
+template <typename T, int E> static const void *gn_flow_e(bool backward, int act, bool kept) {
+#define FLOW(A)                                                                                              \
+    (!backward ? gn_flow_fwd<T, E, A>(kept)                                                                  \
+     : kept    ? (const void *)gn_bwd_flow<T, E, A, true>                                                    \
+               : (const void *)gn_bwd_flow<T, E, A, false>)
+    return act == kActSilu ? FLOW(kActSilu) : act == kActGelu ? FLOW(kActGelu) : FLOW(kActNone);
+#undef FLOW
+}
+// A kernel by 16-byte chunks (wide) or by single values.
+template <typename T> static const void *gn_flow_t(bool backward, bool wide, int act, bool kept) {
+    return wide ? gn_flow_e<T, Elem<T>::E>(backward, act, kept) : gn_flow_e<T, 1>(backward, act, kept);
 }
 
-template <typename T> static const void *gn_kernel_t(int which, bool wide, int act, bool kept) {
-    return wide ? gn_kernel_e<T, Elem<T>::E>(which, act, kept) : gn_kernel_e<T, 1>(which, act, kept);
-}
-
-const void *gn_kernel_f32(int which, bool wide, int act, bool kept);
-const void *gn_kernel_bf16(int which, bool wide, int act, bool kept);
-const void *gn_kernel_f16(int which, bool wide, int act, bool kept);
+#define GN_DECLARE(suf)                                                          \
+    const void *gn_flow_##suf(bool backward, bool wide, int act, bool kept);     \
+    const void *gn_held_##suf(bool backward, bool wide, int act, bool kept);
+GN_DECLARE(f32)
+GN_DECLARE(bf16)
+GN_DECLARE(f16)
+#undef GN_DECLARE
 
 }  // namespace rmsn
