@@ -67,18 +67,19 @@ static bool bwd_plan(int64_t M, int64_t N, int dt, bool fused, bool wide, int sm
         b.bytes = ((size_t)b.dw_parts * N * 4 + 255) / 256 * 256;
         return true;
     }
-    b.threads = std::max(b.k.tpr, 256);
-    const int teams = b.threads / b.k.tpr, an_sm = b.k.tpr > 256 ? 1 : 2;
+    const int consumers = bwd_consumers(b.k.tpr);
+    b.threads = consumers + 32;
+    const int teams = consumers / b.k.tpr, an_sm = b.k.tpr > 256 ? 1 : 2;
     const size_t room = an_sm == 1 ? kBwdSmemWide : kBwdSmem;
     // whole turns of the teams, more of them where rows are short, fewer where
     // there would not be a stage for every CTA
     int turns = 1;
-    while (turns < 64 && StageLayout(teams * turns, (int)N, es, fused).bytes < kStageTarget &&
-           M >= (int64_t)teams * turns * 2 * an_sm * sms)
+    while (turns < 64 && StageLayout(teams * b.k.r * turns, (int)N, es, fused).bytes < kStageTarget &&
+           M >= (int64_t)teams * b.k.r * turns * 2 * an_sm * sms)
         turns *= 2;
-    b.rows = teams * turns;
+    b.rows = teams * b.k.r * turns;
     const size_t stage = StageLayout(b.rows, (int)N, es, fused).bytes;
-    b.depth = (int)std::min<size_t>(6, room / stage);
+    b.depth = (int)std::min<size_t>(kStagesMost, room / stage);
     if (b.depth < 2) return false;
     b.smem = std::max((size_t)b.depth * stage, teams > 1 ? (size_t)N * 4 : 0);
     const int64_t blocks = (M + b.rows - 1) / b.rows;
@@ -129,7 +130,7 @@ static bool id_type(int bytes) { return bytes == 4 || bytes == 8; }
 struct EmbedPlan {
     int ctas, share, bits, passes, tiles;  // the sort: CTAs of the cluster (0: launches over tiles)
     int pieces, words;
-    size_t keys, vals, keys2, vals2, counts, present, open, parts, bytes;
+    size_t keys, vals, keys2, vals2, counts, present, open, ends, parts, bytes;
 };
 
 static EmbedPlan embed_plan(int64_t T, int64_t rows, int64_t N) {
@@ -163,19 +164,23 @@ static EmbedPlan embed_plan(int64_t T, int64_t rows, int64_t N) {
         p.vals2 = take((size_t)T * 4);
         p.counts = take((size_t)kSortBins * (p.tiles + 1) * 4);
     }
-    p.present = take((size_t)p.words * 4);
-    p.open = take((size_t)(p.pieces + 1) * 4);
+    p.present = take(p.ctas ? 0 : (size_t)p.words * 4);
+    p.open = take((size_t)(p.pieces + 1) * 8);
+    p.ends = take((size_t)rows * 4);
     p.parts = take((size_t)p.pieces * 2 * N * 4);
     p.bytes = at;
     return p;
 }
 
-static int run_sort(const EmbedPlan &b, SortParams &p, char *w, cudaStream_t s) {
+static int run_sort(const EmbedPlan &b, SortParams &p, char *w, int dtype, bool out32, bool wide, int sms, cudaStream_t s) {
     auto at = [w](size_t o) { return reinterpret_cast<uint32_t *>(w + o); };
     if (b.ctas) {
         p.keys = at(b.keys), p.vals = at(b.vals);
+        // the other SMs clear the rows without a token meanwhile (whole clusters of CTAs, one an SM)
+        const int clear = p.dtable ? std::max(1, (sms - b.ctas) / b.ctas) * b.ctas : 0;
         void *args[] = {&p, const_cast<int *>(&b.share)};
-        return launch(sort_kernel(0), (unsigned)b.ctas, 1, kSortThreads, sort_shared() + (size_t)b.share * 16, args, s, (unsigned)b.ctas);
+        return launch(embed_sort_kernel(dtype, out32, wide), (unsigned)(b.ctas + clear), 1, kSortThreads,
+                      sort_shared() + std::max((size_t)b.share * 16, (size_t)kClearWords * 4), args, s, (unsigned)b.ctas);
     }
     cudaError_t e = cudaMemsetAsync(p.present, 0, (size_t)b.words * 4, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(p.open, 0, 4, s);
@@ -219,7 +224,7 @@ extern "C" rmsnorm_status_t ckpt8_pack(const void *x, void *codes, uint8_t *scal
         e = launch(other_kernel(kPackBlocks, dt), (unsigned)ctas, 1, 256, 0, args, s);
     } else {
         int n = (int)N;
-        const int64_t blocks = M * ((N + kBlock8 - 1) / kBlock8), ctas = (blocks + 8 * kPackChunks - 1) / (8 * kPackChunks);
+        const int64_t runs = ((N + kBlock8 - 1) / kBlock8 + kRun - 1) / kRun, ctas = (M * runs + 7) / 8;
         if (ctas > 0x7fffffffLL) return RMSNORM_ERR_INVALID_ARG;
         void *args[] = {&x, &codes, &scales, &M, &n};
         e = launch(other_kernel(kPackAny, dt), (unsigned)ctas, 1, 256, 0, args, s);
@@ -243,7 +248,7 @@ extern "C" rmsnorm_status_t ckpt8_unpack(const void *codes, const uint8_t *scale
         e = launch(other_kernel(kUnpackBlocks, dt), (unsigned)ctas, 1, 256, 0, args, s);
     } else {
         int n = (int)N;
-        const int64_t blocks = M * ((N + kBlock8 - 1) / kBlock8), ctas = (blocks + 8 * kPackChunks - 1) / (8 * kPackChunks);
+        const int64_t runs = ((N + kBlock8 - 1) / kBlock8 + kRun - 1) / kRun, ctas = (M * runs + 7) / 8;
         if (ctas > 0x7fffffffLL) return RMSNORM_ERR_INVALID_ARG;
         void *args[] = {&codes, &scales, &x, &M, &n};
         e = launch(other_kernel(kUnpackAny, dt), (unsigned)ctas, 1, 256, 0, args, s);
@@ -355,7 +360,8 @@ extern "C" rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dta
     p.slices = (C + p.team - 1) / p.team;
     const int teams = 256 / p.team;
     const int64_t sums = ((int64_t)b.pieces * p.slices + teams - 1) / teams;
-    const int64_t clears = accumulate ? 0 : (int64_t)b.words * p.slices;
+    // rows without a token: cleared beside the sort where one cluster sorts, else by these CTAs
+    const int64_t clears = accumulate || b.ctas ? 0 : (int64_t)b.words * p.slices;
     if (sums + clears > 0x7fffffffLL) return RMSNORM_ERR_INVALID_ARG;
     p.sum_ctas = (int)sums;
     return with_workspace(workspace, workspace_bytes, b.bytes, s, [&](char *w) {
@@ -363,16 +369,17 @@ extern "C" rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dta
         std::memset(&q, 0, sizeof q);
         q.ids = ids, q.id_bytes = id_bytes, q.rows = rows, q.T = (int)T, q.bits = b.bits, q.passes = b.passes, q.tiles = b.tiles;
         q.words = b.words;
+        q.dtable = accumulate ? nullptr : dtable, q.N = (int)N;
         q.present = reinterpret_cast<uint32_t *>(w + b.present);
         q.open = reinterpret_cast<uint32_t *>(w + b.open);
-        int le = run_sort(b, q, w, s);
+        int le = run_sort(b, q, w, base_of(dt), out32, wide, sms, s);
         p.keys = reinterpret_cast<uint32_t *>(w + b.keys);
         p.vals = reinterpret_cast<uint32_t *>(w + b.vals);
-        p.present = q.present, p.open = q.open, p.parts = reinterpret_cast<float *>(w + b.parts);
+        p.present = q.present, p.open = q.open, p.ends = reinterpret_cast<uint32_t *>(w + b.ends), p.parts = reinterpret_cast<float *>(w + b.parts);
         void *args[] = {&p};
         if (le == 0) le = launch(embed_sum_kernel(base_of(dt), out32, wide), (unsigned)(sums + clears), 1, 256, 0, args, s);
         if (le == 0 && b.pieces > 1)
-            le = launch(embed_join_kernel(base_of(dt), out32, wide), (unsigned)std::min<int64_t>(4 * sms, (int64_t)b.pieces * ((C + 31) / 32)), 1, 256, 0, args, s);
+            le = launch(embed_join_kernel(base_of(dt), out32, wide), (unsigned)std::min<int64_t>(4 * sms, (int64_t)b.pieces * ((C + kJoinChunks - 1) / kJoinChunks)), 1, 256, 0, args, s);
         return le == 0 ? RMSNORM_SUCCESS : head_cuda_fail(le);
     });
 }

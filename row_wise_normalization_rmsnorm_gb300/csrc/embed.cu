@@ -101,6 +101,11 @@ __device__ __forceinline__ uint32_t cluster_address(const void *local, uint32_t 
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(cta));
     return r;
 }
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ uint32_t ld_remote(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -110,21 +115,59 @@ __device__ __forceinline__ void st_remote2(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
+// E values of a row of the table, as up to 16 bytes an access.
+template <typename TO, int E> __device__ __forceinline__ void clear_row(void *dtable, int64_t row, int N, int c) {
+    constexpr int S = E * (int)sizeof(TO) > 16 ? 16 / (int)sizeof(TO) : E;
+    float zero[S];
+    fill_v(0.f, zero);
+    Vals<TO, S> o;
+    o.set(zero);
+#pragma unroll
+    for (int k = 0; k < E; k += S) o.store(static_cast<TO *>(dtable) + row * N + (int64_t)c * E + k);
+}
+
+// The rows without a token, by the CTAs beside the sorting cluster: each
+// marks the ids of its share of the rows in shared memory, then clears the
+// others. (The sort keeps 8 SMs for 15 us, and memory would be idle.)
+template <typename TO, int E> __device__ __forceinline__ void clear_rows(const SortParams &p, uint32_t *marks, int cta, int ctas) {
+    const int64_t v0 = p.rows * cta / ctas, v1 = p.rows * (cta + 1) / ctas;
+    const int C = p.N / E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t lo = v0; lo < v1; lo += (int64_t)kClearWords * 32) {
+        const int n = (int)min((int64_t)kClearWords * 32, v1 - lo);
+        for (int i = threadIdx.x; i < (n + 31) / 32; i += kSortThreads) marks[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int t = threadIdx.x; t < p.T; t += kSortThreads) {
+            const int64_t k = (int64_t)key_of(p, t) - lo;
+            // (a look first: the same few ids come over and over)
+            if (k >= 0 && k < n && !(*(volatile uint32_t *)&marks[k >> 5] >> (k & 31) & 1u)) atomicOr(&marks[k >> 5], 1u << (k & 31));
+        }
+        __syncthreads();
+        for (int r = warp; r < n; r += kSortThreads / 32)
+            if (!(marks[r >> 5] >> (r & 31) & 1u))
+                for (int c = lane; c < C; c += 32) clear_row<TO, E>(p.dtable, lo + r, p.N, c);
+        __syncthreads();
+    }
+}
+
 // Up to kSortCluster kSortTile tokens: one cluster, (id, token) pairs in its
 // shared memory between the passes, each CTA an equal share of the places.
 // smem: SortShared, then two buffers of `share` pairs.
 constexpr int kSortPer = kSortTile / kSortThreads;
-__global__ void __launch_bounds__(kSortThreads) embed_sort(const SortParams p, int share) {
+template <typename TO, int E> __global__ void __launch_bounds__(kSortThreads) embed_sort(const SortParams p, int share) {
     extern __shared__ __align__(16) uint8_t raw[];
     SortShared &s = *reinterpret_cast<SortShared *>(raw);
     uint2 *buf[2] = {reinterpret_cast<uint2 *>(raw + sizeof(SortShared)), reinterpret_cast<uint2 *>(raw + sizeof(SortShared)) + share};
     pdl_wait();
     pdl_trigger();
-    const int rank = (int)cluster_ctarank(), ctas = (int)gridDim.x;
+    const int ctas = (int)cluster_ctas(), rank = (int)cluster_ctarank();
+    if ((int)blockIdx.x >= ctas) {
+        clear_rows<TO, E>(p, reinterpret_cast<uint32_t *>(raw + sizeof(SortShared)), (int)blockIdx.x - ctas, (int)gridDim.x - ctas);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = max(0, min(share, p.T - rank * share));
     const int per = (share + kSortThreads - 1) / kSortThreads;
-    for (int i = rank * kSortThreads + threadIdx.x; i < p.words; i += ctas * kSortThreads) p.present[i] = 0;
     if (rank == 0 && threadIdx.x == 0) p.open[0] = 0;
     uint32_t key[kSortPer], val[kSortPer], place[kSortPer];
 #pragma unroll
@@ -147,7 +190,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort(const SortParams p, i
         }
         const int shift = pass * p.bits;
         rank_tokens<kSortPer>(s, n, per, shift, p.bits, [&](int r) { return key[r]; }, place);
-        cluster_sync();  // the CTAs' totals (and, before the first pass, the cleared bits) are there
+        cluster_sync();  // the CTAs' totals are there
         uint32_t all = 0, before = 0;
         if ((int)threadIdx.x < (1 << p.bits))
             for (int c = 0; c < ctas; ++c) {
@@ -172,7 +215,6 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort(const SortParams p, i
                     const uint32_t cta = to / (uint32_t)share;
                     st_remote2(cluster_address(&buf[(pass + 1) & 1][to - cta * share], cta), key[r], val[r]);
                 }
-                if (pass == 0 && key[r] < (uint32_t)p.rows) atomicOr(&p.present[key[r] >> 5], 1u << (key[r] & 31u));
             }
         }
         cluster_sync();  // pairs have arrived, and nobody reads these totals any more
@@ -294,14 +336,11 @@ __global__ void __launch_bounds__(256) embed_sum(const EmbedSumParams p) {
         const int64_t item = (int64_t)blockIdx.x - p.sum_ctas;
         const int64_t r0 = item / p.slices * 32;
         const uint32_t there = p.present[r0 >> 5];
-        float zero[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) zero[i] = 0.f;
         const int teams = 256 / p.team;
         const int c = (int)(item % p.slices) * p.team + (int)threadIdx.x % p.team;
         if (c < C)
             for (int r = threadIdx.x / p.team; r < 32 && r0 + r < p.rows; r += teams)
-                if (!(there >> r & 1u)) give_row<TO, E>(p, (uint32_t)(r0 + r), c, zero);
+                if (!(there >> r & 1u)) clear_row<TO, E>(p.dtable, r0 + r, p.N, c);
         return;
     }
     const int team = threadIdx.x / p.team, t = threadIdx.x % p.team, teams = 256 / p.team;
@@ -344,7 +383,11 @@ __global__ void __launch_bounds__(256) embed_sum(const EmbedSumParams p) {
                         float *to = part_at<E>(p, piece, whole ? 1 : 0, c);
 #pragma unroll
                         for (int i = 0; i < E; ++i) to[i] = sum[i];
-                        if (whole && c == 0) p.open[1 + atomicAdd(p.open, 1u)] = (uint32_t)piece;  // in any order
+                        if (c == 0 && ends) p.ends[id] = (uint32_t)piece;
+                        if (c == 0 && whole) {  // in any order
+                            const uint32_t i = atomicAdd(p.open, 1u);
+                            *reinterpret_cast<uint2 *>(p.open + 2 + 2 * i) = make_uint2((uint32_t)piece, id);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < E; ++i) sum[i] = 0.f;
@@ -356,35 +399,24 @@ __global__ void __launch_bounds__(256) embed_sum(const EmbedSumParams p) {
 }
 
 // Runs over several pieces: the last part of the piece where the run begins,
-// then the first parts of those behind it, in order. 8 lanes of pieces and 32
-// chunks a CTA; the lanes' sums are added in order.
+// then the first parts of those behind it, in order. 8 lanes of pieces and
+// kJoinChunks chunks a CTA; the lanes' sums are added in order.
 template <typename T, typename TO, int E>
 __global__ void __launch_bounds__(256) embed_join(const EmbedSumParams p) {
-    __shared__ float lane_sum[8][32][E];
+    __shared__ float lane_sum[8][kJoinChunks][E + 1];
     pdl_wait();
     pdl_trigger();
-    const int C = p.N / E, slices = (C + 31) / 32;
+    const int C = p.N / E, slices = (C + kJoinChunks - 1) / kJoinChunks;
     const int64_t items = (int64_t)p.open[0] * slices;
-    const int lane = threadIdx.x >> 5, t = threadIdx.x & 31;
+    const int lane = threadIdx.x / kJoinChunks, t = threadIdx.x % kJoinChunks;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int first = (int)p.open[1 + item / slices];
-        const int c = (int)(item % slices) * 32 + t;
-        // the run's id, and the end of the run: every warp looks for the first place with another id
-        const uint32_t id = p.keys[min((first + 1) * kEmbedPiece, p.T) - 1];
-        int64_t lo = (int64_t)(first + 1) * kEmbedPiece, hi = p.T;  // place lo has the id, place hi (if there) has not
-        while (hi - lo > 1) {
-            const int64_t gap = (hi - lo + 31) / 32, x = lo + gap * t;
-            const uint32_t same = __ballot_sync(0xffffffffu, x < hi && p.keys[min(x, (int64_t)p.T - 1)] == id);
-            const int k = 31 - __clz((int)same);  // lane 0 has it: place lo has the id
-            lo = lo + gap * k;
-            hi = min(hi, lo + gap);
-        }
-        const int last = (int)(lo / kEmbedPiece);  // the last piece with a part of the run
+        const uint2 run = *reinterpret_cast<const uint2 *>(p.open + 2 + 2 * (item / slices));
+        const int first = (int)run.x, last = (int)p.ends[run.y];
+        const int c = (int)(item % slices) * kJoinChunks + t;
+        const int per = (last - first + 1 + 7) / 8, lanes = (last - first + per) / per;  // lanes with pieces
         float sum[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) sum[i] = 0.f;
-        if (c < C) {
-            const int per = (last - first + 1 + 7) / 8;
+        fill_v(0.f, sum);
+        if (c < C && lane < lanes) {
             const int k0 = first + lane * per, k1 = min(k0 + per, last + 1);
 #pragma unroll 4
             for (int k = k0; k < k1; ++k) {
@@ -397,33 +429,37 @@ __global__ void __launch_bounds__(256) embed_join(const EmbedSumParams p) {
         for (int i = 0; i < E; ++i) lane_sum[lane][t][i] = sum[i];
         __syncthreads();
         if (lane == 0 && c < C) {
-            for (int l = 1; l < 8; ++l)
+            for (int l = 1; l < lanes; ++l)
 #pragma unroll
                 for (int i = 0; i < E; ++i) sum[i] += lane_sum[l][t][i];
-            give_row<TO, E>(p, id, c, sum);
+            give_row<TO, E>(p, run.y, c, sum);
         }
         __syncthreads();
     }
 }
 
 const void *sort_kernel(int which) {
-    return which == 0   ? (const void *)embed_sort
-           : which == 1 ? (const void *)embed_sort_count
+    return which == 1   ? (const void *)embed_sort_count
            : which == 2 ? (const void *)embed_sort_scan
                         : (const void *)embed_sort_move;
 }
 size_t sort_shared() { return sizeof(SortShared); }
 
-template <bool JOIN> static const void *embed_pick(int dtype, bool out32, bool wide) {
-#define PICK(T, TO) \
-    (wide ? (JOIN ? (const void *)embed_join<T, TO, Elem<T>::E> : (const void *)embed_sum<T, TO, Elem<T>::E>) \
-          : (JOIN ? (const void *)embed_join<T, TO, 1> : (const void *)embed_sum<T, TO, 1>))
+enum { kPickSort, kPickSum, kPickJoin };
+template <typename T, typename TO, int E> static const void *embed_kernel(int which) {
+    return which == kPickSort  ? (const void *)embed_sort<TO, E>
+           : which == kPickSum ? (const void *)embed_sum<T, TO, E>
+                               : (const void *)embed_join<T, TO, E>;
+}
+static const void *embed_pick(int which, int dtype, bool out32, bool wide) {
+#define PICK(T, TO) (wide ? embed_kernel<T, TO, Elem<T>::E>(which) : embed_kernel<T, TO, 1>(which))
     if (dtype == 0) return PICK(float, float);
     if (dtype == 1) return out32 ? PICK(__nv_bfloat16, float) : PICK(__nv_bfloat16, __nv_bfloat16);
     return out32 ? PICK(__half, float) : PICK(__half, __half);
 #undef PICK
 }
-const void *embed_sum_kernel(int dtype, bool out32, bool wide) { return embed_pick<false>(dtype, out32, wide); }
-const void *embed_join_kernel(int dtype, bool out32, bool wide) { return embed_pick<true>(dtype, out32, wide); }
+const void *embed_sort_kernel(int dtype, bool out32, bool wide) { return embed_pick(kPickSort, dtype, out32, wide); }
+const void *embed_sum_kernel(int dtype, bool out32, bool wide) { return embed_pick(kPickSum, dtype, out32, wide); }
+const void *embed_join_kernel(int dtype, bool out32, bool wide) { return embed_pick(kPickJoin, dtype, out32, wide); }
 
 }  // namespace rmsn

@@ -18,17 +18,19 @@ struct SortParams {
     const void *ids;
     uint32_t *keys_in, *vals_in, *keys, *vals;  // a pass over several launches: from, to (keys_in NULL: from ids)
     uint32_t *counts;   // [kSortBins, tiles] and the bins' totals behind them
-    uint32_t *present;  // one bit a row of the table: some token is its
-    uint32_t *open;     // [0]: how many pieces end inside a row (set to 0 here)
+    uint32_t *present;  // (several launches) one bit a row of the table: some token is its
+    uint32_t *open;     // [0]: how many pieces end inside a run (set to 0 here)
+    void *dtable;       // (one cluster) whose rows without a token are set to zero; NULL: they stay
     int64_t rows;       // of the table; the key of ids outside it
-    int T, id_bytes, shift, bits, passes, tiles, words;
+    int T, N, id_bytes, shift, bits, passes, tiles, words;
 };
 
 struct EmbedSumParams {
     const void *dh;
     void *dtable;
     const uint32_t *keys, *vals, *present;
-    uint32_t *open;     // [0]: count, then the pieces
+    uint32_t *open;     // [0]: count; then pairs from [2]: a piece that ends inside a run, the run's row
+    uint32_t *ends;     // [rows]: the piece where a row's run ends, for runs over several
     float *parts;       // [pieces, 2, N]: the sums of a piece's first row and of its last one, where they are not whole
     int64_t rows;
     int T, N, pieces, team, accumulate;
@@ -36,7 +38,11 @@ struct EmbedSumParams {
     float scale;
 };
 
-const void *sort_kernel(int which);  // 0: a cluster's; 1, 2, 3: a pass's count, scan, move
+constexpr int kClearWords = 8192;    // bits of rows that a clearing CTA holds at once, in words
+constexpr int kJoinChunks = 32;      // of a row, that a CTA joins
+
+const void *embed_sort_kernel(int dtype, bool out32, bool wide);  // a cluster's
+const void *sort_kernel(int which);  // 1, 2, 3: a pass's count, scan, move
 size_t sort_shared();                // bytes of shared memory, without the pairs
 const void *embed_sum_kernel(int dtype, bool out32, bool wide);
 const void *embed_join_kernel(int dtype, bool out32, bool wide);

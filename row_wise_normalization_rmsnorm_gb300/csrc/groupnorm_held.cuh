@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
             if constexpr (KEEP) {
                 const int64_t row = at.first + r;
                 const int c = at.c0 + cc * E;
-                keep_chunk<T, E>(v, true, g.codes + row * g.C + c, g.scales + row * (g.C / kBlock8) + c / kBlock8);
+                keep_chunk<T>(lds128(rows + (size_t)r * pitch + cc * 16), true, block_lanes<T>(), g.codes + row * g.C + c, g.scales + row * (g.C / kBlock8) + c / kBlock8);
             }
         }
     }

@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kFlowThreads, 2) gn_fwd_flow(const FlowParams 
                         o.set(z);
                         o.store(y + (int64_t)rr * g.C + cc * E);
                         if constexpr (KEEP)
-                            keep_chunk<T, E>(v, true, g.codes + (first + rr) * g.C + cc * E,
+                            keep_chunk<T>(c[q].w, true, block_lanes<T>(), g.codes + (first + rr) * g.C + cc * E,
                                              g.scales + (first + rr) * (g.C / kBlock8) + cc * E / kBlock8);
                     }
                 }

@@ -41,14 +41,23 @@ __device__ __forceinline__ float to_codes8(uint32_t b) {
 __device__ __forceinline__ float from_codes8(uint32_t b) {
     return b == kScaleNone ? __uint_as_float(0x7fc00000u) : b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
 }
-// The code of v f: adding 1.5 2^23 rounds to a whole number, ties to even,
-// in the low bits (|v f| <= 128).
-__device__ __forceinline__ int code8(float v, float f) {
-    const float s = fminf(fmaxf(__fmul_rn(v, f), -127.f), 127.f);
-    return (int)(__float_as_uint(__fadd_rn(s, 12582912.f)) & 0xffu);
+// The code of v f, in the low byte: adding 1.5 2^23 rounds to a whole number,
+// ties to even (one fma: the product is exact). |v f| < 127.5 but for a block
+// at the largest scale, whose values are held to 127 steps first.
+__device__ __forceinline__ float held8(float v, float f) { return fminf(fmaxf(v, -127.f / f), 127.f / f); }
+__device__ __forceinline__ uint32_t code8(float v, float f) { return __float_as_uint(__fmaf_rn(v, f, 12582912.f)); }
+template <typename T> __device__ __forceinline__ uint8_t code8_of(float v, uint32_t b) {
+    const float f = to_codes8(b);
+    return (uint8_t)code8(b == MostScale<T>::b ? held8(v, f) : v, f);
 }
-__device__ __forceinline__ uint32_t codes8x4(float a, float b, float c, float d, float f) {
-    return (uint32_t)code8(a, f) | (uint32_t)code8(b, f) << 8 | (uint32_t)code8(c, f) << 16 | (uint32_t)code8(d, f) << 24;
+// Four codes, lowest byte first.
+__device__ __forceinline__ uint32_t codes8x4(float2 a, float2 b, float f) {
+    const float2 ff = make_float2(f, f), magic = make_float2(12582912.f, 12582912.f);
+    a = Pair<true>::fma(a, ff, magic);
+    b = Pair<true>::fma(b, ff, magic);
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
 }
 // Four codes as fp32: code + 128 as the low byte of 2^23, less 2^23 + 128.
 __device__ __forceinline__ void decode8x4(uint32_t codes, float (&v)[4]) {
@@ -60,26 +69,61 @@ __device__ __forceinline__ float decode8(int8_t c) { return (float)c; }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// The codes of a chunk of E values and its block's scale. 32 / E neighbouring
-// lanes hold a block and call this together; one whose chunk lies behind the
-// row's end (`here` false, its values 0) writes nothing.
-template <typename T, int E>
-__device__ __forceinline__ void keep_chunk(const float (&v)[E], bool here, uint8_t *codes, uint8_t *scale) {
-    constexpr int L = kBlock8 / E;
-    uint32_t top = 0;
+// The bits of a 16-byte chunk's largest magnitude, combined over the 32 / E
+// neighbouring lanes that hold its block. 16-bit types are compared as pairs
+// of 16-bit numbers (magnitudes are in the order of their bits).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T> __device__ __forceinline__ uint32_t block_top(const uint4 &c, uint32_t lanes) {
+    constexpr int L = kBlock8 / Elem<T>::E;
+    if constexpr (sizeof(T) == 2) {
+        constexpr uint32_t mag = 0x7fff7fffu;
+        uint32_t m = max_u16x2(max_u16x2(c.x & mag, c.y & mag), max_u16x2(c.z & mag, c.w & mag));
 #pragma unroll
-    for (int i = 0; i < E; ++i) top = max(top, abs_bits(v[i]));
-    const uint32_t lane = threadIdx.x & 31u, mates = ((1u << L) - 1u) << (lane & ~(uint32_t)(L - 1));
+        for (int o = 1; o < L; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(lanes, m, o));
+        m = max(m & 0xffffu, m >> 16);
+        if constexpr (std::is_same<T, __half>::value)
+            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+        else
+            return m << 16;
+    } else {
+        constexpr uint32_t mag = 0x7fffffffu;
+        uint32_t m = max(max(c.x & mag, c.y & mag), max(c.z & mag, c.w & mag));
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
-    const uint32_t b = scale8<T>(top);
-    const float f = to_codes8(b);
+        for (int o = 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(lanes, m, o));
+        return m;
+    }
+}
+// The lanes of this one's block.
+template <typename T> __device__ __forceinline__ uint32_t block_lanes() {
+    constexpr int L = kBlock8 / Elem<T>::E;
+    return ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
+}
+
+// The codes of a 16-byte chunk and its block's scale. The lanes of a block
+// call this together; one whose chunk lies behind the row's end (`here`
+// false, the chunk zeros) writes nothing. `lanes`: those of the block, or all
+// 32 where the whole warp is here.
+template <typename T>
+__device__ __forceinline__ void keep_chunk(const uint4 &raw, bool here, uint32_t lanes, uint8_t *codes, uint8_t *scale) {
+    constexpr int NP = Elem<T>::NP, L = kBlock8 / Elem<T>::E;
+    const uint32_t b = scale8<T>(block_top<T>(raw, lanes));
     if (!here) return;
-    if constexpr (E == 8)
-        *reinterpret_cast<uint2 *>(codes) = make_uint2(codes8x4(v[0], v[1], v[2], v[3], f), codes8x4(v[4], v[5], v[6], v[7], f));
+    const float f = to_codes8(b);
+    float2 v[NP];
+    unpack<T>(raw, v);
+    if (b == MostScale<T>::b) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) v[q] = make_float2(held8(v[q].x, f), held8(v[q].y, f));
+    }
+    if constexpr (NP == 4)
+        *reinterpret_cast<uint2 *>(codes) = make_uint2(codes8x4(v[0], v[1], f), codes8x4(v[2], v[3], f));
     else
-        *reinterpret_cast<uint32_t *>(codes) = codes8x4(v[0], v[1], v[2], v[3], f);
-    if ((lane & (L - 1)) == 0) *scale = (uint8_t)b;
+        *reinterpret_cast<uint32_t *>(codes) = codes8x4(v[0], v[1], f);
+    if ((threadIdx.x & (L - 1)) == 0) *scale = (uint8_t)b;
 }
 
 }  // namespace rmsn

@@ -118,19 +118,15 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) rows_fwd(const RowsPara
     }
     const float rstd = rstd_of(team_allreduce<TPR>(ss.x + ss.y, red[team], t), p.N, p.eps);
     if (ok && t == 0) p.rstd[row] = rstd;
+    const int64_t blocks = (p.N + kBlock8 - 1) / kBlock8;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = v * TPR + t;
         const bool in = ok && c < C;
         float2 a[NP];
         unpack<T>(h[v], a);
-        if constexpr (KEEP) {
-            float f[E];
-#pragma unroll
-            for (int q = 0; q < NP; ++q) f[2 * q] = a[q].x, f[2 * q + 1] = a[q].y;
-            const int64_t blocks = (p.N + kBlock8 - 1) / kBlock8;
-            keep_chunk<T, E>(f, in, p.codes + row * p.N + (int64_t)c * E, p.scales + row * blocks + c * E / kBlock8);
-        }
+        if constexpr (KEEP)
+            keep_chunk<T>(h[v], in, 0xffffffffu, p.codes + row * p.N + c * E, p.scales + row * blocks + c * E / kBlock8);
         if (in) {
             float2 f[NP];
             weights_at<T>(p.w, p.w32, c, p.offset, f);
@@ -181,7 +177,7 @@ __global__ void __launch_bounds__(256) rows_fwd_any(const RowsParams p) {
         const float v = !in ? 0.f : SRC == kSrcPlain ? load_elem(src, j) : load_elem(h, j);
         if constexpr (KEEP) {
             const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v)));
-            if (in) p.codes[row * p.N + j] = (uint8_t)code8(v, to_codes8(b));
+            if (in) p.codes[row * p.N + j] = code8_of<T>(v, b);
             if ((threadIdx.x & 31) == 0) p.scales[row * blocks + j0 / kBlock8] = (uint8_t)b;
         }
         if (in) {
@@ -222,7 +218,7 @@ __global__ void __launch_bounds__(256) embed_rows(const RowsParams p, int tiles)
 constexpr int kPackChunks = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) pack_blocks(const uint4 *x, uint8_t *codes, uint8_t *scales, int64_t chunks) {
-    constexpr int E = Elem<T>::E, NP = Elem<T>::NP;
+    constexpr int E = Elem<T>::E;
     pdl_wait();
     pdl_trigger();
     const int64_t c0 = (int64_t)blockIdx.x * 256 * kPackChunks + threadIdx.x;
@@ -232,12 +228,7 @@ __global__ void __launch_bounds__(256) pack_blocks(const uint4 *x, uint8_t *code
 #pragma unroll
     for (int k = 0; k < kPackChunks; ++k) {
         const int64_t c = c0 + 256 * k;
-        float2 a[NP];
-        float f[E];
-        unpack<T>(r[k], a);
-#pragma unroll
-        for (int q = 0; q < NP; ++q) f[2 * q] = a[q].x, f[2 * q + 1] = a[q].y;
-        keep_chunk<T, E>(f, c < chunks, codes + c * E, scales + c * E / kBlock8);
+        keep_chunk<T>(r[k], c < chunks, 0xffffffffu, codes + c * E, scales + c * E / kBlock8);
     }
 }
 
@@ -281,31 +272,40 @@ __global__ void __launch_bounds__(256) unpack_blocks(const uint8_t *codes, const
         }
 }
 
-// Rows of any length and alignment: a warp a block at a time, lane by lane.
+// Rows of any length and alignment: a warp takes a run of kRun neighbouring
+// blocks of a row, a value a lane.
+constexpr int kRun = 8;
+struct Run {
+    int64_t row;
+    int block, n;  // first block, blocks
+    __device__ __forceinline__ Run(int64_t M, int blocks) {
+        const int runs = (blocks + kRun - 1) / kRun;
+        const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+        row = item / runs;
+        block = (int)(item - row * runs) * kRun;
+        n = row < M ? min(kRun, blocks - block) : 0;
+    }
+};
 template <typename T>
 __global__ void __launch_bounds__(256) pack_any(const T *x, uint8_t *codes, uint8_t *scales, int64_t M, int N) {
     pdl_wait();
     pdl_trigger();
     const int blocks = (N + kBlock8 - 1) / kBlock8, lane = threadIdx.x & 31;
-    const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kPackChunks;
-    const int64_t all = M * blocks;
-    float v[kPackChunks];
+    const Run run(M, blocks);
+    const int j0 = run.block * kBlock8 + lane;
+    const T *src = x + run.row * N + j0;
+    uint8_t *dst = codes + run.row * N + j0;
+    float v[kRun];
+    uint32_t mine = 0;
 #pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) {
-        const int64_t i = first + k, row = i / blocks;
-        const int j = (int)(i - row * blocks) * kBlock8 + lane;
-        v[k] = i < all && j < N ? load_elem(x, row * N + j) : 0.f;
-    }
+    for (int k = 0; k < kRun; ++k) v[k] = k < run.n && j0 + k * kBlock8 < N ? load_elem(src, k * kBlock8) : 0.f;
 #pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) {
-        const int64_t i = first + k, row = i / blocks;
-        const int j = (int)(i - row * blocks) * kBlock8 + lane;
+    for (int k = 0; k < kRun; ++k) {
         const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v[k])));
-        if (i < all) {
-            if (j < N) codes[row * N + j] = (uint8_t)code8(v[k], to_codes8(b));
-            if (lane == 0) scales[i] = (uint8_t)b;
-        }
+        if (k < run.n && j0 + k * kBlock8 < N) dst[k * kBlock8] = code8_of<T>(v[k], b);
+        if (lane == k) mine = b;
     }
+    if (lane < run.n) scales[run.row * blocks + run.block + lane] = (uint8_t)mine;
 }
 
 template <typename T>
@@ -313,74 +313,116 @@ __global__ void __launch_bounds__(256) unpack_any(const uint8_t *codes, const ui
     pdl_wait();
     pdl_trigger();
     const int blocks = (N + kBlock8 - 1) / kBlock8, lane = threadIdx.x & 31;
-    const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kPackChunks;
-    const int64_t all = M * blocks;
+    const Run run(M, blocks);
+    const int j0 = run.block * kBlock8 + lane;
+    const uint8_t *src = codes + run.row * N + j0;
+    T *dst = x + run.row * N + j0;
+    int8_t c[kRun];
 #pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) {
-        const int64_t i = first + k, row = i / blocks;
-        const int j = (int)(i - row * blocks) * kBlock8 + lane;
-        if (i < all && j < N) store_elem(x, row * N + j, decode8((int8_t)codes[row * N + j]) * from_codes8(scales[i]));
+    for (int k = 0; k < kRun; ++k) c[k] = k < run.n && j0 + k * kBlock8 < N ? (int8_t)src[k * kBlock8] : (int8_t)0;
+    const float f = lane < run.n ? from_codes8(scales[run.row * blocks + run.block + lane]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        if (k < run.n && j0 + k * kBlock8 < N) store_elem(dst, k * kBlock8, decode8(c[k]) * fk);
     }
 }
 
+__device__ __forceinline__ uint2 lds64(const void *p) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_u32(p)));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(const void *p) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)));
+    return v;
+}
+
 // ---------------------------------------------------------------- backward --
-// Persistent: CTA i takes blocks of `stage_rows` rows i, i + grid, ..., which
-// bulk copies bring into shared memory `depth` blocks ahead; a team of TPR
-// threads takes a row, holds its chunks in registers between the sum and dx,
-// and keeps dw's sums of its columns until the end. Codes, scales and rstd of
-// a block start anywhere: the 16-byte blocks that hold them are copied.
+// Persistent: CTA i takes blocks of `stage_rows` rows i, i + grid, ... A warp
+// of its own keeps `depth` blocks under way into shared memory (bulk copies;
+// codes and scales of a block start anywhere: the 16-byte blocks that hold
+// them are copied). A team of TPR threads takes R rows at once, so that one
+// barrier and one round of shuffles serve them all, reads them a second time
+// from shared memory for dx, and keeps dw's sums of its columns in registers
+// until the end.
 __host__ __device__ constexpr uint32_t up16(uint32_t n) { return (n + 15u) & ~15u; }
 
 struct StageLayout {  // byte offsets in a stage
-    uint32_t dres, codes, scales, rstd, bytes;
+    uint32_t dres, codes, scales, bytes;
     __host__ __device__ StageLayout(int rows, int N, int es, bool fused) {
         const uint32_t row = (uint32_t)rows * N, blocks = (uint32_t)rows * ((N + kBlock8 - 1) / kBlock8);
         dres = row * es;
         codes = dres + (fused ? row * es : 0u);
         scales = codes + up16(row + 15u);
-        rstd = scales + up16(blocks + 15u);
-        bytes = rstd + up16(rows * 4u + 15u);
+        bytes = scales + up16(blocks + 15u);
     }
 };
 
 constexpr uint32_t kStageWaitLimit = 1u << 20;  // polls of a stage's copies (each may suspend the thread for a while)
+constexpr int kStagesMost = 8;
 
-template <typename T, int TPR, int V, bool FUSED>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2) rows_bwd(const RowsBwdParams p) {
-    constexpr int E = Elem<T>::E, NP = Elem<T>::NP, TEAMS = TPR >= 256 ? 1 : 256 / TPR, W = TPR > 32 ? TPR / 32 : 1;
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Barrier over the first N threads of the CTA.
+template <int N> __device__ __forceinline__ void sync_first() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+
+__host__ __device__ constexpr int bwd_consumers(int tpr) { return tpr > 256 ? tpr : 256; }
+
+template <typename T, int TPR, int V, int R, bool FUSED>
+__global__ void __launch_bounds__(bwd_consumers(TPR) + 32, TPR > 256 ? 1 : 2) rows_bwd(const RowsBwdParams p) {
+    constexpr int E = Elem<T>::E, NP = Elem<T>::NP, NT = bwd_consumers(TPR), TEAMS = NT / TPR, W = TPR > 32 ? TPR / 32 : 1;
     extern __shared__ __align__(128) uint8_t stages[];
-    __shared__ float red[2][TEAMS][W];
-    __shared__ __align__(8) uint64_t full[8];
-    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    __shared__ float red[2][R][TEAMS][W];
+    __shared__ __align__(8) uint64_t full[kStagesMost], empty[kStagesMost];
     const int C = p.N / E, nb = (p.N + kBlock8 - 1) / kBlock8;
     const StageLayout lay(p.stage_rows, p.N, sizeof(T), FUSED);
     const int blocks = (p.M + p.stage_rows - 1) / p.stage_rows;
     const int mine = blocks > (int)blockIdx.x ? (blocks - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < p.depth; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < p.depth; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], NT / 32);
+        }
         mbar_init_fence();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     pdl_wait();
     pdl_trigger();
     __syncthreads();
-    auto fetch = [&](int i) {  // this CTA's i-th block, by one thread
-        uint8_t *s = stages + (size_t)(i % p.depth) * lay.bytes;
-        uint64_t *bar = &full[i % p.depth];
-        const int64_t r0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * p.stage_rows;
-        const uint32_t rows = (uint32_t)min((int64_t)p.stage_rows, p.M - r0);
-        const uint32_t bytes = rows * (uint32_t)p.N * sizeof(T);
-        const Cover cc = cover16(p.codes + r0 * p.N, rows * p.N), cs = cover16(p.scales + r0 * nb, rows * nb),
-                    cr = cover16(p.rstd + r0, rows * 4u);
-        mbar_arrive_expect_tx(bar, bytes * (FUSED ? 2 : 1) + cc.bytes + cs.bytes + cr.bytes);
-        bulk_g2s(s, static_cast<const T *>(p.dy) + r0 * p.N, bytes, bar);
-        if (FUSED) bulk_g2s(s + lay.dres, static_cast<const T *>(p.dres) + r0 * p.N, bytes, bar);
-        bulk_g2s(s + lay.codes, cc.src, cc.bytes, bar);
-        bulk_g2s(s + lay.scales, cs.src, cs.bytes, bar);
-        bulk_g2s(s + lay.rstd, cr.src, cr.bytes, bar);
-    };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < p.depth && i < mine; ++i) fetch(i);
+    bool failed = false;
+    if (threadIdx.x >= NT) {  // the copying warp
+        if (threadIdx.x == NT) {
+            int stage = 0;
+            uint32_t phase = 1;  // (the first wait on an unused stage returns at once)
+            int64_t r0 = (int64_t)blockIdx.x * p.stage_rows;
+            const int64_t step = (int64_t)gridDim.x * p.stage_rows;
+            for (int i = 0; i < mine && !failed; ++i, r0 += step) {
+                if (!mbar_wait(&empty[stage], phase, kStageWaitLimit)) failed = true;
+                if (i >= p.depth) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                uint8_t *s = stages + (size_t)stage * lay.bytes;
+                const uint32_t rows = (uint32_t)min((int64_t)p.stage_rows, p.M - r0), bytes = rows * (uint32_t)p.N * sizeof(T);
+                const Cover cc = cover16(p.codes + r0 * p.N, rows * p.N), cs = cover16(p.scales + r0 * nb, rows * nb);
+                mbar_arrive_expect_tx(&full[stage], bytes * (FUSED ? 2 : 1) + cc.bytes + cs.bytes);
+                bulk_g2s(s, static_cast<const T *>(p.dy) + r0 * p.N, bytes, &full[stage]);
+                if (FUSED) bulk_g2s(s + lay.dres, static_cast<const T *>(p.dres) + r0 * p.N, bytes, &full[stage]);
+                bulk_g2s(s + lay.codes, cc.src, cc.bytes, &full[stage]);
+                bulk_g2s(s + lay.scales, cs.src, cs.bytes, &full[stage]);
+                if (++stage == p.depth) stage = 0, phase ^= 1u;
+            }
+            // (every copy is waited for by the threads that read it)
+            if (failed && p.status) *p.status = 1;
+        }
+        return;
+    }
+    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
     float2 f[V][NP], dw[V][NP];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -389,85 +431,116 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2) rows
         for (int q = 0; q < NP; ++q) f[v][q] = dw[v][q] = make_float2(0.f, 0.f);
         if (c < C) weights_at<T>(p.w, p.w32, c, p.offset, f[v]);
     }
-    int flip = 0;
-    bool failed = false;
-    for (int i = 0; i < mine; ++i) {
-        const uint8_t *s = stages + (size_t)(i % p.depth) * lay.bytes;
-        if (!failed && !mbar_wait(&full[i % p.depth], (uint32_t)(i / p.depth) & 1u, kStageWaitLimit)) failed = true;
-        const int64_t r0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * p.stage_rows;
-        const uint32_t oc = addr_mod16(p.codes + r0 * p.N), os = addr_mod16(p.scales + r0 * nb), orr = addr_mod16(p.rstd + r0);
-        for (int k = 0; k < p.stage_rows; k += TEAMS, flip ^= 1) {
-            const int lr = k + team;
-            const bool ok = lr < p.stage_rows && r0 + lr < p.M;
-            uint4 d[V], dr[FUSED ? V : 1];
-            float2 xh[V][NP];
-            float rstd = 0.f;
-            float2 sum = make_float2(0.f, 0.f);
-            if (ok) rstd = *reinterpret_cast<const float *>(s + lay.rstd + orr + lr * 4);
+    // dy and xhat of chunk c of row lr of the stage
+    auto values = [&](const uint8_t *s, uint32_t oc, uint32_t os, int lr, int c, float rstd, float2 (&d)[NP], float2 (&xh)[NP]) {
+        const uint32_t at = (uint32_t)lr * C + c;
+        unpack<T>(lds128(s + (size_t)at * 16), d);
+        const float to = rstd * from_codes8(lds8(s + lay.scales + os + lr * nb + c * E / kBlock8));
+        const float2 to2 = make_float2(to, to);
+        float x[4];
+        if constexpr (E == 8) {
+            const uint2 code = lds64(s + lay.codes + oc + at * E);
+            decode8x4(code.x, x);
+            xh[0] = Pair<true>::mul(make_float2(x[0], x[1]), to2);
+            xh[1] = Pair<true>::mul(make_float2(x[2], x[3]), to2);
+            decode8x4(code.y, x);
+            xh[2] = Pair<true>::mul(make_float2(x[0], x[1]), to2);
+            xh[3] = Pair<true>::mul(make_float2(x[2], x[3]), to2);
+        } else {
+            decode8x4(lds32(s + lay.codes + oc + at * E), x);
+            xh[0] = Pair<true>::mul(make_float2(x[0], x[1]), to2);
+            xh[1] = Pair<true>::mul(make_float2(x[2], x[3]), to2);
+        }
+    };
+    const float minus_inv = -1.f / (float)p.N;
+    int flip = 0, stage = 0;
+    uint32_t phase = 0;
+    int64_t r0 = (int64_t)blockIdx.x * p.stage_rows;
+    const int64_t step = (int64_t)gridDim.x * p.stage_rows;
+    for (int i = 0; i < mine; ++i, r0 += step) {
+        const uint8_t *s = stages + (size_t)stage * lay.bytes;
+        const uint32_t oc = addr_mod16(p.codes + r0 * p.N), os = addr_mod16(p.scales + r0 * nb);
+        const int rows = (int)min((int64_t)p.stage_rows, p.M - r0);
+        for (int k = 0; k < p.stage_rows; k += TEAMS * R, flip ^= 1) {
+            float rstd[R], part[R];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * TPR + t;
-                if (ok && c < C) {
-                    const uint32_t at = (uint32_t)lr * C + c;
-                    d[v] = lds128(s + (size_t)at * 16);
-                    if constexpr (FUSED) dr[v] = lds128(s + lay.dres + (size_t)at * 16);
-                    const uint8_t *code = s + lay.codes + oc + at * E;
-                    const float to = rstd * from_codes8(s[lay.scales + os + lr * nb + c * E / kBlock8]);
-                    float x[E];
+            for (int j = 0; j < R; ++j) {
+                const int lr = k + j * TEAMS + team;
+                rstd[j] = lr < rows ? p.rstd[r0 + lr] : 0.f;
+            }
+            if (k == 0 && !failed && !mbar_wait(&full[stage], phase, kStageWaitLimit)) failed = true;
 #pragma unroll
-                    for (int e = 0; e < E / 4; ++e) {
-                        float q4[4];
-                        decode8x4(*reinterpret_cast<const uint32_t *>(code + 4 * e), q4);
+            for (int j = 0; j < R; ++j) {
+                const int lr = k + j * TEAMS + team;
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) x[4 * e + m] = q4[m];
-                    }
-                    float2 dyv[NP];
-                    unpack<T>(d[v], dyv);
+                for (int v = 0; v < V; ++v) {
+                    const int c = v * TPR + t;
+                    if (lr < rows && c < C) {
+                        float2 d[NP], xh[NP];
+                        values(s, oc, os, lr, c, rstd[j], d, xh);
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        xh[v][q] = Pair<true>::mul(make_float2(x[2 * q], x[2 * q + 1]), make_float2(to, to));
-                        const float2 dx = Pair<true>::mul(dyv[q], xh[v][q]);
-                        dw[v][q] = Pair<true>::add(dw[v][q], dx);
-                        sum = Pair<true>::fma(dx, f[v][q], sum);
+                        for (int q = 0; q < NP; ++q) {
+                            const float2 x = Pair<true>::mul(d[q], xh[q]);
+                            dw[v][q] = Pair<true>::add(dw[v][q], x);
+                            sum = Pair<true>::fma(x, f[v][q], sum);
+                        }
                     }
                 }
+                part[j] = sum.x + sum.y;
             }
-            const float c1 = team_allreduce<TPR>(sum.x + sum.y, red[flip][team], t) / (float)p.N;
-            if (k + TEAMS >= p.stage_rows) {
-                // every thread holds its part of the last rows: the stage is free
-                if constexpr (TPR <= 32) __syncthreads();
-                if (threadIdx.x == 0 && i + p.depth < mine && !failed) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    fetch(i + p.depth);
-                }
+            constexpr int WIDTH = TPR < 32 ? TPR : 32;
+#pragma unroll
+            for (int o = WIDTH / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < R; ++j) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
+            if constexpr (TPR > 32) {
+                if ((t & 31) == 0)
+#pragma unroll
+                    for (int j = 0; j < R; ++j) red[flip][j][team][t >> 5] = part[j];
+                sync_first<NT>();
+#pragma unroll
+                for (int j = 0; j < R; ++j) part[j] = sum_slots<W>(red[flip][j][team], t & 31);
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * TPR + t;
-                if (ok && c < C) {
-                    float2 g[NP], o[NP];
-                    unpack<T>(d[v], g);
-                    if constexpr (FUSED) unpack<T>(dr[v], o);
+            for (int j = 0; j < R; ++j) {
+                const int lr = k + j * TEAMS + team;
+                const float mc = part[j] * minus_inv;
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        const float2 gw = Pair<true>::mul(g[q], f[v][q]);
-                        const float2 e = Pair<true>::fma(xh[v][q], make_float2(-c1, -c1), gw);
-                        g[q] = FUSED ? Pair<true>::fma(e, make_float2(rstd, rstd), o[q]) : Pair<true>::mul(e, make_float2(rstd, rstd));
+                for (int v = 0; v < V; ++v) {
+                    const int c = v * TPR + t;
+                    if (lr < rows && c < C) {
+                        float2 g[NP], xh[NP];
+                        values(s, oc, os, lr, c, rstd[j], g, xh);
+#pragma unroll
+                        for (int q = 0; q < NP; ++q) {
+                            g[q] = Pair<true>::fma(xh[q], make_float2(mc, mc), Pair<true>::mul(g[q], f[v][q]));
+                            g[q] = Pair<true>::mul(g[q], make_float2(rstd[j], rstd[j]));
+                        }
+                        if constexpr (FUSED) {
+                            float2 o[NP];
+                            unpack<T>(lds128(s + lay.dres + ((size_t)lr * C + c) * 16), o);
+#pragma unroll
+                            for (int q = 0; q < NP; ++q) g[q] = Pair<true>::add(g[q], o[q]);
+                        }
+                        static_cast<uint4 *>(p.dx)[(r0 + lr) * C + c] = pack<T>(g);
                     }
-                    static_cast<uint4 *>(p.dx)[(r0 + lr) * C + c] = pack<T>(g);
                 }
             }
         }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[stage]);
+        if (++stage == p.depth) stage = 0, phase ^= 1u;
     }
     if (failed) {  // no copy may land in shared memory that is another CTA's
-        for (int i = 0; i < p.depth && i < mine; ++i) mbar_wait(&full[i], (uint32_t)((mine - 1 - i) / p.depth) & 1u, kStageWaitLimit);
+        for (int i = max(0, mine - p.depth); i < mine; ++i) mbar_wait(&full[i % p.depth], (uint32_t)(i / p.depth) & 1u, kStageWaitLimit);
         if (p.status) *p.status = 1;
     }
     if (p.ws) {
         // the teams' sums of a column, one team after the other
         float *acc = reinterpret_cast<float *>(stages);
         for (int m = 0; m < TEAMS; ++m) {
-            __syncthreads();
+            sync_first<NT>();
             if (team == m) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -539,36 +612,37 @@ struct TeamSize {
     int tpr, v;
 };
 #define ROWS_FWD_TEAMS(X) X(8, 1) X(32, 1) X(32, 2) X(64, 2) X(64, 4) X(128, 3) X(128, 4) X(256, 3) X(256, 4) X(512, 3) X(512, 4) X(1024, 4) X(1024, 8)
-// (32 fp32 sums of dw a thread at most: 4 chunks of 8 values, 8 of 4)
-#define ROWS_BWD_TEAMS(X) X(8, 1) X(32, 1) X(32, 2) X(64, 2) X(64, 4) X(128, 3) X(128, 4) X(256, 3) X(256, 4) X(512, 3) X(512, 4)
-#define ROWS_BWD_TEAMS4(X) X(512, 6) X(512, 8)
+// (backward: and rows a team takes at once; 32 fp32 sums of dw a thread at most)
+#define ROWS_BWD_TEAMS(X) \
+    X(8, 1, 2) X(32, 1, 2) X(32, 2, 2) X(64, 2, 2) X(128, 2, 2) X(128, 3, 1) X(256, 2, 2) X(256, 3, 1) X(512, 2, 2) X(512, 3, 1) X(512, 4, 1)
+#define ROWS_BWD_TEAMS4(X) X(512, 6, 1) X(512, 8, 1)
 
 struct RowKernels {
     const void *fwd;
-    int tpr, v;  // 0: a CTA a row, any length
+    int tpr, v, r;  // 0: a CTA a row, any length
 };
 
 template <typename T, int SRC, bool KEEP> static RowKernels rows_fwd_pick(int C, bool wide) {
     if (wide) {
 #define X(tpr, v) \
-    if (C <= tpr * v) return {(const void *)rows_fwd<T, tpr, v, SRC, KEEP>, tpr, v};
+    if (C <= tpr * v) return {(const void *)rows_fwd<T, tpr, v, SRC, KEEP>, tpr, v, 1};
         ROWS_FWD_TEAMS(X)
 #undef X
     }
-    return {(const void *)rows_fwd_any<T, SRC, KEEP>, 0, 0};
+    return {(const void *)rows_fwd_any<T, SRC, KEEP>, 0, 0, 0};
 }
 
 template <typename T, bool FUSED> static RowKernels rows_bwd_pick(int C, bool wide) {
     if (wide) {
-#define X(tpr, v) \
-    if (C <= tpr * v) return {(const void *)rows_bwd<T, tpr, v, FUSED>, tpr, v};
+#define X(tpr, v, r) \
+    if (C <= tpr * v) return {(const void *)rows_bwd<T, tpr, v, r, FUSED>, tpr, v, r};
         ROWS_BWD_TEAMS(X)
         if constexpr (Elem<T>::E == 4) {
             ROWS_BWD_TEAMS4(X)
         }
 #undef X
     }
-    return {(const void *)rows_bwd_any<T, FUSED>, 0, 0};
+    return {(const void *)rows_bwd_any<T, FUSED>, 0, 0, 0};
 }
 
 enum { kPackBlocks = 0, kPackAny, kUnpackBlocks, kUnpackAny, kEmbedRows, kDwAny };
