@@ -562,6 +562,7 @@ typedef enum {
 } rmsnorm_act_t;
 
 #define ROWS_MAX_GROUPS 4096
+#define ROWS_MAX_CHANNELS 8192
 
 /*
  * Group norm with an activation, channels last: x [B, S, C] contiguous, S
@@ -576,7 +577,7 @@ typedef enum {
  * no digits. fp32 throughout, y rounded once. y may equal x.
  * codes, scales: NULL, or x kept in 8 bits as by ckpt8_pack of [B S, C].
  * S == 0 sets mean and rstd to 0. INVALID_ARG also: C % G != 0, C >
- * RMSNORM_MAX_N, an unknown act. UNSUPPORTED: G > ROWS_MAX_GROUPS.
+ * ROWS_MAX_CHANNELS, an unknown act. UNSUPPORTED: G > ROWS_MAX_GROUPS.
  */
 rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, const void *beta, void *y, float *mean,
                                float *rstd, void *codes, uint8_t *scales, void *workspace,

@@ -39,7 +39,7 @@ SOURCES = ["api.cu", "fwd_bf16.cu", "fwd_f32.cu", "fwd_f16.cu", "fwd_bf16w32.cu"
            "groupnorm.cu", "groupnorm_f32.cu", "groupnorm_bf16.cu", "groupnorm_f16.cu",
            "ckpt8.cu", "rows_f32.cu", "rows_bf16.cu", "rows_f16.cu", "embed.cu"]
 HEADERS = ["common.cuh", "plans.h", "fwd_kernels.cuh", "bwd_kernels.cuh", "head_rows.h", "tcgen05.cuh",
-           "rows8.cuh", "groupnorm_kernels.cuh", "groupnorm_held.cuh", "rows_kernels.cuh", "embed.cuh", "train_rows.h"]
+           "rows8.cuh", "groupnorm_kernels.cuh", "groupnorm_held.cuh", "groupnorm_flow.cuh", "rows_kernels.cuh", "embed.cuh", "train_rows.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

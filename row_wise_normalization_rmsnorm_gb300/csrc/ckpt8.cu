@@ -164,7 +164,7 @@ static EmbedPlan embed_plan(int64_t T, int64_t rows, int64_t N) {
         p.vals2 = take((size_t)T * 4);
         p.counts = take((size_t)kSortBins * (p.tiles + 1) * 4);
     }
-    p.present = take(p.ctas ? 0 : (size_t)p.words * 4);
+    p.present = take((size_t)p.words * 4);
     p.open = take((size_t)(p.pieces + 1) * 8);
     p.ends = take((size_t)rows * 4);
     p.parts = take((size_t)p.pieces * 2 * N * 4);
@@ -177,7 +177,7 @@ static int run_sort(const EmbedPlan &b, SortParams &p, char *w, int dtype, bool 
     if (b.ctas) {
         p.keys = at(b.keys), p.vals = at(b.vals);
         // the other SMs clear the rows without a token meanwhile (whole clusters of CTAs, one an SM)
-        const int clear = p.dtable ? std::max(1, (sms - b.ctas) / b.ctas) * b.ctas : 0;
+        const int clear = p.early > 0 ? std::max(1, (sms - b.ctas) / b.ctas) * b.ctas : 0;
         void *args[] = {&p, const_cast<int *>(&b.share)};
         return launch(embed_sort_kernel(dtype, out32, wide), (unsigned)(b.ctas + clear), 1, kSortThreads,
                       sort_shared() + std::max((size_t)b.share * 16, (size_t)kClearWords * 4), args, s, (unsigned)b.ctas);
@@ -360,8 +360,10 @@ extern "C" rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dta
     p.slices = (C + p.team - 1) / p.team;
     const int teams = 256 / p.team;
     const int64_t sums = ((int64_t)b.pieces * p.slices + teams - 1) / teams;
-    // rows without a token: cleared beside the sort where one cluster sorts, else by these CTAs
-    const int64_t clears = accumulate || b.ctas ? 0 : (int64_t)b.words * p.slices;
+    // rows without a token: some cleared beside the sort where one cluster sorts, the others by these CTAs
+    const int64_t early = accumulate || !b.ctas ? 0 : std::min<int64_t>(rows, kClearEarly / (N * ob) / 32 * 32);
+    const int64_t clears = accumulate ? 0 : (rows - early + 31) / 32 * p.slices;
+    p.early = early;
     if (sums + clears > 0x7fffffffLL) return RMSNORM_ERR_INVALID_ARG;
     p.sum_ctas = (int)sums;
     return with_workspace(workspace, workspace_bytes, b.bytes, s, [&](char *w) {
@@ -369,7 +371,7 @@ extern "C" rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dta
         std::memset(&q, 0, sizeof q);
         q.ids = ids, q.id_bytes = id_bytes, q.rows = rows, q.T = (int)T, q.bits = b.bits, q.passes = b.passes, q.tiles = b.tiles;
         q.words = b.words;
-        q.dtable = accumulate ? nullptr : dtable, q.N = (int)N;
+        q.dtable = dtable, q.N = (int)N, q.early = early;
         q.present = reinterpret_cast<uint32_t *>(w + b.present);
         q.open = reinterpret_cast<uint32_t *>(w + b.open);
         int le = run_sort(b, q, w, base_of(dt), out32, wide, sms, s);
@@ -379,7 +381,7 @@ extern "C" rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dta
         void *args[] = {&p};
         if (le == 0) le = launch(embed_sum_kernel(base_of(dt), out32, wide), (unsigned)(sums + clears), 1, 256, 0, args, s);
         if (le == 0 && b.pieces > 1)
-            le = launch(embed_join_kernel(base_of(dt), out32, wide), (unsigned)std::min<int64_t>(4 * sms, (int64_t)b.pieces * ((C + kJoinChunks - 1) / kJoinChunks)), 1, 256, 0, args, s);
+            le = launch(embed_join_kernel(base_of(dt), out32, wide), (unsigned)std::min<int64_t>(8 * sms, (int64_t)b.pieces * ((C + kJoinChunks - 1) / kJoinChunks)), 1, 256, 0, args, s);
         return le == 0 ? RMSNORM_SUCCESS : head_cuda_fail(le);
     });
 }

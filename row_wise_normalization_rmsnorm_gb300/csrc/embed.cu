@@ -128,9 +128,11 @@ template <typename TO, int E> __device__ __forceinline__ void clear_row(void *dt
 
 // The rows without a token, by the CTAs beside the sorting cluster: each
 // marks the ids of its share of the rows in shared memory, then clears the
-// others. (The sort keeps 8 SMs for 15 us, and memory would be idle.)
+// others. The sort keeps 8 SMs for 15 us, and memory would be idle; as many
+// rows are cleared here as memory takes in that time (it writes 3.9 TB/s at
+// most, reads and writes 6.7 together), the others beside the sums.
 template <typename TO, int E> __device__ __forceinline__ void clear_rows(const SortParams &p, uint32_t *marks, int cta, int ctas) {
-    const int64_t v0 = p.rows * cta / ctas, v1 = p.rows * (cta + 1) / ctas;
+    const int64_t v0 = p.early * cta / ctas, v1 = p.early * (cta + 1) / ctas;
     const int C = p.N / E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int64_t lo = v0; lo < v1; lo += (int64_t)kClearWords * 32) {
         const int n = (int)min((int64_t)kClearWords * 32, v1 - lo);
@@ -168,6 +170,7 @@ template <typename TO, int E> __global__ void __launch_bounds__(kSortThreads) em
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = max(0, min(share, p.T - rank * share));
     const int per = (share + kSortThreads - 1) / kSortThreads;
+    for (int i = rank * kSortThreads + threadIdx.x; i < p.words; i += ctas * kSortThreads) p.present[i] = 0;
     if (rank == 0 && threadIdx.x == 0) p.open[0] = 0;
     uint32_t key[kSortPer], val[kSortPer], place[kSortPer];
 #pragma unroll
@@ -190,7 +193,7 @@ template <typename TO, int E> __global__ void __launch_bounds__(kSortThreads) em
         }
         const int shift = pass * p.bits;
         rank_tokens<kSortPer>(s, n, per, shift, p.bits, [&](int r) { return key[r]; }, place);
-        cluster_sync();  // the CTAs' totals are there
+        cluster_sync();  // the CTAs' totals (and, before the first pass, the cleared bits) are there
         uint32_t all = 0, before = 0;
         if ((int)threadIdx.x < (1 << p.bits))
             for (int c = 0; c < ctas; ++c) {
@@ -215,6 +218,7 @@ template <typename TO, int E> __global__ void __launch_bounds__(kSortThreads) em
                     const uint32_t cta = to / (uint32_t)share;
                     st_remote2(cluster_address(&buf[(pass + 1) & 1][to - cta * share], cta), key[r], val[r]);
                 }
+                if (pass == 0 && key[r] < (uint32_t)p.rows) atomicOr(&p.present[key[r] >> 5], 1u << (key[r] & 31u));
             }
         }
         cluster_sync();  // pairs have arrived, and nobody reads these totals any more
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(256) embed_sum(const EmbedSumParams p) {
     const int C = p.N / E;
     if ((int)blockIdx.x >= p.sum_ctas) {
         const int64_t item = (int64_t)blockIdx.x - p.sum_ctas;
-        const int64_t r0 = item / p.slices * 32;
+        const int64_t r0 = p.early + item / p.slices * 32;
         const uint32_t there = p.present[r0 >> 5];
         const int teams = 256 / p.team;
         const int c = (int)(item % p.slices) * p.team + (int)threadIdx.x % p.team;
@@ -399,11 +403,11 @@ __global__ void __launch_bounds__(256) embed_sum(const EmbedSumParams p) {
 }
 
 // Runs over several pieces: the last part of the piece where the run begins,
-// then the first parts of those behind it, in order. 8 lanes of pieces and
-// kJoinChunks chunks a CTA; the lanes' sums are added in order.
+// then the first parts of those behind it, in order. kJoinLanes lanes of
+// pieces and kJoinChunks chunks a CTA; the lanes' sums are added in order.
 template <typename T, typename TO, int E>
 __global__ void __launch_bounds__(256) embed_join(const EmbedSumParams p) {
-    __shared__ float lane_sum[8][kJoinChunks][E + 1];
+    __shared__ float lane_sum[kJoinLanes][kJoinChunks][E + 1];
     pdl_wait();
     pdl_trigger();
     const int C = p.N / E, slices = (C + kJoinChunks - 1) / kJoinChunks;
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(256) embed_join(const EmbedSumParams p) {
         const uint2 run = *reinterpret_cast<const uint2 *>(p.open + 2 + 2 * (item / slices));
         const int first = (int)run.x, last = (int)p.ends[run.y];
         const int c = (int)(item % slices) * kJoinChunks + t;
-        const int per = (last - first + 1 + 7) / 8, lanes = (last - first + per) / per;  // lanes with pieces
+        const int per = (last - first + kJoinLanes) / kJoinLanes, lanes = (last - first + per) / per;  // lanes with pieces
         float sum[E];
         fill_v(0.f, sum);
         if (c < C && lane < lanes) {

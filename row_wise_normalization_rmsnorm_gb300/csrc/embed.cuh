@@ -18,10 +18,11 @@ struct SortParams {
     const void *ids;
     uint32_t *keys_in, *vals_in, *keys, *vals;  // a pass over several launches: from, to (keys_in NULL: from ids)
     uint32_t *counts;   // [kSortBins, tiles] and the bins' totals behind them
-    uint32_t *present;  // (several launches) one bit a row of the table: some token is its
+    uint32_t *present;  // one bit a row of the table: some token is its
     uint32_t *open;     // [0]: how many pieces end inside a run (set to 0 here)
-    void *dtable;       // (one cluster) whose rows without a token are set to zero; NULL: they stay
+    void *dtable;       // (one cluster) whose first rows without a token are set to zero here
     int64_t rows;       // of the table; the key of ids outside it
+    int64_t early;      // rows that are cleared beside the sort (a multiple of 32, or all)
     int T, N, id_bytes, shift, bits, passes, tiles, words;
 };
 
@@ -32,14 +33,15 @@ struct EmbedSumParams {
     uint32_t *open;     // [0]: count; then pairs from [2]: a piece that ends inside a run, the run's row
     uint32_t *ends;     // [rows]: the piece where a row's run ends, for runs over several
     float *parts;       // [pieces, 2, N]: the sums of a piece's first row and of its last one, where they are not whole
-    int64_t rows;
+    int64_t rows, early;
     int T, N, pieces, team, accumulate;
     int sum_ctas, slices;  // CTAs that sum, column slices of a row
     float scale;
 };
 
 constexpr int kClearWords = 8192;    // bits of rows that a clearing CTA holds at once, in words
-constexpr int kJoinChunks = 32;      // of a row, that a CTA joins
+constexpr int kJoinChunks = 64, kJoinLanes = 4;  // chunks of a row that a CTA joins, threads a chunk
+constexpr int64_t kClearEarly = 48 << 20;        // bytes of rows that are cleared beside the sort
 
 const void *embed_sort_kernel(int dtype, bool out32, bool wide);  // a cluster's
 const void *sort_kernel(int which);  // 1, 2, 3: a pass's count, scan, move

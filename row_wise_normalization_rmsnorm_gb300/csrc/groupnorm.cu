@@ -4,29 +4,49 @@
 #include <cmath>
 #include <cstring>
 
+#include "groupnorm_flow.cuh"
 #include "groupnorm_held.cuh"
 #include "head_rows.h"
 #include "plans.h"
 #include "train_rows.h"
 
+#ifndef FLOW_KB
+#define FLOW_KB 256
+#endif
+#ifndef FLOW_STAGE
+#define FLOW_STAGE 28
+#endif
+
 namespace rmsn {
 
-static const void *gn_flow(int base, bool backward, bool wide, int act, bool kept) {
-    return base == RMSNORM_BF16 ? gn_flow_bf16(backward, wide, act, kept)
-           : base == RMSNORM_F16 ? gn_flow_f16(backward, wide, act, kept)
-                                 : gn_flow_f32(backward, wide, act, kept);
+static const void *gn_flow(int base, bool backward, int chunk, int act, bool kept) {
+    return base == RMSNORM_BF16 ? gn_flow_bf16(backward, chunk, act, kept)
+           : base == RMSNORM_F16 ? gn_flow_f16(backward, chunk, act, kept)
+                                 : gn_flow_f32(backward, chunk, act, kept);
 }
 
 struct GnCall {
     int64_t B, S, C;
     int G, act, dt;
-    bool backward, kept, wide;
+    bool backward, kept;
+    int chunk;  // values of a chunk: 8 or 4 of them, or single ones
 };
 
-static const void *gn_held(int base, bool backward, bool wide, int act, bool kept) {
-    return base == RMSNORM_BF16 ? gn_held_bf16(backward, wide, act, kept)
-           : base == RMSNORM_F16 ? gn_held_f16(backward, wide, act, kept)
-                                 : gn_held_f32(backward, wide, act, kept);
+// The widest chunk, up to 16 bytes, that the rows (and their codes) are whole
+// numbers of, on its boundary.
+static int chunk_of(int64_t C, int es, std::initializer_list<const void *> rows, const void *codes) {
+    for (int chunk = 16 / es; chunk >= 4; chunk /= 2) {
+        bool fine = C % chunk == 0 && on(codes, (uintptr_t)chunk);
+        for (const void *p : rows) fine = fine && on(p, (uintptr_t)(chunk * es));
+        if (fine) return chunk;
+    }
+    return 1;
+}
+
+static const void *gn_held(int base, bool backward, int chunk, int act, bool kept) {
+    return base == RMSNORM_BF16 ? gn_held_bf16(backward, chunk, act, kept)
+           : base == RMSNORM_F16 ? gn_held_f16(backward, chunk, act, kept)
+                                 : gn_held_f32(backward, chunk, act, kept);
 }
 
 // The cut of the one-launch kernels: a cluster of `ctas` CTAs a unit of K
@@ -41,11 +61,11 @@ constexpr size_t kHeldSmem = 112 * 1024;  // of a CTA: two an SM
 
 // What a cut needs; false: it does not fit.
 static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
-    const int es = bytes_of(c.dt), E = c.wide ? 16 / es : 1, cg = (int)(c.C / c.G);
+    const int es = bytes_of(c.dt), E = c.chunk, cg = (int)(c.C / c.G);
     const int64_t W = (int64_t)K * cg, rows = (c.S + ctas - 1) / ctas;
     const bool span = K < c.G;
     // a span is whole chunks, of 64 bytes a row at least; kept in whole blocks of 32
-    if (W > 4096 || K > 256 || (span && (!c.wide || W % E != 0 || W * es < 64))) return false;
+    if (W > 4096 || K > 256 || (span && (c.chunk == 1 || W % E != 0 || W * es < 64))) return false;
     if (keep && W % kBlock8 != 0) return false;
     const int xb = c.kept ? 1 : es;
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
@@ -88,31 +108,60 @@ static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
 // Workspace of the one-launch gradient: a CTA's channel sums.
 static size_t held_bytes(const GnCall &c, const GnHeld &h) { return ((size_t)c.B * h.ctas * 2 * c.C * 4 + 255) / 256 * 256; }
 
-// The cut of the flow: pieces of `rows` places of a sample.
+// The cut of the flow: pieces of `rows` places of a sample, stages of
+// `stage_rows`.
 struct GnFlow {
-    int rows, pieces, lag, grid, folds;
+    int rows, pieces, lag, grid, folds, stage_rows, depth;
+    uint32_t offset[3], stage_bytes;
     size_t smem;
     size_t state, part, stat, parts, folded, bytes;  // workspace offsets (state_bytes of zeros first)
     size_t state_bytes;
 };
 
-static GnFlow flow_plan(const GnCall &c, int sms) {
+// Values of a chunk of the gradient's flow: with 8 a thread's constants of 8
+// channels spill, with 4 a row of more than 1024 channels is several tiles.
+static int flow_chunk(int chunk, int64_t C) { return chunk > 4 && C <= 4 * kFlowThreads ? 4 : chunk; }
+
+constexpr size_t kFlowSmem = 226 * 1024 / kFlowCtas, kFlowSmemMost = 224 * 1024;  // of a CTA; of the only one on an SM
+
+static GnFlow flow_plan(GnCall c, int sms) {
     GnFlow f;
-    const int es = bytes_of(c.dt), E = c.wide ? 16 / es : 1;
-    const int64_t CC = c.C / E, cols = CC < kFlowThreads ? CC : kFlowThreads, lanes = kFlowThreads / cols;
-    f.grid = 2 * sms;
-    // about four pieces a CTA, of 16 KB at least and 64 KB at most, whole turns of the lanes
-    const int64_t row = c.C * es;
-    int64_t rows = (c.S * c.B + 4 * f.grid - 1) / (4 * f.grid);
-    rows = std::min<int64_t>(std::max<int64_t>(rows, (16 << 10) / row), std::max<int64_t>(1, (64 << 10) / row));
-    rows = std::max<int64_t>(1, (rows + lanes - 1) / lanes) * lanes;
-    while ((c.S + rows - 1) / rows > 65535) rows *= 2;
+    const int es = bytes_of(c.dt), E = c.chunk, xb = c.kept ? 1 : es;
+    const int64_t CC = c.C / E, tiles = (CC + kFlowThreads - 1) / kFlowThreads,
+                  cols = tiles > 1 ? ((CC + tiles - 1) / tiles + 7) / 8 * 8 : CC, lanes = kFlowThreads / cols;
+    const int64_t nb = c.kept ? (c.C + kBlock8 - 1) / kBlock8 : 0;
+    f.smem = 2 * sizeof(float) * kFlowThreads * E + (size_t)c.G * sizeof(float2);
+    // stages: three at least, of whole turns of the lanes
+    const int64_t row = c.C * (c.backward ? xb + es : es) + nb;
+    int64_t room = (int64_t)kFlowSmem - 1024 - (int64_t)f.smem;
+    auto bytes = [&](int64_t rows) {  // of a stage: the 16-byte blocks that hold its rows
+        auto up = [](int64_t n) { return (n + 30) / 16 * 16; };
+        f.offset[0] = 0;
+        f.offset[1] = (uint32_t)up(rows * c.C * xb);
+        f.offset[2] = f.offset[1] + (uint32_t)(c.backward ? up(rows * c.C * es) : 0);
+        f.stage_bytes = f.offset[2] + (uint32_t)(c.kept ? up(rows * nb) : 0);
+        if (!c.backward) f.stage_bytes = f.offset[1];
+        return (int64_t)f.stage_bytes;
+    };
+    int64_t rows = std::max<int64_t>(1, (FLOW_STAGE << 10) / row / lanes) * lanes;
+    while (rows > 1 && 3 * bytes(rows) > room) rows = rows > lanes ? std::max<int64_t>(rows / 2 / lanes, 1) * lanes : rows / 2;
+    if (2 * bytes(rows) > room) room = (int64_t)kFlowSmemMost - (int64_t)f.smem;  // (rows of ROWS_MAX_CHANNELS: two fit)
+    f.stage_rows = (int)rows;
+    f.depth = (int)std::min<int64_t>(kFlowStagesMost, room / std::max<int64_t>(1, bytes(rows)));
+    f.grid = kFlowCtas * sms;
+    // pieces: the sums' joining is a cost a piece, so several stages where a row is one tile
+    // (and whole turns of the lanes fit a stage), but two pieces for every CTA where there are rows enough
+    int64_t turns = 1;
+    if (tiles == 1 && rows % lanes == 0)
+        while (turns < 64 && 2 * turns * rows * row <= (FLOW_KB << 10) && c.S * c.B >= 4 * turns * rows * f.grid) turns *= 2;
+    rows *= turns;
+    while ((c.S + rows - 1) / rows > 65535 && tiles == 1 && rows % lanes == 0) rows *= 2;
     f.rows = (int)std::min<int64_t>(rows, c.S);
     f.pieces = (int)((c.S + f.rows - 1) / f.rows);
     f.lag = f.grid;
     f.grid = (int)std::min<int64_t>(f.grid, c.B * f.pieces);
     if (c.B * f.pieces <= f.lag) f.lag = 0;  // one turn of the CTAs: nothing to put between
-    f.smem = 2 * sizeof(float) * kFlowThreads * E + (size_t)c.G * sizeof(float2);
+    f.smem += (size_t)f.depth * f.stage_bytes;
     size_t at = 0;
     auto take = [&at](size_t n) {
         const size_t a = at;
@@ -137,7 +186,7 @@ static GnFlow flow_plan(const GnCall &c, int sms) {
 static bool gn_sizes(int64_t B, int64_t S, int64_t C, int64_t G, int act, int dt) {
     const int base = dt & ~RMSNORM_WEIGHT_F32;
     if (base != RMSNORM_F32 && base != RMSNORM_BF16 && base != RMSNORM_F16) return false;
-    if (B < 0 || S < 0 || C < 1 || C > RMSNORM_MAX_N || G < 1 || C % G != 0) return false;
+    if (B < 0 || S < 0 || C < 1 || C > ROWS_MAX_CHANNELS || G < 1 || C % G != 0) return false;
     if (B > 0x7fffffffLL || S > 0x7fffffffLL) return false;
     if (B > 0 && S > INT64_MAX / 8 / C / B) return false;
     return act >= kActNone && act <= kActGelu;
@@ -160,7 +209,7 @@ static rmsnorm_status_t gn_run_held(const GnParams &g, const GnCall &c, const Gn
     p.ctas = h.ctas, p.W = h.W, p.K = h.K, p.spans = c.G / h.K;
     p.slab[0] = h.slab[0], p.slab[1] = h.slab[1], p.scales = h.scales;
     p.status = status;
-    const void *k = gn_held(base, c.backward, c.wide, c.act, c.backward ? c.kept : g.codes != nullptr);
+    const void *k = gn_held(base, c.backward, c.chunk, c.act, c.backward ? c.kept : g.codes != nullptr);
     if (h.ctas > 8) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return head_cuda_fail((int)e);
@@ -183,14 +232,16 @@ static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const Gn
     p.g.parts = sums ? reinterpret_cast<float *>(w + f.parts) : nullptr;
     p.pieces = f.pieces, p.lag = f.lag;
     p.tickets = 2 * (c.B * f.pieces + f.pieces + f.lag);
+    p.stage_rows = f.stage_rows, p.depth = f.depth, p.stage_bytes = f.stage_bytes;
+    for (int i = 0; i < 3; ++i) p.offset[i] = f.offset[i];
     p.state = reinterpret_cast<uint32_t *>(w + f.state);
     p.part = reinterpret_cast<float2 *>(w + f.part), p.stat = reinterpret_cast<float2 *>(w + f.stat);
     p.status = status;
     int e = (int)cudaMemsetAsync(p.state, 0, f.state_bytes, s);
     void *args[] = {&p};
     if (e == 0)
-        e = launch(gn_flow(base, c.backward, c.wide, c.act, c.backward ? c.kept : g.codes != nullptr), (unsigned)f.grid, 1, kFlowThreads,
-                   f.smem, args, s);
+        e = launch(gn_flow(base, c.backward, c.chunk, c.act, c.backward ? c.kept : g.codes != nullptr), (unsigned)f.grid, 1, kFlowThreads + 32,
+                   f.smem, args, s, 1);
     if (e == 0 && sums) {
         const float *in = p.g.parts;
         int64_t n = c.B * f.pieces;
@@ -211,15 +262,17 @@ static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, b
     int sms = 0;
     if (!gn_sizes(B, S, C, G, 0, dt) || B == 0 || S == 0 || current_device(&sms, nullptr) != 0) return 0;
     size_t most = 0;
-    for (int wide = 0; wide < 2; ++wide) {
-        if (wide && C % (((dt & ~RMSNORM_WEIGHT_F32) == RMSNORM_F32) ? 4 : 8) != 0) continue;
+    for (int chunk : {8, 4, 1}) {
+        if (C % chunk != 0) continue;
         for (int kept = 0; kept < (backward ? 2 : 1); ++kept) {
-            const GnCall c{B, S, C, (int)G, 0, dt, backward, kept != 0, wide != 0};
+            GnCall c{B, S, C, (int)G, 0, dt, backward, kept != 0, chunk};
             const GnHeld h = held_plan(c, sms, false);
             if (h.ctas)
                 most = backward ? std::max(most, held_bytes(c, h)) : most;
-            else
+            else {
+                if (backward) c.chunk = flow_chunk(c.chunk, C);
                 most = std::max(most, flow_plan(c, sms).bytes);
+            }
         }
     }
     return most;
@@ -246,7 +299,7 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     int sms = 0, *status = nullptr;
     const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
-    GnCall c{B, S, C, (int)G, act, dt, false, false, C % (16 / es) == 0 && on(x, 16) && on(y, 16)};
+    GnCall c{B, S, C, (int)G, act, dt, false, false, chunk_of(C, es, {x, y}, nullptr)};
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.gamma = gamma, p.beta = beta, p.out = y, p.mean = mean, p.rstd = rstd;
@@ -254,7 +307,7 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     p.magic = p.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + p.cg - 1) / p.cg);
     p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32, p.eps = eps;
     // the codes in the same pass where rows are whole blocks of chunks
-    const bool fused = codes && c.wide && C % kBlock8 == 0 && on(codes, 8);
+    const bool fused = codes && c.chunk > 1 && C % kBlock8 == 0 && on(codes, (uintptr_t)c.chunk);
     if (fused) p.codes = static_cast<uint8_t *>(codes), p.scales = scales;
     if (codes && !fused) {  // first: y may be x
         const rmsnorm_status_t st = ckpt8_pack(x, codes, scales, B * S, C, (rmsnorm_dtype_t)base, stream);
@@ -285,8 +338,7 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     int sms = 0, *status = nullptr;
     const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
-    GnCall c{B, S, C, (int)G, act, dt, true, codes != nullptr,
-             C % (16 / es) == 0 && on(dy, 16) && on(dx, 16) && on(x, 16) && on(codes, 8)};
+    GnCall c{B, S, C, (int)G, act, dt, true, codes != nullptr, chunk_of(C, es, {dy, dx, x}, codes)};
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.dy = dy, p.codes_in = static_cast<const uint8_t *>(codes), p.scales_in = scales;
@@ -300,6 +352,7 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
             p.parts = reinterpret_cast<float *>(w);
             return gn_run_held(p, c, h, dgamma, dbeta, sms, status, s);
         });
+    c.chunk = flow_chunk(c.chunk, C);
     const GnFlow f = flow_plan(c, sms);
     return with_workspace(workspace, workspace_bytes, f.bytes, s,
                           [&](char *w) { return gn_run_flow(p, c, f, w, dgamma, dbeta, sms, status, s); });

@@ -1,0 +1,548 @@
+// groupnorm_flow.cuh -- group norm of samples that no cluster holds: one launch
+// of persistent CTAs that take pieces (rows of a sample) by ticket, first to
+// sum them and, `lag` pieces behind the sample's last sum, to normalise them.
+// By then the sample is summed and its rows still lie in the L2, so memory
+// reads them once, and reads and writes overlap all the way.
+//
+// A warp of its own draws the tickets and keeps a ring of stages of rows under
+// way into shared memory (bulk copies, whatever alignment rows have); the
+// others take the stages in order. A piece waits only for pieces with earlier
+// tickets, and every CTA takes its tickets in order: the earliest ticket not
+// yet done is the next of some running CTA and waits for none, so the launch
+// makes progress however few of its CTAs run at once.
+//
+// A piece's group statistics, (mean, sum of squared deviations) or the two
+// sums of the gradient, go to memory; the CTA that brings a sample's last
+// ones joins them, in the pieces' order.
+#pragma once
+
+#include "groupnorm_kernels.cuh"
+
+namespace rmsn {
+
+#ifndef FLOW_CTAS
+#define FLOW_CTAS 2
+#endif
+constexpr int kFlowThreads = 256, kFlowCtas = FLOW_CTAS;  // that compute, of a CTA; CTAs an SM
+constexpr int kFlowStagesMost = 8;
+constexpr uint32_t kFlowWaitLimit = 1u << 22;  // polls of 100 ns for a sample's statistics
+constexpr uint32_t kFlowCopyLimit = 1u << 24;  // polls of a stage (a wait for its reader or its copies)
+
+struct FlowParams {
+    GnParams g;          // rows: of a piece
+    int pieces, lag;     // of a sample; sum and normalise tickets of a piece lie pieces + lag pairs apart
+    int stage_rows, depth;
+    uint32_t offset[3], stage_bytes;  // in a stage: dy (0: x or its codes), scales; its size
+    int64_t tickets;
+    uint32_t *state;     // [0], [1]: the next ticket (64 bits); then [B] pieces summed, [B] samples joined. Zeros at the start
+    float2 *part;        // [B, pieces, G]
+    float2 *stat;        // [B, G]: (-mean, rstd), or the negated means of u gamma and of u gamma xhat
+    int *status;
+};
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void flow_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFlowThreads) : "memory"); }
+__device__ __forceinline__ void flow_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+struct FlowShared {
+    uint64_t full[kFlowStagesMost], empty[kFlowStagesMost];
+    int64_t ticket[kFlowStagesMost];  // of the stage's piece; -1: no more
+    uint32_t before;
+};
+
+// A ticket's piece.
+struct FlowPiece {
+    bool normalise, there;
+    int b, rows;
+    int64_t item, first;  // piece of the batch, first row of the matrix
+    __device__ __forceinline__ FlowPiece(const FlowParams &p, int64_t ticket) {
+        normalise = ticket & 1;
+        item = (ticket >> 1) - (normalise ? p.pieces + p.lag : 0);
+        there = item >= 0 && item < (int64_t)p.g.B * p.pieces;
+        b = there ? (int)(item / p.pieces) : 0;
+        const int64_t r0 = (item - (int64_t)b * p.pieces) * p.g.rows;
+        first = (int64_t)b * p.g.S + r0;
+        rows = (int)min((int64_t)p.g.rows, p.g.S - r0);
+    }
+};
+
+// The copying warp's one thread. N arrays of rows: value bytes es[i], `width[i]` values a row.
+template <int N>
+__device__ __forceinline__ void flow_copies(const FlowParams &p, FlowShared &s, uint8_t *ring, const void *const (&src)[N], const uint32_t (&row)[N]) {
+    unsigned long long *next = reinterpret_cast<unsigned long long *>(p.state);
+    unsigned long long drawn = atomicAdd(next, 1ull);
+    int stage = 0;
+    uint32_t phase = 1;
+    auto advance = [&]() {
+        if (++stage == p.depth) stage = 0, phase ^= 1u;
+    };
+    bool failed = false;
+    while (!failed) {
+        const int64_t ticket = (int64_t)drawn;
+        if (ticket >= p.tickets) break;
+        drawn = atomicAdd(next, 1ull);  // (read when this one's copies are under way)
+        const FlowPiece f(p, ticket);
+        if (!f.there) continue;
+        for (int r = 0; r < f.rows && !failed; r += p.stage_rows, advance()) {
+            if (!mbar_wait(&s.empty[stage], phase, kFlowCopyLimit)) {
+                failed = true;
+                break;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            uint8_t *to = ring + (size_t)stage * p.stage_bytes;
+            const uint32_t rows = (uint32_t)min(p.stage_rows, f.rows - r);
+            Cover c[N];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                c[i] = cover16(static_cast<const char *>(src[i]) + (f.first + r) * row[i], rows * row[i]);
+                bytes += c[i].bytes;
+            }
+            s.ticket[stage] = ticket;
+            mbar_arrive_expect_tx(&s.full[stage], bytes);
+#pragma unroll
+            for (int i = 0; i < N; ++i) bulk_g2s(to + (i ? p.offset[i] : 0u), c[i].src, c[i].bytes, &s.full[stage]);
+        }
+    }
+    if (!failed && mbar_wait(&s.empty[stage], phase, kFlowCopyLimit)) {
+        s.ticket[stage] = -1;
+        flow_arrive(&s.full[stage]);
+    } else if (p.status) {
+        *p.status = 1;
+    }
+}
+// The stages as the computing threads take them.
+struct FlowStages {
+    int stage;
+    uint32_t phase;
+    bool failed;
+    // the stage's piece (-1: no more, or the wait gave up)
+    __device__ __forceinline__ int64_t wait(FlowShared &s) {
+        if (!failed && !mbar_wait(&s.full[stage], phase, kFlowCopyLimit)) failed = true;
+        return failed ? -1 : s.ticket[stage];
+    }
+    __device__ __forceinline__ void release(const FlowParams &p, FlowShared &s) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) flow_arrive(&s.empty[stage]);
+        if (++stage == p.depth) stage = 0, phase ^= 1u;
+    }
+};
+__device__ __forceinline__ void flow_setup(const FlowParams &p, FlowShared &s) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.depth; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], kFlowThreads / 32);
+        }
+        mbar_init_fence();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+}
+
+// Joins a sample's pieces where this CTA's was the last: `join(g, sub, subs)`
+// by `subs` neighbouring lanes a group.
+template <class Join> __device__ __forceinline__ void sum_given(const FlowParams &p, FlowShared &s, int b, Join &&join) {
+    __threadfence();
+    flow_sync();
+    if (threadIdx.x == 0) s.before = atomicAdd(p.state + 2 + b, 1u);
+    flow_sync();
+    if (s.before != (uint32_t)p.pieces - 1) return;
+    __threadfence();
+    constexpr int subs = 8;
+    for (int g = threadIdx.x / subs; g < (p.g.G + kFlowThreads / subs - 1) / (kFlowThreads / subs) * (kFlowThreads / subs); g += kFlowThreads / subs)
+        join(g, (int)threadIdx.x % subs, subs);
+    __threadfence();
+    flow_sync();
+    if (threadIdx.x == 0) st_release(p.state + 2 + p.g.B + b, 1u);
+}
+__device__ __forceinline__ void wait_joined(const FlowParams &p, int b) {
+    if (threadIdx.x == 0) {
+        uint32_t k = 0;
+        while (ld_acquire(p.state + 2 + p.g.B + b) == 0 && ++k < kFlowWaitLimit) __nanosleep(100);
+        if (k >= kFlowWaitLimit && p.status) *p.status = 1;
+    }
+    flow_sync();
+}
+
+template <typename T, int E, int ACT, bool KEEP>
+__global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(const FlowParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) FlowShared fs;
+    float *lane_mean = reinterpret_cast<float *>(ring + (size_t)p.depth * p.stage_bytes), *lane_m2 = lane_mean + kFlowThreads * E;
+    float2 *acc = reinterpret_cast<float2 *>(lane_m2 + kFlowThreads * E);  // [G]: groups over several tiles; then the statistics
+    const GnParams &g = p.g;
+    flow_setup(p, fs);
+    const uint32_t pitch = (uint32_t)g.C * sizeof(T);
+    if (threadIdx.x >= kFlowThreads) {
+        if (threadIdx.x == kFlowThreads) {
+            const void *const src[1] = {g.x};
+            const uint32_t row[1] = {pitch};
+            flow_copies<1>(p, fs, ring, src, row);
+        }
+        return;
+    }
+    const int CC = g.C / E;
+    const Cut cut(CC, kFlowThreads);
+    FlowStages at{0, 0u, false};
+    for (int64_t ticket; (ticket = at.wait(fs)) >= 0;) {
+        const FlowPiece f(p, ticket);
+        if (!f.normalise) {
+            // (pieces of several stages where a row is one tile: the host's rule)
+            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+                const int cc = t0 + cut.col;
+                const bool in = cut.in && cc < CC;
+                float K[E], s1[E], s2[E];
+                fill_v(0.f, K);
+                fill_v(0.f, s1);
+                fill_v(0.f, s2);
+                int n = 0;
+                for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
+                    if (r0 > 0) at.wait(fs);
+                    const uint8_t *rows = ring + (size_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + (f.first + r0) * pitch) + cc * (E * sizeof(T));
+                    const int end = in ? min(p.stage_rows, f.rows - r0) : 0;
+                    int r = cut.lane;
+                    if (n == 0 && r < end) {
+                        held_values<T, E>(rows + (size_t)r * pitch, K);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) K[i] = -K[i];
+                        r += cut.lanes;
+                        n = 1;
+                    }
+#pragma unroll 4
+                    for (; r < end; r += cut.lanes, ++n) {
+                        float v[E];
+                        held_values<T, E>(rows + (size_t)r * pitch, v);
+                        gn_deviate(v, K, s1, s2);
+                    }
+                    if (t0 + cut.cols >= CC) at.release(p, fs);
+                }
+                lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
+                flow_sync();
+                join_lanes<kFlowThreads>(lane_mean, lane_m2, cut.cols * E, cut.lanes, f.rows);
+                flow_sync();
+                // a warp a group: this tile's channels, joined with the tiles before
+                const int c0 = t0 * E, c1 = min((t0 + cut.cols) * E, g.C);
+                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+                for (int k = c0 / g.cg + warp; k * g.cg < c1; k += kFlowThreads / 32) {
+                    const int lo = max(k * g.cg, c0), w = min((k + 1) * g.cg, c1) - lo;
+                    const float *cm = lane_mean + (lo - c0), *cq = lane_m2 + (lo - c0);
+                    const float ref = cm[0];
+                    float s = 0.f, m2 = 0.f;
+                    for (int c = wl; c < w; c += 32) s += cm[c] - ref;
+                    s = sub_sum<32>(s);
+                    float m = ref + s / (float)w;
+                    for (int c = wl; c < w; c += 32) {
+                        const float d = cm[c] - m;
+                        m2 += fmaf((float)f.rows * d, d, cq[c]);
+                    }
+                    m2 = sub_sum<32>(m2);
+                    if (wl == 0) {
+                        const float cnt = (float)f.rows * (float)w;
+                        if (lo > k * g.cg) {
+                            const float2 a = acc[k];
+                            const float na = (float)f.rows * (float)(lo - k * g.cg), d = m - a.x, share = cnt / (na + cnt);
+                            m = a.x + d * share;
+                            m2 = a.y + m2 + d * d * (na * share);
+                        }
+                        if (lo + w < (k + 1) * g.cg)
+                            acc[k] = make_float2(m, m2);
+                        else
+                            p.part[f.item * g.G + k] = make_float2(m, m2);
+                    }
+                }
+                if (t0 + cut.cols < CC) flow_sync();
+            }
+            sum_given(p, fs, f.b, [&](int k, int sub, int subs) {
+                const bool in = k < g.G;
+                const float2 *part = p.part + (int64_t)f.b * p.pieces * g.G + k;
+                const float n = (float)g.S * (float)g.cg;
+                auto count = [&](int i) { return (float)min((int64_t)g.rows, g.S - (int64_t)i * g.rows) * (float)g.cg; };
+                const float ref = in ? __ldcg(part).x : 0.f;
+                float s = 0.f, m2 = 0.f;
+                if (in) {
+#pragma unroll 8
+                    for (int i = sub; i < p.pieces; i += subs) s += count(i) * (__ldcg(part + (int64_t)i * g.G).x - ref);
+                }
+                const float m = ref + sub_sum<8>(s) / n;
+                if (in) {
+#pragma unroll 8
+                    for (int i = sub; i < p.pieces; i += subs) {
+                        const float2 a = __ldcg(part + (int64_t)i * g.G);
+                        const float d = a.x - m;
+                        m2 += fmaf(count(i) * d, d, a.y);
+                    }
+                }
+                m2 = sub_sum<8>(m2);
+                if (in && sub == 0) {
+                    const float r = 1.f / sqrtf(m2 / n + g.eps);
+                    p.stat[(int64_t)f.b * g.G + k] = make_float2(-m, r);
+                    g.mean[(int64_t)f.b * g.G + k] = m;
+                    g.rstd[(int64_t)f.b * g.G + k] = r;
+                }
+            });
+            continue;
+        }
+        wait_joined(p, f.b);
+        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)f.b * g.G + k);
+        flow_sync();
+        for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
+            if (r0 > 0) at.wait(fs);
+            const int64_t first = f.first + r0;
+            const uint8_t *stage = ring + (size_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + first * pitch);
+            const int rows = min(p.stage_rows, f.rows - r0);
+            T *y = static_cast<T *>(g.out) + first * g.C;
+            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+                const int cc = t0 + cut.col;
+                if (!cut.in || cc >= CC) continue;
+                float minus_mean[E], f_[E], gamma[E], beta[E];
+                groups_v(acc, cc * E, g.cg, g.magic, minus_mean, f_);
+                params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
+                params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
+                mul_v(f_, gamma, f_);
+#pragma unroll 2
+                for (int r = cut.lane; r < rows; r += cut.lanes) {
+                    float v[E], z[E];
+                    const Vals<T, E> raw = held_chunk<T, E>(stage + (size_t)r * pitch + cc * (E * sizeof(T)));
+                    raw.get(v);
+                    gn_value<T, ACT>(v, minus_mean, f_, beta, z);
+                    Vals<T, E> o;
+                    o.set(z);
+                    o.store(y + (int64_t)r * g.C + cc * E);
+                    if constexpr (KEEP)
+                        keep_chunk<T, E>(raw.u, true, block_lanes<E>(), g.codes + (first + r) * g.C + cc * E,
+                                         g.scales + (first + r) * (g.C / kBlock8) + cc * E / kBlock8);
+                }
+            }
+            at.release(p, fs);
+        }
+        flow_sync();  // (acc is the next piece's)
+    }
+    if (at.failed && threadIdx.x == 0 && p.status) *p.status = 1;
+}
+
+template <typename T, int E, int ACT, bool KEPT>
+__global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(const FlowParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) FlowShared fs;
+    float *lane_a = reinterpret_cast<float *>(ring + (size_t)p.depth * p.stage_bytes), *lane_s = lane_a + kFlowThreads * E;
+    float2 *acc = reinterpret_cast<float2 *>(lane_s + kFlowThreads * E);  // [G]
+    const GnParams &g = p.g;
+    flow_setup(p, fs);
+    constexpr int XE = KEPT ? 1 : (int)sizeof(T);  // bytes of a value of x
+    const uint32_t pitch = (uint32_t)g.C * sizeof(T), xpitch = (uint32_t)g.C * XE, spitch = (uint32_t)((g.C + kBlock8 - 1) / kBlock8);
+    const char *xsrc = KEPT ? reinterpret_cast<const char *>(g.codes_in) : static_cast<const char *>(g.x);
+    if (threadIdx.x >= kFlowThreads) {
+        if (threadIdx.x == kFlowThreads) {
+            if constexpr (KEPT) {
+                const void *const src[3] = {xsrc, g.dy, g.scales_in};
+                const uint32_t row[3] = {xpitch, pitch, spitch};
+                flow_copies<3>(p, fs, ring, src, row);
+            } else {
+                const void *const src[2] = {xsrc, g.dy};
+                const uint32_t row[2] = {xpitch, pitch};
+                flow_copies<2>(p, fs, ring, src, row);
+            }
+        }
+        return;
+    }
+    const int CC = g.C / E;
+    const Cut cut(CC, kFlowThreads);
+    // where a stage's rows begin
+    struct Rows {
+        const uint8_t *x, *dy, *sc;
+    };
+    auto stage_rows_at = [&](int stage, int64_t first) {
+        const uint8_t *s = ring + (size_t)stage * p.stage_bytes;
+        return Rows{s + addr_mod16(xsrc + first * xpitch), s + p.offset[1] + addr_mod16(static_cast<const char *>(g.dy) + first * pitch),
+                    KEPT ? s + p.offset[2] + addr_mod16(g.scales_in + first * spitch) : nullptr};
+    };
+    auto chunk = [&](const Rows &s, int r, int cc, const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E],
+                     const float (&beta)[E], float (&xhat)[E], float (&u)[E]) {
+        if constexpr (KEPT)
+            held_codes<E>(s.x + (size_t)r * xpitch + cc * E, s.sc[(size_t)r * spitch + cc * E / kBlock8], xhat);
+        else
+            held_values<T, E>(s.x + (size_t)r * xpitch + cc * (E * XE), xhat);
+        held_values<T, E>(s.dy + (size_t)r * pitch + cc * (E * sizeof(T)), u);
+        gn_slope<T, ACT>(xhat, u, minus_mean, rstd, gamma, beta);
+    };
+    FlowStages at{0, 0u, false};
+    for (int64_t ticket; (ticket = at.wait(fs)) >= 0;) {
+        const FlowPiece f(p, ticket);
+        auto constants = [&](int cc, float (&minus_mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
+            const int64_t of = (int64_t)f.b * g.G;
+            auto group = [&](int c) { return g.magic ? (int)__umulhi((uint32_t)c, g.magic) : c; };
+            if (g.cg % E == 0) {
+                const int64_t k = of + group(cc * E);
+                fill_v(-g.mean[k], minus_mean);
+                fill_v(g.rstd[k], rstd);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const int64_t k = of + group(cc * E + i);
+                    minus_mean[i] = -g.mean[k];
+                    rstd[i] = g.rstd[k];
+                }
+            }
+            params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
+            params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
+        };
+        if (!f.normalise) {
+            float *out = g.parts ? g.parts + f.item * 2 * g.C : nullptr;
+            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+                const int cc = t0 + cut.col;
+                const bool in = cut.in && cc < CC;
+                float a[E], s[E], minus_mean[E], rstd[E], gamma[E], beta[E];
+                fill_v(0.f, a);
+                fill_v(0.f, s);
+                if (in) constants(cc, minus_mean, rstd, gamma, beta);
+                for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
+                    if (r0 > 0) at.wait(fs);
+                    const Rows rows = stage_rows_at(at.stage, f.first + r0);
+                    const int end = in ? min(p.stage_rows, f.rows - r0) : 0;
+#pragma unroll 2
+                    for (int r = cut.lane; r < end; r += cut.lanes) {
+                        float xhat[E], u[E];
+                        chunk(rows, r, cc, minus_mean, rstd, gamma, beta, xhat, u);
+                        fma_v(u, xhat, a, a);
+                        add_v(s, u, s);
+                    }
+                    if (t0 + cut.cols >= CC) at.release(p, fs);
+                }
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    lane_a[threadIdx.x * E + i] = a[i];
+                    lane_s[threadIdx.x * E + i] = s[i];
+                }
+                flow_sync();
+                const int width = cut.cols * E, c0 = t0 * E, c1 = min(c0 + width, g.C);
+                for (int c = threadIdx.x; c < c1 - c0; c += kFlowThreads) {
+                    float ta = lane_a[c], ts = lane_s[c];
+#pragma unroll 4
+                    for (int l = 1; l < cut.lanes; ++l) {
+                        ta += lane_a[l * width + c];
+                        ts += lane_s[l * width + c];
+                    }
+                    if (out) {
+                        out[c0 + c] = ta;
+                        out[g.C + c0 + c] = ts;
+                    }
+                    const float ga = param<T>(g.gamma, g.w32, c0 + c, 1.f);
+                    lane_a[c] = ta * ga;
+                    lane_s[c] = ts * ga;
+                }
+                flow_sync();
+                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+                for (int k = c0 / g.cg + warp; k * g.cg < c1; k += kFlowThreads / 32) {
+                    const int lo = max(k * g.cg, c0), hi = min((k + 1) * g.cg, c1);
+                    float2 m = make_float2(0.f, 0.f);
+                    for (int c = lo + wl; c < hi; c += 32) m = add2(m, make_float2(lane_s[c - c0], lane_a[c - c0]));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
+                    if (wl == 0) {
+                        if (lo > k * g.cg) m = add2(acc[k], m);
+                        if (hi < (k + 1) * g.cg)
+                            acc[k] = m;
+                        else
+                            p.part[f.item * g.G + k] = m;
+                    }
+                }
+                if (t0 + cut.cols < CC) flow_sync();
+            }
+            sum_given(p, fs, f.b, [&](int k, int sub, int subs) {
+                const bool in = k < g.G;
+                const float2 *part = p.part + (int64_t)f.b * p.pieces * g.G + k;
+                float2 m = make_float2(0.f, 0.f);
+                if (in) {
+#pragma unroll 8
+                    for (int i = sub; i < p.pieces; i += subs) m = add2(m, __ldcg(part + (int64_t)i * g.G));
+                }
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
+                const float n = (float)g.S * (float)g.cg;
+                if (in && sub == 0) p.stat[(int64_t)f.b * g.G + k] = make_float2(-m.x / n, -m.y / n);
+            });
+            continue;
+        }
+        wait_joined(p, f.b);
+        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)f.b * g.G + k);
+        flow_sync();
+        for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
+            if (r0 > 0) at.wait(fs);
+            const int64_t first = f.first + r0;
+            const Rows s = stage_rows_at(at.stage, first);
+            const int rows = min(p.stage_rows, f.rows - r0);
+            T *dx = static_cast<T *>(g.out) + first * g.C;
+            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
+                const int cc = t0 + cut.col;
+                if (!cut.in || cc >= CC) continue;
+                float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
+                constants(cc, minus_mean, rstd, gamma, beta);
+                groups_v(acc, cc * E, g.cg, g.magic, m1, m2);
+#pragma unroll 1
+                for (int r = cut.lane; r < rows; r += cut.lanes) {
+                    float xhat[E], u[E];
+                    chunk(s, r, cc, minus_mean, rstd, gamma, beta, xhat, u);
+                    gn_dx(xhat, u, rstd, gamma, m1, m2);
+                    Vals<T, E> o;
+                    o.set(u);
+                    o.store(dx + (int64_t)r * g.C + cc * E);
+                }
+            }
+            at.release(p, fs);
+        }
+        flow_sync();  // (acc is the next piece's)
+    }
+    if (at.failed && threadIdx.x == 0 && p.status) *p.status = 1;
+}
+
+// Many rows of sums folded into gridDim.y: row i of the result is the sum of
+// rows [i n / gridDim.y, (i + 1) n / gridDim.y), in order.
+static __global__ void __launch_bounds__(256) gn_fold(const float *in, float *out, int64_t n, int width) {
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    const int64_t i0 = n * blockIdx.y / gridDim.y, i1 = n * (blockIdx.y + 1) / gridDim.y;
+    if (c >= width) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int64_t i = i0; i < i1; ++i) s += in[i * width + c];
+    out[(int64_t)blockIdx.y * width + c] = s;
+}
+
+// ---------------------------------------------------------------- kernels --
+
+// (keeping x in the same pass: chunks only)
+template <typename T, int E, int ACT> static const void *gn_flow_fwd(bool kept) {
+    if constexpr (E > 1) {
+        if (kept) return (const void *)gn_fwd_flow<T, E, ACT, true>;
+    }
+    return (const void *)gn_fwd_flow<T, E, ACT, false>;
+}
+template <typename T, int E> static const void *gn_flow_e(bool backward, int act, bool kept) {
+#define FLOW(A)                                                                                              \
+    (!backward ? gn_flow_fwd<T, E, A>(kept)                                                                  \
+     : kept    ? (const void *)gn_bwd_flow<T, E, A, true>                                                    \
+               : (const void *)gn_bwd_flow<T, E, A, false>)
+    return act == kActSilu ? FLOW(kActSilu) : act == kActGelu ? FLOW(kActGelu) : FLOW(kActNone);
+#undef FLOW
+}
+// A kernel by chunks of `chunk` values.
+template <typename T> static const void *gn_flow_t(bool backward, int chunk, int act, bool kept) {
+    if constexpr (sizeof(T) == 2) {
+        if (chunk == 8) return gn_flow_e<T, 8>(backward, act, kept);
+    }
+    return chunk == 4 ? gn_flow_e<T, 4>(backward, act, kept) : gn_flow_e<T, 1>(backward, act, kept);
+}
+
+}  // namespace rmsn

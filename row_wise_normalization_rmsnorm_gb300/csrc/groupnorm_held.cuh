@@ -17,7 +17,10 @@
 
 namespace rmsn {
 
-constexpr int kHeldThreads = 256;
+#ifndef HELD_THREADS
+#define HELD_THREADS 256
+#endif
+constexpr int kHeldThreads = HELD_THREADS;
 constexpr int kHeldStages = 4;
 constexpr int kHeldCtas = 16;                 // of a cluster at most
 constexpr uint32_t kHeldWaitLimit = 1u << 20;  // polls of a piece's copies
@@ -63,6 +66,7 @@ struct Slab {
     }
 };
 
+// (16 bytes: past the L1)
 template <int BYTES> __device__ __forceinline__ void copy_chunk(uint8_t *to, const void *from) {
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
@@ -85,25 +89,6 @@ static_assert(kHeldStages == 4, "copies_wait");
 // those of piece i end before the end_of(n, i)-th.
 __device__ __forceinline__ int rows_of_lane(int rows, int lane, int lanes) { return lane < rows ? (rows - lane + lanes - 1) / lanes : 0; }
 __device__ __forceinline__ int end_of(int n, int i) { return (n * (i + 1) + kHeldStages - 1) / kHeldStages; }
-
-// E values from shared memory.
-template <typename T, int E> __device__ __forceinline__ void held_values(const uint8_t *p, float (&v)[E]) {
-    if constexpr (E == Elem<T>::E) {
-        Vals<T, E> c;
-        c.w = lds128(p);
-        c.get(v);
-    } else {
-        Vals<T, E> c;
-        c.w = *reinterpret_cast<const typename Vals<T, E>::W *>(p);
-        c.get(v);
-    }
-}
-template <int E> __device__ __forceinline__ void held_codes(const uint8_t *p, uint32_t b, float (&v)[E]) {
-    Kept<E> k;
-    k.w = *reinterpret_cast<const typename Kept<E>::W *>(p);
-    k.b = b;
-    k.get(v);
-}
 
 struct HeldPlace {
     int rank, b, c0, g0, rows;
@@ -132,6 +117,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
     extern __shared__ __align__(128) uint8_t held[];
     __shared__ __align__(8) uint64_t bar[kHeldStages];
     __shared__ bool failed;
+    constexpr int CB = E * (int)sizeof(T);  // bytes of a chunk
     const GnParams &g = p.g;
     float *lane_mean = reinterpret_cast<float *>(held + p.slab[0]), *lane_m2 = lane_mean + kHeldThreads * E;
     float *ch_mean = lane_m2 + kHeldThreads * E, *ch_m2 = ch_mean + p.W;
@@ -153,7 +139,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
     pdl_wait();
     pdl_trigger();
     const int CW = p.W / E;
-    const Cut cut(CW);
+    const Cut cut(CW, kHeldThreads);
     const uint8_t *rows = held + (E == 1 ? xs.off : 0u);
     const uint32_t pitch = (uint32_t)p.W * sizeof(T);
     if constexpr (E == 1) {
@@ -172,11 +158,11 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
         const int n = in ? rows_of_lane(at.rows, cut.lane, cut.lanes) : 0;
         if constexpr (E > 1) {
             const T *x = static_cast<const T *>(g.x) + (at.first + cut.lane) * g.C + at.c0 + cc * E;
-            uint8_t *to = held + (uint32_t)cut.lane * pitch + cc * 16;
+            uint8_t *to = held + (uint32_t)cut.lane * pitch + cc * CB;
             int k = 0;
             for (int i = 0; i < kHeldStages; ++i) {
                 for (const int end = end_of(n, i); k < end; ++k)
-                    copy_chunk<16>(to + (uint32_t)(k * cut.lanes) * pitch, x + (int64_t)k * cut.lanes * g.C);
+                    copy_chunk<CB>(to + (uint32_t)(k * cut.lanes) * pitch, x + (int64_t)k * cut.lanes * g.C);
                 copies_commit();
             }
         }
@@ -205,7 +191,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
         }
         lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
         __syncthreads();
-        join_lanes(lane_mean, lane_m2, cut.cols * E, cut.lanes, at.rows);
+        join_lanes<kHeldThreads>(lane_mean, lane_m2, cut.cols * E, cut.lanes, at.rows);
         __syncthreads();
         for (int c = threadIdx.x; c < cut.cols * E && t0 * E + c < p.W; c += kHeldThreads) {
             ch_mean[t0 * E + c] = lane_mean[c];
@@ -268,7 +254,8 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
 #pragma unroll 2
         for (int r = cut.lane; r < at.rows; r += cut.lanes) {
             float v[E], z[E];
-            held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), v);
+            const Vals<T, E> raw = held_chunk<T, E>(rows + (size_t)r * pitch + cc * CB);
+            raw.get(v);
             gn_value<T, ACT>(v, minus_mean, f, beta, z);
             Vals<T, E> o;
             o.set(z);
@@ -276,7 +263,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
             if constexpr (KEEP) {
                 const int64_t row = at.first + r;
                 const int c = at.c0 + cc * E;
-                keep_chunk<T>(lds128(rows + (size_t)r * pitch + cc * 16), true, block_lanes<T>(), g.codes + row * g.C + c, g.scales + row * (g.C / kBlock8) + c / kBlock8);
+                keep_chunk<T, E>(raw.u, true, block_lanes<E>(), g.codes + row * g.C + c, g.scales + row * (g.C / kBlock8) + c / kBlock8);
             }
         }
     }
@@ -291,6 +278,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
     extern __shared__ __align__(128) uint8_t held[];
     __shared__ __align__(8) uint64_t bar[kHeldStages];
     __shared__ bool failed;
+    constexpr int CB = E * (int)sizeof(T);  // bytes of a chunk
     const GnParams &g = p.g;
     uint8_t *sc = held + p.slab[0] + p.slab[1];  // scale bytes [rows, nsc]
     float *lane_a = reinterpret_cast<float *>(sc + p.scales), *lane_s = lane_a + kHeldThreads * E;
@@ -315,20 +303,20 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
     pdl_wait();
     pdl_trigger();
     const int CW = p.W / E;
-    const Cut cut(CW);
+    const Cut cut(CW, kHeldThreads);
     const uint8_t *xrows = held + (E == 1 ? xs.off : 0u), *drows = held + p.slab[0] + (E == 1 ? ds.off : 0u);
     const uint32_t xpitch = (uint32_t)p.W * XE, dpitch = (uint32_t)p.W * sizeof(T);
     auto copy_column = [&](int cc, int n) {  // a chunk column's rows of this lane
         const int64_t first = (at.first + cut.lane) * g.C + at.c0 + cc * E;
         const char *x = (KEPT ? (const char *)g.codes_in : static_cast<const char *>(g.x)) + first * XE;
         const T *d = static_cast<const T *>(g.dy) + first;
-        uint8_t *xto = held + (uint32_t)cut.lane * xpitch + cc * (E * XE), *dto = held + p.slab[0] + (uint32_t)cut.lane * dpitch + cc * 16;
+        uint8_t *xto = held + (uint32_t)cut.lane * xpitch + cc * (E * XE), *dto = held + p.slab[0] + (uint32_t)cut.lane * dpitch + cc * CB;
         const int64_t step = (int64_t)cut.lanes * g.C;
         int k = 0;
         for (int i = 0; i < kHeldStages; ++i) {
             for (const int end = end_of(n, i); k < end; ++k) {
                 copy_chunk<E * XE>(xto + (uint32_t)(k * cut.lanes) * xpitch, x + k * step * XE);
-                copy_chunk<16>(dto + (uint32_t)(k * cut.lanes) * dpitch, d + k * step);
+                copy_chunk<CB>(dto + (uint32_t)(k * cut.lanes) * dpitch, d + k * step);
             }
             copies_commit();
         }
@@ -481,8 +469,11 @@ template <typename T, int E> static const void *gn_held_e(bool backward, int act
     return act == kActSilu ? HELD(kActSilu) : act == kActGelu ? HELD(kActGelu) : HELD(kActNone);
 #undef HELD
 }
-template <typename T> static const void *gn_held_t(bool backward, bool wide, int act, bool kept) {
-    return wide ? gn_held_e<T, Elem<T>::E>(backward, act, kept) : gn_held_e<T, 1>(backward, act, kept);
+template <typename T> static const void *gn_held_t(bool backward, int chunk, int act, bool kept) {
+    if constexpr (sizeof(T) == 2) {
+        if (chunk == 8) return gn_held_e<T, 8>(backward, act, kept);
+    }
+    return chunk == 4 ? gn_held_e<T, 4>(backward, act, kept) : gn_held_e<T, 1>(backward, act, kept);
 }
 
 }  // namespace rmsn

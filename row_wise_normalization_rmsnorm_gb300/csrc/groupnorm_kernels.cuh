@@ -21,6 +21,8 @@ namespace rmsn {
 
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 
+// Values of a chunk: 16 bytes where the channels' count and the addresses
+// allow it, else 8 bytes of 16-bit rows, else single values.
 struct GnParams {
     const void *x, *dy;
     const uint8_t *codes_in;   // x in 8 bits, in the place of x
@@ -52,34 +54,47 @@ template <> __device__ __forceinline__ float widen<__half>(__half v) { return __
 template <> __device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // E values that lie together, as one access.
+template <typename T> __device__ __forceinline__ float2 widen2(uint32_t u);
+template <> __device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t u) { return bf16x2_to_f2(u); }
+template <> __device__ __forceinline__ float2 widen2<__half>(uint32_t u) { return f16x2_to_f2(u); }
+template <typename T> __device__ __forceinline__ uint32_t narrow2(float2 v);
+template <> __device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float2 v) { return f2_to_bf16x2(v); }
+template <> __device__ __forceinline__ uint32_t narrow2<__half>(float2 v) { return f2_to_f16x2(v); }
+
 template <typename T, int E> struct Vals {
-    using W = typename Word<E * (int)sizeof(T)>::type;
-    W w;
+    static constexpr int B = E * (int)sizeof(T), N = B >= 4 ? B / 4 : 1;
+    using W = typename Word<B>::type;
+    union {
+        W w;
+        uint32_t u[N];
+    };
+    __device__ __forceinline__ Vals() {}
     __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const W *>(p); }
     __device__ __forceinline__ void load_last(const T *p) { w = __ldcs(reinterpret_cast<const W *>(p)); }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<W *>(p) = w; }
     __device__ __forceinline__ void get(float (&v)[E]) const {
-        if constexpr (E == Elem<T>::E) {
-            float2 q[Elem<T>::NP];
-            unpack<T>(w, q);
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) v[2 * i] = q[i].x, v[2 * i + 1] = q[i].y;
+            for (int i = 0; i < E; ++i) v[i] = __uint_as_float(u[i]);
+        } else if constexpr (E > 1) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 q = widen2<T>(u[i]);
+                v[2 * i] = q.x, v[2 * i + 1] = q.y;
+            }
         } else {
-            const T *t = reinterpret_cast<const T *>(&w);
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = widen<T>(t[i]);
+            v[0] = widen<T>(*reinterpret_cast<const T *>(&w));
         }
     }
     __device__ __forceinline__ void set(const float (&v)[E]) {
-        if constexpr (E == Elem<T>::E) {
-            float2 q[Elem<T>::NP];
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) q[i] = make_float2(v[2 * i], v[2 * i + 1]);
-            w = pack<T>(q);
+            for (int i = 0; i < E; ++i) u[i] = __float_as_uint(v[i]);
+        } else if constexpr (E > 1) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) u[i] = narrow2<T>(make_float2(v[2 * i], v[2 * i + 1]));
         } else {
-            T *t = reinterpret_cast<T *>(&w);
-#pragma unroll
-            for (int i = 0; i < E; ++i) store_elem(t, i, v[i]);
+            store_elem(reinterpret_cast<T *>(&w), 0, v[0]);
         }
     }
 };
@@ -169,34 +184,25 @@ __device__ __forceinline__ float rcp_fast(float v) {
     return r;
 }
 
-// The sigmoids of E values. For 16-bit rows one reciprocal serves two
-// (1 / a = b / (a b)): the special-function unit, 16 results a clock and SM,
-// bounds these kernels next to memory, and so it gives 1.5 results a value
-// instead of 2. z is held at -43, where the sigmoid is 2^-62 and a b still
-// finite. (fmaxf drops a NaN; z, which every result is multiplied by, brings
-// it back.) fp32 rows take the accurate exponential.
+// The sigmoids of E values: 1 / (1 + 2^(-z log2 e)), the reciprocal and (for
+// 16-bit rows) the exponential the fast ones; fp32 rows take the accurate
+// exponential. (One reciprocal for two values, 1 / a = b / (a b), takes 12
+// instead of 16 results of the special-function unit for 8 values, but 20
+// instructions more: 64 x 64 x 320 16.5 us so, TBD this way.)
 template <typename T, int E> __device__ __forceinline__ void sigmoid_v(const float (&z)[E], float (&p)[E]) {
     if constexpr (std::is_same<T, float>::value) {
 #pragma unroll
         for (int i = 0; i < E; ++i) p[i] = rcp_fast(1.f + expf(-z[i]));
-    } else if constexpr (E == 1) {
-        p[0] = rcp_fast(1.f + exp2_fast(-1.4426950f * fmaxf(z[0], -43.f)));
     } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) p[i] = fmaxf(z[i], -43.f);
         float k[E], one[E];
         fill_v(-1.4426950f, k);
         fill_v(1.f, one);
-        mul_v(p, k, p);
+        mul_v(z, k, p);
 #pragma unroll
         for (int i = 0; i < E; ++i) p[i] = exp2_fast(p[i]);
         add_v(p, one, p);
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            const float r = rcp_fast(p[i] * p[i + 1]);
-            const float2 q = Pair<true>::mul(make_float2(r, r), make_float2(p[i + 1], p[i]));
-            p[i] = q.x, p[i + 1] = q.y;
-        }
+        for (int i = 0; i < E; ++i) p[i] = rcp_fast(p[i]);
     }
 }
 __device__ __forceinline__ float gelu_of(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); }
@@ -298,104 +304,24 @@ template <int E> __device__ __forceinline__ void gn_deviate(const float (&v)[E],
 }
 
 // ------------------------------------------------------------ the CTA's cut --
-// T threads as row lanes x channel chunks: chunk columns of one pass, lanes,
-// and this thread's place. Where a row has more chunks than the CTA threads
-// (C > E threads) the CTA takes the row in tiles of `cols` chunks.
+// A CTA's threads as row lanes x channel chunks: chunk columns of one pass,
+// lanes, and this thread's place. Where a row has more chunks than the CTA
+// threads, the CTA takes it in tiles of equal width.
 struct Cut {
     int cols, lanes, lane, col;
     bool in;
-    __device__ __forceinline__ Cut(int chunks_in_row) {
-        cols = chunks_in_row < (int)blockDim.x ? chunks_in_row : (int)blockDim.x;
-        lanes = (int)blockDim.x / cols;
+    __device__ __forceinline__ Cut(int chunks_in_row, int threads) {
+        const int tiles = (chunks_in_row + threads - 1) / threads;
+        cols = (chunks_in_row + tiles - 1) / tiles;
+        if (tiles > 1) cols = (cols + 7) & ~7;  // (a block of 32 values is 8 lanes of a tile)
+        lanes = threads / cols;
         lane = (int)threadIdx.x / cols;
         col = (int)threadIdx.x - lane * cols;
         in = lane < lanes;
     }
 };
 
-// x of E channels, from its rows or from what they are kept as.
-template <typename T, int E, bool KEPT> struct XLoad {
-    typename std::conditional<KEPT, Kept<E>, Vals<T, E>>::type c;
-    __device__ __forceinline__ void load(const GnParams &p, int64_t row, int ch) {
-        if constexpr (KEPT)
-            c.load(p.codes_in, p.scales_in, row, p.C, ch);
-        else
-            c.load(static_cast<const T *>(p.x) + row * p.C + ch);
-    }
-};
-
-// ----------------------------------------------------------------- the flow --
-// Samples that no cluster holds: one launch of persistent CTAs that take
-// pieces (rows of a sample) by ticket, first to sum them and, `lag` pieces
-// behind the sample's last sum, to normalise them. By then the piece's sample
-// is summed and its rows still lie in the L2, so memory reads them once, and
-// reads and writes overlap all the way. A piece waits only for pieces with
-// earlier tickets, which running CTAs have taken and which wait for none:
-// the launch makes progress however few of its CTAs run at once.
-//
-// A piece's group statistics, (mean, sum of squared deviations) or the two
-// sums of the gradient, go to memory; the CTA that brings a sample's last
-// ones joins them, in the pieces' order.
-
-struct FlowParams {
-    GnParams g;
-    int pieces, lag;     // of a sample; S and A tickets of a piece lie pieces + lag pairs apart
-    int64_t tickets;
-    uint32_t *state;     // [0], [1]: the next ticket (64 bits); then [B] pieces summed, [B] samples joined. Zeros at the start
-    float2 *part;        // [B, pieces, G]
-    float2 *stat;        // [B, G]: (-mean, rstd), or the negated means of u gamma and of u gamma xhat
-    int *status;
-};
-
-constexpr int kFlowThreads = 256;
-constexpr uint32_t kFlowWaitLimit = 1u << 22;  // polls of 100 ns for a sample's statistics
-
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-struct FlowShared {
-    unsigned long long ticket;
-    uint32_t before;
-};
-
-// The CTA's next ticket.
-__device__ __forceinline__ int64_t next_ticket(const FlowParams &p, FlowShared &s) {
-    __syncthreads();  // everybody is done with the last one
-    if (threadIdx.x == 0) s.ticket = atomicAdd(reinterpret_cast<unsigned long long *>(p.state), 1ull);
-    __syncthreads();
-    return (int64_t)s.ticket;
-}
-
-// Joins a sample's pieces where this CTA's was the last: `join(g, sub, subs)`
-// by `subs` neighbouring lanes a group.
-template <class Join> __device__ __forceinline__ void sum_given(const FlowParams &p, FlowShared &s, int b, Join &&join) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s.before = atomicAdd(p.state + 2 + b, 1u);
-    __syncthreads();
-    if (s.before != (uint32_t)p.pieces - 1) return;
-    __threadfence();
-    constexpr int subs = 8;
-    for (int g = threadIdx.x / subs; g < (p.g.G + kFlowThreads / subs - 1) / (kFlowThreads / subs) * (kFlowThreads / subs); g += kFlowThreads / subs)
-        join(g, (int)threadIdx.x % subs, subs);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) st_release(p.state + 2 + p.g.B + b, 1u);
-}
-__device__ __forceinline__ void wait_joined(const FlowParams &p, int b) {
-    if (threadIdx.x == 0) {
-        uint32_t k = 0;
-        while (ld_acquire(p.state + 2 + p.g.B + b) == 0 && ++k < kFlowWaitLimit) __nanosleep(100);
-        if (k >= kFlowWaitLimit && p.status) *p.status = 1;
-    }
-    __syncthreads();
-}
+// ------------------------------------------------------------- statistics --
 template <int subs> __device__ __forceinline__ float sub_sum(float v) {
 #pragma unroll
     for (int o = subs / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -416,10 +342,10 @@ template <int E> __device__ __forceinline__ void lane_stats(int n, const float (
 }
 // The lanes' statistics of each of `width` channels ([lanes, width]) joined
 // about their common mean, in place of lane 0's; `rows` in all.
-__device__ __forceinline__ void join_lanes(float *mean, float *m2, int width, int lanes, int rows) {
+template <int THREADS> __device__ __forceinline__ void join_lanes(float *mean, float *m2, int width, int lanes, int rows) {
     const int used = min(lanes, rows);
     const float all = 1.f / (float)max(rows, 1);
-    for (int c = threadIdx.x; c < width; c += blockDim.x) {
+    for (int c = threadIdx.x; c < width; c += THREADS) {
         const float ref = mean[c];
         float s = 0.f, q = 0.f;
 #pragma unroll 4
@@ -435,373 +361,23 @@ __device__ __forceinline__ void join_lanes(float *mean, float *m2, int width, in
     }
 }
 
-template <typename T, int E, int ACT, bool KEEP>
-__global__ void __launch_bounds__(kFlowThreads, 2) gn_fwd_flow(const FlowParams p) {
-    extern __shared__ float sm[];
-    __shared__ FlowShared fs;
-    float *lane_mean = sm, *lane_m2 = sm + kFlowThreads * E;
-    float2 *acc = reinterpret_cast<float2 *>(sm + 2 * kFlowThreads * E);  // [G]: groups over several tiles; then the statistics
-    const GnParams &g = p.g;
-    pdl_wait();
-    pdl_trigger();
-    const int CC = g.C / E;
-    const Cut cut(CC);
-    const int64_t all = (int64_t)g.B * p.pieces;
-    for (;;) {
-        const int64_t ticket = next_ticket(p, fs);
-        if (ticket >= p.tickets) return;
-        const bool normalise = ticket & 1;
-        const int64_t item = (ticket >> 1) - (normalise ? p.pieces + p.lag : 0);
-        if (item < 0 || item >= all) continue;
-        const int b = (int)(item / p.pieces), piece = (int)(item - (int64_t)b * p.pieces);
-        const int64_t r0 = (int64_t)piece * g.rows, first = (int64_t)b * g.S + r0;
-        const int rows = (int)min((int64_t)g.rows, g.S - r0);
-        const T *x = static_cast<const T *>(g.x) + first * g.C;
-        const int64_t step = (int64_t)cut.lanes * g.C;
-        if (!normalise) {
-            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-                const int cc = t0 + cut.col;
-                const int n = cut.in && cc < CC && cut.lane < rows ? (rows - cut.lane + cut.lanes - 1) / cut.lanes : 0;
-                float K[E], s1[E], s2[E];
-                fill_v(0.f, K);
-                fill_v(0.f, s1);
-                fill_v(0.f, s2);
-                const T *px = x + (int64_t)cut.lane * g.C + cc * E;
-                if (n > 0) {
-                    Vals<T, E> c;
-                    c.load(px);
-                    c.get(K);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) K[i] = -K[i];
-                }
-                constexpr int BATCH = 8;
-                int k = 1;
-                for (; k + BATCH <= n; k += BATCH) {
-                    Vals<T, E> c[BATCH];
-#pragma unroll
-                    for (int q = 0; q < BATCH; ++q) c[q].load(px + (k + q) * step);
-#pragma unroll
-                    for (int q = 0; q < BATCH; ++q) {
-                        float v[E];
-                        c[q].get(v);
-                        gn_deviate(v, K, s1, s2);
-                    }
-                }
-#pragma unroll 4
-                for (; k < n; ++k) {
-                    Vals<T, E> c;
-                    c.load(px + k * step);
-                    float v[E];
-                    c.get(v);
-                    gn_deviate(v, K, s1, s2);
-                }
-                lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
-                __syncthreads();
-                join_lanes(lane_mean, lane_m2, cut.cols * E, cut.lanes, rows);
-                __syncthreads();
-                // a warp a group: this tile's channels, joined with the tiles before
-                const int c0 = t0 * E, c1 = min((t0 + cut.cols) * E, g.C);
-                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-                for (int k2 = c0 / g.cg + warp; k2 * g.cg < c1; k2 += kFlowThreads / 32) {
-                    const int lo = max(k2 * g.cg, c0), w = min((k2 + 1) * g.cg, c1) - lo;
-                    const float *cm = lane_mean + (lo - c0), *cq = lane_m2 + (lo - c0);
-                    const float ref = cm[0];
-                    float s = 0.f, m2 = 0.f;
-                    for (int c = wl; c < w; c += 32) s += cm[c] - ref;
-                    s = sub_sum<32>(s);
-                    float m = ref + s / (float)w;
-                    for (int c = wl; c < w; c += 32) {
-                        const float d = cm[c] - m;
-                        m2 += fmaf((float)rows * d, d, cq[c]);
-                    }
-                    m2 = sub_sum<32>(m2);
-                    if (wl == 0) {
-                        const float cnt = (float)rows * (float)w;
-                        if (lo > k2 * g.cg) {
-                            const float2 a = acc[k2];
-                            const float na = (float)rows * (float)(lo - k2 * g.cg), d = m - a.x, share = cnt / (na + cnt);
-                            m = a.x + d * share;
-                            m2 = a.y + m2 + d * d * (na * share);
-                        }
-                        if (lo + w < (k2 + 1) * g.cg)
-                            acc[k2] = make_float2(m, m2);
-                        else
-                            p.part[item * g.G + k2] = make_float2(m, m2);
-                    }
-                }
-                __syncthreads();
-            }
-            sum_given(p, fs, b, [&](int k, int sub, int subs) {
-                const bool in = k < g.G;
-                const float2 *part = p.part + (int64_t)b * p.pieces * g.G + k;
-                const float n = (float)g.S * (float)g.cg;
-                auto count = [&](int i) { return (float)min((int64_t)g.rows, g.S - (int64_t)i * g.rows) * (float)g.cg; };
-                const float ref = in ? __ldcg(part).x : 0.f;
-                float s = 0.f, m2 = 0.f;
-                if (in) {
-#pragma unroll 8
-                    for (int i = sub; i < p.pieces; i += subs) s += count(i) * (__ldcg(part + (int64_t)i * g.G).x - ref);
-                }
-                const float m = ref + sub_sum<8>(s) / n;
-                if (in) {
-#pragma unroll 8
-                    for (int i = sub; i < p.pieces; i += subs) {
-                        const float2 a = __ldcg(part + (int64_t)i * g.G);
-                        const float d = a.x - m;
-                        m2 += fmaf(count(i) * d, d, a.y);
-                    }
-                }
-                m2 = sub_sum<8>(m2);
-                if (in && sub == 0) {
-                    const float r = 1.f / sqrtf(m2 / n + g.eps);
-                    p.stat[(int64_t)b * g.G + k] = make_float2(-m, r);
-                    g.mean[(int64_t)b * g.G + k] = m;
-                    g.rstd[(int64_t)b * g.G + k] = r;
-                }
-            });
-            continue;
-        }
-        wait_joined(p, b);
-        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)b * g.G + k);
-        __syncthreads();
-        T *y = static_cast<T *>(g.out) + first * g.C;
-        for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-            const int cc = t0 + cut.col;
-            if (!cut.in || cc >= CC) continue;
-            float minus_mean[E], f[E], gamma[E], beta[E];
-            groups_v(acc, cc * E, g.cg, g.magic, minus_mean, f);
-            params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
-            params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
-            mul_v(f, gamma, f);
-            constexpr int BATCH = 4;
-            for (int r = cut.lane; r < rows; r += BATCH * cut.lanes) {
-                Vals<T, E> c[BATCH];
-#pragma unroll
-                for (int q = 0; q < BATCH; ++q)
-                    if (r + q * cut.lanes < rows) c[q].load_last(x + (int64_t)(r + q * cut.lanes) * g.C + cc * E);
-#pragma unroll
-                for (int q = 0; q < BATCH; ++q) {
-                    const int rr = r + q * cut.lanes;
-                    if (rr < rows) {
-                        float v[E], z[E];
-                        c[q].get(v);
-                        gn_value<T, ACT>(v, minus_mean, f, beta, z);
-                        Vals<T, E> o;
-                        o.set(z);
-                        o.store(y + (int64_t)rr * g.C + cc * E);
-                        if constexpr (KEEP)
-                            keep_chunk<T>(c[q].w, true, block_lanes<T>(), g.codes + (first + rr) * g.C + cc * E,
-                                             g.scales + (first + rr) * (g.C / kBlock8) + cc * E / kBlock8);
-                    }
-                }
-            }
-        }
-    }
+// E values from shared memory.
+template <typename T, int E> __device__ __forceinline__ Vals<T, E> held_chunk(const uint8_t *p) {
+    Vals<T, E> c;
+    c.w = *reinterpret_cast<const typename Vals<T, E>::W *>(p);
+    return c;
 }
-
-template <typename T, int E, int ACT, bool KEPT>
-__global__ void __launch_bounds__(kFlowThreads, 2) gn_bwd_flow(const FlowParams p) {
-    extern __shared__ float sm[];
-    __shared__ FlowShared fs;
-    float *lane_a = sm, *lane_s = sm + kFlowThreads * E;
-    float2 *acc = reinterpret_cast<float2 *>(sm + 2 * kFlowThreads * E);  // [G]
-    const GnParams &g = p.g;
-    pdl_wait();
-    pdl_trigger();
-    const int CC = g.C / E;
-    const Cut cut(CC);
-    const int64_t all = (int64_t)g.B * p.pieces;
-    constexpr int BATCH = 4;
-    for (;;) {
-        const int64_t ticket = next_ticket(p, fs);
-        if (ticket >= p.tickets) return;
-        const bool normalise = ticket & 1;
-        const int64_t item = (ticket >> 1) - (normalise ? p.pieces + p.lag : 0);
-        if (item < 0 || item >= all) continue;
-        const int b = (int)(item / p.pieces), piece = (int)(item - (int64_t)b * p.pieces);
-        const int64_t r0 = (int64_t)piece * g.rows, first = (int64_t)b * g.S + r0;
-        const int rows = (int)min((int64_t)g.rows, g.S - r0);
-        const T *dy = static_cast<const T *>(g.dy) + first * g.C;
-        auto constants = [&](int cc, float (&minus_mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
-            const int64_t at = (int64_t)b * g.G;
-            auto group = [&](int c) { return g.magic ? (int)__umulhi((uint32_t)c, g.magic) : c; };
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int k = group(cc * E + i);
-                minus_mean[i] = -g.mean[at + k];
-                rstd[i] = g.rstd[at + k];
-            }
-            params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
-            params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
-        };
-        if (!normalise) {
-            float *out = g.parts ? g.parts + item * 2 * g.C : nullptr;
-            for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-                const int cc = t0 + cut.col;
-                float a[E], s[E];
-                fill_v(0.f, a);
-                fill_v(0.f, s);
-                if (cut.in && cc < CC) {
-                    float minus_mean[E], rstd[E], gamma[E], beta[E];
-                    constants(cc, minus_mean, rstd, gamma, beta);
-                    for (int r = cut.lane; r < rows; r += BATCH * cut.lanes) {
-                        XLoad<T, E, KEPT> x[BATCH];
-                        Vals<T, E> d[BATCH];
-#pragma unroll
-                        for (int q = 0; q < BATCH; ++q) {
-                            const int rr = r + q * cut.lanes;
-                            if (rr < rows) {
-                                x[q].load(g, first + rr, cc * E);
-                                d[q].load(dy + (int64_t)rr * g.C + cc * E);
-                            }
-                        }
-#pragma unroll
-                        for (int q = 0; q < BATCH; ++q)
-                            if (r + q * cut.lanes < rows) {
-                                float v[E], u[E];
-                                x[q].c.get(v);
-                                d[q].get(u);
-                                gn_slope<T, ACT>(v, u, minus_mean, rstd, gamma, beta);
-                                fma_v(u, v, a, a);
-                                add_v(s, u, s);
-                            }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    lane_a[threadIdx.x * E + i] = a[i];
-                    lane_s[threadIdx.x * E + i] = s[i];
-                }
-                __syncthreads();
-                const int width = cut.cols * E, c0 = t0 * E, c1 = min(c0 + width, g.C);
-                for (int c = threadIdx.x; c < c1 - c0; c += kFlowThreads) {
-                    float ta = lane_a[c], ts = lane_s[c];
-#pragma unroll 4
-                    for (int l = 1; l < cut.lanes; ++l) {
-                        ta += lane_a[l * width + c];
-                        ts += lane_s[l * width + c];
-                    }
-                    if (out) {
-                        out[c0 + c] = ta;
-                        out[g.C + c0 + c] = ts;
-                    }
-                    const float ga = param<T>(g.gamma, g.w32, c0 + c, 1.f);
-                    lane_a[c] = ta * ga;
-                    lane_s[c] = ts * ga;
-                }
-                __syncthreads();
-                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-                for (int k = c0 / g.cg + warp; k * g.cg < c1; k += kFlowThreads / 32) {
-                    const int lo = max(k * g.cg, c0), hi = min((k + 1) * g.cg, c1);
-                    float2 m = make_float2(0.f, 0.f);
-                    for (int c = lo + wl; c < hi; c += 32) m = add2(m, make_float2(lane_s[c - c0], lane_a[c - c0]));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
-                    if (wl == 0) {
-                        if (lo > k * g.cg) m = add2(acc[k], m);
-                        if (hi < (k + 1) * g.cg)
-                            acc[k] = m;
-                        else
-                            p.part[item * g.G + k] = m;
-                    }
-                }
-                __syncthreads();
-            }
-            sum_given(p, fs, b, [&](int k, int sub, int subs) {
-                const bool in = k < g.G;
-                const float2 *part = p.part + (int64_t)b * p.pieces * g.G + k;
-                float2 m = make_float2(0.f, 0.f);
-                if (in) {
-#pragma unroll 8
-                    for (int i = sub; i < p.pieces; i += subs) m = add2(m, __ldcg(part + (int64_t)i * g.G));
-                }
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
-                const float n = (float)g.S * (float)g.cg;
-                if (in && sub == 0) p.stat[(int64_t)b * g.G + k] = make_float2(-m.x / n, -m.y / n);
-            });
-            continue;
-        }
-        wait_joined(p, b);
-        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)b * g.G + k);
-        __syncthreads();
-        T *dx = static_cast<T *>(g.out) + first * g.C;
-        for (int t0 = 0; t0 < CC; t0 += cut.cols) {
-            const int cc = t0 + cut.col;
-            if (!cut.in || cc >= CC) continue;
-            float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
-            constants(cc, minus_mean, rstd, gamma, beta);
-            groups_v(acc, cc * E, g.cg, g.magic, m1, m2);
-            constexpr int HALF = 2;
-            for (int r = cut.lane; r < rows; r += HALF * cut.lanes) {
-                XLoad<T, E, KEPT> x[HALF];
-                Vals<T, E> d[HALF];
-#pragma unroll
-                for (int q = 0; q < HALF; ++q) {
-                    const int rr = r + q * cut.lanes;
-                    if (rr < rows) {
-                        x[q].load(g, first + rr, cc * E);
-                        d[q].load_last(dy + (int64_t)rr * g.C + cc * E);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < HALF; ++q) {
-                    const int rr = r + q * cut.lanes;
-                    if (rr < rows) {
-                        float v[E], u[E];
-                        x[q].c.get(v);
-                        d[q].get(u);
-                        gn_slope<T, ACT>(v, u, minus_mean, rstd, gamma, beta);
-                        gn_dx(v, u, rstd, gamma, m1, m2);
-                        Vals<T, E> o;
-                        o.set(u);
-                        o.store(dx + (int64_t)rr * g.C + cc * E);
-                    }
-                }
-            }
-        }
-    }
-}
-
-// Many rows of sums folded into gridDim.y: row i of the result is the sum of
-// rows [i n / gridDim.y, (i + 1) n / gridDim.y), in order.
-static __global__ void __launch_bounds__(256) gn_fold(const float *in, float *out, int64_t n, int width) {
-    pdl_wait();
-    pdl_trigger();
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    const int64_t i0 = n * blockIdx.y / gridDim.y, i1 = n * (blockIdx.y + 1) / gridDim.y;
-    if (c >= width) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int64_t i = i0; i < i1; ++i) s += in[i * width + c];
-    out[(int64_t)blockIdx.y * width + c] = s;
-}
-
-// ---------------------------------------------------------------- kernels --
-
-// (keeping x in the same pass: whole 16-byte chunks only)
-template <typename T, int E, int ACT> static const void *gn_flow_fwd(bool kept) {
-    if constexpr (E > 1) {
-        if (kept) return (const void *)gn_fwd_flow<T, E, ACT, true>;
-    }
-    return (const void *)gn_fwd_flow<T, E, ACT, false>;
-}
-template <typename T, int E> static const void *gn_flow_e(bool backward, int act, bool kept) {
-#define FLOW(A)                                                                                              \
-    (!backward ? gn_flow_fwd<T, E, A>(kept)                                                                  \
-     : kept    ? (const void *)gn_bwd_flow<T, E, A, true>                                                    \
-               : (const void *)gn_bwd_flow<T, E, A, false>)
-    return act == kActSilu ? FLOW(kActSilu) : act == kActGelu ? FLOW(kActGelu) : FLOW(kActNone);
-#undef FLOW
-}
-// A kernel by 16-byte chunks (wide) or by single values.
-template <typename T> static const void *gn_flow_t(bool backward, bool wide, int act, bool kept) {
-    return wide ? gn_flow_e<T, Elem<T>::E>(backward, act, kept) : gn_flow_e<T, 1>(backward, act, kept);
+template <typename T, int E> __device__ __forceinline__ void held_values(const uint8_t *p, float (&v)[E]) { held_chunk<T, E>(p).get(v); }
+template <int E> __device__ __forceinline__ void held_codes(const uint8_t *p, uint32_t b, float (&v)[E]) {
+    Kept<E> k;
+    k.w = *reinterpret_cast<const typename Kept<E>::W *>(p);
+    k.b = b;
+    k.get(v);
 }
 
 #define GN_DECLARE(suf)                                                          \
-    const void *gn_flow_##suf(bool backward, bool wide, int act, bool kept);     \
-    const void *gn_held_##suf(bool backward, bool wide, int act, bool kept);
+    const void *gn_flow_##suf(bool backward, int chunk, int act, bool kept);     \
+    const void *gn_held_##suf(bool backward, int chunk, int act, bool kept);
 GN_DECLARE(f32)
 GN_DECLARE(bf16)
 GN_DECLARE(f16)

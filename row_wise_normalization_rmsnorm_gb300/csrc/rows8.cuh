@@ -69,61 +69,67 @@ __device__ __forceinline__ float decode8(int8_t c) { return (float)c; }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// The bits of a 16-byte chunk's largest magnitude, combined over the 32 / E
-// neighbouring lanes that hold its block. 16-bit types are compared as pairs
-// of 16-bit numbers (magnitudes are in the order of their bits).
+// The bits of a chunk's largest magnitude (E values in w), combined over the
+// 32 / E neighbouring lanes that hold its block. 16-bit types are compared as
+// pairs of 16-bit numbers (magnitudes are in the order of their bits).
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-template <typename T> __device__ __forceinline__ uint32_t block_top(const uint4 &c, uint32_t lanes) {
-    constexpr int L = kBlock8 / Elem<T>::E;
-    if constexpr (sizeof(T) == 2) {
-        constexpr uint32_t mag = 0x7fff7fffu;
-        uint32_t m = max_u16x2(max_u16x2(c.x & mag, c.y & mag), max_u16x2(c.z & mag, c.w & mag));
+template <typename T, int E> __device__ __forceinline__ uint32_t block_top(const uint32_t *w, uint32_t lanes) {
+    constexpr int L = kBlock8 / E, N = E * (int)sizeof(T) / 4;
+    constexpr uint32_t mag = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+    auto most = [](uint32_t a, uint32_t b) { return sizeof(T) == 2 ? max_u16x2(a, b) : max(a, b); };
+    uint32_t m = w[0] & mag;
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(lanes, m, o));
-        m = max(m & 0xffffu, m >> 16);
-        if constexpr (std::is_same<T, __half>::value)
-            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
-        else
-            return m << 16;
-    } else {
-        constexpr uint32_t mag = 0x7fffffffu;
-        uint32_t m = max(max(c.x & mag, c.y & mag), max(c.z & mag, c.w & mag));
+    for (int i = 1; i < N; ++i) m = most(m, w[i] & mag);
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(lanes, m, o));
-        return m;
-    }
+    for (int o = 1; o < L; o <<= 1) m = most(m, __shfl_xor_sync(lanes, m, o));
+    if constexpr (sizeof(T) == 4) return m;
+    m = max(m & 0xffffu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    return m << 16;
 }
 // The lanes of this one's block.
-template <typename T> __device__ __forceinline__ uint32_t block_lanes() {
-    constexpr int L = kBlock8 / Elem<T>::E;
+template <int E> __device__ __forceinline__ uint32_t block_lanes() {
+    constexpr int L = kBlock8 / E;
     return ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
 }
 
-// The codes of a 16-byte chunk and its block's scale. The lanes of a block
-// call this together; one whose chunk lies behind the row's end (`here`
-// false, the chunk zeros) writes nothing. `lanes`: those of the block, or all
-// 32 where the whole warp is here.
-template <typename T>
-__device__ __forceinline__ void keep_chunk(const uint4 &raw, bool here, uint32_t lanes, uint8_t *codes, uint8_t *scale) {
-    constexpr int NP = Elem<T>::NP, L = kBlock8 / Elem<T>::E;
-    const uint32_t b = scale8<T>(block_top<T>(raw, lanes));
+// The codes of a chunk of E values (8 or 4, in w) and its block's scale. The
+// lanes of a block call this together; one whose chunk lies behind the row's
+// end (`here` false, the chunk zeros) writes nothing. `lanes`: those of the
+// block, or all 32 where the whole warp is here.
+template <typename T, int E>
+__device__ __forceinline__ void keep_chunk(const uint32_t *w, bool here, uint32_t lanes, uint8_t *codes, uint8_t *scale) {
+    const uint32_t b = scale8<T>(block_top<T, E>(w, lanes));
     if (!here) return;
     const float f = to_codes8(b);
-    float2 v[NP];
-    unpack<T>(raw, v);
+    float2 v[E / 2];
+#pragma unroll
+    for (int q = 0; q < E / 2; ++q) {
+        if constexpr (sizeof(T) == 4)
+            v[q] = make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+        else if constexpr (std::is_same<T, __half>::value)
+            v[q] = f16x2_to_f2(w[q]);
+        else
+            v[q] = bf16x2_to_f2(w[q]);
+    }
     if (b == MostScale<T>::b) {
 #pragma unroll
-        for (int q = 0; q < NP; ++q) v[q] = make_float2(held8(v[q].x, f), held8(v[q].y, f));
+        for (int q = 0; q < E / 2; ++q) v[q] = make_float2(held8(v[q].x, f), held8(v[q].y, f));
     }
-    if constexpr (NP == 4)
+    if constexpr (E == 8)
         *reinterpret_cast<uint2 *>(codes) = make_uint2(codes8x4(v[0], v[1], f), codes8x4(v[2], v[3], f));
     else
         *reinterpret_cast<uint32_t *>(codes) = codes8x4(v[0], v[1], f);
-    if ((threadIdx.x & (L - 1)) == 0) *scale = (uint8_t)b;
+    if ((threadIdx.x & (kBlock8 / E - 1)) == 0) *scale = (uint8_t)b;
+}
+template <typename T>
+__device__ __forceinline__ void keep_chunk(const uint4 &c, bool here, uint32_t lanes, uint8_t *codes, uint8_t *scale) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    keep_chunk<T, Elem<T>::E>(w, here, lanes, codes, scale);
 }
 
 }  // namespace rmsn

@@ -327,7 +327,8 @@ def gn_forward(x, gamma, beta, G, act, eps):
 GN_SHAPES = [  # B, places, C, G
     (1, (64,), 1280, 32), (2, (8, 8), 320, 32), (3, (1001,), 90, 9), (2, (17, 3), 64, 64), (1, (1,), 64, 4), (1, (1,), 8, 8),
     (5, (7,), 33, 11), (2, (300,), 128, 1), (1, (4096,), 32, 32), (2, (50,), 5000, 5), (1, (9,), 5120, 1280), (1, (40,), 1025, 1),
-    (2, (2000,), 960, 32), (300, (5,), 16, 4), (1, (20000,), 40, 2), (2, (3,), 20480, 10),
+    (2, (2000,), 960, 32), (300, (5,), 16, 4), (1, (20000,), 40, 2), (2, (3,), 8000, 10), (1, (70,), 8192, 1), (3, (30000,), 12, 4),
+    (2, (9001,), 321, 3),
 ]
 
 

@@ -67,8 +67,8 @@ GN = {"x": A, "gamma": A, "beta": A, "y": A, "mean": A, "rstd": A, "codes": A, "
 
 @pytest.mark.parametrize("bad", [{"x": None}, {"y": None}, {"mean": None}, {"rstd": None}, {"codes": None}, {"scales": None},
                                  {"x": A + 1}, {"y": A + 1}, {"gamma": A + 1}, {"beta": A + 1}, {"mean": A + 2}, {"B": -1}, {"S": -1},
-                                 {"C": 0}, {"C": 65544, "G": 8}, {"G": 0}, {"G": 7}, {"G": 65}, {"act": 3}, {"act": -1}, {"dt": 3},
-                                 {"eps": -1.0}, {"eps": math.inf}, {"B": 2 ** 31}, {"B": 2 ** 30, "S": 2 ** 30, "C": 65536}])
+                                 {"C": 0}, {"C": 8200, "G": 8}, {"G": 0}, {"G": 7}, {"G": 65}, {"act": 3}, {"act": -1}, {"dt": 3},
+                                 {"eps": -1.0}, {"eps": math.inf}, {"B": 2 ** 31}, {"B": 2 ** 30, "S": 2 ** 30, "C": 8192}])
 def test_groupnorm_forward_refuses(rn, bad):
     assert call(rn, "groupnorm_fwd", GN, bad) == INVALID
 
