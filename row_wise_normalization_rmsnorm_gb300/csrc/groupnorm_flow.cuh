@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(cons
     }
     const int CC = g.C / E;
     const Cut cut(CC, kFlowThreads);
+    const uint32_t ring0 = smem_u32(ring);
     FlowStages at{0, 0u, false};
     for (int64_t ticket; (ticket = at.wait(fs)) >= 0;) {
         const FlowPiece f(p, ticket);
@@ -209,22 +210,10 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(cons
                 int n = 0;
                 for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
                     if (r0 > 0) at.wait(fs);
-                    const uint8_t *rows = ring + (size_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + (f.first + r0) * pitch) + cc * (E * sizeof(T));
-                    const int end = in ? min(p.stage_rows, f.rows - r0) : 0;
-                    int r = cut.lane;
-                    if (n == 0 && r < end) {
-                        held_values<T, E>(rows + (size_t)r * pitch, K);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) K[i] = -K[i];
-                        r += cut.lanes;
-                        n = 1;
-                    }
-#pragma unroll 4
-                    for (; r < end; r += cut.lanes, ++n) {
-                        float v[E];
-                        held_values<T, E>(rows + (size_t)r * pitch, v);
-                        gn_deviate(v, K, s1, s2);
-                    }
+                    const uint32_t rows = ring0 + (uint32_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + (f.first + r0) * pitch);
+                    const int more = in ? rows_of_lane(min(p.stage_rows, f.rows - r0), cut.lane, cut.lanes) : 0;
+                    sum_rows<T, E>(rows + (uint32_t)cut.lane * pitch + cc * (E * sizeof(T)), more, (uint32_t)cut.lanes * pitch, n, K, s1, s2);
+                    n += more;
                     if (t0 + cut.cols >= CC) at.release(p, fs);
                 }
                 lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
@@ -296,32 +285,39 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(cons
         wait_joined(p, f.b);
         for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)f.b * g.G + k);
         flow_sync();
+        float minus_mean[E], f_[E], beta[E];
+        auto constants = [&](int cc) {
+            float gamma[E];
+            groups_v(acc, cc * E, g.cg, g.magic, minus_mean, f_);
+            params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
+            params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
+            mul_v(f_, gamma, f_);
+        };
         for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
             if (r0 > 0) at.wait(fs);
             const int64_t first = f.first + r0;
-            const uint8_t *stage = ring + (size_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + first * pitch);
+            const uint32_t stage = ring0 + (uint32_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + first * pitch);
             const int rows = min(p.stage_rows, f.rows - r0);
-            T *y = static_cast<T *>(g.out) + first * g.C;
             for (int t0 = 0; t0 < CC; t0 += cut.cols) {
                 const int cc = t0 + cut.col;
                 if (!cut.in || cc >= CC) continue;
-                float minus_mean[E], f_[E], gamma[E], beta[E];
-                groups_v(acc, cc * E, g.cg, g.magic, minus_mean, f_);
-                params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
-                params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
-                mul_v(f_, gamma, f_);
+                if (r0 == 0 || CC > cut.cols) constants(cc);
+                uint32_t from = stage + (uint32_t)cut.lane * pitch + cc * (E * sizeof(T));
+                const uint32_t step = (uint32_t)cut.lanes * pitch;
+                const int64_t out_step = (int64_t)cut.lanes * g.C;
+                int64_t row = first + cut.lane;
+                T *out = static_cast<T *>(g.out) + row * g.C + cc * E;
 #pragma unroll 2
-                for (int r = cut.lane; r < rows; r += cut.lanes) {
+                for (int n = rows_of_lane(rows, cut.lane, cut.lanes); n > 0; --n, from += step, out += out_step, row += cut.lanes) {
                     float v[E], z[E];
-                    const Vals<T, E> raw = held_chunk<T, E>(stage + (size_t)r * pitch + cc * (E * sizeof(T)));
+                    const Vals<T, E> raw = held_chunk<T, E>(from);
                     raw.get(v);
                     gn_value<T, ACT>(v, minus_mean, f_, beta, z);
                     Vals<T, E> o;
                     o.set(z);
-                    o.store(y + (int64_t)r * g.C + cc * E);
+                    o.store(out);
                     if constexpr (KEEP)
-                        keep_chunk<T, E>(raw.u, true, block_lanes<E>(), g.codes + (first + r) * g.C + cc * E,
-                                         g.scales + (first + r) * (g.C / kBlock8) + cc * E / kBlock8);
+                        keep_chunk<T, E>(raw.u, true, block_lanes<E>(), g.codes + row * g.C + cc * E, g.scales + row * (g.C / kBlock8) + cc * E / kBlock8);
                 }
             }
             at.release(p, fs);
@@ -358,22 +354,27 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
     }
     const int CC = g.C / E;
     const Cut cut(CC, kFlowThreads);
-    // where a stage's rows begin
-    struct Rows {
-        const uint8_t *x, *dy, *sc;
+    const uint32_t ring0 = smem_u32(ring);
+    // A chunk column's places in a stage, from row to row.
+    struct Walk {
+        uint32_t x, d, s;
     };
-    auto stage_rows_at = [&](int stage, int64_t first) {
-        const uint8_t *s = ring + (size_t)stage * p.stage_bytes;
-        return Rows{s + addr_mod16(xsrc + first * xpitch), s + p.offset[1] + addr_mod16(static_cast<const char *>(g.dy) + first * pitch),
-                    KEPT ? s + p.offset[2] + addr_mod16(g.scales_in + first * spitch) : nullptr};
+    auto walk = [&](int stage, int64_t first, int cc) {
+        const uint32_t at = ring0 + (uint32_t)stage * p.stage_bytes;
+        return Walk{at + addr_mod16(xsrc + first * xpitch) + (uint32_t)cut.lane * xpitch + cc * (E * XE),
+                    at + p.offset[1] + addr_mod16(static_cast<const char *>(g.dy) + first * pitch) + (uint32_t)cut.lane * pitch + cc * (E * (uint32_t)sizeof(T)),
+                    KEPT ? at + p.offset[2] + addr_mod16(g.scales_in + first * spitch) + (uint32_t)cut.lane * spitch + cc * E / kBlock8 : 0u};
     };
-    auto chunk = [&](const Rows &s, int r, int cc, const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E],
-                     const float (&beta)[E], float (&xhat)[E], float (&u)[E]) {
+    const Walk step{(uint32_t)cut.lanes * xpitch, (uint32_t)cut.lanes * pitch, (uint32_t)cut.lanes * spitch};
+    auto chunk = [&](Walk &w, const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E],
+                     float (&xhat)[E], float (&u)[E]) {
         if constexpr (KEPT)
-            held_codes<E>(s.x + (size_t)r * xpitch + cc * E, s.sc[(size_t)r * spitch + cc * E / kBlock8], xhat);
+            held_codes<E>(w.x, held_byte(w.s), xhat);
         else
-            held_values<T, E>(s.x + (size_t)r * xpitch + cc * (E * XE), xhat);
-        held_values<T, E>(s.dy + (size_t)r * pitch + cc * (E * sizeof(T)), u);
+            held_values<T, E>(w.x, xhat);
+        held_values<T, E>(w.d, u);
+        w.x += step.x, w.d += step.d;
+        if constexpr (KEPT) w.s += step.s;
         gn_slope<T, ACT>(xhat, u, minus_mean, rstd, gamma, beta);
     };
     FlowStages at{0, 0u, false};
@@ -408,12 +409,12 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
                 if (in) constants(cc, minus_mean, rstd, gamma, beta);
                 for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
                     if (r0 > 0) at.wait(fs);
-                    const Rows rows = stage_rows_at(at.stage, f.first + r0);
-                    const int end = in ? min(p.stage_rows, f.rows - r0) : 0;
+                    Walk w = walk(at.stage, f.first + r0, cc);
+                    const int n = in ? rows_of_lane(min(p.stage_rows, f.rows - r0), cut.lane, cut.lanes) : 0;
 #pragma unroll 2
-                    for (int r = cut.lane; r < end; r += cut.lanes) {
+                    for (int k = 0; k < n; ++k) {
                         float xhat[E], u[E];
-                        chunk(rows, r, cc, minus_mean, rstd, gamma, beta, xhat, u);
+                        chunk(w, minus_mean, rstd, gamma, beta, xhat, u);
                         fma_v(u, xhat, a, a);
                         add_v(s, u, s);
                     }
@@ -477,26 +478,29 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
         wait_joined(p, f.b);
         for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)f.b * g.G + k);
         flow_sync();
+        float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
         for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
             if (r0 > 0) at.wait(fs);
             const int64_t first = f.first + r0;
-            const Rows s = stage_rows_at(at.stage, first);
             const int rows = min(p.stage_rows, f.rows - r0);
-            T *dx = static_cast<T *>(g.out) + first * g.C;
             for (int t0 = 0; t0 < CC; t0 += cut.cols) {
                 const int cc = t0 + cut.col;
                 if (!cut.in || cc >= CC) continue;
-                float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
-                constants(cc, minus_mean, rstd, gamma, beta);
-                groups_v(acc, cc * E, g.cg, g.magic, m1, m2);
-#pragma unroll 1
-                for (int r = cut.lane; r < rows; r += cut.lanes) {
+                if (r0 == 0 || CC > cut.cols) {
+                    constants(cc, minus_mean, rstd, gamma, beta);
+                    groups_v(acc, cc * E, g.cg, g.magic, m1, m2);
+                }
+                Walk w = walk(at.stage, first, cc);
+                const int64_t out_step = (int64_t)cut.lanes * g.C;
+                T *to = static_cast<T *>(g.out) + (first + cut.lane) * g.C + cc * E;
+#pragma unroll(E == 8 ? 1 : 2)
+                for (int n = rows_of_lane(rows, cut.lane, cut.lanes); n > 0; --n, to += out_step) {
                     float xhat[E], u[E];
-                    chunk(s, r, cc, minus_mean, rstd, gamma, beta, xhat, u);
+                    chunk(w, minus_mean, rstd, gamma, beta, xhat, u);
                     gn_dx(xhat, u, rstd, gamma, m1, m2);
                     Vals<T, E> o;
                     o.set(u);
-                    o.store(dx + (int64_t)r * g.C + cc * E);
+                    o.store(to);
                 }
             }
             at.release(p, fs);

@@ -85,9 +85,7 @@ __device__ __forceinline__ void copies_wait(int n) {
 }
 static_assert(kHeldStages == 4, "copies_wait");
 
-// This thread's rows of a chunk column: lane, lane + lanes, ..., n of them;
-// those of piece i end before the end_of(n, i)-th.
-__device__ __forceinline__ int rows_of_lane(int rows, int lane, int lanes) { return lane < rows ? (rows - lane + lanes - 1) / lanes : 0; }
+// Of a thread's n rows of a chunk column, those of pieces 0 .. i.
 __device__ __forceinline__ int end_of(int n, int i) { return (n * (i + 1) + kHeldStages - 1) / kHeldStages; }
 
 struct HeldPlace {
@@ -140,7 +138,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
     pdl_trigger();
     const int CW = p.W / E;
     const Cut cut(CW, kHeldThreads);
-    const uint8_t *rows = held + (E == 1 ? xs.off : 0u);
+    const uint32_t rows = smem_u32(held) + (E == 1 ? xs.off : 0u);
     const uint32_t pitch = (uint32_t)p.W * sizeof(T);
     if constexpr (E == 1) {
         if (threadIdx.x == 0)
@@ -166,28 +164,18 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
                 copies_commit();
             }
         }
-        int r = cut.lane;
-        for (int i = 0; i < kHeldStages; ++i) {
-            int end;
+        const uint32_t from = rows + (uint32_t)cut.lane * pitch + cc * CB, step = (uint32_t)cut.lanes * pitch;
+        for (int i = 0, k = 0; i < kHeldStages; ++i) {
+            int end;  // of this thread's rows
             if constexpr (E > 1) {
                 copies_wait(kHeldStages - 1 - i);
-                end = cut.lane + end_of(n, i) * cut.lanes;
+                end = end_of(n, i);
             } else {
                 if (!mbar_wait(&bar[i], 0, kHeldWaitLimit)) failed = true;
-                end = in ? xs.ready(i, at.rows) : 0;
+                end = in ? rows_of_lane(xs.ready(i, at.rows), cut.lane, cut.lanes) : 0;
             }
-            if (r == cut.lane && r < end) {
-                held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), K);
-#pragma unroll
-                for (int k = 0; k < E; ++k) K[k] = -K[k];
-                r += cut.lanes;
-            }
-#pragma unroll 4
-            for (; r < end; r += cut.lanes) {
-                float v[E];
-                held_values<T, E>(rows + (size_t)r * pitch + cc * (E * sizeof(T)), v);
-                gn_deviate(v, K, s1, s2);
-            }
+            sum_rows<T, E>(from + (uint32_t)k * step, end - k, step, k, K, s1, s2);
+            k = max(k, end);
         }
         lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
         __syncthreads();
@@ -251,17 +239,21 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
         params_v<T>(g.gamma, g.w32, at.c0 + cc * E, 1.f, gamma);
         params_v<T>(g.beta, g.w32, at.c0 + cc * E, 0.f, beta);
         mul_v(f, gamma, f);
+        uint32_t from = rows + (uint32_t)cut.lane * pitch + cc * CB;
+        const uint32_t step = (uint32_t)cut.lanes * pitch;
+        const int64_t out_step = (int64_t)cut.lanes * g.C;
+        T *out = y + (int64_t)cut.lane * g.C + cc * E;
+        int64_t row = at.first + cut.lane;
 #pragma unroll 2
-        for (int r = cut.lane; r < at.rows; r += cut.lanes) {
+        for (int n = rows_of_lane(at.rows, cut.lane, cut.lanes); n > 0; --n, from += step, out += out_step, row += cut.lanes) {
             float v[E], z[E];
-            const Vals<T, E> raw = held_chunk<T, E>(rows + (size_t)r * pitch + cc * CB);
+            const Vals<T, E> raw = held_chunk<T, E>(from);
             raw.get(v);
             gn_value<T, ACT>(v, minus_mean, f, beta, z);
             Vals<T, E> o;
             o.set(z);
-            o.store(y + (int64_t)r * g.C + cc * E);
+            o.store(out);
             if constexpr (KEEP) {
-                const int64_t row = at.first + r;
                 const int c = at.c0 + cc * E;
                 keep_chunk<T, E>(raw.u, true, block_lanes<E>(), g.codes + row * g.C + c, g.scales + row * (g.C / kBlock8) + c / kBlock8);
             }
@@ -304,7 +296,8 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
     pdl_trigger();
     const int CW = p.W / E;
     const Cut cut(CW, kHeldThreads);
-    const uint8_t *xrows = held + (E == 1 ? xs.off : 0u), *drows = held + p.slab[0] + (E == 1 ? ds.off : 0u);
+    const uint32_t xrows = smem_u32(held) + (E == 1 ? xs.off : 0u), drows = smem_u32(held) + p.slab[0] + (E == 1 ? ds.off : 0u),
+                   srows = smem_u32(held) + p.slab[0] + p.slab[1];
     const uint32_t xpitch = (uint32_t)p.W * XE, dpitch = (uint32_t)p.W * sizeof(T);
     auto copy_column = [&](int cc, int n) {  // a chunk column's rows of this lane
         const int64_t first = (at.first + cut.lane) * g.C + at.c0 + cc * E;
@@ -344,14 +337,25 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
         stat[k] = make_float2(-g.mean[i], g.rstd[i]);
     }
     __syncthreads();
+    // A chunk column's places in shared memory, from row to row.
+    struct Walk {
+        uint32_t x, d, s;
+    };
+    auto walk = [&](int r, int cc) {
+        return Walk{xrows + (uint32_t)r * xpitch + cc * (E * XE), drows + (uint32_t)r * dpitch + cc * CB,
+                    srows + (uint32_t)(r * nsc + (at.c0 + cc * E) / kBlock8 - sc0)};
+    };
+    const Walk step{(uint32_t)cut.lanes * xpitch, (uint32_t)cut.lanes * dpitch, (uint32_t)(cut.lanes * nsc)};
     // xhat and u of a chunk: what both passes form anew
-    auto chunk = [&](int r, int cc, const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E],
+    auto chunk = [&](Walk &w, const float (&minus_mean)[E], const float (&rstd)[E], const float (&gamma)[E], const float (&beta)[E],
                      float (&xhat)[E], float (&u)[E]) {
         if constexpr (KEPT)
-            held_codes<E>(xrows + (size_t)r * xpitch + cc * E, sc[r * nsc + (at.c0 + cc * E) / kBlock8 - sc0], xhat);
+            held_codes<E>(w.x, held_byte(w.s), xhat);
         else
-            held_values<T, E>(xrows + (size_t)r * xpitch + cc * (E * XE), xhat);
-        held_values<T, E>(drows + (size_t)r * dpitch + cc * (E * sizeof(T)), u);
+            held_values<T, E>(w.x, xhat);
+        held_values<T, E>(w.d, u);
+        w.x += step.x, w.d += step.d;
+        if constexpr (KEPT) w.s += step.s;
         gn_slope<T, ACT>(xhat, u, minus_mean, rstd, gamma, beta);
     };
     auto constants = [&](int cc, float (&minus_mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
@@ -366,26 +370,26 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
         float a[E], s[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) a[i] = s[i] = 0.f;
-        float mean[E], rstd[E], gamma[E], beta[E];
+        float minus_mean[E], rstd[E], gamma[E], beta[E];
         const int n = in ? rows_of_lane(at.rows, cut.lane, cut.lanes) : 0;
         if constexpr (E > 1) {
             if (t0 > 0) copy_column(cc, n);
         }
-        if (in) constants(cc, mean, rstd, gamma, beta);
-        int r = cut.lane;
-        for (int i = 0; i < kHeldStages; ++i) {
-            int end;
+        if (in) constants(cc, minus_mean, rstd, gamma, beta);
+        Walk w = walk(cut.lane, cc);
+        for (int i = 0, k = 0; i < kHeldStages; ++i) {
+            int end;  // of this thread's rows
             if constexpr (E > 1) {
                 copies_wait(kHeldStages - 1 - i);
-                end = cut.lane + end_of(n, i) * cut.lanes;
+                end = end_of(n, i);
             } else {
                 if (!mbar_wait(&bar[i], 0, kHeldWaitLimit)) failed = true;
-                end = in ? min(xs.ready(i, at.rows), ds.ready(i, at.rows)) : 0;
+                end = in ? rows_of_lane(min(xs.ready(i, at.rows), ds.ready(i, at.rows)), cut.lane, cut.lanes) : 0;
             }
 #pragma unroll 2
-            for (; r < end; r += cut.lanes) {
+            for (; k < end; ++k) {
                 float xhat[E], u[E];
-                chunk(r, cc, mean, rstd, gamma, beta, xhat, u);
+                chunk(w, minus_mean, rstd, gamma, beta, xhat, u);
                 fma_v(u, xhat, a, a);
                 add_v(s, u, s);
             }
@@ -434,18 +438,21 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
     for (int t0 = 0; t0 < CW; t0 += cut.cols) {
         const int cc = t0 + cut.col;
         if (!cut.in || cc >= CW) continue;
-        float mean[E], rstd[E], gamma[E], beta[E];
-        constants(cc, mean, rstd, gamma, beta);
+        float minus_mean[E], rstd[E], gamma[E], beta[E];
+        constants(cc, minus_mean, rstd, gamma, beta);
         float m1[E], m2[E];
         groups_v(means, cc * E, g.cg, g.magic, m1, m2);
+        Walk w = walk(cut.lane, cc);
+        const int64_t out_step = (int64_t)cut.lanes * g.C;
+        T *to = dx + (int64_t)cut.lane * g.C + cc * E;
 #pragma unroll 1
-        for (int r = cut.lane; r < at.rows; r += cut.lanes) {
+        for (int n = rows_of_lane(at.rows, cut.lane, cut.lanes); n > 0; --n, to += out_step) {
             float xhat[E], u[E];
-            chunk(r, cc, mean, rstd, gamma, beta, xhat, u);
+            chunk(w, minus_mean, rstd, gamma, beta, xhat, u);
             gn_dx(xhat, u, rstd, gamma, m1, m2);
             Vals<T, E> o;
             o.set(u);
-            o.store(dx + (int64_t)r * g.C + cc * E);
+            o.store(to);
         }
     }
     if (E == 1 && failed && threadIdx.x == 0) {

@@ -99,33 +99,6 @@ template <typename T, int E> struct Vals {
     }
 };
 
-// E kept values: their codes and their block's scale.
-template <int E> struct Kept {
-    using W = typename std::conditional<E == 8, uint2, typename std::conditional<E == 4, uint32_t, uint8_t>::type>::type;
-    W w;
-    uint32_t b;
-    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, int64_t row, int C, int c) {
-        w = *reinterpret_cast<const W *>(codes + row * C + c);
-        b = scales[row * ((C + kBlock8 - 1) / kBlock8) + c / kBlock8];
-    }
-    __device__ __forceinline__ void get(float (&v)[E]) const {
-        const float f = from_codes8(b);
-        if constexpr (E == 8) {
-            float lo[4], hi[4];
-            decode8x4(w.x, lo);
-            decode8x4(w.y, hi);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = lo[i] * f, v[4 + i] = hi[i] * f;
-        } else if constexpr (E == 4) {
-            decode8x4(w, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] *= f;
-        } else {
-            v[0] = decode8((int8_t)w) * f;
-        }
-    }
-};
-
 template <typename T> __device__ __forceinline__ float param(const void *w, int w32, int c, float none) {
     if (!w) return none;
     return w32 ? static_cast<const float *>(w)[c] : widen<T>(static_cast<const T *>(w)[c]);
@@ -321,6 +294,9 @@ struct Cut {
     }
 };
 
+// A lane's rows of `rows`: lane, lane + lanes, ...
+__device__ __forceinline__ int rows_of_lane(int rows, int lane, int lanes) { return lane < rows ? (rows - lane + lanes - 1) / lanes : 0; }
+
 // ------------------------------------------------------------- statistics --
 template <int subs> __device__ __forceinline__ float sub_sum(float v) {
 #pragma unroll
@@ -343,36 +319,95 @@ template <int E> __device__ __forceinline__ void lane_stats(int n, const float (
 // The lanes' statistics of each of `width` channels ([lanes, width]) joined
 // about their common mean, in place of lane 0's; `rows` in all.
 template <int THREADS> __device__ __forceinline__ void join_lanes(float *mean, float *m2, int width, int lanes, int rows) {
-    const int used = min(lanes, rows);
-    const float all = 1.f / (float)max(rows, 1);
+    const int used = min(lanes, rows), each = rows / lanes, more = rows - each * lanes;  // rows of a lane, lanes with one more
+    const float few = (float)each, many = (float)(each + 1), all = 1.f / (float)max(rows, 1);
     for (int c = threadIdx.x; c < width; c += THREADS) {
         const float ref = mean[c];
         float s = 0.f, q = 0.f;
 #pragma unroll 4
-        for (int l = 1; l < used; ++l) s += (float)((rows - l + lanes - 1) / lanes) * (mean[l * width + c] - ref);
-        const float m = ref + s * all;
+        for (int l = 1; l < used; ++l) s = fmaf(l < more ? many : few, mean[l * width + c] - ref, s);
+        const float m = fmaf(s, all, ref);
 #pragma unroll 4
         for (int l = 0; l < used; ++l) {
             const float d = mean[l * width + c] - m;
-            q += fmaf((float)((rows - l + lanes - 1) / lanes) * d, d, m2[l * width + c]);
+            q += fmaf((l < more ? many : few) * d, d, m2[l * width + c]);
         }
         mean[c] = m;
         m2[c] = q;
     }
 }
 
-// E values from shared memory.
-template <typename T, int E> __device__ __forceinline__ Vals<T, E> held_chunk(const uint8_t *p) {
+// E values, or the codes of E values, from shared memory (addresses in the
+// shared window: the loops over rows step 32-bit numbers).
+template <typename T, int E> __device__ __forceinline__ Vals<T, E> held_chunk(uint32_t at) {
     Vals<T, E> c;
-    c.w = *reinterpret_cast<const typename Vals<T, E>::W *>(p);
+    constexpr int B = Vals<T, E>::B;
+    if constexpr (B == 16)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(c.u[0]), "=r"(c.u[1]), "=r"(c.u[2]), "=r"(c.u[3]) : "r"(at));
+    else if constexpr (B == 8)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(c.u[0]), "=r"(c.u[1]) : "r"(at));
+    else if constexpr (B == 4)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.u[0]) : "r"(at));
+    else
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(c.u[0]) : "r"(at));
     return c;
 }
-template <typename T, int E> __device__ __forceinline__ void held_values(const uint8_t *p, float (&v)[E]) { held_chunk<T, E>(p).get(v); }
-template <int E> __device__ __forceinline__ void held_codes(const uint8_t *p, uint32_t b, float (&v)[E]) {
-    Kept<E> k;
-    k.w = *reinterpret_cast<const typename Kept<E>::W *>(p);
-    k.b = b;
-    k.get(v);
+template <typename T, int E> __device__ __forceinline__ void held_values(uint32_t at, float (&v)[E]) { held_chunk<T, E>(at).get(v); }
+__device__ __forceinline__ uint32_t held_byte(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+template <int E> __device__ __forceinline__ void held_codes(uint32_t at, uint32_t b, float (&v)[E]) {
+    if constexpr (E == 1) {
+        v[0] = decode8((int8_t)held_byte(at)) * from_codes8(b);
+    } else {
+        const float f = from_codes8(b);
+        float ff[E];
+        fill_v(f, ff);
+        uint32_t w[E / 4];
+        if constexpr (E == 8)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+        else
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            float q[4];
+            decode8x4(w[i], q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = q[k];
+        }
+        mul_v(v, ff, v);
+    }
+}
+
+// The statistics' sums of the rows at `from` (shared window), n of them `step`
+// bytes apart: K from the first of a thread's first call (n0 0).
+template <typename T, int E>
+__device__ __forceinline__ void sum_rows(uint32_t from, int n, uint32_t step, int n0, float (&minus_K)[E], float (&s1)[E], float (&s2)[E]) {
+    if (n > 0 && n0 == 0) {
+        held_values<T, E>(from, minus_K);
+#pragma unroll
+        for (int i = 0; i < E; ++i) minus_K[i] = -minus_K[i];
+        from += step;
+        --n;
+    }
+    for (; n >= 4; n -= 4) {
+        Vals<T, E> c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q, from += step) c[q] = held_chunk<T, E>(from);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[E];
+            c[q].get(v);
+            gn_deviate(v, minus_K, s1, s2);
+        }
+    }
+    for (; n > 0; --n, from += step) {
+        float v[E];
+        held_values<T, E>(from, v);
+        gn_deviate(v, minus_K, s1, s2);
+    }
 }
 
 #define GN_DECLARE(suf)                                                          \
