@@ -71,7 +71,7 @@ static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     const int64_t x = up(rows * W * xb + 16), d = c.backward ? up(rows * W * es + 16) : 0;
     const int64_t sc = c.kept ? up(rows * (W / kBlock8 + 2)) : 0;
-    const int64_t fixed = kHeldThreads * E * 8 + W * 8 + (int64_t)ctas * K * 8 + K * 16;
+    const int64_t fixed = kHeldThreads * E * 8 + W * 8 + (int64_t)ctas * K * 8 + K * 16;  // (statistics: the CTAs', the cluster's, this CTA's)
     if (x + d + sc + fixed > (int64_t)kHeldSmem) return false;
     h = GnHeld{ctas, K, (int)W, (int)rows, {(uint32_t)x, (uint32_t)d}, (uint32_t)sc, (size_t)(x + d + sc + fixed)};
     return true;
@@ -111,10 +111,10 @@ static size_t held_bytes(const GnCall &c, const GnHeld &h) { return ((size_t)c.B
 // The cut of the flow: pieces of `rows` places of a sample, stages of
 // `stage_rows`.
 struct GnFlow {
-    int rows, pieces, lag, grid, folds, stage_rows, depth;
-    uint32_t offset[3], stage_bytes;
+    int rows, pieces, fans, lag, grid, folds, stage_rows, depth;
+    uint32_t offset[4], stage_bytes;
     size_t smem;
-    size_t state, part, stat, parts, folded, bytes;  // workspace offsets (state_bytes of zeros first)
+    size_t state, part, fan, stat, parts, folded, bytes;  // workspace offsets (state_bytes of zeros first)
     size_t state_bytes;
 };
 
@@ -139,8 +139,8 @@ static GnFlow flow_plan(GnCall c, int sms) {
         f.offset[0] = 0;
         f.offset[1] = (uint32_t)up(rows * c.C * xb);
         f.offset[2] = f.offset[1] + (uint32_t)(c.backward ? up(rows * c.C * es) : 0);
-        f.stage_bytes = f.offset[2] + (uint32_t)(c.kept ? up(rows * nb) : 0);
-        if (!c.backward) f.stage_bytes = f.offset[1];
+        f.offset[3] = f.offset[2] + (uint32_t)(c.kept ? up(rows * nb) : 0);
+        f.stage_bytes = f.offset[3] + (uint32_t)up((int64_t)c.G * 8);
         return (int64_t)f.stage_bytes;
     };
     int64_t rows = std::max<int64_t>(1, (FLOW_STAGE << 10) / row / lanes) * lanes;
@@ -158,7 +158,10 @@ static GnFlow flow_plan(GnCall c, int sms) {
     while ((c.S + rows - 1) / rows > 65535 && tiles == 1 && rows % lanes == 0) rows *= 2;
     f.rows = (int)std::min<int64_t>(rows, c.S);
     f.pieces = (int)((c.S + f.rows - 1) / f.rows);
-    f.lag = f.grid;
+#ifndef FLOW_LAG
+#define FLOW_LAG 4
+#endif
+    f.lag = f.grid * FLOW_LAG / 4;
     f.grid = (int)std::min<int64_t>(f.grid, c.B * f.pieces);
     if (c.B * f.pieces <= f.lag) f.lag = 0;  // one turn of the CTAs: nothing to put between
     f.smem += (size_t)f.depth * f.stage_bytes;
@@ -168,9 +171,11 @@ static GnFlow flow_plan(GnCall c, int sms) {
         at += (n + 255) / 256 * 256;
         return a;
     };
-    f.state_bytes = (size_t)(2 + 2 * c.B) * 4;
+    f.fans = (f.pieces + kFlowFan - 1) / kFlowFan;
+    f.state_bytes = (size_t)(2 + (2 + f.fans) * c.B) * 4;
     f.state = take(f.state_bytes);
     f.part = take((size_t)c.B * f.pieces * c.G * sizeof(float2));
+    f.fan = take((size_t)c.B * f.fans * c.G * sizeof(float2));
     f.stat = take((size_t)c.B * c.G * sizeof(float2));
     f.parts = f.folded = at;
     f.folds = 0;
@@ -233,14 +238,15 @@ static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const Gn
     p.pieces = f.pieces, p.lag = f.lag;
     p.tickets = 2 * (c.B * f.pieces + f.pieces + f.lag);
     p.stage_rows = f.stage_rows, p.depth = f.depth, p.stage_bytes = f.stage_bytes;
-    for (int i = 0; i < 3; ++i) p.offset[i] = f.offset[i];
+    for (int i = 0; i < 4; ++i) p.offset[i] = f.offset[i];
     p.state = reinterpret_cast<uint32_t *>(w + f.state);
-    p.part = reinterpret_cast<float2 *>(w + f.part), p.stat = reinterpret_cast<float2 *>(w + f.stat);
+    p.fans = f.fans;
+    p.part = reinterpret_cast<float2 *>(w + f.part), p.fan = reinterpret_cast<float2 *>(w + f.fan), p.stat = reinterpret_cast<float2 *>(w + f.stat);
     p.status = status;
     int e = (int)cudaMemsetAsync(p.state, 0, f.state_bytes, s);
     void *args[] = {&p};
     if (e == 0)
-        e = launch(gn_flow(base, c.backward, c.chunk, c.act, c.backward ? c.kept : g.codes != nullptr), (unsigned)f.grid, 1, kFlowThreads + 32,
+        e = launch(gn_flow(base, c.backward, c.chunk, c.act, c.backward ? c.kept : g.codes != nullptr), (unsigned)f.grid, 1, kFlowAll,
                    f.smem, args, s, 1);
     if (e == 0 && sums) {
         const float *in = p.g.parts;

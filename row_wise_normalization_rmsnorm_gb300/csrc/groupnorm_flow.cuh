@@ -4,16 +4,20 @@
 // By then the sample is summed and its rows still lie in the L2, so memory
 // reads them once, and reads and writes overlap all the way.
 //
-// A warp of its own draws the tickets and keeps a ring of stages of rows under
-// way into shared memory (bulk copies, whatever alignment rows have); the
-// others take the stages in order. A piece waits only for pieces with earlier
+// One warp draws the tickets and keeps a ring of stages of rows under way into
+// shared memory (bulk copies, whatever alignment rows have; the sample's
+// statistics with them once they are joined); eight take the stages in order;
+// one joins. A piece waits only for pieces with earlier
 // tickets, and every CTA takes its tickets in order: the earliest ticket not
 // yet done is the next of some running CTA and waits for none, so the launch
 // makes progress however few of its CTAs run at once.
 //
 // A piece's group statistics, (mean, sum of squared deviations) or the two
-// sums of the gradient, go to memory; the CTA that brings a sample's last
-// ones joins them, in the pieces' order.
+// sums of the gradient, go to memory. They are joined in two steps, kFlowFan
+// neighbouring pieces by the CTA that brings the last of them, then a sample's
+// fans by the one that brings the last of those, in their order: the sample
+// waits for two rounds of loads, however many pieces it has. (One join of all
+// pieces kept the sample waiting for 25 to 90 us.)
 #pragma once
 
 #include "groupnorm_kernels.cuh"
@@ -24,18 +28,24 @@ namespace rmsn {
 #define FLOW_CTAS 2
 #endif
 constexpr int kFlowThreads = 256, kFlowCtas = FLOW_CTAS;  // that compute, of a CTA; CTAs an SM
+constexpr int kFlowAll = kFlowThreads + 64;  // threads of a CTA
 constexpr int kFlowStagesMost = 8;
+constexpr int kFlowMail = 4;
+constexpr int kFlowFan = 16;
 constexpr uint32_t kFlowWaitLimit = 1u << 22;  // polls of 100 ns for a sample's statistics
+constexpr uint32_t kFlowMailLimit = 1u << 25;  // polls of 200 ns for the next summed piece
 constexpr uint32_t kFlowCopyLimit = 1u << 24;  // polls of a stage (a wait for its reader or its copies)
 
 struct FlowParams {
     GnParams g;          // rows: of a piece
     int pieces, lag;     // of a sample; sum and normalise tickets of a piece lie pieces + lag pairs apart
     int stage_rows, depth;
-    uint32_t offset[3], stage_bytes;  // in a stage: dy (0: x or its codes), scales; its size
+    uint32_t offset[4], stage_bytes;  // in a stage: dy (0: x or its codes), scales, statistics; its size
     int64_t tickets;
-    uint32_t *state;     // [0], [1]: the next ticket (64 bits); then [B] pieces summed, [B] samples joined. Zeros at the start
+    int fans;            // ceil(pieces / kFlowFan)
+    uint32_t *state;     // [0], [1]: the next ticket (64 bits); then [B] samples joined, [B] fans joined, [B, fans] pieces summed. Zeros at the start
     float2 *part;        // [B, pieces, G]
+    float2 *fan;         // [B, fans, G]
     float2 *stat;        // [B, G]: (-mean, rstd), or the negated means of u gamma and of u gamma xhat
     int *status;
 };
@@ -56,7 +66,8 @@ __device__ __forceinline__ void flow_arrive(uint64_t *bar) {
 struct FlowShared {
     uint64_t full[kFlowStagesMost], empty[kFlowStagesMost];
     int64_t ticket[kFlowStagesMost];  // of the stage's piece; -1: no more
-    uint32_t before;
+    int64_t mail[kFlowMail];          // pieces that are summed; -1: no more
+    uint32_t sent, taken;
 };
 
 // A ticket's piece.
@@ -107,17 +118,27 @@ __device__ __forceinline__ void flow_copies(const FlowParams &p, FlowShared &s, 
                 c[i] = cover16(static_cast<const char *>(src[i]) + (f.first + r) * row[i], rows * row[i]);
                 bytes += c[i].bytes;
             }
+            const bool stats = f.normalise && r == 0;
+            Cover cs;
+            if (stats) {
+                uint32_t k = 0;
+                while (ld_acquire(p.state + 2 + f.b) == 0 && ++k < kFlowWaitLimit) __nanosleep(100);
+                if (k >= kFlowWaitLimit) failed = true;
+                asm volatile("fence.proxy.async;" ::: "memory");
+                cs = cover16(p.stat + (int64_t)f.b * p.g.G, (uint32_t)p.g.G * 8u);
+                bytes += cs.bytes;
+            }
             s.ticket[stage] = ticket;
             mbar_arrive_expect_tx(&s.full[stage], bytes);
+            if (stats) bulk_g2s(to + p.offset[3], cs.src, cs.bytes, &s.full[stage]);
 #pragma unroll
             for (int i = 0; i < N; ++i) bulk_g2s(to + (i ? p.offset[i] : 0u), c[i].src, c[i].bytes, &s.full[stage]);
         }
     }
-    if (!failed && mbar_wait(&s.empty[stage], phase, kFlowCopyLimit)) {
+    if (failed && p.status) *p.status = 1;
+    if (mbar_wait(&s.empty[stage], phase, kFlowCopyLimit)) {
         s.ticket[stage] = -1;
         flow_arrive(&s.full[stage]);
-    } else if (p.status) {
-        *p.status = 1;
     }
 }
 // The stages as the computing threads take them.
@@ -142,6 +163,7 @@ __device__ __forceinline__ void flow_setup(const FlowParams &p, FlowShared &s) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], kFlowThreads / 32);
         }
+        s.sent = s.taken = 0;
         mbar_init_fence();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -150,33 +172,63 @@ __device__ __forceinline__ void flow_setup(const FlowParams &p, FlowShared &s) {
     __syncthreads();
 }
 
-// Joins a sample's pieces where this CTA's was the last: `join(g, sub, subs)`
-// by `subs` neighbouring lanes a group.
-template <class Join> __device__ __forceinline__ void sum_given(const FlowParams &p, FlowShared &s, int b, Join &&join) {
-    __threadfence();
+// The computing threads tell the joining warp that a piece is summed, its sums
+// stored (-1: that no more come).
+__device__ __forceinline__ void flow_tell(FlowShared &s, int64_t item) {
     flow_sync();
-    if (threadIdx.x == 0) s.before = atomicAdd(p.state + 2 + b, 1u);
-    flow_sync();
-    if (s.before != (uint32_t)p.pieces - 1) return;
-    __threadfence();
-    constexpr int subs = 8;
-    for (int g = threadIdx.x / subs; g < (p.g.G + kFlowThreads / subs - 1) / (kFlowThreads / subs) * (kFlowThreads / subs); g += kFlowThreads / subs)
-        join(g, (int)threadIdx.x % subs, subs);
-    __threadfence();
-    flow_sync();
-    if (threadIdx.x == 0) st_release(p.state + 2 + p.g.B + b, 1u);
-}
-__device__ __forceinline__ void wait_joined(const FlowParams &p, int b) {
     if (threadIdx.x == 0) {
+        volatile FlowShared &v = s;
         uint32_t k = 0;
-        while (ld_acquire(p.state + 2 + p.g.B + b) == 0 && ++k < kFlowWaitLimit) __nanosleep(100);
-        if (k >= kFlowWaitLimit && p.status) *p.status = 1;
+        while (v.sent - v.taken >= kFlowMail && ++k < kFlowWaitLimit) __nanosleep(100);
+        v.mail[v.sent % kFlowMail] = item;
+        __threadfence_block();
+        v.sent = v.sent + 1;
     }
-    flow_sync();
+}
+// True in the whole warp where this was the last of `n` to count: what the
+// warp (and whoever told it) stored is there for the last, and what the others
+// stored for it.
+__device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t n) {
+    __syncwarp();
+    uint32_t before = 0;
+    if ((threadIdx.x & 31) == 0) asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    before = __shfl_sync(0xffffffffu, before, 0);
+    __syncwarp();
+    return before == n - 1;
+}
+// The joining warp. join(from, n, count, k): group k's values of n neighbours
+// `from[i G]`, that stand for count(i) rows each, as one; give(b, k, value):
+// the sample's.
+template <class Join, class Give> __device__ __forceinline__ void flow_join(const FlowParams &p, FlowShared &s, Join &&join, Give &&give) {
+    const int lane = threadIdx.x & 31, G = p.g.G;
+    volatile FlowShared &v = s;
+    uint32_t *joined = p.state + 2, *fans_done = joined + p.g.B, *pieces_done = fans_done + p.g.B;
+    // rows of `each` rows a piece, the sample's last having what is left
+    auto rows_at = [&](int i, int64_t each) { return (float)min(each, p.g.S - (int64_t)i * each); };
+    for (uint32_t n = 0;; ++n) {
+        uint32_t k = 0;
+        while (v.sent == n && ++k < kFlowMailLimit) __nanosleep(100);
+        __threadfence_block();
+        const int64_t item = v.sent == n ? -1 : v.mail[n % kFlowMail];
+        __syncwarp();
+        if (lane == 0) v.taken = n + 1;
+        if (item < 0) return;
+        const int b = (int)(item / p.pieces), fan = (int)(item - (int64_t)b * p.pieces) / kFlowFan;
+        const int i0 = fan * kFlowFan, ni = min(kFlowFan, p.pieces - i0);
+        const int64_t at = (int64_t)b * p.fans + fan;
+        if (!last_of(pieces_done + at, (uint32_t)ni)) continue;
+        for (int g = lane; g < G; g += 32)
+            p.fan[at * G + g] = join(p.part + ((int64_t)b * p.pieces + i0) * G + g, ni, [&](int i) { return rows_at(i0 + i, p.g.rows); });
+        if (!last_of(fans_done + b, (uint32_t)p.fans)) continue;
+        for (int g = lane; g < G; g += 32)
+            give(b, g, join(p.fan + (int64_t)b * p.fans * G + g, p.fans, [&](int i) { return rows_at(i, (int64_t)p.g.rows * kFlowFan); }));
+        __syncwarp();
+        if (lane == 0) st_release(joined + b, 1u);
+    }
 }
 
 template <typename T, int E, int ACT, bool KEEP>
-__global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(const FlowParams p) {
+__global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowParams p) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) FlowShared fs;
     float *lane_mean = reinterpret_cast<float *>(ring + (size_t)p.depth * p.stage_bytes), *lane_m2 = lane_mean + kFlowThreads * E;
@@ -189,6 +241,34 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(cons
             const void *const src[1] = {g.x};
             const uint32_t row[1] = {pitch};
             flow_copies<1>(p, fs, ring, src, row);
+        } else if (threadIdx.x >= kFlowThreads + 32) {
+            // about the first one's mean, kFlowFan loads under way
+            auto join = [&](const float2 *from, int n, auto &&rows) {
+                float ref = 0.f, s1 = 0.f, s2 = 0.f, all = 0.f;
+                for (int i0 = 0; i0 < n; i0 += kFlowFan) {
+                    float2 v[kFlowFan];
+#pragma unroll
+                    for (int i = 0; i < kFlowFan; ++i)
+                        if (i0 + i < n) v[i] = __ldcg(from + (int64_t)(i0 + i) * g.G);
+                    if (i0 == 0) ref = v[0].x;
+#pragma unroll
+                    for (int i = 0; i < kFlowFan; ++i)
+                        if (i0 + i < n) {
+                            const float count = rows(i0 + i), d = v[i].x - ref;
+                            s1 = fmaf(count, d, s1);
+                            s2 += fmaf(count * (float)g.cg * d, d, v[i].y);
+                            all += count;
+                        }
+                }
+                const float m = s1 / all;
+                return make_float2(ref + m, fmaxf(s2 - s1 * m * (float)g.cg, 0.f));
+            };
+            flow_join(p, fs, join, [&](int b, int k, float2 v) {
+                const float r = 1.f / sqrtf(v.y / ((float)g.S * (float)g.cg) + g.eps);
+                p.stat[(int64_t)b * g.G + k] = make_float2(-v.x, r);
+                g.mean[(int64_t)b * g.G + k] = v.x;
+                g.rstd[(int64_t)b * g.G + k] = r;
+            });
         }
         return;
     }
@@ -220,75 +300,39 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(cons
                 flow_sync();
                 join_lanes<kFlowThreads>(lane_mean, lane_m2, cut.cols * E, cut.lanes, f.rows);
                 flow_sync();
-                // a warp a group: this tile's channels, joined with the tiles before
+                // a group's channels of this tile, joined with those of the tiles before
                 const int c0 = t0 * E, c1 = min((t0 + cut.cols) * E, g.C);
-                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-                for (int k = c0 / g.cg + warp; k * g.cg < c1; k += kFlowThreads / 32) {
-                    const int lo = max(k * g.cg, c0), w = min((k + 1) * g.cg, c1) - lo;
-                    const float *cm = lane_mean + (lo - c0), *cq = lane_m2 + (lo - c0);
-                    const float ref = cm[0];
-                    float s = 0.f, m2 = 0.f;
-                    for (int c = wl; c < w; c += 32) s += cm[c] - ref;
-                    s = sub_sum<32>(s);
-                    float m = ref + s / (float)w;
-                    for (int c = wl; c < w; c += 32) {
-                        const float d = cm[c] - m;
-                        m2 += fmaf((float)f.rows * d, d, cq[c]);
-                    }
-                    m2 = sub_sum<32>(m2);
-                    if (wl == 0) {
-                        const float cnt = (float)f.rows * (float)w;
+                sum_groups<kFlowThreads>(
+                    c0, c1, g.cg,
+                    [&](int lo, int c) {  // about the first channel's mean
+                        const float d = lane_mean[c - c0] - lane_mean[lo - c0];
+                        return make_float2(d, fmaf((float)f.rows * d, d, lane_m2[c - c0]));
+                    },
+                    [&](int k, int lo, int hi, float2 v) {
+                        const float w = (float)(hi - lo), off = v.x / w, cnt = (float)f.rows * w;
+                        float m = lane_mean[lo - c0] + off, m2 = fmaxf(v.y - (float)f.rows * v.x * off, 0.f);
                         if (lo > k * g.cg) {
                             const float2 a = acc[k];
                             const float na = (float)f.rows * (float)(lo - k * g.cg), d = m - a.x, share = cnt / (na + cnt);
                             m = a.x + d * share;
                             m2 = a.y + m2 + d * d * (na * share);
                         }
-                        if (lo + w < (k + 1) * g.cg)
+                        if (hi < (k + 1) * g.cg)
                             acc[k] = make_float2(m, m2);
                         else
                             p.part[f.item * g.G + k] = make_float2(m, m2);
-                    }
-                }
+                    });
                 if (t0 + cut.cols < CC) flow_sync();
             }
-            sum_given(p, fs, f.b, [&](int k, int sub, int subs) {
-                const bool in = k < g.G;
-                const float2 *part = p.part + (int64_t)f.b * p.pieces * g.G + k;
-                const float n = (float)g.S * (float)g.cg;
-                auto count = [&](int i) { return (float)min((int64_t)g.rows, g.S - (int64_t)i * g.rows) * (float)g.cg; };
-                const float ref = in ? __ldcg(part).x : 0.f;
-                float s = 0.f, m2 = 0.f;
-                if (in) {
-#pragma unroll 8
-                    for (int i = sub; i < p.pieces; i += subs) s += count(i) * (__ldcg(part + (int64_t)i * g.G).x - ref);
-                }
-                const float m = ref + sub_sum<8>(s) / n;
-                if (in) {
-#pragma unroll 8
-                    for (int i = sub; i < p.pieces; i += subs) {
-                        const float2 a = __ldcg(part + (int64_t)i * g.G);
-                        const float d = a.x - m;
-                        m2 += fmaf(count(i) * d, d, a.y);
-                    }
-                }
-                m2 = sub_sum<8>(m2);
-                if (in && sub == 0) {
-                    const float r = 1.f / sqrtf(m2 / n + g.eps);
-                    p.stat[(int64_t)f.b * g.G + k] = make_float2(-m, r);
-                    g.mean[(int64_t)f.b * g.G + k] = m;
-                    g.rstd[(int64_t)f.b * g.G + k] = r;
-                }
-            });
+            flow_tell(fs, f.item);
             continue;
         }
-        wait_joined(p, f.b);
-        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)f.b * g.G + k);
-        flow_sync();
         float minus_mean[E], f_[E], beta[E];
+        const float2 *stat = reinterpret_cast<const float2 *>(ring + (size_t)at.stage * p.stage_bytes + p.offset[3] + addr_mod16(p.stat + (int64_t)f.b * g.G));
+        // (in the piece's first stage: a piece of one tile has its constants from there)
         auto constants = [&](int cc) {
             float gamma[E];
-            groups_v(acc, cc * E, g.cg, g.magic, minus_mean, f_);
+            groups_v(stat, cc * E, g.cg, g.magic, minus_mean, f_);
             params_v<T>(g.gamma, g.w32, cc * E, 1.f, gamma);
             params_v<T>(g.beta, g.w32, cc * E, 0.f, beta);
             mul_v(f_, gamma, f_);
@@ -322,13 +366,13 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_fwd_flow(cons
             }
             at.release(p, fs);
         }
-        flow_sync();  // (acc is the next piece's)
     }
+    flow_tell(fs, -1);
     if (at.failed && threadIdx.x == 0 && p.status) *p.status = 1;
 }
 
 template <typename T, int E, int ACT, bool KEPT>
-__global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(const FlowParams p) {
+__global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowParams p) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) FlowShared fs;
     float *lane_a = reinterpret_cast<float *>(ring + (size_t)p.depth * p.stage_bytes), *lane_s = lane_a + kFlowThreads * E;
@@ -349,6 +393,24 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
                 const uint32_t row[2] = {xpitch, pitch};
                 flow_copies<2>(p, fs, ring, src, row);
             }
+        } else if (threadIdx.x >= kFlowThreads + 32) {
+            auto join = [&](const float2 *from, int n, auto &&) {
+                float2 m = make_float2(0.f, 0.f);
+                for (int i0 = 0; i0 < n; i0 += kFlowFan) {
+                    float2 v[kFlowFan];
+#pragma unroll
+                    for (int i = 0; i < kFlowFan; ++i)
+                        if (i0 + i < n) v[i] = __ldcg(from + (int64_t)(i0 + i) * g.G);
+#pragma unroll
+                    for (int i = 0; i < kFlowFan; ++i)
+                        if (i0 + i < n) m = add2(m, v[i]);
+                }
+                return m;
+            };
+            flow_join(p, fs, join, [&](int b, int k, float2 m) {
+                const float n = (float)g.S * (float)g.cg;
+                p.stat[(int64_t)b * g.G + k] = make_float2(-m.x / n, -m.y / n);
+            });
         }
         return;
     }
@@ -420,16 +482,13 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
                     }
                     if (t0 + cut.cols >= CC) at.release(p, fs);
                 }
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    lane_a[threadIdx.x * E + i] = a[i];
-                    lane_s[threadIdx.x * E + i] = s[i];
-                }
+                put_v(lane_a + threadIdx.x * E, a);
+                put_v(lane_s + threadIdx.x * E, s);
                 flow_sync();
                 const int width = cut.cols * E, c0 = t0 * E, c1 = min(c0 + width, g.C);
                 for (int c = threadIdx.x; c < c1 - c0; c += kFlowThreads) {
                     float ta = lane_a[c], ts = lane_s[c];
-#pragma unroll 4
+#pragma unroll 8
                     for (int l = 1; l < cut.lanes; ++l) {
                         ta += lane_a[l * width + c];
                         ts += lane_s[l * width + c];
@@ -443,41 +502,21 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
                     lane_s[c] = ts * ga;
                 }
                 flow_sync();
-                const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-                for (int k = c0 / g.cg + warp; k * g.cg < c1; k += kFlowThreads / 32) {
-                    const int lo = max(k * g.cg, c0), hi = min((k + 1) * g.cg, c1);
-                    float2 m = make_float2(0.f, 0.f);
-                    for (int c = lo + wl; c < hi; c += 32) m = add2(m, make_float2(lane_s[c - c0], lane_a[c - c0]));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
-                    if (wl == 0) {
+                sum_groups<kFlowThreads>(
+                    c0, c1, g.cg, [&](int, int c) { return make_float2(lane_s[c - c0], lane_a[c - c0]); },
+                    [&](int k, int lo, int hi, float2 m) {
                         if (lo > k * g.cg) m = add2(acc[k], m);
                         if (hi < (k + 1) * g.cg)
                             acc[k] = m;
                         else
                             p.part[f.item * g.G + k] = m;
-                    }
-                }
+                    });
                 if (t0 + cut.cols < CC) flow_sync();
             }
-            sum_given(p, fs, f.b, [&](int k, int sub, int subs) {
-                const bool in = k < g.G;
-                const float2 *part = p.part + (int64_t)f.b * p.pieces * g.G + k;
-                float2 m = make_float2(0.f, 0.f);
-                if (in) {
-#pragma unroll 8
-                    for (int i = sub; i < p.pieces; i += subs) m = add2(m, __ldcg(part + (int64_t)i * g.G));
-                }
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
-                const float n = (float)g.S * (float)g.cg;
-                if (in && sub == 0) p.stat[(int64_t)f.b * g.G + k] = make_float2(-m.x / n, -m.y / n);
-            });
+            flow_tell(fs, f.item);
             continue;
         }
-        wait_joined(p, f.b);
-        for (int k = threadIdx.x; k < g.G; k += kFlowThreads) acc[k] = __ldcg(p.stat + (int64_t)f.b * g.G + k);
-        flow_sync();
+        const float2 *stat = reinterpret_cast<const float2 *>(ring + (size_t)at.stage * p.stage_bytes + p.offset[3] + addr_mod16(p.stat + (int64_t)f.b * g.G));
         float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
         for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
             if (r0 > 0) at.wait(fs);
@@ -488,7 +527,7 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
                 if (!cut.in || cc >= CC) continue;
                 if (r0 == 0 || CC > cut.cols) {
                     constants(cc, minus_mean, rstd, gamma, beta);
-                    groups_v(acc, cc * E, g.cg, g.magic, m1, m2);
+                    groups_v(stat, cc * E, g.cg, g.magic, m1, m2);
                 }
                 Walk w = walk(at.stage, first, cc);
                 const int64_t out_step = (int64_t)cut.lanes * g.C;
@@ -505,8 +544,8 @@ __global__ void __launch_bounds__(kFlowThreads + 32, kFlowCtas) gn_bwd_flow(cons
             }
             at.release(p, fs);
         }
-        flow_sync();  // (acc is the next piece's)
     }
+    flow_tell(fs, -1);
     if (at.failed && threadIdx.x == 0 && p.status) *p.status = 1;
 }
 

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
     float *lane_mean = reinterpret_cast<float *>(held + p.slab[0]), *lane_m2 = lane_mean + kHeldThreads * E;
     float *ch_mean = lane_m2 + kHeldThreads * E, *ch_m2 = ch_mean + p.W;
     float2 *exch = reinterpret_cast<float2 *>(ch_m2 + p.W);
-    float2 *stat = exch + p.ctas * p.K;
+    float2 *stat = exch + p.ctas * p.K, *own = stat + p.K;
     const HeldPlace at(p);
     const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
     const Slab xs(g.x, sizeof(T), at.first, g.C, at.rows, held);
@@ -187,24 +187,21 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
         }
         __syncthreads();
     }
-    // a group's channels (all of at.rows places), a warp a group; then to every CTA of the cluster
+    // a group's channels (all of at.rows places); then to every CTA of the cluster
     cluster_wait();
-    for (int k = warp; k < p.K; k += kHeldThreads / 32) {
-        const float *cm = ch_mean + k * g.cg, *c2 = ch_m2 + k * g.cg;
-        const float ref = cm[0];
-        float s = 0.f, m2 = 0.f;
-        for (int c = wl; c < g.cg; c += 32) s += cm[c] - ref;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float m = ref + s / (float)g.cg;
-        for (int c = wl; c < g.cg; c += 32) {
-            const float d = cm[c] - m;
-            m2 += fmaf((float)at.rows * d, d, c2[c]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-        if (wl < p.ctas) st_cluster2(&exch[at.rank * p.K + k], (uint32_t)wl, make_float2(m, m2));
-    }
+    const float inv_cg = 1.f / (float)g.cg;
+    sum_groups<kHeldThreads>(
+        0, p.W, g.cg,
+        [&](int lo, int c) {  // about the first channel's mean
+            const float d = ch_mean[c] - ch_mean[lo];
+            return make_float2(d, fmaf((float)at.rows * d, d, ch_m2[c]));
+        },
+        [&](int k, int lo, int, float2 m) {
+            const float d = m.x * inv_cg;
+            own[k] = make_float2(ch_mean[lo] + d, fmaxf(m.y - (float)at.rows * m.x * d, 0.f));
+        });
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.K * p.ctas; i += kHeldThreads) st_cluster2(&exch[at.rank * p.K + i % p.K], (uint32_t)(i / p.K), own[i % p.K]);
     cluster_sync();
     for (int k = threadIdx.x; k < p.K; k += kHeldThreads) {
         const float n = (float)g.S * (float)g.cg, ref = exch[k].x;
@@ -394,15 +391,13 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
                 add_v(s, u, s);
             }
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            lane_a[threadIdx.x * E + i] = a[i];
-            lane_s[threadIdx.x * E + i] = s[i];
-        }
+        put_v(lane_a + threadIdx.x * E, a);
+        put_v(lane_s + threadIdx.x * E, s);
         __syncthreads();
         const int width = cut.cols * E;
         for (int c = threadIdx.x; c < width && t0 * E + c < p.W; c += kHeldThreads) {
             float ta = lane_a[c], ts = lane_s[c];
+#pragma unroll 8
             for (int l = 1; l < cut.lanes; ++l) {
                 ta += lane_a[l * width + c];
                 ts += lane_s[l * width + c];
@@ -419,13 +414,10 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
         __syncthreads();
     }
     cluster_wait();
-    for (int k = warp; k < p.K; k += kHeldThreads / 32) {
-        float2 m = make_float2(0.f, 0.f);
-        for (int c = wl; c < g.cg; c += 32) m = add2(m, make_float2(ch_s[k * g.cg + c], ch_a[k * g.cg + c]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
-        if (wl < p.ctas) st_cluster2(&exch[at.rank * p.K + k], (uint32_t)wl, m);
-    }
+    sum_groups<kHeldThreads>(
+        0, p.W, g.cg, [&](int, int c) { return make_float2(ch_s[c], ch_a[c]); }, [&](int k, int, int, float2 m) { means[k] = m; });
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.K * p.ctas; i += kHeldThreads) st_cluster2(&exch[at.rank * p.K + i % p.K], (uint32_t)(i / p.K), means[i % p.K]);
     cluster_sync();
     for (int k = threadIdx.x; k < p.K; k += kHeldThreads) {
         const float n = (float)g.S * (float)g.cg;

@@ -298,42 +298,67 @@ struct Cut {
 __device__ __forceinline__ int rows_of_lane(int rows, int lane, int lanes) { return lane < rows ? (rows - lane + lanes - 1) / lanes : 0; }
 
 // ------------------------------------------------------------- statistics --
-template <int subs> __device__ __forceinline__ float sub_sum(float v) {
-#pragma unroll
-    for (int o = subs / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // A thread's sums of (x - K) and (x - K)^2 a channel as mean and sum of
 // squared deviations. K is its first value, so a mean far from zero costs no
 // digits: the error of its sum of squares is at most n 2^-24 of it.
-template <int E> __device__ __forceinline__ void lane_stats(int n, const float (&minus_K)[E], const float (&s1)[E], const float (&s2)[E], float *mean, float *m2) {
-    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+// E floats to shared memory, 16 bytes at a time.
+template <int E> __device__ __forceinline__ void put_v(float *to, const float (&v)[E]) {
+    if constexpr (E % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float m = s1[i] * inv;
-        mean[i] = m - minus_K[i];
-        m2[i] = fmaxf(s2[i] - s1[i] * m, 0.f);
+        for (int i = 0; i < E; i += 4) *reinterpret_cast<float4 *>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) to[i] = v[i];
     }
 }
-// The lanes' statistics of each of `width` channels ([lanes, width]) joined
-// about their common mean, in place of lane 0's; `rows` in all.
+template <int E> __device__ __forceinline__ void lane_stats(int n, const float (&minus_K)[E], const float (&s1)[E], const float (&s2)[E], float *mean, float *m2) {
+    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+    float m[E], q[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        m[i] = s1[i] * inv;
+        q[i] = fmaxf(s2[i] - s1[i] * m[i], 0.f);
+        m[i] -= minus_K[i];
+    }
+    put_v(mean, m);
+    put_v(m2, q);
+}
+// The lanes' statistics of each of `width` channels ([lanes, width]) joined in
+// place of lane 0's; `rows` in all. About lane 0's mean: with 1 / lanes of the
+// rows its own, it is at most sqrt(lanes) widths off the common one.
 template <int THREADS> __device__ __forceinline__ void join_lanes(float *mean, float *m2, int width, int lanes, int rows) {
     const int used = min(lanes, rows), each = rows / lanes, more = rows - each * lanes;  // rows of a lane, lanes with one more
     const float few = (float)each, many = (float)(each + 1), all = 1.f / (float)max(rows, 1);
+    if (lanes == 1) return;
     for (int c = threadIdx.x; c < width; c += THREADS) {
         const float ref = mean[c];
-        float s = 0.f, q = 0.f;
-#pragma unroll 4
-        for (int l = 1; l < used; ++l) s = fmaf(l < more ? many : few, mean[l * width + c] - ref, s);
-        const float m = fmaf(s, all, ref);
-#pragma unroll 4
-        for (int l = 0; l < used; ++l) {
-            const float d = mean[l * width + c] - m;
-            q += fmaf((l < more ? many : few) * d, d, m2[l * width + c]);
+        float s = 0.f, q = m2[c];
+#pragma unroll 8
+        for (int l = 1; l < used; ++l) {
+            const float d = mean[l * width + c] - ref, nd = (l < more ? many : few) * d;
+            s += nd;
+            q += fmaf(nd, d, m2[l * width + c]);
         }
-        mean[c] = m;
-        m2[c] = q;
+        const float m = s * all;
+        mean[c] = ref + m;
+        m2[c] = fmaxf(q - s * m, 0.f);
+    }
+}
+// For each group with channels among [c0, c1): both values of its channels
+// there summed (`each(c)` gives them), by a team of as many lanes as it has
+// channels (a power of two, a warp at most). give(k, lo, hi, sums) is called by
+// one lane a group.
+template <int THREADS, class Each, class Give>
+__device__ __forceinline__ void sum_groups(int c0, int c1, int cg, Each &&each, Give &&give) {
+    int ts = 1;
+    while (ts < cg && ts < 32) ts *= 2;
+    const int team = (int)threadIdx.x / ts, tl = (int)threadIdx.x % ts, teams = THREADS / ts;
+    for (int k0 = c0 / cg; k0 * cg < c1; k0 += teams) {
+        const int k = k0 + team, lo = max(k * cg, c0), hi = min((k + 1) * cg, c1);
+        float2 m = make_float2(0.f, 0.f);
+        for (int c = lo + tl; c < hi; c += ts) m = add2(m, each(lo, c));
+        for (int o = ts / 2; o > 0; o >>= 1) m = add2(m, shfl_xor2(m, o));
+        if (tl == 0 && lo < hi) give(k, lo, hi, m);
     }
 }
 
