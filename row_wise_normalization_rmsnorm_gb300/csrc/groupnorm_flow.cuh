@@ -196,15 +196,17 @@ __device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t n) {
     __syncwarp();
     return before == n - 1;
 }
-// The joining warp. join(from, n, count, k): group k's values of n neighbours
-// `from[i G]`, that stand for count(i) rows each, as one; give(b, k, value):
-// the sample's.
+// The joining warp. join(from, n, rows, last, last_rows): a group's values of n
+// neighbours `from[i G]`, of `rows` rows each but for the last-th, as one;
+// give(b, k, value): the sample's.
 template <class Join, class Give> __device__ __forceinline__ void flow_join(const FlowParams &p, FlowShared &s, Join &&join, Give &&give) {
     const int lane = threadIdx.x & 31, G = p.g.G;
     volatile FlowShared &v = s;
     uint32_t *joined = p.state + 2, *fans_done = joined + p.g.B, *pieces_done = fans_done + p.g.B;
-    // rows of `each` rows a piece, the sample's last having what is left
-    auto rows_at = [&](int i, int64_t each) { return (float)min(each, p.g.S - (int64_t)i * each); };
+    // rows of a piece and of a fan, and of a sample's last ones
+    const int64_t fan_rows = (int64_t)p.g.rows * kFlowFan;
+    const float rows = (float)p.g.rows, last_rows = (float)(p.g.S - (int64_t)(p.pieces - 1) * p.g.rows);
+    const float many = (float)fan_rows, last_many = (float)(p.g.S - (int64_t)(p.fans - 1) * fan_rows);
     for (uint32_t n = 0;; ++n) {
         uint32_t k = 0;
         while (v.sent == n && ++k < kFlowMailLimit) __nanosleep(100);
@@ -218,10 +220,10 @@ template <class Join, class Give> __device__ __forceinline__ void flow_join(cons
         const int64_t at = (int64_t)b * p.fans + fan;
         if (!last_of(pieces_done + at, (uint32_t)ni)) continue;
         for (int g = lane; g < G; g += 32)
-            p.fan[at * G + g] = join(p.part + ((int64_t)b * p.pieces + i0) * G + g, ni, [&](int i) { return rows_at(i0 + i, p.g.rows); });
+            p.fan[at * G + g] = join(p.part + ((int64_t)b * p.pieces + i0) * G + g, ni, rows, p.pieces - 1 - i0, last_rows);
         if (!last_of(fans_done + b, (uint32_t)p.fans)) continue;
         for (int g = lane; g < G; g += 32)
-            give(b, g, join(p.fan + (int64_t)b * p.fans * G + g, p.fans, [&](int i) { return rows_at(i, (int64_t)p.g.rows * kFlowFan); }));
+            give(b, g, join(p.fan + (int64_t)b * p.fans * G + g, p.fans, many, p.fans - 1, last_many));
         __syncwarp();
         if (lane == 0) st_release(joined + b, 1u);
     }
@@ -242,26 +244,26 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
             const uint32_t row[1] = {pitch};
             flow_copies<1>(p, fs, ring, src, row);
         } else if (threadIdx.x >= kFlowThreads + 32) {
-            // about the first one's mean, kFlowFan loads under way
-            auto join = [&](const float2 *from, int n, auto &&rows) {
-                float ref = 0.f, s1 = 0.f, s2 = 0.f, all = 0.f;
+            // about the first one's mean, kFlowFan loads under way; `last` stands for fewer rows than the others
+            auto join = [&](const float2 *from, int n, float rows, int last, float last_rows) {
+                float ref = 0.f, s1 = 0.f, s2 = 0.f;
+                const float each = rows * (float)g.cg, final = last_rows * (float)g.cg;
                 for (int i0 = 0; i0 < n; i0 += kFlowFan) {
                     float2 v[kFlowFan];
 #pragma unroll
-                    for (int i = 0; i < kFlowFan; ++i)
-                        if (i0 + i < n) v[i] = __ldcg(from + (int64_t)(i0 + i) * g.G);
+                    for (int i = 0; i < kFlowFan; ++i) v[i] = __ldcg(from + min(i0 + i, n - 1) * g.G);
                     if (i0 == 0) ref = v[0].x;
 #pragma unroll
-                    for (int i = 0; i < kFlowFan; ++i)
+                    for (int i = 0; i < kFlowFan; ++i) {
+                        const float d = v[i].x - ref, nd = (i0 + i == last ? final : each) * d;
                         if (i0 + i < n) {
-                            const float count = rows(i0 + i), d = v[i].x - ref;
-                            s1 = fmaf(count, d, s1);
-                            s2 += fmaf(count * (float)g.cg * d, d, v[i].y);
-                            all += count;
+                            s1 += nd;
+                            s2 += fmaf(nd, d, v[i].y);
                         }
+                    }
                 }
-                const float m = s1 / all;
-                return make_float2(ref + m, fmaxf(s2 - s1 * m * (float)g.cg, 0.f));
+                const float m = s1 / (last < n ? each * (float)(n - 1) + final : each * (float)n);
+                return make_float2(ref + m, fmaxf(s2 - s1 * m, 0.f));
             };
             flow_join(p, fs, join, [&](int b, int k, float2 v) {
                 const float r = 1.f / sqrtf(v.y / ((float)g.S * (float)g.cg) + g.eps);
@@ -394,13 +396,12 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowPar
                 flow_copies<2>(p, fs, ring, src, row);
             }
         } else if (threadIdx.x >= kFlowThreads + 32) {
-            auto join = [&](const float2 *from, int n, auto &&) {
+            auto join = [&](const float2 *from, int n, float, int, float) {
                 float2 m = make_float2(0.f, 0.f);
                 for (int i0 = 0; i0 < n; i0 += kFlowFan) {
                     float2 v[kFlowFan];
 #pragma unroll
-                    for (int i = 0; i < kFlowFan; ++i)
-                        if (i0 + i < n) v[i] = __ldcg(from + (int64_t)(i0 + i) * g.G);
+                    for (int i = 0; i < kFlowFan; ++i) v[i] = __ldcg(from + min(i0 + i, n - 1) * g.G);
 #pragma unroll
                     for (int i = 0; i < kFlowFan; ++i)
                         if (i0 + i < n) m = add2(m, v[i]);
