@@ -10,13 +10,6 @@
 #include "plans.h"
 #include "train_rows.h"
 
-#ifndef FLOW_KB
-#define FLOW_KB 256
-#endif
-#ifndef FLOW_STAGE
-#define FLOW_STAGE 28
-#endif
-
 namespace rmsn {
 
 static const void *gn_flow(int base, bool backward, int chunk, int act, bool kept) {
@@ -78,8 +71,10 @@ static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
 }
 
 // The cheapest cut by estimate: rounds of the CTAs that an SM holds at once
-// (two), at 3 us each, and the bytes at the rate of memory, those of a span
+// (two), at 4.5 us each, and the bytes at the rate of memory, those of a span
 // that begins or ends inside a 32-byte sector counted with the whole sector.
+// (The gradient of 8 x 4096 x 320: spans of 80 bytes in clusters of 8 take 33
+// us, of 160 bytes in clusters of 16 39, the flow 57.)
 static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
     GnHeld best{0, 0, 0, 0, {0, 0}, 0, 0};
     double least = 0;
@@ -90,12 +85,12 @@ static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
             GnHeld h;
             if ((n > 1 && (c.S + n - 1) / n * (n - 1) >= c.S) || !held_cut(c, K, n, keep, h)) continue;
             const double row = (double)h.W * es, sectors = K == c.G || (h.W * es) % 32 == 0 ? row : row + 32;
-            const double bytes = (double)c.B * c.S * c.C * es * (c.backward ? 3 : 2) * (sectors / row) * (row < 128 && K < c.G ? 1.25 : 1.0);
+            const double bytes = (double)c.B * c.S * c.C * es * (c.backward ? 3 : 2) * (sectors / row);
             // clusters of 16 leave SMs without a CTA where a GPU's groups of SMs are no multiple of 8
             const double ctas = (double)c.B * (c.G / K) * n, places = 2.0 * sms * (n == 16 ? 0.73 : n == 8 ? 0.94 : 1.0);
             const double rounds = std::ceil(ctas / places);
             const double share = ctas < sms ? sms / ctas : 1.0;  // SMs without a CTA
-            const double cost = 3.0 * rounds + (n > 1 ? 0.5 : 0.0) + bytes * share / 6.7e6;
+            const double cost = 4.5 * rounds + (n > 1 ? 0.5 : 0.0) + bytes * share / 6.7e6;
             if (best.ctas == 0 || cost < least) {
                 best = h;
                 least = cost;
@@ -122,6 +117,9 @@ struct GnFlow {
 // channels spill, with 4 a row of more than 1024 channels is several tiles.
 static int flow_chunk(int chunk, int64_t C) { return chunk > 4 && C <= 4 * kFlowThreads ? 4 : chunk; }
 
+// Bytes of a stage and of a piece at most. (256 x 256 x 256, 8 images: 154 us;
+// pieces of 128 KB 152, of 64 KB 158; a lag of half the CTAs 183.)
+constexpr int64_t kFlowStage = 28 << 10, kFlowPiece = 256 << 10;
 constexpr size_t kFlowSmem = 226 * 1024 / kFlowCtas, kFlowSmemMost = 224 * 1024;  // of a CTA; of the only one on an SM
 
 static GnFlow flow_plan(GnCall c, int sms) {
@@ -143,7 +141,7 @@ static GnFlow flow_plan(GnCall c, int sms) {
         f.stage_bytes = f.offset[3] + (uint32_t)up((int64_t)c.G * 8);
         return (int64_t)f.stage_bytes;
     };
-    int64_t rows = std::max<int64_t>(1, (FLOW_STAGE << 10) / row / lanes) * lanes;
+    int64_t rows = std::max<int64_t>(1, kFlowStage / row / lanes) * lanes;
     while (rows > 1 && 3 * bytes(rows) > room) rows = rows > lanes ? std::max<int64_t>(rows / 2 / lanes, 1) * lanes : rows / 2;
     if (2 * bytes(rows) > room) room = (int64_t)kFlowSmemMost - (int64_t)f.smem;  // (rows of ROWS_MAX_CHANNELS: two fit)
     f.stage_rows = (int)rows;
@@ -153,15 +151,12 @@ static GnFlow flow_plan(GnCall c, int sms) {
     // (and whole turns of the lanes fit a stage), but two pieces for every CTA where there are rows enough
     int64_t turns = 1;
     if (tiles == 1 && rows % lanes == 0)
-        while (turns < 64 && 2 * turns * rows * row <= (FLOW_KB << 10) && c.S * c.B >= 4 * turns * rows * f.grid) turns *= 2;
+        while (turns < 64 && 2 * turns * rows * row <= kFlowPiece && c.S * c.B >= 4 * turns * rows * f.grid) turns *= 2;
     rows *= turns;
     while ((c.S + rows - 1) / rows > 65535 && tiles == 1 && rows % lanes == 0) rows *= 2;
     f.rows = (int)std::min<int64_t>(rows, c.S);
     f.pieces = (int)((c.S + f.rows - 1) / f.rows);
-#ifndef FLOW_LAG
-#define FLOW_LAG 4
-#endif
-    f.lag = f.grid * FLOW_LAG / 4;
+    f.lag = f.grid;
     f.grid = (int)std::min<int64_t>(f.grid, c.B * f.pieces);
     if (c.B * f.pieces <= f.lag) f.lag = 0;  // one turn of the CTAs: nothing to put between
     f.smem += (size_t)f.depth * f.stage_bytes;

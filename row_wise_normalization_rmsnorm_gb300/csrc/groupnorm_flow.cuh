@@ -24,10 +24,7 @@
 
 namespace rmsn {
 
-#ifndef FLOW_CTAS
-#define FLOW_CTAS 2
-#endif
-constexpr int kFlowThreads = 256, kFlowCtas = FLOW_CTAS;  // that compute, of a CTA; CTAs an SM
+constexpr int kFlowThreads = 256, kFlowCtas = 2;  // that compute, of a CTA; CTAs an SM
 constexpr int kFlowAll = kFlowThreads + 64;  // threads of a CTA
 constexpr int kFlowStagesMost = 8;
 constexpr int kFlowMail = 4;

@@ -17,10 +17,7 @@
 
 namespace rmsn {
 
-#ifndef HELD_THREADS
-#define HELD_THREADS 256
-#endif
-constexpr int kHeldThreads = HELD_THREADS;
+constexpr int kHeldThreads = 256;
 constexpr int kHeldStages = 4;
 constexpr int kHeldCtas = 16;                 // of a cluster at most
 constexpr uint32_t kHeldWaitLimit = 1u << 20;  // polls of a piece's copies

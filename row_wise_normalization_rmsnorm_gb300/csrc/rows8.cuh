@@ -43,12 +43,10 @@ __device__ __forceinline__ float from_codes8(uint32_t b) {
 }
 // The code of v f, in the low byte: adding 1.5 2^23 rounds to a whole number,
 // ties to even (one fma: the product is exact). |v f| < 127.5 but for a block
-// at the largest scale, whose values are held to 127 steps first.
-__device__ __forceinline__ float held8(float v, float f) { return fminf(fmaxf(v, -127.f / f), 127.f / f); }
-__device__ __forceinline__ uint32_t code8(float v, float f) { return __float_as_uint(__fmaf_rn(v, f, 12582912.f)); }
-template <typename T> __device__ __forceinline__ uint8_t code8_of(float v, uint32_t b) {
-    const float f = to_codes8(b);
-    return (uint8_t)code8(b == MostScale<T>::b ? held8(v, f) : v, f);
+// at the largest scale, whose steps are held to 127.
+__device__ __forceinline__ float held8(float steps) { return fminf(fmaxf(steps, -127.f), 127.f); }
+__device__ __forceinline__ uint8_t code8(float v, uint32_t b) {
+    return (uint8_t)__float_as_uint(__fadd_rn(held8(__fmul_rn(v, to_codes8(b))), 12582912.f));
 }
 // Four codes, lowest byte first.
 __device__ __forceinline__ uint32_t codes8x4(float2 a, float2 b, float f) {
@@ -105,7 +103,7 @@ template <typename T, int E>
 __device__ __forceinline__ void keep_chunk(const uint32_t *w, bool here, uint32_t lanes, uint8_t *codes, uint8_t *scale) {
     const uint32_t b = scale8<T>(block_top<T, E>(w, lanes));
     if (!here) return;
-    const float f = to_codes8(b);
+    float f = to_codes8(b);
     float2 v[E / 2];
 #pragma unroll
     for (int q = 0; q < E / 2; ++q) {
@@ -118,7 +116,8 @@ __device__ __forceinline__ void keep_chunk(const uint32_t *w, bool here, uint32_
     }
     if (b == MostScale<T>::b) {
 #pragma unroll
-        for (int q = 0; q < E / 2; ++q) v[q] = make_float2(held8(v[q].x, f), held8(v[q].y, f));
+        for (int q = 0; q < E / 2; ++q) v[q] = make_float2(held8(v[q].x * f), held8(v[q].y * f));
+        f = 1.f;
     }
     if constexpr (E == 8)
         *reinterpret_cast<uint2 *>(codes) = make_uint2(codes8x4(v[0], v[1], f), codes8x4(v[2], v[3], f));

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(256) rows_fwd_any(const RowsParams p) {
         const float v = !in ? 0.f : SRC == kSrcPlain ? load_elem(src, j) : load_elem(h, j);
         if constexpr (KEEP) {
             const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v)));
-            if (in) p.codes[row * p.N + j] = code8_of<T>(v, b);
+            if (in) p.codes[row * p.N + j] = code8(v, b);
             if ((threadIdx.x & 31) == 0) p.scales[row * blocks + j0 / kBlock8] = (uint8_t)b;
         }
         if (in) {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(256) pack_any(const T *x, uint8_t *codes, uint
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
         const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v[k])));
-        if (k < run.n && j0 + k * kBlock8 < N) dst[k * kBlock8] = code8_of<T>(v[k], b);
+        if (k < run.n && j0 + k * kBlock8 < N) dst[k * kBlock8] = code8(v[k], b);
         if (lane == k) mine = b;
     }
     if (lane < run.n) scales[run.row * blocks + run.block + lane] = (uint8_t)mine;
