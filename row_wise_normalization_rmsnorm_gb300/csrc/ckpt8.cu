@@ -14,15 +14,15 @@ namespace rmsn {
 static const void *other_kernel(int which, int base) {
     return base == RMSNORM_BF16 ? rows_other_bf16(which) : base == RMSNORM_F16 ? rows_other_f16(which) : rows_other_f32(which);
 }
-static RowKernels fwd_kernel(int base, int src, int C, bool wide) {
-    return base == RMSNORM_BF16  ? rows_fwd_bf16(src, C, wide)
-           : base == RMSNORM_F16 ? rows_fwd_f16(src, C, wide)
-                                 : rows_fwd_f32(src, C, wide);
+static RowKernels fwd_kernel(int base, int src, int N, bool wide) {
+    return base == RMSNORM_BF16  ? rows_fwd_bf16(src, N, wide)
+           : base == RMSNORM_F16 ? rows_fwd_f16(src, N, wide)
+                                 : rows_fwd_f32(src, N, wide);
 }
-static RowKernels bwd_kernel(int base, bool fused, int C, bool wide) {
-    return base == RMSNORM_BF16  ? rows_bwd_bf16(fused, C, wide)
-           : base == RMSNORM_F16 ? rows_bwd_f16(fused, C, wide)
-                                 : rows_bwd_f32(fused, C, wide);
+static RowKernels bwd_kernel(int base, bool fused, int N, bool wide) {
+    return base == RMSNORM_BF16  ? rows_bwd_bf16(fused, N, wide)
+           : base == RMSNORM_F16 ? rows_bwd_f16(fused, N, wide)
+                                 : rows_bwd_f32(fused, N, wide);
 }
 
 static bool matrix(int64_t M, int64_t N, int dt) {
@@ -35,7 +35,7 @@ static bool scalars(float eps, float offset) { return std::isfinite(eps) && std:
 static rmsnorm_status_t run_fwd(RowsParams &p, int src, int dt, bool aligned, cudaStream_t s) {
     const int base = base_of(dt), E = 16 / bytes_of(dt);
     const bool wide = aligned && p.N % E == 0;
-    const RowKernels k = fwd_kernel(base, src, p.N / E, wide);
+    const RowKernels k = fwd_kernel(base, src, p.N, wide);
     const int teams = k.tpr == 0 || k.tpr >= 256 ? 1 : 256 / k.tpr;
     void *args[] = {&p};
     const int e = launch(k.fwd, (unsigned)((p.M + (int64_t)teams - 1) / teams), 1, k.tpr > 256 ? k.tpr : 256, 0, args, s);
@@ -57,7 +57,7 @@ constexpr int kBwdSmemWide = 220 * 1024;  // of a CTA of 512 threads: one an SM
 
 static bool bwd_plan(int64_t M, int64_t N, int dt, bool fused, bool wide, int sms, BwdPlan &b) {
     const int es = bytes_of(dt), E = 16 / es;
-    b.k = bwd_kernel(base_of(dt), fused, (int)(N / E), wide && N % E == 0);
+    b.k = bwd_kernel(base_of(dt), fused, (int)N, wide && N % E == 0);
     b.dw_rows = b.dw_parts = 0;
     if (b.k.tpr == 0) {
         b.threads = 256, b.rows = b.depth = 0, b.smem = 0, b.grid = (int)M;
@@ -65,6 +65,14 @@ static bool bwd_plan(int64_t M, int64_t N, int dt, bool fused, bool wide, int sm
         b.dw_rows = (int)std::max<int64_t>((M + want - 1) / want, 16);
         b.dw_parts = (int)((M + b.dw_rows - 1) / b.dw_rows);
         b.bytes = ((size_t)b.dw_parts * N * 4 + 255) / 256 * 256;
+        return true;
+    }
+    if (b.k.r == 0) {  // value by value
+        b.threads = 256, b.rows = b.depth = 0;
+        const int teams = b.threads / b.k.tpr;
+        b.smem = teams > 1 ? (size_t)N * 4 : 0;
+        b.grid = (int)std::min<int64_t>((M + teams - 1) / teams, (int64_t)4 * sms);
+        b.bytes = ((size_t)b.grid * N * 4 + 255) / 256 * 256;
         return true;
     }
     const int consumers = bwd_consumers(b.k.tpr);
@@ -112,7 +120,7 @@ static rmsnorm_status_t norm_bwd(const void *dy, const void *dres, const void *c
             void *dargs[] = {&p, &b.dw_rows};
             le = launch(other_kernel(kDwAny, base), (unsigned)((N + 255) / 256), (unsigned)b.dw_parts, 256, 0, dargs, s);
         }
-        if (le == 0) le = launch(b.k.fwd, (unsigned)b.grid, 1, b.threads, b.smem, args, s, b.k.tpr ? 1 : 0);
+        if (le == 0) le = launch(b.k.fwd, (unsigned)b.grid, 1, b.threads, b.smem, args, s, b.k.r ? 1 : 0);
         if (le == 0 && ws) {
             auto *fin = wb == 4 ? launch_dw_finalize_f32 : base == RMSNORM_BF16 ? launch_dw_finalize_bf16 : launch_dw_finalize_f16;
             le = fin(p.ws, b.k.tpr ? b.grid : b.dw_parts, (int)N, dw, nullptr, (int)N, 0, s, false, sms);
@@ -129,12 +137,14 @@ static bool id_type(int bytes) { return bytes == 4 || bytes == 8; }
 
 struct EmbedPlan {
     int ctas, share, bits, passes, tiles;  // the sort: CTAs of the cluster (0: launches over tiles)
-    int pieces, words;
+    int piece, pieces, words;
     size_t keys, vals, keys2, vals2, counts, present, open, ends, parts, bytes;
 };
 
 static EmbedPlan embed_plan(int64_t T, int64_t rows, int64_t N) {
     EmbedPlan p;
+    // tokens of a piece: a team adds them one batch after the other, so few tokens are cut finer
+    p.piece = T * N <= (int64_t)kEmbedSmall ? 8 : kEmbedPiece;
     int bits = 0;
     while (bits < 32 && (rows >> bits) != 0) ++bits;  // keys 0 .. rows
     p.passes = (bits + kSortBits - 1) / kSortBits;
@@ -148,7 +158,7 @@ static EmbedPlan embed_plan(int64_t T, int64_t rows, int64_t N) {
         while (p.ctas < kSortCluster && (int64_t)p.ctas * kSortThreads < T) p.ctas *= 2;
         p.share = (int)((T + p.ctas - 1) / p.ctas);
     }
-    p.pieces = (int)((T + kEmbedPiece - 1) / kEmbedPiece);
+    p.pieces = (int)((T + p.piece - 1) / p.piece);
     p.words = (int)((rows + 31) / 32);
     size_t at = 0;
     auto take = [&at](size_t n) {
@@ -353,7 +363,7 @@ extern "C" rmsnorm_status_t embed_bwd(const void *dh, const void *ids, void *dta
     const int C = (int)(wide ? N / E : N);
     EmbedSumParams p;
     std::memset(&p, 0, sizeof p);
-    p.dh = dh, p.dtable = dtable, p.rows = rows, p.T = (int)T, p.N = (int)N, p.pieces = b.pieces, p.accumulate = accumulate != 0;
+    p.dh = dh, p.dtable = dtable, p.rows = rows, p.T = (int)T, p.N = (int)N, p.piece = b.piece, p.pieces = b.pieces, p.accumulate = accumulate != 0;
     p.scale = scale;
     p.team = 8;
     while (p.team < 256 && p.team < C) p.team *= 2;

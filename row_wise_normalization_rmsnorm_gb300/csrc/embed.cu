@@ -3,8 +3,8 @@
 // Tokens are sorted by id, stably, so that a row's gradient is one run of
 // tokens in their order: its sum has one order whatever the launch does, with
 // no atomics on values. Runs are of very unlike lengths (a text's tokens
-// follow a power law), so the sorted tokens are cut into pieces of 32 that a
-// team each sums. A run inside a piece goes to its row at once; what a piece
+// follow a power law), so the sorted tokens are cut into pieces of 32 (few
+// tokens: 8) that a team each sums. A run inside a piece goes to its row at once; what a piece
 // has of a run that goes on beyond it is joined in a second launch.
 // Rows without a token are set to zero by other CTAs of the first launch.
 //
@@ -351,10 +351,10 @@ __global__ void __launch_bounds__(256) embed_sum(const EmbedSumParams p) {
     const int64_t item = (int64_t)blockIdx.x * teams + team;
     const int piece = (int)(item / p.slices);
     const int c = (int)(item - (int64_t)piece * p.slices) * p.team + t;
-    const int at = piece * kEmbedPiece;
-    const int n = piece < p.pieces ? min(kEmbedPiece, p.T - at) : 0;
+    const int at = piece * p.piece;
+    const int n = piece < p.pieces ? min(p.piece, p.T - at) : 0;
     // the piece's ids with a neighbour on either side, and its tokens
-    for (int i = t; i < kEmbedPiece + 2; i += p.team) {
+    for (int i = t; i < p.piece + 2; i += p.team) {
         const int g = at + i - 1;
         key[team][i] = n > 0 && i <= n + 1 && g >= 0 && g < p.T ? p.keys[g] : 0xffffffffu;  // of no row
         if (i < n) val[team][i] = p.vals[at + i];

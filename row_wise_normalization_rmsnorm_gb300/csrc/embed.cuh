@@ -7,7 +7,8 @@
 
 namespace rmsn {
 
-constexpr int kEmbedPiece = 32;      // sorted tokens that one team sums
+constexpr int kEmbedPiece = 32;      // sorted tokens that one team sums at most
+constexpr int kEmbedSmall = 8 << 20;  // values (of all tokens) up to which it is 8
 constexpr int kSortThreads = 1024;
 constexpr int kSortBits = 9;         // of an id, a pass at most
 constexpr int kSortBins = 1 << kSortBits;
@@ -34,7 +35,7 @@ struct EmbedSumParams {
     uint32_t *ends;     // [rows]: the piece where a row's run ends, for runs over several
     float *parts;       // [pieces, 2, N]: the sums of a piece's first row and of its last one, where they are not whole
     int64_t rows, early;
-    int T, N, pieces, team, accumulate;
+    int T, N, piece, pieces, team, accumulate;
     int sum_ctas, slices;  // CTAs that sum, column slices of a row
     float scale;
 };

@@ -3,6 +3,6 @@
 
 namespace rmsn {
 const void *rows_other_bf16(int which) { return rows_other_t<__nv_bfloat16>(which); }
-RowKernels rows_fwd_bf16(int src, int C, bool wide) { return rows_fwd_t<__nv_bfloat16>(src, C, wide); }
-RowKernels rows_bwd_bf16(bool fused, int C, bool wide) { return rows_bwd_t<__nv_bfloat16>(fused, C, wide); }
+RowKernels rows_fwd_bf16(int src, int N, bool wide) { return rows_fwd_t<__nv_bfloat16>(src, N, wide); }
+RowKernels rows_bwd_bf16(bool fused, int N, bool wide) { return rows_bwd_t<__nv_bfloat16>(fused, N, wide); }
 }  // namespace rmsn

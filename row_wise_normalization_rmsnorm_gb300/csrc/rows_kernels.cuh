@@ -137,8 +137,65 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) rows_fwd(const RowsPara
     }
 }
 
-// Rows of any length and alignment: a CTA a row, value by value. Consecutive
+// Rows of any alignment, value by value: a team of TPR threads (whole warps) a
+// row, K values a thread in registers, all loads under way at once. Consecutive
 // lanes take consecutive values, so a warp's 32 are a block.
+template <typename T, int TPR, int K, int SRC, bool KEEP>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) rows_fwd_lanes(const RowsParams p) {
+    constexpr int TEAMS = TPR >= 256 ? 1 : 256 / TPR, W = TPR / 32;
+    __shared__ float red[TEAMS][W];
+    pdl_wait();
+    pdl_trigger();
+    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+    const bool ok = row < p.M;
+    const T *src = nullptr;
+    if (ok) {
+        if constexpr (SRC == kSrcEmbed)
+            src = table_row<T>(p, row);
+        else
+            src = static_cast<const T *>(p.x) + row * p.N;
+    }
+    float v[K], r[SRC == kSrcAdd ? K : 1];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = k * TPR + t;
+        v[k] = src && j < p.N ? load_elem(src, j) : 0.f;
+        if constexpr (SRC == kSrcAdd) r[k] = src && j < p.N ? load_elem(static_cast<const T *>(p.residual) + row * p.N, j) : 0.f;
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = k * TPR + t;
+        if constexpr (SRC != kSrcPlain) {
+            v[k] = round_to(SRC == kSrcAdd ? v[k] + r[k] : v[k] * p.scale, static_cast<const T *>(nullptr));
+            if (ok && j < p.N) store_elem(static_cast<T *>(p.h) + row * p.N, j, v[k]);
+        }
+        ss = fmaf(v[k], v[k], ss);
+    }
+    if constexpr (SRC == kSrcEmbed) {
+        if (!p.y) return;
+    }
+    const float rstd = rstd_of(team_allreduce<TPR>(ss, red[team], t), p.N, p.eps);
+    if (ok && t == 0) p.rstd[row] = rstd;
+    const int blocks = (p.N + kBlock8 - 1) / kBlock8;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = k * TPR + t;
+        const bool in = ok && j < p.N;
+        if constexpr (KEEP) {
+            const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v[k])));
+            if (in) p.codes[row * p.N + j] = code8(v[k], b);
+            if (in && (t & 31) == 0) p.scales[row * blocks + j / kBlock8] = (uint8_t)b;
+        }
+        if (in) {
+            const float f = !p.w ? 1.f : p.offset + (p.w32 ? load_w(static_cast<const float *>(p.w), j) : load_w(static_cast<const T *>(p.w), j));
+            store_elem(static_cast<T *>(p.y) + row * p.N, j, v[k] * rstd * f);
+        }
+    }
+}
+
+// The same for rows of any length: a CTA a row, read twice.
 template <typename T, int SRC, bool KEEP>
 __global__ void __launch_bounds__(256) rows_fwd_any(const RowsParams p) {
     __shared__ float red[32];
@@ -562,7 +619,90 @@ __global__ void __launch_bounds__(bwd_consumers(TPR) + 32, TPR > 256 ? 1 : 2) ro
     }
 }
 
-// Any length and alignment: a CTA a row for dx ...
+// Rows of any alignment, value by value: persistent teams of TPR threads, a
+// row at a time, K values a thread and their columns' sums in registers.
+template <typename T, int TPR, int K, bool FUSED>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) rows_bwd_lanes(const RowsBwdParams p) {
+    constexpr int TEAMS = TPR >= 256 ? 1 : 256 / TPR, W = TPR / 32;
+    __shared__ float red[2][TEAMS][W];
+    extern __shared__ __align__(16) uint8_t stages[];  // several teams: [N] floats
+    pdl_wait();
+    pdl_trigger();
+    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    const int nb = (p.N + kBlock8 - 1) / kBlock8;
+    float f[K], dw[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = k * TPR + t;
+        f[k] = !p.w ? 1.f : j >= p.N ? 0.f : p.offset + (p.w32 ? load_w(static_cast<const float *>(p.w), j) : load_w(static_cast<const T *>(p.w), j));
+        dw[k] = 0.f;
+    }
+    int flip = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * TEAMS; r0 < p.M; r0 += (int64_t)gridDim.x * TEAMS, flip ^= 1) {
+        const int64_t row = r0 + team;
+        const bool ok = row < p.M;
+        const T *dy = static_cast<const T *>(p.dy) + row * p.N;
+        const float rstd = ok ? p.rstd[row] : 0.f;
+        // (all loads before the first use)
+        T raw[K];
+        int8_t code[K];
+        uint8_t scale[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = k * TPR + t;
+            if (ok && j < p.N) {
+                raw[k] = dy[j];
+                code[k] = (int8_t)p.codes[row * p.N + j];
+                scale[k] = p.scales[row * nb + j / kBlock8];
+            }
+        }
+        float d[K], xh[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool in = ok && k * TPR + t < p.N;
+            d[k] = in ? load_elem(&raw[k], 0) : 0.f;
+            xh[k] = in ? decode8(code[k]) * (rstd * from_codes8(scale[k])) : 0.f;
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float x = d[k] * xh[k];
+            dw[k] += x;
+            s = fmaf(x, f[k], s);
+        }
+        const float c1 = team_allreduce<TPR>(s, red[flip][team], t) / (float)p.N;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = k * TPR + t;
+            if (ok && j < p.N) {
+                float v = rstd * fmaf(xh[k], -c1, d[k] * f[k]);
+                if constexpr (FUSED) v += load_elem(static_cast<const T *>(p.dres) + row * p.N, j);
+                store_elem(static_cast<T *>(p.dx) + row * p.N, j, v);
+            }
+        }
+    }
+    if (p.ws) {
+        float *acc = reinterpret_cast<float *>(stages);
+        for (int m = 0; m < TEAMS; ++m) {
+            __syncthreads();
+            if (team == m) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int j = k * TPR + t;
+                    if (j < p.N) {
+                        const float z = m == 0 ? dw[k] : acc[j] + dw[k];
+                        if (m == TEAMS - 1)
+                            p.ws[(int64_t)blockIdx.x * p.N + j] = z;
+                        else
+                            acc[j] = z;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Any length: a CTA a row for dx, read twice ...
 template <typename T, bool FUSED>
 __global__ void __launch_bounds__(256) rows_bwd_any(const RowsBwdParams p) {
     __shared__ float red[32];
@@ -617,22 +757,34 @@ struct TeamSize {
     X(8, 1, 2) X(32, 1, 2) X(32, 2, 2) X(64, 2, 2) X(128, 2, 2) X(128, 3, 1) X(256, 2, 2) X(256, 3, 1) X(512, 2, 2) X(512, 3, 1) X(512, 4, 1)
 #define ROWS_BWD_TEAMS4(X) X(512, 6, 1) X(512, 8, 1)
 
+// Value by value: threads a row and values a thread.
+#define ROWS_FWD_LANES(X) X(32, 1) X(32, 4) X(32, 16) X(128, 8) X(256, 8) X(256, 16) X(256, 32) X(512, 32)
+// (backward of longer rows: a row's loads wait for one another's results in so few
+// threads. 12000 x 5003: 600 us so, 420 in two launches of a CTA a row)
+#define ROWS_BWD_LANES(X) X(32, 1) X(32, 4) X(32, 16) X(128, 8)
+
 struct RowKernels {
     const void *fwd;
-    int tpr, v, r;  // 0: a CTA a row, any length
+    int tpr, v, r;  // r 0: value by value; tpr 0: a CTA a row, any length
 };
 
-template <typename T, int SRC, bool KEEP> static RowKernels rows_fwd_pick(int C, bool wide) {
+template <typename T, int SRC, bool KEEP> static RowKernels rows_fwd_pick(int N, bool wide) {
+    const int C = N / Elem<T>::E;
     if (wide) {
 #define X(tpr, v) \
     if (C <= tpr * v) return {(const void *)rows_fwd<T, tpr, v, SRC, KEEP>, tpr, v, 1};
         ROWS_FWD_TEAMS(X)
 #undef X
     }
+#define X(tpr, v) \
+    if (N <= tpr * v) return {(const void *)rows_fwd_lanes<T, tpr, v, SRC, KEEP>, tpr, v, 0};
+    ROWS_FWD_LANES(X)
+#undef X
     return {(const void *)rows_fwd_any<T, SRC, KEEP>, 0, 0, 0};
 }
 
-template <typename T, bool FUSED> static RowKernels rows_bwd_pick(int C, bool wide) {
+template <typename T, bool FUSED> static RowKernels rows_bwd_pick(int N, bool wide) {
+    const int C = N / Elem<T>::E;
     if (wide) {
 #define X(tpr, v, r) \
     if (C <= tpr * v) return {(const void *)rows_bwd<T, tpr, v, r, FUSED>, tpr, v, r};
@@ -642,6 +794,10 @@ template <typename T, bool FUSED> static RowKernels rows_bwd_pick(int C, bool wi
         }
 #undef X
     }
+#define X(tpr, v) \
+    if (N <= tpr * v) return {(const void *)rows_bwd_lanes<T, tpr, v, FUSED>, tpr, v, 0};
+    ROWS_BWD_LANES(X)
+#undef X
     return {(const void *)rows_bwd_any<T, FUSED>, 0, 0, 0};
 }
 
@@ -657,19 +813,19 @@ template <typename T> static const void *rows_other_t(int which) {
     default: return (const void *)rows_dw_any<T>;
     }
 }
-template <typename T> static RowKernels rows_fwd_t(int src, int C, bool wide) {
-    return src == kSrcPlain ? rows_fwd_pick<T, kSrcPlain, true>(C, wide)
-           : src == kSrcAdd ? rows_fwd_pick<T, kSrcAdd, true>(C, wide)
-                            : rows_fwd_pick<T, kSrcEmbed, false>(C, wide);
+template <typename T> static RowKernels rows_fwd_t(int src, int N, bool wide) {
+    return src == kSrcPlain ? rows_fwd_pick<T, kSrcPlain, true>(N, wide)
+           : src == kSrcAdd ? rows_fwd_pick<T, kSrcAdd, true>(N, wide)
+                            : rows_fwd_pick<T, kSrcEmbed, false>(N, wide);
 }
-template <typename T> static RowKernels rows_bwd_t(bool fused, int C, bool wide) {
-    return fused ? rows_bwd_pick<T, true>(C, wide) : rows_bwd_pick<T, false>(C, wide);
+template <typename T> static RowKernels rows_bwd_t(bool fused, int N, bool wide) {
+    return fused ? rows_bwd_pick<T, true>(N, wide) : rows_bwd_pick<T, false>(N, wide);
 }
 
 #define ROWS_DECLARE(suf)                                   \
     const void *rows_other_##suf(int which);                \
-    RowKernels rows_fwd_##suf(int src, int C, bool wide);   \
-    RowKernels rows_bwd_##suf(bool fused, int C, bool wide);
+    RowKernels rows_fwd_##suf(int src, int N, bool wide);   \
+    RowKernels rows_bwd_##suf(bool fused, int N, bool wide);
 ROWS_DECLARE(f32)
 ROWS_DECLARE(bf16)
 ROWS_DECLARE(f16)
