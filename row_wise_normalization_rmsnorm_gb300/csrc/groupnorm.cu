@@ -51,6 +51,7 @@ struct GnHeld {
 };
 
 constexpr size_t kHeldSmem = 112 * 1024;  // of a CTA: two an SM
+constexpr int kHeldGroups = 256;          // of a cluster at most
 
 // What a cut needs; false: it does not fit.
 static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
@@ -58,7 +59,7 @@ static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
     const int64_t W = (int64_t)K * cg, rows = (c.S + ctas - 1) / ctas;
     const bool span = K < c.G;
     // a span is whole chunks, of 64 bytes a row at least; kept in whole blocks of 32
-    if (W > 4096 || K > 256 || (span && (c.chunk == 1 || W % E != 0 || W * es < 64))) return false;
+    if (W > 4096 || c.B * (c.G / K) * ctas > 0x7fffffffLL || (span && (c.chunk == 1 || W % E != 0 || W * es < 64))) return false;
     if (keep && W % kBlock8 != 0) return false;
     const int xb = c.kept ? 1 : es;
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
@@ -79,7 +80,7 @@ static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
     GnHeld best{0, 0, 0, 0, {0, 0}, 0, 0};
     double least = 0;
     const int es = bytes_of(c.dt);
-    for (int K = 1; K <= c.G; ++K) {
+    for (int K = 1; K <= c.G && K <= kHeldGroups; ++K) {
         if (c.G % K != 0) continue;
         for (int n = 1; n <= kHeldCtas; n *= 2) {
             GnHeld h;

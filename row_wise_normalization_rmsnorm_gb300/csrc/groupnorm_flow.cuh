@@ -31,7 +31,7 @@ constexpr int kFlowMail = 4;
 constexpr int kFlowFan = 16;
 constexpr uint32_t kFlowWaitLimit = 1u << 22;  // polls of 100 ns for a sample's statistics
 constexpr uint32_t kFlowMailLimit = 1u << 25;  // polls of 200 ns for the next summed piece
-constexpr uint32_t kFlowCopyLimit = 1u << 24;  // polls of a stage (a wait for its reader or its copies)
+constexpr uint32_t kFlowCopyLimit = 1u << 22;  // polls of a stage (a wait for its reader or its copies)
 
 struct FlowParams {
     GnParams g;          // rows: of a piece
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
                     }
                 }
                 const float m = s1 / (last < n ? each * (float)(n - 1) + final : each * (float)n);
-                return make_float2(ref + m, fmaxf(s2 - s1 * m, 0.f));
+                return make_float2(ref + m, at_least_0(s2 - s1 * m));
             };
             flow_join(p, fs, join, [&](int b, int k, float2 v) {
                 const float r = 1.f / sqrtf(v.y / ((float)g.S * (float)g.cg) + g.eps);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
                     },
                     [&](int k, int lo, int hi, float2 v) {
                         const float w = (float)(hi - lo), off = v.x / w, cnt = (float)f.rows * w;
-                        float m = lane_mean[lo - c0] + off, m2 = fmaxf(v.y - (float)f.rows * v.x * off, 0.f);
+                        float m = lane_mean[lo - c0] + off, m2 = at_least_0(v.y - (float)f.rows * v.x * off);
                         if (lo > k * g.cg) {
                             const float2 a = acc[k];
                             const float na = (float)f.rows * (float)(lo - k * g.cg), d = m - a.x, share = cnt / (na + cnt);

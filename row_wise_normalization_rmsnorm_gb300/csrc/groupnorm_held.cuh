@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
         },
         [&](int k, int lo, int, float2 m) {
             const float d = m.x * inv_cg;
-            own[k] = make_float2(ch_mean[lo] + d, fmaxf(m.y - (float)at.rows * m.x * d, 0.f));
+            own[k] = make_float2(ch_mean[lo] + d, at_least_0(m.y - (float)at.rows * m.x * d));
         });
     __syncthreads();
     for (int i = threadIdx.x; i < p.K * p.ctas; i += kHeldThreads) st_cluster2(&exch[at.rank * p.K + i % p.K], (uint32_t)(i / p.K), own[i % p.K]);

@@ -311,13 +311,15 @@ template <int E> __device__ __forceinline__ void put_v(float *to, const float (&
         for (int i = 0; i < E; ++i) to[i] = v[i];
     }
 }
+// A sum of squares that cancellation left below 0 is 0; a NaN stays.
+__device__ __forceinline__ float at_least_0(float v) { return v < 0.f ? 0.f : v; }
 template <int E> __device__ __forceinline__ void lane_stats(int n, const float (&minus_K)[E], const float (&s1)[E], const float (&s2)[E], float *mean, float *m2) {
     const float inv = n > 0 ? 1.f / (float)n : 0.f;
     float m[E], q[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         m[i] = s1[i] * inv;
-        q[i] = fmaxf(s2[i] - s1[i] * m[i], 0.f);
+        q[i] = at_least_0(s2[i] - s1[i] * m[i]);
         m[i] -= minus_K[i];
     }
     put_v(mean, m);
@@ -341,7 +343,7 @@ template <int THREADS> __device__ __forceinline__ void join_lanes(float *mean, f
         }
         const float m = s * all;
         mean[c] = ref + m;
-        m2[c] = fmaxf(q - s * m, 0.f);
+        m2[c] = at_least_0(q - s * m);
     }
 }
 // For each group with channels among [c0, c1): both values of its channels

@@ -493,6 +493,28 @@ def test_groupnorm_nan_stays_in_its_group(rn):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("S,C,G", [(100, 64, 8), (40000, 32, 4), (30, 33, 3)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_groupnorm_of_what_is_not_finite(rn, S, C, G, bad):
+    """One value that is no number leaves no number in its group (the mean is not finite, the variance none), and
+    every other group its bits."""
+    g = gen(6)
+    x, dy = normal(g, 2, S, C), normal(g, 2, S, C)
+    clean = rn.groupnorm_fwd(x, None, None, G, act="silu")
+    at = (1, S // 2, C // 2)
+    x[at] = bad
+    f = rn.groupnorm_fwd(x, None, None, G, act="silu")
+    lo = (C // 2) // (C // G) * (C // G)
+    hit = slice(lo, lo + C // G)
+    assert bool(torch.isnan(f["rstd"][1, lo // (C // G)])) and bool(torch.isnan(f["y"][1, :, hit]).all())
+    b = rn.groupnorm_bwd(dy, x, None, None, f["mean"], f["rstd"], G, act="silu", want_dbeta=False)
+    assert bool(torch.isnan(b["dx"][1, :, hit]).all())
+    f["y"][1, :, hit] = clean["y"][1, :, hit]
+    assert torch.equal(f["y"], clean["y"])
+    b["dx"][1, :, hit] = 0
+    assert bool(torch.isfinite(b["dx"]).all())
+
+
 # ----------------------------------------------------------------- embedding --
 
 EMBED_SHAPES = [(1, 10, 64), (8, 1000, 8192), (33, 50, 100), (1000, 300, 33), (257, 7, 4096), (5000, 2, 24), (300, 100000, 128),
