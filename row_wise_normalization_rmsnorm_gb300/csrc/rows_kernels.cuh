@@ -8,7 +8,8 @@
 //             g = dy (offset + w),  c = (1/N) sum g xhat,  dx = rstd (g - xhat c) [+ dres],  dw = sum dy xhat
 //
 // All of it is bound by memory: bytes a value of bf16 are 5.03 for the
-// forward with its checkpoint (x, y, code), 5.03 for the backward.
+// forward with its checkpoint (x, y, code), 5.03 for the backward. 16384 x 8192
+// in bf16: 115 us (5.9 TB/s) and 123 us (5.5), of 101 at the rate of a copy.
 #pragma once
 
 #include "rows8.cuh"
