@@ -344,6 +344,20 @@ struct Run {
         n = row < M ? min(kRun, blocks - block) : 0;
     }
 };
+// A run's blocks: FULL, all kRun of them whole (no test a value).
+template <typename T, bool FULL>
+__device__ __forceinline__ void pack_run(const T *src, uint8_t *dst, int left, uint32_t &mine) {
+    const int lane = threadIdx.x & 31;
+    float v[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) v[k] = FULL || k * kBlock8 < left ? load_elem(src, k * kBlock8) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v[k])));
+        if (FULL || k * kBlock8 < left) dst[k * kBlock8] = code8(v[k], b);
+        if (lane == k) mine = b;
+    }
+}
 template <typename T>
 __global__ void __launch_bounds__(256) pack_any(const T *x, uint8_t *codes, uint8_t *scales, int64_t M, int N) {
     pdl_wait();
@@ -353,19 +367,27 @@ __global__ void __launch_bounds__(256) pack_any(const T *x, uint8_t *codes, uint
     const int j0 = run.block * kBlock8 + lane;
     const T *src = x + run.row * N + j0;
     uint8_t *dst = codes + run.row * N + j0;
-    float v[kRun];
     uint32_t mine = 0;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) v[k] = k < run.n && j0 + k * kBlock8 < N ? load_elem(src, k * kBlock8) : 0.f;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-        const uint32_t b = scale8<T>(__reduce_max_sync(0xffffffffu, abs_bits(v[k])));
-        if (k < run.n && j0 + k * kBlock8 < N) dst[k * kBlock8] = code8(v[k], b);
-        if (lane == k) mine = b;
-    }
+    if (run.n == kRun && (run.block + kRun) * kBlock8 <= N)  // (the same in the whole warp)
+        pack_run<T, true>(src, dst, 0, mine);
+    else
+        pack_run<T, false>(src, dst, run.n > 0 ? N - j0 : 0, mine);
     if (lane < run.n) scales[run.row * blocks + run.block + lane] = (uint8_t)mine;
 }
 
+template <typename T, bool FULL>
+__device__ __forceinline__ void unpack_run(const uint8_t *src, T *dst, int left, float f) {
+    uint8_t c[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) c[k] = FULL || k * kBlock8 < left ? src[k * kBlock8] : (uint8_t)0;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        // (as decode8x4)
+        const float v = __uint_as_float(((uint32_t)c[k] ^ 0x80u) | 0x4b000000u) - 8388736.f;
+        if (FULL || k * kBlock8 < left) store_elem(dst, k * kBlock8, v * fk);
+    }
+}
 template <typename T>
 __global__ void __launch_bounds__(256) unpack_any(const uint8_t *codes, const uint8_t *scales, T *x, int64_t M, int N) {
     pdl_wait();
@@ -375,15 +397,11 @@ __global__ void __launch_bounds__(256) unpack_any(const uint8_t *codes, const ui
     const int j0 = run.block * kBlock8 + lane;
     const uint8_t *src = codes + run.row * N + j0;
     T *dst = x + run.row * N + j0;
-    int8_t c[kRun];
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) c[k] = k < run.n && j0 + k * kBlock8 < N ? (int8_t)src[k * kBlock8] : (int8_t)0;
     const float f = lane < run.n ? from_codes8(scales[run.row * blocks + run.block + lane]) : 0.f;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        if (k < run.n && j0 + k * kBlock8 < N) store_elem(dst, k * kBlock8, decode8(c[k]) * fk);
-    }
+    if (run.n == kRun && (run.block + kRun) * kBlock8 <= N)
+        unpack_run<T, true>(src, dst, 0, f);
+    else
+        unpack_run<T, false>(src, dst, run.n > 0 ? N - j0 : 0, f);
 }
 
 __device__ __forceinline__ uint2 lds64(const void *p) {
