@@ -118,9 +118,12 @@ struct GnFlow {
 // channels spill, with 4 a row of more than 1024 channels is several tiles.
 static int flow_chunk(int chunk, int64_t C) { return chunk > 4 && C <= 4 * kFlowThreads ? 4 : chunk; }
 
-// Bytes of a stage and of a piece at most. (256 x 256 x 256, 8 images: 154 us;
-// pieces of 128 KB 152, of 64 KB 158; a lag of half the CTAs 183.)
-constexpr int64_t kFlowStage = 28 << 10, kFlowPiece = 256 << 10;
+// Bytes of a stage, and of a piece at most: small pieces are summed, joined and
+// normalised sooner, large ones cost fewer joins. (256 x 256 x 256, 8 images:
+// pieces of 128 KB and a lag of one and a half rounds of the CTAs 144 us, of 256
+// KB and one round 154, of 64 KB and one round 158. The gradient, which reads two
+// tensors a piece: 281 and 267 with the first two.)
+constexpr int64_t kFlowStage = 28 << 10, kFlowPiece = 128 << 10, kFlowBwdPiece = 256 << 10;
 constexpr size_t kFlowSmem = 226 * 1024 / kFlowCtas, kFlowSmemMost = 224 * 1024;  // of a CTA; of the only one on an SM
 
 static GnFlow flow_plan(GnCall c, int sms) {
@@ -152,14 +155,14 @@ static GnFlow flow_plan(GnCall c, int sms) {
     // (and whole turns of the lanes fit a stage), but two pieces for every CTA where there are rows enough
     int64_t turns = 1;
     if (tiles == 1 && rows % lanes == 0)
-        while (turns < 64 && 2 * turns * rows * row <= kFlowPiece && c.S * c.B >= 4 * turns * rows * f.grid) turns *= 2;
+        while (turns < 64 && 2 * turns * rows * row <= (c.backward ? kFlowBwdPiece : kFlowPiece) && c.S * c.B >= 4 * turns * rows * f.grid) turns *= 2;
     rows *= turns;
     while ((c.S + rows - 1) / rows > 65535 && tiles == 1 && rows % lanes == 0) rows *= 2;
     f.rows = (int)std::min<int64_t>(rows, c.S);
     f.pieces = (int)((c.S + f.rows - 1) / f.rows);
-    f.lag = f.grid;
+    f.lag = c.backward ? f.grid : f.grid * 3 / 2;
     f.grid = (int)std::min<int64_t>(f.grid, c.B * f.pieces);
-    if (c.B * f.pieces <= f.lag) f.lag = 0;  // one turn of the CTAs: nothing to put between
+    if (c.B * f.pieces <= f.grid) f.lag = 0;  // one turn of the CTAs: nothing to put between
     f.smem += (size_t)f.depth * f.stage_bytes;
     size_t at = 0;
     auto take = [&at](size_t n) {
