@@ -575,7 +575,9 @@ typedef enum {
  * mean, rstd [B, G] fp32; gamma, beta [C] or NULL (1 and 0). The variance is
  * summed about the pieces' own means and joined, so a mean far from 0 costs
  * no digits. fp32 throughout, y rounded once. y may equal x.
- * codes, scales: NULL, or x kept in 8 bits as by ckpt8_pack of [B S, C].
+ * codes, scales: NULL, or x kept in 8 bits as by ckpt8_pack of [B S, C] (the
+ * work may then be cut another way: y, mean and rstd may differ in their last
+ * bits from those of the call without).
  * S == 0 sets mean and rstd to 0. INVALID_ARG also: C % G != 0, C >
  * ROWS_MAX_CHANNELS, an unknown act. UNSUPPORTED: G > ROWS_MAX_GROUPS.
  */
@@ -601,8 +603,31 @@ rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const void *codes,
                                rmsnorm_dtype_t dt, rmsnorm_stream_t stream);
 
 /* Workspace bytes of groupnorm_fwd (backward 0) or groupnorm_bwd on the
- * current device; 0 for invalid sizes or without a device. */
+ * current device, enough for arrays of any alignment, with x kept in 8 bits
+ * or not; 0 where no such call takes any, for invalid sizes or without a
+ * device. */
 size_t groupnorm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward);
+
+/* How groupnorm_fwd or groupnorm_bwd cuts a call. */
+typedef struct {
+    int32_t chunk;   /* values of an access: 8 or 4 neighbours, or 1                   */
+    int32_t cluster; /* CTAs that hold whole groups of a sample; 0: pieces by ticket   */
+    int32_t groups;  /* that a cluster takes (0 by pieces)                             */
+    int32_t rows;    /* places that a CTA of a cluster holds, or of a piece            */
+    int32_t stages;  /* that a CTA keeps under way (0 in a cluster)                    */
+    int32_t smem_bytes;
+    int64_t workspace_bytes;
+} groupnorm_plan_t;
+
+/* The cut for these sizes, launching nothing. kept: the forward writes codes,
+ * the backward reads them in the place of x. row_align, code_align: a power of
+ * two that the addresses of x and y (dy, x and dx) and of codes are multiples
+ * of (16: any larger one too); row_align 0: workspace_bytes alone is set, to
+ * the most of all alignments, kept or not. num_sms > 0: for a device of that
+ * many SMs, no device is needed; 0: the current one. */
+rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward,
+                                      int kept, int32_t row_align, int32_t code_align, int32_t num_sms,
+                                      groupnorm_plan_t *plan);
 
 /*
  * Embedding rows: h_t = R(scale table[id_t]), table [rows, N], ids [T] int32

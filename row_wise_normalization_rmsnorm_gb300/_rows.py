@@ -88,7 +88,8 @@ def groupnorm_bwd_ckpt8(dy, codes, scales, gamma, beta, mean, rstd, groups: int,
 
 
 def groupnorm_workspace_bytes(batch: int, places: int, channels: int, groups: int, dtype, *, backward=False) -> int:
-    """Bytes of workspace groupnorm_fwd (or _bwd) takes for these sizes on the current device."""
+    """Bytes of workspace that groupnorm_fwd (or _bwd) and its _ckpt8 form take at most for these sizes on the current
+    device, wherever the arrays lie."""
     return _ext().workspace(batch, places, channels, groups, _code(dtype), bool(backward))
 
 

@@ -21,19 +21,32 @@ static const void *gn_flow(int base, bool backward, int chunk, int act, bool kep
 struct GnCall {
     int64_t B, S, C;
     int G, act, dt;
-    bool backward, kept;
+    bool backward;
+    bool kept;  // backward: x comes as codes; forward: codes are written in the same pass
     int chunk;  // values of a chunk: 8 or 4 of them, or single ones
 };
 
-// The widest chunk, up to 16 bytes, that the rows (and their codes) are whole
-// numbers of, on its boundary.
-static int chunk_of(int64_t C, int es, std::initializer_list<const void *> rows, const void *codes) {
-    for (int chunk = 16 / es; chunk >= 4; chunk /= 2) {
-        bool fine = C % chunk == 0 && on(codes, (uintptr_t)chunk);
-        for (const void *p : rows) fine = fine && on(p, (uintptr_t)(chunk * es));
-        if (fine) return chunk;
-    }
+// The largest power of two, up to 16, that all addresses are multiples of.
+static int align_of(std::initializer_list<const void *> rows) {
+    uintptr_t all = 16;
+    for (const void *p : rows) all |= (uintptr_t)p;
+    return (int)(all & (~all + 1));
+}
+
+// The widest chunk, up to 16 bytes, that the rows (and the codes that are read)
+// are whole numbers of, on its boundary.
+static int chunk_of(int64_t C, int es, int row_align, int code_align) {
+    for (int chunk = 16 / es; chunk >= 4; chunk /= 2)
+        if (C % chunk == 0 && row_align >= chunk * es && code_align >= chunk) return chunk;
     return 1;
+}
+
+// A call whose arrays lie on these boundaries. The forward keeps x in its own
+// pass where rows are whole blocks of chunks, else by a launch of ckpt8_pack.
+static GnCall gn_call(int64_t B, int64_t S, int64_t C, int64_t G, int act, int dt, bool backward, bool kept, int row_align, int code_align) {
+    GnCall c{B, S, C, (int)G, act, dt, backward, kept, chunk_of(C, bytes_of(dt), row_align, backward && kept ? code_align : 16)};
+    if (!backward) c.kept = kept && c.chunk > 1 && C % kBlock8 == 0 && code_align >= c.chunk;
+    return c;
 }
 
 static const void *gn_held(int base, bool backward, int chunk, int act, bool kept) {
@@ -54,17 +67,18 @@ constexpr size_t kHeldSmem = 112 * 1024;  // of a CTA: two an SM
 constexpr int kHeldGroups = 256;          // of a cluster at most
 
 // What a cut needs; false: it does not fit.
-static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
+static bool held_cut(const GnCall &c, int K, int ctas, GnHeld &h) {
     const int es = bytes_of(c.dt), E = c.chunk, cg = (int)(c.C / c.G);
     const int64_t W = (int64_t)K * cg, rows = (c.S + ctas - 1) / ctas;
     const bool span = K < c.G;
     // a span is whole chunks, of 64 bytes a row at least; kept in whole blocks of 32
     if (W > 4096 || c.B * (c.G / K) * ctas > 0x7fffffffLL || (span && (c.chunk == 1 || W % E != 0 || W * es < 64))) return false;
-    if (keep && W % kBlock8 != 0) return false;
-    const int xb = c.kept ? 1 : es;
+    if (!c.backward && c.kept && W % kBlock8 != 0) return false;
+    const bool codes = c.backward && c.kept;
+    const int xb = codes ? 1 : es;
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     const int64_t x = up(rows * W * xb + 16), d = c.backward ? up(rows * W * es + 16) : 0;
-    const int64_t sc = c.kept ? up(rows * (W / kBlock8 + 2)) : 0;
+    const int64_t sc = codes ? up(rows * (W / kBlock8 + 2)) : 0;
     const int64_t fixed = kHeldThreads * E * 8 + W * 8 + (int64_t)ctas * K * 8 + K * 16;  // (statistics: the CTAs', the cluster's, this CTA's)
     if (x + d + sc + fixed > (int64_t)kHeldSmem) return false;
     h = GnHeld{ctas, K, (int)W, (int)rows, {(uint32_t)x, (uint32_t)d}, (uint32_t)sc, (size_t)(x + d + sc + fixed)};
@@ -76,7 +90,7 @@ static bool held_cut(const GnCall &c, int K, int ctas, bool keep, GnHeld &h) {
 // that begins or ends inside a 32-byte sector counted with the whole sector.
 // (The gradient of 8 x 4096 x 320: spans of 80 bytes in clusters of 8 take 33
 // us, of 160 bytes in clusters of 16 39, the flow 57.)
-static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
+static GnHeld held_plan(const GnCall &c, int sms) {
     GnHeld best{0, 0, 0, 0, {0, 0}, 0, 0};
     double least = 0;
     const int es = bytes_of(c.dt);
@@ -84,7 +98,7 @@ static GnHeld held_plan(const GnCall &c, int sms, bool keep) {
         if (c.G % K != 0) continue;
         for (int n = 1; n <= kHeldCtas; n *= 2) {
             GnHeld h;
-            if ((n > 1 && (c.S + n - 1) / n * (n - 1) >= c.S) || !held_cut(c, K, n, keep, h)) continue;
+            if ((n > 1 && (c.S + n - 1) / n * (n - 1) >= c.S) || !held_cut(c, K, n, h)) continue;
             const double row = (double)h.W * es, sectors = K == c.G || (h.W * es) % 32 == 0 ? row : row + 32;
             const double bytes = (double)c.B * c.S * c.C * es * (c.backward ? 3 : 2) * (sectors / row);
             // clusters of 16 leave SMs without a CTA where a GPU's groups of SMs are no multiple of 8
@@ -126,12 +140,13 @@ static int flow_chunk(int chunk, int64_t C) { return chunk > 4 && C <= 4 * kFlow
 constexpr int64_t kFlowStage = 28 << 10, kFlowPiece = 128 << 10, kFlowBwdPiece = 256 << 10;
 constexpr size_t kFlowSmem = 226 * 1024 / kFlowCtas, kFlowSmemMost = 224 * 1024;  // of a CTA; of the only one on an SM
 
-static GnFlow flow_plan(GnCall c, int sms) {
+static GnFlow flow_plan(const GnCall &c, int sms) {
     GnFlow f;
-    const int es = bytes_of(c.dt), E = c.chunk, xb = c.kept ? 1 : es;
+    const bool codes = c.backward && c.kept;
+    const int es = bytes_of(c.dt), E = c.chunk, xb = codes ? 1 : es;
     const int64_t CC = c.C / E, tiles = (CC + kFlowThreads - 1) / kFlowThreads,
                   cols = tiles > 1 ? ((CC + tiles - 1) / tiles + 7) / 8 * 8 : CC, lanes = kFlowThreads / cols;
-    const int64_t nb = c.kept ? (c.C + kBlock8 - 1) / kBlock8 : 0;
+    const int64_t nb = codes ? (c.C + kBlock8 - 1) / kBlock8 : 0;
     f.smem = 2 * sizeof(float) * kFlowThreads * E + (size_t)c.G * sizeof(float2);
     // stages: three at least, of whole turns of the lanes
     const int64_t row = c.C * (c.backward ? xb + es : es) + nb;
@@ -141,7 +156,7 @@ static GnFlow flow_plan(GnCall c, int sms) {
         f.offset[0] = 0;
         f.offset[1] = (uint32_t)up(rows * c.C * xb);
         f.offset[2] = f.offset[1] + (uint32_t)(c.backward ? up(rows * c.C * es) : 0);
-        f.offset[3] = f.offset[2] + (uint32_t)(c.kept ? up(rows * nb) : 0);
+        f.offset[3] = f.offset[2] + (uint32_t)(codes ? up(rows * nb) : 0);
         f.stage_bytes = f.offset[3] + (uint32_t)up((int64_t)c.G * 8);
         return (int64_t)f.stage_bytes;
     };
@@ -185,6 +200,29 @@ static GnFlow flow_plan(GnCall c, int sms) {
     }
     f.bytes = at;
     return f;
+}
+
+// The cut of a call and the workspace that it takes: what the calls launch by
+// and what the queries answer from.
+struct GnCut {
+    GnCall c;  // with the chunk of the kernels that run
+    GnHeld h;
+    GnFlow f;  // where h.ctas is 0
+    size_t bytes;
+};
+static GnCut gn_cut(const GnCall &c, int sms) {
+    GnCut k;
+    std::memset(&k, 0, sizeof k);
+    k.c = c;
+    k.h = held_plan(c, sms);
+    if (k.h.ctas) {
+        k.bytes = c.backward ? held_bytes(c, k.h) : 0;
+    } else {
+        if (c.backward) k.c.chunk = flow_chunk(c.chunk, c.C);
+        k.f = flow_plan(k.c, sms);
+        k.bytes = k.f.bytes;
+    }
+    return k;
 }
 
 static bool gn_sizes(int64_t B, int64_t S, int64_t C, int64_t G, int act, int dt) {
@@ -263,23 +301,21 @@ static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const Gn
     return e == 0 ? RMSNORM_SUCCESS : head_cuda_fail(e);
 }
 
-static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, bool backward) {
-    int sms = 0;
-    if (!gn_sizes(B, S, C, G, 0, dt) || B == 0 || S == 0 || current_device(&sms, nullptr) != 0) return 0;
+// The most that any alignment takes, with x kept in 8 bits or not.
+static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, bool backward, int sms) {
     size_t most = 0;
-    for (int chunk : {8, 4, 1}) {
-        if (C % chunk != 0) continue;
-        for (int kept = 0; kept < (backward ? 2 : 1); ++kept) {
-            GnCall c{B, S, C, (int)G, 0, dt, backward, kept != 0, chunk};
-            const GnHeld h = held_plan(c, sms, false);
-            if (h.ctas)
-                most = backward ? std::max(most, held_bytes(c, h)) : most;
-            else {
-                if (backward) c.chunk = flow_chunk(c.chunk, C);
-                most = std::max(most, flow_plan(c, sms).bytes);
+    for (int row = 16; row > 0; row /= 2)
+        for (int code = 16; code > 0; code /= 2)
+            for (int kept = 0; kept < 2; ++kept) {
+                // each cut once: of the least alignment that gives its chunk
+                const GnCall c = gn_call(B, S, C, G, 0, dt, backward, kept != 0, row, code);
+                if (row > 1 && c.chunk == gn_call(B, S, C, G, 0, dt, backward, kept != 0, row / 2, code).chunk) continue;
+                if (code > 1) {
+                    const GnCall less = gn_call(B, S, C, G, 0, dt, backward, kept != 0, row, code / 2);
+                    if (c.chunk == less.chunk && c.kept == less.kept) continue;
+                }
+                most = std::max(most, gn_cut(c, sms).bytes);
             }
-        }
-    }
     return most;
 }
 
@@ -304,25 +340,21 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     int sms = 0, *status = nullptr;
     const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
-    GnCall c{B, S, C, (int)G, act, dt, false, false, chunk_of(C, es, {x, y}, nullptr)};
+    const GnCut k = gn_cut(gn_call(B, S, C, G, act, dt, false, codes != nullptr, align_of({x, y}), align_of({codes})), sms);
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.gamma = gamma, p.beta = beta, p.out = y, p.mean = mean, p.rstd = rstd;
     p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G);
     p.magic = p.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + p.cg - 1) / p.cg);
     p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32, p.eps = eps;
-    // the codes in the same pass where rows are whole blocks of chunks
-    const bool fused = codes && c.chunk > 1 && C % kBlock8 == 0 && on(codes, (uintptr_t)c.chunk);
-    if (fused) p.codes = static_cast<uint8_t *>(codes), p.scales = scales;
-    if (codes && !fused) {  // first: y may be x
+    if (k.c.kept) p.codes = static_cast<uint8_t *>(codes), p.scales = scales;
+    if (codes && !k.c.kept) {  // first: y may be x
         const rmsnorm_status_t st = ckpt8_pack(x, codes, scales, B * S, C, (rmsnorm_dtype_t)base, stream);
         if (st != RMSNORM_SUCCESS) return st;
     }
-    const GnHeld h = held_plan(c, sms, fused);
-    if (h.ctas) return gn_run_held(p, c, h, nullptr, nullptr, sms, status, s);
-    const GnFlow f = flow_plan(c, sms);
-    return with_workspace(workspace, workspace_bytes, f.bytes, s,
-                          [&](char *w) { return gn_run_flow(p, c, f, w, nullptr, nullptr, sms, status, s); });
+    if (k.h.ctas) return gn_run_held(p, k.c, k.h, nullptr, nullptr, sms, status, s);
+    return with_workspace(workspace, workspace_bytes, k.bytes, s,
+                          [&](char *w) { return gn_run_flow(p, k.c, k.f, w, nullptr, nullptr, sms, status, s); });
 }
 
 extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const void *codes, const uint8_t *scales,
@@ -343,7 +375,7 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     int sms = 0, *status = nullptr;
     const int e = current_device(&sms, &status);
     if (e != 0) return head_cuda_fail(e);
-    GnCall c{B, S, C, (int)G, act, dt, true, codes != nullptr, chunk_of(C, es, {dy, dx, x}, codes)};
+    const GnCut k = gn_cut(gn_call(B, S, C, G, act, dt, true, codes != nullptr, align_of({dy, dx, x}), align_of({codes})), sms);
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.dy = dy, p.codes_in = static_cast<const uint8_t *>(codes), p.scales_in = scales;
@@ -351,18 +383,39 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G);
     p.magic = p.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + p.cg - 1) / p.cg);
     p.w32 = (dt & RMSNORM_WEIGHT_F32) || base == RMSNORM_F32;
-    const GnHeld h = held_plan(c, sms, false);
-    if (h.ctas)
-        return with_workspace(workspace, workspace_bytes, held_bytes(c, h), s, [&](char *w) {
-            p.parts = reinterpret_cast<float *>(w);
-            return gn_run_held(p, c, h, dgamma, dbeta, sms, status, s);
-        });
-    c.chunk = flow_chunk(c.chunk, C);
-    const GnFlow f = flow_plan(c, sms);
-    return with_workspace(workspace, workspace_bytes, f.bytes, s,
-                          [&](char *w) { return gn_run_flow(p, c, f, w, dgamma, dbeta, sms, status, s); });
+    return with_workspace(workspace, workspace_bytes, k.bytes, s, [&](char *w) {
+        if (!k.h.ctas) return gn_run_flow(p, k.c, k.f, w, dgamma, dbeta, sms, status, s);
+        p.parts = reinterpret_cast<float *>(w);
+        return gn_run_held(p, k.c, k.h, dgamma, dbeta, sms, status, s);
+    });
+}
+
+extern "C" rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward,
+                                                 int kept, int32_t row_align, int32_t code_align, int32_t num_sms,
+                                                 groupnorm_plan_t *plan) {
+    if (!plan || !gn_sizes(B, S, C, G, 0, dt) || num_sms < 0 || row_align < 0 || code_align < 0) return RMSNORM_ERR_INVALID_ARG;
+    if (G > ROWS_MAX_GROUPS) return RMSNORM_ERR_UNSUPPORTED;
+    std::memset(plan, 0, sizeof *plan);
+    if (B == 0 || S == 0) return RMSNORM_SUCCESS;
+    int sms = num_sms;
+    if (sms == 0) {
+        const int e = current_device(&sms, nullptr);
+        if (e != 0) return head_cuda_fail(e);
+    }
+    if (row_align == 0) {
+        plan->workspace_bytes = (int64_t)gn_workspace(B, S, C, G, dt, backward != 0, sms);
+        return RMSNORM_SUCCESS;
+    }
+    const GnCut k = gn_cut(gn_call(B, S, C, G, 0, dt, backward != 0, kept != 0, row_align, code_align), sms);
+    plan->chunk = k.c.chunk, plan->cluster = k.h.ctas, plan->groups = k.h.K;
+    plan->rows = k.h.ctas ? k.h.rows : k.f.rows;
+    plan->stages = k.h.ctas ? 0 : k.f.depth;
+    plan->smem_bytes = (int32_t)(k.h.ctas ? k.h.smem : k.f.smem);
+    plan->workspace_bytes = (int64_t)k.bytes;
+    return RMSNORM_SUCCESS;
 }
 
 extern "C" size_t groupnorm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward) {
-    return gn_workspace(B, S, C, G, dt, backward != 0);
+    groupnorm_plan_t plan;
+    return groupnorm_plan_query(B, S, C, G, dt, backward, 0, 0, 0, 0, &plan) == RMSNORM_SUCCESS ? (size_t)plan.workspace_bytes : 0;
 }

@@ -287,6 +287,21 @@ struct Places {
     }
 };
 
+// The largest power of two, up to 16, that the addresses are multiples of.
+int32_t align_of(std::initializer_list<const void *> at) {
+    uintptr_t all = 16;
+    for (const void *q : at) all |= reinterpret_cast<uintptr_t>(q);
+    return (int32_t)(all & (~all + 1));
+}
+// Workspace bytes of a group norm whose row arrays (and codes, or NULL) lie
+// there; 0 for a call that will be refused.
+size_t gn_need(const Places &p, int dt, bool backward, std::initializer_list<const void *> rows, const void *codes) {
+    groupnorm_plan_t plan;
+    const rmsnorm_status_t st = groupnorm_plan_query(p.B, p.S, p.C, p.G, (rmsnorm_dtype_t)dt, backward, codes != nullptr,
+                                                     align_of(rows), align_of({codes}), 0, &plan);
+    return st == RMSNORM_SUCCESS ? (size_t)plan.workspace_bytes : 0;
+}
+
 // gn_fwd(x, gamma, beta, groups, act, eps, keep, y, mean, rstd, codes, scales, workspace, stream)
 //   -> y, mean, rstd, codes, scales
 PyObject *gn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -310,7 +325,7 @@ PyObject *gn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
             scales.emplace(a[11], "scales", scales_shape(x.sizes()), at::kByte, x, s);
         }
         OnDevice on(x);
-        Workspace ws(a[12], a[12] == Py_None ? groupnorm_workspace_bytes(p.B, p.S, p.C, p.G, code(dt), 0) : 0, x, s);
+        Workspace ws(a[12], a[12] == Py_None && !s.named ? gn_need(p, dt, false, {ptr(x), y.p}, keep ? codes->p : nullptr) : 0, x, s);
         rmsnorm_status_t st;
         Py_BEGIN_ALLOW_THREADS
         st = groupnorm_fwd(ptr(x), gamma, beta, y.p, static_cast<float *>(mean.p), static_cast<float *>(rstd.p),
@@ -357,7 +372,8 @@ PyObject *gn_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (want_gamma) dgamma.emplace(a[13], "dgamma", at::IntArrayRef{p.C}, pt, dy, s);
         if (want_beta) dbeta.emplace(a[14], "dbeta", at::IntArrayRef{p.C}, pt, dy, s);
         OnDevice on(dy);
-        Workspace ws(a[15], a[15] == Py_None ? groupnorm_workspace_bytes(p.B, p.S, p.C, p.G, code(dt), 1) : 0, dy, s);
+        Workspace ws(a[15], a[15] == Py_None && !s.named ? gn_need(p, dt, true, {ptr(dy), dx.p, x ? ptr(*x) : nullptr}, codes ? ptr(*codes) : nullptr) : 0,
+                     dy, s);
         rmsnorm_status_t st;
         Py_BEGIN_ALLOW_THREADS
         st = groupnorm_bwd(ptr(dy), x ? ptr(*x) : nullptr, codes ? ptr(*codes) : nullptr,
