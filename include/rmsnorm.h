@@ -629,6 +629,16 @@ rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C, int64_t G
                                       int kept, int32_t row_align, int32_t code_align, int32_t num_sms,
                                       groupnorm_plan_t *plan);
 
+/* For tests of what a launch by pieces does where a wait gives up:
+ * groupnorm_fwd of x (dy NULL, eps 1e-5) into out, or groupnorm_bwd of dy and x,
+ * without parameters or an activation, of which one sample is counted wrongly and so
+ * never joined; the wait for it ends after `polls` polls (of about 1 us). The
+ * launch ends, sets the device status, and leaves in out what the rows that it
+ * did not normalise had there, that sample's among them. */
+rmsnorm_status_t groupnorm_give_up_check(const void *dy, const void *x, float *mean, float *rstd, void *out, int64_t B,
+                                         int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int64_t sample,
+                                         uint32_t polls, rmsnorm_stream_t stream);
+
 /*
  * Embedding rows: h_t = R(scale table[id_t]), table [rows, N], ids [T] int32
  * or int64 (id_bytes 4 or 8). A token whose id is negative or not below

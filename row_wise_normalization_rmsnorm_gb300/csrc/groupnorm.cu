@@ -263,8 +263,14 @@ static rmsnorm_status_t gn_run_held(const GnParams &g, const GnCall &c, const Gn
     return e == 0 ? RMSNORM_SUCCESS : head_cuda_fail(e);
 }
 
+// A sample whose pieces are never joined, and the polls that are made for it.
+struct GnLose {
+    int64_t sample;
+    uint32_t polls;
+};
+
 static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const GnFlow &f, char *w, void *dgamma, void *dbeta,
-                                    int sms, int *status, cudaStream_t s) {
+                                    int sms, int *status, cudaStream_t s, const GnLose *lose = nullptr) {
     const int base = base_of(c.dt);
     FlowParams p;
     std::memset(&p, 0, sizeof p);
@@ -279,8 +285,10 @@ static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const Gn
     p.state = reinterpret_cast<uint32_t *>(w + f.state);
     p.fans = f.fans;
     p.part = reinterpret_cast<float2 *>(w + f.part), p.fan = reinterpret_cast<float2 *>(w + f.fan), p.stat = reinterpret_cast<float2 *>(w + f.stat);
+    p.stat_limit = lose ? lose->polls : kFlowStatLimit;
     p.status = status;
     int e = (int)cudaMemsetAsync(p.state, 0, f.state_bytes, s);
+    if (e == 0 && lose) e = (int)cudaMemsetAsync(p.state + 2 + c.B + lose->sample, 0x40, 4, s);  // a count that the sample's pieces do not end
     void *args[] = {&p};
     if (e == 0)
         e = launch(gn_flow(base, c.backward, c.chunk, c.act, c.backward ? c.kept : g.codes != nullptr), (unsigned)f.grid, 1, kFlowAll,
@@ -418,4 +426,29 @@ extern "C" rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C
 extern "C" size_t groupnorm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward) {
     groupnorm_plan_t plan;
     return groupnorm_plan_query(B, S, C, G, dt, backward, 0, 0, 0, 0, &plan) == RMSNORM_SUCCESS ? (size_t)plan.workspace_bytes : 0;
+}
+
+extern "C" rmsnorm_status_t groupnorm_give_up_check(const void *dy, const void *x, float *mean, float *rstd, void *out, int64_t B,
+                                                    int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int64_t sample,
+                                                    uint32_t polls, rmsnorm_stream_t stream) {
+    if (!gn_sizes(B, S, C, G, 0, dt) || base_of(dt) != dt || B == 0 || S == 0 || G > ROWS_MAX_GROUPS || sample < 0 || sample >= B || polls == 0)
+        return RMSNORM_ERR_INVALID_ARG;
+    const int es = bytes_of(dt);
+    if (!x || !out || !mean || !rstd || !on(x, es) || !on(out, es) || !on(dy, es) || !on(mean, 4) || !on(rstd, 4)) return RMSNORM_ERR_INVALID_ARG;
+    int sms = 0, *status = nullptr;
+    const int e = current_device(&sms, &status);
+    if (e != 0) return head_cuda_fail(e);
+    GnCall c = gn_call(B, S, C, G, 0, dt, dy != nullptr, false, align_of({dy, x, out}), 16);
+    if (dy) c.chunk = flow_chunk(c.chunk, C);
+    const GnFlow f = flow_plan(c, sms);
+    GnParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = x, p.dy = dy, p.out = out, p.mean = mean, p.rstd = rstd;
+    p.S = S, p.B = (int)B, p.C = (int)C, p.G = (int)G, p.cg = (int)(C / G);
+    p.magic = p.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + p.cg - 1) / p.cg);
+    p.eps = 1e-5f;
+    const GnLose lose{sample, polls};
+    return with_workspace(nullptr, 0, f.bytes, (cudaStream_t)stream, [&](char *w) {
+        return gn_run_flow(p, c, f, w, nullptr, nullptr, sms, status, (cudaStream_t)stream, &lose);
+    });
 }

@@ -33,9 +33,11 @@ constexpr int kFlowAll = kFlowThreads + 64;  // threads of a CTA
 constexpr int kFlowStagesMost = 8;
 constexpr int kFlowMail = 4;
 constexpr int kFlowFan = 16;
-constexpr uint32_t kFlowWaitLimit = 1u << 24;  // polls of 100 ns for a sample's statistics
-constexpr uint32_t kFlowMailLimit = 1u << 25;  // polls of 100 ns for the next summed piece
-constexpr uint32_t kFlowCopyLimit = 1u << 22;  // polls of a stage (a wait for its reader or its copies)
+// Polls before a wait gives up, each wait longer than those it depends on.
+constexpr uint32_t kFlowStatLimit = 1u << 22;   // of a sample's statistics (with 100 ns between: some 4 s)
+constexpr uint32_t kFlowEmptyLimit = 1u << 22;  // of a stage's readers (a failed poll takes 1.4 us: 6 s)
+constexpr uint32_t kFlowFullLimit = 1u << 23;   // of a stage's copies
+constexpr uint32_t kFlowMailLimit = 1u << 27;   // of the mailbox (with 100 ns between)
 
 struct FlowParams {
     GnParams g;          // rows: of a piece
@@ -48,6 +50,7 @@ struct FlowParams {
     float2 *part;        // [B, pieces, G]
     float2 *fan;         // [B, fans, G]
     float2 *stat;        // [B, G]: (-mean, rstd), or the negated means of u gamma and of u gamma xhat
+    uint32_t stat_limit; // polls of them before the launch gives up
     int *status;
 };
 
@@ -60,6 +63,19 @@ __device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 __device__ __forceinline__ void flow_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFlowThreads) : "memory"); }
+// The same, and true in all computing threads where `v` is in one.
+__device__ __forceinline__ bool flow_sync_any(bool v) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)v), "n"(kFlowThreads)
+        : "memory");
+    return any != 0;
+}
 __device__ __forceinline__ void flow_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -94,19 +110,20 @@ __device__ __forceinline__ void flow_copies(const FlowParams &p, FlowShared &s, 
     unsigned long long drawn = atomicAdd(next, 1ull);
     int stage = 0;
     uint32_t phase = 1;
+    bool round = false;  // the ring has gone round once
     auto advance = [&]() {
-        if (++stage == p.depth) stage = 0, phase ^= 1u;
+        if (++stage == p.depth) stage = 0, phase ^= 1u, round = true;
     };
-    bool failed = false;
-    while (!failed) {
+    bool stuck = false, failed = false;  // no stage came free, or a sample was not joined
+    while (!stuck && !failed) {
         const int64_t ticket = (int64_t)drawn;
         if (ticket >= p.tickets) break;
         drawn = atomicAdd(next, 1ull);  // (read when this one's copies are under way)
         const FlowPiece f(p, ticket);
         if (!f.there) continue;
-        for (int r = 0; r < f.rows && !failed; r += p.stage_rows, advance()) {
-            if (!mbar_wait(&s.empty[stage], phase, kFlowCopyLimit)) {
-                failed = true;
+        for (int r = 0; r < f.rows; r += p.stage_rows, advance()) {
+            if (!mbar_wait(&s.empty[stage], phase, kFlowEmptyLimit)) {
+                stuck = true;
                 break;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -122,9 +139,14 @@ __device__ __forceinline__ void flow_copies(const FlowParams &p, FlowShared &s, 
             const bool stats = f.normalise && r == 0;
             Cover cs;
             if (stats) {
-                uint32_t k = 0;
-                while (ld_acquire(p.state + 2 + f.b) == 0 && ++k < kFlowWaitLimit) __nanosleep(100);
-                if (k >= kFlowWaitLimit) failed = true;
+                for (uint32_t k = 0; ld_acquire(p.state + 2 + f.b) == 0;) {
+                    if (++k >= p.stat_limit) {
+                        failed = true;
+                        break;
+                    }
+                    __nanosleep(100);
+                }
+                if (failed) break;
                 asm volatile("fence.proxy.async;" ::: "memory");
                 cs = cover16(p.stat + (int64_t)f.b * p.g.G, (uint32_t)p.g.G * 8u);
                 bytes += cs.bytes;
@@ -136,21 +158,37 @@ __device__ __forceinline__ void flow_copies(const FlowParams &p, FlowShared &s, 
             for (int i = 0; i < N; ++i) bulk_g2s(to + (i ? p.offset[i] : 0u), c[i].src, c[i].bytes, &s.full[stage]);
         }
     }
-    if (failed && p.status) *p.status = 1;
-    if (mbar_wait(&s.empty[stage], phase, kFlowCopyLimit)) {
+    if ((stuck || failed) && p.status) *p.status = 1;
+    // No copy is under way once this CTA has ended, whoever still waits for it:
+    // the last of each stage, of this round of the ring or (from `stage` on) of the one before.
+    for (int i = 0; i < p.depth; ++i)
+        if (i < stage || round) mbar_wait(&s.full[i], i < stage ? phase ^ 1u : phase, kFlowFullLimit);
+    if (!stuck && mbar_wait(&s.empty[stage], phase, kFlowEmptyLimit)) {
         s.ticket[stage] = -1;
         flow_arrive(&s.full[stage]);
     }
 }
-// The stages as the computing threads take them.
+// The stages as the computing threads take them. Where a wait gives up, or the
+// later stages of a piece do not come, the whole CTA ends its work. The lanes
+// of a warp decide that together, at each stage. A warp that ends goes to the
+// last barrier (flow_end); the others meet it there or behind the rows of
+// their next sum, whichever comes first, and both of these barriers tell all
+// threads that one has failed, so that none goes on to another. No thread can
+// fail between two barriers of one sum.
 struct FlowStages {
     int stage;
     uint32_t phase;
     bool failed;
     // the stage's piece (-1: no more, or the wait gave up)
     __device__ __forceinline__ int64_t wait(FlowShared &s) {
-        if (!failed && !mbar_wait(&s.full[stage], phase, kFlowCopyLimit)) failed = true;
+        if (!failed && !mbar_wait(&s.full[stage], phase, kFlowFullLimit)) failed = true;
+        failed = __any_sync(0xffffffffu, failed);
         return failed ? -1 : s.ticket[stage];
+    }
+    // the next stage of this piece; false: it does not come
+    __device__ __forceinline__ bool more(FlowShared &s, int64_t ticket) {
+        if (wait(s) != ticket) failed = true;
+        return !failed;
     }
     __device__ __forceinline__ void release(const FlowParams &p, FlowShared &s) {
         __syncwarp();
@@ -173,17 +211,30 @@ __device__ __forceinline__ void flow_setup(const FlowParams &p, FlowShared &s) {
     __syncthreads();
 }
 
-// The computing threads tell the joining warp that a piece is summed, its sums
-// stored (-1: that no more come).
-__device__ __forceinline__ void flow_tell(FlowShared &s, int64_t item) {
+// Thread 0 tells the joining warp that a piece is summed (-1: that no more
+// come). False: the mailbox stayed full.
+__device__ __forceinline__ bool flow_mail(FlowShared &s, int64_t item) {
+    volatile FlowShared &v = s;
+    for (uint32_t k = 0; v.sent - v.taken >= kFlowMail; ++k) {
+        if (k >= kFlowMailLimit) return false;
+        __nanosleep(100);
+    }
+    v.mail[v.sent % kFlowMail] = item;
+    __threadfence_block();
+    v.sent = v.sent + 1;
+    return true;
+}
+// A piece is summed and its sums are stored.
+__device__ __forceinline__ void flow_tell(FlowShared &s, FlowStages &at, int64_t item) {
     flow_sync();
+    if (threadIdx.x == 0 && !flow_mail(s, item)) at.failed = true;
+}
+// The computing threads' end; `met`: they have left a sum together.
+__device__ __forceinline__ void flow_end(const FlowParams &p, FlowShared &s, const FlowStages &at, bool met) {
+    const bool failed = met || flow_sync_any(at.failed);
     if (threadIdx.x == 0) {
-        volatile FlowShared &v = s;
-        uint32_t k = 0;
-        while (v.sent - v.taken >= kFlowMail && ++k < kFlowWaitLimit) __nanosleep(100);
-        v.mail[v.sent % kFlowMail] = item;
-        __threadfence_block();
-        v.sent = v.sent + 1;
+        if (failed && p.status) *p.status = 1;
+        flow_mail(s, -1);
     }
 }
 // True in the whole warp where this was the last of `n` to count: what the
@@ -211,8 +262,12 @@ template <class Join, class Give> __device__ __forceinline__ void flow_join(cons
     for (uint32_t n = 0;; ++n) {
         uint32_t k = 0;
         while (v.sent == n && ++k < kFlowMailLimit) __nanosleep(100);
+        if (!__any_sync(0xffffffffu, v.sent != n)) {
+            if (lane == 0 && p.status) *p.status = 1;
+            return;
+        }
         __threadfence_block();
-        const int64_t item = v.sent == n ? -1 : v.mail[n % kFlowMail];
+        const int64_t item = v.mail[n % kFlowMail];
         __syncwarp();
         if (lane == 0) v.taken = n + 1;
         if (item < 0) return;
@@ -279,6 +334,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
     const Cut cut(CC, kFlowThreads);
     const uint32_t ring0 = smem_u32(ring);
     FlowStages at{0, 0u, false};
+    bool met = false;
     for (int64_t ticket; (ticket = at.wait(fs)) >= 0;) {
         const FlowPiece f(p, ticket);
         if (!f.normalise) {
@@ -292,7 +348,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
                 fill_v(0.f, s2);
                 int n = 0;
                 for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
-                    if (r0 > 0) at.wait(fs);
+                    if (r0 > 0 && !at.more(fs, ticket)) break;
                     const uint32_t rows = ring0 + (uint32_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + (f.first + r0) * pitch);
                     const int more = in ? rows_of_lane(min(p.stage_rows, f.rows - r0), cut.lane, cut.lanes) : 0;
                     sum_rows<T, E>(rows + (uint32_t)cut.lane * pitch + cc * (E * sizeof(T)), more, (uint32_t)cut.lanes * pitch, n, K, s1, s2);
@@ -300,7 +356,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
                     if (t0 + cut.cols >= CC) at.release(p, fs);
                 }
                 lane_stats(n, K, s1, s2, lane_mean + threadIdx.x * E, lane_m2 + threadIdx.x * E);
-                flow_sync();
+                if ((met = flow_sync_any(at.failed))) break;
                 join_lanes<kFlowThreads>(lane_mean, lane_m2, cut.cols * E, cut.lanes, f.rows);
                 flow_sync();
                 // a group's channels of this tile, joined with those of the tiles before
@@ -327,7 +383,8 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
                     });
                 if (t0 + cut.cols < CC) flow_sync();
             }
-            flow_tell(fs, f.item);
+            if (met) break;
+            flow_tell(fs, at, f.item);
             continue;
         }
         float minus_mean[E], f_[E], beta[E];
@@ -341,7 +398,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
             mul_v(f_, gamma, f_);
         };
         for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
-            if (r0 > 0) at.wait(fs);
+            if (r0 > 0 && !at.more(fs, ticket)) break;
             const int64_t first = f.first + r0;
             const uint32_t stage = ring0 + (uint32_t)at.stage * p.stage_bytes + addr_mod16(static_cast<const char *>(g.x) + first * pitch);
             const int rows = min(p.stage_rows, f.rows - r0);
@@ -370,8 +427,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_fwd_flow(const FlowPar
             at.release(p, fs);
         }
     }
-    flow_tell(fs, -1);
-    if (at.failed && threadIdx.x == 0 && p.status) *p.status = 1;
+    flow_end(p, fs, at, met);
 }
 
 template <typename T, int E, int ACT, bool KEPT>
@@ -442,6 +498,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowPar
         gn_slope<T, ACT>(xhat, u, minus_mean, rstd, gamma, beta);
     };
     FlowStages at{0, 0u, false};
+    bool met = false;
     for (int64_t ticket; (ticket = at.wait(fs)) >= 0;) {
         const FlowPiece f(p, ticket);
         auto constants = [&](int cc, float (&minus_mean)[E], float (&rstd)[E], float (&gamma)[E], float (&beta)[E]) {
@@ -472,7 +529,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowPar
                 fill_v(0.f, s);
                 if (in) constants(cc, minus_mean, rstd, gamma, beta);
                 for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
-                    if (r0 > 0) at.wait(fs);
+                    if (r0 > 0 && !at.more(fs, ticket)) break;
                     Walk w = walk(at.stage, f.first + r0, cc);
                     const int n = in ? rows_of_lane(min(p.stage_rows, f.rows - r0), cut.lane, cut.lanes) : 0;
 #pragma unroll 2
@@ -486,7 +543,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowPar
                 }
                 put_v(lane_a + threadIdx.x * E, a);
                 put_v(lane_s + threadIdx.x * E, s);
-                flow_sync();
+                if ((met = flow_sync_any(at.failed))) break;
                 const int width = cut.cols * E, c0 = t0 * E, c1 = min(c0 + width, g.C);
                 for (int c = threadIdx.x; c < c1 - c0; c += kFlowThreads) {
                     float ta = lane_a[c], ts = lane_s[c];
@@ -515,13 +572,14 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowPar
                     });
                 if (t0 + cut.cols < CC) flow_sync();
             }
-            flow_tell(fs, f.item);
+            if (met) break;
+            flow_tell(fs, at, f.item);
             continue;
         }
         const float2 *stat = reinterpret_cast<const float2 *>(ring + (size_t)at.stage * p.stage_bytes + p.offset[3] + addr_mod16(p.stat + (int64_t)f.b * g.G));
         float minus_mean[E], rstd[E], gamma[E], beta[E], m1[E], m2[E];
         for (int r0 = 0; r0 < f.rows; r0 += p.stage_rows) {
-            if (r0 > 0) at.wait(fs);
+            if (r0 > 0 && !at.more(fs, ticket)) break;
             const int64_t first = f.first + r0;
             const int rows = min(p.stage_rows, f.rows - r0);
             for (int t0 = 0; t0 < CC; t0 += cut.cols) {
@@ -547,8 +605,7 @@ __global__ void __launch_bounds__(kFlowAll, kFlowCtas) gn_bwd_flow(const FlowPar
             at.release(p, fs);
         }
     }
-    flow_tell(fs, -1);
-    if (at.failed && threadIdx.x == 0 && p.status) *p.status = 1;
+    flow_end(p, fs, at, met);
 }
 
 // Many rows of sums folded into gridDim.y: row i of the result is the sum of

@@ -1,10 +1,13 @@
 """Group norms of samples that no cluster holds (pieces by ticket), against the
 definitions and tolerances of test_gpu_rows: their workspaces, streams, graphs,
 in-place results and rings of stages."""
+import ctypes
+
 import pytest
 import torch
 
-from test_gpu_rows import TYPES, bits, check_kept, gen, gn_backward, gn_forward, half_step, kept, near, normal, offset_view, rn  # noqa: F401
+from test_gpu_rows import TYPES, bits, check_kept, gen, gn_forward, half_step, near, normal, rn  # noqa: F401
+from test_rows_plan_cpu import Plan
 
 pytestmark = pytest.mark.gpu
 
@@ -21,6 +24,12 @@ def check_forward(out, x, gamma, beta, G, act):
     near(out["mean"], mean, em, "mean")
     near(out["rstd"], rstd, er, "rstd")
     near(out["y"], y, half_step(t) * y.abs() + ey + 2.0 ** -25 * (t == torch.float16), "y")
+
+
+def cut(rn, B, S, C, G, t, backward=False, kept=False, row=16, code=16):
+    p, dt = Plan(), {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t]
+    assert rn.lib().groupnorm_plan_query(B, S, C, G, dt, backward, kept, row, code, 0, ctypes.byref(p)) == 0
+    return p
 
 
 def full_workspace(rn, shape, G, t, backward=False):
@@ -46,3 +55,32 @@ def test_the_keeping_forward_has_the_workspace_that_it_takes(rn, dt, B, S, C, G)
     assert all(torch.equal(bits(again[k]), bits(out[k])) for k in out)
     with pytest.raises(rn.RMSNormError):
         rn.groupnorm_fwd_ckpt8(x, gamma, beta, G, act="silu", workspace=ws[:256])
+
+
+# ------------------------------------------------------ a wait that gives up --
+
+@pytest.mark.parametrize("dt,B,S,C,G,stages", [("bf16", 2, 140000, 128, 8, 2), ("f32", 3, 3000, 1030, 10, 1), ("f16", 2, 5001, 321, 3, 1)])
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("lost", [0, 1])
+def test_a_launch_whose_wait_gives_up_ends_and_says_so(rn, dt, B, S, C, G, stages, backward, lost):
+    """One sample is never joined and the wait for it is a short one: the launch ends, the status word is set, no row
+    is written that was not normalised, and the next call is as ever."""
+    t, status = TYPES[dt], rn.lib().rmsnorm_device_status
+    x, dy = sample(1, B, S, C, t)[0], normal(gen(2), B, S, C, dt=t)
+    p = cut(rn, B, S, C, G, t, backward)
+    assert p.cluster == 0 and p.stages >= 2 and (stages == 1 or p.rows * C * x.element_size() > 2 * 28 * 1024)
+    f = rn.groupnorm_fwd(x, None, None, G)
+    want = rn.groupnorm_bwd(dy, x, None, None, f["mean"], f["rstd"], G, want_dbeta=False)["dx"] if backward else f["y"]
+    assert status(0) == 0
+    out, mean, rstd = torch.full_like(x, 7.0), f["mean"].clone(), f["rstd"].clone()
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t]
+    got = rn.lib().groupnorm_give_up_check(dy.data_ptr() if backward else None, x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                           out.data_ptr(), B, S, C, G, code, lost, 2000, torch.cuda.current_stream().cuda_stream)
+    assert got == 0
+    torch.cuda.synchronize()
+    assert status(1) == 1 and status(0) == 0
+    assert bool((out[lost] == 7).all())
+    untouched = (out == 7).all(-1)
+    assert torch.equal(out[~untouched], want[~untouched])
+    again = rn.groupnorm_fwd(x, None, None, G)
+    assert torch.equal(bits(again["y"]), bits(f["y"])) and status(0) == 0

@@ -71,3 +71,13 @@ def test_plan_queries_refuse(rn):
     assert ask(1, 64, 8192, 8192, BF16, 0, 0, 16, 16, 152, p) == UNSUPPORTED
     for none in ((0, 64), (2, 0)):
         assert plan(rn, *none, 64, 8, BF16).workspace_bytes == 0
+
+
+GIVE_UP = {"dy": None, "x": 4096, "mean": 4096, "rstd": 4096, "out": 4096, "B": 2, "S": 64, "C": 64, "G": 8, "dt": BF16, "sample": 0,
+           "polls": 100, "stream": None}
+
+
+@pytest.mark.parametrize("bad", [{"x": None}, {"out": None}, {"mean": None}, {"rstd": None}, {"x": 4097}, {"dy": 4097}, {"B": 0}, {"S": 0},
+                                 {"G": 7}, {"dt": 5}, {"dt": BF16 | W32}, {"sample": 2}, {"sample": -1}, {"polls": 0}, {"C": 8192, "G": 8192}])
+def test_the_check_of_a_wait_that_gives_up_refuses(rn, bad):
+    assert rn.lib().groupnorm_give_up_check(*{**GIVE_UP, **bad}.values()) == INVALID
