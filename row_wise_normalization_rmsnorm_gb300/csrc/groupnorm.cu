@@ -148,7 +148,7 @@ static GnFlow flow_plan(const GnCall &c, int sms) {
                   cols = tiles > 1 ? ((CC + tiles - 1) / tiles + 7) / 8 * 8 : CC, lanes = kFlowThreads / cols;
     const int64_t nb = codes ? (c.C + kBlock8 - 1) / kBlock8 : 0;
     f.smem = 2 * sizeof(float) * kFlowThreads * E + (size_t)c.G * sizeof(float2);
-    // stages: three at least, of whole turns of the lanes
+    // stages: three at least, of whole turns of the lanes, where a row is small enough
     const int64_t row = c.C * (c.backward ? xb + es : es) + nb;
     int64_t room = (int64_t)kFlowSmem - 1024 - (int64_t)f.smem;
     auto bytes = [&](int64_t rows) {  // of a stage: the 16-byte blocks that hold its rows
@@ -162,7 +162,9 @@ static GnFlow flow_plan(const GnCall &c, int sms) {
     };
     int64_t rows = std::max<int64_t>(1, kFlowStage / row / lanes) * lanes;
     while (rows > 1 && 3 * bytes(rows) > room) rows = rows > lanes ? std::max<int64_t>(rows / 2 / lanes, 1) * lanes : rows / 2;
-    if (2 * bytes(rows) > room) room = (int64_t)kFlowSmemMost - (int64_t)f.smem;  // (rows of ROWS_MAX_CHANNELS: two fit)
+    // (rows of ROWS_MAX_CHANNELS in one CTA an SM: two stages fit, but for the fp32 gradient with
+    // more than 3900 groups, whose statistics are as large as a row: one, 98 KB)
+    if (2 * bytes(rows) > room) room = (int64_t)kFlowSmemMost - (int64_t)f.smem;
     f.stage_rows = (int)rows;
     f.depth = (int)std::min<int64_t>(kFlowStagesMost, room / std::max<int64_t>(1, bytes(rows)));
     f.grid = kFlowCtas * sms;
@@ -272,6 +274,7 @@ struct GnLose {
 static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const GnFlow &f, char *w, void *dgamma, void *dbeta,
                                     int sms, int *status, cudaStream_t s, const GnLose *lose = nullptr) {
     const int base = base_of(c.dt);
+    if (f.depth < 1) return RMSNORM_ERR_UNSUPPORTED;  // (no size that is taken: rows of ROWS_MAX_CHANNELS have a stage)
     FlowParams p;
     std::memset(&p, 0, sizeof p);
     p.g = g;

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 import torch
 
-from test_gpu_rows import TYPES, bits, check_kept, gen, gn_forward, half_step, near, normal, rn  # noqa: F401
+from test_gpu_rows import TYPES, bits, check_kept, gen, gn_backward, gn_forward, half_step, near, normal, offset_view, rn  # noqa: F401
 from test_rows_plan_cpu import Plan
 
 pytestmark = pytest.mark.gpu
@@ -24,6 +24,15 @@ def check_forward(out, x, gamma, beta, G, act):
     near(out["mean"], mean, em, "mean")
     near(out["rstd"], rstd, er, "rstd")
     near(out["y"], y, half_step(t) * y.abs() + ey + 2.0 ** -25 * (t == torch.float16), "y")
+
+
+def check_backward(out, dy, x, gamma, beta, f, G, act):
+    t = dy.dtype
+    dx, ex, dg, eg, db, eb = gn_backward(dy, x, gamma, beta, f["mean"], f["rstd"], G, act)
+    small = 2.0 ** -25 * (t == torch.float16)
+    near(out["dx"], dx, half_step(t) * dx.abs() + ex + small, "dx")
+    near(out["dgamma"], dg, half_step(gamma.dtype) * dg.abs() + eg + small, "dgamma")
+    near(out["dbeta"], db, half_step(beta.dtype) * db.abs() + eb + small, "dbeta")
 
 
 def cut(rn, B, S, C, G, t, backward=False, kept=False, row=16, code=16):
@@ -84,3 +93,17 @@ def test_a_launch_whose_wait_gives_up_ends_and_says_so(rn, dt, B, S, C, G, stage
     assert torch.equal(out[~untouched], want[~untouched])
     again = rn.groupnorm_fwd(x, None, None, G)
     assert torch.equal(bits(again["y"]), bits(f["y"])) and status(0) == 0
+
+
+# -------------------------------------------------------------- rings of stages --
+
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_a_gradient_whose_ring_has_one_stage(rn, act):
+    """8192 fp32 channels in 4096 groups at an odd address: copies and sums take turns."""
+    t, (B, S, C, G) = torch.float32, (2, 300, 8192, 4096)
+    x, gamma, beta = sample(3, B, S, C, t)
+    x, dy = offset_view(x, 1), offset_view(normal(gen(4), B, S, C), 1)
+    assert cut(rn, B, S, C, G, t, backward=True, row=4).stages == 1
+    f = rn.groupnorm_fwd(x, gamma, beta, G, act=act)
+    check_forward(f, x, gamma, beta, G, act)
+    check_backward(rn.groupnorm_bwd(dy, x, gamma, beta, f["mean"], f["rstd"], G, act=act), dy, x, gamma, beta, f, G, act)

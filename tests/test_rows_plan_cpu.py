@@ -60,6 +60,22 @@ def test_the_workspace_that_is_asked_for_is_enough_for_every_call(rn):
         assert max(needs) == most, (B, S, C, G, dt, backward)
 
 
+def test_every_ring_has_a_stage_and_fits_an_sm(rn):
+    """The widest rows with the most groups: a stage at least, in the shared memory that a CTA may have (227 KB, of
+    which barriers and the mailbox take less than 1 KB)."""
+    least = 9
+    for C, G in [(C, G) for C in (8192, 8190, 8000, 7900, 5120, 4099, 2050, 1030) for G in (1, 2, 5, 10, C // 8, C // 4, C // 2, 4096)]:
+        if C % G or G > 4096:
+            continue
+        for dt, backward, kept, row in itertools.product((F32, BF16), (0, 1), (0, 1), (1, 16)):
+            p = plan(rn, 2, 30000, C, G, dt, backward, kept, row, row)
+            assert p.smem_bytes <= 226 * 1024
+            if p.cluster == 0:
+                assert p.stages >= 1, (C, G, dt, backward, kept, row)
+                least = min(least, p.stages)
+    assert least == 1  # the fp32 gradient of 8192 channels in 4096 groups
+
+
 def test_plan_queries_refuse(rn):
     ask, p = rn.lib().groupnorm_plan_query, ctypes.byref(Plan())
     assert ask(1, 64, 64, 8, BF16, 0, 0, 16, 16, 152, None) == INVALID
