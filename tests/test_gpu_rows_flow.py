@@ -107,3 +107,117 @@ def test_a_gradient_whose_ring_has_one_stage(rn, act):
     f = rn.groupnorm_fwd(x, gamma, beta, G, act=act)
     check_forward(f, x, gamma, beta, G, act)
     check_backward(rn.groupnorm_bwd(dy, x, gamma, beta, f["mean"], f["rstd"], G, act=act), dy, x, gamma, beta, f, G, act)
+
+
+# ------------------------------------- workspaces, streams, graphs, in place --
+
+FLOWS = [("bf16", 2, 40000, 32, 4), ("f32", 2, 40000, 33, 3), ("f16", 1, 20001, 90, 9)]
+
+
+def flow_calls(rn, dt, B, S, C, G):
+    """name -> (whether backward, a call that makes its results anew or into what it is given)."""
+    t = TYPES[dt]
+    x, gamma, beta = sample(5, B, S, C, t)
+    dy = normal(gen(6), B, S, C, dt=t)
+    f = rn.groupnorm_fwd_ckpt8(x, gamma, beta, G, act="silu")
+    for backward, held in ((False, False), (False, True), (True, False), (True, True)):
+        assert cut(rn, B, S, C, G, t, backward, held).cluster == 0
+    a = (gamma, beta, G)
+    m = (f["mean"], f["rstd"])
+    return {
+        "forward": (False, lambda **k: rn.groupnorm_fwd(x, *a, act="silu", **k)),
+        "keeping": (False, lambda **k: rn.groupnorm_fwd_ckpt8(x, *a, act="silu", **k)),
+        "gradient": (True, lambda **k: rn.groupnorm_bwd(dy, x, gamma, beta, *m, G, act="silu", **k)),
+        "gradient from kept": (True, lambda **k: rn.groupnorm_bwd_ckpt8(dy, f["codes"], f["scales"], gamma, beta, *m, G, act="silu", **k)),
+    }
+
+
+def same(got, want):
+    return got.keys() == want.keys() and all(torch.equal(bits(got[k]), bits(want[k])) for k in want)
+
+
+@pytest.mark.parametrize("op", ["forward", "keeping", "gradient", "gradient from kept"])
+@pytest.mark.parametrize("dt,B,S,C,G", FLOWS)
+def test_flows_on_streams_in_graphs_and_in_given_workspaces(rn, dt, B, S, C, G, op):
+    backward, call = flow_calls(rn, dt, B, S, C, G)[op]
+    want = {k: v.clone() for k, v in call().items()}
+    # the workspace that the query names, whatever is in it; none that is smaller than the cut's
+    ws = full_workspace(rn, (B, S, C), G, TYPES[dt], backward)
+    need = cut(rn, B, S, C, G, TYPES[dt], backward, "kept" in op or op == "keeping").workspace_bytes
+    assert ws.numel() >= need > 256
+    for _ in range(2):
+        assert same(call(workspace=ws), want)
+    assert same(call(workspace=ws[:need]), want)
+    with pytest.raises(rn.RMSNormError):
+        call(workspace=ws[:need - 16])
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream, 0):
+        got = call(stream=stream)
+        torch.cuda.synchronize()
+        assert same(got, want)
+    # two streams at once, each call in a workspace of its own
+    streams, results = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                results.append(call())
+    torch.cuda.synchronize()
+    assert all(same(r, want) for r in results)
+    # captured and replayed: the tickets begin anew
+    for given in (None, ws):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call(workspace=given)
+        for _ in range(3):
+            for t in got.values():
+                t.zero_()
+            if given is not None:
+                given.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert same(got, want)
+
+
+@pytest.mark.parametrize("dt,B,S,C,G", FLOWS)
+def test_two_graphs_share_a_workspace_of_a_flow(rn, dt, B, S, C, G):
+    """One after the other on one stream, in either order, forward and gradient in the same memory."""
+    calls = flow_calls(rn, dt, B, S, C, G)
+    want = {op: {k: v.clone() for k, v in calls[op][1]().items()} for op in ("keeping", "gradient")}
+    ws = torch.full((max(rn.groupnorm_workspace_bytes(B, S, C, G, TYPES[dt], backward=b) for b in (False, True)),), 255, dtype=torch.uint8,
+                    device="cuda")
+    graphs = {}
+    for op in want:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = calls[op][1](workspace=ws)
+        graphs[op] = (g, got)
+    for op in ("keeping", "gradient", "gradient", "keeping", "keeping", "gradient"):
+        for t in graphs[op][1].values():
+            t.zero_()
+        graphs[op][0].replay()
+        torch.cuda.synchronize()
+        assert same(graphs[op][1], want[op])
+
+
+@pytest.mark.parametrize("dt,B,S,C,G", FLOWS)
+def test_flows_in_place(rn, dt, B, S, C, G):
+    t = TYPES[dt]
+    x, gamma, beta = sample(7, B, S, C, t)
+    dy = normal(gen(8), B, S, C, dt=t)
+    want = rn.groupnorm_fwd(x, gamma, beta, G, act="gelu")
+    check_forward(want, x, gamma, beta, G, "gelu")
+    y = x.clone()
+    assert rn.groupnorm_fwd(y, gamma, beta, G, act="gelu", y=y)["y"] is y and torch.equal(bits(y), bits(want["y"]))
+    keeping = rn.groupnorm_fwd_ckpt8(x, gamma, beta, G, act="gelu")
+    y = x.clone()
+    got = rn.groupnorm_fwd_ckpt8(y, gamma, beta, G, act="gelu", y=y)
+    assert same(got, keeping)
+    check_kept(x, got["codes"], got["scales"])
+    back = rn.groupnorm_bwd(dy, x, gamma, beta, want["mean"], want["rstd"], G, act="gelu")
+    check_backward(back, dy, x, gamma, beta, want, G, "gelu")
+    for into in ("dy", "x"):
+        a, b = dy.clone(), x.clone()
+        assert same(rn.groupnorm_bwd(a, b, gamma, beta, want["mean"], want["rstd"], G, act="gelu", dx=a if into == "dy" else b), back)
+    a = dy.clone()
+    kept_back = rn.groupnorm_bwd_ckpt8(dy, keeping["codes"], keeping["scales"], gamma, beta, want["mean"], want["rstd"], G, act="gelu")
+    assert same(rn.groupnorm_bwd_ckpt8(a, keeping["codes"], keeping["scales"], gamma, beta, want["mean"], want["rstd"], G, act="gelu", dx=a), kept_back)
