@@ -624,10 +624,11 @@ typedef struct {
  * two that the addresses of x and y (dy, x and dx) and of codes are multiples
  * of (16: any larger one too); row_align 0: workspace_bytes alone is set, to
  * the most of all alignments, kept or not. num_sms > 0: for a device of that
- * many SMs, no device is needed; 0: the current one. */
+ * many SMs that holds clusters of up to max_cluster CTAs, no device is needed;
+ * 0: the current one, which is asked once for the largest that it holds. */
 rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward,
                                       int kept, int32_t row_align, int32_t code_align, int32_t num_sms,
-                                      groupnorm_plan_t *plan);
+                                      int32_t max_cluster, groupnorm_plan_t *plan);
 
 /* For tests of what a launch by pieces does where a wait gives up:
  * groupnorm_fwd of x (dy NULL, eps 1e-5) into out, or groupnorm_bwd of dy and x,

@@ -108,7 +108,7 @@ SIGNATURES = {
     "groupnorm_fwd": (_i, [_vp] * 9 + [_sz, _i64, _i64, _i64, _i64, _i, _i, _f, _vp]),
     "groupnorm_bwd": (_i, [_vp] * 12 + [_sz, _i64, _i64, _i64, _i64, _i, _i, _vp]),
     "groupnorm_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i, _i]),
-    "groupnorm_plan_query": (_i, [_i64] * 4 + [_i] * 6 + [_vp]),
+    "groupnorm_plan_query": (_i, [_i64] * 4 + [_i] * 7 + [_vp]),
     "groupnorm_give_up_check": (_i, [_vp] * 5 + [_i64] * 4 + [_i, _i64, ctypes.c_uint32, _vp]),
     "embed_fwd": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _f, _vp]),
     "rmsnorm_embed_fwd": (_i, [_vp] * 6 + [_i64, _i64, _i64, _i, _i, _f, _f, _f, _vp]),

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "groupnorm_flow.cuh"
 #include "groupnorm_held.cuh"
@@ -66,6 +67,39 @@ struct GnHeld {
 constexpr size_t kHeldSmem = 112 * 1024;  // of a CTA: two an SM
 constexpr int kHeldGroups = 256;          // of a cluster at most
 
+// A device as the plans see it: its SMs, and the CTAs of the largest cluster
+// (1, 2, 4, 8 or 16) that it holds with a held CTA's threads and shared memory.
+struct GnDevice {
+    int sms, cluster;
+};
+
+// (never launched: what the runtime is asked about)
+__global__ void __launch_bounds__(kHeldThreads, 2) gn_cluster_room() {}
+
+// The current device, asked once; a cudaError_t.
+static int gn_device(GnDevice &on, int **status) {
+    static std::mutex mu;
+    static int most[64];
+    int dev = 0;
+    const int e = current_device(&on.sms, status, &dev);
+    if (e != 0) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (most[dev] == 0) {
+        auto *kernel = gn_cluster_room;
+        most[dev] = 1;
+        const bool ok = allow_staged_smem(reinterpret_cast<const void *>(kernel)) == 0;
+        const bool wide = ok && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+        for (int size = wide ? kHeldCtas : 8; ok && size > 1 && most[dev] == 1; size /= 2) {
+            LaunchCfg lc((unsigned)(size * on.sms), kHeldThreads, kHeldSmem, nullptr, (unsigned)size, false);
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &lc.cfg) == cudaSuccess && n > 0) most[dev] = size;
+        }
+        (void)cudaGetLastError();
+    }
+    on.cluster = most[dev];
+    return 0;
+}
+
 // What a cut needs; false: it does not fit.
 static bool held_cut(const GnCall &c, int K, int ctas, GnHeld &h) {
     const int es = bytes_of(c.dt), E = c.chunk, cg = (int)(c.C / c.G);
@@ -90,13 +124,14 @@ static bool held_cut(const GnCall &c, int K, int ctas, GnHeld &h) {
 // that begins or ends inside a 32-byte sector counted with the whole sector.
 // (The gradient of 8 x 4096 x 320: spans of 80 bytes in clusters of 8 take 33
 // us, of 160 bytes in clusters of 16 39, the flow 57.)
-static GnHeld held_plan(const GnCall &c, int sms) {
+static GnHeld held_plan(const GnCall &c, const GnDevice &on) {
+    const int sms = on.sms;
     GnHeld best{0, 0, 0, 0, {0, 0}, 0, 0};
     double least = 0;
     const int es = bytes_of(c.dt);
     for (int K = 1; K <= c.G && K <= kHeldGroups; ++K) {
         if (c.G % K != 0) continue;
-        for (int n = 1; n <= kHeldCtas; n *= 2) {
+        for (int n = 1; n <= on.cluster; n *= 2) {
             GnHeld h;
             if ((n > 1 && (c.S + n - 1) / n * (n - 1) >= c.S) || !held_cut(c, K, n, h)) continue;
             const double row = (double)h.W * es, sectors = K == c.G || (h.W * es) % 32 == 0 ? row : row + 32;
@@ -212,16 +247,16 @@ struct GnCut {
     GnFlow f;  // where h.ctas is 0
     size_t bytes;
 };
-static GnCut gn_cut(const GnCall &c, int sms) {
+static GnCut gn_cut(const GnCall &c, const GnDevice &on) {
     GnCut k;
     std::memset(&k, 0, sizeof k);
     k.c = c;
-    k.h = held_plan(c, sms);
+    k.h = held_plan(c, on);
     if (k.h.ctas) {
         k.bytes = c.backward ? held_bytes(c, k.h) : 0;
     } else {
         if (c.backward) k.c.chunk = flow_chunk(c.chunk, c.C);
-        k.f = flow_plan(k.c, sms);
+        k.f = flow_plan(k.c, on.sms);
         k.bytes = k.f.bytes;
     }
     return k;
@@ -313,7 +348,7 @@ static rmsnorm_status_t gn_run_flow(const GnParams &g, const GnCall &c, const Gn
 }
 
 // The most that any alignment takes, with x kept in 8 bits or not.
-static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, bool backward, int sms) {
+static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, bool backward, const GnDevice &on) {
     size_t most = 0;
     for (int row = 16; row > 0; row /= 2)
         for (int code = 16; code > 0; code /= 2)
@@ -325,7 +360,7 @@ static size_t gn_workspace(int64_t B, int64_t S, int64_t C, int64_t G, int dt, b
                     const GnCall less = gn_call(B, S, C, G, 0, dt, backward, kept != 0, row, code / 2);
                     if (c.chunk == less.chunk && c.kept == less.kept) continue;
                 }
-                most = std::max(most, gn_cut(c, sms).bytes);
+                most = std::max(most, gn_cut(c, on).bytes);
             }
     return most;
 }
@@ -348,10 +383,12 @@ extern "C" rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, cons
     cudaStream_t s = (cudaStream_t)stream;
     if (S == 0) return zeros({{mean, (size_t)(B * G) * 4}, {rstd, (size_t)(B * G) * 4}}, s);
     if (!x || !y || !on(x, es) || !on(y, es)) return RMSNORM_ERR_INVALID_ARG;
-    int sms = 0, *status = nullptr;
-    const int e = current_device(&sms, &status);
+    GnDevice here;
+    int *status = nullptr;
+    const int e = gn_device(here, &status);
     if (e != 0) return head_cuda_fail(e);
-    const GnCut k = gn_cut(gn_call(B, S, C, G, act, dt, false, codes != nullptr, align_of({x, y}), align_of({codes})), sms);
+    const int sms = here.sms;
+    const GnCut k = gn_cut(gn_call(B, S, C, G, act, dt, false, codes != nullptr, align_of({x, y}), align_of({codes})), here);
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.gamma = gamma, p.beta = beta, p.out = y, p.mean = mean, p.rstd = rstd;
@@ -383,10 +420,12 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
     if (G > ROWS_MAX_GROUPS) return RMSNORM_ERR_UNSUPPORTED;
     if (!dy || !dx || !mean || !rstd || (x == nullptr) == (codes == nullptr)) return RMSNORM_ERR_INVALID_ARG;
     if (!on(dy, es) || !on(dx, es) || !on(x, es) || !on(mean, 4) || !on(rstd, 4)) return RMSNORM_ERR_INVALID_ARG;
-    int sms = 0, *status = nullptr;
-    const int e = current_device(&sms, &status);
+    GnDevice here;
+    int *status = nullptr;
+    const int e = gn_device(here, &status);
     if (e != 0) return head_cuda_fail(e);
-    const GnCut k = gn_cut(gn_call(B, S, C, G, act, dt, true, codes != nullptr, align_of({dy, dx, x}), align_of({codes})), sms);
+    const int sms = here.sms;
+    const GnCut k = gn_cut(gn_call(B, S, C, G, act, dt, true, codes != nullptr, align_of({dy, dx, x}), align_of({codes})), here);
     GnParams p;
     std::memset(&p, 0, sizeof p);
     p.x = x, p.dy = dy, p.codes_in = static_cast<const uint8_t *>(codes), p.scales_in = scales;
@@ -403,21 +442,22 @@ extern "C" rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const v
 
 extern "C" rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward,
                                                  int kept, int32_t row_align, int32_t code_align, int32_t num_sms,
-                                                 groupnorm_plan_t *plan) {
-    if (!plan || !gn_sizes(B, S, C, G, 0, dt) || num_sms < 0 || row_align < 0 || code_align < 0) return RMSNORM_ERR_INVALID_ARG;
+                                                 int32_t max_cluster, groupnorm_plan_t *plan) {
+    if (!plan || !gn_sizes(B, S, C, G, 0, dt) || num_sms < 0 || row_align < 0 || code_align < 0 || (num_sms > 0 && max_cluster < 1))
+        return RMSNORM_ERR_INVALID_ARG;
     if (G > ROWS_MAX_GROUPS) return RMSNORM_ERR_UNSUPPORTED;
     std::memset(plan, 0, sizeof *plan);
     if (B == 0 || S == 0) return RMSNORM_SUCCESS;
-    int sms = num_sms;
-    if (sms == 0) {
-        const int e = current_device(&sms, nullptr);
+    GnDevice on{num_sms, max_cluster < kHeldCtas ? max_cluster : kHeldCtas};
+    if (num_sms == 0) {
+        const int e = gn_device(on, nullptr);
         if (e != 0) return head_cuda_fail(e);
     }
     if (row_align == 0) {
-        plan->workspace_bytes = (int64_t)gn_workspace(B, S, C, G, dt, backward != 0, sms);
+        plan->workspace_bytes = (int64_t)gn_workspace(B, S, C, G, dt, backward != 0, on);
         return RMSNORM_SUCCESS;
     }
-    const GnCut k = gn_cut(gn_call(B, S, C, G, 0, dt, backward != 0, kept != 0, row_align, code_align), sms);
+    const GnCut k = gn_cut(gn_call(B, S, C, G, 0, dt, backward != 0, kept != 0, row_align, code_align), on);
     plan->chunk = k.c.chunk, plan->cluster = k.h.ctas, plan->groups = k.h.K;
     plan->rows = k.h.ctas ? k.h.rows : k.f.rows;
     plan->stages = k.h.ctas ? 0 : k.f.depth;
@@ -428,7 +468,7 @@ extern "C" rmsnorm_status_t groupnorm_plan_query(int64_t B, int64_t S, int64_t C
 
 extern "C" size_t groupnorm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rmsnorm_dtype_t dt, int backward) {
     groupnorm_plan_t plan;
-    return groupnorm_plan_query(B, S, C, G, dt, backward, 0, 0, 0, 0, &plan) == RMSNORM_SUCCESS ? (size_t)plan.workspace_bytes : 0;
+    return groupnorm_plan_query(B, S, C, G, dt, backward, 0, 0, 0, 0, 0, &plan) == RMSNORM_SUCCESS ? (size_t)plan.workspace_bytes : 0;
 }
 
 extern "C" rmsnorm_status_t groupnorm_give_up_check(const void *dy, const void *x, float *mean, float *rstd, void *out, int64_t B,
@@ -438,9 +478,11 @@ extern "C" rmsnorm_status_t groupnorm_give_up_check(const void *dy, const void *
         return RMSNORM_ERR_INVALID_ARG;
     const int es = bytes_of(dt);
     if (!x || !out || !mean || !rstd || !on(x, es) || !on(out, es) || !on(dy, es) || !on(mean, 4) || !on(rstd, 4)) return RMSNORM_ERR_INVALID_ARG;
-    int sms = 0, *status = nullptr;
-    const int e = current_device(&sms, &status);
+    GnDevice here;
+    int *status = nullptr;
+    const int e = gn_device(here, &status);
     if (e != 0) return head_cuda_fail(e);
+    const int sms = here.sms;
     GnCall c = gn_call(B, S, C, G, 0, dt, dy != nullptr, false, align_of({dy, x, out}), 16);
     if (dy) c.chunk = flow_chunk(c.chunk, C);
     const GnFlow f = flow_plan(c, sms);

@@ -298,7 +298,7 @@ int32_t align_of(std::initializer_list<const void *> at) {
 size_t gn_need(const Places &p, int dt, bool backward, std::initializer_list<const void *> rows, const void *codes) {
     groupnorm_plan_t plan;
     const rmsnorm_status_t st = groupnorm_plan_query(p.B, p.S, p.C, p.G, (rmsnorm_dtype_t)dt, backward, codes != nullptr,
-                                                     align_of(rows), align_of({codes}), 0, &plan);
+                                                     align_of(rows), align_of({codes}), 0, 0, &plan);
     return st == RMSNORM_SUCCESS ? (size_t)plan.workspace_bytes : 0;
 }
 

@@ -37,7 +37,7 @@ def check_backward(out, dy, x, gamma, beta, f, G, act):
 
 def cut(rn, B, S, C, G, t, backward=False, kept=False, row=16, code=16):
     p, dt = Plan(), {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t]
-    assert rn.lib().groupnorm_plan_query(B, S, C, G, dt, backward, kept, row, code, 0, ctypes.byref(p)) == 0
+    assert rn.lib().groupnorm_plan_query(B, S, C, G, dt, backward, kept, row, code, 0, 0, ctypes.byref(p)) == 0
     return p
 
 
@@ -221,3 +221,16 @@ def test_flows_in_place(rn, dt, B, S, C, G):
     a = dy.clone()
     kept_back = rn.groupnorm_bwd_ckpt8(dy, keeping["codes"], keeping["scales"], gamma, beta, want["mean"], want["rstd"], G, act="gelu")
     assert same(rn.groupnorm_bwd_ckpt8(a, keeping["codes"], keeping["scales"], gamma, beta, want["mean"], want["rstd"], G, act="gelu", dx=a), kept_back)
+
+
+def test_the_device_is_asked_for_the_clusters_that_it_holds(rn):
+    """The cut on this device is that for the largest cluster that it says it holds; clusters of 8 are every device's."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for size in ((3, 2000, 90, 9), (8, 4096, 320, 32), (2, 16384, 64, 8)):
+        for backward in (False, True):
+            here = cut(rn, *size, torch.float32, backward)
+            for_most = {}
+            for most in (8, 16):
+                for_most[most] = Plan()
+                assert rn.lib().groupnorm_plan_query(*size, 0, backward, 0, 16, 16, sms, most, ctypes.byref(for_most[most])) == 0
+            assert bytes(here) in (bytes(for_most[8]), bytes(for_most[16]))

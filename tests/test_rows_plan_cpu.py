@@ -24,9 +24,9 @@ def rn():
     return pkg
 
 
-def plan(rn, B, S, C, G, dt, backward=0, kept=0, row=16, code=16, sms=152):
+def plan(rn, B, S, C, G, dt, backward=0, kept=0, row=16, code=16, sms=152, most=16):
     p = Plan()
-    assert rn.lib().groupnorm_plan_query(B, S, C, G, dt, backward, kept, row, code, sms, ctypes.byref(p)) == OK
+    assert rn.lib().groupnorm_plan_query(B, S, C, G, dt, backward, kept, row, code, sms, most, ctypes.byref(p)) == OK
     return p
 
 
@@ -76,15 +76,28 @@ def test_every_ring_has_a_stage_and_fits_an_sm(rn):
     assert least == 1  # the fp32 gradient of 8192 channels in 4096 groups
 
 
+def test_clusters_are_no_larger_than_the_device_holds(rn):
+    """A device that holds no clusters of 16 (or 8 ...) is given smaller ones, or pieces."""
+    seen = {most: set() for most in (1, 2, 4, 8, 16)}
+    for B, S, C, G in some_sizes(300):
+        for most, backward in itertools.product(seen, (0, 1)):
+            p = plan(rn, B, S, C, G, BF16, backward, most=most)
+            assert p.cluster <= most
+            assert (p.cluster > 0) != (p.stages > 0)
+            seen[most].add(p.cluster)
+    assert all(max(seen[most]) == most and 0 in seen[most] for most in seen)
+
+
 def test_plan_queries_refuse(rn):
     ask, p = rn.lib().groupnorm_plan_query, ctypes.byref(Plan())
-    assert ask(1, 64, 64, 8, BF16, 0, 0, 16, 16, 152, None) == INVALID
+    assert ask(1, 64, 64, 8, BF16, 0, 0, 16, 16, 152, 16, None) == INVALID
     for bad in ((-1, 64, 64, 8, BF16), (1, -1, 64, 8, BF16), (1, 64, 0, 8, BF16), (1, 64, 64, 7, BF16), (1, 64, 8200, 8, BF16),
                 (1, 64, 64, 8, 5)):
-        assert ask(*bad, 0, 0, 16, 16, 152, p) == INVALID
-    assert ask(1, 64, 64, 8, BF16, 0, 0, -1, 16, 152, p) == INVALID
-    assert ask(1, 64, 64, 8, BF16, 0, 0, 16, 16, -1, p) == INVALID
-    assert ask(1, 64, 8192, 8192, BF16, 0, 0, 16, 16, 152, p) == UNSUPPORTED
+        assert ask(*bad, 0, 0, 16, 16, 152, 16, p) == INVALID
+    assert ask(1, 64, 64, 8, BF16, 0, 0, -1, 16, 152, 16, p) == INVALID
+    assert ask(1, 64, 64, 8, BF16, 0, 0, 16, 16, -1, 16, p) == INVALID
+    assert ask(1, 64, 64, 8, BF16, 0, 0, 16, 16, 152, 0, p) == INVALID
+    assert ask(1, 64, 8192, 8192, BF16, 0, 0, 16, 16, 152, 16, p) == UNSUPPORTED
     for none in ((0, 64), (2, 0)):
         assert plan(rn, *none, 64, 8, BF16).workspace_bytes == 0
 
