@@ -656,7 +656,9 @@ rmsnorm_status_t rmsnorm_embed_fwd(const void *ids, const void *table, const voi
 
 /*
  * The table's gradient: dtable_v = scale sum_{t: id_t = v} dh_t, summed in
- * fp32 in an order that depends on the ids alone and rounded once; tokens
+ * fp32 in an order that depends on the ids, T and N alone (where T N is above
+ * 2^23 in longer pieces, so columns taken by themselves may differ in their
+ * last bits from the same ones of a longer row) and rounded once; tokens
  * whose id is outside the table add nothing. accumulate 0: every row of
  * dtable [rows, N] is written (zeros where no token is); else the sums are
  * added to what is there, and rows without a token are not touched. dtable is

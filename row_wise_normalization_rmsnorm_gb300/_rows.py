@@ -112,7 +112,7 @@ def embed_bwd(dh, ids, rows: int, *, scale: float = 1.0, dtype=None, dtable=None
               stream=None):
     """The table's gradient [rows, N] from that of its looked-up rows: for
     each row scale times the sum of dh over the row's tokens, in an order that
-    depends on the ids alone. In dh's type or (``dtype``, or a given
+    depends on the ids, their number and N alone. In dh's type or (``dtype``, or a given
     ``dtable``) fp32. accumulate: added to ``dtable``, of which only the rows
     with tokens are touched; otherwise every row is written."""
     return _ext().embed_grad(dh, ids, rows, scale, dtype, dtable, accumulate, workspace, stream)

@@ -4,8 +4,9 @@
 // tokens in their order: its sum has one order whatever the launch does, with
 // no atomics on values. Runs are of very unlike lengths (a text's tokens
 // follow a power law), so the sorted tokens are cut into pieces of 32 (few
-// tokens: 8) that a team each sums. A run inside a piece goes to its row at once; what a piece
-// has of a run that goes on beyond it is joined in a second launch.
+// values: 8) that a team each sums. A run inside a piece goes to its row at once; what a piece
+// has of a run that goes on beyond it is joined in a second launch. A sum has a piece's tokens
+// in sequence, then a quarter of its run's pieces, then the quarters.
 // Rows without a token are set to zero by other CTAs of the first launch.
 //
 // Bytes: T N of dh read and V N of dtable written, once each; the sort moves
