@@ -122,7 +122,6 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_fwd_held(const HeldParams 
     float2 *exch = reinterpret_cast<float2 *>(ch_m2 + p.W);
     float2 *stat = exch + p.ctas * p.K, *own = stat + p.K;
     const HeldPlace at(p);
-    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
     const Slab xs(g.x, sizeof(T), at.first, g.C, at.rows, held);
     if constexpr (E == 1) {
         if (threadIdx.x == 0) {
@@ -275,7 +274,6 @@ __global__ void __launch_bounds__(kHeldThreads, 2) gn_bwd_held(const HeldParams 
     float2 *exch = reinterpret_cast<float2 *>(ch_s + p.W);
     float2 *means = exch + p.ctas * p.K, *stat = means + p.K;
     const HeldPlace at(p);
-    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
     constexpr int XE = KEPT ? 1 : (int)sizeof(T);  // bytes of a value of x
     const Slab xs(KEPT ? (const void *)g.codes_in : g.x, XE, at.first, g.C, at.rows, held);
     const Slab ds(g.dy, sizeof(T), at.first, g.C, at.rows, held + p.slab[0]);

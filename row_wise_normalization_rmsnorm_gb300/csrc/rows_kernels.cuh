@@ -767,9 +767,6 @@ template <typename T> __global__ void __launch_bounds__(256) rows_dw_any(const R
 // ---------------------------------------------------------------- kernels --
 // The teams that the kernels are compiled for: threads a row and chunks a
 // thread, by the chunks they hold. A row takes the first that holds it.
-struct TeamSize {
-    int tpr, v;
-};
 #define ROWS_FWD_TEAMS(X) X(8, 1) X(32, 1) X(32, 2) X(64, 2) X(64, 4) X(128, 3) X(128, 4) X(256, 3) X(256, 4) X(512, 3) X(512, 4) X(1024, 4) X(1024, 8)
 // (backward: and rows a team takes at once; 32 fp32 sums of dw a thread at most)
 #define ROWS_BWD_TEAMS(X) \
