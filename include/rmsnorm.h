@@ -560,6 +560,7 @@ typedef enum {
     ROWS_ACT_SILU = 1, /* z / (1 + exp(-z))              */
     ROWS_ACT_GELU = 2  /* z (1 + erf(z / sqrt(2))) / 2   */
 } rmsnorm_act_t;
+/* (In fp32 GELU is off by up to 5e-7, so its values below z = -4 keep few digits.) */
 
 #define ROWS_MAX_GROUPS 4096
 #define ROWS_MAX_CHANNELS 8192
@@ -594,7 +595,9 @@ rmsnorm_status_t groupnorm_fwd(const void *x, const void *gamma, const void *bet
  *   dx = rstd (u gamma - mean_n(u gamma) - xhat mean_n(u gamma xhat))
  *
  * dgamma, dbeta [C] or NULL (not wanted; dgamma needs gamma); their sums
- * have a fixed order. dx may equal dy or x.
+ * have a fixed order. dx may equal dy or x. The workspace holds 2 C partial
+ * sums for each CTA of a cluster or for each piece: with samples of few places
+ * (or rows of several tiles) it is larger than x, 4 times for bf16 with S 1.
  */
 rmsnorm_status_t groupnorm_bwd(const void *dy, const void *x, const void *codes, const uint8_t *scales,
                                const void *gamma, const void *beta, const float *mean, const float *rstd,

@@ -65,7 +65,9 @@ def groupnorm_fwd(x, gamma, beta, groups: int, *, act=None, eps: float = 1e-5, y
 
 def groupnorm_fwd_ckpt8(x, gamma, beta, groups: int, *, act=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
                         codes=None, scales=None, workspace=None, stream=None) -> dict:
-    """groupnorm_fwd with x kept in 8 bits: also codes and scales."""
+    """groupnorm_fwd with x kept in 8 bits: also codes and scales. (The work may
+    be cut another way: y, mean and rstd may differ in their last bits from
+    those of groupnorm_fwd.)"""
     out = _ext().gn_fwd(x, gamma, beta, groups, act, eps, True, y, mean, rstd, codes, scales, workspace, stream)
     return dict(zip(("y", "mean", "rstd", "codes", "scales"), out))
 
@@ -73,7 +75,8 @@ def groupnorm_fwd_ckpt8(x, gamma, beta, groups: int, *, act=None, eps: float = 1
 def groupnorm_bwd(dy, x, gamma, beta, mean, rstd, groups: int, *, act=None, want_dgamma=True, want_dbeta=True,
                   dx=None, dgamma=None, dbeta=None, workspace=None, stream=None) -> dict:
     """dx, dgamma and dbeta of groupnorm_fwd given its mean and rstd (dgamma
-    None without gamma or when not wanted, dbeta when not wanted)."""
+    None without gamma or when not wanted, dbeta when not wanted: a tensor
+    given for it is then left as it is, as in layernorm_bwd)."""
     out = _ext().gn_bwd(dy, x, None, None, gamma, beta, mean, rstd, groups, act, bool(want_dgamma), bool(want_dbeta),
                         dx, dgamma, dbeta, workspace, stream)
     return dict(zip(("dx", "dgamma", "dbeta"), out))

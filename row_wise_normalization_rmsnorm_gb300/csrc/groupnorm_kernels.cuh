@@ -159,7 +159,8 @@ __device__ __forceinline__ float rcp_fast(float v) {
 
 // The sigmoids of E values: 1 / (1 + 2^(-z log2 e)), the reciprocal and (for
 // 16-bit rows) the exponential the fast ones; fp32 rows take the accurate
-// exponential. (One reciprocal for two values, 1 / a = b / (a b), takes 12
+// exponential. (SiLU in fp32 over [-8, 8]: rms error 1.50e-7 with the fast
+// reciprocal, 1.44e-7 with a division; its slope 1.11e-7 and 1.06e-7.) (One reciprocal for two values, 1 / a = b / (a b), takes 12
 // instead of 16 results of the special-function unit for 8 values, but 20
 // instructions more, and was no faster: 16.5 and 16.9 us for 8 x 4096 x 320.)
 template <typename T, int E> __device__ __forceinline__ void sigmoid_v(const float (&z)[E], float (&p)[E]) {
@@ -178,6 +179,10 @@ template <typename T, int E> __device__ __forceinline__ void sigmoid_v(const flo
         for (int i = 0; i < E; ++i) p[i] = rcp_fast(p[i]);
     }
 }
+// GELU as 1 + erf: over [-8, 8] off by 4.9e-7 at most (8 2^-24, rms 7e-8); below
+// z = -4 the digits that cancel are lost (6% of the value at -5), as in any form
+// with 1 + erf in 32 bits. The slope is off by 1.4e-7 at most (rms 2.7e-8), the
+// same with expf in the place of __expf.
 __device__ __forceinline__ float gelu_of(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); }
 __device__ __forceinline__ float gelu_slope(float z) {
     return 0.5f * (1.f + erff(z * 0.70710678f)) + z * __expf(-0.5f * z * z) * 0.39894228f;
